@@ -228,6 +228,126 @@ attn_status attn_qkv_proj_bwd(const void *x, const void *w_q, const void *w_k, c
                               int d_k, cudaStream_t stream);
 
 /*
+ * The rest of a transformer block around the attention: the linear layers with their epilogue,
+ * the root-mean-square norm, and the 8-bit forms of both.  Shared rules:
+ *   - Matrices are dense, row-major bf16 (or e4m3 with fp32 scales where a name ends in _q8);
+ *     vectors (bias, norm weight, scales, 1/rms) are fp32.  M counts rows (tokens), 0 <= M < 2^31;
+ *     with M = 0 the forward calls do nothing and the backward calls write zeros to the gradients
+ *     of the parameters.
+ *   - Widths (K, N_out, D) are multiples of 8 (16 for e4m3 rows) and below 2^20; no operand holds
+ *     2^40 elements or more.  Other widths are refused with ATTN_ERR_INVALID_ARG.
+ *   - Pointers are 16-byte aligned, and outputs overlap no input and no other output, except
+ *     where an entry point allows it by name.
+ */
+typedef enum {
+    ATTN_ACT_NONE = 0,
+    ATTN_ACT_RELU = 1,
+    ATTN_ACT_GELU = 2,       /* z Phi(z), with the normal distribution function (erf form) */
+    ATTN_ACT_GELU_TANH = 3,  /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+    ATTN_ACT_SILU = 4        /* z / (1 + exp(-z)) */
+} attn_activation;
+
+/*
+ * Linear layer: z = x w + bias, y = act(z) + residual, in one kernel.
+ *   x : [M, K] bf16.   w : [K, N_out] bf16 (input dimension x output columns, as w_q above).
+ *   bias : [N_out] fp32 or null.   residual : [M, N_out] bf16 or null.
+ *   y : [M, N_out] bf16 output; it may be `residual` itself.
+ *   z : [M, N_out] bf16 output or null: the pre-activation, kept for attn_linear_bwd().
+ * Arithmetic: bf16 products summed in fp32, bias, activation and residual in fp32, y and z each
+ * rounded once.
+ */
+attn_status attn_linear(const void *x, const void *w, const float *bias, const void *residual,
+                        void *y, void *z, int M, int K, int N_out, attn_activation act,
+                        cudaStream_t stream);
+
+/*
+ * Output projection: attn_linear() without an activation, reading attention's output in the
+ * layout attn_fwd() writes it, so that the heads need no copy to be put side by side:
+ *   y[b, i, :] = sum_h o[b, h, i, :] w[h d_k : (h+1) d_k, :] + bias + residual[b, i, :].
+ *   o : [B, H, N, d_k] bf16.   w : [H * d_k, N_out] bf16.   residual, y : [B, N, N_out] bf16.
+ */
+attn_status attn_out_proj(const void *o, const void *w, const float *bias, const void *residual,
+                          void *y, int B, int H, int N, int d_k, int N_out, cudaStream_t stream);
+
+/*
+ * Bytes of device workspace attn_linear_bwd() (with these sizes; act selects whether dz is kept)
+ * and attn_out_proj_bwd() need.  Both return 0 for sizes the calls reject.
+ */
+size_t attn_linear_bwd_workspace_size(int M, int K, int N_out, attn_activation act);
+size_t attn_out_proj_bwd_workspace_size(int B, int H, int N, int d_k, int N_out);
+
+/*
+ * Backward of attn_linear().  With dz = dy * act'(z) (dz = dy for ATTN_ACT_NONE):
+ *   dx = dz w^T;  dw = x^T dz;  dbias = sum over rows of dz.  (The residual's gradient is dy.)
+ *   dy : [M, N_out] bf16.   z : [M, N_out] bf16 from attn_linear (null for ATTN_ACT_NONE).
+ *   dx : [M, K] bf16, dw : [K, N_out] bf16, dbias : [N_out] fp32; each may be null (not computed).
+ *   workspace : caller-owned, 256-byte aligned, at least the size above, overwritten.
+ * dz is rounded to bf16 for the two products and summed unrounded for dbias.  All sums are in
+ * fp32 in a fixed order: results are bitwise reproducible.
+ */
+attn_status attn_linear_bwd(const void *x, const void *w, const void *dy, const void *z, void *dx,
+                            void *dw, float *dbias, void *workspace, size_t workspace_bytes, int M,
+                            int K, int N_out, attn_activation act, cudaStream_t stream);
+
+/* Backward of attn_out_proj(): d_o [B, H, N, d_k], dw [H * d_k, N_out], dbias; as above. */
+attn_status attn_out_proj_bwd(const void *o, const void *w, const void *dy, void *d_o, void *dw,
+                              float *dbias, void *workspace, size_t workspace_bytes, int B, int H,
+                              int N, int d_k, int N_out, cudaStream_t stream);
+
+/*
+ * Root-mean-square norm with the residual's addition:
+ *   h = x + residual (h = x without one);  rstd = 1 / sqrt(mean(h^2) + eps);
+ *   y = h * rstd * weight.
+ *   x, residual : [M, D] bf16 (residual may be null).   weight : [D] fp32.   0 <= eps, finite.
+ *   y : [M, D] bf16 output.   rstd : [M] fp32 output or null, kept for attn_rms_norm_bwd().
+ *   h : [M, D] bf16 output or null; may be x or residual itself.  Without a residual it is not
+ *       written and must be null.
+ * The statistics and y are taken from the unrounded fp32 sum; h and y are each rounded once.
+ */
+attn_status attn_rms_norm(const void *x, const void *residual, const float *weight, void *y, void *h,
+                          float *rstd, int M, int D, float eps, cudaStream_t stream);
+
+/* Bytes of device workspace attn_rms_norm_bwd() needs (0 for sizes it rejects). */
+size_t attn_rms_norm_bwd_workspace_size(int M, int D);
+
+/*
+ * Backward of attn_rms_norm().  With g = dy * weight and n = h * rstd:
+ *   dx = rstd * (g - n * mean(g * n)) + dh;   dweight = sum over rows of dy * n.
+ * dx is the gradient of x and of the residual alike.
+ *   dy, h : [M, D] bf16.   rstd : [M] fp32.   dh : [M, D] bf16 or null, the gradient that reaches
+ *   h by its other uses.   dx : [M, D] bf16 output, may be dh itself.   dweight : [D] fp32 output.
+ *   workspace : caller-owned, 256-byte aligned, overwritten.  Bitwise reproducible.
+ */
+attn_status attn_rms_norm_bwd(const void *dy, const void *h, const float *weight, const float *rstd,
+                              const void *dh, void *dx, float *dweight, void *workspace,
+                              size_t workspace_bytes, int M, int D, cudaStream_t stream);
+
+/*
+ * attn_rms_norm() with y in e4m3 and one fp32 scale a row:
+ *   scale = max(max |y|, 1e-30) / 448;  yq = y / scale rounded to nearest e4m3.
+ * A row that holds an infinity or a NaN gets a NaN scale: nothing it stands for is finite.
+ *   yq : [M, D] e4m3 output.   scale : [M] fp32 output.   Others as attn_rms_norm; D % 16 = 0.
+ */
+attn_status attn_rms_norm_q8(const void *x, const void *residual, const float *weight, void *yq,
+                             float *scale, void *h, int M, int D, float eps, cudaStream_t stream);
+
+/*
+ * Rows of x [M, D] bf16 as e4m3 with one fp32 scale each, by the rule of attn_rms_norm_q8(): the
+ * activations between two 8-bit products, and (as [N_out, K] rows) the weights of attn_linear_q8().
+ */
+attn_status attn_quantize_q8(const void *x, void *xq, float *scale, int M, int D, cudaStream_t stream);
+
+/*
+ * attn_linear() in 8 bits: z = x_scale[m] w_scale[n] (xq wq^T) + bias, y = act(z) + residual.
+ *   xq : [M, K] e4m3, x_scale : [M] fp32.   wq : [N_out, K] e4m3 (one row an output column),
+ *   w_scale : [N_out] fp32.   bias, residual, y as attn_linear.   K % 16 = 0, N_out % 8 = 0.
+ * e4m3 products (exact) summed in fp32.
+ */
+attn_status attn_linear_q8(const void *xq, const float *x_scale, const void *wq, const float *w_scale,
+                           const float *bias, const void *residual, void *y, int M, int K, int N_out,
+                           attn_activation act, cudaStream_t stream);
+
+/*
  * Bytes of device workspace attn_fwd_unfused() needs: the fp32 score matrix S [B,H,N,N] and the
  * bf16 probabilities P [B,H,N,N], each region 256-byte aligned (6 B H N^2 bytes and padding).
  * Returns 0 if the sizes are unsupported.

@@ -30,6 +30,12 @@ __all__ = [
     "vector_add", "attn_bwd_deterministic", "attn_qkv_proj", "attn_qkv_proj_bwd", "qkv_proj",
     "qkv_proj_backward",
     "forward", "forward_diagnostic", "backward", "attention",
+    "attn_linear", "attn_out_proj", "attn_linear_bwd", "attn_linear_bwd_workspace_size",
+    "attn_out_proj_bwd", "attn_out_proj_bwd_workspace_size", "attn_linear_q8", "attn_rms_norm",
+    "attn_rms_norm_bwd", "attn_rms_norm_bwd_workspace_size", "attn_rms_norm_q8", "attn_quantize_q8",
+    "linear_forward", "linear_backward", "linear", "out_proj_forward", "out_proj_backward", "out_proj",
+    "rms_norm_forward", "rms_norm_backward", "rms_norm", "rms_norm_q8", "quantize_q8", "linear_q8",
+    "ACTIVATIONS",
     "load_library", "STATUS",
 ]
 
@@ -42,7 +48,13 @@ EXPORTS = ("attn_fwd", "attn_fwd_workspace_size", "attn_fwd_with_workspace", "at
            "attn_bwd_main", "attn_bwd_dq_convert", "attn_get_device_status", "attn_status_string",
            "attn_last_error_string", "attn_debug_wait_timeout", "attn_bwd_noalloc", "vector_add",
            "attn_bwd_deterministic", "attn_qkv_proj", "attn_qkv_proj_bwd",
-           "attn_fwd_unfused", "attn_fwd_unfused_workspace_size")
+           "attn_fwd_unfused", "attn_fwd_unfused_workspace_size",
+           "attn_linear", "attn_out_proj", "attn_linear_bwd", "attn_linear_bwd_workspace_size",
+           "attn_out_proj_bwd", "attn_out_proj_bwd_workspace_size", "attn_linear_q8", "attn_rms_norm",
+           "attn_rms_norm_bwd", "attn_rms_norm_bwd_workspace_size", "attn_rms_norm_q8",
+           "attn_quantize_q8")
+# attn_activation
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
 
 class AttnError(RuntimeError):
@@ -108,6 +120,21 @@ def load_library(path: str = LIB_PATH):
     lib.attn_fwd_unfused.restype = _I
     lib.attn_debug_wait_timeout.argtypes = [ctypes.c_uint, _VP]
     lib.attn_debug_wait_timeout.restype = _I
+    for name, args in (("attn_linear", [_VP] * 6 + [_I] * 4 + [_VP]),
+                       ("attn_out_proj", [_VP] * 5 + [_I] * 5 + [_VP]),
+                       ("attn_linear_bwd", [_VP] * 8 + [_SZ] + [_I] * 4 + [_VP]),
+                       ("attn_out_proj_bwd", [_VP] * 7 + [_SZ] + [_I] * 5 + [_VP]),
+                       ("attn_linear_q8", [_VP] * 7 + [_I] * 4 + [_VP]),
+                       ("attn_rms_norm", [_VP] * 6 + [_I] * 2 + [_F, _VP]),
+                       ("attn_rms_norm_bwd", [_VP] * 8 + [_SZ] + [_I] * 2 + [_VP]),
+                       ("attn_rms_norm_q8", [_VP] * 6 + [_I] * 2 + [_F, _VP]),
+                       ("attn_quantize_q8", [_VP] * 3 + [_I] * 2 + [_VP])):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = _I
+    for name, n in (("attn_linear_bwd_workspace_size", 4), ("attn_out_proj_bwd_workspace_size", 5),
+                    ("attn_rms_norm_bwd_workspace_size", 2)):
+        getattr(lib, name).argtypes = [_I] * n
+        getattr(lib, name).restype = _SZ
     if path == LIB_PATH:
         _lib = lib
     return lib
@@ -250,6 +277,78 @@ def attn_qkv_proj_bwd(x, w_q, w_k, w_v, dq, dk, dv, dx, dw_q, dw_k, dw_v, B: int
     _raise(load_library().attn_qkv_proj_bwd(
         _ptr(x), _ptr(w_q), _ptr(w_k), _ptr(w_v), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dx),
         _ptr(dw_q), _ptr(dw_k), _ptr(dw_v), B, N, D, H, d_k, _stream(stream)), "attn_qkv_proj_bwd")
+
+
+def _opt(t):
+    """The address of an operand that may be left out."""
+    return None if t is None else _ptr(t)
+
+
+def attn_linear(x, w, bias, residual, y, z, M: int, K: int, N_out: int, act: int, stream=None):
+    """Enqueue y = act(x w + bias) + residual (bias, residual, z may be None)."""
+    _raise(load_library().attn_linear(_ptr(x), _ptr(w), _opt(bias), _opt(residual), _ptr(y), _opt(z), M, K,
+                                      N_out, int(act), _stream(stream)), "attn_linear")
+
+
+def attn_out_proj(o, w, bias, residual, y, B: int, H: int, N: int, d_k: int, N_out: int, stream=None):
+    """Enqueue the output projection of o [B,H,N,d_k] into y [B,N,N_out]."""
+    _raise(load_library().attn_out_proj(_ptr(o), _ptr(w), _opt(bias), _opt(residual), _ptr(y), B, H, N, d_k,
+                                        N_out, _stream(stream)), "attn_out_proj")
+
+
+def attn_linear_bwd_workspace_size(M: int, K: int, N_out: int, act: int) -> int:
+    return int(load_library().attn_linear_bwd_workspace_size(M, K, N_out, int(act)))
+
+
+def attn_out_proj_bwd_workspace_size(B: int, H: int, N: int, d_k: int, N_out: int) -> int:
+    return int(load_library().attn_out_proj_bwd_workspace_size(B, H, N, d_k, N_out))
+
+
+def attn_linear_bwd(x, w, dy, z, dx, dw, dbias, workspace, workspace_bytes: int, M: int, K: int, N_out: int,
+                    act: int, stream=None):
+    _raise(load_library().attn_linear_bwd(_ptr(x), _ptr(w), _ptr(dy), _opt(z), _opt(dx), _opt(dw), _opt(dbias),
+                                          _ptr(workspace), int(workspace_bytes), M, K, N_out, int(act),
+                                          _stream(stream)), "attn_linear_bwd")
+
+
+def attn_out_proj_bwd(o, w, dy, d_o, dw, dbias, workspace, workspace_bytes: int, B: int, H: int, N: int,
+                      d_k: int, N_out: int, stream=None):
+    _raise(load_library().attn_out_proj_bwd(_ptr(o), _ptr(w), _ptr(dy), _opt(d_o), _opt(dw), _opt(dbias),
+                                            _ptr(workspace), int(workspace_bytes), B, H, N, d_k, N_out,
+                                            _stream(stream)), "attn_out_proj_bwd")
+
+
+def attn_linear_q8(xq, x_scale, wq, w_scale, bias, residual, y, M: int, K: int, N_out: int, act: int,
+                   stream=None):
+    _raise(load_library().attn_linear_q8(_ptr(xq), _ptr(x_scale), _ptr(wq), _ptr(w_scale), _opt(bias),
+                                         _opt(residual), _ptr(y), M, K, N_out, int(act), _stream(stream)),
+           "attn_linear_q8")
+
+
+def attn_rms_norm(x, residual, weight, y, h, rstd, M: int, D: int, eps: float, stream=None):
+    _raise(load_library().attn_rms_norm(_ptr(x), _opt(residual), _ptr(weight), _ptr(y), _opt(h), _opt(rstd), M, D,
+                                        float(eps), _stream(stream)), "attn_rms_norm")
+
+
+def attn_rms_norm_bwd_workspace_size(M: int, D: int) -> int:
+    return int(load_library().attn_rms_norm_bwd_workspace_size(M, D))
+
+
+def attn_rms_norm_bwd(dy, h, weight, rstd, dh, dx, dweight, workspace, workspace_bytes: int, M: int, D: int,
+                      stream=None):
+    _raise(load_library().attn_rms_norm_bwd(_ptr(dy), _ptr(h), _ptr(weight), _ptr(rstd), _opt(dh), _ptr(dx),
+                                            _ptr(dweight), _ptr(workspace), int(workspace_bytes), M, D,
+                                            _stream(stream)), "attn_rms_norm_bwd")
+
+
+def attn_rms_norm_q8(x, residual, weight, yq, scale, h, M: int, D: int, eps: float, stream=None):
+    _raise(load_library().attn_rms_norm_q8(_ptr(x), _opt(residual), _ptr(weight), _ptr(yq), _ptr(scale), _opt(h),
+                                           M, D, float(eps), _stream(stream)), "attn_rms_norm_q8")
+
+
+def attn_quantize_q8(x, xq, scale, M: int, D: int, stream=None):
+    _raise(load_library().attn_quantize_q8(_ptr(x), _ptr(xq), _ptr(scale), M, D, _stream(stream)),
+           "attn_quantize_q8")
 
 
 def _scratch(nbytes: int, dev, st):
@@ -401,3 +500,303 @@ def attention(q, k, v, scale: float | None = None):
     """softmax(scale * Q K^T) V with autograd support."""
     D = q.shape[-1]
     return _Attention.apply(q, k, v, 1.0 / math.sqrt(D) if scale is None else scale)
+
+
+# ------------------------------------------------- the rest of the block: linear layers and norms
+_BF16, _F32, _E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+
+
+def _want(name, t, dtype, shape, dev):
+    """One operand: a contiguous tensor of this type and shape on this device."""
+    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}"
+                         f"{'' if t.is_contiguous() else ', not contiguous'}")
+
+
+def _rows(name, x, dtype=_BF16):
+    """[..., K] rows -> (M, K, device)."""
+    if not x.is_cuda or x.dtype is not dtype or x.dim() < 1 or not x.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} CUDA tensor [..., width]")
+    K = x.shape[-1]
+    return (x.numel() // K if K else 0), K, x.device
+
+
+def _act(activation) -> int:
+    act = ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"activation {activation!r}: one of {', '.join(ACTIVATIONS)}")
+    return act
+
+
+def _on(dev, stream, tensors, fn):
+    """fn(raw stream) with `dev` current.  On another stream than the device's current one the
+    operands are recorded on it, and what fn allocates belongs to it."""
+    if stream is None and torch.cuda.current_device() == dev.index:
+        return fn(torch._C._cuda_getCurrentRawStream(dev.index))
+    with torch.cuda.device(dev):
+        st = _device_stream(dev, stream)
+        if not isinstance(st, torch.cuda.Stream):
+            st = torch.cuda.ExternalStream(int(st), device=dev)
+        if st != torch.cuda.current_stream(dev):
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(st)
+        with torch.cuda.stream(st):
+            return fn(st.cuda_stream)
+
+
+def linear_forward(x, w, bias=None, residual=None, activation: str = "none", keep_z: bool = False, stream=None):
+    """y = act(x w + bias) + residual: x [..., K], w [K, N] bf16, bias [N] fp32, residual [..., N]
+    bf16.  Returns y [..., N] bf16, or (y, z) with keep_z: z is the pre-activation that
+    linear_backward() takes."""
+    act = _act(activation)
+    M, K, dev = _rows("x", x)
+    N = w.shape[-1]
+    shape = x.shape[:-1] + (N,)
+    _want("w", w, _BF16, (K, N), dev)
+    if bias is not None:
+        _want("bias", bias, _F32, (N,), dev)
+    if residual is not None:
+        _want("residual", residual, _BF16, shape, dev)
+
+    def call(st):
+        y = torch.empty(shape, dtype=_BF16, device=dev)
+        z = torch.empty(shape, dtype=_BF16, device=dev) if keep_z else None
+        attn_linear(x, w, bias, residual, y, z, M, K, N, act, st)
+        return (y, z) if keep_z else y
+
+    return _on(dev, stream, (x, w, bias, residual), call)
+
+
+def linear_backward(x, w, dy, z=None, activation: str = "none", bias: bool = True, need_dx: bool = True,
+                    need_dw: bool = True, stream=None):
+    """(dx [..., K] bf16, dw [K, N] bf16, dbias [N] fp32) of linear_forward() for dy = dL/dy; None
+    for what is not asked for.  z: what linear_forward(keep_z=True) kept (none without an
+    activation).  The residual's gradient is dy itself."""
+    act = _act(activation)
+    M, K, dev = _rows("x", x)
+    N = w.shape[-1]
+    _want("w", w, _BF16, (K, N), dev)
+    _want("dy", dy, _BF16, x.shape[:-1] + (N,), dev)
+    if act == 0:
+        z = None
+    elif z is None:
+        raise ValueError("linear_backward needs the pre-activation z that linear_forward(keep_z=True) returns")
+    else:
+        _want("z", z, _BF16, dy.shape, dev)
+
+    def call(st):
+        dx = torch.empty_like(x) if need_dx else None
+        dw = torch.empty_like(w) if need_dw else None
+        db = torch.empty(N, dtype=_F32, device=dev) if bias else None
+        nbytes = attn_linear_bwd_workspace_size(M, K, N, act)
+        ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
+        attn_linear_bwd(x, w, dy, z, dx, dw, db, ws, nbytes, M, K, N, act, st)
+        return dx, dw, db
+
+    return _on(dev, stream, (x, w, dy, z), call)
+
+
+def out_proj_forward(o, w, bias=None, residual=None, stream=None):
+    """Output projection of attention's o [B,H,N,d_k], heads side by side: y [B,N,N_out] = o w +
+    bias + residual, with w [H*d_k, N_out] bf16, bias [N_out] fp32, residual [B,N,N_out] bf16."""
+    B, H, N, D = _check_inputs(o)
+    dev, n_out = o.device, w.shape[-1]
+    _want("w", w, _BF16, (H * D, n_out), dev)
+    if bias is not None:
+        _want("bias", bias, _F32, (n_out,), dev)
+    if residual is not None:
+        _want("residual", residual, _BF16, (B, N, n_out), dev)
+
+    def call(st):
+        y = torch.empty((B, N, n_out), dtype=_BF16, device=dev)
+        attn_out_proj(o, w, bias, residual, y, B, H, N, D, n_out, st)
+        return y
+
+    return _on(dev, stream, (o, w, bias, residual), call)
+
+
+def out_proj_backward(o, w, dy, bias: bool = True, need_do: bool = True, need_dw: bool = True, stream=None):
+    """(do [B,H,N,d_k] bf16, dw [H*d_k,N_out] bf16, dbias [N_out] fp32) of out_proj_forward()."""
+    B, H, N, D = _check_inputs(o)
+    dev, n_out = o.device, w.shape[-1]
+    _want("w", w, _BF16, (H * D, n_out), dev)
+    _want("dy", dy, _BF16, (B, N, n_out), dev)
+
+    def call(st):
+        do = torch.empty_like(o) if need_do else None
+        dw = torch.empty_like(w) if need_dw else None
+        db = torch.empty(n_out, dtype=_F32, device=dev) if bias else None
+        nbytes = attn_out_proj_bwd_workspace_size(B, H, N, D, n_out)
+        ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
+        attn_out_proj_bwd(o, w, dy, do, dw, db, ws, nbytes, B, H, N, D, n_out, st)
+        return do, dw, db
+
+    return _on(dev, stream, (o, w, dy), call)
+
+
+def rms_norm_forward(x, weight, residual=None, eps: float = 1e-6, stream=None):
+    """(y, h, rstd): h = x + residual (x itself without one), rstd = 1/sqrt(mean(h^2) + eps),
+    y = h rstd weight.  x, residual [..., D] bf16, weight [D] fp32; rstd [...] fp32."""
+    M, D, dev = _rows("x", x)
+    _want("weight", weight, _F32, (D,), dev)
+    if residual is not None:
+        _want("residual", residual, _BF16, x.shape, dev)
+
+    def call(st):
+        y = torch.empty_like(x)
+        h = torch.empty_like(x) if residual is not None else None
+        rstd = torch.empty(x.shape[:-1], dtype=_F32, device=dev)
+        attn_rms_norm(x, residual, weight, y, h, rstd, M, D, eps, st)
+        return y, (x if h is None else h), rstd
+
+    return _on(dev, stream, (x, weight, residual), call)
+
+
+def rms_norm_backward(dy, h, weight, rstd, dh=None, stream=None):
+    """(dx [..., D] bf16, dweight [D] fp32) of rms_norm_forward(); dh is the gradient that reaches h
+    by its other uses.  dx is the gradient of x and of the residual alike."""
+    M, D, dev = _rows("h", h)
+    _want("dy", dy, _BF16, h.shape, dev)
+    _want("weight", weight, _F32, (D,), dev)
+    _want("rstd", rstd, _F32, h.shape[:-1], dev)
+    if dh is not None:
+        _want("dh", dh, _BF16, h.shape, dev)
+
+    def call(st):
+        dx = torch.empty_like(h)
+        dweight = torch.empty(D, dtype=_F32, device=dev)
+        nbytes = attn_rms_norm_bwd_workspace_size(M, D)
+        ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
+        attn_rms_norm_bwd(dy, h, weight, rstd, dh, dx, dweight, ws, nbytes, M, D, st)
+        return dx, dweight
+
+    return _on(dev, stream, (dy, h, weight, rstd, dh), call)
+
+
+def rms_norm_q8(x, weight, residual=None, eps: float = 1e-6, stream=None):
+    """(yq, scale, h): rms_norm_forward() with y as e4m3 rows, y ~ yq * scale[..., None]."""
+    M, D, dev = _rows("x", x)
+    _want("weight", weight, _F32, (D,), dev)
+    if residual is not None:
+        _want("residual", residual, _BF16, x.shape, dev)
+
+    def call(st):
+        yq = torch.empty(x.shape, dtype=_E4M3, device=dev)
+        scale = torch.empty(x.shape[:-1], dtype=_F32, device=dev)
+        h = torch.empty_like(x) if residual is not None else None
+        attn_rms_norm_q8(x, residual, weight, yq, scale, h, M, D, eps, st)
+        return yq, scale, (x if h is None else h)
+
+    return _on(dev, stream, (x, weight, residual), call)
+
+
+def quantize_q8(x, stream=None):
+    """(xq, scale): the rows of x [..., D] bf16 as e4m3 with one fp32 scale each.  The weights of
+    linear_q8() are quantize_q8(w.t().contiguous())."""
+    M, D, dev = _rows("x", x)
+
+    def call(st):
+        xq = torch.empty(x.shape, dtype=_E4M3, device=dev)
+        scale = torch.empty(x.shape[:-1], dtype=_F32, device=dev)
+        attn_quantize_q8(x, xq, scale, M, D, st)
+        return xq, scale
+
+    return _on(dev, stream, (x,), call)
+
+
+def linear_q8(xq, x_scale, wq, w_scale, bias=None, residual=None, activation: str = "none", stream=None):
+    """y [..., N] bf16 = act((xq wq^T) x_scale w_scale + bias) + residual: xq [..., K] and wq [N, K]
+    e4m3, x_scale [...] and w_scale [N] fp32 (as quantize_q8() and rms_norm_q8() make them)."""
+    act = _act(activation)
+    M, K, dev = _rows("xq", xq, _E4M3)
+    N = wq.shape[0]
+    shape = xq.shape[:-1] + (N,)
+    _want("x_scale", x_scale, _F32, xq.shape[:-1], dev)
+    _want("wq", wq, _E4M3, (N, K), dev)
+    _want("w_scale", w_scale, _F32, (N,), dev)
+    if bias is not None:
+        _want("bias", bias, _F32, (N,), dev)
+    if residual is not None:
+        _want("residual", residual, _BF16, shape, dev)
+
+    def call(st):
+        y = torch.empty(shape, dtype=_BF16, device=dev)
+        attn_linear_q8(xq, x_scale, wq, w_scale, bias, residual, y, M, K, N, act, st)
+        return y
+
+    return _on(dev, stream, (xq, x_scale, wq, w_scale, bias, residual), call)
+
+
+class _Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, bias, residual, activation):
+        keep = activation != "none" and any(ctx.needs_input_grad[:3])
+        out = linear_forward(x, w, bias, residual, activation, keep_z=keep)
+        y, z = out if keep else (out, None)
+        ctx.save_for_backward(x, w, z)
+        ctx.activation = activation
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, w, z = ctx.saved_tensors
+        need_x, need_w, need_b, need_r = ctx.needs_input_grad[:4]
+        dy = dy.contiguous()
+        dx = dw = db = None
+        if need_x or need_w or need_b:
+            dx, dw, db = linear_backward(x, w, dy, z, ctx.activation, bias=need_b, need_dx=need_x, need_dw=need_w)
+        return dx, dw, db, dy if need_r else None, None
+
+
+def linear(x, w, bias=None, residual=None, activation: str = "none"):
+    """act(x w + bias) + residual with autograd support (see linear_forward)."""
+    return _Linear.apply(x, w, bias, residual, activation)
+
+
+class _OutProj(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, o, w, bias, residual):
+        ctx.save_for_backward(o, w)
+        return out_proj_forward(o, w, bias, residual)
+
+    @staticmethod
+    def backward(ctx, dy):
+        o, w = ctx.saved_tensors
+        need_o, need_w, need_b, need_r = ctx.needs_input_grad
+        dy = dy.contiguous()
+        do = dw = db = None
+        if need_o or need_w or need_b:
+            do, dw, db = out_proj_backward(o, w, dy, bias=need_b, need_do=need_o, need_dw=need_w)
+        return do, dw, db, dy if need_r else None
+
+
+def out_proj(o, w, bias=None, residual=None):
+    """The output projection with autograd support (see out_proj_forward)."""
+    return _OutProj.apply(o, w, bias, residual)
+
+
+class _RmsNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps):
+        y, h, rstd = rms_norm_forward(x, weight, residual, eps)
+        ctx.save_for_backward(h, weight, rstd)
+        ctx.set_materialize_grads(False)
+        return (y, h) if residual is not None else y
+
+    @staticmethod
+    def backward(ctx, dy, dh=None):
+        h, weight, rstd = ctx.saved_tensors
+        need_x, need_w, need_r = ctx.needs_input_grad[:3]
+        if dy is None:      # only h was used (or nothing was)
+            return (dh if need_x else None, torch.zeros_like(weight) if need_w else None,
+                    dh if need_r else None, None)
+        dx, dweight = rms_norm_backward(dy.contiguous(), h, weight, rstd,
+                                        None if dh is None else dh.contiguous())
+        return dx if need_x else None, dweight if need_w else None, dx if need_r else None, None
+
+
+def rms_norm(x, weight, residual=None, eps: float = 1e-6):
+    """The norm with autograd support: y, or (y, h) with a residual (see rms_norm_forward)."""
+    return _RmsNorm.apply(x, weight, residual, eps)

@@ -756,3 +756,299 @@ extern "C" attn_status attn_bwd_noalloc(const void *q, const void *k, const void
     if (e == cudaSuccess) e = launch_bwd_convert(a, stream);
     return e == cudaSuccess ? ATTN_OK : fail("attn_bwd_noalloc launch", e);
 }
+
+// --------------------------------------------------------------------------------------------
+// Linear layers, the root-mean-square norm and their 8-bit forms.
+namespace {
+
+bool width_ok(long long w, int unit) { return w >= unit && w % unit == 0 && w < (1LL << 20); }
+
+bool size_ok(long long rows, long long width) { return rows * width < (1LL << 40); }
+
+// Alignment of the given pointers, and that no output range touches another output or an input;
+// `same` is an output that may be exactly the input `same_in`.  Null pointers are skipped.
+struct Operand {
+    const void *p;
+    size_t bytes;
+};
+
+template <int NI, int NO>
+attn_status check_operands(const Operand (&ins)[NI], const Operand (&outs)[NO], const void *same = nullptr,
+                           const void *same_in = nullptr, const void *same_in2 = nullptr)
+{
+    for (const Operand &o : ins)
+        if (o.p && !aligned16(o.p)) return ATTN_ERR_MISALIGNED;
+    for (const Operand &o : outs)
+        if (o.p && !aligned16(o.p)) return ATTN_ERR_MISALIGNED;
+    for (int i = 0; i < NO; ++i) {
+        if (!outs[i].p) continue;
+        const Range r = span(outs[i].p, outs[i].bytes);
+        for (const Operand &o : ins) {
+            if (!o.p || !overlap(r, span(o.p, o.bytes))) continue;
+            if (outs[i].p == same && o.p == same && (o.p == same_in || o.p == same_in2)) continue;
+            return ATTN_ERR_INVALID_ARG;
+        }
+        for (int j = i + 1; j < NO; ++j)
+            if (outs[j].p && overlap(r, span(outs[j].p, outs[j].bytes))) return ATTN_ERR_INVALID_ARG;
+    }
+    return ATTN_OK;
+}
+
+attn_status check_linear_sizes(long long M, long long K, long long N_out, int act, int unit)
+{
+    if (M < 0 || M > 0x7fffffffLL || !width_ok(K, unit) || !width_ok(N_out, 8)) return ATTN_ERR_INVALID_ARG;
+    if (!size_ok(M, K) || !size_ok(M, N_out)) return ATTN_ERR_INVALID_ARG;
+    if (act < ATTN_ACT_NONE || act > ATTN_ACT_SILU) return ATTN_ERR_INVALID_ARG;
+    return ATTN_OK;
+}
+
+// Heads side by side: sizes of the [B, H, N, d_k] view of the output projection's input.
+attn_status check_heads(int B, int H, int N, int d_k)
+{
+    if (d_k != 64 && d_k != 128) return ATTN_ERR_UNSUPPORTED_DK;
+    if (B < 1 || H < 1 || N < 1 || (long long)B * N > 0x7fffffffLL || (long long)B * H > 0x7fffffffLL ||
+        (long long)H * d_k >= (1LL << 20))
+        return ATTN_ERR_INVALID_ARG;
+    return ATTN_OK;
+}
+
+attn_status run_linear(LinArgs &a, cudaStream_t stream, const char *what)
+{
+    if (!a.x || !a.w || !a.y || (a.q8 && (!a.x_scale || !a.w_scale))) return ATTN_ERR_INVALID_ARG;
+    const size_t M = a.M, K = a.K, N = a.N, es = a.q8 ? 1 : 2;
+    const Operand ins[6] = {{a.x, M * K * es}, {a.w, K * N * es}, {a.bias, N * 4}, {a.residual, M * N * 2},
+                            {a.x_scale, M * 4}, {a.w_scale, N * 4}};
+    const Operand outs[2] = {{a.y, M * N * 2}, {a.z, M * N * 2}};
+    attn_status st = check_operands(ins, outs, a.y, a.residual);
+    if (st != ATTN_OK) return st;
+    DeviceState *dev = nullptr;
+    if ((st = device_state(&dev)) != ATTN_OK) return st;
+    a.status = dev->status;
+    const cudaError_t e = launch_linear(a, stream);
+    return e == cudaSuccess ? ATTN_OK : fail(what, e);
+}
+
+struct LinBwdLayout {
+    size_t dz_off, col_off, dw_off, total;
+};
+
+LinBwdLayout lin_bwd_layout(int G, int T, int M, int K, int N, int act)
+{
+    LinBwdLayout l;
+    l.dz_off = 0;
+    l.col_off = act != ATTN_ACT_NONE ? align256((size_t)M * N * 2) : 0;
+    l.dw_off = l.col_off + align256((size_t)lin_bwd_row_blocks(M, N) * N * 4);
+    const int splits = lin_dw_splits(G, T, K, N);
+    l.total = l.dw_off + (splits > 1 ? align256((size_t)splits * K * N * 4) : 0);
+    return l;
+}
+
+attn_status run_linear_bwd(LinBwdArgs &a, void *workspace, size_t workspace_bytes, cudaStream_t stream,
+                           const char *what)
+{
+    const size_t M = a.M, K = a.K, N = a.N;
+    if (!a.w || (M > 0 && (!a.x || !a.dy || (a.act != ATTN_ACT_NONE && !a.z)))) return ATTN_ERR_INVALID_ARG;
+    if (a.act == ATTN_ACT_NONE) a.z = nullptr;
+    const LinBwdLayout l = lin_bwd_layout(a.G, a.T, a.M, a.K, a.N, a.act);
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < l.total)
+        return ATTN_ERR_WORKSPACE;
+    const Operand ins[4] = {{a.x, M * K * 2}, {a.w, K * N * 2}, {a.dy, M * N * 2}, {a.z, M * N * 2}};
+    const Operand outs[4] = {{a.dx, M * K * 2}, {a.dw, K * N * 2}, {a.dbias, N * 4}, {workspace, l.total}};
+    attn_status st = check_operands(ins, outs);
+    if (st != ATTN_OK) return st;
+    DeviceState *dev = nullptr;
+    if ((st = device_state(&dev)) != ATTN_OK) return st;
+    a.status = dev->status;
+    char *ws = static_cast<char *>(workspace);
+    a.dz = ws + l.dz_off;
+    a.col_part = reinterpret_cast<float *>(ws + l.col_off);
+    a.dw_part = reinterpret_cast<float *>(ws + l.dw_off);
+    cudaError_t e;
+    if (M == 0) {   // no rows: the sums are zero
+        e = a.dw ? cudaMemsetAsync(a.dw, 0, K * N * 2, stream) : cudaSuccess;
+        if (e == cudaSuccess && a.dbias) e = cudaMemsetAsync(a.dbias, 0, N * 4, stream);
+    } else {
+        e = launch_linear_bwd(a, stream);
+    }
+    return e == cudaSuccess ? ATTN_OK : fail(what, e);
+}
+
+}  // namespace
+
+extern "C" attn_status attn_linear(const void *x, const void *w, const float *bias, const void *residual,
+                                   void *y, void *z, int M, int K, int N_out, attn_activation act,
+                                   cudaStream_t stream)
+{
+    attn_status st = check_linear_sizes(M, K, N_out, act, 8);
+    if (st != ATTN_OK) return st;
+    if (M == 0) return ATTN_OK;
+    LinArgs a = {};
+    a.x = x; a.w = w; a.bias = bias; a.residual = residual; a.y = y; a.z = z;
+    a.G = a.H = 1; a.T = M; a.dk = K;
+    a.M = M; a.K = K; a.N = N_out; a.act = act;
+    return run_linear(a, stream, "attn_linear launch");
+}
+
+extern "C" attn_status attn_out_proj(const void *o, const void *w, const float *bias, const void *residual,
+                                     void *y, int B, int H, int N, int d_k, int N_out, cudaStream_t stream)
+{
+    attn_status st = check_heads(B, H, N, d_k);
+    if (st == ATTN_OK) st = check_linear_sizes((long long)B * N, (long long)H * d_k, N_out, ATTN_ACT_NONE, 8);
+    if (st != ATTN_OK) return st;
+    LinArgs a = {};
+    a.x = o; a.w = w; a.bias = bias; a.residual = residual; a.y = y;
+    a.G = B; a.H = H; a.T = N; a.dk = d_k;
+    a.M = B * N; a.K = H * d_k; a.N = N_out; a.act = ATTN_ACT_NONE;
+    return run_linear(a, stream, "attn_out_proj launch");
+}
+
+extern "C" attn_status attn_linear_q8(const void *xq, const float *x_scale, const void *wq,
+                                      const float *w_scale, const float *bias, const void *residual, void *y,
+                                      int M, int K, int N_out, attn_activation act, cudaStream_t stream)
+{
+    attn_status st = check_linear_sizes(M, K, N_out, act, 16);
+    if (st != ATTN_OK) return st;
+    if (M == 0) return ATTN_OK;
+    LinArgs a = {};
+    a.x = xq; a.w = wq; a.x_scale = x_scale; a.w_scale = w_scale;
+    a.bias = bias; a.residual = residual; a.y = y;
+    a.G = a.H = 1; a.T = M; a.dk = K;
+    a.M = M; a.K = K; a.N = N_out; a.act = act; a.q8 = 1;
+    return run_linear(a, stream, "attn_linear_q8 launch");
+}
+
+extern "C" size_t attn_linear_bwd_workspace_size(int M, int K, int N_out, attn_activation act)
+{
+    if (check_linear_sizes(M, K, N_out, act, 8) != ATTN_OK) return 0;
+    return lin_bwd_layout(1, M, M, K, N_out, act).total;
+}
+
+extern "C" size_t attn_out_proj_bwd_workspace_size(int B, int H, int N, int d_k, int N_out)
+{
+    if (check_heads(B, H, N, d_k) != ATTN_OK ||
+        check_linear_sizes((long long)B * N, (long long)H * d_k, N_out, ATTN_ACT_NONE, 8) != ATTN_OK)
+        return 0;
+    return lin_bwd_layout(B, N, B * N, H * d_k, N_out, ATTN_ACT_NONE).total;
+}
+
+extern "C" attn_status attn_linear_bwd(const void *x, const void *w, const void *dy, const void *z, void *dx,
+                                       void *dw, float *dbias, void *workspace, size_t workspace_bytes, int M,
+                                       int K, int N_out, attn_activation act, cudaStream_t stream)
+{
+    attn_status st = check_linear_sizes(M, K, N_out, act, 8);
+    if (st != ATTN_OK) return st;
+    LinBwdArgs a = {};
+    a.x = x; a.w = w; a.dy = dy; a.z = z; a.dx = dx; a.dw = dw; a.dbias = dbias;
+    a.G = a.H = 1; a.T = M; a.dk = K;
+    a.M = M; a.K = K; a.N = N_out; a.act = act;
+    return run_linear_bwd(a, workspace, workspace_bytes, stream, "attn_linear_bwd launch");
+}
+
+extern "C" attn_status attn_out_proj_bwd(const void *o, const void *w, const void *dy, void *d_o, void *dw,
+                                         float *dbias, void *workspace, size_t workspace_bytes, int B, int H,
+                                         int N, int d_k, int N_out, cudaStream_t stream)
+{
+    attn_status st = check_heads(B, H, N, d_k);
+    if (st == ATTN_OK) st = check_linear_sizes((long long)B * N, (long long)H * d_k, N_out, ATTN_ACT_NONE, 8);
+    if (st != ATTN_OK) return st;
+    LinBwdArgs a = {};
+    a.x = o; a.w = w; a.dy = dy; a.dx = d_o; a.dw = dw; a.dbias = dbias;
+    a.G = B; a.H = H; a.T = N; a.dk = d_k;
+    a.M = B * N; a.K = H * d_k; a.N = N_out; a.act = ATTN_ACT_NONE;
+    return run_linear_bwd(a, workspace, workspace_bytes, stream, "attn_out_proj_bwd launch");
+}
+
+namespace {
+
+attn_status check_norm_sizes(int M, int D, float eps, int unit)
+{
+    if (M < 0 || !width_ok(D, unit) || !size_ok(M, D)) return ATTN_ERR_INVALID_ARG;
+    return std::isfinite(eps) && eps >= 0.f ? ATTN_OK : ATTN_ERR_INVALID_ARG;
+}
+
+attn_status run_norm(const NormArgs &a, cudaStream_t stream, const char *what)
+{
+    if (!a.x || !a.y || (a.q8 && !a.scale) || (a.h && !a.residual)) return ATTN_ERR_INVALID_ARG;
+    const size_t M = a.M, D = a.D;
+    const Operand ins[3] = {{a.x, M * D * 2}, {a.residual, M * D * 2}, {a.weight, D * 4}};
+    const Operand outs[4] = {{a.y, M * D * (a.q8 ? 1 : 2)}, {a.scale, M * 4}, {a.h, M * D * 2}, {a.rstd, M * 4}};
+    attn_status st = check_operands(ins, outs, a.h, a.x, a.residual);
+    if (st != ATTN_OK) return st;
+    DeviceState *dev = nullptr;
+    if ((st = device_state(&dev)) != ATTN_OK) return st;
+    const cudaError_t e = launch_rms_norm(a, stream);
+    return e == cudaSuccess ? ATTN_OK : fail(what, e);
+}
+
+}  // namespace
+
+extern "C" attn_status attn_rms_norm(const void *x, const void *residual, const float *weight, void *y,
+                                     void *h, float *rstd, int M, int D, float eps, cudaStream_t stream)
+{
+    attn_status st = check_norm_sizes(M, D, eps, 8);
+    if (st != ATTN_OK) return st;
+    if (M == 0) return ATTN_OK;
+    if (!weight) return ATTN_ERR_INVALID_ARG;
+    NormArgs a = {};
+    a.x = x; a.residual = residual; a.weight = weight; a.y = y; a.h = h; a.rstd = rstd;
+    a.M = M; a.D = D; a.eps = eps;
+    return run_norm(a, stream, "attn_rms_norm launch");
+}
+
+extern "C" attn_status attn_rms_norm_q8(const void *x, const void *residual, const float *weight, void *yq,
+                                        float *scale, void *h, int M, int D, float eps, cudaStream_t stream)
+{
+    attn_status st = check_norm_sizes(M, D, eps, 16);
+    if (st != ATTN_OK) return st;
+    if (M == 0) return ATTN_OK;
+    if (!weight) return ATTN_ERR_INVALID_ARG;
+    NormArgs a = {};
+    a.x = x; a.residual = residual; a.weight = weight; a.y = yq; a.scale = scale; a.h = h;
+    a.M = M; a.D = D; a.eps = eps; a.q8 = 1;
+    return run_norm(a, stream, "attn_rms_norm_q8 launch");
+}
+
+extern "C" attn_status attn_quantize_q8(const void *x, void *xq, float *scale, int M, int D,
+                                        cudaStream_t stream)
+{
+    attn_status st = check_norm_sizes(M, D, 0.f, 16);
+    if (st != ATTN_OK) return st;
+    if (M == 0) return ATTN_OK;
+    NormArgs a = {};
+    a.x = x; a.y = xq; a.scale = scale; a.M = M; a.D = D; a.q8 = 1;
+    return run_norm(a, stream, "attn_quantize_q8 launch");
+}
+
+extern "C" size_t attn_rms_norm_bwd_workspace_size(int M, int D)
+{
+    if (check_norm_sizes(M, D, 0.f, 8) != ATTN_OK) return 0;
+    return align256((size_t)norm_bwd_blocks(M, D) * D * 4);
+}
+
+extern "C" attn_status attn_rms_norm_bwd(const void *dy, const void *h, const float *weight, const float *rstd,
+                                         const void *dh, void *dx, float *dweight, void *workspace,
+                                         size_t workspace_bytes, int M, int D, cudaStream_t stream)
+{
+    attn_status st = check_norm_sizes(M, D, 0.f, 8);
+    if (st != ATTN_OK) return st;
+    if (!weight || !dweight || (M > 0 && (!dy || !h || !rstd || !dx))) return ATTN_ERR_INVALID_ARG;
+    const size_t need = attn_rms_norm_bwd_workspace_size(M, D), m = M, d = D;
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < need)
+        return ATTN_ERR_WORKSPACE;
+    const Operand ins[5] = {{dy, m * d * 2}, {h, m * d * 2}, {weight, d * 4}, {rstd, m * 4}, {dh, m * d * 2}};
+    const Operand outs[3] = {{dx, m * d * 2}, {dweight, d * 4}, {workspace, need}};
+    if ((st = check_operands(ins, outs, dx, dh)) != ATTN_OK) return st;
+    DeviceState *dev = nullptr;
+    if ((st = device_state(&dev)) != ATTN_OK) return st;
+    cudaError_t e;
+    if (M == 0) {
+        e = cudaMemsetAsync(dweight, 0, d * 4, stream);
+    } else {
+        NormBwdArgs a = {};
+        a.dy = dy; a.h = h; a.dh = dh; a.weight = weight; a.rstd = rstd; a.dx = dx; a.dweight = dweight;
+        a.part = static_cast<float *>(workspace);
+        a.M = M; a.D = D;
+        e = launch_rms_norm_bwd(a, stream);
+    }
+    return e == cudaSuccess ? ATTN_OK : fail("attn_rms_norm_bwd launch", e);
+}

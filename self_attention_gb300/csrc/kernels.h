@@ -75,6 +75,62 @@ cudaError_t launch_proj_dw(const ProjMaps &m, const ProjArgs &a, cudaStream_t st
 const char *launch_fwd_unfused(const FwdArgs &a, const void *q, const void *k, const void *v, float *s,
                                void *p, cudaStream_t stream, cudaError_t *err);
 
+// Linear layers (see linear.cu).  The x side is seen as [G, H, T, dk]: row m = g T + i, column
+// c = h dk + e; a plain [M, K] matrix is G = H = 1, T = M, dk = K.
+struct LinArgs {
+    const void *x, *w;               // bf16 [G,H,T,dk], [K,N]; q8: e4m3 [M,K], [N,K]
+    const float *x_scale, *w_scale;  // q8: [M], [N]
+    const float *bias;               // null, or [N]
+    const void *residual;            // null, or [M,N] bf16
+    void *y, *z;                     // [M,N] bf16; z may be null
+    int G, T, H, dk;
+    int M, K, N;
+    int act, q8;
+    int *status;
+};
+cudaError_t launch_linear(const LinArgs &a, cudaStream_t stream);
+
+struct LinBwdArgs {
+    const void *x, *w, *dy, *z;      // z null: dz is dy
+    void *dx, *dw;                   // bf16, each may be null
+    float *dbias;                    // null, or [N]
+    void *dz;                        // workspace: [M,N] bf16 (z given)
+    float *col_part;                 // workspace: partial column sums, lin_bwd_row_blocks() x [N]
+    float *dw_part;                  // workspace: lin_dw_splits() x [K,N] where that is > 1
+    int G, T, H, dk;
+    int M, K, N;
+    int act;
+    int *status;
+};
+// The plan of the backward, a function of the sizes alone: how many blocks of rows the column
+// sums are taken in, and how many ways the rows of dw = x^T dz are split.
+int lin_bwd_row_blocks(int M, int N);
+int lin_dw_splits(int G, int T, int K, int N);
+cudaError_t launch_linear_bwd(const LinBwdArgs &a, cudaStream_t stream);
+
+// Root-mean-square norm (see norm.cu).
+struct NormArgs {
+    const void *x, *residual;   // bf16 [M,D]
+    const float *weight;        // [D]; null: no norm, the rows themselves are quantised (q8)
+    void *y;                    // bf16 or e4m3
+    float *scale;               // q8: [M]
+    void *h;                    // null, or bf16 [M,D]
+    float *rstd;                // null, or [M]
+    int M, D, q8;
+    float eps;
+};
+cudaError_t launch_rms_norm(const NormArgs &a, cudaStream_t stream);
+struct NormBwdArgs {
+    const void *dy, *h, *dh;
+    const float *weight, *rstd;
+    void *dx;
+    float *dweight;
+    float *part;                // workspace: norm_bwd_blocks() x [D]
+    int M, D;
+};
+int norm_bwd_blocks(int M, int D);
+cudaError_t launch_rms_norm_bwd(const NormBwdArgs &a, cudaStream_t stream);
+
 cudaError_t launch_vector_add(const float *a, const float *b, float *c, long long n,
                               cudaStream_t stream);
 cudaError_t launch_wait_selftest(int *status, uint64_t limit_ns, cudaStream_t stream);
