@@ -234,7 +234,7 @@ attn_status attn_qkv_proj_bwd(const void *x, const void *w_q, const void *w_k, c
  *     vectors (bias, norm weight, scales, 1/rms) are fp32.  M counts rows (tokens), 0 <= M < 2^31;
  *     with M = 0 the forward calls do nothing and the backward calls write zeros to the gradients
  *     of the parameters.
- *   - Widths (K, N_out, D) are multiples of 8 (16 for e4m3 rows) and below 2^20; no operand holds
+ *   - Widths (K, N_out, D) are multiples of 8 (K of e4m3 operands: 16) and below 2^20; no operand holds
  *     2^40 elements or more.  Other widths are refused with ATTN_ERR_INVALID_ARG.
  *   - Pointers are 16-byte aligned, and outputs overlap no input and no other output, except
  *     where an entry point allows it by name.
@@ -302,7 +302,8 @@ attn_status attn_out_proj_bwd(const void *o, const void *w, const void *dy, void
  *   y : [M, D] bf16 output.   rstd : [M] fp32 output or null, kept for attn_rms_norm_bwd().
  *   h : [M, D] bf16 output or null; may be x or residual itself.  Without a residual it is not
  *       written and must be null.
- * The statistics and y are taken from the unrounded fp32 sum; h and y are each rounded once.
+ * The statistics and y are taken from the unrounded fp32 sum; h and y are each rounded once.  The
+ * sum of a row's squares has to fit fp32.
  */
 attn_status attn_rms_norm(const void *x, const void *residual, const float *weight, void *y, void *h,
                           float *rstd, int M, int D, float eps, cudaStream_t stream);
@@ -326,7 +327,7 @@ attn_status attn_rms_norm_bwd(const void *dy, const void *h, const float *weight
  * attn_rms_norm() with y in e4m3 and one fp32 scale a row:
  *   scale = max(max |y|, 1e-30) / 448;  yq = y / scale rounded to nearest e4m3.
  * A row that holds an infinity or a NaN gets a NaN scale: nothing it stands for is finite.
- *   yq : [M, D] e4m3 output.   scale : [M] fp32 output.   Others as attn_rms_norm; D % 16 = 0.
+ *   yq : [M, D] e4m3 output.   scale : [M] fp32 output.   Others as attn_rms_norm.
  */
 attn_status attn_rms_norm_q8(const void *x, const void *residual, const float *weight, void *yq,
                              float *scale, void *h, int M, int D, float eps, cudaStream_t stream);

@@ -146,6 +146,19 @@ attn_status check_sizes(int B, int H, int N, int d_k, float scale)
 }  // namespace
 }  // namespace attn
 
+CUresult attn::make_map_3d(CUtensorMap *m, const void *base, CUtensorMapDataType type, int elem_bytes, long long d0,
+                           long long d1, long long d2, int box0, int box1)
+{
+    cuuint64_t dims[3] = {(cuuint64_t)d0, (cuuint64_t)d1, (cuuint64_t)d2};
+    // the stride of a single outermost slice is never used, but has to stay in the encodable range
+    cuuint64_t strides[2] = {(cuuint64_t)d0 * elem_bytes, (cuuint64_t)d0 * elem_bytes * (d2 > 1 ? d1 : 1)};
+    cuuint32_t box[3] = {(cuuint32_t)box0, (cuuint32_t)box1, 1};
+    cuuint32_t elem[3] = {1, 1, 1};
+    return g_encode(m, type, 3, const_cast<void *>(base), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
 using namespace attn;
 
 namespace {
@@ -812,6 +825,17 @@ attn_status check_heads(int B, int H, int N, int d_k)
     return ATTN_OK;
 }
 
+// The [B, H, N, d_k] view of x.  With one token a sequence it is the plain [B, H * d_k] matrix.
+template <class Args>
+void set_heads(Args &a, int B, int H, int N, int d_k)
+{
+    const bool plain = N == 1 || H == 1;
+    a.G = plain ? 1 : B;
+    a.H = plain ? 1 : H;
+    a.T = plain ? B * N : N;
+    a.dk = plain ? H * d_k : d_k;
+}
+
 attn_status run_linear(LinArgs &a, cudaStream_t stream, const char *what)
 {
     if (!a.x || !a.w || !a.y || (a.q8 && (!a.x_scale || !a.w_scale))) return ATTN_ERR_INVALID_ARG;
@@ -897,7 +921,7 @@ extern "C" attn_status attn_out_proj(const void *o, const void *w, const float *
     if (st != ATTN_OK) return st;
     LinArgs a = {};
     a.x = o; a.w = w; a.bias = bias; a.residual = residual; a.y = y;
-    a.G = B; a.H = H; a.T = N; a.dk = d_k;
+    set_heads(a, B, H, N, d_k);
     a.M = B * N; a.K = H * d_k; a.N = N_out; a.act = ATTN_ACT_NONE;
     return run_linear(a, stream, "attn_out_proj launch");
 }
@@ -928,7 +952,9 @@ extern "C" size_t attn_out_proj_bwd_workspace_size(int B, int H, int N, int d_k,
     if (check_heads(B, H, N, d_k) != ATTN_OK ||
         check_linear_sizes((long long)B * N, (long long)H * d_k, N_out, ATTN_ACT_NONE, 8) != ATTN_OK)
         return 0;
-    return lin_bwd_layout(B, N, B * N, H * d_k, N_out, ATTN_ACT_NONE).total;
+    LinBwdArgs a = {};
+    set_heads(a, B, H, N, d_k);
+    return lin_bwd_layout(a.G, a.T, B * N, H * d_k, N_out, ATTN_ACT_NONE).total;
 }
 
 extern "C" attn_status attn_linear_bwd(const void *x, const void *w, const void *dy, const void *z, void *dx,
@@ -953,16 +979,16 @@ extern "C" attn_status attn_out_proj_bwd(const void *o, const void *w, const voi
     if (st != ATTN_OK) return st;
     LinBwdArgs a = {};
     a.x = o; a.w = w; a.dy = dy; a.dx = d_o; a.dw = dw; a.dbias = dbias;
-    a.G = B; a.H = H; a.T = N; a.dk = d_k;
+    set_heads(a, B, H, N, d_k);
     a.M = B * N; a.K = H * d_k; a.N = N_out; a.act = ATTN_ACT_NONE;
     return run_linear_bwd(a, workspace, workspace_bytes, stream, "attn_out_proj_bwd launch");
 }
 
 namespace {
 
-attn_status check_norm_sizes(int M, int D, float eps, int unit)
+attn_status check_norm_sizes(int M, int D, float eps)
 {
-    if (M < 0 || !width_ok(D, unit) || !size_ok(M, D)) return ATTN_ERR_INVALID_ARG;
+    if (M < 0 || !width_ok(D, 8) || !size_ok(M, D)) return ATTN_ERR_INVALID_ARG;
     return std::isfinite(eps) && eps >= 0.f ? ATTN_OK : ATTN_ERR_INVALID_ARG;
 }
 
@@ -985,7 +1011,7 @@ attn_status run_norm(const NormArgs &a, cudaStream_t stream, const char *what)
 extern "C" attn_status attn_rms_norm(const void *x, const void *residual, const float *weight, void *y,
                                      void *h, float *rstd, int M, int D, float eps, cudaStream_t stream)
 {
-    attn_status st = check_norm_sizes(M, D, eps, 8);
+    attn_status st = check_norm_sizes(M, D, eps);
     if (st != ATTN_OK) return st;
     if (M == 0) return ATTN_OK;
     if (!weight) return ATTN_ERR_INVALID_ARG;
@@ -998,7 +1024,7 @@ extern "C" attn_status attn_rms_norm(const void *x, const void *residual, const 
 extern "C" attn_status attn_rms_norm_q8(const void *x, const void *residual, const float *weight, void *yq,
                                         float *scale, void *h, int M, int D, float eps, cudaStream_t stream)
 {
-    attn_status st = check_norm_sizes(M, D, eps, 16);
+    attn_status st = check_norm_sizes(M, D, eps);
     if (st != ATTN_OK) return st;
     if (M == 0) return ATTN_OK;
     if (!weight) return ATTN_ERR_INVALID_ARG;
@@ -1011,7 +1037,7 @@ extern "C" attn_status attn_rms_norm_q8(const void *x, const void *residual, con
 extern "C" attn_status attn_quantize_q8(const void *x, void *xq, float *scale, int M, int D,
                                         cudaStream_t stream)
 {
-    attn_status st = check_norm_sizes(M, D, 0.f, 16);
+    attn_status st = check_norm_sizes(M, D, 0.f);
     if (st != ATTN_OK) return st;
     if (M == 0) return ATTN_OK;
     NormArgs a = {};
@@ -1021,7 +1047,7 @@ extern "C" attn_status attn_quantize_q8(const void *x, void *xq, float *scale, i
 
 extern "C" size_t attn_rms_norm_bwd_workspace_size(int M, int D)
 {
-    if (check_norm_sizes(M, D, 0.f, 8) != ATTN_OK) return 0;
+    if (check_norm_sizes(M, D, 0.f) != ATTN_OK) return 0;
     return align256((size_t)norm_bwd_blocks(M, D) * D * 4);
 }
 
@@ -1029,7 +1055,7 @@ extern "C" attn_status attn_rms_norm_bwd(const void *dy, const void *h, const fl
                                          const void *dh, void *dx, float *dweight, void *workspace,
                                          size_t workspace_bytes, int M, int D, cudaStream_t stream)
 {
-    attn_status st = check_norm_sizes(M, D, 0.f, 8);
+    attn_status st = check_norm_sizes(M, D, 0.f);
     if (st != ATTN_OK) return st;
     if (!weight || !dweight || (M > 0 && (!dy || !h || !rstd || !dx))) return ATTN_ERR_INVALID_ARG;
     const size_t need = attn_rms_norm_bwd_workspace_size(M, D), m = M, d = D;

@@ -75,6 +75,11 @@ cudaError_t launch_proj_dw(const ProjMaps &m, const ProjArgs &a, cudaStream_t st
 const char *launch_fwd_unfused(const FwdArgs &a, const void *q, const void *k, const void *v, float *s,
                                void *p, cudaStream_t stream, cudaError_t *err);
 
+// 3-D tensor map (innermost first: d0, d1, d2 elements, dense) with boxes of box0 x box1 x 1 and
+// the 128-byte swizzle; elements outside read as zeros and are not written.
+CUresult make_map_3d(CUtensorMap *m, const void *base, CUtensorMapDataType type, int elem_bytes, long long d0,
+                     long long d1, long long d2, int box0, int box1);
+
 // Linear layers (see linear.cu).  The x side is seen as [G, H, T, dk]: row m = g T + i, column
 // c = h dk + e; a plain [M, K] matrix is G = H = 1, T = M, dk = K.
 struct LinArgs {
@@ -128,6 +133,8 @@ struct NormBwdArgs {
     float *part;                // workspace: norm_bwd_blocks() x [D]
     int M, D;
 };
+// out[c] = sum over rows of part[row][c], in a fixed order.
+cudaError_t launch_sum_rows(const float *part, float *out, int rows, int cols, cudaStream_t stream);
 int norm_bwd_blocks(int M, int D);
 cudaError_t launch_rms_norm_bwd(const NormBwdArgs &a, cudaStream_t stream);
 

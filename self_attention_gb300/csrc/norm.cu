@@ -1,135 +1,416 @@
 // Root-mean-square norm with the residual's addition, its 8-bit form and its backward.
+//
+// All of it is bound by HBM: each row is read once into registers, reduced, and written once.  A row
+// is taken by a warp (up to 2048 columns; no barrier, only shuffles), by 256 threads (to 16384) or
+// by 1024 threads (to 32768), each thread holding chunks of 8 neighbouring columns (16-byte loads);
+// longer rows are read a second time from L2.
 #include "common.cuh"
 #include "kernels.h"
-
-#include <cuda_fp8.h>
 
 namespace attn {
 namespace {
 
 constexpr float kQ8Max = 448.f;      // largest e4m3
 constexpr float kAmaxFloor = 1e-30f;
+constexpr int kPlanSms = 152;        // the plan of the backward is a function of the sizes alone
 
-__device__ __forceinline__ float bf(const void *p, size_t i)
+__device__ __forceinline__ float add(float a, float b) { return a + b; }
+__device__ __forceinline__ float max_nan(float a, float b)
 {
-    return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
 }
 
-template <bool MAX>
-__device__ __forceinline__ float block_reduce(float v)
+__device__ __forceinline__ void unpack8(const uint4 &u, float (&f)[8])
 {
-    __shared__ float part[32], all;
-    __syncthreads();
-    auto op = [](float a, float b) {
-        float r;
-        if (MAX)
-            asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-        else
-            r = a + b;
-        return r;
-    };
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        f[2 * e] = __uint_as_float(w[e] << 16);
+        f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+    }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&f)[8])
+{
+    return make_uint4(ptx::pack_bf16x2(f[0], f[1]), ptx::pack_bf16x2(f[2], f[3]), ptx::pack_bf16x2(f[4], f[5]),
+                      ptx::pack_bf16x2(f[6], f[7]));
+}
+
+// Two fp32 values -> two e4m3 (round to nearest even, saturating); `lo` in the low byte.
+__device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ void load8(const float *p, float (&f)[8])
+{
+    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+}
+
+// Reduction over the TPR threads that hold a row (a warp, or the whole block).
+template <int TPR, class Op>
+__device__ __forceinline__ float row_reduce(float v, Op op)
+{
+#pragma unroll
     for (int o = 16; o; o >>= 1) v = op(v, __shfl_xor_sync(~0u, v, o));
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        float t = part[0];
-        for (unsigned i = 1; i < blockDim.x / 32; ++i) t = op(t, part[i]);
-        all = t;
+    if constexpr (TPR > 32) {
+        __shared__ float part[TPR / 32];
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+        __syncthreads();
+        v = part[0];
+#pragma unroll 8
+        for (int i = 1; i < TPR / 32; ++i) v = op(v, part[i]);
     }
-    __syncthreads();
-    return all;
+    return v;
 }
 
-// One block a row.
-__global__ void __launch_bounds__(256) rms_norm_kernel(const NormArgs a)
+// Writes 8 columns of the normalised (or plain) row, in bf16 or in e4m3 times `inv`.
+template <bool Q8>
+__device__ __forceinline__ void store_y(void *y, size_t at, const float (&f)[8], float inv)
 {
-    for (long long m = blockIdx.x; m < a.M; m += gridDim.x) {
-        const size_t row = (size_t)m * a.D;
-        auto h = [&](int d) { return bf(a.x, row + d) + (a.residual ? bf(a.residual, row + d) : 0.f); };
-        float s = 0.f;
-        for (int d = threadIdx.x; d < a.D; d += blockDim.x) s += h(d) * h(d);
-        const float rstd = a.weight ? 1.f / sqrtf(block_reduce<false>(s) / a.D + a.eps) : 1.f;
-        auto y = [&](int d) { return a.weight ? h(d) * rstd * a.weight[d] : h(d); };
-        float inv = 1.f;
-        if (a.q8) {
-            float t = 0.f;
-            for (int d = threadIdx.x; d < a.D; d += blockDim.x) {
-                const float v = fabsf(y(d));
-                asm("max.NaN.f32 %0, %1, %0;" : "+f"(t) : "f"(v));
-            }
-            t = block_reduce<true>(t);
-            t = t < kAmaxFloor ? kAmaxFloor : t;
-            if (!(t <= 3.4e38f)) t = __int_as_float(0x7fffffff);
-            inv = kQ8Max / t;
-            if (threadIdx.x == 0) a.scale[m] = t / kQ8Max;
+    if (Q8)
+        static_cast<uint2 *>(y)[at] =
+            make_uint2(pack_e4m3x2(f[0] * inv, f[1] * inv) | pack_e4m3x2(f[2] * inv, f[3] * inv) << 16,
+                       pack_e4m3x2(f[4] * inv, f[5] * inv) | pack_e4m3x2(f[6] * inv, f[7] * inv) << 16);
+    else
+        static_cast<uint4 *>(y)[at] = pack8(f);
+}
+
+// 448 / max(amax, floor); NaN for a row with an infinity or a NaN.
+__device__ __forceinline__ float q8_inverse(float amax, float &scale)
+{
+    float a = amax < kAmaxFloor ? kAmaxFloor : amax;
+    if (!(a <= 3.402823466e38f)) a = __int_as_float(0x7fffffff);
+    scale = a / kQ8Max;
+    return kQ8Max / a;
+}
+
+__host__ __device__ constexpr int rows_per_block(int tpr) { return tpr == 32 ? 4 : 1; }
+
+template <int TPR, int CH, bool Q8>
+__global__ void __launch_bounds__(TPR *rows_per_block(TPR)) rms_norm_kernel(const NormArgs a)
+{
+    const long long m = (long long)blockIdx.x * rows_per_block(TPR) + threadIdx.x / TPR;
+    if (m >= a.M) return;   // whole warps (TPR = 32), or never
+    const int t = threadIdx.x % TPR, nch = a.D / 8;
+    const size_t row = (size_t)m * nch;   // in chunks
+    const uint4 *x = static_cast<const uint4 *>(a.x) + row, *r = static_cast<const uint4 *>(a.residual) + row;
+    float h[CH][8];
+    uint4 xv[CH], rv[CH];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        const int i = t + c * TPR;
+        if (i < nch) {
+            xv[c] = x[i];
+            if (a.residual) rv[c] = r[i];
         }
-        if (a.rstd && threadIdx.x == 0) a.rstd[m] = rstd;
-        for (int d = threadIdx.x; d < a.D; d += blockDim.x) {
-            const float hv = h(d), yv = y(d);
-            if (a.h) static_cast<__nv_bfloat16 *>(a.h)[row + d] = __float2bfloat16(hv);
-            if (a.q8)
-                static_cast<__nv_fp8_storage_t *>(a.y)[row + d] =
-                    __nv_cvt_float_to_fp8(yv * inv, __NV_SATFINITE, __NV_E4M3);
-            else
-                static_cast<__nv_bfloat16 *>(a.y)[row + d] = __float2bfloat16(yv);
+    }
+    float s = 0.f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        const int i = t + c * TPR;
+        if (i >= nch) continue;
+        unpack8(xv[c], h[c]);
+        if (a.residual) {
+            float f[8];
+            unpack8(rv[c], f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h[c][e] += f[e];
+            if (a.h) static_cast<uint4 *>(a.h)[row + i] = pack8(h[c]);
         }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s = fmaf(h[c][e], h[c][e], s);
+    }
+    if (a.weight) {
+        const float rstd = 1.f / sqrtf(row_reduce<TPR>(s, add) / (float)a.D + a.eps);
+        if (a.rstd && t == 0) a.rstd[m] = rstd;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int i = t + c * TPR;
+            if (i >= nch) continue;
+            float w[8];
+            load8(a.weight + i * 8, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h[c][e] = h[c][e] * rstd * w[e];
+            if (!Q8) store_y<false>(a.y, row + i, h[c], 1.f);
+        }
+    }
+    if (Q8) {
+        float amax = 0.f, scale;
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+            if (t + c * TPR < nch)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) amax = max_nan(amax, fabsf(h[c][e]));
+        const float inv = q8_inverse(row_reduce<TPR>(amax, max_nan), scale);
+        if (t == 0) a.scale[m] = scale;
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+            if (t + c * TPR < nch) store_y<true>(a.y, row + t + c * TPR, h[c], inv);
     }
 }
 
-__global__ void __launch_bounds__(256) rms_norm_dx_kernel(const NormBwdArgs a)
+// Rows of more than 32768 columns: the row is read again for each pass over it.  h may be one of the
+// inputs, so it is written in the last pass, by the thread that reads those elements.
+template <bool Q8>
+__global__ void __launch_bounds__(1024) rms_norm_long_kernel(const NormArgs a)
 {
-    for (long long m = blockIdx.x; m < a.M; m += gridDim.x) {
-        const size_t row = (size_t)m * a.D;
+    const size_t row = (size_t)blockIdx.x * (a.D / 8);
+    auto load_h = [&](int i, float (&h)[8]) {
+        unpack8(static_cast<const uint4 *>(a.x)[row + i], h);
+        if (a.residual) {
+            float f[8];
+            unpack8(static_cast<const uint4 *>(a.residual)[row + i], f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h[e] += f[e];
+        }
+    };
+    float s = 0.f, rstd = 1.f, amax = 0.f, inv = 1.f;
+    float h[8], w[8];
+    if (a.weight) {
+        for (int i = threadIdx.x; i < a.D / 8; i += 1024) {
+            load_h(i, h);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s = fmaf(h[e], h[e], s);
+        }
+        rstd = 1.f / sqrtf(row_reduce<1024>(s, add) / (float)a.D + a.eps);
+        if (a.rstd && threadIdx.x == 0) a.rstd[blockIdx.x] = rstd;
+    }
+    auto load_y = [&](int i, float (&y)[8]) {
+        if (!a.weight) return;
+        load8(a.weight + i * 8, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = y[e] * rstd * w[e];
+    };
+    if (Q8) {
+        for (int i = threadIdx.x; i < a.D / 8; i += 1024) {
+            load_h(i, h);
+            load_y(i, h);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) amax = max_nan(amax, fabsf(h[e]));
+        }
+        float scale;
+        inv = q8_inverse(row_reduce<1024>(amax, max_nan), scale);
+        if (threadIdx.x == 0) a.scale[blockIdx.x] = scale;
+    }
+    for (int i = threadIdx.x; i < a.D / 8; i += 1024) {
+        load_h(i, h);
+        if (a.h) static_cast<uint4 *>(a.h)[row + i] = pack8(h);
+        load_y(i, h);
+        store_y<Q8>(a.y, row + i, h, inv);
+    }
+}
+
+// dx and the partial sums of dweight: each row-holder (a warp, or the block) walks its rows, keeping
+// the sums of dy n for its columns in registers; the warps of a block then add theirs up in order.
+// The rows a block takes, and so the order of the sums, follow from the sizes alone.
+template <int TPR, int CH>
+__global__ void __launch_bounds__(TPR == 32 ? 256 : TPR) rms_norm_bwd_kernel(const NormBwdArgs a, int blocks)
+{
+    constexpr int RPB = TPR == 32 ? 8 : 1;   // row-holders a block
+    const int t = threadIdx.x % TPR, holder = threadIdx.x / TPR, nch = a.D / 8;
+    float acc[CH][8] = {};
+    for (long long m = (long long)blockIdx.x * RPB + holder; m < a.M; m += (long long)blocks * RPB) {
+        const size_t row = (size_t)m * nch;
+        const uint4 *dy = static_cast<const uint4 *>(a.dy) + row, *h = static_cast<const uint4 *>(a.h) + row,
+                    *dh = static_cast<const uint4 *>(a.dh) + row;
+        uint4 dv[CH], hv[CH];
         const float r = a.rstd[m];
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int i = t + c * TPR;
+            if (i < nch) {
+                dv[c] = dy[i];
+                hv[c] = h[i];
+            }
+        }
         float s = 0.f;
-        for (int d = threadIdx.x; d < a.D; d += blockDim.x)
-            s += bf(a.dy, row + d) * a.weight[d] * (bf(a.h, row + d) * r);
-        s = block_reduce<false>(s) / a.D;
-        for (int d = threadIdx.x; d < a.D; d += blockDim.x) {
-            float v = r * (bf(a.dy, row + d) * a.weight[d] - bf(a.h, row + d) * r * s);
-            if (a.dh) v += bf(a.dh, row + d);
-            static_cast<__nv_bfloat16 *>(a.dx)[row + d] = __float2bfloat16(v);
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int i = t + c * TPR;
+            if (i >= nch) continue;
+            float d[8], n[8], w[8];
+            unpack8(dv[c], d);
+            unpack8(hv[c], n);
+            load8(a.weight + i * 8, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float p = d[e] * (n[e] * r);
+                acc[c][e] += p;
+                s = fmaf(p, w[e], s);
+            }
+        }
+        s = row_reduce<TPR>(s, add) / (float)a.D;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int i = t + c * TPR;
+            if (i >= nch) continue;
+            float d[8], n[8], w[8], o[8];
+            unpack8(dv[c], d);
+            unpack8(hv[c], n);
+            load8(a.weight + i * 8, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = r * fmaf(d[e], w[e], -(n[e] * r) * s);
+            if (a.dh) {
+                float g[8];
+                unpack8(dh[i], g);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] += g[e];
+            }
+            static_cast<uint4 *>(a.dx)[row + i] = pack8(o);
+        }
+    }
+    float *part = a.part + (size_t)blockIdx.x * a.D;
+    if constexpr (RPB == 1) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int i = t + c * TPR;
+            if (i >= nch) continue;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) part[i * 8 + e] = acc[c][e];
+        }
+    } else {
+        __shared__ float sums[RPB][256];
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {   // 32 chunks = 256 columns at a time
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sums[holder][t * 8 + e] = acc[c][e];
+            __syncthreads();
+            const int col = c * 256 + threadIdx.x;
+            if (col < a.D) {
+                float v = 0.f;
+#pragma unroll
+                for (int w = 0; w < RPB; ++w) v += sums[w][threadIdx.x];
+                part[col] = v;
+            }
         }
     }
 }
 
-// Partial sums over a block of rows, one thread a column; then their sum.
-__global__ void rms_norm_dw_kernel(const NormBwdArgs a, int blocks)
+// The same for rows of more than 16384 columns: two passes over each row, the sums of dy n in a
+// block's own row of the workspace.
+__global__ void __launch_bounds__(1024) rms_norm_bwd_long_kernel(const NormBwdArgs a, int blocks)
 {
-    const int d = blockIdx.x * blockDim.x + threadIdx.x;
-    if (d >= a.D) return;
-    float s = 0.f;
-    for (long long m = blockIdx.y; m < a.M; m += blocks)
-        s += bf(a.dy, (size_t)m * a.D + d) * bf(a.h, (size_t)m * a.D + d) * a.rstd[m];
-    a.part[(size_t)blockIdx.y * a.D + d] = s;
+    float *part = a.part + (size_t)blockIdx.x * a.D;
+    for (long long m = blockIdx.x; m < a.M; m += blocks) {
+        const size_t row = (size_t)m * (a.D / 8);
+        const float r = a.rstd[m];
+        float d[8], n[8], w[8], s = 0.f;
+        for (int i = threadIdx.x; i < a.D / 8; i += 1024) {
+            unpack8(static_cast<const uint4 *>(a.dy)[row + i], d);
+            unpack8(static_cast<const uint4 *>(a.h)[row + i], n);
+            load8(a.weight + i * 8, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float p = d[e] * (n[e] * r);
+                part[i * 8 + e] = (m == blockIdx.x ? 0.f : part[i * 8 + e]) + p;
+                s = fmaf(p, w[e], s);
+            }
+        }
+        s = row_reduce<1024>(s, add) / (float)a.D;
+        for (int i = threadIdx.x; i < a.D / 8; i += 1024) {
+            unpack8(static_cast<const uint4 *>(a.dy)[row + i], d);
+            unpack8(static_cast<const uint4 *>(a.h)[row + i], n);
+            load8(a.weight + i * 8, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) d[e] = r * fmaf(d[e], w[e], -(n[e] * r) * s);
+            if (a.dh) {
+                unpack8(static_cast<const uint4 *>(a.dh)[row + i], n);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) d[e] += n[e];
+            }
+            static_cast<uint4 *>(a.dx)[row + i] = pack8(d);
+        }
+    }
 }
 
-__global__ void sum_parts_kernel(const float *part, float *out, int blocks, int D)
+// out[c] = the sum over rows of part[row][c], in a fixed order: a block takes 32 columns, its 32
+// warps every 32nd row, then one warp adds the 32 sums up.
+__global__ void __launch_bounds__(1024) sum_rows_kernel(const float *part, float *out, int rows, int cols)
 {
-    const int d = blockIdx.x * blockDim.x + threadIdx.x;
-    if (d >= D) return;
+    __shared__ float sums[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float s = 0.f;
-    for (int b = 0; b < blocks; ++b) s += part[(size_t)b * D + d];
-    out[d] = s;
+    if (c < cols)
+#pragma unroll 4
+        for (int r = warp; r < rows; r += 32) s += part[(size_t)r * cols + c];
+    sums[warp][lane] = s;
+    __syncthreads();
+    s = sums[lane][warp];   // column `warp`, its 32 sums over the lanes
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+    const int cw = blockIdx.x * 32 + warp;
+    if (lane == 0 && cw < cols) out[cw] = s;
+}
+
+template <int TPR, int CH>
+void launch_norm(const NormArgs &a, cudaStream_t stream)
+{
+    constexpr int R = rows_per_block(TPR);
+    const unsigned grid = (unsigned)(((long long)a.M + R - 1) / R);
+    if (a.q8)
+        rms_norm_kernel<TPR, CH, true><<<grid, TPR * R, 0, stream>>>(a);
+    else
+        rms_norm_kernel<TPR, CH, false><<<grid, TPR * R, 0, stream>>>(a);
 }
 
 }  // namespace
 
-cudaError_t launch_rms_norm(const NormArgs &a, cudaStream_t stream)
+cudaError_t launch_sum_rows(const float *part, float *out, int rows, int cols, cudaStream_t stream)
 {
-    rms_norm_kernel<<<a.M < 65536 ? a.M : 65536, 256, 0, stream>>>(a);
+    sum_rows_kernel<<<(cols + 31) / 32, 1024, 0, stream>>>(part, out, rows, cols);
     return cudaGetLastError();
 }
 
-int norm_bwd_blocks(int M, int) { return M < 128 ? (M > 0 ? M : 1) : 128; }
+cudaError_t launch_rms_norm(const NormArgs &a, cudaStream_t stream)
+{
+    const int D = a.D;
+    if (D <= 256) launch_norm<32, 1>(a, stream);
+    else if (D <= 512) launch_norm<32, 2>(a, stream);
+    else if (D <= 1024) launch_norm<32, 4>(a, stream);
+    else if (D <= 2048) launch_norm<32, 8>(a, stream);
+    else if (D <= 4096) launch_norm<256, 2>(a, stream);
+    else if (D <= 8192) launch_norm<256, 4>(a, stream);
+    else if (D <= 16384) launch_norm<256, 8>(a, stream);
+    else if (D <= 32768) launch_norm<1024, 4>(a, stream);
+    else if (a.q8) rms_norm_long_kernel<true><<<a.M, 1024, 0, stream>>>(a);
+    else rms_norm_long_kernel<false><<<a.M, 1024, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
+// Two blocks of 8 warps an SM where a warp holds a row of up to 1024 columns (its registers allow
+// it), else one; no more blocks than there are rows for.
+int norm_bwd_blocks(int M, int D)
+{
+    const int rpb = D <= 2048 ? 8 : 1;
+    const int want = D <= 1024 || (D > 2048 && D <= 8192) ? 2 * kPlanSms : kPlanSms;
+    const int most = (int)(((long long)M + rpb - 1) / rpb);
+    const int b = want < most ? want : most;
+    return b > 1 ? b : 1;
+}
 
 cudaError_t launch_rms_norm_bwd(const NormBwdArgs &a, cudaStream_t stream)
 {
-    const int blocks = norm_bwd_blocks(a.M, a.D);
-    rms_norm_dw_kernel<<<dim3((a.D + 127) / 128, blocks), 128, 0, stream>>>(a, blocks);
-    sum_parts_kernel<<<(a.D + 127) / 128, 128, 0, stream>>>(a.part, a.dweight, blocks, a.D);
-    rms_norm_dx_kernel<<<a.M < 65536 ? a.M : 65536, 256, 0, stream>>>(a);
-    return cudaGetLastError();
+    const int blocks = norm_bwd_blocks(a.M, a.D), D = a.D;
+    if (D <= 256) rms_norm_bwd_kernel<32, 1><<<blocks, 256, 0, stream>>>(a, blocks);
+    else if (D <= 512) rms_norm_bwd_kernel<32, 2><<<blocks, 256, 0, stream>>>(a, blocks);
+    else if (D <= 768) rms_norm_bwd_kernel<32, 3><<<blocks, 256, 0, stream>>>(a, blocks);
+    else if (D <= 1024) rms_norm_bwd_kernel<32, 4><<<blocks, 256, 0, stream>>>(a, blocks);
+    else if (D <= 2048) rms_norm_bwd_kernel<32, 8><<<blocks, 256, 0, stream>>>(a, blocks);
+    else if (D <= 4096) rms_norm_bwd_kernel<256, 2><<<blocks, 256, 0, stream>>>(a, blocks);
+    else if (D <= 8192) rms_norm_bwd_kernel<256, 4><<<blocks, 256, 0, stream>>>(a, blocks);
+    else if (D <= 16384) rms_norm_bwd_kernel<256, 8><<<blocks, 256, 0, stream>>>(a, blocks);
+    else rms_norm_bwd_long_kernel<<<blocks, 1024, 0, stream>>>(a, blocks);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? launch_sum_rows(a.part, a.dweight, blocks, D, stream) : e;
 }
 
 }  // namespace attn

@@ -91,7 +91,7 @@ def test_q8_argument_errors(lib):
     def quant(x=X, q=Y, s=Z, M=16, D=64):
         return lib.attn_quantize_q8(x, q, s, M, D, None)
 
-    assert quant(D=72) == 1 and quant(M=-1) == 1 and quant(x=0) == 1 and quant(s=0) == 1
+    assert quant(D=60) == 1 and quant(M=-1) == 1 and quant(x=0) == 1 and quant(s=0) == 1
     assert quant(q=X) == 1 and quant(s=Y + 256) == 1 and quant(q=Y + 8) == 3 and quant(M=0, x=0, q=0, s=0) == 0
 
 
@@ -110,7 +110,7 @@ def test_rms_norm_argument_errors(lib):
     assert fwd(y=X) == 1 and fwd(y=Z) == 1 and fwd(h=RES + 16) == 1 and fwd(h=W) == 1 and fwd(r=W) == 1
     assert fwd(M=0, x=0, y=0) == 0
     assert lib.attn_rms_norm_q8(X, RES, W, Y, 0, Z, 16, 64, f(1e-6), None) == 1      # no scale
-    assert lib.attn_rms_norm_q8(X, RES, W, Y, DB, Z, 16, 72, f(1e-6), None) == 1     # D % 16
+    assert lib.attn_rms_norm_q8(X, RES, W, Y, DB, Z, 16, 60, f(1e-6), None) == 1     # D % 8
     assert lib.attn_rms_norm_q8(X, RES, W, Y, DB, Y + 512, 16, 64, f(1e-6), None) == 1
 
     need = sa.attn_rms_norm_bwd_workspace_size(16, 64)
