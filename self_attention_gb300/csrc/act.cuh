@@ -1,4 +1,5 @@
-// The activations of the linear layers and their slopes, in fp32.
+// The activations of the linear layers and their slopes, in fp32.  `act` is uniform over the grid:
+// each function branches on it once for a whole array.
 #pragma once
 
 #include "attn.h"
@@ -13,65 +14,125 @@ __device__ __forceinline__ float rcp_approx(float x)
     return y;
 }
 
-constexpr float kLog2e = 1.4426950408889634f;
-
-// 1 / (1 + exp(-x)): two MUFU operations, relative error a few 2^-23.
-__device__ __forceinline__ float sigmoid(float x) { return rcp_approx(1.f + ptx::ex2(-kLog2e * x)); }
-
-// The normal distribution function, Phi(z) = erfc(-z / sqrt 2) / 2, by the rational approximation
-// 7.1.26 of Abramowitz and Stegun's Handbook of Mathematical Functions:
-//   erfc(x) = (a1 t + a2 t^2 + ... + a5 t^5) exp(-x^2) + e, t = 1 / (1 + p x), x >= 0, |e| <= 1.5e-7,
-// far below the bf16 rounding of what it multiplies.  `density` gets exp(-z^2 / 2).
-__device__ __forceinline__ float normal_cdf(float z, float &density)
+// min(|x|, limit), NaN if x is one.
+__device__ __forceinline__ float abs_min(float x, float limit)
 {
-    const float x = fabsf(z) * 0.70710678118654752f;
-    const float t = rcp_approx(fmaf(0.3275911f, x, 1.f));
-    density = ptx::ex2(-kLog2e * x * x);
-    float s = fmaf(t, 1.061405429f, -1.453152027f);
-    s = fmaf(t, s, 1.421413741f);
-    s = fmaf(t, s, -0.284496736f);
-    s = fmaf(t, s, 0.254829592f);
-    const float half_erfc = 0.5f * t * s * density;
-    return z >= 0.f ? 1.f - half_erfc : half_erfc;
+    float y;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(fabsf(x)), "f"(limit));
+    return y;
 }
 
+__device__ __forceinline__ uint64_t f2_both(float x) { return ptx::f2_pack(x, x); }
+
+__device__ __forceinline__ uint64_t f2_ex2(uint64_t x)
+{
+    float lo, hi;
+    ptx::f2_unpack(x, lo, hi);
+    return ptx::f2_pack(ptx::ex2(lo), ptx::ex2(hi));
+}
+
+__device__ __forceinline__ uint64_t f2_rcp(uint64_t x)
+{
+    float lo, hi;
+    ptx::f2_unpack(x, lo, hi);
+    return ptx::f2_pack(rcp_approx(lo), rcp_approx(hi));
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGeluK = 0.79788456080286536f;   // sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
 
-// act(z).  `act` is uniform over the grid, so the branch costs one predicate.
-__device__ __forceinline__ float activate(float z, int act)
+// erfc(x) / 2 for x >= 0 by the rational approximation 7.1.26 of Abramowitz and Stegun's Handbook
+// of Mathematical Functions,
+//   erfc(x) = (a1 t + a2 t^2 + ... + a5 t^5) exp(-x^2) + e, t = 1 / (1 + p x), |e| <= 1.5e-7,
+// far below the bf16 rounding of what it multiplies.
+constexpr float kErfP = 0.3275911f, kErfA1 = 0.254829592f, kErfA2 = -0.284496736f, kErfA3 = 1.421413741f,
+                kErfA4 = -1.453152027f, kErfA5 = 1.061405429f;
+constexpr float kSqrtHalf = 0.70710678118654752f;
+
+// z <- act(z) for pairs of values (packed fp32 arithmetic: two multiply-adds an instruction, which
+// keeps the epilogues that use it ahead of the tensor cores).
+template <int NP>
+__device__ __forceinline__ void activate(uint64_t (&z)[NP], int act)
 {
-    float e;
-    switch (act) {
-    case ATTN_ACT_RELU: return z > 0.f ? z : (z != z ? z : 0.f);
-    case ATTN_ACT_GELU: return z * normal_cdf(z, e);
-    // (1 + tanh u) / 2 = sigmoid(2 u)
-    case ATTN_ACT_GELU_TANH: return z * sigmoid(2.f * kGeluK * z * fmaf(kGeluA * z, z, 1.f));
-    case ATTN_ACT_SILU: return z * sigmoid(z);
-    default: return z;
+    using namespace ptx;
+    if (act == ATTN_ACT_GELU) {
+        // z Phi(z) = max(z, 0) - |z| erfc(|z| / sqrt 2) / 2; |z| stops at 100, where the second term
+        // has long vanished, so that an infinity keeps its value
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            float lo, hi;
+            f2_unpack(z[i], lo, hi);
+            const uint64_t a = f2_pack(abs_min(lo, 100.f), abs_min(hi, 100.f));
+            const uint64_t t = f2_rcp(fma_f32x2(a, f2_both(kErfP * kSqrtHalf), f2_both(1.f)));
+            const uint64_t e = f2_ex2(mul_f32x2(mul_f32x2(a, f2_both(-0.5f * kLog2e)), a));
+            uint64_t s = fma_f32x2(t, f2_both(-0.5f * kErfA5), f2_both(-0.5f * kErfA4));
+            s = fma_f32x2(t, s, f2_both(-0.5f * kErfA3));
+            s = fma_f32x2(t, s, f2_both(-0.5f * kErfA2));
+            s = fma_f32x2(t, s, f2_both(-0.5f * kErfA1));
+            s = mul_f32x2(mul_f32x2(t, s), e);
+            z[i] = fma_f32x2(a, s, f2_pack(fmaxf(lo, 0.f), fmaxf(hi, 0.f)));
+        }
+    } else if (act == ATTN_ACT_GELU_TANH) {
+        // (1 + tanh u) / 2 = 1 / (1 + exp(-2 u))
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const uint64_t w = fma_f32x2(mul_f32x2(z[i], z[i]), f2_both(-2.f * kLog2e * kGeluK * kGeluA),
+                                         f2_both(-2.f * kLog2e * kGeluK));
+            z[i] = mul_f32x2(z[i], f2_rcp(add_f32x2(f2_ex2(mul_f32x2(z[i], w)), f2_both(1.f))));
+        }
+    } else if (act == ATTN_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+            z[i] = mul_f32x2(z[i], f2_rcp(add_f32x2(f2_ex2(mul_f32x2(z[i], f2_both(-kLog2e))), f2_both(1.f))));
+    } else if (act == ATTN_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            float lo, hi;
+            f2_unpack(z[i], lo, hi);
+            asm("max.NaN.f32 %0, %0, 0f00000000;" : "+f"(lo));
+            asm("max.NaN.f32 %0, %0, 0f00000000;" : "+f"(hi));
+            z[i] = f2_pack(lo, hi);
+        }
     }
 }
 
-// act'(z).
-__device__ __forceinline__ float act_slope(float z, int act)
+__device__ __forceinline__ float sigmoid(float x) { return rcp_approx(1.f + ptx::ex2(-kLog2e * x)); }
+
+// d <- d act'(z).
+template <int N>
+__device__ __forceinline__ void times_slope(float (&d)[N], const float (&z)[N], int act)
 {
-    switch (act) {
-    case ATTN_ACT_RELU: return z > 0.f ? 1.f : 0.f;
-    case ATTN_ACT_GELU: {
-        float e;
-        const float cdf = normal_cdf(z, e);
-        return fmaf(z * 0.39894228040143268f, e, cdf);   // Phi(z) + z phi(z)
-    }
-    case ATTN_ACT_GELU_TANH: {
-        const float p = sigmoid(2.f * kGeluK * z * fmaf(kGeluA * z, z, 1.f)), r = p * (1.f - p);
-        // r is 0 where z^2 may overflow
-        return r == 0.f ? p : fmaf(z * r, 2.f * kGeluK * fmaf(3.f * kGeluA * z, z, 1.f), p);
-    }
-    case ATTN_ACT_SILU: {
-        const float p = sigmoid(z);
-        return p * fmaf(z, 1.f - p, 1.f);
-    }
-    default: return 1.f;
+    if (act == ATTN_ACT_GELU) {
+        // Phi(z) + z phi(z), with Phi(-a) = 1 - Phi(a)
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float a = abs_min(z[i], 100.f);
+            const float t = rcp_approx(fmaf(a, kErfP * kSqrtHalf, 1.f)), e = ptx::ex2(-0.5f * kLog2e * a * a);
+            float s = fmaf(t, 0.5f * kErfA5, 0.5f * kErfA4);
+            s = fmaf(t, s, 0.5f * kErfA3);
+            s = fmaf(t, s, 0.5f * kErfA2);
+            s = fmaf(t, s, 0.5f * kErfA1);
+            // slope(a) = 1 - tail for z >= 0, tail for z < 0
+            const float tail = e * fmaf(t, s, -0.39894228040143268f * a);
+            d[i] *= z[i] >= 0.f ? 1.f - tail : tail;
+        }
+    } else if (act == ATTN_ACT_GELU_TANH) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float x = z[i], q = x * x, p = sigmoid(2.f * kGeluK * x * fmaf(kGeluA, q, 1.f)), r = p * (1.f - p);
+            // r is 0 where the square may overflow
+            d[i] *= r == 0.f ? p : fmaf(x * r, 2.f * kGeluK * fmaf(3.f * kGeluA, q, 1.f), p);
+        }
+    } else if (act == ATTN_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float p = sigmoid(z[i]);
+            d[i] *= p * fmaf(z[i], 1.f - p, 1.f);
+        }
+    } else if (act == ATTN_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) d[i] = z[i] > 0.f ? d[i] : 0.f;
     }
 }
 

@@ -6,8 +6,8 @@
 //   Dx    : A = dz (K-major), B = w (K-major: the rows of w are the columns of dx).
 //   Dw    : A = x^T, B = dz, both MN-major; the K steps are 64 rows each.
 // x (and dx) may be split by heads, [G, H, T, dk] with row m = g T + i and column c = h dk + e: a
-// 64-column box lies in one head, so only the coordinates of the copies differ.  Row tiles (and, for
-// dw, steps) lie in one group g; the copies' zero fill and clipping end a tile at the group's last row.
+// 64-column box lies in one head, so only the coordinates of the copies differ.  A row block (and, for
+// dw, a step) lies in one group g; the copies' zero fill and clipping end it at the group's last row.
 //
 // A cluster of two CTAs computes a 256 x BN tile together (tcgen05 cta_group::2): each loads 128 rows
 // of A and BN / 2 columns of B a step, 32 KB for 2 x 128 x 256 x 64 multiply-adds where a single CTA
@@ -37,14 +37,16 @@ struct GemmMaps {
 };
 
 struct GemmParams {
-    int T, mblocks;                // rows of one group, its row tiles
-    int n_mtiles, n_ntiles, N;     // row tiles of all groups, column tiles, columns
+    int T;                         // rows of one group
+    int rb, rblocks, n_rblocks;    // rows of a row block, row blocks of one group and of all
+    int n_mtiles, n_ntiles, N;     // row tiles, column tiles, columns
     int dk, H;                     // the head split of the side that has one (A; Dx: y)
-    int ksteps, steps_per_split, tblocks;   // K steps in all and per item; Dw: steps of one group
+    int ksteps, steps_per_split;   // K steps in all and per item
+    int tblocks, T_k;              // Dw: steps and rows of one group
     int n_items;
     const float *bias, *x_scale, *w_scale;
     int has_z, has_r, act;
-    float *part;                   // Dw split over K: [splits][rows][N] fp32 partial sums
+    int part;                      // Dw split over K: y maps [splits][rows][N] fp32 partial sums
     int *status;
 };
 
@@ -69,6 +71,27 @@ __device__ __forceinline__ uint64_t desc_k(uint32_t base, int kk) { return ptx::
 __device__ __forceinline__ uint64_t desc_mn(uint32_t base, int kk)
 {
     return ptx::sdesc_sw128(base + kk * 2048, 8192, 1024);
+}
+
+// Four pairs of fp32 -> eight bf16, rounded to nearest even.
+__device__ __forceinline__ uint4 pack_bf16x8(const uint64_t *f)
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        float lo, hi;
+        ptx::f2_unpack(f[e], lo, hi);
+        w[e] = ptx::pack_bf16x2(lo, hi);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ uint2 pack_bf16x4(const uint64_t (&f)[2])
+{
+    float a, b, c, d;
+    ptx::f2_unpack(f[0], a, b);
+    ptx::f2_unpack(f[1], c, d);
+    return make_uint2(ptx::pack_bf16x2(a, b), ptx::pack_bf16x2(c, d));
 }
 
 template <Policy P, int BN>
@@ -124,34 +147,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
 
     if (warp == 0) {
         if (ptx::elect_one()) {
-            int j = 0;   // position in the stage ring, across items
+            int s = 0;          // place in the stage ring, and the parity of its turn, across items
+            uint32_t ph = 0;
+            const uint32_t full0 = ptx::cluster_addr(ptx::smem_u32(&bar_full[0]), 0);
             for (int item = cluster; item < p.n_items; item += n_clusters) {
                 int ks, mt, nt, k_begin, nk;
                 decode(item, ks, mt, nt, k_begin, nk);
-                const int grp = mt / p.mblocks, i0 = (mt % p.mblocks) * BM + (int)rank * 128;
+                // this CTA's 128 rows: one block of 128, or four of 32 that may lie in different groups
+                const int per_cta = 128 / p.rb, block0 = (mt * 2 + (int)rank) * per_cta;
+                int grp[4], i0[4];
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    grp[h] = (block0 + h) / p.rblocks;
+                    i0[h] = (block0 + h) % p.rblocks * p.rb;
+                }
                 const int n0 = nt * BN + (int)rank * (BN / 2);
-                for (int q = 0; q < nk; ++q, ++j) {
-                    const int s = j % STAGES, step = k_begin + q;
-                    wait_bounded(&bar_empty[s], ((j / STAGES) & 1) ^ 1, g);
+                // Walking K without divisions, which would take this one thread longer than a step:
+                // Dw: group gk, row t0 of it; else: column c of A, at ce of head ch.
+                int gk = 0, t0 = 0, c = k_begin * C::KE, ce = c, ch = 0, col[2], head[2];
+                if (P == Dw) {
+                    gk = k_begin / p.tblocks;
+                    t0 = (k_begin - gk * p.tblocks) * 64;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        head[h] = (i0[0] + 64 * h) / p.dk;
+                        col[h] = i0[0] + 64 * h - head[h] * p.dk;
+                    }
+                } else if (P != Dx) {
+                    ch = c / p.dk;
+                    ce = c - ch * p.dk;
+                }
+                for (int q = 0; q < nk; ++q) {
+                    wait_bounded(&bar_empty[s], ph ^ 1, g);
                     if (rank == 0) ptx::mbar_arrive_expect_tx(&bar_full[s], 2 * C::STAGE);
-                    const uint32_t bar = ptx::cluster_addr(ptx::smem_u32(&bar_full[s]), 0);
+                    const uint32_t bar = full0 + s * 8;
                     uint8_t *sa = smem + s * C::STAGE, *sb = sa + C::A_BYTES;
                     if (P == Dw) {
-                        const int gk = step / p.tblocks, t0 = (step % p.tblocks) * 64;
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int c = i0 + 64 * h;
-                            ptx::tma_load_3d_pair(sa + h * 8192, &maps.a, bar, c % p.dk, t0, gk * p.H + c / p.dk);
-                        }
+                        for (int h = 0; h < 2; ++h)
+                            ptx::tma_load_3d_pair(sa + h * 8192, &maps.a, bar, col[h], t0, gk * p.H + head[h]);
 #pragma unroll
                         for (int h = 0; h < BN / 128; ++h)
                             ptx::tma_load_3d_pair(sb + h * 8192, &maps.b, bar, n0 + 64 * h, t0, gk);
+                        t0 += 64;
+                        if (t0 >= p.T_k) {
+                            t0 = 0;
+                            ++gk;
+                        }
                     } else {
-                        const int c = step * C::KE;
-                        if (P == Dx)
-                            ptx::tma_load_3d_pair(sa, &maps.a, bar, c, i0, grp);
-                        else
-                            ptx::tma_load_3d_pair(sa, &maps.a, bar, c % p.dk, i0, grp * p.H + c / p.dk);
+                        const int heads = P == Dx ? 1 : p.H;
+                        ptx::tma_load_3d_pair(sa, &maps.a, bar, ce, i0[0], grp[0] * heads + ch);
+                        if (per_cta == 4)
+#pragma unroll
+                            for (int h = 1; h < 4; ++h)
+                                ptx::tma_load_3d_pair(sa + h * 4096, &maps.a, bar, ce, i0[h], grp[h] * heads + ch);
                         if (P == Fwd) {
 #pragma unroll
                             for (int h = 0; h < BN / 128; ++h)
@@ -159,28 +208,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
                         } else {
                             ptx::tma_load_3d_pair(sb, &maps.b, bar, c, n0, 0);
                         }
+                        c += C::KE;
+                        ce += C::KE;
+                        if (P == Fwd && ce >= p.dk) {
+                            ce = 0;
+                            ++ch;
+                        }
+                    }
+                    if (++s == STAGES) {
+                        s = 0;
+                        ph ^= 1;
                     }
                 }
             }
-            if (rank == 0)   // both CTAs' copies have landed before either leaves
-                for (int q = (j > STAGES ? j - STAGES : 0); q < j; ++q)
-                    wait_bounded(&bar_full[q % STAGES], (q / STAGES) & 1, g);
+            // both CTAs' copies have landed before either leaves: the last turn of every stage (a stage
+            // that had none yet passes at once)
+            if (rank == 0)
+                for (int q = 0; q < STAGES; ++q) wait_bounded(&bar_full[q], q < s ? ph : ph ^ 1, g);
         }
     } else if (warp == 1 && rank == 0) {
         if (ptx::elect_one()) {
             const uint32_t idesc = C::FP8 ? ptx::idesc_f16_f32(BM, BN, false, false)   // format 0: e4m3
                                           : ptx::idesc_bf16_f32(BM, BN, C::A_MN, C::B_MN);
             const uint32_t base = ptx::smem_u32(smem);
-            int j = 0, li = 0;
+            int s = 0, li = 0;
+            uint32_t ph = 0;
             for (int item = cluster; item < p.n_items; item += n_clusters, ++li) {
                 int ks, mt, nt, k_begin, nk;
                 decode(item, ks, mt, nt, k_begin, nk);
                 const int ab = li & 1;
                 wait_bounded<true>(&bar_acc_empty[ab], ((li >> 1) & 1) ^ 1, g);   // epilogues of item li-2 done
                 ptx::tc_fence_after();
-                for (int q = 0; q < nk; ++q, ++j) {
-                    const int s = j % STAGES;
-                    wait_bounded<true>(&bar_full[s], (j / STAGES) & 1, g);
+                for (int q = 0; q < nk; ++q) {
+                    wait_bounded<true>(&bar_full[s], ph, g);
                     ptx::tc_fence_after();
                     const uint32_t sa = base + s * C::STAGE, sb = sa + C::A_BYTES;
 #pragma unroll
@@ -189,6 +249,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
                                               C::B_MN ? desc_mn(sb, kk) : desc_k(sb, kk), idesc,
                                               (q > 0 || kk > 0) ? 1u : 0u);
                     ptx::mma_commit_pair(&bar_empty[s]);
+                    if (++s == STAGES) {
+                        s = 0;
+                        ph ^= 1;
+                    }
                 }
                 ptx::mma_commit_pair(&bar_acc_full[ab]);
             }
@@ -211,9 +275,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
             int ks, mt, nt, k_begin, nk;
             decode(item, ks, mt, nt, k_begin, nk);
             const int ab = li & 1;
-            const int grp = mt / p.mblocks, i0 = (mt % p.mblocks) * BM + (int)rank * 128 + quarter * 32;
+            const int first = mt * BM + (int)rank * 128 + quarter * 32, block = first / p.rb;
+            const int grp = block / p.rblocks, i0 = block % p.rblocks * p.rb + first % p.rb;
             const int n0 = nt * BN;
-            const bool rows = i0 < p.T;
+            const bool rows = i0 < p.T && block < p.n_rblocks;
             // buffer of chunk j: alternating, or both for y and z
             auto load_res = [&](int col, int b) {
                 ptx::mbar_arrive_expect_tx(&rbar[b], 4096);
@@ -227,7 +292,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
                 }
             }
             __syncwarp();
-            const float xs = (P == FwdQ8 && i0 + lane < p.T) ? p.x_scale[i0 + lane] : 0.f;
+            const uint64_t xs = f2_both((P == FwdQ8 && i0 + lane < p.T) ? p.x_scale[i0 + lane] : 0.f);
             wait_bounded(&bar_acc_full[ab], (li >> 1) & 1, g);
             ptx::tc_fence_after();
             const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + ab * BN;
@@ -254,59 +319,64 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
                     ptx::tmem_ld32(taddr + c0 + half * 32, v);
                     ptx::tmem_ld_wait();
                     reg_fence(v);
-                    if (P == Dw && p.part) {   // fp32 partial sums, a 128-byte line a thread
-                        if (i0 + lane < p.T) {
-                            float *dst = p.part + ((size_t)ks * p.T + i0 + lane) * p.N + col0 + half * 32;
+                    if (P == Dw && p.part) {   // fp32 partial sums: 32 columns are a 128-byte row
+                        if (lane == 0) ptx::bulk_wait_group_read<1>();   // the buffer's last store
+                        __syncwarp();
 #pragma unroll
-                            for (int q = 0; q < 8; ++q)
-                                if (col0 + half * 32 + 4 * q < p.N)
-                                    reinterpret_cast<uint4 *>(dst)[q] =
-                                        make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                        for (int q = 0; q < 8; ++q)
+                            sts_u128(sbuf + half * 4096 + lane * 128 + ((q ^ (lane & 7)) << 4),
+                                     make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]));
+                        ptx::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (col0 + half * 32 < p.N)
+                                ptx::tma_store_3d(&maps.y, buf + half * 4096, col0 + half * 32, i0, ks);
+                            ptx::bulk_commit_group();
                         }
                         continue;
                     }
+                    uint64_t f[16];   // pairs of neighbouring columns
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {   // 8 columns: 16 bytes of the row
-                        const int col = col0 + half * 32 + q * 8;
-                        const uint32_t off = (uint32_t)(((half * 4 + q) ^ (lane & 7)) << 4);
-                        float f[8];
+                    for (int i = 0; i < 16; ++i)
+                        f[i] = ptx::f2_pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                    if (P == Fwd || P == FwdQ8) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[8 * q + e]);
-                        if (P == Fwd || P == FwdQ8) {
-                            if (col < p.N) {
-                                if (P == FwdQ8) {
-                                    const float4 s0 = __ldg(reinterpret_cast<const float4 *>(p.w_scale + col));
-                                    const float4 s1 = __ldg(reinterpret_cast<const float4 *>(p.w_scale + col) + 1);
-                                    f[0] *= xs * s0.x; f[1] *= xs * s0.y; f[2] *= xs * s0.z; f[3] *= xs * s0.w;
-                                    f[4] *= xs * s1.x; f[5] *= xs * s1.y; f[6] *= xs * s1.z; f[7] *= xs * s1.w;
-                                }
-                                if (p.bias) {
-                                    const float4 b0 = __ldg(reinterpret_cast<const float4 *>(p.bias + col));
-                                    const float4 b1 = __ldg(reinterpret_cast<const float4 *>(p.bias + col) + 1);
-                                    f[0] += b0.x; f[1] += b0.y; f[2] += b0.z; f[3] += b0.w;
-                                    f[4] += b1.x; f[5] += b1.y; f[6] += b1.z; f[7] += b1.w;
-                                }
-                            }
-                            if (p.has_z)
-                                sts_u128(zrow + off, make_uint4(ptx::pack_bf16x2(f[0], f[1]), ptx::pack_bf16x2(f[2], f[3]),
-                                                                ptx::pack_bf16x2(f[4], f[5]), ptx::pack_bf16x2(f[6], f[7])));
-                            if (p.act != ATTN_ACT_NONE) {
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) f[e] = activate(f[e], p.act);
-                            }
-                            if (p.has_r) {
-                                const uint4 r = lds_u128(yrow + off);
-                                const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    f[2 * e] += __uint_as_float(w[e] << 16);
-                                    f[2 * e + 1] += __uint_as_float(w[e] & 0xffff0000u);
-                                }
+                        for (int q = 0; q < 8; ++q) {   // 4 columns
+                            const int col = col0 + half * 32 + q * 4;
+                            ulonglong2 b = make_ulonglong2(0, 0);
+                            if (p.bias && col < p.N) b = __ldg(reinterpret_cast<const ulonglong2 *>(p.bias + col));
+                            if (P == FwdQ8) {
+                                ulonglong2 w = make_ulonglong2(0, 0);
+                                if (col < p.N) w = __ldg(reinterpret_cast<const ulonglong2 *>(p.w_scale + col));
+                                f[2 * q] = ptx::fma_f32x2(f[2 * q], ptx::mul_f32x2(w.x, xs), b.x);
+                                f[2 * q + 1] = ptx::fma_f32x2(f[2 * q + 1], ptx::mul_f32x2(w.y, xs), b.y);
+                            } else if (p.bias) {
+                                f[2 * q] = ptx::add_f32x2(f[2 * q], b.x);
+                                f[2 * q + 1] = ptx::add_f32x2(f[2 * q + 1], b.y);
                             }
                         }
-                        sts_u128(yrow + off, make_uint4(ptx::pack_bf16x2(f[0], f[1]), ptx::pack_bf16x2(f[2], f[3]),
-                                                        ptx::pack_bf16x2(f[4], f[5]), ptx::pack_bf16x2(f[6], f[7])));
+                        if (p.has_z) {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                sts_u128(zrow + (((half * 4 + q) ^ (lane & 7)) << 4), pack_bf16x8(f + 4 * q));
+                        }
+                        activate(f, p.act);
+                        if (p.has_r) {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const uint4 r = lds_u128(yrow + (((half * 4 + q) ^ (lane & 7)) << 4));
+                                const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    f[4 * q + e] = ptx::add_f32x2(
+                                        f[4 * q + e], ptx::f2_pack(__uint_as_float(w[e] << 16),
+                                                                   __uint_as_float(w[e] & 0xffff0000u)));
+                            }
+                        }
                     }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)   // 8 columns: 16 bytes of the row
+                        sts_u128(yrow + (((half * 4 + q) ^ (lane & 7)) << 4), pack_bf16x8(f + 4 * q));
                 }
                 if (!(P == Dw && p.part)) {
                     ptx::fence_proxy_async_smem();
@@ -337,6 +407,254 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
     }
 }
 
+// Few rows: the weights are the large operand, and the time is what it takes to stream them.  The
+// product is turned round, C^T[128 columns of y x TN rows] with the weights as the MMA's A operand, so
+// that TN follows the number of rows, and K is split over the CTAs of a cluster, so that many SMs
+// read (one 2048 x 8192 matrix is 64 column tiles).  Each CTA leaves its partial tile in its shared
+// memory; after a cluster barrier each sums its share of the rows over all of them in order, applies
+// the epilogue and stores.  Up to TN = 64 two CTAs fit an SM.
+struct SplitParams {
+    int T, rb, rblocks, n_rblocks; // rows as in GemmParams, in tiles of TN
+    int N, n_ntiles;               // columns of y, tiles of 128
+    int dk, H;                     // the head split of A's side (Dx: of y)
+    int ksteps, steps_per_cta;
+    const float *bias, *x_scale, *w_scale;
+    const __nv_bfloat16 *residual;
+    __nv_bfloat16 *y, *z;
+    int act;
+    int *status;
+};
+
+template <Policy P, int TN>
+struct SplitCfg {
+    static constexpr bool FP8 = P == FwdQ8;
+    static constexpr int KE = FP8 ? 128 : 64;
+    static constexpr int A_BYTES = 128 * 128, B_BYTES = TN * 128, STAGE = A_BYTES + B_BYTES;
+    static constexpr int STAGES = TN <= 16 ? 6 : TN <= 32 ? 5 : TN <= 64 ? 4 : TN <= 128 ? 6 : 4;
+    static constexpr int SMEM = STAGES * STAGE + 1024;
+    static constexpr uint32_t TM_COLS = TN < 32 ? 32 : TN;
+    static_assert(STAGES * STAGE >= TN * 128 * 4, "the partial tile reuses the stages");
+};
+
+// Sums this CTA's share of the rows over the S partial tiles of the cluster, in order, and finishes
+// them: a warp a row, 4 columns a lane, R rows at a time so that their loads are in flight together.
+template <Policy P, int TN, int S, int R>
+__device__ __forceinline__ void join_rows(const SplitParams &p, const uint8_t *smem, int rank, int mt, int n0)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = n0 + lane * 4;
+    const uint32_t part = ptx::smem_u32(smem) + lane * 16;
+    constexpr int STRIDE = S * 8;   // rows of the cluster's warps
+    for (int r0 = rank * 8 + warp; r0 < TN; r0 += STRIDE * R) {
+        float4 t[R][S];
+#pragma unroll
+        for (int q = 0; q < R; ++q)
+            if (r0 + q * STRIDE < TN)
+#pragma unroll
+                for (int k = 0; k < S; ++k)
+                    t[q][k] = ptx::ld_cluster_f32x4(ptx::cluster_addr(part + (r0 + q * STRIDE) * 512, k));
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            const int r = r0 + q * STRIDE, at = mt * TN + r, block = at / p.rb, i = block % p.rblocks * p.rb + at % p.rb;
+            if (r >= TN || block >= p.n_rblocks || i >= p.T || col >= p.N) continue;
+            float4 f = t[q][0];
+#pragma unroll
+            for (int k = 1; k < S; ++k) {
+                f.x += t[q][k].x; f.y += t[q][k].y; f.z += t[q][k].z; f.w += t[q][k].w;
+            }
+            const int grp = block / p.rblocks;
+            const size_t row = (size_t)grp * p.T + i;
+            uint64_t v[2] = {ptx::f2_pack(f.x, f.y), ptx::f2_pack(f.z, f.w)};
+            size_t out = row * p.N + col;
+            if (P == Dx) {
+                out = (((size_t)grp * p.H + col / p.dk) * p.T + i) * p.dk + col % p.dk;
+            } else {
+                ulonglong2 b = make_ulonglong2(0, 0);
+                if (p.bias) b = __ldg(reinterpret_cast<const ulonglong2 *>(p.bias + col));
+                if (P == FwdQ8) {
+                    const uint64_t xs = f2_both(p.x_scale[row]);
+                    const ulonglong2 w = __ldg(reinterpret_cast<const ulonglong2 *>(p.w_scale + col));
+                    v[0] = ptx::fma_f32x2(v[0], ptx::mul_f32x2(w.x, xs), b.x);
+                    v[1] = ptx::fma_f32x2(v[1], ptx::mul_f32x2(w.y, xs), b.y);
+                } else if (p.bias) {
+                    v[0] = ptx::add_f32x2(v[0], b.x);
+                    v[1] = ptx::add_f32x2(v[1], b.y);
+                }
+                if (p.z) *reinterpret_cast<uint2 *>(p.z + out) = pack_bf16x4(v);
+                activate(v, p.act);
+                if (p.residual) {
+                    const uint2 u = *reinterpret_cast<const uint2 *>(p.residual + out);
+                    v[0] = ptx::add_f32x2(v[0], ptx::f2_pack(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u)));
+                    v[1] = ptx::add_f32x2(v[1], ptx::f2_pack(__uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u)));
+                }
+            }
+            *reinterpret_cast<uint2 *>(p.y + out) = pack_bf16x4(v);
+        }
+    }
+}
+
+template <Policy P, int TN>
+__global__ void __launch_bounds__(256) gemm_split_kernel(const __grid_constant__ CUtensorMap map_w,
+                                                         const __grid_constant__ CUtensorMap map_x,
+                                                         const __grid_constant__ SplitParams p)
+{
+    using C = SplitCfg<P, TN>;
+    constexpr int STAGES = C::STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = align1024(smem_raw);
+    __shared__ uint64_t bar_full[STAGES], bar_empty[STAGES], bar_acc;
+    __shared__ uint32_t tmem_sh;
+    __shared__ int abort_sh;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)ptx::cluster_rank(), splits = (int)ptx::cluster_size();
+    const int tile = blockIdx.x / splits, mt = tile / p.n_ntiles, n0 = tile % p.n_ntiles * 128;
+    const int k_begin = rank * p.steps_per_cta, nk = max(0, min(p.steps_per_cta, p.ksteps - k_begin));
+    const Guard g{&abort_sh, p.status, kWaitLimitNs};
+
+    if (threadIdx.x == 0) {
+        abort_sh = 0;
+        for (int s = 0; s < STAGES; ++s) {
+            ptx::mbar_init(&bar_full[s], 1);
+            ptx::mbar_init(&bar_empty[s], 1);
+        }
+        ptx::mbar_init(&bar_acc, 1);
+        ptx::fence_mbar_init();
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(&tmem_sh, C::TM_COLS);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = tmem_sh;
+
+    if (warp == 0) {
+        if (ptx::elect_one()) {
+            // Everything that takes a division is worked out ahead of the loop (see the pair kernel).
+            constexpr int BOXES = TN <= 32 ? 1 : TN / 32;
+            const int boxes = TN / p.rb, heads = P == Dx ? 1 : p.H;
+            int c = k_begin * C::KE, ch = P == Fwd ? c / p.dk : 0, ce = c - ch * p.dk, row[BOXES], slice[BOXES];
+            if (P != Fwd) ce = c;
+#pragma unroll
+            for (int h = 0; h < BOXES; ++h) {
+                const int block = mt * boxes + h, grp = block / p.rblocks;
+                row[h] = (block - grp * p.rblocks) * p.rb;
+                slice[h] = grp * heads;
+            }
+            int s = 0;
+            uint32_t ph = 0;
+            for (int q = 0; q < nk; ++q) {
+                wait_bounded(&bar_empty[s], ph ^ 1, g);
+                ptx::mbar_arrive_expect_tx(&bar_full[s], C::STAGE);
+                uint8_t *sa = smem + s * C::STAGE, *sb = sa + C::A_BYTES;
+                if (P == Fwd) {
+                    ptx::tma_load_3d(sa, &map_w, &bar_full[s], n0, c, 0);
+                    ptx::tma_load_3d(sa + 8192, &map_w, &bar_full[s], n0 + 64, c, 0);
+                } else {
+                    ptx::tma_load_3d(sa, &map_w, &bar_full[s], c, n0, 0);
+                }
+#pragma unroll
+                for (int h = 0; h < BOXES; ++h)
+                    if (h < boxes)
+                        ptx::tma_load_3d(sb + h * p.rb * 128, &map_x, &bar_full[s], ce, row[h], slice[h] + ch);
+                c += C::KE;
+                ce += C::KE;
+                if (P == Fwd && ce >= p.dk) {
+                    ce = 0;
+                    ++ch;
+                }
+                if (++s == STAGES) {
+                    s = 0;
+                    ph ^= 1;
+                }
+            }
+            for (int q = (nk > STAGES ? nk - STAGES : 0); q < nk; ++q)   // no copy outlives the CTA
+                wait_bounded(&bar_full[q % STAGES], (q / STAGES) & 1, g);
+        }
+    } else if (warp == 1) {
+        if (ptx::elect_one() && nk > 0) {
+            const uint32_t idesc =
+                C::FP8 ? ptx::idesc_f16_f32(128, TN, false, false) : ptx::idesc_bf16_f32(128, TN, P == Fwd, false);
+            const uint32_t base = ptx::smem_u32(smem);
+            for (int q = 0; q < nk; ++q) {
+                const int s = q % STAGES;
+                wait_bounded(&bar_full[s], (q / STAGES) & 1, g);
+                ptx::tc_fence_after();
+                const uint32_t sa = base + s * C::STAGE, sb = sa + C::A_BYTES;
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    const uint64_t da = P == Fwd ? desc_mn(sa, kk) : desc_k(sa, kk);
+                    if (C::FP8)
+                        ptx::mma_ss_e4m3(tmem, da, desc_k(sb, kk), idesc, (q > 0 || kk > 0) ? 1u : 0u);
+                    else
+                        ptx::mma_ss(tmem, da, desc_k(sb, kk), idesc, (q > 0 || kk > 0) ? 1u : 0u);
+                }
+                ptx::mma_commit(&bar_empty[s]);
+            }
+            ptx::mma_commit(&bar_acc);
+            wait_bounded(&bar_acc, 0, g);
+        }
+    } else if (warp >= 4) {
+        // the partial tile, [row][128 columns] fp32, over the stages: every copy has been consumed
+        const int quarter = warp & 3;
+        const uint32_t dst = ptx::smem_u32(smem) + (quarter * 32 + lane) * 4;
+        if (nk > 0) wait_bounded(&bar_acc, 0, g);
+        ptx::tc_fence_after();
+        const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16);
+        if constexpr (TN == 16) {
+            uint32_t v[16] = {};
+            if (nk > 0) {
+                ptx::tmem_ld16(taddr, v);
+                ptx::tmem_ld_wait();
+                reg_fence(v);
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) sts_f32(dst + e * 512, __uint_as_float(v[e]));
+        } else {
+            constexpr int W = TN < 64 ? 32 : 64;   // columns read at a time
+#pragma unroll 1
+            for (int c = 0; c < TN; c += W) {
+                uint32_t v[W] = {};
+                if (nk > 0) {
+                    ptx::tmem_ld32_at<0>(taddr + c, v);
+                    if constexpr (W == 64) ptx::tmem_ld32_at<32>(taddr + c + 32, v);
+                    ptx::tmem_ld_wait();
+                    reg_fence(v);
+                }
+#pragma unroll
+                for (int e = 0; e < W; ++e) sts_f32(dst + (c + e) * 512, __uint_as_float(v[e]));
+            }
+        }
+        ptx::tc_fence_before();
+    }
+    __syncwarp();
+    __syncthreads();
+    ptx::cluster_sync();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, C::TM_COLS);
+    }
+
+    switch (splits) {   // 16 loads in flight a lane
+    case 1: join_rows<P, TN, 1, 8>(p, smem, rank, mt, n0); break;
+    case 2: join_rows<P, TN, 2, 8>(p, smem, rank, mt, n0); break;
+    case 4: join_rows<P, TN, 4, 4>(p, smem, rank, mt, n0); break;
+    default: join_rows<P, TN, 8, 2>(p, smem, rank, mt, n0); break;
+    }
+    ptx::cluster_sync();   // the others may still read this CTA's partial tile
+}
+
+__device__ __forceinline__ void unpack_bf16x8(const uint4 &u, float (&f)[8])
+{
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        f[2 * e] = __uint_as_float(w[e] << 16);
+        f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+    }
+}
+
 // dz = dy act'(z) in bf16, and the column sums of the unrounded dz over a block of rows.  A warp
 // takes a row's 256 columns at a time (8 a thread, 16 bytes), the block's 8 warps neighbouring rows.
 __global__ void __launch_bounds__(256) dz_kernel(const LinBwdArgs a, int blocks)
@@ -348,29 +666,32 @@ __global__ void __launch_bounds__(256) dz_kernel(const LinBwdArgs a, int blocks)
     if (n < a.N) {
         const int per = (a.M + blocks - 1) / blocks;
         const long long m_end = min((long long)a.M, (long long)(blockIdx.y + 1) * per);
-        for (long long m = (long long)blockIdx.y * per + warp; m < m_end; m += 8) {
-            const size_t at = ((size_t)m * a.N + n) / 8;
-            const uint4 d4 = static_cast<const uint4 *>(a.dy)[at];
-            const uint32_t d[4] = {d4.x, d4.y, d4.z, d4.w};
-            float f[8];
+        // two rows at a time: their loads are in flight together
+        for (long long m = (long long)blockIdx.y * per + warp; m < m_end; m += 16) {
+            const size_t at[2] = {((size_t)m * a.N + n) / 8, ((size_t)(m + 8) * a.N + n) / 8};
+            const bool two = m + 8 < m_end;
+            uint4 d4[2], z4[2];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                f[2 * e] = __uint_as_float(d[e] << 16);
-                f[2 * e + 1] = __uint_as_float(d[e] & 0xffff0000u);
-            }
-            if (a.z) {
-                const uint4 z4 = static_cast<const uint4 *>(a.z)[at];
-                const uint32_t z[4] = {z4.x, z4.y, z4.z, z4.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    f[2 * e] *= act_slope(__uint_as_float(z[e] << 16), a.act);
-                    f[2 * e + 1] *= act_slope(__uint_as_float(z[e] & 0xffff0000u), a.act);
+            for (int k = 0; k < 2; ++k)
+                if (k == 0 || two) {
+                    d4[k] = static_cast<const uint4 *>(a.dy)[at[k]];
+                    if (a.z) z4[k] = static_cast<const uint4 *>(a.z)[at[k]];
                 }
-                static_cast<uint4 *>(a.dz)[at] = make_uint4(ptx::pack_bf16x2(f[0], f[1]), ptx::pack_bf16x2(f[2], f[3]),
-                                                            ptx::pack_bf16x2(f[4], f[5]), ptx::pack_bf16x2(f[6], f[7]));
-            }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s[e] += f[e];
+            for (int k = 0; k < 2; ++k)
+                if (k == 0 || two) {
+                    float f[8], z[8];
+                    unpack_bf16x8(d4[k], f);
+                    if (a.z) {
+                        unpack_bf16x8(z4[k], z);
+                        times_slope(f, z, a.act);
+                        static_cast<uint4 *>(a.dz)[at[k]] =
+                            make_uint4(ptx::pack_bf16x2(f[0], f[1]), ptx::pack_bf16x2(f[2], f[3]),
+                                       ptx::pack_bf16x2(f[4], f[5]), ptx::pack_bf16x2(f[6], f[7]));
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) s[e] += f[e];
+                }
         }
     }
     if (!a.dbias) return;
@@ -406,23 +727,120 @@ int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 // do not depend on where the plan is made): a GB300's 152 SMs.
 constexpr int kPlanPairs = 76;
 
+// Raises the kernel's shared-memory limit, once per device.
+cudaError_t raise_smem(const void *kernel, int bytes, std::atomic<bool> (&set)[64])
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (set[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) == cudaSuccess)
+        set[dev].store(true, std::memory_order_relaxed);
+    return e;
+}
+
 template <Policy P, int BN>
 cudaError_t launch_pair(const GemmMaps &m, const GemmParams &p, cudaStream_t stream)
 {
     using C = Cfg<P, BN>;
     static std::atomic<bool> set[64];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    const cudaError_t e = raise_smem((const void *)gemm_pair_kernel<P, BN>, C::SMEM, set);
     if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!set[dev].load(std::memory_order_relaxed)) {
-        e = cudaFuncSetAttribute(gemm_pair_kernel<P, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-        if (e != cudaSuccess) return e;
-        set[dev].store(true, std::memory_order_relaxed);
-    }
     const int pairs = device_sm_count() / 2;
     gemm_pair_kernel<P, BN><<<2 * (p.n_items < pairs ? p.n_items : pairs), 384, C::SMEM, stream>>>(m, p);
     return cudaGetLastError();
+}
+
+template <Policy P, int TN>
+cudaError_t launch_split_tn(const CUtensorMap &w, const CUtensorMap &x, const SplitParams &p, int tiles, int splits,
+                            cudaStream_t stream)
+{
+    using C = SplitCfg<P, TN>;
+    static std::atomic<bool> set[64];
+    cudaError_t e = raise_smem((const void *)gemm_split_kernel<P, TN>, C::SMEM, set);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = splits;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(tiles * splits);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, gemm_split_kernel<P, TN>, w, x, p);
+}
+
+// How few-row products are laid out: rows a tile, CTAs a tile.
+struct SplitPlan {
+    int tn, splits, tiles;
+    double us;   // estimated time
+};
+
+// The plan with the least estimated time, in us.  The terms are fitted to a sweep of every plan over
+// 1 to 2048 rows at K, N from 768 to 8192 (the chosen plan is within 15 % of the best one there):
+// start, join and end of the kernel; a K step, 0.21 (0.27 at 256 rows, whose product alone takes that)
+// or the step's bytes at L2's rate of 15 TB/s.
+SplitPlan split_plan(int G, int T, int N, int ksteps)
+{
+    SplitPlan best{};
+    best.us = 1e30;
+    const long long M = (long long)G * T;
+    for (int tn = 16; tn <= 256; tn *= 2) {
+        const int rb = G > 1 && tn > 32 ? 32 : tn;
+        const long long tiles = (long long)ceil_div((long long)ceil_div(T, rb) * G, tn / rb) * ceil_div(N, 128);
+        if (tiles >= 0x7fffffff / 8) continue;
+        const int slots = (tn <= 64 ? 2 : 1) * 2 * kPlanPairs;
+        for (int s = 1; s <= 8 && s <= ksteps; s *= 2) {
+            const long long ctas = tiles * s;
+            if (ctas > slots) break;   // all at once, or not at all
+            const double bytes = (double)ctas * (16384 + tn * 128) / 15e6, step = tn == 256 ? 0.27 : 0.21;
+            const double us = 4.4 + tn * (0.018 + 0.024 / s) + (ctas > 2 * kPlanPairs ? 0.9 : 0.0) +
+                              ceil_div(ksteps, s) * (bytes > step ? bytes : step);
+            if (us < best.us) best = SplitPlan{tn, s, (int)tiles, us};
+        }
+        if (tn >= M) break;
+    }
+    return best;
+}
+
+template <Policy P>
+cudaError_t launch_split(const CUtensorMap &w, const CUtensorMap &x, SplitParams &p, const SplitPlan &s,
+                         cudaStream_t stream)
+{
+    p.n_ntiles = ceil_div(p.N, 128);
+    p.steps_per_cta = ceil_div(p.ksteps, s.splits);
+    switch (s.tn) {
+    case 16: return launch_split_tn<P, 16>(w, x, p, s.tiles, s.splits, stream);
+    case 32: return launch_split_tn<P, 32>(w, x, p, s.tiles, s.splits, stream);
+    case 64: return launch_split_tn<P, 64>(w, x, p, s.tiles, s.splits, stream);
+    case 128: return launch_split_tn<P, 128>(w, x, p, s.tiles, s.splits, stream);
+    default: return launch_split_tn<P, 256>(w, x, p, s.tiles, s.splits, stream);
+    }
+}
+
+// Row blocks: 128 rows of the only group, or 32 rows of one of several groups, so that a tile spans
+// groups and wastes at most 31 rows a group (576 rows a group: 18 blocks, 256-row tiles would take
+// 768 rows).
+bool set_rows(GemmParams &p, int G)
+{
+    p.rb = G > 1 ? 32 : 128;
+    p.rblocks = ceil_div(p.T, p.rb);
+    const long long all = (long long)p.rblocks * G;
+    p.n_rblocks = (int)all;
+    p.n_mtiles = ceil_div(all, BM / p.rb);
+    return all <= 0x7ffffff0LL;
+}
+
+void set_split_rows(SplitParams &p, int G, int T, int tn)
+{
+    p.T = T;
+    p.rb = G > 1 && tn > 32 ? 32 : tn;
+    p.rblocks = ceil_div(T, p.rb);
+    p.n_rblocks = p.rblocks * G;
 }
 
 bool set_items(GemmParams &p, int splits)
@@ -434,9 +852,21 @@ bool set_items(GemmParams &p, int splits)
 
 constexpr CUtensorMapDataType kBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kU8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
 
-// Whether 256-column tiles give every pair of CTAs a tile; else 128-column ones spread the work
-// over more of them.
-bool wide_tiles(long long mtiles, int N) { return mtiles * ceil_div(N, 256) >= kPlanPairs; }
+// Tiles of 256 or 128 columns, whichever is estimated to take less: rounds of tiles per pair x (K
+// steps x time of a step + a tile's fill and drain).
+struct PairPlan {
+    bool wide;
+    double us;
+};
+
+constexpr double kStepWide = 0.29, kStepNarrow = 0.22;   // us a K step (the sweep of split_plan)
+
+PairPlan pair_plan(long long mtiles, int N, int ksteps)
+{
+    auto rounds = [&](int bn) { return (double)((mtiles * ceil_div(N, bn) + kPlanPairs - 1) / kPlanPairs); };
+    const double w = 6.0 + rounds(256) * ksteps * kStepWide, n = 5.0 + rounds(128) * ksteps * kStepNarrow;
+    return w <= n ? PairPlan{true, w} : PairPlan{false, n};
+}
 
 struct DwPlan {
     bool wide;
@@ -445,8 +875,8 @@ struct DwPlan {
 
 // dw has few tiles (K x N) and a long sum (the rows), so the rows are split over pairs of CTAs where
 // the partial sums' traffic costs less than the idle pairs: the plan takes the least of
-//   rounds of items per pair x steps per item x time of a step  +  partial sums written and read.
-// 0.27 us: a step of a 256 x 256 tile at the tensor cores' rate; 5 bytes/ps: what the join reads at.
+//   rounds of items per pair x (steps per item x time of a step + 2)  +  the join's launch and traffic
+// (2.5 us, 5 bytes/ps).
 DwPlan dw_plan(int G, int T, int K, int N)
 {
     const long long steps = (long long)G * ceil_div(T, 64), mt = ceil_div(K, BM);
@@ -457,7 +887,7 @@ DwPlan dw_plan(int G, int T, int K, int N)
         for (int s = 1; s <= 16 && s <= steps; ++s) {
             const long long per = (steps + s - 1) / s;
             if ((steps + per - 1) / per != s) continue;
-            double t = (double)((tiles * s + kPlanPairs - 1) / kPlanPairs) * (per * (wide ? 0.27 : 0.16) + 1.5);
+            double t = (double)((tiles * s + kPlanPairs - 1) / kPlanPairs) * (per * (wide ? kStepWide : kStepNarrow) + 2.0);
             if (s > 1) t += 2.5 + (double)s * K * N * 8 / 5e6;
             if (t < best_t) {
                 best_t = t;
@@ -472,10 +902,39 @@ DwPlan dw_plan(int G, int T, int K, int N)
 
 cudaError_t launch_linear(const LinArgs &a, cudaStream_t stream)
 {
+    const int ksteps = ceil_div(a.K, a.q8 ? 128 : 64);
     GemmParams p = {};
     p.T = a.T;
-    p.mblocks = ceil_div(a.T, BM);
-    p.n_mtiles = p.mblocks * a.G;   // at most M
+    if (!set_rows(p, a.G)) return cudaErrorInvalidValue;
+    const PairPlan plan = pair_plan(p.n_mtiles, a.N, ksteps);
+    const SplitPlan split = split_plan(a.G, a.T, a.N, ksteps);
+    GemmMaps m;
+    CUresult r;
+    if (split.us < plan.us) {
+        SplitParams sp = {};
+        set_split_rows(sp, a.G, a.T, split.tn);
+        sp.N = a.N;
+        sp.dk = a.dk;
+        sp.H = a.H;
+        sp.ksteps = ksteps;
+        sp.bias = a.bias;
+        sp.x_scale = a.x_scale;
+        sp.w_scale = a.w_scale;
+        sp.residual = static_cast<const __nv_bfloat16 *>(a.residual);
+        sp.y = static_cast<__nv_bfloat16 *>(a.y);
+        sp.z = static_cast<__nv_bfloat16 *>(a.z);
+        sp.act = a.act;
+        sp.status = a.status;
+        if (a.q8) {
+            r = make_map_3d(&m.a, a.x, kU8, 1, a.K, a.M, 1, 128, sp.rb);
+            if (r == CUDA_SUCCESS) r = make_map_3d(&m.b, a.w, kU8, 1, a.K, a.N, 1, 128, 128);
+        } else {
+            r = make_map_3d(&m.a, a.x, kBf16, 2, a.dk, a.T, (long long)a.G * a.H, 64, sp.rb);
+            if (r == CUDA_SUCCESS) r = make_map_3d(&m.b, a.w, kBf16, 2, a.N, a.K, 1, 64, 64);
+        }
+        if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
+        return a.q8 ? launch_split<FwdQ8>(m.b, m.a, sp, split, stream) : launch_split<Fwd>(m.b, m.a, sp, split, stream);
+    }
     p.N = a.N;
     p.dk = a.dk;
     p.H = a.H;
@@ -486,18 +945,15 @@ cudaError_t launch_linear(const LinArgs &a, cudaStream_t stream)
     p.has_r = a.residual != nullptr;
     p.act = a.act;
     p.status = a.status;
-    const bool wide = wide_tiles(p.n_mtiles, a.N);
-    const int bn = wide ? 256 : 128;
+    const int bn = plan.wide ? 256 : 128;
     p.n_ntiles = ceil_div(a.N, bn);
     if (!set_items(p, 1)) return cudaErrorInvalidValue;
-    p.ksteps = p.steps_per_split = ceil_div(a.K, a.q8 ? 128 : 64);
-    GemmMaps m;
-    CUresult r;
+    p.ksteps = p.steps_per_split = ksteps;
     if (a.q8) {
         r = make_map_3d(&m.a, a.x, kU8, 1, a.K, a.M, 1, 128, 128);
         if (r == CUDA_SUCCESS) r = make_map_3d(&m.b, a.w, kU8, 1, a.K, a.N, 1, 128, bn / 2);
     } else {
-        r = make_map_3d(&m.a, a.x, kBf16, 2, a.dk, a.T, (long long)a.G * a.H, 64, 128);
+        r = make_map_3d(&m.a, a.x, kBf16, 2, a.dk, a.T, (long long)a.G * a.H, 64, p.rb);
         if (r == CUDA_SUCCESS) r = make_map_3d(&m.b, a.w, kBf16, 2, a.N, a.K, 1, 64, 64);
     }
     if (r == CUDA_SUCCESS) r = make_map_3d(&m.y, a.y, kBf16, 2, a.N, a.T, a.G, 64, 32);
@@ -505,8 +961,8 @@ cudaError_t launch_linear(const LinArgs &a, cudaStream_t stream)
     if (r == CUDA_SUCCESS && a.residual) r = make_map_3d(&m.r, a.residual, kBf16, 2, a.N, a.T, a.G, 64, 32);
     if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
     if (a.q8)
-        return wide ? launch_pair<FwdQ8, 256>(m, p, stream) : launch_pair<FwdQ8, 128>(m, p, stream);
-    return wide ? launch_pair<Fwd, 256>(m, p, stream) : launch_pair<Fwd, 128>(m, p, stream);
+        return plan.wide ? launch_pair<FwdQ8, 256>(m, p, stream) : launch_pair<FwdQ8, 128>(m, p, stream);
+    return plan.wide ? launch_pair<Fwd, 256>(m, p, stream) : launch_pair<Fwd, 128>(m, p, stream);
 }
 
 // Blocks of rows of the column sums: enough for four blocks of threads an SM, at least 16 rows each.
@@ -535,44 +991,63 @@ cudaError_t launch_linear_bwd(const LinBwdArgs &a, cudaStream_t stream)
     GemmMaps m;
     CUresult r;
     if (a.dx) {
+        const int ksteps = ceil_div(a.N, 64);
         GemmParams p = {};
         p.T = a.T;
-        p.mblocks = ceil_div(a.T, BM);
-        p.n_mtiles = p.mblocks * a.G;
-        p.N = a.K;
-        p.dk = a.dk;
-        p.H = a.H;
-        p.status = a.status;
-        const bool wide = wide_tiles(p.n_mtiles, a.K);
-        const int bn = wide ? 256 : 128;
-        p.n_ntiles = ceil_div(a.K, bn);
-        if (!set_items(p, 1)) return cudaErrorInvalidValue;
-        p.ksteps = p.steps_per_split = ceil_div(a.N, 64);
-        r = make_map_3d(&m.a, dz, kBf16, 2, a.N, a.T, a.G, 64, 128);
-        if (r == CUDA_SUCCESS) r = make_map_3d(&m.b, a.w, kBf16, 2, a.N, a.K, 1, 64, bn / 2);
-        if (r == CUDA_SUCCESS) r = make_map_3d(&m.y, a.dx, kBf16, 2, a.dk, a.T, (long long)a.G * a.H, 64, 32);
-        if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
-        e = wide ? launch_pair<Dx, 256>(m, p, stream) : launch_pair<Dx, 128>(m, p, stream);
+        if (!set_rows(p, a.G)) return cudaErrorInvalidValue;
+        const PairPlan plan = pair_plan(p.n_mtiles, a.K, ksteps);
+        const SplitPlan split = split_plan(a.G, a.T, a.K, ksteps);
+        if (split.us < plan.us) {
+            SplitParams sp = {};
+            set_split_rows(sp, a.G, a.T, split.tn);
+                sp.N = a.K;
+            sp.dk = a.dk;
+            sp.H = a.H;
+            sp.ksteps = ksteps;
+            sp.y = static_cast<__nv_bfloat16 *>(a.dx);
+            sp.status = a.status;
+            r = make_map_3d(&m.a, dz, kBf16, 2, a.N, a.T, a.G, 64, sp.rb);
+            if (r == CUDA_SUCCESS) r = make_map_3d(&m.b, a.w, kBf16, 2, a.N, a.K, 1, 64, 128);
+            if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
+            e = launch_split<Dx>(m.b, m.a, sp, split, stream);
+        } else {
+            p.N = a.K;
+            p.dk = a.dk;
+            p.H = a.H;
+            p.status = a.status;
+            const int bn = plan.wide ? 256 : 128;
+            p.n_ntiles = ceil_div(a.K, bn);
+            if (!set_items(p, 1)) return cudaErrorInvalidValue;
+            p.ksteps = p.steps_per_split = ksteps;
+            r = make_map_3d(&m.a, dz, kBf16, 2, a.N, a.T, a.G, 64, p.rb);
+            if (r == CUDA_SUCCESS) r = make_map_3d(&m.b, a.w, kBf16, 2, a.N, a.K, 1, 64, bn / 2);
+            if (r == CUDA_SUCCESS) r = make_map_3d(&m.y, a.dx, kBf16, 2, a.dk, a.T, (long long)a.G * a.H, 64, 32);
+            if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
+            e = plan.wide ? launch_pair<Dx, 256>(m, p, stream) : launch_pair<Dx, 128>(m, p, stream);
+        }
         if (e != cudaSuccess) return e;
     }
     if (a.dw) {
         const DwPlan plan = dw_plan(a.G, a.T, a.K, a.N);
         GemmParams p = {};
         p.T = a.K;
-        p.mblocks = p.n_mtiles = ceil_div(a.K, BM);
+        if (!set_rows(p, 1)) return cudaErrorInvalidValue;
         p.N = a.N;
         p.dk = a.dk;
         p.H = a.H;
         p.status = a.status;
         p.n_ntiles = ceil_div(a.N, plan.wide ? 256 : 128);
         p.tblocks = ceil_div(a.T, 64);
+        p.T_k = a.T;
         p.ksteps = a.G * p.tblocks;
         p.steps_per_split = plan.steps_per_split;
         if (!set_items(p, plan.splits)) return cudaErrorInvalidValue;
-        p.part = plan.splits > 1 ? a.dw_part : nullptr;
+        p.part = plan.splits > 1;
         r = make_map_3d(&m.a, a.x, kBf16, 2, a.dk, a.T, (long long)a.G * a.H, 64, 64);
         if (r == CUDA_SUCCESS) r = make_map_3d(&m.b, dz, kBf16, 2, a.N, a.T, a.G, 64, 64);
-        if (r == CUDA_SUCCESS) r = make_map_3d(&m.y, a.dw, kBf16, 2, a.N, a.K, 1, 64, 32);
+        if (r == CUDA_SUCCESS)
+            r = p.part ? make_map_3d(&m.y, a.dw_part, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, a.N, a.K, plan.splits, 32, 32)
+                       : make_map_3d(&m.y, a.dw, kBf16, 2, a.N, a.K, 1, 64, 32);
         if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
         e = plan.wide ? launch_pair<Dw, 256>(m, p, stream) : launch_pair<Dw, 128>(m, p, stream);
         if (e == cudaSuccess && plan.splits > 1) {
