@@ -13,13 +13,14 @@
 // of A and BN / 2 columns of B a step, 32 KB for 2 x 128 x 256 x 64 multiply-adds where a single CTA
 // with the same tile of its own would load 48 KB, which is what bounds the K loop (L2 bandwidth and
 // the reads of shared memory).  Each CTA: warp 0 TMA producer, warp 1 tcgen05 issuer (even CTA),
-// warps 4-11 epilogue; the accumulator is double-buffered in TMEM, so a tile's epilogue overlaps the
+// warps 4-19 epilogue; the accumulator is double-buffered in TMEM, so a tile's epilogue overlaps the
 // products of the next.
 //
-// Epilogue: a warp owns 32 rows x 64 columns at a time (thread = row): TMEM -> registers, scales,
-// bias, activation, residual in fp32, one rounding to bf16, a swizzled 4 KB buffer in shared memory,
-// one TMA store.  The residual comes the same way round, by a TMA load into that buffer before the
-// accumulator is ready.
+// Epilogue: a warp owns 32 rows x 64 columns of a tile (thread = row): TMEM -> registers, scales, bias,
+// activation, residual in fp32, one rounding to bf16, a swizzled 4 KB buffer in shared memory, one TMA
+// store.  The residual comes the same way round, by a TMA load into that buffer before the accumulator
+// is ready.  Sixteen warps, since a warp's chain of loads, MUFU operations and stores is long: with
+// eight, GELU with z kept took longer than the products of 1024 of K.
 #include "act.cuh"
 #include "common.cuh"
 #include "kernels.h"
@@ -30,6 +31,7 @@ namespace attn {
 namespace {
 
 constexpr int BM = 256;            // rows of a tile (both CTAs)
+constexpr int kEpiWarps = 16;      // four for each 32 rows of a CTA, each with 64 of 256 columns
 constexpr int kGroupM = 8;         // row tiles walked side by side, for reuse of B in L2
 
 struct GemmMaps {
@@ -60,7 +62,7 @@ struct Cfg {
     static constexpr int A_BYTES = 128 * 128, B_BYTES = BN / 2 * 128;
     static constexpr int STAGE = A_BYTES + B_BYTES;
     static constexpr int STAGES = BN == 256 ? 5 : 6;
-    static constexpr int EPI = 8 * 2 * 4096;               // two buffers for each epilogue warp
+    static constexpr int EPI = kEpiWarps * 4096;           // a 32 x 64 bf16 buffer for each epilogue warp
     static constexpr int SMEM = STAGES * STAGE + EPI + 1024;
     static constexpr uint32_t TM_COLS = 2 * BN;
 };
@@ -95,14 +97,14 @@ __device__ __forceinline__ uint2 pack_bf16x4(const uint64_t (&f)[2])
 }
 
 template <Policy P, int BN>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 32 * kEpiWarps, 1)
     gemm_pair_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmParams p)
 {
     using C = Cfg<P, BN>;
     constexpr int STAGES = C::STAGES;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = align1024(smem_raw);
-    __shared__ uint64_t bar_full[STAGES], bar_empty[STAGES], bar_acc_full[2], bar_acc_empty[2], bar_res[16];
+    __shared__ uint64_t bar_full[STAGES], bar_empty[STAGES], bar_acc_full[2], bar_acc_empty[2], bar_res[kEpiWarps];
     __shared__ uint32_t tmem_sh;
     __shared__ int abort_sh;
 
@@ -130,9 +132,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
         }
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(&bar_acc_full[b], 1);
-            ptx::mbar_init(&bar_acc_empty[b], 16);   // the epilogue warps of both CTAs
+            ptx::mbar_init(&bar_acc_empty[b], 2 * kEpiWarps);   // the epilogue warps of both CTAs
         }
-        for (int b = 0; b < 16; ++b) ptx::mbar_init(&bar_res[b], 1);
+        for (int b = 0; b < kEpiWarps; ++b) ptx::mbar_init(&bar_res[b], 1);
         ptx::fence_mbar_init();
     }
     if (warp == 1) {
@@ -264,12 +266,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
         }
     } else if (warp >= 4) {
         const int quarter = warp & 3, set = (warp - 4) >> 2, ew = warp - 4;
-        uint8_t *buf = smem + STAGES * C::STAGE + ew * 8192;
-        uint64_t *rbar = bar_res + 2 * ew;
-        uint32_t rphase = 0;   // bit b: the parity the next load into buffer b completes
-        const uint32_t sbuf = ptx::smem_u32(buf);
+        uint8_t *buf = smem + STAGES * C::STAGE + ew * 4096;
+        uint64_t *rbar = bar_res + ew;
+        uint32_t rphase = 0;
+        const uint32_t sbuf = ptx::smem_u32(buf), row = sbuf + lane * 128;
         const uint32_t empty0 = ptx::cluster_addr(ptx::smem_u32(&bar_acc_empty[0]), 0);
-        const uint32_t empty1 = ptx::cluster_addr(ptx::smem_u32(&bar_acc_empty[1]), 0);
         int li = 0;
         for (int item = cluster; item < p.n_items; item += n_clusters, ++li) {
             int ks, mt, nt, k_begin, nk;
@@ -277,123 +278,132 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
             const int ab = li & 1;
             const int first = mt * BM + (int)rank * 128 + quarter * 32, block = first / p.rb;
             const int grp = block / p.rblocks, i0 = block % p.rblocks * p.rb + first % p.rb;
-            const int n0 = nt * BN;
-            const bool rows = i0 < p.T && block < p.n_rblocks;
-            // buffer of chunk j: alternating, or both for y and z
-            auto load_res = [&](int col, int b) {
-                ptx::mbar_arrive_expect_tx(&rbar[b], 4096);
-                ptx::tma_load_3d(buf + b * 4096, &maps.r, &rbar[b], col, i0, grp);
+            const int col0 = nt * BN + set * 64;
+            const bool mine = set * 64 < BN && col0 < p.N && i0 < p.T && block < p.n_rblocks;
+            auto load_res = [&] {
+                ptx::mbar_arrive_expect_tx(rbar, 4096);
+                ptx::tma_load_3d(buf, &maps.r, rbar, col0, i0, grp);
             };
-            if (lane == 0) {
-                ptx::bulk_wait_group_read<0>();   // the buffers are free again
-                if (p.has_r && rows) {
-                    if (n0 + set * 64 < p.N) load_res(n0 + set * 64, 0);
-                    if (!p.has_z && BN == 256 && n0 + set * 64 + 128 < p.N) load_res(n0 + set * 64 + 128, 1);
+            // Leaves the buffer to a TMA store.
+            auto store = [&](const CUtensorMap *map, int c, int slice) {
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    ptx::tma_store_3d(map, buf, c, i0, slice);
+                    ptx::bulk_commit_group();
                 }
-            }
-            __syncwarp();
-            const uint64_t xs = f2_both((P == FwdQ8 && i0 + lane < p.T) ? p.x_scale[i0 + lane] : 0.f);
+            };
+            // The buffer is free again.
+            auto reclaim = [&] {
+                if (lane == 0) ptx::bulk_wait_group_read<0>();
+                __syncwarp();
+            };
+            reclaim();
+            if (lane == 0 && p.has_r && !p.has_z && mine) load_res();
+            const uint64_t xs = f2_both((P == FwdQ8 && mine && i0 + lane < p.T) ? p.x_scale[i0 + lane] : 0.f);
             wait_bounded(&bar_acc_full[ab], (li >> 1) & 1, g);
             ptx::tc_fence_after();
-            const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + ab * BN;
-#pragma unroll 1
-            for (int j = 0; j < BN / 128; ++j) {
-                const int c0 = set * 64 + j * 128, col0 = n0 + c0;
-                if (col0 >= p.N || !rows) break;
-                const int b = p.has_z ? 0 : j;
-                if (p.has_z && j > 0) {
-                    if (lane == 0) {
-                        ptx::bulk_wait_group_read<0>();
-                        if (p.has_r) load_res(col0, 0);
-                    }
-                    __syncwarp();
-                }
-                if (p.has_r) {
-                    wait_bounded(&rbar[b], (rphase >> b) & 1, g);
-                    rphase ^= 1u << b;
-                }
-                const uint32_t yrow = sbuf + b * 4096 + lane * 128, zrow = sbuf + 4096 + lane * 128;
+            const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + ab * BN + set * 64;
+            auto release = [&] {   // this warp has read its part of the accumulator
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive_cluster(empty0 + ab * 8);
+            };
+            if (!mine) {
+                release();
+                continue;
+            }
+            if (P == Dw && p.part) {   // fp32 partial sums: 32 columns are a 128-byte row
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
                     uint32_t v[32];
-                    ptx::tmem_ld32(taddr + c0 + half * 32, v);
+                    ptx::tmem_ld32(taddr + half * 32, v);
                     ptx::tmem_ld_wait();
                     reg_fence(v);
-                    if (P == Dw && p.part) {   // fp32 partial sums: 32 columns are a 128-byte row
-                        if (lane == 0) ptx::bulk_wait_group_read<1>();   // the buffer's last store
-                        __syncwarp();
-#pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            sts_u128(sbuf + half * 4096 + lane * 128 + ((q ^ (lane & 7)) << 4),
-                                     make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]));
-                        ptx::fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) {
-                            if (col0 + half * 32 < p.N)
-                                ptx::tma_store_3d(&maps.y, buf + half * 4096, col0 + half * 32, i0, ks);
-                            ptx::bulk_commit_group();
-                        }
-                        continue;
+                    if (half) {
+                        release();
+                        reclaim();
                     }
-                    uint64_t f[16];   // pairs of neighbouring columns
+                    if (col0 + half * 32 >= p.N) continue;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        f[i] = ptx::f2_pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-                    if (P == Fwd || P == FwdQ8) {
+                    for (int q = 0; q < 8; ++q)
+                        sts_u128(row + ((q ^ (lane & 7)) << 4),
+                                 make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]));
+                    store(&maps.y, col0 + half * 32, ks);
+                }
+                continue;
+            }
+            // z (or, without scales and bias, the sums) of 32 columns, as pairs
+            auto load_z = [&](int half, uint64_t (&f)[16]) {
+                uint32_t v[32];
+                ptx::tmem_ld32(taddr + half * 32, v);
+                ptx::tmem_ld_wait();
+                reg_fence(v);
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) {   // 4 columns
-                            const int col = col0 + half * 32 + q * 4;
-                            ulonglong2 b = make_ulonglong2(0, 0);
-                            if (p.bias && col < p.N) b = __ldg(reinterpret_cast<const ulonglong2 *>(p.bias + col));
-                            if (P == FwdQ8) {
-                                ulonglong2 w = make_ulonglong2(0, 0);
-                                if (col < p.N) w = __ldg(reinterpret_cast<const ulonglong2 *>(p.w_scale + col));
-                                f[2 * q] = ptx::fma_f32x2(f[2 * q], ptx::mul_f32x2(w.x, xs), b.x);
-                                f[2 * q + 1] = ptx::fma_f32x2(f[2 * q + 1], ptx::mul_f32x2(w.y, xs), b.y);
-                            } else if (p.bias) {
-                                f[2 * q] = ptx::add_f32x2(f[2 * q], b.x);
-                                f[2 * q + 1] = ptx::add_f32x2(f[2 * q + 1], b.y);
-                            }
-                        }
-                        if (p.has_z) {
+                for (int i = 0; i < 16; ++i)
+                    f[i] = ptx::f2_pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                if (P != Fwd && P != FwdQ8) return;
 #pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                sts_u128(zrow + (((half * 4 + q) ^ (lane & 7)) << 4), pack_bf16x8(f + 4 * q));
-                        }
-                        activate(f, p.act);
-                        if (p.has_r) {
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                const uint4 r = lds_u128(yrow + (((half * 4 + q) ^ (lane & 7)) << 4));
-                                const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    f[4 * q + e] = ptx::add_f32x2(
-                                        f[4 * q + e], ptx::f2_pack(__uint_as_float(w[e] << 16),
-                                                                   __uint_as_float(w[e] & 0xffff0000u)));
-                            }
-                        }
+                for (int q = 0; q < 8; ++q) {   // 4 columns
+                    const int col = col0 + half * 32 + q * 4;
+                    ulonglong2 b = make_ulonglong2(0, 0);
+                    if (p.bias && col < p.N) b = __ldg(reinterpret_cast<const ulonglong2 *>(p.bias + col));
+                    if (P == FwdQ8) {
+                        ulonglong2 w = make_ulonglong2(0, 0);
+                        if (col < p.N) w = __ldg(reinterpret_cast<const ulonglong2 *>(p.w_scale + col));
+                        f[2 * q] = ptx::fma_f32x2(f[2 * q], ptx::mul_f32x2(w.x, xs), b.x);
+                        f[2 * q + 1] = ptx::fma_f32x2(f[2 * q + 1], ptx::mul_f32x2(w.y, xs), b.y);
+                    } else if (p.bias) {
+                        f[2 * q] = ptx::add_f32x2(f[2 * q], b.x);
+                        f[2 * q + 1] = ptx::add_f32x2(f[2 * q + 1], b.y);
                     }
+                }
+            };
+            if (p.has_z) {   // a pass of its own: reading the accumulator twice is cheaper than a second buffer
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    uint64_t f[16];
+                    load_z(half, f);
 #pragma unroll
                     for (int q = 0; q < 4; ++q)   // 8 columns: 16 bytes of the row
-                        sts_u128(yrow + (((half * 4 + q) ^ (lane & 7)) << 4), pack_bf16x8(f + 4 * q));
+                        sts_u128(row + (((half * 4 + q) ^ (lane & 7)) << 4), pack_bf16x8(f + 4 * q));
                 }
-                if (!(P == Dw && p.part)) {
-                    ptx::fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (P == Dx)
-                            ptx::tma_store_3d(&maps.y, buf + b * 4096, col0 % p.dk, i0, grp * p.H + col0 / p.dk);
-                        else
-                            ptx::tma_store_3d(&maps.y, buf + b * 4096, col0, i0, grp);
-                        if (p.has_z) ptx::tma_store_3d(&maps.z, buf + 4096, col0, i0, grp);
-                        ptx::bulk_commit_group();
+                store(&maps.z, col0, grp);
+            }
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+                uint64_t f[16];
+                load_z(half, f);
+                if (half) release();
+                if (P == Fwd || P == FwdQ8) activate(f, p.act);
+                if (half == 0 && p.has_z) {
+                    reclaim();
+                    if (p.has_r && lane == 0) load_res();
+                }
+                if ((P == Fwd || P == FwdQ8) && p.has_r) {
+                    if (half == 0) {
+                        wait_bounded(rbar, rphase, g);
+                        rphase ^= 1;
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint4 r = lds_u128(row + (((half * 4 + q) ^ (lane & 7)) << 4));
+                        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            f[4 * q + e] =
+                                ptx::add_f32x2(f[4 * q + e], ptx::f2_pack(__uint_as_float(w[e] << 16),
+                                                                          __uint_as_float(w[e] & 0xffff0000u)));
                     }
                 }
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    sts_u128(row + (((half * 4 + q) ^ (lane & 7)) << 4), pack_bf16x8(f + 4 * q));
             }
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive_cluster(ab ? empty1 : empty0);
+            if (P == Dx)
+                store(&maps.y, col0 % p.dk, grp * p.H + col0 / p.dk);
+            else
+                store(&maps.y, col0, grp);
         }
         if (lane == 0) ptx::bulk_wait_group<0>();
     }
@@ -748,7 +758,7 @@ cudaError_t launch_pair(const GemmMaps &m, const GemmParams &p, cudaStream_t str
     const cudaError_t e = raise_smem((const void *)gemm_pair_kernel<P, BN>, C::SMEM, set);
     if (e != cudaSuccess) return e;
     const int pairs = device_sm_count() / 2;
-    gemm_pair_kernel<P, BN><<<2 * (p.n_items < pairs ? p.n_items : pairs), 384, C::SMEM, stream>>>(m, p);
+    gemm_pair_kernel<P, BN><<<2 * (p.n_items < pairs ? p.n_items : pairs), 128 + 32 * kEpiWarps, C::SMEM, stream>>>(m, p);
     return cudaGetLastError();
 }
 
