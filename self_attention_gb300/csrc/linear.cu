@@ -3,8 +3,8 @@
 // C[256 x BN] = sum over K steps of A B, with operand policies:
 //   Fwd   : A = x (K-major), B = w [K, N] (MN-major).
 //   FwdQ8 : A = xq, B = wq [N, K], both K-major, e4m3.
-//   Dx    : A = dz (K-major), B = w (K-major: the rows of w are the columns of dx).
-//   Dw    : A = x^T, B = dz, both MN-major; the K steps are 64 rows each.
+//   Bwd   : dx with A = dz, B = w (both K-major: the rows of w are the columns of dx), and dw with
+//           A = x^T, B = dz (both MN-major), its K steps 64 rows each, in one launch.
 // x (and dx) may be split by heads, [G, H, T, dk] with row m = g T + i and column c = h dk + e: a
 // 64-column box lies in one head, so only the coordinates of the copies differ.  A row block (and, for
 // dw, a step) lies in one group g; the copies' zero fill and clipping end it at the group's last row.
@@ -35,29 +35,39 @@ constexpr int kEpiWarps = 16;      // four for each 32 rows of a CTA, each with 
 constexpr int kGroupM = 8;         // row tiles walked side by side, for reuse of B in L2
 
 struct GemmMaps {
-    CUtensorMap a, b, y, z, r;
+    CUtensorMap a, b, y;       // Fwd, FwdQ8; Bwd: of dx
+    CUtensorMap a2, b2, y2;    // Bwd: of dw; Fwd, FwdQ8: a2 the residual, y2 z
 };
 
-struct GemmParams {
+// One product: rows in groups, tiles, steps.
+struct Prob {
     int T;                         // rows of one group
     int rb, rblocks, n_rblocks;    // rows of a row block, row blocks of one group and of all
     int n_mtiles, n_ntiles, N;     // row tiles, column tiles, columns
-    int dk, H;                     // the head split of the side that has one (A; Dx: y)
+    int dk, H;                     // the head split of the side that has one (A; dx: y)
     int ksteps, steps_per_split;   // K steps in all and per item
-    int tblocks, T_k;              // Dw: steps and rows of one group
+    int tblocks, T_k;              // dw: steps and rows of one group
     int n_items;
+};
+
+struct GemmParams {
+    Prob q[2];                     // [0] Fwd, FwdQ8, dx; [1] dw
     const float *bias, *x_scale, *w_scale;
     int has_z, has_r, act;
-    int part;                      // Dw split over K: y maps [splits][rows][N] fp32 partial sums
+    // Bwd: items of dx each cluster takes, and how many more those from a_clusters on take first; whether
+    // y2 maps [splits][rows][N] fp32 partial sums; the column sums to finish (col_rows partial rows)
+    int x_all, x_early, a_clusters, part;
+    const float *col_part;
+    float *dbias;
+    int col_rows, col_n;
     int *status;
 };
 
-enum Policy { Fwd, FwdQ8, Dx, Dw };
+enum Policy { Fwd, FwdQ8, Bwd, Dx /* split kernel only */ };
 
 template <Policy P, int BN>
 struct Cfg {
     static constexpr bool FP8 = P == FwdQ8;
-    static constexpr bool A_MN = P == Dw, B_MN = P == Fwd || P == Dw;
     static constexpr int KE = FP8 ? 128 : 64;              // elements of K a step: 128 bytes
     static constexpr int A_BYTES = 128 * 128, B_BYTES = BN / 2 * 128;
     static constexpr int STAGE = A_BYTES + B_BYTES;
@@ -111,16 +121,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 32 * kEpiWarps
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = ptx::cluster_rank();
     const int cluster = blockIdx.x >> 1, n_clusters = gridDim.x >> 1;
-    const int tiles = p.n_mtiles * p.n_ntiles;
+    // The cluster's items: Fwd every n_clusters-th tile.  Bwd: its share of dw's (w = 1), then as many of
+    // dx's as fill it up to the others' level.  The clusters with less of dw deal out the first of dx's
+    // items among themselves, then all of them deal out the rest: at any time they work on neighbouring
+    // tiles, whose operands L2 then holds.
+    const int n_dw = P == Bwd && cluster < p.q[1].n_items ? (p.q[1].n_items - cluster - 1) / n_clusters + 1 : 0;
+    const int early = P == Bwd && cluster >= p.a_clusters ? p.x_early : 0;
+    auto item_at = [&](int li, int &w, int &item) {
+        w = li < n_dw;
+        if (P != Bwd || w) {
+            item = cluster + li * n_clusters;
+            return w || item < p.q[0].n_items;
+        }
+        const int j = li - n_dw;
+        if (j >= early + p.x_all) return false;
+        const long long at = j < early ? (long long)j * (n_clusters - p.a_clusters) + cluster - p.a_clusters
+                                       : (long long)p.x_early * (n_clusters - p.a_clusters) +
+                                             (long long)(j - early) * n_clusters + cluster;
+        item = (int)min(at, (long long)p.q[0].n_items);
+        return item < p.q[0].n_items;
+    };
     // item -> K range, row tile, column tile: kGroupM row tiles side by side, column by column
-    auto decode = [&](int item, int &ks, int &mt, int &nt, int &k_begin, int &nk) {
+    auto decode = [&](const Prob &q, int item, int &ks, int &mt, int &nt, int &k_begin, int &nk) {
+        const int tiles = q.n_mtiles * q.n_ntiles;
         ks = item / tiles;
-        const int t = item - ks * tiles, per = kGroupM * p.n_ntiles, first = t / per * kGroupM, q = t % per;
-        const int rows = min(kGroupM, p.n_mtiles - first);
-        mt = first + q % rows;
-        nt = q / rows;
-        k_begin = ks * p.steps_per_split;
-        nk = min(p.steps_per_split, p.ksteps - k_begin);
+        const int t = item - ks * tiles, per = kGroupM * q.n_ntiles, first = t / per * kGroupM, r = t % per;
+        const int rows = min(kGroupM, q.n_mtiles - first);
+        mt = first + r % rows;
+        nt = r / rows;
+        k_begin = ks * q.steps_per_split;
+        nk = min(q.steps_per_split, q.ksteps - k_begin);
     };
     const Guard g{&abort_sh, p.status, kWaitLimitNs};
 
@@ -152,52 +182,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 32 * kEpiWarps
             int s = 0;          // place in the stage ring, and the parity of its turn, across items
             uint32_t ph = 0;
             const uint32_t full0 = ptx::cluster_addr(ptx::smem_u32(&bar_full[0]), 0);
-            for (int item = cluster; item < p.n_items; item += n_clusters) {
+            int w, item;
+            for (int li = 0; item_at(li, w, item); ++li) {
+                const Prob &pr = p.q[P == Bwd ? w : 0];
                 int ks, mt, nt, k_begin, nk;
-                decode(item, ks, mt, nt, k_begin, nk);
+                decode(pr, item, ks, mt, nt, k_begin, nk);
                 // this CTA's 128 rows: one block of 128, or four of 32 that may lie in different groups
-                const int per_cta = 128 / p.rb, block0 = (mt * 2 + (int)rank) * per_cta;
+                const int per_cta = 128 / pr.rb, block0 = (mt * 2 + (int)rank) * per_cta;
                 int grp[4], i0[4];
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
-                    grp[h] = (block0 + h) / p.rblocks;
-                    i0[h] = (block0 + h) % p.rblocks * p.rb;
+                    grp[h] = (block0 + h) / pr.rblocks;
+                    i0[h] = (block0 + h) % pr.rblocks * pr.rb;
                 }
                 const int n0 = nt * BN + (int)rank * (BN / 2);
-                // Walking K without divisions, which would take this one thread longer than a step:
-                // Dw: group gk, row t0 of it; else: column c of A, at ce of head ch.
-                int gk = 0, t0 = 0, c = k_begin * C::KE, ce = c, ch = 0, col[2], head[2];
-                if (P == Dw) {
-                    gk = k_begin / p.tblocks;
-                    t0 = (k_begin - gk * p.tblocks) * 64;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        head[h] = (i0[0] + 64 * h) / p.dk;
-                        col[h] = i0[0] + 64 * h - head[h] * p.dk;
-                    }
-                } else if (P != Dx) {
-                    ch = c / p.dk;
-                    ce = c - ch * p.dk;
-                }
-                for (int q = 0; q < nk; ++q) {
+                // K is walked without divisions, which would take this one thread longer than a step
+                auto turn = [&] {   // the next stage is free; both CTAs' copies complete on the even one's barrier
                     wait_bounded(&bar_empty[s], ph ^ 1, g);
                     if (rank == 0) ptx::mbar_arrive_expect_tx(&bar_full[s], 2 * C::STAGE);
-                    const uint32_t bar = full0 + s * 8;
-                    uint8_t *sa = smem + s * C::STAGE, *sb = sa + C::A_BYTES;
-                    if (P == Dw) {
+                };
+                auto next = [&] {
+                    if (++s == STAGES) {
+                        s = 0;
+                        ph ^= 1;
+                    }
+                };
+                if (P == Bwd && w) {   // dw: 64 rows t0.. of group gk
+                    int gk = k_begin / pr.tblocks, t0 = (k_begin - gk * pr.tblocks) * 64, col[2], head[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        head[h] = (i0[0] + 64 * h) / pr.dk;
+                        col[h] = i0[0] + 64 * h - head[h] * pr.dk;
+                    }
+                    for (int q = 0; q < nk; ++q) {
+                        turn();
+                        const uint32_t bar = full0 + s * 8;
+                        uint8_t *sa = smem + s * C::STAGE, *sb = sa + C::A_BYTES;
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
-                            ptx::tma_load_3d_pair(sa + h * 8192, &maps.a, bar, col[h], t0, gk * p.H + head[h]);
+                            ptx::tma_load_3d_pair(sa + h * 8192, &maps.a2, bar, col[h], t0, gk * pr.H + head[h]);
 #pragma unroll
                         for (int h = 0; h < BN / 128; ++h)
-                            ptx::tma_load_3d_pair(sb + h * 8192, &maps.b, bar, n0 + 64 * h, t0, gk);
+                            ptx::tma_load_3d_pair(sb + h * 8192, &maps.b2, bar, n0 + 64 * h, t0, gk);
                         t0 += 64;
-                        if (t0 >= p.T_k) {
+                        if (t0 >= pr.T_k) {
                             t0 = 0;
                             ++gk;
                         }
-                    } else {
-                        const int heads = P == Dx ? 1 : p.H;
+                        next();
+                    }
+                } else {   // column c of A: ce of head ch
+                    int c = k_begin * C::KE, ch = P == Fwd ? c / pr.dk : 0, ce = c - ch * pr.dk;
+                    if (P != Fwd) ce = c;
+                    const int heads = P == Bwd ? 1 : pr.H;
+                    for (int q = 0; q < nk; ++q) {
+                        turn();
+                        const uint32_t bar = full0 + s * 8;
+                        uint8_t *sa = smem + s * C::STAGE, *sb = sa + C::A_BYTES;
                         ptx::tma_load_3d_pair(sa, &maps.a, bar, ce, i0[0], grp[0] * heads + ch);
                         if (per_cta == 4)
 #pragma unroll
@@ -212,14 +253,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 32 * kEpiWarps
                         }
                         c += C::KE;
                         ce += C::KE;
-                        if (P == Fwd && ce >= p.dk) {
+                        if (P == Fwd && ce >= pr.dk) {
                             ce = 0;
                             ++ch;
                         }
-                    }
-                    if (++s == STAGES) {
-                        s = 0;
-                        ph ^= 1;
+                        next();
                     }
                 }
             }
@@ -230,14 +268,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 32 * kEpiWarps
         }
     } else if (warp == 1 && rank == 0) {
         if (ptx::elect_one()) {
-            const uint32_t idesc = C::FP8 ? ptx::idesc_f16_f32(BM, BN, false, false)   // format 0: e4m3
-                                          : ptx::idesc_bf16_f32(BM, BN, C::A_MN, C::B_MN);
             const uint32_t base = ptx::smem_u32(smem);
-            int s = 0, li = 0;
+            int s = 0, li = 0, w, item;
             uint32_t ph = 0;
-            for (int item = cluster; item < p.n_items; item += n_clusters, ++li) {
+            for (; item_at(li, w, item); ++li) {
+                const Prob &pr = p.q[P == Bwd ? w : 0];
                 int ks, mt, nt, k_begin, nk;
-                decode(item, ks, mt, nt, k_begin, nk);
+                decode(pr, item, ks, mt, nt, k_begin, nk);
+                const bool a_mn = P == Bwd && w, b_mn = P == Fwd || a_mn;
+                const uint32_t idesc = C::FP8 ? ptx::idesc_f16_f32(BM, BN, false, false)   // format 0: e4m3
+                                              : ptx::idesc_bf16_f32(BM, BN, a_mn, b_mn);
                 const int ab = li & 1;
                 wait_bounded<true>(&bar_acc_empty[ab], ((li >> 1) & 1) ^ 1, g);   // epilogues of item li-2 done
                 ptx::tc_fence_after();
@@ -247,8 +287,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 32 * kEpiWarps
                     const uint32_t sa = base + s * C::STAGE, sb = sa + C::A_BYTES;
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        ptx::mma_pair<C::FP8>(tmem + ab * BN, C::A_MN ? desc_mn(sa, kk) : desc_k(sa, kk),
-                                              C::B_MN ? desc_mn(sb, kk) : desc_k(sb, kk), idesc,
+                        ptx::mma_pair<C::FP8>(tmem + ab * BN, a_mn ? desc_mn(sa, kk) : desc_k(sa, kk),
+                                              b_mn ? desc_mn(sb, kk) : desc_k(sb, kk), idesc,
                                               (q > 0 || kk > 0) ? 1u : 0u);
                     ptx::mma_commit_pair(&bar_empty[s]);
                     if (++s == STAGES) {
@@ -271,18 +311,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 32 * kEpiWarps
         uint32_t rphase = 0;
         const uint32_t sbuf = ptx::smem_u32(buf), row = sbuf + lane * 128;
         const uint32_t empty0 = ptx::cluster_addr(ptx::smem_u32(&bar_acc_empty[0]), 0);
-        int li = 0;
-        for (int item = cluster; item < p.n_items; item += n_clusters, ++li) {
+        int w, item;
+        for (int li = 0; item_at(li, w, item); ++li) {
+            const Prob &pr = p.q[P == Bwd ? w : 0];
             int ks, mt, nt, k_begin, nk;
-            decode(item, ks, mt, nt, k_begin, nk);
+            decode(pr, item, ks, mt, nt, k_begin, nk);
             const int ab = li & 1;
-            const int first = mt * BM + (int)rank * 128 + quarter * 32, block = first / p.rb;
-            const int grp = block / p.rblocks, i0 = block % p.rblocks * p.rb + first % p.rb;
+            const int first = mt * BM + (int)rank * 128 + quarter * 32, block = first / pr.rb;
+            const int grp = block / pr.rblocks, i0 = block % pr.rblocks * pr.rb + first % pr.rb;
             const int col0 = nt * BN + set * 64;
-            const bool mine = set * 64 < BN && col0 < p.N && i0 < p.T && block < p.n_rblocks;
+            const bool mine = set * 64 < BN && col0 < pr.N && i0 < pr.T && block < pr.n_rblocks;
             auto load_res = [&] {
                 ptx::mbar_arrive_expect_tx(rbar, 4096);
-                ptx::tma_load_3d(buf, &maps.r, rbar, col0, i0, grp);
+                ptx::tma_load_3d(buf, &maps.a2, rbar, col0, i0, grp);
             };
             // Leaves the buffer to a TMA store.
             auto store = [&](const CUtensorMap *map, int c, int slice) {
@@ -300,7 +341,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 32 * kEpiWarps
             };
             reclaim();
             if (lane == 0 && p.has_r && !p.has_z && mine) load_res();
-            const uint64_t xs = f2_both((P == FwdQ8 && mine && i0 + lane < p.T) ? p.x_scale[i0 + lane] : 0.f);
+            const uint64_t xs = f2_both((P == FwdQ8 && mine && i0 + lane < pr.T) ? p.x_scale[i0 + lane] : 0.f);
             wait_bounded(&bar_acc_full[ab], (li >> 1) & 1, g);
             ptx::tc_fence_after();
             const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + ab * BN + set * 64;
@@ -313,7 +354,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 32 * kEpiWarps
                 release();
                 continue;
             }
-            if (P == Dw && p.part) {   // fp32 partial sums: 32 columns are a 128-byte row
+            if (P == Bwd && w && p.part) {   // fp32 partial sums: 32 columns are a 128-byte row
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
                     uint32_t v[32];
@@ -324,12 +365,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 32 * kEpiWarps
                         release();
                         reclaim();
                     }
-                    if (col0 + half * 32 >= p.N) continue;
+                    if (col0 + half * 32 >= pr.N) continue;
 #pragma unroll
                     for (int q = 0; q < 8; ++q)
                         sts_u128(row + ((q ^ (lane & 7)) << 4),
                                  make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]));
-                    store(&maps.y, col0 + half * 32, ks);
+                    store(&maps.y2, col0 + half * 32, ks);
                 }
                 continue;
             }
@@ -342,20 +383,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 32 * kEpiWarps
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     f[i] = ptx::f2_pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-                if (P != Fwd && P != FwdQ8) return;
+                if constexpr (P == Fwd || P == FwdQ8) {
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {   // 4 columns
-                    const int col = col0 + half * 32 + q * 4;
-                    ulonglong2 b = make_ulonglong2(0, 0);
-                    if (p.bias && col < p.N) b = __ldg(reinterpret_cast<const ulonglong2 *>(p.bias + col));
-                    if (P == FwdQ8) {
-                        ulonglong2 w = make_ulonglong2(0, 0);
-                        if (col < p.N) w = __ldg(reinterpret_cast<const ulonglong2 *>(p.w_scale + col));
-                        f[2 * q] = ptx::fma_f32x2(f[2 * q], ptx::mul_f32x2(w.x, xs), b.x);
-                        f[2 * q + 1] = ptx::fma_f32x2(f[2 * q + 1], ptx::mul_f32x2(w.y, xs), b.y);
-                    } else if (p.bias) {
-                        f[2 * q] = ptx::add_f32x2(f[2 * q], b.x);
-                        f[2 * q + 1] = ptx::add_f32x2(f[2 * q + 1], b.y);
+                    for (int q = 0; q < 8; ++q) {   // 4 columns
+                        const int col = col0 + half * 32 + q * 4;
+                        ulonglong2 bias = make_ulonglong2(0, 0);
+                        if (p.bias && col < pr.N) bias = __ldg(reinterpret_cast<const ulonglong2 *>(p.bias + col));
+                        if (P == FwdQ8) {
+                            ulonglong2 ws = make_ulonglong2(0, 0);
+                            if (col < pr.N) ws = __ldg(reinterpret_cast<const ulonglong2 *>(p.w_scale + col));
+                            f[2 * q] = ptx::fma_f32x2(f[2 * q], ptx::mul_f32x2(ws.x, xs), bias.x);
+                            f[2 * q + 1] = ptx::fma_f32x2(f[2 * q + 1], ptx::mul_f32x2(ws.y, xs), bias.y);
+                        } else if (p.bias) {
+                            f[2 * q] = ptx::add_f32x2(f[2 * q], bias.x);
+                            f[2 * q + 1] = ptx::add_f32x2(f[2 * q + 1], bias.y);
+                        }
                     }
                 }
             };
@@ -368,7 +410,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 32 * kEpiWarps
                     for (int q = 0; q < 4; ++q)   // 8 columns: 16 bytes of the row
                         sts_u128(row + (((half * 4 + q) ^ (lane & 7)) << 4), pack_bf16x8(f + 4 * q));
                 }
-                store(&maps.z, col0, grp);
+                store(&maps.y2, col0, grp);
             }
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
@@ -400,12 +442,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 32 * kEpiWarps
                 for (int q = 0; q < 4; ++q)
                     sts_u128(row + (((half * 4 + q) ^ (lane & 7)) << 4), pack_bf16x8(f + 4 * q));
             }
-            if (P == Dx)
-                store(&maps.y, col0 % p.dk, grp * p.H + col0 / p.dk);
+            if (P == Bwd && w)
+                store(&maps.y2, col0, 0);
+            else if (P == Bwd)
+                store(&maps.y, col0 % pr.dk, grp * pr.H + col0 / pr.dk);
             else
                 store(&maps.y, col0, grp);
         }
         if (lane == 0) ptx::bulk_wait_group<0>();
+    } else if (P == Bwd && warp >= 2) {
+        // the bias gradient: its partial sums (see dz_kernel) added up by the two warps that have no
+        // other work, 32 columns a warp, while the products run
+        for (int c = (blockIdx.x * 2 + warp - 2) * 32 + lane; c < p.col_n; c += gridDim.x * 64) {
+            float s = 0.f;
+#pragma unroll 16
+            for (int r = 0; r < p.col_rows; ++r) s += p.col_part[(size_t)r * p.col_n + c];
+            p.dbias[c] = s;
+        }
     }
     __syncwarp();
     ptx::tc_fence_before();
@@ -678,24 +731,23 @@ __global__ void __launch_bounds__(256) dz_kernel(const LinBwdArgs a, int blocks)
         const long long m_end = min((long long)a.M, (long long)(blockIdx.y + 1) * per);
         // two rows at a time: their loads are in flight together
         for (long long m = (long long)blockIdx.y * per + warp; m < m_end; m += 16) {
-            const size_t at[2] = {((size_t)m * a.N + n) / 8, ((size_t)(m + 8) * a.N + n) / 8};
-            const bool two = m + 8 < m_end;
             uint4 d4[2], z4[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k)
-                if (k == 0 || two) {
-                    d4[k] = static_cast<const uint4 *>(a.dy)[at[k]];
-                    if (a.z) z4[k] = static_cast<const uint4 *>(a.z)[at[k]];
+                if (m + 8 * k < m_end) {
+                    const size_t at = ((size_t)(m + 8 * k) * a.N + n) / 8;
+                    d4[k] = static_cast<const uint4 *>(a.dy)[at];
+                    if (a.z) z4[k] = static_cast<const uint4 *>(a.z)[at];
                 }
 #pragma unroll
             for (int k = 0; k < 2; ++k)
-                if (k == 0 || two) {
+                if (m + 8 * k < m_end) {
                     float f[8], z[8];
                     unpack_bf16x8(d4[k], f);
                     if (a.z) {
                         unpack_bf16x8(z4[k], z);
                         times_slope(f, z, a.act);
-                        static_cast<uint4 *>(a.dz)[at[k]] =
+                        static_cast<uint4 *>(a.dz)[((size_t)(m + 8 * k) * a.N + n) / 8] =
                             make_uint4(ptx::pack_bf16x2(f[0], f[1]), ptx::pack_bf16x2(f[2], f[3]),
                                        ptx::pack_bf16x2(f[4], f[5]), ptx::pack_bf16x2(f[6], f[7]));
                     }
@@ -751,14 +803,13 @@ cudaError_t raise_smem(const void *kernel, int bytes, std::atomic<bool> (&set)[6
 }
 
 template <Policy P, int BN>
-cudaError_t launch_pair(const GemmMaps &m, const GemmParams &p, cudaStream_t stream)
+cudaError_t launch_pair(const GemmMaps &m, const GemmParams &p, int clusters, cudaStream_t stream)
 {
     using C = Cfg<P, BN>;
     static std::atomic<bool> set[64];
     const cudaError_t e = raise_smem((const void *)gemm_pair_kernel<P, BN>, C::SMEM, set);
     if (e != cudaSuccess) return e;
-    const int pairs = device_sm_count() / 2;
-    gemm_pair_kernel<P, BN><<<2 * (p.n_items < pairs ? p.n_items : pairs), 128 + 32 * kEpiWarps, C::SMEM, stream>>>(m, p);
+    gemm_pair_kernel<P, BN><<<2 * clusters, 128 + 32 * kEpiWarps, C::SMEM, stream>>>(m, p);
     return cudaGetLastError();
 }
 
@@ -835,14 +886,23 @@ cudaError_t launch_split(const CUtensorMap &w, const CUtensorMap &x, SplitParams
 // Row blocks: 128 rows of the only group, or 32 rows of one of several groups, so that a tile spans
 // groups and wastes at most 31 rows a group (576 rows a group: 18 blocks, 256-row tiles would take
 // 768 rows).
-bool set_rows(GemmParams &p, int G)
+int row_block(int G) { return G > 1 ? 32 : 128; }
+
+long long row_tiles(int G, int T) { return ceil_div((long long)ceil_div(T, row_block(G)) * G, BM / row_block(G)); }
+
+// Fills in the rows and the tiles; false if there are too many to count in an int.
+bool set_tiles(Prob &q, int G, int T, int N, int bn, int splits)
 {
-    p.rb = G > 1 ? 32 : 128;
-    p.rblocks = ceil_div(p.T, p.rb);
-    const long long all = (long long)p.rblocks * G;
-    p.n_rblocks = (int)all;
-    p.n_mtiles = ceil_div(all, BM / p.rb);
-    return all <= 0x7ffffff0LL;
+    q.T = T;
+    q.rb = row_block(G);
+    q.rblocks = ceil_div(T, q.rb);
+    q.n_rblocks = q.rblocks * G;
+    q.n_mtiles = (int)row_tiles(G, T);
+    q.N = N;
+    q.n_ntiles = ceil_div(N, bn);
+    const long long blocks = (long long)q.rblocks * G, items = (long long)q.n_mtiles * q.n_ntiles * splits;
+    q.n_items = (int)items;
+    return blocks <= 0x7ffffff0LL && items <= 0x7fffffffLL;
 }
 
 void set_split_rows(SplitParams &p, int G, int T, int tn)
@@ -851,13 +911,6 @@ void set_split_rows(SplitParams &p, int G, int T, int tn)
     p.rb = G > 1 && tn > 32 ? 32 : tn;
     p.rblocks = ceil_div(T, p.rb);
     p.n_rblocks = p.rblocks * G;
-}
-
-bool set_items(GemmParams &p, int splits)
-{
-    const long long items = (long long)p.n_mtiles * p.n_ntiles * splits;
-    p.n_items = (int)items;
-    return items <= 0x7fffffffLL;
 }
 
 constexpr CUtensorMapDataType kBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kU8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
@@ -878,34 +931,59 @@ PairPlan pair_plan(long long mtiles, int N, int ksteps)
     return w <= n ? PairPlan{true, w} : PairPlan{false, n};
 }
 
-struct DwPlan {
+// The backward runs both products in one launch, so that one's tiles fill the pairs that the other's
+// leave idle and there is one start and end (18432 rows, 768 x 768: 42 us apart, 33 together; 1111 rows,
+// 1000 x 520: 20 and 12; where both fill the GPU, 32768 rows, 1024 x 4096, the power limit makes it the
+// same).  dw has few tiles (K x N) and a long sum (the rows), which is split over items only where that
+// still pays for the partial sums' join (2.5 us, 5 bytes/ps).  Times in K steps: an item's fill and drain
+// costs 2 for dx, 4 for dw.
+struct BwdPlan {
     bool wide;
     int splits, steps_per_split;
+    double us, dw_us;   // of both, of dw alone
 };
 
-// dw has few tiles (K x N) and a long sum (the rows), so the rows are split over pairs of CTAs where
-// the partial sums' traffic costs less than the idle pairs: the plan takes the least of
-//   rounds of items per pair x (steps per item x time of a step + 2)  +  the join's launch and traffic
-// (2.5 us, 5 bytes/ps).
-DwPlan dw_plan(int G, int T, int K, int N)
+constexpr int kDxExtra = 2, kDwExtra = 4;
+
+BwdPlan bwd_plan(int G, int T, int K, int N)
 {
-    const long long steps = (long long)G * ceil_div(T, 64), mt = ceil_div(K, BM);
-    DwPlan best{true, 1, (int)steps};
-    double best_t = 1e30;
+    const long long steps = (long long)G * ceil_div(T, 64), mx = row_tiles(G, T), mw = ceil_div(K, BM);
+    BwdPlan best{};
+    best.us = 1e30;
     for (int wide = 1; wide >= 0; --wide) {
-        const long long tiles = mt * ceil_div(N, wide ? 256 : 128);
+        const int bn = wide ? 256 : 128;
+        const double dx = (double)mx * ceil_div(K, bn) * (ceil_div(N, 64) + kDxExtra);
         for (int s = 1; s <= 16 && s <= steps; ++s) {
-            const long long per = (steps + s - 1) / s;
+            const long long per = (steps + s - 1) / s, items = mw * ceil_div(N, bn) * s;
             if ((steps + per - 1) / per != s) continue;
-            double t = (double)((tiles * s + kPlanPairs - 1) / kPlanPairs) * (per * (wide ? kStepWide : kStepNarrow) + 2.0);
-            if (s > 1) t += 2.5 + (double)s * K * N * 8 / 5e6;
-            if (t < best_t) {
-                best_t = t;
-                best = DwPlan{wide == 1, s, (int)per};
-            }
+            const double most = (double)ceil_div(items, kPlanPairs) * (per + kDwExtra);
+            const double even = ((double)items * (per + kDwExtra) + dx) / kPlanPairs + 0.5 * (ceil_div(N, 64) + kDxExtra);
+            const double step = wide ? kStepWide : kStepNarrow, join = s > 1 ? 2.5 + (double)s * K * N * 8 / 5e6 : 0.0;
+            const double us = 6.0 + (most > even ? most : even) * step + join;
+            if (us < best.us) best = BwdPlan{wide == 1, s, (int)per, us, 6.0 + most * step + join};
         }
     }
     return best;
+}
+
+// How many of dx's items each cluster takes, so that all end at about the same step: the least level t
+// at which the room left beside dw's items holds them.
+void level_items(GemmParams &p, int clusters)
+{
+    const long long a = p.q[1].steps_per_split + kDwExtra, b = p.q[0].ksteps + kDxExtra;
+    const long long nd = p.q[1].n_items, nx = p.q[0].n_items, whole = nd / clusters, rest = nd % clusters;
+    auto room = [&](long long t, long long dw) { return t > dw * a ? (t - dw * a) / b : 0; };
+    long long lo = 0, hi = (whole + 1) * a + (nx / clusters + 1) * b;
+    while (lo < hi) {
+        const long long t = (lo + hi) / 2;
+        if (rest * room(t, whole + 1) + (clusters - rest) * room(t, whole) >= nx)
+            hi = t;
+        else
+            lo = t + 1;
+    }
+    p.a_clusters = (int)rest;
+    p.x_all = (int)room(lo, rest ? whole + 1 : whole);
+    p.x_early = (int)room(lo, whole) - p.x_all;
 }
 
 }  // namespace
@@ -913,10 +991,7 @@ DwPlan dw_plan(int G, int T, int K, int N)
 cudaError_t launch_linear(const LinArgs &a, cudaStream_t stream)
 {
     const int ksteps = ceil_div(a.K, a.q8 ? 128 : 64);
-    GemmParams p = {};
-    p.T = a.T;
-    if (!set_rows(p, a.G)) return cudaErrorInvalidValue;
-    const PairPlan plan = pair_plan(p.n_mtiles, a.N, ksteps);
+    const PairPlan plan = pair_plan(row_tiles(a.G, a.T), a.N, ksteps);
     const SplitPlan split = split_plan(a.G, a.T, a.N, ksteps);
     GemmMaps m;
     CUresult r;
@@ -945,9 +1020,13 @@ cudaError_t launch_linear(const LinArgs &a, cudaStream_t stream)
         if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
         return a.q8 ? launch_split<FwdQ8>(m.b, m.a, sp, split, stream) : launch_split<Fwd>(m.b, m.a, sp, split, stream);
     }
-    p.N = a.N;
-    p.dk = a.dk;
-    p.H = a.H;
+    const int bn = plan.wide ? 256 : 128;
+    GemmParams p = {};
+    Prob &q = p.q[0];
+    if (!set_tiles(q, a.G, a.T, a.N, bn, 1)) return cudaErrorInvalidValue;
+    q.dk = a.dk;
+    q.H = a.H;
+    q.ksteps = q.steps_per_split = ksteps;
     p.bias = a.bias;
     p.x_scale = a.x_scale;
     p.w_scale = a.w_scale;
@@ -955,116 +1034,115 @@ cudaError_t launch_linear(const LinArgs &a, cudaStream_t stream)
     p.has_r = a.residual != nullptr;
     p.act = a.act;
     p.status = a.status;
-    const int bn = plan.wide ? 256 : 128;
-    p.n_ntiles = ceil_div(a.N, bn);
-    if (!set_items(p, 1)) return cudaErrorInvalidValue;
-    p.ksteps = p.steps_per_split = ksteps;
     if (a.q8) {
         r = make_map_3d(&m.a, a.x, kU8, 1, a.K, a.M, 1, 128, 128);
         if (r == CUDA_SUCCESS) r = make_map_3d(&m.b, a.w, kU8, 1, a.K, a.N, 1, 128, bn / 2);
     } else {
-        r = make_map_3d(&m.a, a.x, kBf16, 2, a.dk, a.T, (long long)a.G * a.H, 64, p.rb);
+        r = make_map_3d(&m.a, a.x, kBf16, 2, a.dk, a.T, (long long)a.G * a.H, 64, q.rb);
         if (r == CUDA_SUCCESS) r = make_map_3d(&m.b, a.w, kBf16, 2, a.N, a.K, 1, 64, 64);
     }
     if (r == CUDA_SUCCESS) r = make_map_3d(&m.y, a.y, kBf16, 2, a.N, a.T, a.G, 64, 32);
-    if (r == CUDA_SUCCESS && a.z) r = make_map_3d(&m.z, a.z, kBf16, 2, a.N, a.T, a.G, 64, 32);
-    if (r == CUDA_SUCCESS && a.residual) r = make_map_3d(&m.r, a.residual, kBf16, 2, a.N, a.T, a.G, 64, 32);
+    if (r == CUDA_SUCCESS && a.z) r = make_map_3d(&m.y2, a.z, kBf16, 2, a.N, a.T, a.G, 64, 32);
+    if (r == CUDA_SUCCESS && a.residual) r = make_map_3d(&m.a2, a.residual, kBf16, 2, a.N, a.T, a.G, 64, 32);
     if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
+    const int pairs = device_sm_count() / 2, clusters = q.n_items < pairs ? q.n_items : pairs;
     if (a.q8)
-        return plan.wide ? launch_pair<FwdQ8, 256>(m, p, stream) : launch_pair<FwdQ8, 128>(m, p, stream);
-    return plan.wide ? launch_pair<Fwd, 256>(m, p, stream) : launch_pair<Fwd, 128>(m, p, stream);
+        return plan.wide ? launch_pair<FwdQ8, 256>(m, p, clusters, stream) : launch_pair<FwdQ8, 128>(m, p, clusters, stream);
+    return plan.wide ? launch_pair<Fwd, 256>(m, p, clusters, stream) : launch_pair<Fwd, 128>(m, p, clusters, stream);
 }
 
-// Blocks of rows of the column sums: enough for four blocks of threads an SM, at least 16 rows each.
+// Blocks of rows of the column sums: four blocks of threads an SM, at least 16 rows each, and no more
+// than two warps of each CTA can add up behind the products.
 int lin_bwd_row_blocks(int M, int N)
 {
     const int strips = ceil_div(N, 256);
-    const int want = ceil_div(8 * kPlanPairs, strips), most = ceil_div(M, 16);
-    const int b = want < most ? want : most;
+    int b = ceil_div(8 * kPlanPairs, strips);
+    if (b > 256) b = 256;
+    if (b > ceil_div(M, 16)) b = ceil_div(M, 16);
     return b > 1 ? b : 1;
 }
 
-int lin_dw_splits(int G, int T, int K, int N) { return T > 0 ? dw_plan(G, T, K, N).splits : 1; }
+int lin_dw_splits(int G, int T, int K, int N) { return T > 0 ? bwd_plan(G, T, K, N).splits : 1; }
 
 cudaError_t launch_linear_bwd(const LinBwdArgs &a, cudaStream_t stream)
 {
     cudaError_t e = cudaSuccess;
+    const int blocks = lin_bwd_row_blocks(a.M, a.N);
     if (a.dbias || (a.z && (a.dx || a.dw))) {
-        const int blocks = lin_bwd_row_blocks(a.M, a.N);
         dz_kernel<<<dim3(ceil_div(a.N, 256), blocks), 256, 0, stream>>>(a, blocks);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        if (a.dbias) {
-            if ((e = launch_sum_rows(a.col_part, a.dbias, blocks, a.N, stream)) != cudaSuccess) return e;
-        }
     }
     const void *dz = a.z ? a.dz : a.dy;
-    GemmMaps m;
-    CUresult r;
-    if (a.dx) {
-        const int ksteps = ceil_div(a.N, 64);
-        GemmParams p = {};
-        p.T = a.T;
-        if (!set_rows(p, a.G)) return cudaErrorInvalidValue;
-        const PairPlan plan = pair_plan(p.n_mtiles, a.K, ksteps);
+    const BwdPlan plan = bwd_plan(a.G, a.T, a.K, a.N);
+    const int ksteps = ceil_div(a.N, 64);
+    CUresult r = CUDA_SUCCESS;
+    bool dx_left = a.dx != nullptr;
+    if (a.dx) {   // few rows: dx by the split kernel, beside dw alone
         const SplitPlan split = split_plan(a.G, a.T, a.K, ksteps);
-        if (split.us < plan.us) {
+        if (split.us + plan.dw_us < plan.us) {
             SplitParams sp = {};
             set_split_rows(sp, a.G, a.T, split.tn);
-                sp.N = a.K;
+            sp.N = a.K;
             sp.dk = a.dk;
             sp.H = a.H;
             sp.ksteps = ksteps;
             sp.y = static_cast<__nv_bfloat16 *>(a.dx);
             sp.status = a.status;
-            r = make_map_3d(&m.a, dz, kBf16, 2, a.N, a.T, a.G, 64, sp.rb);
-            if (r == CUDA_SUCCESS) r = make_map_3d(&m.b, a.w, kBf16, 2, a.N, a.K, 1, 64, 128);
+            CUtensorMap mx, mw;
+            r = make_map_3d(&mx, dz, kBf16, 2, a.N, a.T, a.G, 64, sp.rb);
+            if (r == CUDA_SUCCESS) r = make_map_3d(&mw, a.w, kBf16, 2, a.N, a.K, 1, 64, 128);
             if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
-            e = launch_split<Dx>(m.b, m.a, sp, split, stream);
-        } else {
-            p.N = a.K;
-            p.dk = a.dk;
-            p.H = a.H;
-            p.status = a.status;
-            const int bn = plan.wide ? 256 : 128;
-            p.n_ntiles = ceil_div(a.K, bn);
-            if (!set_items(p, 1)) return cudaErrorInvalidValue;
-            p.ksteps = p.steps_per_split = ksteps;
-            r = make_map_3d(&m.a, dz, kBf16, 2, a.N, a.T, a.G, 64, p.rb);
-            if (r == CUDA_SUCCESS) r = make_map_3d(&m.b, a.w, kBf16, 2, a.N, a.K, 1, 64, bn / 2);
-            if (r == CUDA_SUCCESS) r = make_map_3d(&m.y, a.dx, kBf16, 2, a.dk, a.T, (long long)a.G * a.H, 64, 32);
-            if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
-            e = plan.wide ? launch_pair<Dx, 256>(m, p, stream) : launch_pair<Dx, 128>(m, p, stream);
+            if ((e = launch_split<Dx>(mw, mx, sp, split, stream)) != cudaSuccess) return e;
+            dx_left = false;
         }
-        if (e != cudaSuccess) return e;
     }
-    if (a.dw) {
-        const DwPlan plan = dw_plan(a.G, a.T, a.K, a.N);
-        GemmParams p = {};
-        p.T = a.K;
-        if (!set_rows(p, 1)) return cudaErrorInvalidValue;
-        p.N = a.N;
-        p.dk = a.dk;
-        p.H = a.H;
-        p.status = a.status;
-        p.n_ntiles = ceil_div(a.N, plan.wide ? 256 : 128);
-        p.tblocks = ceil_div(a.T, 64);
-        p.T_k = a.T;
-        p.ksteps = a.G * p.tblocks;
-        p.steps_per_split = plan.steps_per_split;
-        if (!set_items(p, plan.splits)) return cudaErrorInvalidValue;
+    if (!dx_left && !a.dw) return a.dbias ? launch_sum_rows(a.col_part, a.dbias, blocks, a.N, stream) : e;
+
+    const int bn = plan.wide ? 256 : 128;
+    GemmMaps m;
+    GemmParams p = {};
+    p.status = a.status;
+    if (dx_left) {
+        Prob &q = p.q[0];
+        if (!set_tiles(q, a.G, a.T, a.K, bn, 1)) return cudaErrorInvalidValue;
+        q.dk = a.dk;
+        q.H = a.H;
+        q.ksteps = q.steps_per_split = ksteps;
+        r = make_map_3d(&m.a, dz, kBf16, 2, a.N, a.T, a.G, 64, q.rb);
+        if (r == CUDA_SUCCESS) r = make_map_3d(&m.b, a.w, kBf16, 2, a.N, a.K, 1, 64, bn / 2);
+        if (r == CUDA_SUCCESS) r = make_map_3d(&m.y, a.dx, kBf16, 2, a.dk, a.T, (long long)a.G * a.H, 64, 32);
+    }
+    if (a.dw && r == CUDA_SUCCESS) {
+        Prob &q = p.q[1];
+        if (!set_tiles(q, 1, a.K, a.N, bn, plan.splits)) return cudaErrorInvalidValue;
+        q.dk = a.dk;
+        q.H = a.H;
+        q.tblocks = ceil_div(a.T, 64);
+        q.T_k = a.T;
+        q.ksteps = a.G * q.tblocks;
+        q.steps_per_split = plan.steps_per_split;
         p.part = plan.splits > 1;
-        r = make_map_3d(&m.a, a.x, kBf16, 2, a.dk, a.T, (long long)a.G * a.H, 64, 64);
-        if (r == CUDA_SUCCESS) r = make_map_3d(&m.b, dz, kBf16, 2, a.N, a.T, a.G, 64, 64);
+        r = make_map_3d(&m.a2, a.x, kBf16, 2, a.dk, a.T, (long long)a.G * a.H, 64, 64);
+        if (r == CUDA_SUCCESS) r = make_map_3d(&m.b2, dz, kBf16, 2, a.N, a.T, a.G, 64, 64);
         if (r == CUDA_SUCCESS)
-            r = p.part ? make_map_3d(&m.y, a.dw_part, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, a.N, a.K, plan.splits, 32, 32)
-                       : make_map_3d(&m.y, a.dw, kBf16, 2, a.N, a.K, 1, 64, 32);
-        if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
-        e = plan.wide ? launch_pair<Dw, 256>(m, p, stream) : launch_pair<Dw, 128>(m, p, stream);
-        if (e == cudaSuccess && plan.splits > 1) {
-            const long long elems = (long long)a.K * a.N;
-            dw_join_kernel<<<ceil_div(elems, 1024), 256, 0, stream>>>(a.dw_part, a.dw, plan.splits, elems);
-            e = cudaGetLastError();
-        }
+            r = p.part ? make_map_3d(&m.y2, a.dw_part, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, a.N, a.K, plan.splits, 32, 32)
+                       : make_map_3d(&m.y2, a.dw, kBf16, 2, a.N, a.K, 1, 64, 32);
+    }
+    if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
+    if (a.dbias) {
+        p.col_part = a.col_part;
+        p.dbias = a.dbias;
+        p.col_rows = blocks;
+        p.col_n = a.N;
+    }
+    const long long items = (long long)p.q[0].n_items + p.q[1].n_items;
+    const int pairs = device_sm_count() / 2, clusters = items < pairs ? (int)items : pairs;
+    level_items(p, clusters);
+    e = plan.wide ? launch_pair<Bwd, 256>(m, p, clusters, stream) : launch_pair<Bwd, 128>(m, p, clusters, stream);
+    if (e == cudaSuccess && p.part) {
+        const long long elems = (long long)a.K * a.N;
+        dw_join_kernel<<<ceil_div(elems, 1024), 256, 0, stream>>>(a.dw_part, a.dw, plan.splits, elems);
+        e = cudaGetLastError();
     }
     return e;
 }
