@@ -107,7 +107,7 @@ __device__ __forceinline__ uint2 pack_bf16x4(const uint64_t (&f)[2])
 }
 
 template <Policy P, int BN>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 32 * kEpiWarps, 1)
+__global__ void __launch_bounds__(128 + 32 * kEpiWarps, 1)
     gemm_pair_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmParams p)
 {
     using C = Cfg<P, BN>;
@@ -175,6 +175,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 32 * kEpiWarps
     __syncthreads();
     ptx::cluster_sync();   // both CTAs' barriers exist before either signals the other
     ptx::tc_fence_after();
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
     const uint32_t tmem = tmem_sh;
 
     if (warp == 0) {
@@ -591,6 +593,8 @@ __global__ void __launch_bounds__(256) gemm_split_kernel(const __grid_constant__
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = tmem_sh;
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
 
     if (warp == 0) {
         if (ptx::elect_one()) {
@@ -726,6 +730,8 @@ __global__ void __launch_bounds__(256) dz_kernel(const LinBwdArgs a, int blocks)
     const int n = blockIdx.x * 256 + lane * 8;
     __shared__ float part[8][256];
     float s[8] = {};
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
     if (n < a.N) {
         const int per = (a.M + blocks - 1) / blocks;
         const long long m_end = min((long long)a.M, (long long)(blockIdx.y + 1) * per);
@@ -772,6 +778,8 @@ __global__ void __launch_bounds__(256) dz_kernel(const LinBwdArgs a, int blocks)
 __global__ void __launch_bounds__(256) dw_join_kernel(const float *part, void *dw, int splits, long long elems)
 {
     const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 4;
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
     if (i >= elems) return;
     float4 s = *reinterpret_cast<const float4 *>(part + i);
     for (int k = 1; k < splits; ++k) {
@@ -809,8 +817,7 @@ cudaError_t launch_pair(const GemmMaps &m, const GemmParams &p, int clusters, cu
     static std::atomic<bool> set[64];
     const cudaError_t e = raise_smem((const void *)gemm_pair_kernel<P, BN>, C::SMEM, set);
     if (e != cudaSuccess) return e;
-    gemm_pair_kernel<P, BN><<<2 * clusters, 128 + 32 * kEpiWarps, C::SMEM, stream>>>(m, p);
-    return cudaGetLastError();
+    return launch_overlapped(gemm_pair_kernel<P, BN>, 2 * clusters, 128 + 32 * kEpiWarps, C::SMEM, 2, stream, m, p);
 }
 
 template <Policy P, int TN>
@@ -821,18 +828,7 @@ cudaError_t launch_split_tn(const CUtensorMap &w, const CUtensorMap &x, const Sp
     static std::atomic<bool> set[64];
     cudaError_t e = raise_smem((const void *)gemm_split_kernel<P, TN>, C::SMEM, set);
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = splits;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(tiles * splits);
-    cfg.blockDim = dim3(256);
-    cfg.dynamicSmemBytes = C::SMEM;
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, gemm_split_kernel<P, TN>, w, x, p);
+    return launch_overlapped(gemm_split_kernel<P, TN>, tiles * splits, 256, C::SMEM, splits, stream, w, x, p);
 }
 
 // How few-row products are laid out: rows a tile, CTAs a tile.
@@ -1069,8 +1065,8 @@ cudaError_t launch_linear_bwd(const LinBwdArgs &a, cudaStream_t stream)
     cudaError_t e = cudaSuccess;
     const int blocks = lin_bwd_row_blocks(a.M, a.N);
     if (a.dbias || (a.z && (a.dx || a.dw))) {
-        dz_kernel<<<dim3(ceil_div(a.N, 256), blocks), 256, 0, stream>>>(a, blocks);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        e = launch_overlapped(dz_kernel, dim3(ceil_div(a.N, 256), blocks), 256, 0, 1, stream, a, blocks);
+        if (e != cudaSuccess) return e;
     }
     const void *dz = a.z ? a.dz : a.dy;
     const BwdPlan plan = bwd_plan(a.G, a.T, a.K, a.N);
@@ -1141,8 +1137,7 @@ cudaError_t launch_linear_bwd(const LinBwdArgs &a, cudaStream_t stream)
     e = plan.wide ? launch_pair<Bwd, 256>(m, p, clusters, stream) : launch_pair<Bwd, 128>(m, p, clusters, stream);
     if (e == cudaSuccess && p.part) {
         const long long elems = (long long)a.K * a.N;
-        dw_join_kernel<<<ceil_div(elems, 1024), 256, 0, stream>>>(a.dw_part, a.dw, plan.splits, elems);
-        e = cudaGetLastError();
+        e = launch_overlapped(dw_join_kernel, ceil_div(elems, 1024), 256, 0, 1, stream, a.dw_part, a.dw, plan.splits, elems);
     }
     return e;
 }

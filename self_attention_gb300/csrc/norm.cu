@@ -98,6 +98,8 @@ template <int TPR, int CH, bool Q8>
 __global__ void __launch_bounds__(TPR *rows_per_block(TPR)) rms_norm_kernel(const NormArgs a)
 {
     const long long m = (long long)blockIdx.x * rows_per_block(TPR) + threadIdx.x / TPR;
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
     if (m >= a.M) return;   // whole warps (TPR = 32), or never
     const int t = threadIdx.x % TPR, nch = a.D / 8;
     const size_t row = (size_t)m * nch;   // in chunks
@@ -163,6 +165,8 @@ template <bool Q8>
 __global__ void __launch_bounds__(1024) rms_norm_long_kernel(const NormArgs a)
 {
     const size_t row = (size_t)blockIdx.x * (a.D / 8);
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
     auto load_h = [&](int i, float (&h)[8]) {
         unpack8(static_cast<const uint4 *>(a.x)[row + i], h);
         if (a.residual) {
@@ -219,6 +223,8 @@ __global__ void __launch_bounds__(256, bwd_blocks_per_sm(CH)) rms_norm_bwd_kerne
     constexpr int RPB = TPR == 32 ? 8 : 1;   // row-holders a block
     const int t = threadIdx.x % TPR, holder = threadIdx.x / TPR, nch = a.D / 8;
     float acc[CH][8] = {};
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
     for (long long m = (long long)blockIdx.x * RPB + holder; m < a.M; m += (long long)blocks * RPB) {
         const size_t row = (size_t)m * nch;
         const uint4 *dy = static_cast<const uint4 *>(a.dy) + row, *h = static_cast<const uint4 *>(a.h) + row,
@@ -304,6 +310,8 @@ __global__ void __launch_bounds__(256, bwd_blocks_per_sm(CH)) rms_norm_bwd_kerne
 __global__ void __launch_bounds__(1024) rms_norm_bwd_long_kernel(const NormBwdArgs a, int blocks)
 {
     float *part = a.part + (size_t)blockIdx.x * a.D;
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
     for (long long m = blockIdx.x; m < a.M; m += blocks) {
         const size_t row = (size_t)m * (a.D / 8);
         const float r = a.rstd[m];
@@ -343,6 +351,8 @@ __global__ void __launch_bounds__(1024) sum_rows_kernel(const float *part, float
     __shared__ float sums[32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float s = 0.f;
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
     if (c < cols)
 #pragma unroll 4
         for (int r = warp; r < rows; r += 32) s += part[(size_t)r * cols + c];
@@ -356,41 +366,42 @@ __global__ void __launch_bounds__(1024) sum_rows_kernel(const float *part, float
 }
 
 template <int TPR, int CH>
-void launch_norm(const NormArgs &a, cudaStream_t stream)
+cudaError_t launch_norm(const NormArgs &a, cudaStream_t stream)
 {
     constexpr int R = rows_per_block(TPR);
     const unsigned grid = (unsigned)(((long long)a.M + R - 1) / R);
-    if (a.q8)
-        rms_norm_kernel<TPR, CH, true><<<grid, TPR * R, 0, stream>>>(a);
-    else
-        rms_norm_kernel<TPR, CH, false><<<grid, TPR * R, 0, stream>>>(a);
+    return a.q8 ? launch_overlapped(rms_norm_kernel<TPR, CH, true>, grid, TPR * R, 0, 1, stream, a)
+                : launch_overlapped(rms_norm_kernel<TPR, CH, false>, grid, TPR * R, 0, 1, stream, a);
+}
+
+template <int TPR, int CH>
+cudaError_t launch_norm_bwd(const NormBwdArgs &a, int blocks, cudaStream_t stream)
+{
+    return launch_overlapped(rms_norm_bwd_kernel<TPR, CH>, blocks, 256, 0, 1, stream, a, blocks);
 }
 
 }  // namespace
 
 cudaError_t launch_sum_rows(const float *part, float *out, int rows, int cols, cudaStream_t stream)
 {
-    sum_rows_kernel<<<(cols + 31) / 32, 1024, 0, stream>>>(part, out, rows, cols);
-    return cudaGetLastError();
+    return launch_overlapped(sum_rows_kernel, (cols + 31) / 32, 1024, 0, 1, stream, part, out, rows, cols);
 }
 
 cudaError_t launch_rms_norm(const NormArgs &a, cudaStream_t stream)
 {
     const int D = a.D;
     // a few rows (no more than two blocks an SM): 256 threads each hold one chunk of a row, which is read
-    // and reduced sooner than by a warp (7 x 2048 to 8 bits: 2.9 against 4.0 us)
-    if (D > 256 && D <= 2048 && a.M <= 2 * kPlanSms) launch_norm<256, 1>(a, stream);
-    else if (D <= 256) launch_norm<32, 1>(a, stream);
-    else if (D <= 512) launch_norm<32, 2>(a, stream);
-    else if (D <= 1024) launch_norm<32, 4>(a, stream);
-    else if (D <= 2048) launch_norm<32, 8>(a, stream);
-    else if (D <= 4096) launch_norm<256, 2>(a, stream);
-    else if (D <= 8192) launch_norm<256, 4>(a, stream);
-    else if (D <= 16384) launch_norm<256, 8>(a, stream);
-    else if (D <= 32768) launch_norm<1024, 4>(a, stream);
-    else if (a.q8) rms_norm_long_kernel<true><<<a.M, 1024, 0, stream>>>(a);
-    else rms_norm_long_kernel<false><<<a.M, 1024, 0, stream>>>(a);
-    return cudaGetLastError();
+    // and reduced sooner than by a warp (7 x 2048 to 8 bits: 4.8 against 6.1 us a call)
+    if (D > 256 && D <= 2048 && a.M <= 2 * kPlanSms) return launch_norm<256, 1>(a, stream);
+    if (D <= 256) return launch_norm<32, 1>(a, stream);
+    if (D <= 512) return launch_norm<32, 2>(a, stream);
+    if (D <= 1024) return launch_norm<32, 4>(a, stream);
+    if (D <= 2048) return launch_norm<32, 8>(a, stream);
+    if (D <= 4096) return launch_norm<256, 2>(a, stream);
+    if (D <= 8192) return launch_norm<256, 4>(a, stream);
+    if (D <= 16384) return launch_norm<256, 8>(a, stream);
+    if (D <= 32768) return launch_norm<1024, 4>(a, stream);
+    return launch_overlapped(a.q8 ? rms_norm_long_kernel<true> : rms_norm_long_kernel<false>, a.M, 1024, 0, 1, stream, a);
 }
 
 // As many blocks as fit the SMs at once (see bwd_blocks_per_sm); no more than there are rows for.
@@ -406,16 +417,15 @@ int norm_bwd_blocks(int M, int D)
 cudaError_t launch_rms_norm_bwd(const NormBwdArgs &a, cudaStream_t stream)
 {
     const int blocks = norm_bwd_blocks(a.M, a.D), D = a.D;
-    if (D <= 256) rms_norm_bwd_kernel<32, 1><<<blocks, 256, 0, stream>>>(a, blocks);
-    else if (D <= 512) rms_norm_bwd_kernel<32, 2><<<blocks, 256, 0, stream>>>(a, blocks);
-    else if (D <= 768) rms_norm_bwd_kernel<32, 3><<<blocks, 256, 0, stream>>>(a, blocks);
-    else if (D <= 1024) rms_norm_bwd_kernel<32, 4><<<blocks, 256, 0, stream>>>(a, blocks);
-    else if (D <= 2048) rms_norm_bwd_kernel<32, 8><<<blocks, 256, 0, stream>>>(a, blocks);
-    else if (D <= 4096) rms_norm_bwd_kernel<256, 2><<<blocks, 256, 0, stream>>>(a, blocks);
-    else if (D <= 8192) rms_norm_bwd_kernel<256, 4><<<blocks, 256, 0, stream>>>(a, blocks);
-    else if (D <= 16384) rms_norm_bwd_kernel<256, 8><<<blocks, 256, 0, stream>>>(a, blocks);
-    else rms_norm_bwd_long_kernel<<<blocks, 1024, 0, stream>>>(a, blocks);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = D <= 256     ? launch_norm_bwd<32, 1>(a, blocks, stream)
+                          : D <= 512   ? launch_norm_bwd<32, 2>(a, blocks, stream)
+                          : D <= 768   ? launch_norm_bwd<32, 3>(a, blocks, stream)
+                          : D <= 1024  ? launch_norm_bwd<32, 4>(a, blocks, stream)
+                          : D <= 2048  ? launch_norm_bwd<32, 8>(a, blocks, stream)
+                          : D <= 4096  ? launch_norm_bwd<256, 2>(a, blocks, stream)
+                          : D <= 8192  ? launch_norm_bwd<256, 4>(a, blocks, stream)
+                          : D <= 16384 ? launch_norm_bwd<256, 8>(a, blocks, stream)
+                                       : launch_overlapped(rms_norm_bwd_long_kernel, blocks, 1024, 0, 1, stream, a, blocks);
     return e == cudaSuccess ? launch_sum_rows(a.part, a.dweight, blocks, D, stream) : e;
 }
 

@@ -293,6 +293,15 @@ __device__ __forceinline__ void tma_load_3d_pair(void *smem_dst, const CUtensorM
 }
 
 // ------------------------------------------------------------------------------------------
+// Programmatic dependent launch: a kernel may start while the one before it on the stream ends.
+// grid_dep_wait() returns when that one has completed and its writes are visible; a thread calls it
+// before its first access to global memory (every thread does, so that a grid's end always implies
+// the end of the grids before it).  grid_dep_launch() lets the next kernel start.
+// ------------------------------------------------------------------------------------------
+__device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// ------------------------------------------------------------------------------------------
 // Clusters
 // ------------------------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t cluster_rank()
