@@ -503,7 +503,13 @@ def attention(q, k, v, scale: float | None = None):
 
 
 # ------------------------------------------------- the rest of the block: linear layers and norms
+# These calls take as long on the host as the smallest kernels do on the GPU, so they go to the library
+# directly rather than through the mirrors above.
 _BF16, _F32, _E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _want(name, t, dtype, shape, dev):
@@ -532,7 +538,7 @@ def _act(activation) -> int:
 def _on(dev, stream, tensors, fn):
     """fn(raw stream) with `dev` current.  On another stream than the device's current one the
     operands are recorded on it, and what fn allocates belongs to it."""
-    if stream is None and torch.cuda.current_device() == dev.index:
+    if stream is None and torch._C._cuda_getDevice() == dev.index:
         return fn(torch._C._cuda_getCurrentRawStream(dev.index))
     with torch.cuda.device(dev):
         st = _device_stream(dev, stream)
@@ -563,7 +569,8 @@ def linear_forward(x, w, bias=None, residual=None, activation: str = "none", kee
     def call(st):
         y = torch.empty(shape, dtype=_BF16, device=dev)
         z = torch.empty(shape, dtype=_BF16, device=dev) if keep_z else None
-        attn_linear(x, w, bias, residual, y, z, M, K, N, act, st)
+        _raise(load_library().attn_linear(x.data_ptr(), w.data_ptr(), _at(bias), _at(residual), y.data_ptr(), _at(z),
+                                          M, K, N, act, st), "attn_linear")
         return (y, z) if keep_z else y
 
     return _on(dev, stream, (x, w, bias, residual), call)
@@ -590,9 +597,11 @@ def linear_backward(x, w, dy, z=None, activation: str = "none", bias: bool = Tru
         dx = torch.empty_like(x) if need_dx else None
         dw = torch.empty_like(w) if need_dw else None
         db = torch.empty(N, dtype=_F32, device=dev) if bias else None
-        nbytes = attn_linear_bwd_workspace_size(M, K, N, act)
+        lib = load_library()
+        nbytes = lib.attn_linear_bwd_workspace_size(M, K, N, act)
         ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
-        attn_linear_bwd(x, w, dy, z, dx, dw, db, ws, nbytes, M, K, N, act, st)
+        _raise(lib.attn_linear_bwd(x.data_ptr(), w.data_ptr(), dy.data_ptr(), _at(z), _at(dx), _at(dw), _at(db),
+                                   ws.data_ptr(), nbytes, M, K, N, act, st), "attn_linear_bwd")
         return dx, dw, db
 
     return _on(dev, stream, (x, w, dy, z), call)
@@ -611,7 +620,8 @@ def out_proj_forward(o, w, bias=None, residual=None, stream=None):
 
     def call(st):
         y = torch.empty((B, N, n_out), dtype=_BF16, device=dev)
-        attn_out_proj(o, w, bias, residual, y, B, H, N, D, n_out, st)
+        _raise(load_library().attn_out_proj(o.data_ptr(), w.data_ptr(), _at(bias), _at(residual), y.data_ptr(),
+                                            B, H, N, D, n_out, st), "attn_out_proj")
         return y
 
     return _on(dev, stream, (o, w, bias, residual), call)
@@ -628,9 +638,11 @@ def out_proj_backward(o, w, dy, bias: bool = True, need_do: bool = True, need_dw
         do = torch.empty_like(o) if need_do else None
         dw = torch.empty_like(w) if need_dw else None
         db = torch.empty(n_out, dtype=_F32, device=dev) if bias else None
-        nbytes = attn_out_proj_bwd_workspace_size(B, H, N, D, n_out)
+        lib = load_library()
+        nbytes = lib.attn_out_proj_bwd_workspace_size(B, H, N, D, n_out)
         ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
-        attn_out_proj_bwd(o, w, dy, do, dw, db, ws, nbytes, B, H, N, D, n_out, st)
+        _raise(lib.attn_out_proj_bwd(o.data_ptr(), w.data_ptr(), dy.data_ptr(), _at(do), _at(dw), _at(db),
+                                     ws.data_ptr(), nbytes, B, H, N, D, n_out, st), "attn_out_proj_bwd")
         return do, dw, db
 
     return _on(dev, stream, (o, w, dy), call)
@@ -648,7 +660,8 @@ def rms_norm_forward(x, weight, residual=None, eps: float = 1e-6, stream=None):
         y = torch.empty_like(x)
         h = torch.empty_like(x) if residual is not None else None
         rstd = torch.empty(x.shape[:-1], dtype=_F32, device=dev)
-        attn_rms_norm(x, residual, weight, y, h, rstd, M, D, eps, st)
+        _raise(load_library().attn_rms_norm(x.data_ptr(), _at(residual), weight.data_ptr(), y.data_ptr(), _at(h),
+                                            rstd.data_ptr(), M, D, eps, st), "attn_rms_norm")
         return y, (x if h is None else h), rstd
 
     return _on(dev, stream, (x, weight, residual), call)
@@ -667,9 +680,12 @@ def rms_norm_backward(dy, h, weight, rstd, dh=None, stream=None):
     def call(st):
         dx = torch.empty_like(h)
         dweight = torch.empty(D, dtype=_F32, device=dev)
-        nbytes = attn_rms_norm_bwd_workspace_size(M, D)
+        lib = load_library()
+        nbytes = lib.attn_rms_norm_bwd_workspace_size(M, D)
         ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
-        attn_rms_norm_bwd(dy, h, weight, rstd, dh, dx, dweight, ws, nbytes, M, D, st)
+        _raise(lib.attn_rms_norm_bwd(dy.data_ptr(), h.data_ptr(), weight.data_ptr(), rstd.data_ptr(), _at(dh),
+                                     dx.data_ptr(), dweight.data_ptr(), ws.data_ptr(), nbytes, M, D, st),
+               "attn_rms_norm_bwd")
         return dx, dweight
 
     return _on(dev, stream, (dy, h, weight, rstd, dh), call)
@@ -686,7 +702,8 @@ def rms_norm_q8(x, weight, residual=None, eps: float = 1e-6, stream=None):
         yq = torch.empty(x.shape, dtype=_E4M3, device=dev)
         scale = torch.empty(x.shape[:-1], dtype=_F32, device=dev)
         h = torch.empty_like(x) if residual is not None else None
-        attn_rms_norm_q8(x, residual, weight, yq, scale, h, M, D, eps, st)
+        _raise(load_library().attn_rms_norm_q8(x.data_ptr(), _at(residual), weight.data_ptr(), yq.data_ptr(),
+                                               scale.data_ptr(), _at(h), M, D, eps, st), "attn_rms_norm_q8")
         return yq, scale, (x if h is None else h)
 
     return _on(dev, stream, (x, weight, residual), call)
@@ -700,7 +717,8 @@ def quantize_q8(x, stream=None):
     def call(st):
         xq = torch.empty(x.shape, dtype=_E4M3, device=dev)
         scale = torch.empty(x.shape[:-1], dtype=_F32, device=dev)
-        attn_quantize_q8(x, xq, scale, M, D, st)
+        _raise(load_library().attn_quantize_q8(x.data_ptr(), xq.data_ptr(), scale.data_ptr(), M, D, st),
+               "attn_quantize_q8")
         return xq, scale
 
     return _on(dev, stream, (x,), call)
@@ -723,7 +741,9 @@ def linear_q8(xq, x_scale, wq, w_scale, bias=None, residual=None, activation: st
 
     def call(st):
         y = torch.empty(shape, dtype=_BF16, device=dev)
-        attn_linear_q8(xq, x_scale, wq, w_scale, bias, residual, y, M, K, N, act, st)
+        _raise(load_library().attn_linear_q8(xq.data_ptr(), x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(),
+                                             _at(bias), _at(residual), y.data_ptr(), M, K, N, act, st),
+               "attn_linear_q8")
         return y
 
     return _on(dev, stream, (xq, x_scale, wq, w_scale, bias, residual), call)
