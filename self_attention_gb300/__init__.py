@@ -19,6 +19,7 @@ import math
 import os
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from .build import LIB_PATH
 
@@ -760,6 +761,7 @@ class _Linear(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, w, z = ctx.saved_tensors
         need_x, need_w, need_b, need_r = ctx.needs_input_grad[:4]
@@ -782,6 +784,7 @@ class _OutProj(torch.autograd.Function):
         return out_proj_forward(o, w, bias, residual)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         o, w = ctx.saved_tensors
         need_o, need_w, need_b, need_r = ctx.needs_input_grad
@@ -806,6 +809,7 @@ class _RmsNorm(torch.autograd.Function):
         return (y, h) if residual is not None else y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dh=None):
         h, weight, rstd = ctx.saved_tensors
         need_x, need_w, need_r = ctx.needs_input_grad[:3]

@@ -29,16 +29,13 @@ struct Guard {
 };
 
 // Waits for the phase of `bar` with parity `parity` to complete.  Returns true on success,
-// false if the wait timed out or the CTA had already aborted.  CLUSTER: arrivals come from
-// another CTA of the cluster too.
-template <bool CLUSTER = false>
+// false if the wait timed out or the CTA had already aborted.
 __device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t parity, const Guard &g)
 {
-    auto done = [&] { return CLUSTER ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity); };
-    if (done()) return true;
+    if (ptx::mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
     while (true) {
-        if (done()) return true;
+        if (ptx::mbar_try_wait(bar, parity)) return true;
         if (*(volatile int *)g.abort_smem) return false;
         if (globaltimer_ns() - t0 > g.limit_ns) {
             *(volatile int *)g.abort_smem = 1;

@@ -22,7 +22,7 @@
 // is ready.  Sixteen warps, since a warp's chain of loads, MUFU operations and stores is long: with
 // eight, GELU with z kept took longer than the products of 1024 of K.
 #include "act.cuh"
-#include "common.cuh"
+#include "cluster.cuh"
 #include "kernels.h"
 
 #include <atomic>
@@ -281,10 +281,10 @@ __global__ void __launch_bounds__(128 + 32 * kEpiWarps, 1)
                 const uint32_t idesc = C::FP8 ? ptx::idesc_f16_f32(BM, BN, false, false)   // format 0: e4m3
                                               : ptx::idesc_bf16_f32(BM, BN, a_mn, b_mn);
                 const int ab = li & 1;
-                wait_bounded<true>(&bar_acc_empty[ab], ((li >> 1) & 1) ^ 1, g);   // epilogues of item li-2 done
+                wait_bounded_cluster(&bar_acc_empty[ab], ((li >> 1) & 1) ^ 1, g);   // epilogues of item li-2 done
                 ptx::tc_fence_after();
                 for (int q = 0; q < nk; ++q) {
-                    wait_bounded<true>(&bar_full[s], ph, g);
+                    wait_bounded_cluster(&bar_full[s], ph, g);
                     ptx::tc_fence_after();
                     const uint32_t sa = base + s * C::STAGE, sb = sa + C::A_BYTES;
 #pragma unroll
@@ -884,7 +884,11 @@ cudaError_t launch_split(const CUtensorMap &w, const CUtensorMap &x, SplitParams
 // 768 rows).
 int row_block(int G) { return G > 1 ? 32 : 128; }
 
-long long row_tiles(int G, int T) { return ceil_div((long long)ceil_div(T, row_block(G)) * G, BM / row_block(G)); }
+long long row_tiles(int G, int T)
+{
+    const long long blocks = (long long)ceil_div(T, row_block(G)) * G, per = BM / row_block(G);
+    return (blocks + per - 1) / per;
+}
 
 // Fills in the rows and the tiles; false if there are too many to count in an int.
 bool set_tiles(Prob &q, int G, int T, int N, int bn, int splits)
@@ -896,9 +900,10 @@ bool set_tiles(Prob &q, int G, int T, int N, int bn, int splits)
     q.n_mtiles = (int)row_tiles(G, T);
     q.N = N;
     q.n_ntiles = ceil_div(N, bn);
-    const long long blocks = (long long)q.rblocks * G, items = (long long)q.n_mtiles * q.n_ntiles * splits;
+    const long long items = (long long)q.n_mtiles * q.n_ntiles * splits;
     q.n_items = (int)items;
-    return blocks <= 0x7ffffff0LL && items <= 0x7fffffffLL;
+    // the kernel counts rows, those that pad a block included, and items in ints
+    return row_tiles(G, T) * BM <= 0x7fffffffLL && items <= 0x7fffffffLL;
 }
 
 void set_split_rows(SplitParams &p, int G, int T, int tn)

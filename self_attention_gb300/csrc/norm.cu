@@ -4,7 +4,7 @@
 // is taken by a warp (up to 2048 columns; no barrier, only shuffles), by 256 threads (to 16384) or
 // by 1024 threads (to 32768), each thread holding chunks of 8 neighbouring columns (16-byte loads);
 // longer rows are read a second time from L2.
-#include "common.cuh"
+#include "cluster.cuh"
 #include "kernels.h"
 
 namespace attn {
