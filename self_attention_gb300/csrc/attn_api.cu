@@ -155,7 +155,8 @@ CUresult attn::make_map_3d(CUtensorMap *m, const void *base, CUtensorMapDataType
     cuuint32_t box[3] = {(cuuint32_t)box0, (cuuint32_t)box1, 1};
     cuuint32_t elem[3] = {1, 1, 1};
     return g_encode(m, type, 3, const_cast<void *>(base), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    box0 * elem_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 

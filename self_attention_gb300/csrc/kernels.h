@@ -97,8 +97,9 @@ cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, dim3 block, size_
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// 3-D tensor map (innermost first: d0, d1, d2 elements, dense) with boxes of box0 x box1 x 1 and
-// the 128-byte swizzle; elements outside read as zeros and are not written.
+// 3-D tensor map (innermost first: d0, d1, d2 elements, dense) with boxes of box0 x box1 x 1 whose
+// rows, 64 or 128 bytes, are swizzled over their length; elements outside read as zeros and are not
+// written.
 CUresult make_map_3d(CUtensorMap *m, const void *base, CUtensorMapDataType type, int elem_bytes, long long d0,
                      long long d1, long long d2, int box0, int box1);
 

@@ -323,9 +323,23 @@ __global__ void __launch_bounds__(128 + 32 * kEpiWarps, 1)
             const int grp = block / pr.rblocks, i0 = block % pr.rblocks * pr.rb + first % pr.rb;
             const int col0 = nt * BN + set * 64;
             const bool mine = set * 64 < BN && col0 < pr.N && i0 < pr.T && block < pr.n_rblocks;
-            auto load_res = [&] {
-                ptx::mbar_arrive_expect_tx(rbar, 4096);
-                ptx::tma_load_3d(buf, &maps.a2, rbar, col0, i0, grp);
+            // The residual of the warp's 64 columns, or (beside z) of 32 of them behind the half for z.
+            auto load_res = [&](int half) {
+                ptx::mbar_arrive_expect_tx(rbar, p.has_z ? 2048 : 4096);
+                ptx::tma_load_3d(buf + (p.has_z ? 2048 : 0), &maps.a2, rbar, col0 + half * 32, i0, grp);
+            };
+            auto wait_res = [&] {
+                wait_bounded(rbar, rphase, g);
+                rphase ^= 1;
+            };
+            // f += the residual's 8 columns at `addr`
+            auto add_res = [&](uint64_t *f, uint32_t addr) {
+                const uint4 r = lds_u128(addr);
+                const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    f[e] = ptx::add_f32x2(f[e], ptx::f2_pack(__uint_as_float(w[e] << 16),
+                                                             __uint_as_float(w[e] & 0xffff0000u)));
             };
             // Leaves the buffer to a TMA store.
             auto store = [&](const CUtensorMap *map, int c, int slice) {
@@ -342,7 +356,7 @@ __global__ void __launch_bounds__(128 + 32 * kEpiWarps, 1)
                 __syncwarp();
             };
             reclaim();
-            if (lane == 0 && p.has_r && !p.has_z && mine) load_res();
+            if (lane == 0 && p.has_r && mine) load_res(0);
             const uint64_t xs = f2_both((P == FwdQ8 && mine && i0 + lane < pr.T) ? p.x_scale[i0 + lane] : 0.f);
             wait_bounded(&bar_acc_full[ab], (li >> 1) & 1, g);
             ptx::tc_fence_after();
@@ -379,40 +393,72 @@ __global__ void __launch_bounds__(128 + 32 * kEpiWarps, 1)
             // z (or, without scales and bias, the sums) of 32 columns, as pairs
             auto load_z = [&](int half, uint64_t (&f)[16]) {
                 uint32_t v[32];
+                ulonglong2 bias[8];
+                if constexpr (P == Fwd) {   // asked for ahead of the wait for the accumulator
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const int col = col0 + half * 32 + q * 4;
+                        bias[q] = p.bias && col < pr.N ? __ldg(reinterpret_cast<const ulonglong2 *>(p.bias + col))
+                                                       : make_ulonglong2(0, 0);
+                    }
+                }
                 ptx::tmem_ld32(taddr + half * 32, v);
                 ptx::tmem_ld_wait();
                 reg_fence(v);
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     f[i] = ptx::f2_pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-                if constexpr (P == Fwd || P == FwdQ8) {
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) {   // 4 columns
+                for (int q = 0; q < 8; ++q) {   // 4 columns
+                    if constexpr (P == FwdQ8) {
                         const int col = col0 + half * 32 + q * 4;
-                        ulonglong2 bias = make_ulonglong2(0, 0);
-                        if (p.bias && col < pr.N) bias = __ldg(reinterpret_cast<const ulonglong2 *>(p.bias + col));
-                        if (P == FwdQ8) {
-                            ulonglong2 ws = make_ulonglong2(0, 0);
-                            if (col < pr.N) ws = __ldg(reinterpret_cast<const ulonglong2 *>(p.w_scale + col));
-                            f[2 * q] = ptx::fma_f32x2(f[2 * q], ptx::mul_f32x2(ws.x, xs), bias.x);
-                            f[2 * q + 1] = ptx::fma_f32x2(f[2 * q + 1], ptx::mul_f32x2(ws.y, xs), bias.y);
-                        } else if (p.bias) {
-                            f[2 * q] = ptx::add_f32x2(f[2 * q], bias.x);
-                            f[2 * q + 1] = ptx::add_f32x2(f[2 * q + 1], bias.y);
-                        }
+                        ulonglong2 b = make_ulonglong2(0, 0), ws = b;
+                        if (p.bias && col < pr.N) b = __ldg(reinterpret_cast<const ulonglong2 *>(p.bias + col));
+                        if (col < pr.N) ws = __ldg(reinterpret_cast<const ulonglong2 *>(p.w_scale + col));
+                        f[2 * q] = ptx::fma_f32x2(f[2 * q], ptx::mul_f32x2(ws.x, xs), b.x);
+                        f[2 * q + 1] = ptx::fma_f32x2(f[2 * q + 1], ptx::mul_f32x2(ws.y, xs), b.y);
+                    } else if constexpr (P == Fwd) {
+                        f[2 * q] = ptx::add_f32x2(f[2 * q], bias[q].x);
+                        f[2 * q + 1] = ptx::add_f32x2(f[2 * q + 1], bias[q].y);
                     }
                 }
             };
-            if (p.has_z) {   // a pass of its own: reading the accumulator twice is cheaper than a second buffer
+            if (P == Fwd && p.has_z) {
+                // 32 columns at a time: z in the buffer's first half, y in the second (rows of 64 bytes, the
+                // 16-byte chunk c of row r at c ^ (r / 2 & 3)); reading the accumulator costs too much beside
+                // the products to take z in a pass of its own
+                const uint32_t zrow = sbuf + lane * 64, swz = (lane >> 1) & 3;
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
                     uint64_t f[16];
+                    uint4 z[4];
                     load_z(half, f);
+                    if (half) release();
+                    if (col0 + half * 32 >= pr.N) continue;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)   // 8 columns: 16 bytes of the row
-                        sts_u128(row + (((half * 4 + q) ^ (lane & 7)) << 4), pack_bf16x8(f + 4 * q));
+                    for (int q = 0; q < 4; ++q) z[q] = pack_bf16x8(f + 4 * q);
+                    activate(f, p.act);
+                    if (half) {
+                        reclaim();
+                        if (p.has_r && lane == 0) load_res(1);
+                    }
+                    if (p.has_r) wait_res();
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t at = zrow + ((q ^ swz) << 4);
+                        sts_u128(at, z[q]);
+                        if (p.has_r) add_res(f + 4 * q, at + 2048);
+                        sts_u128(at + 2048, pack_bf16x8(f + 4 * q));
+                    }
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        ptx::tma_store_3d(&maps.y2, buf, col0 + half * 32, i0, grp);
+                        ptx::tma_store_3d(&maps.y, buf + 2048, col0 + half * 32, i0, grp);
+                        ptx::bulk_commit_group();
+                    }
                 }
-                store(&maps.y2, col0, grp);
+                continue;
             }
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
@@ -420,29 +466,13 @@ __global__ void __launch_bounds__(128 + 32 * kEpiWarps, 1)
                 load_z(half, f);
                 if (half) release();
                 if (P == Fwd || P == FwdQ8) activate(f, p.act);
-                if (half == 0 && p.has_z) {
-                    reclaim();
-                    if (p.has_r && lane == 0) load_res();
+                if ((P == Fwd || P == FwdQ8) && p.has_r && half == 0) wait_res();
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {   // 8 columns: 16 bytes of the row
+                    const uint32_t at = row + (((half * 4 + q) ^ (lane & 7)) << 4);
+                    if ((P == Fwd || P == FwdQ8) && p.has_r) add_res(f + 4 * q, at);
+                    sts_u128(at, pack_bf16x8(f + 4 * q));
                 }
-                if ((P == Fwd || P == FwdQ8) && p.has_r) {
-                    if (half == 0) {
-                        wait_bounded(rbar, rphase, g);
-                        rphase ^= 1;
-                    }
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const uint4 r = lds_u128(row + (((half * 4 + q) ^ (lane & 7)) << 4));
-                        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            f[4 * q + e] =
-                                ptx::add_f32x2(f[4 * q + e], ptx::f2_pack(__uint_as_float(w[e] << 16),
-                                                                          __uint_as_float(w[e] & 0xffff0000u)));
-                    }
-                }
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    sts_u128(row + (((half * 4 + q) ^ (lane & 7)) << 4), pack_bf16x8(f + 4 * q));
             }
             if (P == Bwd && w)
                 store(&maps.y2, col0, 0);
@@ -1042,9 +1072,10 @@ cudaError_t launch_linear(const LinArgs &a, cudaStream_t stream)
         r = make_map_3d(&m.a, a.x, kBf16, 2, a.dk, a.T, (long long)a.G * a.H, 64, q.rb);
         if (r == CUDA_SUCCESS) r = make_map_3d(&m.b, a.w, kBf16, 2, a.N, a.K, 1, 64, 64);
     }
-    if (r == CUDA_SUCCESS) r = make_map_3d(&m.y, a.y, kBf16, 2, a.N, a.T, a.G, 64, 32);
-    if (r == CUDA_SUCCESS && a.z) r = make_map_3d(&m.y2, a.z, kBf16, 2, a.N, a.T, a.G, 64, 32);
-    if (r == CUDA_SUCCESS && a.residual) r = make_map_3d(&m.a2, a.residual, kBf16, 2, a.N, a.T, a.G, 64, 32);
+    const int oc = a.z ? 32 : 64;   // columns of a store (see the epilogue)
+    if (r == CUDA_SUCCESS) r = make_map_3d(&m.y, a.y, kBf16, 2, a.N, a.T, a.G, oc, 32);
+    if (r == CUDA_SUCCESS && a.z) r = make_map_3d(&m.y2, a.z, kBf16, 2, a.N, a.T, a.G, oc, 32);
+    if (r == CUDA_SUCCESS && a.residual) r = make_map_3d(&m.a2, a.residual, kBf16, 2, a.N, a.T, a.G, oc, 32);
     if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
     const int pairs = device_sm_count() / 2, clusters = q.n_items < pairs ? q.n_items : pairs;
     if (a.q8)
