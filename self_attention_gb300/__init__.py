@@ -15,13 +15,14 @@ pass recomputes the attention tiles from (section 3, "Recomputation in backpropa
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import math
 import os
 
 import torch
 from torch.autograd.function import once_differentiable
 
-from .build import LIB_PATH
+from .build import BINDING_PATH, LIB_PATH
 
 __all__ = [
     "AttnError", "attn_fwd", "attn_fwd_workspace_size", "attn_fwd_with_workspace", "attn_fwd_diagnostic",
@@ -504,29 +505,24 @@ def attention(q, k, v, scale: float | None = None):
 
 
 # ------------------------------------------------- the rest of the block: linear layers and norms
-# These calls take as long on the host as the smallest kernels do on the GPU, so they go to the library
-# directly rather than through the mirrors above.
-_BF16, _F32, _E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+# The smallest of these calls take a few microseconds on the GPU, so their checks, allocations and the call
+# of the library are compiled (csrc/binding.cpp); the operands' types, shapes and devices are checked there.
+_binding_module = None
 
 
-def _at(t):
-    return None if t is None else t.data_ptr()
-
-
-def _want(name, t, dtype, shape, dev):
-    """One operand: a contiguous tensor of this type and shape on this device."""
-    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, got "
-                         f"{t.dtype} {tuple(t.shape)} on {t.device}"
-                         f"{'' if t.is_contiguous() else ', not contiguous'}")
-
-
-def _rows(name, x, dtype=_BF16):
-    """[..., K] rows -> (M, K, device)."""
-    if not x.is_cuda or x.dtype is not dtype or x.dim() < 1 or not x.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtype} CUDA tensor [..., width]")
-    K = x.shape[-1]
-    return (x.numel() // K if K else 0), K, x.device
+def _binding():
+    global _binding_module
+    if _binding_module is None:
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(f"attn_binding.so not found at {BINDING_PATH}: build it with "
+                               "`python -c 'import __graft_entry__ as g; g.build()'`")
+        load_library()
+        spec = importlib.util.spec_from_file_location("attn_binding", BINDING_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.set_error(_raise)
+        _binding_module = module
+    return _binding_module
 
 
 def _act(activation) -> int:
@@ -536,45 +532,32 @@ def _act(activation) -> int:
     return act
 
 
-def _on(dev, stream, tensors, fn):
-    """fn(raw stream) with `dev` current.  On another stream than the device's current one the
-    operands are recorded on it, and what fn allocates belongs to it."""
-    if stream is None and torch._C._cuda_getDevice() == dev.index:
-        return fn(torch._C._cuda_getCurrentRawStream(dev.index))
+def _on(stream, fn, *args):
+    """fn(*args) on `stream`, a stream of its first tensor's device: the tensors are recorded on it, and
+    what fn allocates belongs to it."""
+    tensors = [t for t in args if isinstance(t, torch.Tensor)]
+    if not tensors or not all(t.is_cuda for t in tensors):
+        raise ValueError("expected CUDA tensors")
+    dev = tensors[0].device
     with torch.cuda.device(dev):
         st = _device_stream(dev, stream)
         if not isinstance(st, torch.cuda.Stream):
             st = torch.cuda.ExternalStream(int(st), device=dev)
         if st != torch.cuda.current_stream(dev):
             for t in tensors:
-                if t is not None:
-                    t.record_stream(st)
+                t.record_stream(st)
         with torch.cuda.stream(st):
-            return fn(st.cuda_stream)
+            return fn(*args)
 
 
 def linear_forward(x, w, bias=None, residual=None, activation: str = "none", keep_z: bool = False, stream=None):
     """y = act(x w + bias) + residual: x [..., K], w [K, N] bf16, bias [N] fp32, residual [..., N]
     bf16.  Returns y [..., N] bf16, or (y, z) with keep_z: z is the pre-activation that
     linear_backward() takes."""
-    act = _act(activation)
-    M, K, dev = _rows("x", x)
-    N = w.shape[-1]
-    shape = x.shape[:-1] + (N,)
-    _want("w", w, _BF16, (K, N), dev)
-    if bias is not None:
-        _want("bias", bias, _F32, (N,), dev)
-    if residual is not None:
-        _want("residual", residual, _BF16, shape, dev)
-
-    def call(st):
-        y = torch.empty(shape, dtype=_BF16, device=dev)
-        z = torch.empty(shape, dtype=_BF16, device=dev) if keep_z else None
-        _raise(load_library().attn_linear(x.data_ptr(), w.data_ptr(), _at(bias), _at(residual), y.data_ptr(), _at(z),
-                                          M, K, N, act, st), "attn_linear")
-        return (y, z) if keep_z else y
-
-    return _on(dev, stream, (x, w, bias, residual), call)
+    fn, act = _binding().linear_forward, _act(activation)
+    if stream is None:
+        return fn(x, w, bias, residual, act, keep_z)
+    return _on(stream, fn, x, w, bias, residual, act, keep_z)
 
 
 def linear_backward(x, w, dy, z=None, activation: str = "none", bias: bool = True, need_dx: bool = True,
@@ -582,172 +565,63 @@ def linear_backward(x, w, dy, z=None, activation: str = "none", bias: bool = Tru
     """(dx [..., K] bf16, dw [K, N] bf16, dbias [N] fp32) of linear_forward() for dy = dL/dy; None
     for what is not asked for.  z: what linear_forward(keep_z=True) kept (none without an
     activation).  The residual's gradient is dy itself."""
-    act = _act(activation)
-    M, K, dev = _rows("x", x)
-    N = w.shape[-1]
-    _want("w", w, _BF16, (K, N), dev)
-    _want("dy", dy, _BF16, x.shape[:-1] + (N,), dev)
-    if act == 0:
-        z = None
-    elif z is None:
-        raise ValueError("linear_backward needs the pre-activation z that linear_forward(keep_z=True) returns")
-    else:
-        _want("z", z, _BF16, dy.shape, dev)
-
-    def call(st):
-        dx = torch.empty_like(x) if need_dx else None
-        dw = torch.empty_like(w) if need_dw else None
-        db = torch.empty(N, dtype=_F32, device=dev) if bias else None
-        lib = load_library()
-        nbytes = lib.attn_linear_bwd_workspace_size(M, K, N, act)
-        ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
-        _raise(lib.attn_linear_bwd(x.data_ptr(), w.data_ptr(), dy.data_ptr(), _at(z), _at(dx), _at(dw), _at(db),
-                                   ws.data_ptr(), nbytes, M, K, N, act, st), "attn_linear_bwd")
-        return dx, dw, db
-
-    return _on(dev, stream, (x, w, dy, z), call)
+    fn, act = _binding().linear_backward, _act(activation)
+    if stream is None:
+        return fn(x, w, dy, z, act, bias, need_dx, need_dw)
+    return _on(stream, fn, x, w, dy, z, act, bias, need_dx, need_dw)
 
 
 def out_proj_forward(o, w, bias=None, residual=None, stream=None):
     """Output projection of attention's o [B,H,N,d_k], heads side by side: y [B,N,N_out] = o w +
     bias + residual, with w [H*d_k, N_out] bf16, bias [N_out] fp32, residual [B,N,N_out] bf16."""
-    B, H, N, D = _check_inputs(o)
-    dev, n_out = o.device, w.shape[-1]
-    _want("w", w, _BF16, (H * D, n_out), dev)
-    if bias is not None:
-        _want("bias", bias, _F32, (n_out,), dev)
-    if residual is not None:
-        _want("residual", residual, _BF16, (B, N, n_out), dev)
-
-    def call(st):
-        y = torch.empty((B, N, n_out), dtype=_BF16, device=dev)
-        _raise(load_library().attn_out_proj(o.data_ptr(), w.data_ptr(), _at(bias), _at(residual), y.data_ptr(),
-                                            B, H, N, D, n_out, st), "attn_out_proj")
-        return y
-
-    return _on(dev, stream, (o, w, bias, residual), call)
+    fn = _binding().out_proj_forward
+    return fn(o, w, bias, residual) if stream is None else _on(stream, fn, o, w, bias, residual)
 
 
 def out_proj_backward(o, w, dy, bias: bool = True, need_do: bool = True, need_dw: bool = True, stream=None):
     """(do [B,H,N,d_k] bf16, dw [H*d_k,N_out] bf16, dbias [N_out] fp32) of out_proj_forward()."""
-    B, H, N, D = _check_inputs(o)
-    dev, n_out = o.device, w.shape[-1]
-    _want("w", w, _BF16, (H * D, n_out), dev)
-    _want("dy", dy, _BF16, (B, N, n_out), dev)
-
-    def call(st):
-        do = torch.empty_like(o) if need_do else None
-        dw = torch.empty_like(w) if need_dw else None
-        db = torch.empty(n_out, dtype=_F32, device=dev) if bias else None
-        lib = load_library()
-        nbytes = lib.attn_out_proj_bwd_workspace_size(B, H, N, D, n_out)
-        ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
-        _raise(lib.attn_out_proj_bwd(o.data_ptr(), w.data_ptr(), dy.data_ptr(), _at(do), _at(dw), _at(db),
-                                     ws.data_ptr(), nbytes, B, H, N, D, n_out, st), "attn_out_proj_bwd")
-        return do, dw, db
-
-    return _on(dev, stream, (o, w, dy), call)
+    fn = _binding().out_proj_backward
+    if stream is None:
+        return fn(o, w, dy, bias, need_do, need_dw)
+    return _on(stream, fn, o, w, dy, bias, need_do, need_dw)
 
 
 def rms_norm_forward(x, weight, residual=None, eps: float = 1e-6, stream=None):
     """(y, h, rstd): h = x + residual (x itself without one), rstd = 1/sqrt(mean(h^2) + eps),
     y = h rstd weight.  x, residual [..., D] bf16, weight [D] fp32; rstd [...] fp32."""
-    M, D, dev = _rows("x", x)
-    _want("weight", weight, _F32, (D,), dev)
-    if residual is not None:
-        _want("residual", residual, _BF16, x.shape, dev)
-
-    def call(st):
-        y = torch.empty_like(x)
-        h = torch.empty_like(x) if residual is not None else None
-        rstd = torch.empty(x.shape[:-1], dtype=_F32, device=dev)
-        _raise(load_library().attn_rms_norm(x.data_ptr(), _at(residual), weight.data_ptr(), y.data_ptr(), _at(h),
-                                            rstd.data_ptr(), M, D, eps, st), "attn_rms_norm")
-        return y, (x if h is None else h), rstd
-
-    return _on(dev, stream, (x, weight, residual), call)
+    fn = _binding().rms_norm_forward
+    y, h, rstd = fn(x, weight, residual, eps) if stream is None else _on(stream, fn, x, weight, residual, eps)
+    return y, (x if h is None else h), rstd
 
 
 def rms_norm_backward(dy, h, weight, rstd, dh=None, stream=None):
     """(dx [..., D] bf16, dweight [D] fp32) of rms_norm_forward(); dh is the gradient that reaches h
     by its other uses.  dx is the gradient of x and of the residual alike."""
-    M, D, dev = _rows("h", h)
-    _want("dy", dy, _BF16, h.shape, dev)
-    _want("weight", weight, _F32, (D,), dev)
-    _want("rstd", rstd, _F32, h.shape[:-1], dev)
-    if dh is not None:
-        _want("dh", dh, _BF16, h.shape, dev)
-
-    def call(st):
-        dx = torch.empty_like(h)
-        dweight = torch.empty(D, dtype=_F32, device=dev)
-        lib = load_library()
-        nbytes = lib.attn_rms_norm_bwd_workspace_size(M, D)
-        ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
-        _raise(lib.attn_rms_norm_bwd(dy.data_ptr(), h.data_ptr(), weight.data_ptr(), rstd.data_ptr(), _at(dh),
-                                     dx.data_ptr(), dweight.data_ptr(), ws.data_ptr(), nbytes, M, D, st),
-               "attn_rms_norm_bwd")
-        return dx, dweight
-
-    return _on(dev, stream, (dy, h, weight, rstd, dh), call)
+    fn = _binding().rms_norm_backward
+    return fn(dy, h, weight, rstd, dh) if stream is None else _on(stream, fn, dy, h, weight, rstd, dh)
 
 
 def rms_norm_q8(x, weight, residual=None, eps: float = 1e-6, stream=None):
     """(yq, scale, h): rms_norm_forward() with y as e4m3 rows, y ~ yq * scale[..., None]."""
-    M, D, dev = _rows("x", x)
-    _want("weight", weight, _F32, (D,), dev)
-    if residual is not None:
-        _want("residual", residual, _BF16, x.shape, dev)
-
-    def call(st):
-        yq = torch.empty(x.shape, dtype=_E4M3, device=dev)
-        scale = torch.empty(x.shape[:-1], dtype=_F32, device=dev)
-        h = torch.empty_like(x) if residual is not None else None
-        _raise(load_library().attn_rms_norm_q8(x.data_ptr(), _at(residual), weight.data_ptr(), yq.data_ptr(),
-                                               scale.data_ptr(), _at(h), M, D, eps, st), "attn_rms_norm_q8")
-        return yq, scale, (x if h is None else h)
-
-    return _on(dev, stream, (x, weight, residual), call)
+    fn = _binding().rms_norm_q8
+    yq, scale, h = fn(x, weight, residual, eps) if stream is None else _on(stream, fn, x, weight, residual, eps)
+    return yq, scale, (x if h is None else h)
 
 
 def quantize_q8(x, stream=None):
     """(xq, scale): the rows of x [..., D] bf16 as e4m3 with one fp32 scale each.  The weights of
     linear_q8() are quantize_q8(w.t().contiguous())."""
-    M, D, dev = _rows("x", x)
-
-    def call(st):
-        xq = torch.empty(x.shape, dtype=_E4M3, device=dev)
-        scale = torch.empty(x.shape[:-1], dtype=_F32, device=dev)
-        _raise(load_library().attn_quantize_q8(x.data_ptr(), xq.data_ptr(), scale.data_ptr(), M, D, st),
-               "attn_quantize_q8")
-        return xq, scale
-
-    return _on(dev, stream, (x,), call)
+    fn = _binding().quantize_q8
+    return fn(x) if stream is None else _on(stream, fn, x)
 
 
 def linear_q8(xq, x_scale, wq, w_scale, bias=None, residual=None, activation: str = "none", stream=None):
     """y [..., N] bf16 = act((xq wq^T) x_scale w_scale + bias) + residual: xq [..., K] and wq [N, K]
     e4m3, x_scale [...] and w_scale [N] fp32 (as quantize_q8() and rms_norm_q8() make them)."""
-    act = _act(activation)
-    M, K, dev = _rows("xq", xq, _E4M3)
-    N = wq.shape[0]
-    shape = xq.shape[:-1] + (N,)
-    _want("x_scale", x_scale, _F32, xq.shape[:-1], dev)
-    _want("wq", wq, _E4M3, (N, K), dev)
-    _want("w_scale", w_scale, _F32, (N,), dev)
-    if bias is not None:
-        _want("bias", bias, _F32, (N,), dev)
-    if residual is not None:
-        _want("residual", residual, _BF16, shape, dev)
-
-    def call(st):
-        y = torch.empty(shape, dtype=_BF16, device=dev)
-        _raise(load_library().attn_linear_q8(xq.data_ptr(), x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(),
-                                             _at(bias), _at(residual), y.data_ptr(), M, K, N, act, st),
-               "attn_linear_q8")
-        return y
-
-    return _on(dev, stream, (xq, x_scale, wq, w_scale, bias, residual), call)
+    fn, act = _binding().linear_q8, _act(activation)
+    if stream is None:
+        return fn(xq, x_scale, wq, w_scale, bias, residual, act)
+    return _on(stream, fn, xq, x_scale, wq, w_scale, bias, residual, act)
 
 
 class _Linear(torch.autograd.Function):

@@ -4,14 +4,17 @@ Each .cu file is compiled as its own translation unit, in parallel, then linked 
 shared library under self_attention_gb300/_build/.  The CUDA runtime is the shared one: a process
 that has loaded PyTorch then holds one runtime instead of two, which takes about 2 us off a call that
 follows a tensor's allocation (measured on the GB300's host).  The driver is reached through
-cudaGetDriverEntryPointByVersion, so no -lcuda is needed.
+cudaGetDriverEntryPointByVersion, so no -lcuda is needed.  The tensor-level calls of the linear layers
+and the norm go through a small CPython extension beside the library (csrc/binding.cpp, g++).
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +23,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_NAME = "libattn_gb300.so"
 LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
+BINDING_PATH = os.path.join(BUILD_DIR, "attn_binding.so")   # CPython extension over the library and PyTorch
 
 SOURCES = ["attn_api.cu", "attn_fwd.cu", "attn_bwd.cu", "vector_add.cu", "proj.cu", "unfused.cu", "linear.cu", "norm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -40,9 +44,41 @@ def _inputs_newest() -> float:
     return max(os.path.getmtime(f) for f in files)
 
 
+def _torch_dir() -> str:
+    return importlib.util.find_spec("torch").submodule_search_locations[0]
+
+
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+
+
+def _compile_binding(tool: str, tag: str) -> str:
+    obj = os.path.join(BUILD_DIR, f"binding.{tag}.o")
+    torch_inc = os.path.join(_torch_dir(), "include")
+    cuda_inc = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(tool))), "include")
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", f"-I{INCLUDE}", f"-I{torch_inc}",
+          f"-I{os.path.join(torch_inc, 'torch', 'csrc', 'api', 'include')}", f"-I{cuda_inc}",
+          f"-I{sysconfig.get_paths()['include']}", "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj],
+         "g++ on binding.cpp")
+    return obj
+
+
+def _link_binding(obj: str, tag: str):
+    lib = os.path.join(_torch_dir(), "lib")
+    tmp = BINDING_PATH + f".{tag}.tmp"
+    _run(["g++", "-shared", "-o", tmp, obj, f"-L{BUILD_DIR}", "-l:" + LIB_NAME, f"-L{lib}", "-ltorch_python", "-ltorch",
+          "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"],
+         "linking the binding")
+    os.remove(obj)
+    os.replace(tmp, BINDING_PATH)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile (if stale) and return the path of libattn_gb300.so."""
-    if not force and os.path.exists(LIB_PATH) and os.path.getmtime(LIB_PATH) >= _inputs_newest():
+    """Compile (if stale) the library and the Python binding; returns the path of libattn_gb300.so."""
+    newest = _inputs_newest()
+    if not force and all(os.path.exists(p) and os.path.getmtime(p) >= newest for p in (LIB_PATH, BINDING_PATH)):
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     tool = nvcc()
@@ -58,8 +94,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+        binding = ex.submit(_compile_binding, tool, tag)
         results = list(ex.map(compile_one, SOURCES))
+        binding_obj = binding.result()
     objs = [o for o, _ in results]
     tmp = LIB_PATH + f".{tag}.tmp"
     runtime = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(tool))), "lib64")
@@ -70,6 +108,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    _link_binding(binding_obj, tag)
     if verbose:
         for _, log in results:
             print(log)

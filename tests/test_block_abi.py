@@ -167,3 +167,18 @@ def test_gradients_of_the_formulas_against_differences():
         up[at], dn[at] = args[at] + e * v, args[at] - e * v
         diff = (loss(*up) - loss(*dn)) / (2 * e)
         assert abs(float(diff - (grads[key][0] * v).sum())) < 1e-6
+
+
+def test_tensor_level_refusals_without_a_gpu(lib):
+    """The compiled binding loads without a GPU and refuses what are no CUDA tensors with a ValueError,
+    unknown activations by name, and never reaches the device."""
+    x, w, v = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(64, 32, dtype=torch.bfloat16), torch.zeros(64)
+    for bad in (lambda: sa.linear_forward(x, w), lambda: sa.linear_forward(None, w), lambda: sa.linear_forward(3, w),
+                lambda: sa.linear_backward(x, w, x), lambda: sa.out_proj_forward(x, w), lambda: sa.out_proj_backward(x, w, x),
+                lambda: sa.linear_q8(x, v, w, v), lambda: sa.rms_norm_forward(x, v), lambda: sa.rms_norm_q8(x, v),
+                lambda: sa.rms_norm_backward(x, x, v, v), lambda: sa.quantize_q8(x), lambda: sa.quantize_q8("x"),
+                lambda: sa.linear_forward(x, w, activation="swish"), lambda: sa.quantize_q8(x, stream=0)):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(TypeError):
+        sa._binding().quantize_q8(x, x)
