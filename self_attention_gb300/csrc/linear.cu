@@ -167,6 +167,12 @@ __global__ void __launch_bounds__(128 + 32 * kEpiWarps, 1)
         for (int b = 0; b < kEpiWarps; ++b) ptx::mbar_init(&bar_res[b], 1);
         ptx::fence_mbar_init();
     }
+    if (warp == 2 && ptx::elect_one()) {
+        ptx::tma_prefetch_desc(&maps.a);
+        ptx::tma_prefetch_desc(&maps.b);
+        if (P == Bwd || p.has_r) ptx::tma_prefetch_desc(&maps.a2);
+        if (P == Bwd) ptx::tma_prefetch_desc(&maps.b2);
+    }
     if (warp == 1) {
         ptx::tmem_alloc_pair(&tmem_sh, C::TM_COLS);
         ptx::tmem_relinquish_pair();
@@ -481,7 +487,7 @@ __global__ void __launch_bounds__(128 + 32 * kEpiWarps, 1)
             else
                 store(&maps.y, col0, grp);
         }
-        if (lane == 0) ptx::bulk_wait_group<0>();
+        if (lane == 0) ptx::bulk_wait_group<0>();   // complete before the CTA exits
     } else if (P == Bwd && warp >= 2) {
         // the bias gradient: its partial sums (see dz_kernel) added up by the two warps that have no
         // other work, 32 columns a warp, while the products run
@@ -614,6 +620,10 @@ __global__ void __launch_bounds__(256) gemm_split_kernel(const __grid_constant__
         }
         ptx::mbar_init(&bar_acc, 1);
         ptx::fence_mbar_init();
+    }
+    if (warp == 2 && ptx::elect_one()) {
+        ptx::tma_prefetch_desc(&map_w);
+        ptx::tma_prefetch_desc(&map_x);
     }
     if (warp == 1) {
         ptx::tmem_alloc(&tmem_sh, C::TM_COLS);
