@@ -149,17 +149,25 @@ __device__ __forceinline__ uint32_t cluster_size()
     return r;
 }
 
-__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr)
+// The two halves of cluster_sync(): what a thread wrote before it arrives is visible to those that have
+// waited.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
+__device__ __forceinline__ void st_cluster_b32(uint32_t addr, uint32_t v)
 {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
+    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 }  // namespace ptx
+
+// Four fp32 from shared memory, as two pairs.
+__device__ __forceinline__ ulonglong2 lds_f32x4(uint32_t addr)
+{
+    ulonglong2 v;
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(v.x), "=l"(v.y) : "r"(addr) : "memory");
+    return v;
+}
 
 // wait_bounded() for a barrier on which another CTA of the cluster arrives too.
 __device__ __forceinline__ bool wait_bounded_cluster(uint64_t *bar, uint32_t parity, const Guard &g)

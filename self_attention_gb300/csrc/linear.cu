@@ -511,9 +511,11 @@ __global__ void __launch_bounds__(128 + 32 * kEpiWarps, 1)
 // Few rows: the weights are the large operand, and the time is what it takes to stream them.  The
 // product is turned round, C^T[128 columns of y x TN rows] with the weights as the MMA's A operand, so
 // that TN follows the number of rows, and K is split over the CTAs of a cluster, so that many SMs
-// read (one 2048 x 8192 matrix is 64 column tiles).  Each CTA leaves its partial tile in its shared
-// memory; after a cluster barrier each sums its share of the rows over all of them in order, applies
-// the epilogue and stores.  Up to TN = 64 two CTAs fit an SM.
+// read (one 2048 x 8192 matrix is 64 column tiles).  Each CTA sends the rows of its partial tile to the
+// CTAs that own them (row r to rank r mod splits), straight from tensor memory into their shared memory;
+// after one cluster barrier each sums its rows over the ranks in order, applies the epilogue and stores.
+// (Leaving the partial tiles in place and fetching them takes a second barrier, and remote loads that
+// are waited for: 1 us of 7 more.)  Up to TN = 64 two CTAs fit an SM.
 struct SplitParams {
     int T, rb, rblocks, n_rblocks; // rows as in GemmParams, in tiles of TN
     int N, n_ntiles;               // columns of y, tiles of 128
@@ -531,65 +533,80 @@ struct SplitCfg {
     static constexpr bool FP8 = P == FwdQ8;
     static constexpr int KE = FP8 ? 128 : 64;
     static constexpr int A_BYTES = 128 * 128, B_BYTES = TN * 128, STAGE = A_BYTES + B_BYTES;
-    static constexpr int STAGES = TN <= 16 ? 6 : TN <= 32 ? 5 : TN <= 64 ? 4 : TN <= 128 ? 6 : 4;
-    static constexpr int SMEM = STAGES * STAGE + 1024;
+    static constexpr int RECV = TN * 512;   // partial rows sent here: [rank][row of this CTA][128] fp32
+    static constexpr int STAGES = TN <= 16 ? 5 : TN <= 32 ? 4 : TN <= 64 ? 3 : 5;
+    static constexpr int SMEM = STAGES * STAGE + RECV + 1024;
     static constexpr uint32_t TM_COLS = TN < 32 ? 32 : TN;
-    static_assert(STAGES * STAGE >= TN * 128 * 4, "the partial tile reuses the stages");
 };
 
-// Sums this CTA's share of the rows over the S partial tiles of the cluster, in order, and finishes
-// them: a warp a row, 4 columns a lane, R rows at a time so that their loads are in flight together.
-template <Policy P, int TN, int S, int R>
-__device__ __forceinline__ void join_rows(const SplitParams &p, const uint8_t *smem, int rank, int mt, int n0)
+// After every CTA of the cluster has arrived: sums this CTA's rows over the S ranks, in order, and finishes
+// them, a warp a row, 4 columns a lane.  What a row's epilogue reads is asked for a row ahead, the first
+// row's before the wait for the cluster.
+template <Policy P, int TN, int S>
+__device__ __forceinline__ void join_rows(const SplitParams &p, uint32_t recv, int rank, int mt, int n0)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = n0 + lane * 4;
-    const uint32_t part = ptx::smem_u32(smem) + lane * 16;
-    constexpr int STRIDE = S * 8;   // rows of the cluster's warps
-    for (int r0 = rank * 8 + warp; r0 < TN; r0 += STRIDE * R) {
-        float4 t[R][S];
-#pragma unroll
-        for (int q = 0; q < R; ++q)
-            if (r0 + q * STRIDE < TN)
-#pragma unroll
-                for (int k = 0; k < S; ++k)
-                    t[q][k] = ptx::ld_cluster_f32x4(ptx::cluster_addr(part + (r0 + q * STRIDE) * 512, k));
-#pragma unroll
-        for (int q = 0; q < R; ++q) {
-            const int r = r0 + q * STRIDE, at = mt * TN + r, block = at / p.rb, i = block % p.rblocks * p.rb + at % p.rb;
-            if (r >= TN || block >= p.n_rblocks || i >= p.T || col >= p.N) continue;
-            float4 f = t[q][0];
-#pragma unroll
-            for (int k = 1; k < S; ++k) {
-                f.x += t[q][k].x; f.y += t[q][k].y; f.z += t[q][k].z; f.w += t[q][k].w;
-            }
-            const int grp = block / p.rblocks;
-            const size_t row = (size_t)grp * p.T + i;
-            uint64_t v[2] = {ptx::f2_pack(f.x, f.y), ptx::f2_pack(f.z, f.w)};
-            size_t out = row * p.N + col;
-            if (P == Dx) {
-                out = (((size_t)grp * p.H + col / p.dk) * p.T + i) * p.dk + col % p.dk;
-            } else {
-                ulonglong2 b = make_ulonglong2(0, 0);
-                if (p.bias) b = __ldg(reinterpret_cast<const ulonglong2 *>(p.bias + col));
-                if (P == FwdQ8) {
-                    const uint64_t xs = f2_both(p.x_scale[row]);
-                    const ulonglong2 w = __ldg(reinterpret_cast<const ulonglong2 *>(p.w_scale + col));
-                    v[0] = ptx::fma_f32x2(v[0], ptx::mul_f32x2(w.x, xs), b.x);
-                    v[1] = ptx::fma_f32x2(v[1], ptx::mul_f32x2(w.y, xs), b.y);
-                } else if (p.bias) {
-                    v[0] = ptx::add_f32x2(v[0], b.x);
-                    v[1] = ptx::add_f32x2(v[1], b.y);
-                }
-                if (p.z) *reinterpret_cast<uint2 *>(p.z + out) = pack_bf16x4(v);
-                activate(v, p.act);
-                if (p.residual) {
-                    const uint2 u = *reinterpret_cast<const uint2 *>(p.residual + out);
-                    v[0] = ptx::add_f32x2(v[0], ptx::f2_pack(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u)));
-                    v[1] = ptx::add_f32x2(v[1], ptx::f2_pack(__uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u)));
-                }
-            }
-            *reinterpret_cast<uint2 *>(p.y + out) = pack_bf16x4(v);
+    struct Row {
+        bool mine;
+        size_t out;
+        uint2 res;
+        float xs;
+    };
+    const bool one_group = p.n_rblocks == p.rblocks;
+    const int head = P == Dx ? col / p.dk : 0, in_head = P == Dx ? col - head * p.dk : 0;
+    auto ask = [&](int l) {
+        Row w{};
+        const int at = mt * TN + l * S + rank;
+        int grp = 0, i = at;
+        bool there = true;
+        if (!one_group) {
+            const int block = at / p.rb;
+            grp = block / p.rblocks;
+            i = (block - grp * p.rblocks) * p.rb + at % p.rb;
+            there = block < p.n_rblocks;
         }
+        w.mine = there && l < TN / S && i < p.T && col < p.N;
+        if (!w.mine) return w;
+        const size_t row = (size_t)grp * p.T + i;
+        w.out = P == Dx ? (((size_t)grp * p.H + head) * p.T + i) * p.dk + in_head : row * p.N + col;
+        if (P != Dx && p.residual) w.res = *reinterpret_cast<const uint2 *>(p.residual + w.out);
+        if (P == FwdQ8) w.xs = p.x_scale[row];
+        return w;
+    };
+    Row next = ask(warp);
+    ulonglong2 b = make_ulonglong2(0, 0), ws = b;
+    if (P != Dx && p.bias && col < p.N) b = __ldg(reinterpret_cast<const ulonglong2 *>(p.bias + col));
+    if (P == FwdQ8 && col < p.N) ws = __ldg(reinterpret_cast<const ulonglong2 *>(p.w_scale + col));
+    ptx::cluster_wait();
+    for (int l = warp; l < TN / S; l += 8) {
+        const Row w = next;
+        next = ask(l + 8);
+        if (!w.mine) continue;
+        ulonglong2 f = lds_f32x4(recv + l * 512 + lane * 16);
+#pragma unroll
+        for (int k = 1; k < S; ++k) {
+            const ulonglong2 t = lds_f32x4(recv + (k * (TN / S) + l) * 512 + lane * 16);
+            f.x = ptx::add_f32x2(f.x, t.x);
+            f.y = ptx::add_f32x2(f.y, t.y);
+        }
+        uint64_t v[2] = {f.x, f.y};
+        if (P != Dx) {
+            if (P == FwdQ8) {
+                const uint64_t xs = f2_both(w.xs);
+                v[0] = ptx::fma_f32x2(v[0], ptx::mul_f32x2(ws.x, xs), b.x);
+                v[1] = ptx::fma_f32x2(v[1], ptx::mul_f32x2(ws.y, xs), b.y);
+            } else if (p.bias) {
+                v[0] = ptx::add_f32x2(v[0], b.x);
+                v[1] = ptx::add_f32x2(v[1], b.y);
+            }
+            if (p.z) *reinterpret_cast<uint2 *>(p.z + w.out) = pack_bf16x4(v);
+            activate(v, p.act);
+            if (p.residual) {
+                v[0] = ptx::add_f32x2(v[0], ptx::f2_pack(__uint_as_float(w.res.x << 16), __uint_as_float(w.res.x & 0xffff0000u)));
+                v[1] = ptx::add_f32x2(v[1], ptx::f2_pack(__uint_as_float(w.res.y << 16), __uint_as_float(w.res.y & 0xffff0000u)));
+            }
+        }
+        *reinterpret_cast<uint2 *>(p.y + w.out) = pack_bf16x4(v);
     }
 }
 
@@ -632,7 +649,8 @@ __global__ void __launch_bounds__(256) gemm_split_kernel(const __grid_constant__
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    const uint32_t tmem = tmem_sh;
+    const uint32_t tmem = tmem_sh, recv = ptx::smem_u32(smem + STAGES * C::STAGE);
+    ptx::cluster_arrive();
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
 
@@ -703,53 +721,47 @@ __global__ void __launch_bounds__(256) gemm_split_kernel(const __grid_constant__
             wait_bounded(&bar_acc, 0, g);
         }
     } else if (warp >= 4) {
-        // the partial tile, [row][128 columns] fp32, over the stages: every copy has been consumed
-        const int quarter = warp & 3;
-        const uint32_t dst = ptx::smem_u32(smem) + (quarter * 32 + lane) * 4;
+        // the rows of the partial tile to their owners: row r to rank r mod splits as its row r / splits
+        const int quarter = warp & 3, log2s = 31 - __clz(splits);
+        const uint32_t mine = recv + ((uint32_t)(rank * (TN / splits)) * 128 + quarter * 32 + lane) * 4;
+        const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16);
+        // rows that there are (with several groups a tile may have gaps: all are sent)
+        const int valid = p.n_rblocks == p.rblocks ? min(TN, p.T - mt * TN) : TN;
         if (nk > 0) wait_bounded(&bar_acc, 0, g);
         ptx::tc_fence_after();
-        const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16);
-        if constexpr (TN == 16) {
-            uint32_t v[16] = {};
+        ptx::cluster_wait();   // every CTA of the cluster runs
+        constexpr int W = TN < 32 ? 16 : 32;   // columns read at a time
+#pragma unroll 1
+        for (int c = 0; c < valid; c += W) {
+            uint32_t v[W] = {};
             if (nk > 0) {
-                ptx::tmem_ld16(taddr, v);
+                if constexpr (W == 16)
+                    ptx::tmem_ld16(taddr + c, v);
+                else
+                    ptx::tmem_ld32(taddr + c, v);
                 ptx::tmem_ld_wait();
                 reg_fence(v);
             }
 #pragma unroll
-            for (int e = 0; e < 16; ++e) sts_f32(dst + e * 512, __uint_as_float(v[e]));
-        } else {
-            constexpr int W = TN < 64 ? 32 : 64;   // columns read at a time
-#pragma unroll 1
-            for (int c = 0; c < TN; c += W) {
-                uint32_t v[W] = {};
-                if (nk > 0) {
-                    ptx::tmem_ld32_at<0>(taddr + c, v);
-                    if constexpr (W == 64) ptx::tmem_ld32_at<32>(taddr + c + 32, v);
-                    ptx::tmem_ld_wait();
-                    reg_fence(v);
-                }
-#pragma unroll
-                for (int e = 0; e < W; ++e) sts_f32(dst + (c + e) * 512, __uint_as_float(v[e]));
-            }
+            for (int e = 0; e < W; ++e)
+                if (c + e < valid)
+                    ptx::st_cluster_b32(ptx::cluster_addr(mine + ((c + e) >> log2s) * 512, (c + e) & (splits - 1)), v[e]);
         }
         ptx::tc_fence_before();
     }
     __syncwarp();
-    __syncthreads();
-    ptx::cluster_sync();
+    if (warp < 4) ptx::cluster_wait();
+    ptx::cluster_arrive();   // this CTA's rows are sent
+    switch (splits) {        // (the wait for the others is in there)
+    case 1: join_rows<P, TN, 1>(p, recv, rank, mt, n0); break;
+    case 2: join_rows<P, TN, 2>(p, recv, rank, mt, n0); break;
+    case 4: join_rows<P, TN, 4>(p, recv, rank, mt, n0); break;
+    default: join_rows<P, TN, 8>(p, recv, rank, mt, n0); break;
+    }
     if (warp == 1) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, C::TM_COLS);
     }
-
-    switch (splits) {   // 16 loads in flight a lane
-    case 1: join_rows<P, TN, 1, 8>(p, smem, rank, mt, n0); break;
-    case 2: join_rows<P, TN, 2, 8>(p, smem, rank, mt, n0); break;
-    case 4: join_rows<P, TN, 4, 4>(p, smem, rank, mt, n0); break;
-    default: join_rows<P, TN, 8, 2>(p, smem, rank, mt, n0); break;
-    }
-    ptx::cluster_sync();   // the others may still read this CTA's partial tile
 }
 
 __device__ __forceinline__ void unpack_bf16x8(const uint4 &u, float (&f)[8])
@@ -877,26 +889,40 @@ struct SplitPlan {
     double us;   // estimated time
 };
 
-// The plan with the least estimated time, in us.  The terms are fitted to a sweep of every plan over
-// 1 to 2048 rows at K, N from 768 to 8192 (the chosen plan is within 15 % of the best one there):
-// start, join and end of the kernel; a K step, 0.21 (0.27 at 256 rows, whose product alone takes that)
-// or the step's bytes at L2's rate of 15 TB/s.
+// CTAs of the split kernel that the GPU holds at once: two an SM up to 64 rows, else one; clusters of
+// four and eight leave some of a GPC's SMs over (from cudaOccupancyMaxActiveClusters on a GB300).
+int split_slots(int tn, int s)
+{
+    if (tn <= 64) return s == 8 ? 288 : s == 4 ? 296 : 304;
+    return s == 8 ? 120 : s == 4 ? 144 : 152;
+}
+
+// The plan with the least estimated time, in us.  The terms are fitted to a sweep of every plan over 1
+// to 2048 rows at K, N from 768 to 8192 (the chosen plan takes 0.6 % more than the best one there on
+// average, 23 % at most): start, join and end; a K step 0.21, or what the ring of stages leaves of the memory's latency once all SMs
+// load, or the steps' bytes at L2's rate of 15 TB/s, or the weights at HBM's.
 SplitPlan split_plan(int G, int T, int N, int ksteps)
 {
     SplitPlan best{};
     best.us = 1e30;
     const long long M = (long long)G * T;
-    for (int tn = 16; tn <= 256; tn *= 2) {
+    for (int tn = 16; tn <= 128; tn *= 2) {
         const int rb = G > 1 && tn > 32 ? 32 : tn;
         const long long tiles = (long long)ceil_div((long long)ceil_div(T, rb) * G, tn / rb) * ceil_div(N, 128);
         if (tiles >= 0x7fffffff / 8) continue;
-        const int slots = (tn <= 64 ? 2 : 1) * 2 * kPlanPairs;
         for (int s = 1; s <= 8 && s <= ksteps; s *= 2) {
             const long long ctas = tiles * s;
-            if (ctas > slots) break;   // all at once, or not at all
-            const double bytes = (double)ctas * (16384 + tn * 128) / 15e6, step = tn == 256 ? 0.27 : 0.21;
-            const double us = 4.4 + tn * (0.018 + 0.024 / s) + (ctas > 2 * kPlanPairs ? 0.9 : 0.0) +
-                              ceil_div(ksteps, s) * (bytes > step ? bytes : step);
+            if (ctas > split_slots(tn, s)) break;   // all at once, or not at all
+            const int steps = ceil_div(ksteps, s);
+            const bool two = ctas > 2 * kPlanPairs;   // on some SMs
+            const int stages = tn == 64 ? 3 : tn == 32 ? 4 : 5;
+            const double ring = 1.4 / stages * (ctas < 2 * kPlanPairs ? ctas / (2.0 * kPlanPairs) : 1.0);
+            const double l2 = (double)steps * ctas * (16384 + tn * 128) / 15e6;
+            const double hbm = (double)ksteps * 128 * N / (two ? 6.2e6 : 5.6e6);
+            double loop = steps * (ring > 0.21 ? ring : 0.21);
+            loop = loop > l2 ? loop : l2;
+            loop = loop > hbm ? loop : hbm;
+            const double us = 2.9 + tn * (0.024 + 0.047 / (s * s)) + (two ? 0.35 : 0.0) + loop;
             if (us < best.us) best = SplitPlan{tn, s, (int)tiles, us};
         }
         if (tn >= M) break;
@@ -914,8 +940,7 @@ cudaError_t launch_split(const CUtensorMap &w, const CUtensorMap &x, SplitParams
     case 16: return launch_split_tn<P, 16>(w, x, p, s.tiles, s.splits, stream);
     case 32: return launch_split_tn<P, 32>(w, x, p, s.tiles, s.splits, stream);
     case 64: return launch_split_tn<P, 64>(w, x, p, s.tiles, s.splits, stream);
-    case 128: return launch_split_tn<P, 128>(w, x, p, s.tiles, s.splits, stream);
-    default: return launch_split_tn<P, 256>(w, x, p, s.tiles, s.splits, stream);
+    default: return launch_split_tn<P, 128>(w, x, p, s.tiles, s.splits, stream);
     }
 }
 
@@ -963,12 +988,12 @@ struct PairPlan {
     double us;
 };
 
-constexpr double kStepWide = 0.29, kStepNarrow = 0.22;   // us a K step (the sweep of split_plan)
+constexpr double kStepWide = 0.285, kStepNarrow = 0.205;   // us a K step (the sweep of split_plan)
 
 PairPlan pair_plan(long long mtiles, int N, int ksteps)
 {
     auto rounds = [&](int bn) { return (double)((mtiles * ceil_div(N, bn) + kPlanPairs - 1) / kPlanPairs); };
-    const double w = 6.0 + rounds(256) * ksteps * kStepWide, n = 5.0 + rounds(128) * ksteps * kStepNarrow;
+    const double w = 5.5 + rounds(256) * ksteps * kStepWide, n = 4.8 + rounds(128) * ksteps * kStepNarrow;
     return w <= n ? PairPlan{true, w} : PairPlan{false, n};
 }
 
