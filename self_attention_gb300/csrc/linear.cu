@@ -269,10 +269,9 @@ __global__ void __launch_bounds__(128 + 32 * kEpiWarps, 1)
                     }
                 }
             }
-            // both CTAs' copies have landed before either leaves: the last turn of every stage (a stage
-            // that had none yet passes at once)
-            if (rank == 0)
-                for (int q = 0; q < STAGES; ++q) wait_bounded(&bar_full[q], q < s ? ph : ph ^ 1, g);
+            // The last turn of every stage has been consumed (a stage that had none passes at once): no copy
+            // is in flight, and no arrival on this CTA's barriers, when it leaves.
+            for (int q = 0; q < STAGES; ++q) wait_bounded_cluster(&bar_empty[q], q < s ? ph : ph ^ 1, g);
         }
     } else if (warp == 1 && rank == 0) {
         if (ptx::elect_one()) {
