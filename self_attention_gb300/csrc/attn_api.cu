@@ -862,7 +862,7 @@ LinBwdLayout lin_bwd_layout(int G, int T, int M, int K, int N, int act)
     LinBwdLayout l;
     l.dz_off = 0;
     l.col_off = act != ATTN_ACT_NONE ? align256((size_t)M * N * 2) : 0;
-    l.dw_off = l.col_off + align256((size_t)lin_bwd_row_blocks(M, N) * N * 4);
+    l.dw_off = l.col_off + align256((size_t)lin_bwd_col_rows(M, N) * N * 4);
     const int splits = lin_dw_splits(G, T, K, N);
     l.total = l.dw_off + (splits > 1 ? align256((size_t)splits * K * N * 4) : 0);
     return l;

@@ -123,16 +123,16 @@ struct LinBwdArgs {
     void *dx, *dw;                   // bf16, each may be null
     float *dbias;                    // null, or [N]
     void *dz;                        // workspace: [M,N] bf16 (z given)
-    float *col_part;                 // workspace: partial column sums, lin_bwd_row_blocks() x [N]
+    float *col_part;                 // workspace: partial column sums, lin_bwd_col_rows() x [N]
     float *dw_part;                  // workspace: lin_dw_splits() x [K,N] where that is > 1
     int G, T, H, dk;
     int M, K, N;
     int act;
     int *status;
 };
-// The plan of the backward, a function of the sizes alone: how many blocks of rows the column
-// sums are taken in, and how many ways the rows of dw = x^T dz are split.
-int lin_bwd_row_blocks(int M, int N);
+// The plan of the backward, a function of the sizes alone: how many partial column sums there are at
+// most, and how many ways the rows of dw = x^T dz are split.
+int lin_bwd_col_rows(int M, int N);
 int lin_dw_splits(int G, int T, int K, int N);
 cudaError_t launch_linear_bwd(const LinBwdArgs &a, cudaStream_t stream);
 

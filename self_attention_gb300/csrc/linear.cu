@@ -55,11 +55,14 @@ struct GemmParams {
     const float *bias, *x_scale, *w_scale;
     int has_z, has_r, act;
     // Bwd: items of dx each cluster takes, and how many more those from a_clusters on take first; whether
-    // y2 maps [splits][rows][N] fp32 partial sums; the column sums to finish (col_rows partial rows)
+    // y2 maps [splits][rows][N] fp32 partial sums
     int x_all, x_early, a_clusters, part;
-    const float *col_part;
-    float *dbias;
+    // Bwd, the bias gradient: either col_rows partial rows to add up into dbias, or (sum_x) rows of dy to
+    // add up, per_slice at a time, into `slices` partial rows
+    float *col_part, *dbias;
     int col_rows, col_n;
+    const __nv_bfloat16 *sum_x;
+    int sum_m, per_slice, slices;
     int *status;
 };
 
@@ -83,6 +86,16 @@ __device__ __forceinline__ uint64_t desc_k(uint32_t base, int kk) { return ptx::
 __device__ __forceinline__ uint64_t desc_mn(uint32_t base, int kk)
 {
     return ptx::sdesc_sw128(base + kk * 2048, 8192, 1024);
+}
+
+__device__ __forceinline__ void unpack_bf16x8(const uint4 &u, float (&f)[8])
+{
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        f[2 * e] = __uint_as_float(w[e] << 16);
+        f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+    }
 }
 
 // Four pairs of fp32 -> eight bf16, rounded to nearest even.
@@ -488,13 +501,39 @@ __global__ void __launch_bounds__(128 + 32 * kEpiWarps, 1)
         }
         if (lane == 0) ptx::bulk_wait_group<0>();   // complete before the CTA exits
     } else if (P == Bwd && warp >= 2) {
-        // the bias gradient: its partial sums (see dz_kernel) added up by the two warps that have no
-        // other work, 32 columns a warp, while the products run
-        for (int c = (blockIdx.x * 2 + warp - 2) * 32 + lane; c < p.col_n; c += gridDim.x * 64) {
-            float s = 0.f;
+        // the bias gradient, by the two warps that have no other work, while the products run
+        const int first = blockIdx.x * 2 + warp - 2, warps = gridDim.x * 2;
+        if (p.sum_x) {   // dz is dy: sums over slices of its rows, 8 columns a lane, 16 rows in flight
+            for (int sl = first; sl < p.slices; sl += warps) {
+                const long long m0 = (long long)sl * p.per_slice, m1 = min((long long)p.sum_m, m0 + p.per_slice);
+                for (int n = lane * 8; n < p.col_n; n += 256) {
+                    float s[8] = {};
+                    for (long long m = m0; m < m1; m += 16) {
+                        uint4 v[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            v[k] = m + k < m1 ? __ldg(reinterpret_cast<const uint4 *>(p.sum_x + (size_t)(m + k) * p.col_n + n))
+                                              : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            float f[8];
+                            unpack_bf16x8(v[k], f);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) s[e] += f[e];
+                        }
+                    }
+                    float4 *dst = reinterpret_cast<float4 *>(p.col_part + (size_t)sl * p.col_n + n);
+                    dst[0] = make_float4(s[0], s[1], s[2], s[3]);
+                    dst[1] = make_float4(s[4], s[5], s[6], s[7]);
+                }
+            }
+        } else {   // the partial sums of dz_kernel, 32 columns a warp
+            for (int c = first * 32 + lane; c < p.col_n; c += warps * 32) {
+                float s = 0.f;
 #pragma unroll 16
-            for (int r = 0; r < p.col_rows; ++r) s += p.col_part[(size_t)r * p.col_n + c];
-            p.dbias[c] = s;
+                for (int r = 0; r < p.col_rows; ++r) s += p.col_part[(size_t)r * p.col_n + c];
+                p.dbias[c] = s;
+            }
         }
     }
     __syncwarp();
@@ -763,16 +802,6 @@ __global__ void __launch_bounds__(256) gemm_split_kernel(const __grid_constant__
     }
 }
 
-__device__ __forceinline__ void unpack_bf16x8(const uint4 &u, float (&f)[8])
-{
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        f[2 * e] = __uint_as_float(w[e] << 16);
-        f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-    }
-}
-
 // dz = dy act'(z) in bf16, and the column sums of the unrounded dz over a block of rows.  A warp
 // takes a row's 256 columns at a time (8 a thread, 16 bytes), the block's 8 warps neighbouring rows.
 __global__ void __launch_bounds__(256) dz_kernel(const LinBwdArgs a, int blocks)
@@ -825,12 +854,32 @@ __global__ void __launch_bounds__(256) dz_kernel(const LinBwdArgs a, int blocks)
     a.col_part[(size_t)blockIdx.y * a.N + c] = t;
 }
 
-// dw = the sum of the partial sums, in order, rounded once; 4 elements a thread.
-__global__ void __launch_bounds__(256) dw_join_kernel(const float *part, void *dw, int splits, long long elems)
+// What is left after the products: dw = the sum of its partial sums, in order, rounded once, 4 elements a
+// thread, in the first `dw_blocks` blocks; the bias gradient's partial sums, 32 columns a block, in the
+// others.
+__global__ void __launch_bounds__(256) bwd_join_kernel(const float *part, void *dw, int splits, long long elems,
+                                                       int dw_blocks, const float *col_part, float *dbias, int slices,
+                                                       int N)
 {
-    const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 4;
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
+    if ((int)blockIdx.x >= dw_blocks) {
+        __shared__ float sums[8][32];
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = (blockIdx.x - dw_blocks) * 32 + lane;
+        float s = 0.f;
+        if (c < N)
+#pragma unroll 8
+            for (int r = warp; r < slices; r += 8) s += col_part[(size_t)r * N + c];
+        sums[warp][lane] = s;
+        __syncthreads();
+        if (warp == 0 && c < N) {
+#pragma unroll
+            for (int w = 1; w < 8; ++w) s += sums[w][lane];
+            dbias[c] = s;
+        }
+        return;
+    }
+    const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 4;
     if (i >= elems) return;
     float4 s = *reinterpret_cast<const float4 *>(part + i);
     for (int k = 1; k < splits; ++k) {
@@ -1119,7 +1168,7 @@ cudaError_t launch_linear(const LinArgs &a, cudaStream_t stream)
 
 // Blocks of rows of the column sums: four blocks of threads an SM, at least 16 rows each, and no more
 // than two warps of each CTA can add up behind the products.
-int lin_bwd_row_blocks(int M, int N)
+static int lin_bwd_row_blocks(int M, int N)
 {
     const int strips = ceil_div(N, 256);
     int b = ceil_div(8 * kPlanPairs, strips);
@@ -1128,13 +1177,31 @@ int lin_bwd_row_blocks(int M, int N)
     return b > 1 ? b : 1;
 }
 
+// Slices of rows of the same sums where dz is dy: one for each of the warps that take them beside the
+// products, at least 16 rows each.
+int lin_bwd_slices(int M)
+{
+    const int most = ceil_div(M, 16);
+    return most < 4 * kPlanPairs ? (most > 1 ? most : 1) : 4 * kPlanPairs;
+}
+
+int lin_bwd_col_rows(int M, int N)
+{
+    const int b = lin_bwd_row_blocks(M, N), s = lin_bwd_slices(M);
+    return b > s ? b : s;
+}
+
 int lin_dw_splits(int G, int T, int K, int N) { return T > 0 ? bwd_plan(G, T, K, N).splits : 1; }
 
 cudaError_t launch_linear_bwd(const LinBwdArgs &a, cudaStream_t stream)
 {
     cudaError_t e = cudaSuccess;
     const int blocks = lin_bwd_row_blocks(a.M, a.N);
-    if (a.dbias || (a.z && (a.dx || a.dw))) {
+    // Where dz is dy and dw is taken, the two idle warps of the product kernel's CTAs read dy for the bias
+    // gradient: that costs nothing while the products take longer, from K of about 450 on (16 KB in
+    // flight a CTA against 4 K flops an element); else a pass of its own.
+    const bool beside = a.dbias && !a.z && a.dw && a.K >= 512;
+    if ((a.dbias && !beside) || (a.z && (a.dx || a.dw))) {
         e = launch_overlapped(dz_kernel, dim3(ceil_div(a.N, 256), blocks), 256, 0, 1, stream, a, blocks);
         if (e != cudaSuccess) return e;
     }
@@ -1200,14 +1267,22 @@ cudaError_t launch_linear_bwd(const LinBwdArgs &a, cudaStream_t stream)
         p.dbias = a.dbias;
         p.col_rows = blocks;
         p.col_n = a.N;
+        if (beside) {
+            p.sum_x = static_cast<const __nv_bfloat16 *>(a.dy);
+            p.sum_m = a.M;
+            p.slices = lin_bwd_slices(a.M);
+            p.per_slice = ceil_div(a.M, p.slices);
+        }
     }
     const long long items = (long long)p.q[0].n_items + p.q[1].n_items;
     const int pairs = device_sm_count() / 2, clusters = items < pairs ? (int)items : pairs;
     level_items(p, clusters);
     e = plan.wide ? launch_pair<Bwd, 256>(m, p, clusters, stream) : launch_pair<Bwd, 128>(m, p, clusters, stream);
-    if (e == cudaSuccess && p.part) {
-        const long long elems = (long long)a.K * a.N;
-        e = launch_overlapped(dw_join_kernel, ceil_div(elems, 1024), 256, 0, 1, stream, a.dw_part, a.dw, plan.splits, elems);
+    if (e == cudaSuccess && (p.part || beside)) {
+        const long long elems = p.part ? (long long)a.K * a.N : 0;
+        const int dw_blocks = ceil_div(elems, 1024), sum_blocks = beside ? ceil_div(a.N, 32) : 0;
+        e = launch_overlapped(bwd_join_kernel, dw_blocks + sum_blocks, 256, 0, 1, stream, (const float *)a.dw_part, a.dw,
+                              plan.splits, elems, dw_blocks, (const float *)a.col_part, a.dbias, p.slices, a.N);
     }
     return e;
 }
