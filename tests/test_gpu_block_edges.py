@@ -161,6 +161,22 @@ def test_streams_and_host_threads_at_once():
     assert not wrong and sa.attn_get_device_status() == 0
 
 
+def test_streams_by_handle():
+    """A stream may be given as a torch stream or as its handle, the default stream's 0 included."""
+    g = _gen("handles")
+    x, w = _randn(g, 33, 64), _randn(g, 64, 72)
+    one, want = torch.ones(64, device="cuda"), sa.linear_forward(x, w)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for st in (0, side.cuda_stream, side, torch.cuda.current_stream()):
+        y = sa.linear_forward(x, w, stream=st)
+        n, _, _ = sa.rms_norm_forward(x, one, stream=st)
+        q, s = sa.quantize_q8(x, stream=st)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+        assert torch.equal(n, sa.rms_norm_forward(x, one)[0]) and torch.equal(s, sa.quantize_q8(x)[1])
+
+
 def test_no_second_derivative():
     x, w = (torch.ones(8, 8, dtype=torch.bfloat16, device="cuda", requires_grad=True) for _ in range(2))
     y = sa.linear(x, w, None, None, "gelu")
