@@ -86,6 +86,8 @@ struct Cfg {
     static constexpr int EPI = kEpiWarps * 4096;           // a 32 x 64 bf16 buffer for each epilogue warp
     static constexpr int SMEM = STAGES * STAGE + EPI + 1024;
     static constexpr uint32_t TM_COLS = 2 * BN;
+    // The epilogue warps that take an item: with 128 columns half of them, the other half the next item.
+    static constexpr int TAKERS = kEpiWarps * BN / 256;
 };
 
 // K-major rows of 128 bytes: the k-th 32-byte slice starts 32 bytes in.
@@ -183,7 +185,7 @@ __global__ void __launch_bounds__(128 + 32 * kEpiWarps, 1)
         }
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(&bar_acc_full[b], 1);
-            ptx::mbar_init(&bar_acc_empty[b], 2 * kEpiWarps);   // the epilogue warps of both CTAs
+            ptx::mbar_init(&bar_acc_empty[b], 2 * C::TAKERS);   // the epilogue warps of both CTAs
         }
         for (int b = 0; b < kEpiWarps; ++b) ptx::mbar_init(&bar_res[b], 1);
         ptx::fence_mbar_init();
@@ -333,7 +335,8 @@ __global__ void __launch_bounds__(128 + 32 * kEpiWarps, 1)
             }
         }
     } else if (warp >= 4) {
-        const int quarter = warp & 3, set = (warp - 4) >> 2, ew = warp - 4;
+        // sets of four warps: with 256 columns a set takes 64 of every item, with 128 of every second one
+        const int quarter = warp & 3, ew = warp - 4, set = (ew >> 2) % (BN / 64), turn = (ew >> 2) / (BN / 64);
         uint8_t *buf = smem + STAGES * C::STAGE + ew * 4096;
         uint64_t *rbar = bar_res + ew;
         uint32_t rphase = 0;
@@ -341,6 +344,7 @@ __global__ void __launch_bounds__(128 + 32 * kEpiWarps, 1)
         const uint32_t empty0 = ptx::cluster_addr(ptx::smem_u32(&bar_acc_empty[0]), 0);
         int w, item;
         for (int li = 0; item_at(li, w, item); ++li) {
+            if (BN == 128 && (li & 1) != turn) continue;   // (and so the same accumulator every time)
             const Prob &pr = p.q[P == Bwd ? w : 0];
             int ks, mt, nt, k_begin, nk;
             decode(pr, item, ks, mt, nt, k_begin, nk);
@@ -348,7 +352,7 @@ __global__ void __launch_bounds__(128 + 32 * kEpiWarps, 1)
             const int first = mt * BM + (int)rank * 128 + quarter * 32, block = first / pr.rb;
             const int grp = block / pr.rblocks, i0 = block % pr.rblocks * pr.rb + first % pr.rb;
             const int col0 = nt * BN + set * 64;
-            const bool mine = set * 64 < BN && col0 < pr.N && i0 < pr.T && block < pr.n_rblocks;
+            const bool mine = col0 < pr.N && i0 < pr.T && block < pr.n_rblocks;
             // The residual of the warp's 64 columns, or (beside z) of 32 of them behind the half for z.
             auto load_res = [&](int half) {
                 ptx::mbar_arrive_expect_tx(rbar, p.has_z ? 2048 : 4096);
