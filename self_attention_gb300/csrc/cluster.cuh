@@ -122,24 +122,12 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
 }
 
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
+// Arrives on a barrier of any CTA of the cluster.  The release is the CTA's: one of cluster scope waits for
+// the thread's earlier stores (0.6 us an epilogue), and what these arrivals report, reads of tensor memory
+// and consumed stages, is ordered by the tcgen05 fences.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t bar)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n"
-        " .reg .pred p;\n"
-        " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-        " selp.b32 %0, 1, 0, p;\n"
-        "}\n"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ uint32_t cluster_size()
@@ -167,22 +155,6 @@ __device__ __forceinline__ ulonglong2 lds_f32x4(uint32_t addr)
     ulonglong2 v;
     asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(v.x), "=l"(v.y) : "r"(addr) : "memory");
     return v;
-}
-
-// wait_bounded() for a barrier on which another CTA of the cluster arrives too.
-__device__ __forceinline__ bool wait_bounded_cluster(uint64_t *bar, uint32_t parity, const Guard &g)
-{
-    if (ptx::mbar_try_wait_cluster(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    while (true) {
-        if (ptx::mbar_try_wait_cluster(bar, parity)) return true;
-        if (*(volatile int *)g.abort_smem) return false;
-        if (globaltimer_ns() - t0 > g.limit_ns) {
-            *(volatile int *)g.abort_smem = 1;
-            atomicCAS(g.status, 0, kStatusTimeout);
-            return false;
-        }
-    }
 }
 
 }  // namespace attn

@@ -42,6 +42,21 @@ constexpr int BM = 256;            // rows of a tile (both CTAs)
 constexpr int kEpiWarps = 16;      // four for each 32 rows of a CTA, each with 64 of 256 columns
 constexpr int kGroupM = 8;         // row tiles walked side by side, for reuse of B in L2
 
+// n / d for 0 <= n < 2^31 by a multiplication (the epilogue warps decode an item in their critical path,
+// where each integer division takes 0.1 us): q = (hi(n m) + n) >> s with s = ceil(log2 d) and
+// m = floor(2^32 (2^s - d) / d) + 1.
+struct FastDiv {
+    unsigned m, s, d;
+    __device__ int div(int n) const { return (int)((__umulhi((unsigned)n, m) + (unsigned)n) >> s); }
+};
+
+FastDiv fast_div(int d)
+{
+    unsigned s = 0;
+    while ((1ull << s) < (unsigned long long)d) ++s;
+    return FastDiv{(unsigned)(((1ull << 32) * ((1ull << s) - d)) / d + 1), s, (unsigned)d};
+}
+
 struct GemmMaps {
     CUtensorMap a, b, y;       // Fwd, FwdQ8; Bwd: of dx
     CUtensorMap a2, b2, y2;    // Bwd: of dw; Fwd, FwdQ8: a2 the residual, y2 z
@@ -50,8 +65,10 @@ struct GemmMaps {
 // One product: rows in groups, tiles, steps.
 struct Prob {
     int T;                         // rows of one group
-    int rb, rblocks, n_rblocks;    // rows of a row block, row blocks of one group and of all
+    int rb_log2, n_rblocks;        // rows of a row block, row blocks of all groups
+    FastDiv rblocks;               // row blocks of one group
     int n_mtiles, n_ntiles, N;     // row tiles, column tiles, columns
+    FastDiv tiles, per_group;      // tiles of a K split, of kGroupM row tiles
     int dk, H;                     // the head split of the side that has one (A; dx: y)
     int ksteps, steps_per_split;   // K steps in all and per item
     int tblocks, T_k;              // dw: steps and rows of one group
@@ -166,14 +183,23 @@ __global__ void __launch_bounds__(128 + 32 * kEpiWarps, 1)
     };
     // item -> K range, row tile, column tile: kGroupM row tiles side by side, column by column
     auto decode = [&](const Prob &q, int item, int &ks, int &mt, int &nt, int &k_begin, int &nk) {
-        const int tiles = q.n_mtiles * q.n_ntiles;
-        ks = item / tiles;
-        const int t = item - ks * tiles, per = kGroupM * q.n_ntiles, first = t / per * kGroupM, r = t % per;
-        const int rows = min(kGroupM, q.n_mtiles - first);
-        mt = first + r % rows;
-        nt = r / rows;
+        ks = q.tiles.div(item);
+        const int t = item - ks * (int)q.tiles.d, group = q.per_group.div(t);
+        const int first = group * kGroupM, r = t - group * (int)q.per_group.d, rows = q.n_mtiles - first;
+        if (rows >= kGroupM) {
+            nt = r / kGroupM;
+            mt = first + r % kGroupM;
+        } else {   // the last, smaller group
+            nt = r / rows;
+            mt = first + r - nt * rows;
+        }
         k_begin = ks * q.steps_per_split;
         nk = min(q.steps_per_split, q.ksteps - k_begin);
+    };
+    // row block -> group, first row
+    auto locate = [&](const Prob &q, int block, int &grp, int &row) {
+        grp = q.rblocks.div(block);
+        row = (block - grp * (int)q.rblocks.d) << q.rb_log2;
     };
     const Guard g{&abort_sh, p.status, kWaitLimitNs};
 
@@ -219,13 +245,10 @@ __global__ void __launch_bounds__(128 + 32 * kEpiWarps, 1)
                 int ks, mt, nt, k_begin, nk;
                 decode(pr, item, ks, mt, nt, k_begin, nk);
                 // this CTA's 128 rows: one block of 128, or four of 32 that may lie in different groups
-                const int per_cta = 128 / pr.rb, block0 = (mt * 2 + (int)rank) * per_cta;
+                const int per_cta = 128 >> pr.rb_log2, block0 = (mt * 2 + (int)rank) * per_cta;
                 int grp[4], i0[4];
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    grp[h] = (block0 + h) / pr.rblocks;
-                    i0[h] = (block0 + h) % pr.rblocks * pr.rb;
-                }
+                for (int h = 0; h < 4; ++h) locate(pr, block0 + h, grp[h], i0[h]);
                 const int n0 = nt * BN + (int)rank * (BN / 2);
                 // K is walked without divisions, which would take this one thread longer than a step
                 auto turn = [&] {   // the next stage is free; both CTAs' copies complete on the even one's barrier
@@ -294,7 +317,7 @@ __global__ void __launch_bounds__(128 + 32 * kEpiWarps, 1)
             }
             // The last turn of every stage has been consumed (a stage that had none passes at once): no copy
             // is in flight, and no arrival on this CTA's barriers, when it leaves.
-            for (int q = 0; q < STAGES; ++q) wait_bounded_cluster(&bar_empty[q], q < s ? ph : ph ^ 1, g);
+            for (int q = 0; q < STAGES; ++q) wait_bounded(&bar_empty[q], q < s ? ph : ph ^ 1, g);
         }
     } else if (warp == 1 && rank == 0) {
         if (ptx::elect_one()) {
@@ -309,10 +332,10 @@ __global__ void __launch_bounds__(128 + 32 * kEpiWarps, 1)
                 const uint32_t idesc = C::FP8 ? ptx::idesc_f16_f32(BM, BN, false, false)   // format 0: e4m3
                                               : ptx::idesc_bf16_f32(BM, BN, a_mn, b_mn);
                 const int ab = li & 1;
-                wait_bounded_cluster(&bar_acc_empty[ab], ((li >> 1) & 1) ^ 1, g);   // epilogues of item li-2 done
+                wait_bounded(&bar_acc_empty[ab], ((li >> 1) & 1) ^ 1, g);   // epilogues of item li-2 done
                 ptx::tc_fence_after();
                 for (int q = 0; q < nk; ++q) {
-                    wait_bounded_cluster(&bar_full[s], ph, g);
+                    wait_bounded(&bar_full[s], ph, g);
                     ptx::tc_fence_after();
                     const uint32_t sa = base + s * C::STAGE, sb = sa + C::A_BYTES;
 #pragma unroll
@@ -349,8 +372,10 @@ __global__ void __launch_bounds__(128 + 32 * kEpiWarps, 1)
             int ks, mt, nt, k_begin, nk;
             decode(pr, item, ks, mt, nt, k_begin, nk);
             const int ab = li & 1;
-            const int first = mt * BM + (int)rank * 128 + quarter * 32, block = first / pr.rb;
-            const int grp = block / pr.rblocks, i0 = block % pr.rblocks * pr.rb + first % pr.rb;
+            const int first = mt * BM + (int)rank * 128 + quarter * 32, block = first >> pr.rb_log2;
+            int grp, i0;
+            locate(pr, block, grp, i0);
+            i0 += first & ((1 << pr.rb_log2) - 1);
             const int col0 = nt * BN + set * 64;
             const bool mine = col0 < pr.N && i0 < pr.T && block < pr.n_rblocks;
             // The residual of the warp's 64 columns, or (beside z) of 32 of them behind the half for z.
@@ -394,7 +419,7 @@ __global__ void __launch_bounds__(128 + 32 * kEpiWarps, 1)
             auto release = [&] {   // this warp has read its part of the accumulator
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive_cluster(empty0 + ab * 8);
+                if (lane == 0) ptx::mbar_arrive_remote(empty0 + ab * 8);
             };
             if (!mine) {
                 release();
@@ -506,8 +531,10 @@ __global__ void __launch_bounds__(128 + 32 * kEpiWarps, 1)
             }
             if (P == Bwd && w)
                 store(&maps.y2, col0, 0);
-            else if (P == Bwd)
-                store(&maps.y, col0 % pr.dk, grp * pr.H + col0 / pr.dk);
+            else if (P == Bwd) {
+                const int head = pr.H > 1 ? col0 >> (pr.dk == 64 ? 6 : 7) : 0;   // heads are 64 or 128 wide
+                store(&maps.y, col0 - head * pr.dk, grp * pr.H + head);
+            }
             else
                 store(&maps.y, col0, grp);
         }
@@ -1019,17 +1046,21 @@ long long row_tiles(int G, int T)
 // Fills in the rows and the tiles; false if there are too many to count in an int.
 bool set_tiles(Prob &q, int G, int T, int N, int bn, int splits)
 {
+    const int rb = row_block(G), rblocks = ceil_div(T, rb);
+    const long long mtiles = row_tiles(G, T), tiles = mtiles * ceil_div(N, bn);
+    // the kernel counts rows, those that pad a block included, and items in ints
+    if (mtiles * BM > 0x7fffffffLL || tiles * splits > 0x7fffffffLL) return false;
     q.T = T;
-    q.rb = row_block(G);
-    q.rblocks = ceil_div(T, q.rb);
-    q.n_rblocks = q.rblocks * G;
-    q.n_mtiles = (int)row_tiles(G, T);
+    q.rb_log2 = rb == 32 ? 5 : 7;
+    q.rblocks = fast_div(rblocks);
+    q.n_rblocks = rblocks * G;
+    q.n_mtiles = (int)mtiles;
     q.N = N;
     q.n_ntiles = ceil_div(N, bn);
-    const long long items = (long long)q.n_mtiles * q.n_ntiles * splits;
-    q.n_items = (int)items;
-    // the kernel counts rows, those that pad a block included, and items in ints
-    return row_tiles(G, T) * BM <= 0x7fffffffLL && items <= 0x7fffffffLL;
+    q.tiles = fast_div((int)tiles);
+    q.per_group = fast_div(kGroupM * q.n_ntiles);
+    q.n_items = (int)(tiles * splits);
+    return true;
 }
 
 void set_split_rows(SplitParams &p, int G, int T, int tn)
@@ -1165,7 +1196,7 @@ cudaError_t launch_linear(const LinArgs &a, cudaStream_t stream)
         r = make_map_3d(&m.a, a.x, kU8, 1, a.K, a.M, 1, 128, 128);
         if (r == CUDA_SUCCESS) r = make_map_3d(&m.b, a.w, kU8, 1, a.K, a.N, 1, 128, bn / 2);
     } else {
-        r = make_map_3d(&m.a, a.x, kBf16, 2, a.dk, a.T, (long long)a.G * a.H, 64, q.rb);
+        r = make_map_3d(&m.a, a.x, kBf16, 2, a.dk, a.T, (long long)a.G * a.H, 64, 1 << q.rb_log2);
         if (r == CUDA_SUCCESS) r = make_map_3d(&m.b, a.w, kBf16, 2, a.N, a.K, 1, 64, 64);
     }
     const int oc = a.z ? 32 : 64;   // columns of a store (see the epilogue)
@@ -1254,7 +1285,7 @@ cudaError_t launch_linear_bwd(const LinBwdArgs &a, cudaStream_t stream)
         q.dk = a.dk;
         q.H = a.H;
         q.ksteps = q.steps_per_split = ksteps;
-        r = make_map_3d(&m.a, dz, kBf16, 2, a.N, a.T, a.G, 64, q.rb);
+        r = make_map_3d(&m.a, dz, kBf16, 2, a.N, a.T, a.G, 64, 1 << q.rb_log2);
         if (r == CUDA_SUCCESS) r = make_map_3d(&m.b, a.w, kBf16, 2, a.N, a.K, 1, 64, bn / 2);
         if (r == CUDA_SUCCESS) r = make_map_3d(&m.y, a.dx, kBf16, 2, a.dk, a.T, (long long)a.G * a.H, 64, 32);
     }
