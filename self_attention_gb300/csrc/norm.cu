@@ -407,19 +407,22 @@ cudaError_t launch_rms_norm(const NormArgs &a, cudaStream_t stream)
     return launch_overlapped(a.q8 ? rms_norm_long_kernel<true> : rms_norm_long_kernel<false>, a.M, 1024, 0, 1, stream, a);
 }
 
-// As many blocks as fit the SMs at once (see bwd_blocks_per_sm); no more than there are rows for.
+// As many blocks as fit the SMs at once (see bwd_blocks_per_sm); no more than there are rows for, and one
+// for up to two rows a holder: its sums are dweight itself, which saves the join.
 int norm_bwd_blocks(int M, int D)
 {
     const int rpb = D <= 2048 ? 8 : 1, span = D <= 2048 ? 256 : 2048, ch = D <= 16384 ? (D + span - 1) / span : 8;
     const int want = bwd_blocks_per_sm(ch) * kPlanSms;
     const int most = (int)(((long long)M + rpb - 1) / rpb);
     const int b = want < most ? want : most;
-    return b > 1 ? b : 1;
+    return b > 2 ? b : 1;
 }
 
-cudaError_t launch_rms_norm_bwd(const NormBwdArgs &a, cudaStream_t stream)
+cudaError_t launch_rms_norm_bwd(const NormBwdArgs &args, cudaStream_t stream)
 {
+    NormBwdArgs a = args;
     const int blocks = norm_bwd_blocks(a.M, a.D), D = a.D;
+    if (blocks == 1) a.part = a.dweight;
     const cudaError_t e = D <= 256     ? launch_norm_bwd<32, 1>(a, blocks, stream)
                           : D <= 512   ? launch_norm_bwd<32, 2>(a, blocks, stream)
                           : D <= 768   ? launch_norm_bwd<32, 3>(a, blocks, stream)
@@ -429,7 +432,7 @@ cudaError_t launch_rms_norm_bwd(const NormBwdArgs &a, cudaStream_t stream)
                           : D <= 8192  ? launch_norm_bwd<256, 4>(a, blocks, stream)
                           : D <= 16384 ? launch_norm_bwd<256, 8>(a, blocks, stream)
                                        : launch_overlapped(rms_norm_bwd_long_kernel, blocks, 1024, 0, 1, stream, a, blocks);
-    return e == cudaSuccess ? launch_sum_rows(a.part, a.dweight, blocks, D, stream) : e;
+    return e == cudaSuccess && blocks > 1 ? launch_sum_rows(a.part, a.dweight, blocks, D, stream) : e;
 }
 
 }  // namespace attn
