@@ -20,15 +20,16 @@
 // activation, residual in fp32, one rounding to bf16, a swizzled 4 KB buffer in shared memory, TMA
 // stores.  The residual comes the same way round, by a TMA load into that buffer before the accumulator
 // is ready.  Sixteen warps, since a warp's chain of loads, MUFU operations and stores is long: with
-// eight, GELU with z kept took 218 us instead of 197 at 32768 x 1024 x 4096.
+// eight, GELU with z kept took a tenth longer at 32768 x 1024 x 4096.
 //
 // What bounds it: the products and, over a second or more of them, the power limit (32768 rows, 1024 x
-// 4096: 163 us without an activation, 1.69 PFLOP/s, and 174 with GELU in short runs; 184 and 197 in long
-// ones at 1.5 to 1.6 GHz; 8192^3: 585 us, 1.88 PFLOP/s; e4m3 8192^3: 309 us, 3.56 PFLOP/s).  Shared
-// memory is nearly full too: operands written (64 B a cycle) and read (64), so each 64 KB that the
-// epilogue writes and reads back shows: z kept costs 25 us more.  Measured and not kept: copying the
-// buffers out by 128-byte lines instead of TMA (GELU 203, with z 237 us, against 199 and 226), storing z
-// straight from registers (242).
+// 4096, in long runs at 1.5 to 1.6 GHz: 177 us without an activation, 1.55 PFLOP/s, 191 with GELU, 215
+// with z kept as well, 194 in short runs; 8192^3 in short runs: 585 us, 1.88 PFLOP/s, e4m3 309 us, 3.56
+// PFLOP/s).  Shared memory is nearly full too: operands written (64 B a cycle) and read (64), so each 64
+// KB that the epilogue writes and reads back shows.  With short K the epilogue's own chain counts: 1.9
+// us a tile (32768 x 64 x 4096: 56 us, 4.9 TB/s).  Measured and not kept: copying the buffers out by
+// 128-byte lines instead of TMA (4 % slower with z kept, 2 % without), storing z straight from
+// registers (7 %).
 #include "act.cuh"
 #include "cluster.cuh"
 #include "kernels.h"
@@ -1091,8 +1092,7 @@ PairPlan pair_plan(long long mtiles, int N, int ksteps)
 
 // The backward runs both products in one launch, so that one's tiles fill the pairs that the other's
 // leave idle and there is one start and end (18432 rows, 768 x 768: 42 us apart, 33 together; 1111 rows,
-// 1000 x 520: 20 and 12; where both fill the GPU, 32768 rows, 1024 x 4096, the power limit makes it the
-// same).  dw has few tiles (K x N) and a long sum (the rows), which is split over items only where that
+// 1000 x 520: 20 and 12; 32768 rows, 1024 x 4096: 307 and 295, 1.86 PFLOP/s).  dw has few tiles (K x N) and a long sum (the rows), which is split over items only where that
 // still pays for the partial sums' join (2.5 us, 5 bytes/ps).  Times in K steps: an item's fill and drain
 // costs 2 for dx, 4 for dw.
 struct BwdPlan {
