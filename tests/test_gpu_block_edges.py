@@ -177,6 +177,14 @@ def test_streams_by_handle():
         assert torch.equal(n, sa.rms_norm_forward(x, one)[0]) and torch.equal(s, sa.quantize_q8(x)[1])
 
 
+def test_an_allocation_that_fails():
+    """An output of 1.1 TB: PyTorch's own error, and the next call works."""
+    x, w = torch.zeros(1 << 20, 8, dtype=torch.bfloat16, device="cuda"), torch.zeros(8, 524_288, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(torch.OutOfMemoryError):
+        sa.linear_forward(x, w)
+    assert not bool(sa.linear_forward(x[:3].contiguous(), w).any())
+
+
 def test_no_second_derivative():
     x, w = (torch.ones(8, 8, dtype=torch.bfloat16, device="cuda", requires_grad=True) for _ in range(2))
     y = sa.linear(x, w, None, None, "gelu")
