@@ -779,16 +779,18 @@ bool width_ok(long long w, int unit) { return w >= unit && w % unit == 0 && w < 
 
 bool size_ok(long long rows, long long width) { return rows * width < (1LL << 40); }
 
-// Alignment of the given pointers, and that no output range touches another output or an input;
-// `same` is an output that may be exactly the input `same_in`.  Null pointers are skipped.
+// Alignment of the given pointers, and that no output range touches another output or an input; the
+// output with index `over` may lie exactly over the inputs of the mask `over_ins`, whose elements the thread
+// that writes them has read (over those operands only: where one of them is another input as well, the
+// other refuses it).  Null pointers are skipped.
 struct Operand {
     const void *p;
     size_t bytes;
 };
 
 template <int NI, int NO>
-attn_status check_operands(const Operand (&ins)[NI], const Operand (&outs)[NO], const void *same = nullptr,
-                           const void *same_in = nullptr, const void *same_in2 = nullptr)
+attn_status check_operands(const Operand (&ins)[NI], const Operand (&outs)[NO], int over = -1,
+                           unsigned over_ins = 0)
 {
     for (const Operand &o : ins)
         if (o.p && !aligned16(o.p)) return ATTN_ERR_MISALIGNED;
@@ -797,9 +799,9 @@ attn_status check_operands(const Operand (&ins)[NI], const Operand (&outs)[NO], 
     for (int i = 0; i < NO; ++i) {
         if (!outs[i].p) continue;
         const Range r = span(outs[i].p, outs[i].bytes);
-        for (const Operand &o : ins) {
-            if (!o.p || !overlap(r, span(o.p, o.bytes))) continue;
-            if (outs[i].p == same && o.p == same && (o.p == same_in || o.p == same_in2)) continue;
+        for (int k = 0; k < NI; ++k) {
+            if (!ins[k].p || !overlap(r, span(ins[k].p, ins[k].bytes))) continue;
+            if (i == over && (over_ins >> k & 1) && ins[k].p == outs[i].p) continue;
             return ATTN_ERR_INVALID_ARG;
         }
         for (int j = i + 1; j < NO; ++j)
@@ -844,7 +846,7 @@ attn_status run_linear(LinArgs &a, cudaStream_t stream, const char *what)
     const Operand ins[6] = {{a.x, M * K * es}, {a.w, K * N * es}, {a.bias, N * 4}, {a.residual, M * N * 2},
                             {a.x_scale, M * 4}, {a.w_scale, N * 4}};
     const Operand outs[2] = {{a.y, M * N * 2}, {a.z, M * N * 2}};
-    attn_status st = check_operands(ins, outs, a.y, a.residual);
+    attn_status st = check_operands(ins, outs, 0, 1u << 3);   // y over the residual
     if (st != ATTN_OK) return st;
     DeviceState *dev = nullptr;
     if ((st = device_state(&dev)) != ATTN_OK) return st;
@@ -999,7 +1001,7 @@ attn_status run_norm(const NormArgs &a, cudaStream_t stream, const char *what)
     const size_t M = a.M, D = a.D;
     const Operand ins[3] = {{a.x, M * D * 2}, {a.residual, M * D * 2}, {a.weight, D * 4}};
     const Operand outs[4] = {{a.y, M * D * (a.q8 ? 1 : 2)}, {a.scale, M * 4}, {a.h, M * D * 2}, {a.rstd, M * 4}};
-    attn_status st = check_operands(ins, outs, a.h, a.x, a.residual);
+    attn_status st = check_operands(ins, outs, 2, 3u);   // h over x or the residual
     if (st != ATTN_OK) return st;
     DeviceState *dev = nullptr;
     if ((st = device_state(&dev)) != ATTN_OK) return st;
@@ -1064,7 +1066,7 @@ extern "C" attn_status attn_rms_norm_bwd(const void *dy, const void *h, const fl
         return ATTN_ERR_WORKSPACE;
     const Operand ins[5] = {{dy, m * d * 2}, {h, m * d * 2}, {weight, d * 4}, {rstd, m * 4}, {dh, m * d * 2}};
     const Operand outs[3] = {{dx, m * d * 2}, {dweight, d * 4}, {workspace, need}};
-    if ((st = check_operands(ins, outs, dx, dh)) != ATTN_OK) return st;
+    if ((st = check_operands(ins, outs, 0, 1u << 4)) != ATTN_OK) return st;   // dx over dh
     DeviceState *dev = nullptr;
     if ((st = device_state(&dev)) != ATTN_OK) return st;
     cudaError_t e;

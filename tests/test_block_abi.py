@@ -125,6 +125,21 @@ def test_rms_norm_argument_errors(lib):
     assert bwd(dx=X) == 1 and bwd(dx=RES + 16) == 1 and bwd(dw=W) == 1 and bwd(dx=WS) == 1
 
 
+def test_in_place_goes_by_operand(lib):
+    """Only the operand that an output may lie over excuses it: y over a residual that is x as well would
+    overwrite rows of x that other tiles still read."""
+    import ctypes
+    assert lib.attn_linear(X, W, BIAS, X, X, 0, 16, 64, 64, 0, None) == 1
+    assert lib.attn_linear(X, RES, BIAS, RES, RES, 0, 64, 64, 64, 0, None) == 1
+    assert lib.attn_out_proj(X, W, 0, X, X, 2, 2, 8, 64, 128, None) == 1
+    assert lib.attn_linear_q8(X, BIAS, X, RES, 0, X, X, 16, 64, 32, 0, None) == 1
+    f = ctypes.c_float(1e-6)
+    assert lib.attn_rms_norm(X, RES, X, Y, X, DB, 1, 64, f, None) == 1
+    need = sa.attn_rms_norm_bwd_workspace_size(16, 64)
+    assert lib.attn_rms_norm_bwd(DX, X, W, DB, DX, DX, DW, WS, need, 16, 64, None) == 1
+    assert lib.attn_rms_norm_bwd(Y, DX, W, DB, DX, DX, DW, WS, need, 16, 64, None) == 1
+
+
 @pytest.mark.parametrize("name", ref.ACTS)
 def test_slopes_against_differences(name):
     """act_slope is the slope of act: central differences, whose own error is the third derivative
