@@ -156,7 +156,12 @@ PyObject *entry(PyObject *, Args a, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
-bool flag(PyObject *o) { return PyObject_IsTrue(o) == 1; }
+bool flag(PyObject *o)
+{
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw Refused{};
+    return v == 1;
+}
 
 int integer(PyObject *o)
 {

@@ -217,3 +217,16 @@ def test_a_row_is_the_same_in_any_batch_of_its_plan():
         x2[1:], dy2[1:] = x2[1:] * 3, dy2[1:] * 3
         assert torch.equal(sa.linear_forward(x2, w)[0], y[0])
         assert torch.equal(sa.linear_backward(x2, w, dy2)[0][0], dx[0])
+
+
+def test_a_flag_without_a_truth_value():
+    """Its own error comes through, from before anything is launched."""
+    class NoTruth:
+        def __bool__(self):
+            raise KeyError("no truth value")
+
+    x, w = torch.zeros(4, 64, device="cuda", dtype=torch.bfloat16), torch.zeros(64, 32, device="cuda", dtype=torch.bfloat16)
+    with pytest.raises(KeyError):
+        sa.linear_forward(x, w, keep_z=NoTruth())
+    with pytest.raises(KeyError):
+        sa.linear_backward(x, w, torch.zeros(4, 32, device="cuda", dtype=torch.bfloat16), need_dw=NoTruth())
