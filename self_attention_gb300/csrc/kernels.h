@@ -4,6 +4,7 @@
 
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstdint>
 #include <cuda_bf16.h>
 
@@ -95,6 +96,19 @@ cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, dim3 block, size_
     cfg.attrs = attr;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Raises the kernel's shared-memory limit, once per device.
+inline cudaError_t raise_smem(const void *kernel, int bytes, std::atomic<bool> (&set)[64])
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (set[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) == cudaSuccess)
+        set[dev].store(true, std::memory_order_relaxed);
+    return e;
 }
 
 // 3-D tensor map (innermost first: d0, d1, d2 elements, dense) with boxes of box0 x box1 x 1 whose

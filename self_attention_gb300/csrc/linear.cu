@@ -34,8 +34,6 @@
 #include "cluster.cuh"
 #include "kernels.h"
 
-#include <atomic>
-
 namespace attn {
 namespace {
 
@@ -937,19 +935,6 @@ int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 // The pairs the plans are made for (a function of the sizes alone, so that results and workspaces
 // do not depend on where the plan is made): a GB300's 152 SMs.
 constexpr int kPlanPairs = 76;
-
-// Raises the kernel's shared-memory limit, once per device.
-cudaError_t raise_smem(const void *kernel, int bytes, std::atomic<bool> (&set)[64])
-{
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (set[dev].load(std::memory_order_relaxed)) return cudaSuccess;
-    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) == cudaSuccess)
-        set[dev].store(true, std::memory_order_relaxed);
-    return e;
-}
 
 template <Policy P, int BN>
 cudaError_t launch_pair(const GemmMaps &m, const GemmParams &p, int clusters, cudaStream_t stream)

@@ -5,8 +5,8 @@
 // by 1024 threads (to 32768), each thread holding chunks of 8 neighbouring columns (16-byte loads);
 // longer rows are read a second time from L2.  Measured on 128 to 470 MB in calls back to back: forward
 // 32768 x 1024 with residual 40.9 us (6.6 TB/s, 0.97 of the measured copy), to 8 bits 32768 x 2048 70.0
-// us (6.7 TB/s); backward 18432 x 768 26.2 us with the join of dweight's partial sums, 32768 x 1024 5.3
-// TB/s: its rows are taken one after another by the same warps, for dweight's sums.
+// us (6.7 TB/s); backward 32768 x 1024 47 us (5.7 TB/s), 18432 x 768 23.4 us with the join of dweight's
+// partial sums: its rows are taken one after another by the same warps, for those sums.
 #include "cluster.cuh"
 #include "kernels.h"
 
@@ -33,6 +33,12 @@ __device__ __forceinline__ void unpack8(const uint4 &u, float (&f)[8])
         f[2 * e] = __uint_as_float(w[e] << 16);
         f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
     }
+}
+
+// Two bf16 -> a pair of fp32.
+__device__ __forceinline__ uint64_t pair(uint32_t w)
+{
+    return ptx::f2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
 __device__ __forceinline__ uint4 pack8(const float (&f)[8])
@@ -218,23 +224,33 @@ __global__ void __launch_bounds__(1024) rms_norm_long_kernel(const NormArgs a)
 // dx and the partial sums of dweight: each row-holder (a warp, or the block) walks its rows, keeping
 // the sums of dy n for its columns in registers; the warps of a block then add theirs up in order.
 // The rows a block takes, and so the order of the sums, follow from the sizes alone.
-constexpr int bwd_blocks_per_sm(int ch) { return ch <= 1 ? 4 : ch <= 3 ? 3 : ch <= 4 ? 2 : 1; }
+// The SM's own work shows beside the memory's (L1's data pipe was 64 % busy, the schedulers 48 %), so the
+// weights lie in shared memory in two planes that are read without conflicts, and the arithmetic is on
+// pairs: 18432 x 768 25.5 -> 23.5 us, 2048 x 16384 72 -> 63.  Measured and not kept: the next rows on their
+// way to shared memory meanwhile (cp.async; 28.5 us, the data passes that pipe twice more), or to registers
+// (26.1).  Threads and blocks an SM are the most whose registers hold a row, the sums and four columns of
+// operands without spilling.
+__host__ __device__ constexpr int bwd_blocks_per_sm(int ch) { return ch <= 1 ? 4 : ch <= 2 ? 3 : ch <= 4 ? 2 : 1; }
+__host__ __device__ constexpr int bwd_threads(int tpr, int ch) { return tpr == 32 && ch == 3 ? 320 : 256; }
 
 template <int TPR, int CH>
-__global__ void __launch_bounds__(256, bwd_blocks_per_sm(CH)) rms_norm_bwd_kernel(const NormBwdArgs a, int blocks)
+__global__ void __launch_bounds__(bwd_threads(TPR, CH), bwd_blocks_per_sm(CH))
+    rms_norm_bwd_kernel(const NormBwdArgs a, int blocks)
 {
-    constexpr int RPB = TPR == 32 ? 8 : 1;   // row-holders a block
+    constexpr int THREADS = bwd_threads(TPR, CH), RPB = THREADS / TPR;   // row-holders a block
+    extern __shared__ __align__(16) float weights[];
     const int t = threadIdx.x % TPR, holder = threadIdx.x / TPR, nch = a.D / 8;
-    float acc[CH][8] = {};
-    ptx::grid_dep_launch();
-    ptx::grid_dep_wait();
-    for (long long m = (long long)blockIdx.x * RPB + holder; m < a.M; m += (long long)blocks * RPB) {
+    const long long step = (long long)blocks * RPB;
+    long long m = (long long)blockIdx.x * RPB + holder;
+    uint64_t acc[CH][4] = {};
+    uint4 dv[CH], hv[CH], gv[CH];
+    float r = 0.f;
+    auto load_row = [&] {   // everything the row needs is asked for at once
+        if (m >= a.M) return;
         const size_t row = (size_t)m * nch;
         const uint4 *dy = static_cast<const uint4 *>(a.dy) + row, *h = static_cast<const uint4 *>(a.h) + row,
                     *dh = static_cast<const uint4 *>(a.dh) + row;
-        // everything the row needs is asked for at once
-        uint4 dv[CH], hv[CH], gv[CH];
-        const float r = a.rstd[m];
+        r = a.rstd[m];
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             const int i = t + c * TPR;
@@ -244,40 +260,60 @@ __global__ void __launch_bounds__(256, bwd_blocks_per_sm(CH)) rms_norm_bwd_kerne
                 if (a.dh) gv[c] = dh[i];
             }
         }
-        float s = 0.f;
+    };
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
+    load_row();
+    // a chunk's 8 weights as two planes of 16 bytes a thread: read side by side, without conflicts
+    for (int i = threadIdx.x; i < a.D / 4; i += THREADS) {
+        const int chunk = i >> 1;
+        reinterpret_cast<float4 *>(weights)[(chunk / TPR * 2 + (i & 1)) * TPR + chunk % TPR] =
+            __ldg(reinterpret_cast<const float4 *>(a.weight) + i);
+    }
+    __syncthreads();
+    const uint32_t wt = ptx::smem_u32(weights) + t * 16;
+    for (; m < a.M; m += step, load_row()) {
+        uint64_t sum = 0;
+        const uint64_t rr = ptx::f2_pack(r, r);
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const int i = t + c * TPR;
-            if (i >= nch) continue;
-            float d[8], n[8], w[8];
-            unpack8(dv[c], d);
-            unpack8(hv[c], n);
-            load8(a.weight + i * 8, w);
+            if (t + c * TPR >= nch) continue;
+            const uint32_t dw[4] = {dv[c].x, dv[c].y, dv[c].z, dv[c].w}, hw[4] = {hv[c].x, hv[c].y, hv[c].z, hv[c].w};
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float p = d[e] * (n[e] * r);
-                acc[c][e] += p;
-                s = fmaf(p, w[e], s);
+            for (int q = 0; q < 2; ++q) {   // four columns
+                const ulonglong2 w4 = lds_f32x4(wt + (2 * c + q) * TPR * 16);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint64_t p = ptx::mul_f32x2(pair(dw[2 * q + e]), ptx::mul_f32x2(pair(hw[2 * q + e]), rr));
+                    acc[c][2 * q + e] = ptx::add_f32x2(acc[c][2 * q + e], p);
+                    sum = ptx::fma_f32x2(p, e ? w4.y : w4.x, sum);
+                }
             }
         }
-        s = row_reduce<TPR>(s, add) / (float)a.D;
+        float lo, hi;
+        ptx::f2_unpack(sum, lo, hi);
+        const float s = -row_reduce<TPR>(lo + hi, add) / (float)a.D;
+        const uint64_t ss = ptx::f2_pack(s, s);
+        uint4 *dx = static_cast<uint4 *>(a.dx) + (size_t)m * nch;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const int i = t + c * TPR;
-            if (i >= nch) continue;
-            float d[8], n[8], w[8], o[8];
-            unpack8(dv[c], d);
-            unpack8(hv[c], n);
-            load8(a.weight + i * 8, w);
+            if (t + c * TPR >= nch) continue;
+            const uint32_t dw[4] = {dv[c].x, dv[c].y, dv[c].z, dv[c].w}, hw[4] = {hv[c].x, hv[c].y, hv[c].z, hv[c].w},
+                           gw[4] = {gv[c].x, gv[c].y, gv[c].z, gv[c].w};
+            uint32_t o[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = r * fmaf(d[e], w[e], -(n[e] * r) * s);
-            if (a.dh) {
-                float g[8];
-                unpack8(gv[c], g);
+            for (int q = 0; q < 2; ++q) {
+                const ulonglong2 w4 = lds_f32x4(wt + (2 * c + q) * TPR * 16);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] += g[e];
+                for (int e = 0; e < 2; ++e) {
+                    const int k = 2 * q + e;
+                    const uint64_t v = ptx::fma_f32x2(pair(dw[k]), e ? w4.y : w4.x,
+                                                      ptx::mul_f32x2(ptx::mul_f32x2(pair(hw[k]), rr), ss));
+                    ptx::f2_unpack(a.dh ? ptx::fma_f32x2(v, rr, pair(gw[k])) : ptx::mul_f32x2(v, rr), lo, hi);
+                    o[k] = ptx::pack_bf16x2(lo, hi);
+                }
             }
-            static_cast<uint4 *>(a.dx)[row + i] = pack8(o);
+            dx[t + c * TPR] = make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
     float *part = a.part + (size_t)blockIdx.x * a.D;
@@ -287,18 +323,18 @@ __global__ void __launch_bounds__(256, bwd_blocks_per_sm(CH)) rms_norm_bwd_kerne
             const int i = t + c * TPR;
             if (i >= nch) continue;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) part[i * 8 + e] = acc[c][e];
+            for (int e = 0; e < 4; ++e) reinterpret_cast<uint64_t *>(part)[i * 4 + e] = acc[c][e];
         }
     } else {
-        __shared__ float sums[RPB][256];
+        __shared__ __align__(16) float sums[RPB][256];
 #pragma unroll
         for (int c = 0; c < CH; ++c) {   // 32 chunks = 256 columns at a time
             __syncthreads();
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sums[holder][t * 8 + e] = acc[c][e];
+            for (int e = 0; e < 4; ++e) reinterpret_cast<uint64_t *>(sums[holder])[t * 4 + e] = acc[c][e];
             __syncthreads();
             const int col = c * 256 + threadIdx.x;
-            if (col < a.D) {
+            if (threadIdx.x < 256 && col < a.D) {
                 float v = 0.f;
 #pragma unroll
                 for (int w = 0; w < RPB; ++w) v += sums[w][threadIdx.x];
@@ -347,25 +383,25 @@ __global__ void __launch_bounds__(1024) rms_norm_bwd_long_kernel(const NormBwdAr
     }
 }
 
-// out[c] = the sum over rows of part[row][c], in a fixed order: a block takes 32 columns, its 32
-// warps every 32nd row, then one warp adds the 32 sums up.
-__global__ void __launch_bounds__(1024) sum_rows_kernel(const float *part, float *out, int rows, int cols)
+// out[c] = the sum over rows of part[row][c], in a fixed order: a block takes 8 columns (a sector of each
+// row), its 32 lanes of rows every 32nd row, then a warp adds a column's 32 sums up.  Blocks this small find
+// room beside the kernel before, and wait there for its end (of 1024 threads: 1111 x 768 6.2 us, so 5.7).
+__global__ void __launch_bounds__(256) sum_rows_kernel(const float *part, float *out, int rows, int cols)
 {
-    __shared__ float sums[32][33];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+    __shared__ float sums[32 * 9];
+    const int in = threadIdx.x & 7, from = threadIdx.x >> 3, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int c = blockIdx.x * 8 + in;
     float s = 0.f;
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
-    if (c < cols)
 #pragma unroll 4
-        for (int r = warp; r < rows; r += 32) s += part[(size_t)r * cols + c];
-    sums[warp][lane] = s;
+    for (int r = from; r < rows; r += 32) s += part[(size_t)r * cols + c];
+    sums[from * 9 + in] = s;
     __syncthreads();
-    s = sums[lane][warp];   // column `warp`, its 32 sums over the lanes
+    s = sums[lane * 9 + warp];   // column `warp`, its 32 sums over the lanes
 #pragma unroll
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
-    const int cw = blockIdx.x * 32 + warp;
-    if (lane == 0 && cw < cols) out[cw] = s;
+    if (lane == 0) out[blockIdx.x * 8 + warp] = s;
 }
 
 template <int TPR, int CH>
@@ -380,14 +416,20 @@ cudaError_t launch_norm(const NormArgs &a, cudaStream_t stream)
 template <int TPR, int CH>
 cudaError_t launch_norm_bwd(const NormBwdArgs &a, int blocks, cudaStream_t stream)
 {
-    return launch_overlapped(rms_norm_bwd_kernel<TPR, CH>, blocks, 256, 0, 1, stream, a, blocks);
+    constexpr int weights = CH * TPR * 32;
+    if (weights > 32768) {
+        static std::atomic<bool> set[64];
+        const cudaError_t e = raise_smem((const void *)rms_norm_bwd_kernel<TPR, CH>, weights, set);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_overlapped(rms_norm_bwd_kernel<TPR, CH>, blocks, bwd_threads(TPR, CH), weights, 1, stream, a, blocks);
 }
 
 }  // namespace
 
 cudaError_t launch_sum_rows(const float *part, float *out, int rows, int cols, cudaStream_t stream)
 {
-    return launch_overlapped(sum_rows_kernel, (cols + 31) / 32, 1024, 0, 1, stream, part, out, rows, cols);
+    return launch_overlapped(sum_rows_kernel, cols / 8, 256, 0, 1, stream, part, out, rows, cols);   // cols % 8 == 0
 }
 
 cudaError_t launch_rms_norm(const NormArgs &a, cudaStream_t stream)
@@ -411,8 +453,8 @@ cudaError_t launch_rms_norm(const NormArgs &a, cudaStream_t stream)
 // for up to two rows a holder: its sums are dweight itself, which saves the join.
 int norm_bwd_blocks(int M, int D)
 {
-    const int rpb = D <= 2048 ? 8 : 1, span = D <= 2048 ? 256 : 2048, ch = D <= 16384 ? (D + span - 1) / span : 8;
-    const int want = bwd_blocks_per_sm(ch) * kPlanSms;
+    const int tpr = D <= 2048 ? 32 : 256, ch = D <= 16384 ? (D + 8 * tpr - 1) / (8 * tpr) : 8;
+    const int rpb = bwd_threads(tpr, ch) / tpr, want = bwd_blocks_per_sm(ch) * kPlanSms;
     const int most = (int)(((long long)M + rpb - 1) / rpb);
     const int b = want < most ? want : most;
     return b > 2 ? b : 1;
