@@ -230,3 +230,39 @@ def test_a_flag_without_a_truth_value():
         sa.linear_forward(x, w, keep_z=NoTruth())
     with pytest.raises(KeyError):
         sa.linear_backward(x, w, torch.zeros(4, 32, device="cuda", dtype=torch.bfloat16), need_dw=NoTruth())
+
+
+@pytest.mark.parametrize("N,d", [(1024, 64), (2048, 128)])
+def test_beside_attention_on_another_stream(N, d):
+    """Attention's kernels and these share the SMs' tensor memory when they run at once; each gives what it
+    gives alone."""
+    g = _gen("beside", N, d)
+    q, k, v = (_randn(g, 2, 8, N, d) for _ in range(3))
+    few, many = _randn(g, 24, 1024), _randn(g, 4096, 1024)
+    w, gain = _randn(g, 1024, 1024, std=0.05), torch.rand(1024, device="cuda") + 0.5
+
+    def attend():
+        return list(sa.forward(q, k, v, d ** -0.5))
+
+    def rows():
+        out = []
+        for x in (few, many):
+            y, h, rstd = sa.rms_norm_forward(x, gain, x)
+            z = sa.linear_forward(y, w, None, h, "gelu")
+            out += [z, *sa.linear_backward(y, w, z), *sa.rms_norm_backward(z, h, gain, rstd)]
+        return out
+
+    want = attend(), rows()
+    torch.cuda.synchronize()
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    got = [], []
+    for _ in range(12):
+        for st, fn, to in zip(streams, (attend, rows), got):
+            st.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(st):
+                to.append(fn())
+    torch.cuda.synchronize()
+    for results, alone in zip(got, want):
+        for r in results:
+            for a, b in zip(r, alone):
+                assert torch.equal(a, b)
