@@ -82,7 +82,7 @@ struct GemmParams {
     // y2 maps [splits][rows][N] fp32 partial sums
     int x_all, x_early, a_clusters, part;
     // Bwd, the bias gradient: either col_rows partial rows to add up into dbias, or (sum_x) rows of dy to
-    // add up, per_slice at a time, into `slices` partial rows
+    // add up, per_slice at a time, into `slices` partial rows, or all at once (slices = 0) into dbias
     float *col_part, *dbias;
     int col_rows, col_n;
     const __nv_bfloat16 *sum_x;
@@ -541,7 +541,38 @@ __global__ void __launch_bounds__(128 + 32 * kEpiWarps, 1)
     } else if (P == Bwd && warp >= 2) {
         // the bias gradient, by the two warps that have no other work, while the products run
         const int first = blockIdx.x * 2 + warp - 2, warps = gridDim.x * 2;
-        if (p.sum_x) {   // dz is dy: sums over slices of its rows, 8 columns a lane, 16 rows in flight
+        if (p.sum_x && p.slices == 0) {   // dz is dy, of few rows: 64 columns a warp, 64 rows in flight
+            const int from = lane >> 3;
+            for (int c = first * 64; c < p.col_n; c += warps * 64) {
+                const int n = c + (lane & 7) * 8;
+                float s[8] = {};
+                for (int m = from; m < p.sum_m; m += 64) {
+                    uint4 v[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        v[k] = m + 4 * k < p.sum_m && n < p.col_n
+                                   ? __ldg(reinterpret_cast<const uint4 *>(p.sum_x + (size_t)(m + 4 * k) * p.col_n + n))
+                                   : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        float f[8];
+                        unpack_bf16x8(v[k], f);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) s[e] += f[e];
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    s[e] += __shfl_xor_sync(~0u, s[e], 8);
+                    s[e] += __shfl_xor_sync(~0u, s[e], 16);
+                }
+                if (from == 0 && n < p.col_n) {
+                    float4 *dst = reinterpret_cast<float4 *>(p.dbias + n);
+                    dst[0] = make_float4(s[0], s[1], s[2], s[3]);
+                    dst[1] = make_float4(s[4], s[5], s[6], s[7]);
+                }
+            }
+        } else if (p.sum_x) {   // dz is dy: sums over slices of its rows, 8 columns a lane, 16 rows in flight
             for (int sl = first; sl < p.slices; sl += warps) {
                 const long long m0 = (long long)sl * p.per_slice, m1 = min((long long)p.sum_m, m0 + p.per_slice);
                 for (int n = lane * 8; n < p.col_n; n += 256) {
@@ -1226,37 +1257,41 @@ cudaError_t launch_linear_bwd(const LinBwdArgs &a, cudaStream_t stream)
 {
     cudaError_t e = cudaSuccess;
     const int blocks = lin_bwd_row_blocks(a.M, a.N);
+    const BwdPlan plan = bwd_plan(a.G, a.T, a.K, a.N);
+    const int ksteps = ceil_div(a.N, 64);
+    // few rows: dx by the split kernel, beside dw alone
+    const SplitPlan split = a.dx ? split_plan(a.G, a.T, a.K, ksteps) : SplitPlan{};
+    const bool dx_split = a.dx && split.us + plan.dw_us < plan.us;
     // Where dz is dy and dw is taken, the two idle warps of the product kernel's CTAs read dy for the bias
-    // gradient: that costs nothing while the products take longer, from K of about 450 on (16 KB in
-    // flight a CTA against 4 K flops an element); else a pass of its own.
-    const bool beside = a.dbias && !a.z && a.dw && a.K >= 512;
+    // gradient.  Each adds up whole columns where that (0.8 us for 64 rows) ends with the products or within
+    // a join's time (196 x 768 x 768: 6.2 us, with the join 7.7; 16 x 1024 x 4096 10.3 and 17.8; 1024 x 768 x
+    // 768 11.8 and 8.7).  Else slices of rows, which costs nothing while the products take longer, from K of
+    // about 450 on (16 KB in flight a CTA against 4 K flops an element); else a pass of its own.
+    const int col_warps = 4 * (a.N < 256 * kPlanPairs ? ceil_div(a.N, 256) : kPlanPairs);   // at least
+    const double direct_us = 0.8 * ceil_div(a.M, 64) * ceil_div(ceil_div(a.N, 64), col_warps);
+    const bool direct = a.dbias && !a.z && a.dw && direct_us <= (a.dx && !dx_split ? plan.us : plan.dw_us) + 0.5;
+    const bool beside = direct || (a.dbias && !a.z && a.dw && a.K >= 512);
     if ((a.dbias && !beside) || (a.z && (a.dx || a.dw))) {
         e = launch_overlapped(dz_kernel, dim3(ceil_div(a.N, 256), blocks), 256, 0, 1, stream, a, blocks);
         if (e != cudaSuccess) return e;
     }
     const void *dz = a.z ? a.dz : a.dy;
-    const BwdPlan plan = bwd_plan(a.G, a.T, a.K, a.N);
-    const int ksteps = ceil_div(a.N, 64);
     CUresult r = CUDA_SUCCESS;
-    bool dx_left = a.dx != nullptr;
-    if (a.dx) {   // few rows: dx by the split kernel, beside dw alone
-        const SplitPlan split = split_plan(a.G, a.T, a.K, ksteps);
-        if (split.us + plan.dw_us < plan.us) {
-            SplitParams sp = {};
-            set_split_rows(sp, a.G, a.T, split.tn);
-            sp.N = a.K;
-            sp.dk = a.dk;
-            sp.H = a.H;
-            sp.ksteps = ksteps;
-            sp.y = static_cast<__nv_bfloat16 *>(a.dx);
-            sp.status = a.status;
-            CUtensorMap mx, mw;
-            r = make_map_3d(&mx, dz, kBf16, 2, a.N, a.T, a.G, 64, sp.rb);
-            if (r == CUDA_SUCCESS) r = make_map_3d(&mw, a.w, kBf16, 2, a.N, a.K, 1, 64, 128);
-            if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
-            if ((e = launch_split<Dx>(mw, mx, sp, split, stream)) != cudaSuccess) return e;
-            dx_left = false;
-        }
+    const bool dx_left = a.dx && !dx_split;
+    if (dx_split) {
+        SplitParams sp = {};
+        set_split_rows(sp, a.G, a.T, split.tn);
+        sp.N = a.K;
+        sp.dk = a.dk;
+        sp.H = a.H;
+        sp.ksteps = ksteps;
+        sp.y = static_cast<__nv_bfloat16 *>(a.dx);
+        sp.status = a.status;
+        CUtensorMap mx, mw;
+        r = make_map_3d(&mx, dz, kBf16, 2, a.N, a.T, a.G, 64, sp.rb);
+        if (r == CUDA_SUCCESS) r = make_map_3d(&mw, a.w, kBf16, 2, a.N, a.K, 1, 64, 128);
+        if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
+        if ((e = launch_split<Dx>(mw, mx, sp, split, stream)) != cudaSuccess) return e;
     }
     if (!dx_left && !a.dw) return a.dbias ? launch_sum_rows(a.col_part, a.dbias, blocks, a.N, stream) : e;
 
@@ -1299,17 +1334,17 @@ cudaError_t launch_linear_bwd(const LinBwdArgs &a, cudaStream_t stream)
         if (beside) {
             p.sum_x = static_cast<const __nv_bfloat16 *>(a.dy);
             p.sum_m = a.M;
-            p.slices = lin_bwd_slices(a.M);
-            p.per_slice = ceil_div(a.M, p.slices);
+            p.slices = direct ? 0 : lin_bwd_slices(a.M);
+            p.per_slice = direct ? 0 : ceil_div(a.M, p.slices);
         }
     }
     const long long items = (long long)p.q[0].n_items + p.q[1].n_items;
     const int pairs = device_sm_count() / 2, clusters = items < pairs ? (int)items : pairs;
     level_items(p, clusters);
     e = plan.wide ? launch_pair<Bwd, 256>(m, p, clusters, stream) : launch_pair<Bwd, 128>(m, p, clusters, stream);
-    if (e == cudaSuccess && (p.part || beside)) {
+    if (e == cudaSuccess && (p.part || p.slices)) {
         const long long elems = p.part ? (long long)a.K * a.N : 0;
-        const int dw_blocks = ceil_div(elems, 1024), sum_blocks = beside ? ceil_div(a.N, 32) : 0;
+        const int dw_blocks = ceil_div(elems, 1024), sum_blocks = p.slices ? ceil_div(a.N, 32) : 0;
         e = launch_overlapped(bwd_join_kernel, dw_blocks + sum_blocks, 256, 0, 1, stream, (const float *)a.dw_part, a.dw,
                               plan.splits, elems, dw_blocks, (const float *)a.col_part, a.dbias, p.slices, a.N);
     }

@@ -277,3 +277,20 @@ def test_refusals_by_tensor():
         y = torch.zeros(4, 32, dtype=torch.bfloat16, device="cuda")
         sa.attn_linear(x.view(-1)[1:], w, None, None, y, None, 3, 64, 32, 0)
     assert e.value.code == 3
+
+
+@pytest.mark.parametrize("M,K,N", [(1, 8, 8), (70, 16, 20008), (65, 520, 72), (513, 64, 264), (640, 1032, 1000),
+                                   (2049, 264, 4104)])
+def test_bias_gradient_of_few_and_many_rows(M, K, N):
+    """By whole columns, by slices of rows and in a pass of its own; with and without the other gradients."""
+    g = _gen("bias", M, K, N)
+    x, w, dy = _randn(g, M, K), _randn(g, K, N, std=0.05), _randn(g, M, N)
+    want = ref.linear_bwd(x, w, dy)
+    for need_dx, need_dw in ((True, True), (False, True), (True, False), (False, False)):
+        dx, dw, db = sa.linear_backward(x, w, dy, need_dx=need_dx, need_dw=need_dw)
+        ref.check("db", db, *want["db"])
+        assert torch.equal(db, sa.linear_backward(x, w, dy, need_dx=need_dx, need_dw=need_dw)[2])
+        if need_dx:
+            ref.check("dx", dx, *want["dx"])
+        if need_dw:
+            ref.check("dw", dw, *want["dw"])
