@@ -33,6 +33,7 @@
 #include "act.cuh"
 #include "cluster.cuh"
 #include "kernels.h"
+#include "sum_rows.cuh"
 
 namespace attn {
 namespace {
@@ -925,8 +926,7 @@ __global__ void __launch_bounds__(256) dz_kernel(const LinBwdArgs a, int blocks)
 }
 
 // What is left after the products: dw = the sum of its partial sums, in order, rounded once, 4 elements a
-// thread, in the first `dw_blocks` blocks; the bias gradient's partial sums, 32 columns a block, in the
-// others.
+// thread, in the first `dw_blocks` blocks; the bias gradient's partial sums in the others.
 __global__ void __launch_bounds__(256) bwd_join_kernel(const float *part, void *dw, int splits, long long elems,
                                                        int dw_blocks, const float *col_part, float *dbias, int slices,
                                                        int N)
@@ -934,19 +934,7 @@ __global__ void __launch_bounds__(256) bwd_join_kernel(const float *part, void *
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
     if ((int)blockIdx.x >= dw_blocks) {
-        __shared__ float sums[8][32];
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = (blockIdx.x - dw_blocks) * 32 + lane;
-        float s = 0.f;
-        if (c < N)
-#pragma unroll 8
-            for (int r = warp; r < slices; r += 8) s += col_part[(size_t)r * N + c];
-        sums[warp][lane] = s;
-        __syncthreads();
-        if (warp == 0 && c < N) {
-#pragma unroll
-            for (int w = 1; w < 8; ++w) s += sums[w][lane];
-            dbias[c] = s;
-        }
+        sum_columns(col_part, dbias, slices, N, ((int)blockIdx.x - dw_blocks) * kSumCols);
         return;
     }
     const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 4;
@@ -1344,7 +1332,7 @@ cudaError_t launch_linear_bwd(const LinBwdArgs &a, cudaStream_t stream)
     e = plan.wide ? launch_pair<Bwd, 256>(m, p, clusters, stream) : launch_pair<Bwd, 128>(m, p, clusters, stream);
     if (e == cudaSuccess && (p.part || p.slices)) {
         const long long elems = p.part ? (long long)a.K * a.N : 0;
-        const int dw_blocks = ceil_div(elems, 1024), sum_blocks = p.slices ? ceil_div(a.N, 32) : 0;
+        const int dw_blocks = ceil_div(elems, 1024), sum_blocks = p.slices ? a.N / kSumCols : 0;   // N % 8 == 0
         e = launch_overlapped(bwd_join_kernel, dw_blocks + sum_blocks, 256, 0, 1, stream, (const float *)a.dw_part, a.dw,
                               plan.splits, elems, dw_blocks, (const float *)a.col_part, a.dbias, p.slices, a.N);
     }
