@@ -1096,56 +1096,79 @@ PairPlan pair_plan(long long mtiles, int N, int ksteps)
 
 // The backward runs both products in one launch, so that one's tiles fill the pairs that the other's
 // leave idle and there is one start and end (18432 rows, 768 x 768: 42 us apart, 33 together; 1111 rows,
-// 1000 x 520: 20 and 12; 32768 rows, 1024 x 4096: 307 and 295, 1.86 PFLOP/s).  dw has few tiles (K x N) and a long sum (the rows), which is split over items only where that
-// still pays for the partial sums' join (2.5 us, 5 bytes/ps).  Times in K steps: an item's fill and drain
-// costs 2 for dx, 4 for dw.
+// 1000 x 520: 20 and 12; 32768 rows, 1024 x 4096: 307 and 295, 1.86 PFLOP/s).
+//
+// How `clusters` share nd items of dw, of a steps each, and nx of dx, of b.
+struct Shares {
+    long long nd, nx, a, b, whole, rest, clusters;   // rest clusters have whole + 1 items of dw
+    Shares(long long nd, long long nx, long long a, long long b, int clusters)
+        : nd(nd), nx(nx), a(a), b(b), whole(nd / clusters), rest(nd % clusters), clusters(clusters)
+    {
+    }
+    // dx's items that fit up to step t beside `dw` items of dw
+    long long room(long long t, long long dw) const { return t > dw * a ? (t - dw * a) / b : 0; }
+    long long even() const { return (nd * a + nx * b + clusters - 1) / clusters; }
+    long long longest_dw() const { return (whole + (rest > 0)) * a; }
+    // The least level t >= lo at which dx's items fit: all clusters end at about that step.  (They do at
+    // even() + b, where no cluster wastes an item's room.)
+    long long level(long long lo) const
+    {
+        long long hi = even() + b;
+        while (lo < hi) {
+            const long long t = (lo + hi) / 2;
+            if (rest * room(t, whole + 1) + (clusters - rest) * room(t, whole) >= nx)
+                hi = t;
+            else
+                lo = t + 1;
+        }
+        return lo;
+    }
+};
+
+// dw has few tiles (K x N) and a long sum (the rows), which is split over items where that pays for the
+// partial sums' join.  The estimate is fitted to a sweep of every plan over 64 to 18432 rows at twelve sizes
+// of K and N from 256 to 4096 (the chosen plan takes 1 % more than the best one there on average); an item's
+// fill and drain counts as one more step of dx, two of dw.
 struct BwdPlan {
     bool wide;
     int splits, steps_per_split;
     double us, dw_us;   // of both, of dw alone
 };
 
-constexpr int kDxExtra = 2, kDwExtra = 4;
-
 BwdPlan bwd_plan(int G, int T, int K, int N)
 {
+    constexpr double kStart = 3.8, kStep[2] = {0.222, 0.335}, kJoin = 2.2, kJoinRate = 9.4e6;
     const long long steps = (long long)G * ceil_div(T, 64), mx = row_tiles(G, T), mw = ceil_div(K, BM);
+    const int ksteps = ceil_div(N, 64);
     BwdPlan best{};
     best.us = 1e30;
     for (int wide = 1; wide >= 0; --wide) {
         const int bn = wide ? 256 : 128;
-        const double dx = (double)mx * ceil_div(K, bn) * (ceil_div(N, 64) + kDxExtra);
         for (int s = 1; s <= 16 && s <= steps; ++s) {
-            const long long per = (steps + s - 1) / s, items = mw * ceil_div(N, bn) * s;
+            const long long per = (steps + s - 1) / s;
             if ((steps + per - 1) / per != s) continue;
-            const double most = (double)ceil_div(items, kPlanPairs) * (per + kDwExtra);
-            const double even = ((double)items * (per + kDwExtra) + dx) / kPlanPairs + 0.5 * (ceil_div(N, 64) + kDxExtra);
-            const double step = wide ? kStepWide : kStepNarrow, join = s > 1 ? 2.5 + (double)s * K * N * 8 / 5e6 : 0.0;
-            const double us = 6.0 + (most > even ? most : even) * step + join;
-            if (us < best.us) best = BwdPlan{wide == 1, s, (int)per, us, 6.0 + most * step + join};
+            const double fixed = kStart + (s > 1 ? kJoin + (double)s * K * N * 8 / kJoinRate : 0.0);
+            if (fixed >= best.us) break;
+            const Shares h(mw * ceil_div(N, bn) * s, mx * ceil_div(K, bn), per + 2, ksteps + 1, kPlanPairs);
+            const long long even = h.even(), dw = h.longest_dw();
+            if (fixed + (even > dw ? even : dw) * kStep[wide] >= best.us) continue;
+            const long long level = h.level(even), last = level > dw ? level : dw;
+            const double us = fixed + last * kStep[wide];
+            if (us < best.us) best = BwdPlan{wide == 1, s, (int)per, us, fixed + dw * kStep[wide]};
         }
     }
     return best;
 }
 
-// How many of dx's items each cluster takes, so that all end at about the same step: the least level t
-// at which the room left beside dw's items holds them.
+// How many of dx's items each cluster takes.  (Beside other items a fill and drain counts twice that; the
+// sweep was run with these.)
 void level_items(GemmParams &p, int clusters)
 {
-    const long long a = p.q[1].steps_per_split + kDwExtra, b = p.q[0].ksteps + kDxExtra;
-    const long long nd = p.q[1].n_items, nx = p.q[0].n_items, whole = nd / clusters, rest = nd % clusters;
-    auto room = [&](long long t, long long dw) { return t > dw * a ? (t - dw * a) / b : 0; };
-    long long lo = 0, hi = (whole + 1) * a + (nx / clusters + 1) * b;
-    while (lo < hi) {
-        const long long t = (lo + hi) / 2;
-        if (rest * room(t, whole + 1) + (clusters - rest) * room(t, whole) >= nx)
-            hi = t;
-        else
-            lo = t + 1;
-    }
-    p.a_clusters = (int)rest;
-    p.x_all = (int)room(lo, rest ? whole + 1 : whole);
-    p.x_early = (int)room(lo, whole) - p.x_all;
+    const Shares h(p.q[1].n_items, p.q[0].n_items, p.q[1].steps_per_split + 4, p.q[0].ksteps + 2, clusters);
+    const long long t = h.level(0);
+    p.a_clusters = (int)h.rest;
+    p.x_all = (int)h.room(t, h.rest ? h.whole + 1 : h.whole);
+    p.x_early = (int)h.room(t, h.whole) - p.x_all;
 }
 
 }  // namespace
