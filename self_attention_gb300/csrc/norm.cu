@@ -1,12 +1,12 @@
 // Root-mean-square norm with the residual's addition, its 8-bit form and its backward.
 //
 // All of it is bound by HBM: each row is read once into registers, reduced, and written once.  A row
-// is taken by a warp (up to 2048 columns; no barrier, only shuffles), by 256 threads (to 16384) or
-// by 1024 threads (to 32768), each thread holding chunks of 8 neighbouring columns (16-byte loads);
-// longer rows are read a second time from L2.  Measured on 128 to 470 MB in calls back to back: forward
-// 32768 x 1024 with residual 40.9 us (6.6 TB/s, 0.97 of the measured copy), to 8 bits 32768 x 2048 70.0
-// us (6.7 TB/s); backward 32768 x 1024 47 us (5.7 TB/s), 18432 x 768 23.4 us with the join of dweight's
-// partial sums: its rows are taken one after another by the same warps, for those sums.
+// is taken by 8 or 16 lanes (up to 64 and 128 columns), a warp (to 2048; no barrier, only shuffles), by
+// 256 threads (to 16384) or by 1024 threads (to 32768), each thread holding chunks of 8 neighbouring
+// columns (16-byte loads); longer rows are read a second time from L2.  Measured on 128 to 470 MB in calls
+// back to back: forward 32768 x 1024 with residual 40.9 us (6.6 TB/s, 0.97 of the measured copy), to 8 bits
+// 32768 x 2048 70.0 us (6.7 TB/s); backward 32768 x 1024 47 us (5.7 TB/s), 18432 x 768 23.4 us with the join
+// of dweight's partial sums: its rows are taken one after another by the same warps, for those sums.
 #include "cluster.cuh"
 #include "kernels.h"
 #include "sum_rows.cuh"
@@ -63,12 +63,12 @@ __device__ __forceinline__ void load8(const float *p, float (&f)[8])
     f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
 }
 
-// Reduction over the TPR threads that hold a row (a warp, or the whole block).
+// Reduction over the TPR threads that hold a row (a part of a warp, a warp, or the whole block).
 template <int TPR, class Op>
 __device__ __forceinline__ float row_reduce(float v, Op op)
 {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) v = op(v, __shfl_xor_sync(~0u, v, o));
+    for (int o = TPR < 32 ? TPR / 2 : 16; o; o >>= 1) v = op(v, __shfl_xor_sync(~0u, v, o));
     if constexpr (TPR > 32) {
         __shared__ float part[TPR / 32];
         __syncthreads();
@@ -102,70 +102,79 @@ __device__ __forceinline__ float q8_inverse(float amax, float &scale)
     return kQ8Max / a;
 }
 
-__host__ __device__ constexpr int rows_per_block(int tpr) { return tpr == 32 ? 4 : 1; }
+__host__ __device__ constexpr int holders(int tpr) { return tpr <= 32 ? 128 / tpr : 1; }   // of a block
 
-template <int TPR, int CH, bool Q8>
-__global__ void __launch_bounds__(TPR *rows_per_block(TPR)) rms_norm_kernel(const NormArgs a)
+// Each holder (TPR threads) takes ROWS rows, all of them in flight at once.
+template <int TPR, int CH, int ROWS, bool Q8>
+__global__ void __launch_bounds__(TPR *holders(TPR)) rms_norm_kernel(const NormArgs a)
 {
-    const long long m = (long long)blockIdx.x * rows_per_block(TPR) + threadIdx.x / TPR;
+    const long long m0 = (long long)blockIdx.x * holders(TPR) * ROWS + threadIdx.x / TPR;
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
-    if (m >= a.M) return;   // whole warps (TPR = 32), or never
+    if (TPR >= 32 && m0 >= a.M) return;   // whole warps (TPR = 32), or never
     const int t = threadIdx.x % TPR, nch = a.D / 8;
-    const size_t row = (size_t)m * nch;   // in chunks
-    const uint4 *x = static_cast<const uint4 *>(a.x) + row, *r = static_cast<const uint4 *>(a.residual) + row;
-    float h[CH][8];
-    uint4 xv[CH], rv[CH];
+    uint4 xv[ROWS][CH], rv[ROWS][CH];
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-        const int i = t + c * TPR;
-        if (i < nch) {
-            xv[c] = x[i];
-            if (a.residual) rv[c] = r[i];
-        }
-    }
-    float s = 0.f;
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-        const int i = t + c * TPR;
-        if (i >= nch) continue;
-        unpack8(xv[c], h[c]);
-        if (a.residual) {
-            float f[8];
-            unpack8(rv[c], f);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) h[c][e] += f[e];
-            if (a.h) static_cast<uint4 *>(a.h)[row + i] = pack8(h[c]);
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s = fmaf(h[c][e], h[c][e], s);
-    }
-    if (a.weight) {
-        const float rstd = 1.f / sqrtf(row_reduce<TPR>(s, add) / (float)a.D + a.eps);
-        if (a.rstd && t == 0) a.rstd[m] = rstd;
+    for (int k = 0; k < ROWS; ++k) {
+        const long long m = m0 + k * holders(TPR);
+        const size_t row = (size_t)m * nch;   // in chunks
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             const int i = t + c * TPR;
-            if (i >= nch) continue;
-            float w[8];
-            load8(a.weight + i * 8, w);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) h[c][e] = h[c][e] * rstd * w[e];
-            if (!Q8) store_y<false>(a.y, row + i, h[c], 1.f);
+            if (i < nch && m < a.M) {
+                xv[k][c] = static_cast<const uint4 *>(a.x)[row + i];
+                if (a.residual) rv[k][c] = static_cast<const uint4 *>(a.residual)[row + i];
+            }
         }
     }
-    if (Q8) {
-        float amax = 0.f, scale;
 #pragma unroll
-        for (int c = 0; c < CH; ++c)
-            if (t + c * TPR < nch)
+    for (int k = 0; k < ROWS; ++k) {
+        const long long m = m0 + k * holders(TPR);
+        const size_t row = (size_t)m * nch;
+        const int n = m < a.M ? nch : 0;   // (every lane takes part in the sums)
+        float h[CH][8], s = 0.f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) amax = max_nan(amax, fabsf(h[c][e]));
-        const float inv = q8_inverse(row_reduce<TPR>(amax, max_nan), scale);
-        if (t == 0) a.scale[m] = scale;
+        for (int c = 0; c < CH; ++c) {
+            const int i = t + c * TPR;
+            if (i >= n) continue;
+            unpack8(xv[k][c], h[c]);
+            if (a.residual) {
+                float f[8];
+                unpack8(rv[k][c], f);
 #pragma unroll
-        for (int c = 0; c < CH; ++c)
-            if (t + c * TPR < nch) store_y<true>(a.y, row + t + c * TPR, h[c], inv);
+                for (int e = 0; e < 8; ++e) h[c][e] += f[e];
+                if (a.h) static_cast<uint4 *>(a.h)[row + i] = pack8(h[c]);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s = fmaf(h[c][e], h[c][e], s);
+        }
+        if (a.weight) {
+            const float rstd = 1.f / sqrtf(row_reduce<TPR>(s, add) / (float)a.D + a.eps);
+            if (a.rstd && t < n && t == 0) a.rstd[m] = rstd;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const int i = t + c * TPR;
+                if (i >= n) continue;
+                float w[8];
+                load8(a.weight + i * 8, w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) h[c][e] = h[c][e] * rstd * w[e];
+                if (!Q8) store_y<false>(a.y, row + i, h[c], 1.f);
+            }
+        }
+        if (Q8) {
+            float amax = 0.f, scale;
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+                if (t + c * TPR < n)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) amax = max_nan(amax, fabsf(h[c][e]));
+            const float inv = q8_inverse(row_reduce<TPR>(amax, max_nan), scale);
+            if (t < n && t == 0) a.scale[m] = scale;
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+                if (t + c * TPR < n) store_y<true>(a.y, row + t + c * TPR, h[c], inv);
+        }
     }
 }
 
@@ -233,6 +242,7 @@ __global__ void __launch_bounds__(1024) rms_norm_long_kernel(const NormArgs a)
 // operands without spilling.
 __host__ __device__ constexpr int bwd_blocks_per_sm(int ch) { return ch <= 1 ? 4 : ch <= 2 ? 3 : ch <= 4 ? 2 : 1; }
 __host__ __device__ constexpr int bwd_threads(int tpr, int ch) { return tpr == 32 && ch == 3 ? 320 : 256; }
+__host__ __device__ constexpr int bwd_tpr(int D) { return D <= 64 ? 8 : D <= 128 ? 16 : D <= 2048 ? 32 : 256; }
 
 template <int TPR, int CH>
 __global__ void __launch_bounds__(bwd_threads(TPR, CH), bwd_blocks_per_sm(CH))
@@ -247,7 +257,13 @@ __global__ void __launch_bounds__(bwd_threads(TPR, CH), bwd_blocks_per_sm(CH))
     uint4 dv[CH], hv[CH], gv[CH];
     float r = 0.f;
     auto load_row = [&] {   // everything the row needs is asked for at once
-        if (m >= a.M) return;
+        if (m >= a.M) {   // (only beside another row of the warp)
+            if (TPR < 32) {
+                r = 0.f;
+                dv[0] = hv[0] = gv[0] = make_uint4(0, 0, 0, 0);
+            }
+            return;
+        }
         const size_t row = (size_t)m * nch;
         const uint4 *dy = static_cast<const uint4 *>(a.dy) + row, *h = static_cast<const uint4 *>(a.h) + row,
                     *dh = static_cast<const uint4 *>(a.dh) + row;
@@ -273,7 +289,8 @@ __global__ void __launch_bounds__(bwd_threads(TPR, CH), bwd_blocks_per_sm(CH))
     }
     __syncthreads();
     const uint32_t wt = ptx::smem_u32(weights) + t * 16;
-    for (; m < a.M; m += step, load_row()) {
+    const int in_warp = TPR < 32 ? holder % (32 / TPR) : 0;   // a warp's rows are neighbours, and end together
+    for (; m - in_warp < a.M; m += step, load_row()) {
         uint64_t sum = 0;
         const uint64_t rr = ptx::f2_pack(r, r);
 #pragma unroll
@@ -314,11 +331,11 @@ __global__ void __launch_bounds__(bwd_threads(TPR, CH), bwd_blocks_per_sm(CH))
                     o[k] = ptx::pack_bf16x2(lo, hi);
                 }
             }
-            dx[t + c * TPR] = make_uint4(o[0], o[1], o[2], o[3]);
+            if (TPR >= 32 || m < a.M) dx[t + c * TPR] = make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
     float *part = a.part + (size_t)blockIdx.x * a.D;
-    if constexpr (RPB == 1) {
+    if constexpr (TPR > 32) {
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             const int i = t + c * TPR;
@@ -327,15 +344,16 @@ __global__ void __launch_bounds__(bwd_threads(TPR, CH), bwd_blocks_per_sm(CH))
             for (int e = 0; e < 4; ++e) reinterpret_cast<uint64_t *>(part)[i * 4 + e] = acc[c][e];
         }
     } else {
-        __shared__ __align__(16) float sums[RPB][256];
+        constexpr int COLS = 8 * TPR;   // at a time
+        __shared__ __align__(16) float sums[RPB][COLS];
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {   // 32 chunks = 256 columns at a time
+        for (int c = 0; c < CH; ++c) {
             __syncthreads();
 #pragma unroll
             for (int e = 0; e < 4; ++e) reinterpret_cast<uint64_t *>(sums[holder])[t * 4 + e] = acc[c][e];
             __syncthreads();
-            const int col = c * 256 + threadIdx.x;
-            if (threadIdx.x < 256 && col < a.D) {
+            const int col = c * COLS + threadIdx.x;
+            if (threadIdx.x < COLS && col < a.D) {
                 float v = 0.f;
 #pragma unroll
                 for (int w = 0; w < RPB; ++w) v += sums[w][threadIdx.x];
@@ -393,13 +411,13 @@ __global__ void __launch_bounds__(256) sum_rows_kernel(const float *part, float 
     sum_columns(part, out, rows, cols, blockIdx.x * kSumCols);
 }
 
-template <int TPR, int CH>
+template <int TPR, int CH, int ROWS = 1>
 cudaError_t launch_norm(const NormArgs &a, cudaStream_t stream)
 {
-    constexpr int R = rows_per_block(TPR);
+    constexpr int R = holders(TPR) * ROWS;
     const unsigned grid = (unsigned)(((long long)a.M + R - 1) / R);
-    return a.q8 ? launch_overlapped(rms_norm_kernel<TPR, CH, true>, grid, TPR * R, 0, 1, stream, a)
-                : launch_overlapped(rms_norm_kernel<TPR, CH, false>, grid, TPR * R, 0, 1, stream, a);
+    return a.q8 ? launch_overlapped(rms_norm_kernel<TPR, CH, ROWS, true>, grid, TPR * holders(TPR), 0, 1, stream, a)
+                : launch_overlapped(rms_norm_kernel<TPR, CH, ROWS, false>, grid, TPR * holders(TPR), 0, 1, stream, a);
 }
 
 template <int TPR, int CH>
@@ -427,7 +445,13 @@ cudaError_t launch_rms_norm(const NormArgs &a, cudaStream_t stream)
     // a few rows (no more than two blocks an SM): 256 threads each hold one chunk of a row, which is read
     // and reduced sooner than by a warp (7 x 2048 to 8 bits: 4.8 against 6.1 us a call)
     if (D > 256 && D <= 2048 && a.M <= 2 * kPlanSms) return launch_norm<256, 1>(a, stream);
-    if (D <= 256) return launch_norm<32, 1>(a, stream);
+    // Short rows: as many threads a row as it has chunks, and of many rows (eight blocks an SM) four a holder,
+    // since blocks of 2 KB start no faster than one a nanosecond (524288 x 64 with residual: 43 us, by whole
+    // warps and one row 134; 131072 x 256 26 and 36, but with residual, twice the bytes a row, 42.5 and 41.4).
+    const bool many = (long long)a.M * D >= 8LL * kPlanSms * 4096;
+    if (D <= 64) return many ? launch_norm<8, 1, 4>(a, stream) : launch_norm<8, 1>(a, stream);
+    if (D <= 128) return many ? launch_norm<16, 1, 4>(a, stream) : launch_norm<16, 1>(a, stream);
+    if (D <= 256) return many && !a.residual ? launch_norm<32, 1, 4>(a, stream) : launch_norm<32, 1>(a, stream);
     if (D <= 512) return launch_norm<32, 2>(a, stream);
     if (D <= 1024) return launch_norm<32, 4>(a, stream);
     if (D <= 2048) return launch_norm<32, 8>(a, stream);
@@ -442,7 +466,7 @@ cudaError_t launch_rms_norm(const NormArgs &a, cudaStream_t stream)
 // for up to two rows a holder: its sums are dweight itself, which saves the join.
 int norm_bwd_blocks(int M, int D)
 {
-    const int tpr = D <= 2048 ? 32 : 256, ch = D <= 16384 ? (D + 8 * tpr - 1) / (8 * tpr) : 8;
+    const int tpr = bwd_tpr(D), ch = D <= 16384 ? (D + 8 * tpr - 1) / (8 * tpr) : 8;
     const int rpb = bwd_threads(tpr, ch) / tpr, want = bwd_blocks_per_sm(ch) * kPlanSms;
     const int most = (int)(((long long)M + rpb - 1) / rpb);
     const int b = want < most ? want : most;
@@ -454,7 +478,9 @@ cudaError_t launch_rms_norm_bwd(const NormBwdArgs &args, cudaStream_t stream)
     NormBwdArgs a = args;
     const int blocks = norm_bwd_blocks(a.M, a.D), D = a.D;
     if (blocks == 1) a.part = a.dweight;
-    const cudaError_t e = D <= 256     ? launch_norm_bwd<32, 1>(a, blocks, stream)
+    const cudaError_t e = D <= 64      ? launch_norm_bwd<8, 1>(a, blocks, stream)
+                          : D <= 128   ? launch_norm_bwd<16, 1>(a, blocks, stream)
+                          : D <= 256   ? launch_norm_bwd<32, 1>(a, blocks, stream)
                           : D <= 512   ? launch_norm_bwd<32, 2>(a, blocks, stream)
                           : D <= 768   ? launch_norm_bwd<32, 3>(a, blocks, stream)
                           : D <= 1024  ? launch_norm_bwd<32, 4>(a, blocks, stream)

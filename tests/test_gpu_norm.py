@@ -202,3 +202,44 @@ def test_refusals_by_tensor():
         with pytest.raises(sa.AttnError) as e:
             bad()
         assert e.value.code == 1
+
+
+@pytest.mark.parametrize("M,D", [(1, 64), (5, 8), (33, 64), (1000, 72), (7, 128), (777, 128), (100_003, 64), (40_001, 128),
+                                 (30_001, 200), (20_003, 256), (13_001, 392), (10_007, 512)])
+def test_short_rows(M, D):
+    """Several rows a warp, and several a thread where there are many; numbers of rows that end inside both."""
+    for flag in (False, True):
+        test_rms_norm(M, D, flag)
+        test_rms_norm_q8(M, D, flag)
+        test_rms_norm_backward(M, D, flag)
+
+
+@pytest.mark.parametrize("M,D", [(45, 64), (45, 128), (90_001, 64), (50_001, 128)])
+def test_short_rows_do_not_see_one_another(M, D):
+    """A NaN or an infinity stays in its row, and nothing is written behind the last."""
+    g = _gen("alone", M, D)
+    x, dy, w = _randn(g, M, D), _randn(g, M, D), 1 + _randn(g, D, std=0.2, dtype=torch.float32)
+    bad = torch.zeros(M, dtype=torch.bool, device="cuda")
+    bad[torch.tensor([0, 3, 9, M // 2, M - 1], device="cuda")] = True
+    x2, dy2 = x.clone(), dy.clone()
+    x2[bad, 5] = float("nan")
+    dy2[bad, 1] = float("inf")
+    (y, _, rstd), (q, scale, _) = sa.rms_norm_forward(x, w), sa.rms_norm_q8(x, w)
+    (y2, _, rstd2), (q2, scale2, _) = sa.rms_norm_forward(x2, w), sa.rms_norm_q8(x2, w)
+    assert torch.equal(y[~bad], y2[~bad]) and torch.equal(rstd[~bad], rstd2[~bad]) and bool(rstd2[bad].isnan().all())
+    assert torch.equal(q[~bad].float(), q2[~bad].float()) and torch.equal(scale[~bad], scale2[~bad])
+    assert bool(scale2[bad].isnan().all())
+    dx, dx2 = sa.rms_norm_backward(dy, x, w, rstd)[0], sa.rms_norm_backward(dy2, x, w, rstd)[0]
+    assert torch.equal(dx[~bad], dx2[~bad]) and bool((~dx2[bad].isfinite()).any(-1).all())
+
+    rows = 40   # behind the last
+    full = [torch.full((M + rows, D), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+    stat = torch.full((M + rows,), 7.0, device="cuda")
+    sa.attn_rms_norm(x, x, w, full[0], full[1], stat, M, D, 1e-6)
+    n = sa.attn_rms_norm_bwd_workspace_size(M, D)
+    dw, ws = torch.empty(D, device="cuda"), torch.empty(n, dtype=torch.uint8, device="cuda")
+    sa.attn_rms_norm_bwd(dy, x, w, rstd, None, full[2], dw, ws, n, M, D)
+    torch.cuda.synchronize()
+    for t in (*full, stat):
+        assert bool((t[M:] == 7.0).all())
+    assert torch.equal(full[2][:M], dx)
