@@ -622,6 +622,7 @@ __global__ void __launch_bounds__(128 + 32 * kEpiWarps, 1)
 // read (one 2048 x 8192 matrix is 64 column tiles).  Each CTA sends the rows of its partial tile to the
 // CTAs that own them (row r to rank r mod splits), straight from tensor memory into their shared memory;
 // after one cluster barrier each sums its rows over the ranks in order, applies the epilogue and stores.
+// Where K is not split, each warp finishes its strip of the tile from tensor memory.
 // (Leaving the partial tiles in place and fetching them takes a second barrier, and remote loads that
 // are waited for: 1 us of 7 more.)  Up to TN = 64 two CTAs fit an SM.
 struct SplitParams {
@@ -718,6 +719,81 @@ __device__ __forceinline__ void join_rows(const SplitParams &p, uint32_t recv, i
     }
 }
 
+// K is not split: each warp finishes a 32-column strip of the tile from tensor memory, W rows at a time, warps
+// w and w + 4 in turn.  Neighbouring lanes exchange values, so that a lane holds two columns of every second
+// row.
+template <Policy P, int TN>
+__device__ __forceinline__ void finish_rows(const SplitParams &p, uint32_t tmem, int mt, int n0, uint64_t *bar_acc,
+                                            const Guard &g)
+{
+    constexpr int W = TN < 64 ? 16 : 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quarter = warp & 3, odd = lane & 1;
+    const int col = n0 + quarter * 32 + lane - odd;   // and the next; p.N is even
+    const bool cols = col < p.N;
+    const int head = P == Dx ? col / p.dk : 0, in_head = P == Dx ? col - head * p.dk : 0;
+    uint64_t b = 0, ws = 0;
+    if (P != Dx && p.bias && cols) b = __ldg(reinterpret_cast<const uint64_t *>(p.bias + col));
+    if (P == FwdQ8 && cols) ws = __ldg(reinterpret_cast<const uint64_t *>(p.w_scale + col));
+    bool ready = false;
+#pragma unroll 1
+    for (int c = (warp >> 2) * W; c < TN; c += 2 * W) {   // (rb >= W: W rows lie in one block)
+        const int at = mt * TN + c, block = at / p.rb, grp = block / p.rblocks;
+        const int i0 = (block - grp * p.rblocks) * p.rb + at % p.rb + odd;
+        const int rows = block < p.n_rblocks && cols ? min(W, p.T - i0) : 0;   // of this lane: 0, 2, 4.. below it
+        const size_t step = P == Dx ? p.dk : p.N;
+        const size_t out = P == Dx ? (((size_t)grp * p.H + head) * p.T + i0) * p.dk + in_head
+                                   : ((size_t)grp * p.T + i0) * p.N + col;
+        uint32_t res[W / 2] = {};
+        float xs[W / 2] = {};
+#pragma unroll
+        for (int k = 0; k < W / 2; ++k)
+            if (2 * k < rows) {
+                if (P != Dx && p.residual) res[k] = *reinterpret_cast<const uint32_t *>(p.residual + out + 2 * k * step);
+                if (P == FwdQ8) xs[k] = p.x_scale[(size_t)grp * p.T + i0 + 2 * k];
+            }
+        if (!ready) {
+            wait_bounded(bar_acc, 0, g);
+            ptx::tc_fence_after();
+            ready = true;
+        }
+        uint32_t v[W];
+        if constexpr (W == 16)
+            ptx::tmem_ld16(tmem + ((uint32_t)(quarter * 32) << 16) + c, v);
+        else
+            ptx::tmem_ld32(tmem + ((uint32_t)(quarter * 32) << 16) + c, v);
+        ptx::tmem_ld_wait();
+        reg_fence(v);
+        uint64_t f[W / 2];
+#pragma unroll
+        for (int k = 0; k < W / 2; ++k) {
+            const uint32_t other = __shfl_xor_sync(~0u, odd ? v[2 * k] : v[2 * k + 1], 1);
+            f[k] = odd ? ptx::f2_pack(__uint_as_float(other), __uint_as_float(v[2 * k + 1]))
+                       : ptx::f2_pack(__uint_as_float(v[2 * k]), __uint_as_float(other));
+            if (P == FwdQ8) f[k] = ptx::fma_f32x2(f[k], ptx::mul_f32x2(ws, f2_both(xs[k])), b);
+            if (P == Fwd) f[k] = ptx::add_f32x2(f[k], b);
+        }
+        auto put = [&](__nv_bfloat16 *to) {
+#pragma unroll
+            for (int k = 0; k < W / 2; ++k) {
+                float lo, hi;
+                ptx::f2_unpack(f[k], lo, hi);
+                if (2 * k < rows) *reinterpret_cast<uint32_t *>(to + out + 2 * k * step) = ptx::pack_bf16x2(lo, hi);
+            }
+        };
+        if (P == Fwd && p.z) put(p.z);
+        if (P != Dx) {
+            activate(f, p.act);
+            if (p.residual) {
+#pragma unroll
+                for (int k = 0; k < W / 2; ++k)
+                    f[k] = ptx::add_f32x2(f[k], ptx::f2_pack(__uint_as_float(res[k] << 16),
+                                                             __uint_as_float(res[k] & 0xffff0000u)));
+            }
+        }
+        put(p.y);
+    }
+}
+
 template <Policy P, int TN>
 __global__ void __launch_bounds__(256) gemm_split_kernel(const __grid_constant__ CUtensorMap map_w,
                                                          const __grid_constant__ CUtensorMap map_x,
@@ -758,7 +834,7 @@ __global__ void __launch_bounds__(256) gemm_split_kernel(const __grid_constant__
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = tmem_sh, recv = ptx::smem_u32(smem + STAGES * C::STAGE);
-    ptx::cluster_arrive();
+    if (splits > 1) ptx::cluster_arrive();
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
 
@@ -828,7 +904,7 @@ __global__ void __launch_bounds__(256) gemm_split_kernel(const __grid_constant__
             ptx::mma_commit(&bar_acc);
             wait_bounded(&bar_acc, 0, g);
         }
-    } else if (warp >= 4) {
+    } else if (warp >= 4 && splits > 1) {
         // the rows of the partial tile to their owners: row r to rank r mod splits as its row r / splits
         const int quarter = warp & 3, log2s = 31 - __clz(splits);
         const uint32_t mine = recv + ((uint32_t)(rank * (TN / splits)) * 128 + quarter * 32 + lane) * 4;
@@ -858,13 +934,18 @@ __global__ void __launch_bounds__(256) gemm_split_kernel(const __grid_constant__
         ptx::tc_fence_before();
     }
     __syncwarp();
-    if (warp < 4) ptx::cluster_wait();
-    ptx::cluster_arrive();   // this CTA's rows are sent
-    switch (splits) {        // (the wait for the others is in there)
-    case 1: join_rows<P, TN, 1>(p, recv, rank, mt, n0); break;
-    case 2: join_rows<P, TN, 2>(p, recv, rank, mt, n0); break;
-    case 4: join_rows<P, TN, 4>(p, recv, rank, mt, n0); break;
-    default: join_rows<P, TN, 8>(p, recv, rank, mt, n0); break;
+    if (splits == 1) {
+        finish_rows<P, TN>(p, tmem, mt, n0, &bar_acc, g);
+        ptx::tc_fence_before();
+        __syncthreads();
+    } else {
+        if (warp < 4) ptx::cluster_wait();
+        ptx::cluster_arrive();   // this CTA's rows are sent
+        switch (splits) {        // (the wait for the others is in there)
+        case 2: join_rows<P, TN, 2>(p, recv, rank, mt, n0); break;
+        case 4: join_rows<P, TN, 4>(p, recv, rank, mt, n0); break;
+        default: join_rows<P, TN, 8>(p, recv, rank, mt, n0); break;
+        }
     }
     if (warp == 1) {
         ptx::tc_fence_after();
@@ -991,9 +1072,10 @@ int split_slots(int tn, int s)
 }
 
 // The plan with the least estimated time, in us.  The terms are fitted to a sweep of every plan over 1
-// to 2048 rows at K, N from 768 to 8192 (the chosen plan takes 0.2 % more than the best one there on
-// average, 9 % at most): start, join and end; a K step 0.21, or what the ring of stages leaves of the memory's latency once all SMs
-// load, or the steps' bytes at L2's rate of 15 TB/s, or the weights at HBM's.
+// to 8192 rows at sixteen sizes of K and N from 64 to 8192 (the chosen plan takes 0.7 % more than the best
+// one there on average, 12 % at most): start, join and end; a K step 0.27, or what the ring of stages leaves of
+// the memory's latency once all SMs load, or the steps' bytes at L2's rate of 18 TB/s, or the weights at HBM's
+// and L2's.
 SplitPlan split_plan(int G, int T, int N, int ksteps)
 {
     SplitPlan best{};
@@ -1009,13 +1091,14 @@ SplitPlan split_plan(int G, int T, int N, int ksteps)
             const int steps = ceil_div(ksteps, s);
             const bool two = ctas > 2 * kPlanPairs;   // on some SMs
             const int stages = tn == 64 ? 3 : tn == 32 ? 4 : 5;
-            const double ring = 1.4 / stages * (ctas < 2 * kPlanPairs ? ctas / (2.0 * kPlanPairs) : 1.0);
-            const double l2 = (double)steps * ctas * (16384 + tn * 128) / 15e6;
-            const double hbm = (double)ksteps * 128 * N / (two ? 6.2e6 : 5.6e6);
-            double loop = steps * (ring > 0.21 ? ring : 0.21);
+            const double ring = 1.16 / stages * (ctas < 2 * kPlanPairs ? ctas / (2.0 * kPlanPairs) : 1.0);
+            const double l2 = (double)steps * ctas * (16384 + tn * 128) / 18e6;
+            const double hbm = (double)ksteps * 128 * N / (two ? 10e6 : 9e6);
+            double loop = steps * (ring > 0.27 ? ring : 0.27);
             loop = loop > l2 ? loop : l2;
             loop = loop > hbm ? loop : hbm;
-            const double us = 2.9 + tn * (0.024 + 0.047 / (s * s)) + (two ? 0.35 : 0.0) + loop;
+            const double ends = s == 1 ? 3.6 + tn * 0.024 : 3.25 + tn * (0.031 + 0.0315 / (s * s));
+            const double us = ends + (two ? 0.62 : 0.0) + loop;
             if (us < best.us) best = SplitPlan{tn, s, (int)tiles, us};
         }
         if (tn >= M) break;
@@ -1085,12 +1168,12 @@ struct PairPlan {
     double us;
 };
 
-constexpr double kStepWide = 0.285, kStepNarrow = 0.205;   // us a K step (the sweep of split_plan)
+constexpr double kStepWide = 0.246, kStepNarrow = 0.212;   // us a K step (the sweep of split_plan)
 
 PairPlan pair_plan(long long mtiles, int N, int ksteps)
 {
     auto rounds = [&](int bn) { return (double)((mtiles * ceil_div(N, bn) + kPlanPairs - 1) / kPlanPairs); };
-    const double w = 5.5 + rounds(256) * ksteps * kStepWide, n = 4.8 + rounds(128) * ksteps * kStepNarrow;
+    const double w = 6.35 + rounds(256) * ksteps * kStepWide, n = 5.45 + rounds(128) * ksteps * kStepNarrow;
     return w <= n ? PairPlan{true, w} : PairPlan{false, n};
 }
 
