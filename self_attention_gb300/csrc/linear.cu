@@ -649,10 +649,11 @@ struct SplitCfg {
 };
 
 // After every CTA of the cluster has arrived: sums this CTA's rows over the S ranks, in order, and finishes
-// them, a warp a row, 4 columns a lane.  What a row's epilogue reads is asked for a row ahead, the first
-// row's before the wait for the cluster.
+// them, a warp a row, 4 columns a lane (b, ws: their bias and scales).  What a row's epilogue reads is asked
+// for a row ahead, the first row's before the wait for the cluster.
 template <Policy P, int TN, int S>
-__device__ __forceinline__ void join_rows(const SplitParams &p, uint32_t recv, int rank, int mt, int n0)
+__device__ __forceinline__ void join_rows(const SplitParams &p, uint32_t recv, int rank, int mt, int n0, ulonglong2 b,
+                                          ulonglong2 ws)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = n0 + lane * 4;
     struct Row {
@@ -683,9 +684,6 @@ __device__ __forceinline__ void join_rows(const SplitParams &p, uint32_t recv, i
         return w;
     };
     Row next = ask(warp);
-    ulonglong2 b = make_ulonglong2(0, 0), ws = b;
-    if (P != Dx && p.bias && col < p.N) b = __ldg(reinterpret_cast<const ulonglong2 *>(p.bias + col));
-    if (P == FwdQ8 && col < p.N) ws = __ldg(reinterpret_cast<const ulonglong2 *>(p.w_scale + col));
     ptx::cluster_wait();
     for (int l = warp; l < TN / S; l += 8) {
         const Row w = next;
@@ -719,24 +717,24 @@ __device__ __forceinline__ void join_rows(const SplitParams &p, uint32_t recv, i
     }
 }
 
+// The two columns that a lane finishes where K is not split (p.N is even).
+__device__ __forceinline__ int lane_col(int n0) { return n0 + (threadIdx.x & 126); }
+
 // K is not split: each warp finishes a 32-column strip of the tile from tensor memory, W rows at a time, warps
-// w and w + 4 in turn.  Neighbouring lanes exchange values, so that a lane holds two columns of every second
-// row.
+// w + 4, which have had no other work, and w in turn.  Neighbouring lanes exchange values, so that a lane holds
+// two columns of every second row.  b, ws: bias and scales of the columns.
 template <Policy P, int TN>
-__device__ __forceinline__ void finish_rows(const SplitParams &p, uint32_t tmem, int mt, int n0, uint64_t *bar_acc,
-                                            const Guard &g)
+__device__ __forceinline__ void finish_rows(const SplitParams &p, uint32_t tmem, int mt, int n0, uint64_t b, uint64_t ws,
+                                            uint64_t *bar_acc, const Guard &g)
 {
     constexpr int W = TN < 64 ? 16 : 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quarter = warp & 3, odd = lane & 1;
-    const int col = n0 + quarter * 32 + lane - odd;   // and the next; p.N is even
+    const int col = lane_col(n0);
     const bool cols = col < p.N;
     const int head = P == Dx ? col / p.dk : 0, in_head = P == Dx ? col - head * p.dk : 0;
-    uint64_t b = 0, ws = 0;
-    if (P != Dx && p.bias && cols) b = __ldg(reinterpret_cast<const uint64_t *>(p.bias + col));
-    if (P == FwdQ8 && cols) ws = __ldg(reinterpret_cast<const uint64_t *>(p.w_scale + col));
     bool ready = false;
 #pragma unroll 1
-    for (int c = (warp >> 2) * W; c < TN; c += 2 * W) {   // (rb >= W: W rows lie in one block)
+    for (int c = (warp >> 2 ^ 1) * W; c < TN; c += 2 * W) {   // (rb >= W: W rows lie in one block)
         const int at = mt * TN + c, block = at / p.rb, grp = block / p.rblocks;
         const int i0 = (block - grp * p.rblocks) * p.rb + at % p.rb + odd;
         const int rows = block < p.n_rblocks && cols ? min(W, p.T - i0) : 0;   // of this lane: 0, 2, 4.. below it
@@ -837,6 +835,18 @@ __global__ void __launch_bounds__(256) gemm_split_kernel(const __grid_constant__
     if (splits > 1) ptx::cluster_arrive();
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
+    // asked for ahead of the roles: their latency is behind the first copies'
+    ulonglong2 b = make_ulonglong2(0, 0), ws = b;   // of two or four columns (see finish_rows, join_rows)
+    if (P != Dx) {
+        const int c2 = lane_col(n0), c4 = n0 + lane * 4;
+        if (splits == 1 && c2 < p.N) {
+            if (p.bias) b.x = __ldg(reinterpret_cast<const uint64_t *>(p.bias + c2));
+            if (P == FwdQ8) ws.x = __ldg(reinterpret_cast<const uint64_t *>(p.w_scale + c2));
+        } else if (splits > 1 && c4 < p.N) {
+            if (p.bias) b = __ldg(reinterpret_cast<const ulonglong2 *>(p.bias + c4));
+            if (P == FwdQ8) ws = __ldg(reinterpret_cast<const ulonglong2 *>(p.w_scale + c4));
+        }
+    }
 
     if (warp == 0) {
         if (ptx::elect_one()) {
@@ -935,16 +945,16 @@ __global__ void __launch_bounds__(256) gemm_split_kernel(const __grid_constant__
     }
     __syncwarp();
     if (splits == 1) {
-        finish_rows<P, TN>(p, tmem, mt, n0, &bar_acc, g);
+        finish_rows<P, TN>(p, tmem, mt, n0, b.x, ws.x, &bar_acc, g);
         ptx::tc_fence_before();
         __syncthreads();
     } else {
         if (warp < 4) ptx::cluster_wait();
         ptx::cluster_arrive();   // this CTA's rows are sent
         switch (splits) {        // (the wait for the others is in there)
-        case 2: join_rows<P, TN, 2>(p, recv, rank, mt, n0); break;
-        case 4: join_rows<P, TN, 4>(p, recv, rank, mt, n0); break;
-        default: join_rows<P, TN, 8>(p, recv, rank, mt, n0); break;
+        case 2: join_rows<P, TN, 2>(p, recv, rank, mt, n0, b, ws); break;
+        case 4: join_rows<P, TN, 4>(p, recv, rank, mt, n0, b, ws); break;
+        default: join_rows<P, TN, 8>(p, recv, rank, mt, n0, b, ws); break;
         }
     }
     if (warp == 1) {
