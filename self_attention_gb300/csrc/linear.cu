@@ -146,6 +146,11 @@ __device__ __forceinline__ uint2 pack_bf16x4(const uint64_t (&f)[2])
     return make_uint2(ptx::pack_bf16x2(a, b), ptx::pack_bf16x2(c, d));
 }
 
+__device__ __forceinline__ void prefetch_l1(const void *p)
+{
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(__cvta_generic_to_global(p)) : "memory");
+}
+
 template <Policy P, int BN>
 __global__ void __launch_bounds__(128 + 32 * kEpiWarps, 1)
     gemm_pair_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmParams p)
@@ -412,6 +417,14 @@ __global__ void __launch_bounds__(128 + 32 * kEpiWarps, 1)
             };
             reclaim();
             if (lane == 0 && p.has_r && mine) load_res(0);
+            // what load_z reads is on its way to L1 while the warp waits for the accumulator
+            if (P == Fwd || P == FwdQ8) {
+                const int c = col0 + (lane & 1) * 32;
+                if (lane < 2 && mine && c < pr.N) {
+                    if (p.bias) prefetch_l1(p.bias + c);
+                    if (P == FwdQ8) prefetch_l1(p.w_scale + c);
+                }
+            }
             const uint64_t xs = f2_both((P == FwdQ8 && mine && i0 + lane < pr.T) ? p.x_scale[i0 + lane] : 0.f);
             wait_bounded(&bar_acc_full[ab], (li >> 1) & 1, g);
             ptx::tc_fence_after();
@@ -609,7 +622,7 @@ __global__ void __launch_bounds__(128 + 32 * kEpiWarps, 1)
     __syncwarp();
     ptx::tc_fence_before();
     __syncthreads();
-    ptx::cluster_sync();   // neither CTA leaves while the other may read its shared memory or signal it
+    ptx::cluster_sync_relaxed();   // neither CTA leaves while the other may read its shared memory or signal it
     if (warp == 1) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc_pair(tmem, C::TM_COLS);
