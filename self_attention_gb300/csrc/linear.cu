@@ -1095,9 +1095,9 @@ int split_slots(int tn, int s)
 }
 
 // The plan with the least estimated time, in us.  The terms are fitted to a sweep of every plan over 1
-// to 8192 rows at sixteen sizes of K and N from 64 to 8192 (the chosen plan takes 0.7 % more than the best
-// one there on average, 12 % at most): start, join and end; a K step 0.27, or what the ring of stages leaves of
-// the memory's latency once all SMs load, or the steps' bytes at L2's rate of 18 TB/s, or the weights at HBM's
+// to 8192 rows at sixteen sizes of K and N from 64 to 8192 (the chosen plan takes 0.5 % more than the best
+// one there on average, 11 % at most): start, join and end; a K step 0.26, or what the ring of stages leaves of
+// the memory's latency once all SMs load, or the steps' bytes at L2's rate of 20 TB/s, or the weights at HBM's
 // and L2's.
 SplitPlan split_plan(int G, int T, int N, int ksteps)
 {
@@ -1114,14 +1114,15 @@ SplitPlan split_plan(int G, int T, int N, int ksteps)
             const int steps = ceil_div(ksteps, s);
             const bool two = ctas > 2 * kPlanPairs;   // on some SMs
             const int stages = tn == 64 ? 3 : tn == 32 ? 4 : 5;
-            const double ring = 1.16 / stages * (ctas < 2 * kPlanPairs ? ctas / (2.0 * kPlanPairs) : 1.0);
-            const double l2 = (double)steps * ctas * (16384 + tn * 128) / 18e6;
-            const double hbm = (double)ksteps * 128 * N / (two ? 10e6 : 9e6);
-            double loop = steps * (ring > 0.27 ? ring : 0.27);
+            const double ring = 1.106 / stages * (ctas < 2 * kPlanPairs ? ctas / (2.0 * kPlanPairs) : 1.0);
+            const double l2 = (double)steps * ctas * (16384 + tn * 128) / 20.3e6;
+            const double hbm = (double)ksteps * 128 * N / (two ? 10.2e6 : 9.2e6);
+            double loop = steps * (ring > 0.258 ? ring : 0.258);
             loop = loop > l2 ? loop : l2;
             loop = loop > hbm ? loop : hbm;
-            const double ends = s == 1 ? 3.6 + tn * 0.024 : 3.25 + tn * (0.031 + 0.0315 / (s * s));
-            const double us = ends + (two ? 0.62 : 0.0) + loop;
+            const double ends = s == 1 ? 3.4 + tn * 0.0272 + (two ? 0.195 : 0.0)
+                                       : 3.72 + tn * (0.0281 + 0.0369 / (s * s)) + (two ? 0.56 : 0.0);
+            const double us = ends + loop;
             if (us < best.us) best = SplitPlan{tn, s, (int)tiles, us};
         }
         if (tn >= M) break;
@@ -1191,12 +1192,12 @@ struct PairPlan {
     double us;
 };
 
-constexpr double kStepWide = 0.246, kStepNarrow = 0.212;   // us a K step (the sweep of split_plan)
+constexpr double kStepWide = 0.298, kStepNarrow = 0.219;   // us a K step (the sweep of split_plan)
 
 PairPlan pair_plan(long long mtiles, int N, int ksteps)
 {
     auto rounds = [&](int bn) { return (double)((mtiles * ceil_div(N, bn) + kPlanPairs - 1) / kPlanPairs); };
-    const double w = 6.35 + rounds(256) * ksteps * kStepWide, n = 5.45 + rounds(128) * ksteps * kStepNarrow;
+    const double w = 5.58 + rounds(256) * ksteps * kStepWide, n = 4.975 + rounds(128) * ksteps * kStepNarrow;
     return w <= n ? PairPlan{true, w} : PairPlan{false, n};
 }
 
