@@ -356,10 +356,12 @@ __global__ void __launch_bounds__(128 + 32 * kEpiWarps, 1)
                 }
                 ptx::mma_commit_pair(&bar_acc_full[ab]);
             }
-            // every MMA must have finished before TMEM is released (matters after a timeout)
+            // every MMA must have finished before TMEM is released (matters after a timeout), and the last
+            // arrivals from the odd CTA must have come in before this one leaves
             for (int b = 0; b < 2 && b < li; ++b) {
                 const int last = li - 1 - ((li - 1 - b) & 1);
                 wait_bounded(&bar_acc_full[last & 1], (last >> 1) & 1, g);
+                wait_bounded(&bar_acc_empty[last & 1], (last >> 1) & 1, g);
             }
         }
     } else if (warp >= 4) {
@@ -622,7 +624,9 @@ __global__ void __launch_bounds__(128 + 32 * kEpiWarps, 1)
     __syncwarp();
     ptx::tc_fence_before();
     __syncthreads();
-    ptx::cluster_sync_relaxed();   // neither CTA leaves while the other may read its shared memory or signal it
+    // neither CTA leaves while the other may read its shared memory or signal it (each has waited for what it
+    // was sent: the even one for the accumulators' release, the odd one's producer for every stage's)
+    ptx::cluster_sync_relaxed();
     if (warp == 1) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc_pair(tmem, C::TM_COLS);
@@ -697,6 +701,7 @@ __device__ __forceinline__ void join_rows(const SplitParams &p, uint32_t recv, i
         return w;
     };
     Row next = ask(warp);
+    __syncwarp();
     ptx::cluster_wait();
     for (int l = warp; l < TN / S; l += 8) {
         const Row w = next;
@@ -936,6 +941,7 @@ __global__ void __launch_bounds__(256) gemm_split_kernel(const __grid_constant__
         const int valid = p.n_rblocks == p.rblocks ? min(TN, p.T - mt * TN) : TN;
         if (nk > 0) wait_bounded(&bar_acc, 0, g);
         ptx::tc_fence_after();
+        __syncwarp();
         ptx::cluster_wait();   // every CTA of the cluster runs
         constexpr int W = TN < 32 ? 16 : 32;   // columns read at a time
 #pragma unroll 1
