@@ -95,6 +95,11 @@ __device__ __forceinline__ void tma_load_3d_pair(void *smem_dst, const CUtensorM
 // grid_dep_wait() returns when that one has completed and its writes are visible; a thread calls it
 // before its first access to global memory (every thread does, so that a grid's end always implies
 // the end of the grids before it).  grid_dep_launch() lets the next kernel start.
+//
+// What is read after grid_dep_wait() may have been written by that kernel, so while this one was running:
+// such operands are read by ordinary loads (or TMA), which the wait orders.  Non-coherent ones (__ldg,
+// ld.global.nc, const __restrict__ parameters) hold only for memory that nobody writes in the kernel's whole
+// lifetime: the compiler may move them above the wait, and they may hit stale lines.
 // ------------------------------------------------------------------------------------------
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

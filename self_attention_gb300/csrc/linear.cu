@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(128 + 32 * kEpiWarps, 1)
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
                         const int col = col0 + half * 32 + q * 4;
-                        bias[q] = p.bias && col < pr.N ? __ldg(reinterpret_cast<const ulonglong2 *>(p.bias + col))
+                        bias[q] = p.bias && col < pr.N ? *reinterpret_cast<const ulonglong2 *>(p.bias + col)
                                                        : make_ulonglong2(0, 0);
                     }
                 }
@@ -483,8 +483,8 @@ __global__ void __launch_bounds__(128 + 32 * kEpiWarps, 1)
                     if constexpr (P == FwdQ8) {
                         const int col = col0 + half * 32 + q * 4;
                         ulonglong2 b = make_ulonglong2(0, 0), ws = b;
-                        if (p.bias && col < pr.N) b = __ldg(reinterpret_cast<const ulonglong2 *>(p.bias + col));
-                        if (col < pr.N) ws = __ldg(reinterpret_cast<const ulonglong2 *>(p.w_scale + col));
+                        if (p.bias && col < pr.N) b = *reinterpret_cast<const ulonglong2 *>(p.bias + col);
+                        if (col < pr.N) ws = *reinterpret_cast<const ulonglong2 *>(p.w_scale + col);
                         f[2 * q] = ptx::fma_f32x2(f[2 * q], ptx::mul_f32x2(ws.x, xs), b.x);
                         f[2 * q + 1] = ptx::fma_f32x2(f[2 * q + 1], ptx::mul_f32x2(ws.y, xs), b.y);
                     } else if constexpr (P == Fwd) {
@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(128 + 32 * kEpiWarps, 1)
 #pragma unroll
                     for (int k = 0; k < 16; ++k)
                         v[k] = m + 4 * k < p.sum_m && n < p.col_n
-                                   ? __ldg(reinterpret_cast<const uint4 *>(p.sum_x + (size_t)(m + 4 * k) * p.col_n + n))
+                                   ? *reinterpret_cast<const uint4 *>(p.sum_x + (size_t)(m + 4 * k) * p.col_n + n)
                                    : make_uint4(0, 0, 0, 0);
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
@@ -597,7 +597,7 @@ __global__ void __launch_bounds__(128 + 32 * kEpiWarps, 1)
                         uint4 v[16];
 #pragma unroll
                         for (int k = 0; k < 16; ++k)
-                            v[k] = m + k < m1 ? __ldg(reinterpret_cast<const uint4 *>(p.sum_x + (size_t)(m + k) * p.col_n + n))
+                            v[k] = m + k < m1 ? *reinterpret_cast<const uint4 *>(p.sum_x + (size_t)(m + k) * p.col_n + n)
                                               : make_uint4(0, 0, 0, 0);
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
@@ -858,11 +858,11 @@ __global__ void __launch_bounds__(256) gemm_split_kernel(const __grid_constant__
     if (P != Dx) {
         const int c2 = lane_col(n0), c4 = n0 + lane * 4;
         if (splits == 1 && c2 < p.N) {
-            if (p.bias) b.x = __ldg(reinterpret_cast<const uint64_t *>(p.bias + c2));
-            if (P == FwdQ8) ws.x = __ldg(reinterpret_cast<const uint64_t *>(p.w_scale + c2));
+            if (p.bias) b.x = *reinterpret_cast<const uint64_t *>(p.bias + c2);
+            if (P == FwdQ8) ws.x = *reinterpret_cast<const uint64_t *>(p.w_scale + c2);
         } else if (splits > 1 && c4 < p.N) {
-            if (p.bias) b = __ldg(reinterpret_cast<const ulonglong2 *>(p.bias + c4));
-            if (P == FwdQ8) ws = __ldg(reinterpret_cast<const ulonglong2 *>(p.w_scale + c4));
+            if (p.bias) b = *reinterpret_cast<const ulonglong2 *>(p.bias + c4);
+            if (P == FwdQ8) ws = *reinterpret_cast<const ulonglong2 *>(p.w_scale + c4);
         }
     }
 

@@ -58,7 +58,7 @@ __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi)
 
 __device__ __forceinline__ void load8(const float *p, float (&f)[8])
 {
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    const float4 a = *reinterpret_cast<const float4 *>(p), b = *(reinterpret_cast<const float4 *>(p) + 1);
     f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
     f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
 }
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(bwd_threads(TPR, CH), bwd_blocks_per_sm(CH))
     for (int i = threadIdx.x; i < a.D / 4; i += THREADS) {
         const int chunk = i >> 1;
         reinterpret_cast<float4 *>(weights)[(chunk / TPR * 2 + (i & 1)) * TPR + chunk % TPR] =
-            __ldg(reinterpret_cast<const float4 *>(a.weight) + i);
+            *(reinterpret_cast<const float4 *>(a.weight) + i);
     }
     __syncthreads();
     const uint32_t wt = ptx::smem_u32(weights) + t * 16;
