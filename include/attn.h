@@ -231,9 +231,11 @@ attn_status attn_qkv_proj_bwd(const void *x, const void *w_q, const void *w_k, c
  * The rest of a transformer block around the attention: the linear layers with their epilogue,
  * the root-mean-square norm, and the 8-bit forms of both.  Shared rules:
  *   - Matrices are dense, row-major bf16 (or e4m3 with fp32 scales where a name ends in _q8);
- *     vectors (bias, norm weight, scales, 1/rms) are fp32.  M counts rows (tokens), 0 <= M < 2^31;
- *     with M = 0 the forward calls do nothing and the backward calls write zeros to the gradients
- *     of the parameters.
+ *     vectors (bias, norm weight, scales, 1/rms) are fp32.  M counts rows (tokens), 0 <= M < 2^31
+ *     (the linear layers: M <= 2^31 - 256, and with several sequences and heads (attn_out_proj) the
+ *     sequences, each padded to a multiple of 32 rows, together that many; more are refused with
+ *     ATTN_ERR_INVALID_ARG, and their workspace sizes are 0).  With M = 0 the forward calls do nothing
+ *     and the backward calls write zeros to the gradients of the parameters.
  *   - Widths (K, N_out, D) are multiples of 8 (K of e4m3 operands: 16) and below 2^20; no operand holds
  *     2^40 elements or more.  Other widths are refused with ATTN_ERR_INVALID_ARG.
  *   - Pointers are 16-byte aligned, and outputs overlap no input and no other output, except

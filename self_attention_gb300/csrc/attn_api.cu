@@ -810,21 +810,13 @@ attn_status check_operands(const Operand (&ins)[NI], const Operand (&outs)[NO], 
     return ATTN_OK;
 }
 
-attn_status check_linear_sizes(long long M, long long K, long long N_out, int act, int unit)
+// M rows as G groups of T each.
+attn_status check_linear_sizes(int G, int T, long long K, long long N_out, int act, int unit)
 {
-    if (M < 0 || M > 0x7fffffffLL || !width_ok(K, unit) || !width_ok(N_out, 8)) return ATTN_ERR_INVALID_ARG;
+    const long long M = (long long)G * T;
+    if (M < 0 || !width_ok(K, unit) || !width_ok(N_out, 8) || !lin_rows_fit(G, T)) return ATTN_ERR_INVALID_ARG;
     if (!size_ok(M, K) || !size_ok(M, N_out)) return ATTN_ERR_INVALID_ARG;
     if (act < ATTN_ACT_NONE || act > ATTN_ACT_SILU) return ATTN_ERR_INVALID_ARG;
-    return ATTN_OK;
-}
-
-// Heads side by side: sizes of the [B, H, N, d_k] view of the output projection's input.
-attn_status check_heads(int B, int H, int N, int d_k)
-{
-    if (d_k != 64 && d_k != 128) return ATTN_ERR_UNSUPPORTED_DK;
-    if (B < 1 || H < 1 || N < 1 || (long long)B * N > 0x7fffffffLL || (long long)B * H > 0x7fffffffLL ||
-        (long long)H * d_k >= (1LL << 20))
-        return ATTN_ERR_INVALID_ARG;
     return ATTN_OK;
 }
 
@@ -837,6 +829,18 @@ void set_heads(Args &a, int B, int H, int N, int d_k)
     a.H = plain ? 1 : H;
     a.T = plain ? B * N : N;
     a.dk = plain ? H * d_k : d_k;
+}
+
+// Sizes of the output projection, whose input's heads are put side by side.
+attn_status check_out_proj_sizes(int B, int H, int N, int d_k, int N_out)
+{
+    if (d_k != 64 && d_k != 128) return ATTN_ERR_UNSUPPORTED_DK;
+    if (B < 1 || H < 1 || N < 1 || (long long)B * N > 0x7fffffffLL || (long long)B * H > 0x7fffffffLL ||
+        (long long)H * d_k >= (1LL << 20))
+        return ATTN_ERR_INVALID_ARG;
+    LinArgs a = {};
+    set_heads(a, B, H, N, d_k);
+    return check_linear_sizes(a.G, a.T, (long long)H * d_k, N_out, ATTN_ACT_NONE, 8);
 }
 
 attn_status run_linear(LinArgs &a, cudaStream_t stream, const char *what)
@@ -906,7 +910,7 @@ extern "C" attn_status attn_linear(const void *x, const void *w, const float *bi
                                    void *y, void *z, int M, int K, int N_out, attn_activation act,
                                    cudaStream_t stream)
 {
-    attn_status st = check_linear_sizes(M, K, N_out, act, 8);
+    attn_status st = check_linear_sizes(1, M, K, N_out, act, 8);
     if (st != ATTN_OK) return st;
     if (M == 0) return ATTN_OK;
     LinArgs a = {};
@@ -919,8 +923,7 @@ extern "C" attn_status attn_linear(const void *x, const void *w, const float *bi
 extern "C" attn_status attn_out_proj(const void *o, const void *w, const float *bias, const void *residual,
                                      void *y, int B, int H, int N, int d_k, int N_out, cudaStream_t stream)
 {
-    attn_status st = check_heads(B, H, N, d_k);
-    if (st == ATTN_OK) st = check_linear_sizes((long long)B * N, (long long)H * d_k, N_out, ATTN_ACT_NONE, 8);
+    attn_status st = check_out_proj_sizes(B, H, N, d_k, N_out);
     if (st != ATTN_OK) return st;
     LinArgs a = {};
     a.x = o; a.w = w; a.bias = bias; a.residual = residual; a.y = y;
@@ -933,7 +936,7 @@ extern "C" attn_status attn_linear_q8(const void *xq, const float *x_scale, cons
                                       const float *w_scale, const float *bias, const void *residual, void *y,
                                       int M, int K, int N_out, attn_activation act, cudaStream_t stream)
 {
-    attn_status st = check_linear_sizes(M, K, N_out, act, 16);
+    attn_status st = check_linear_sizes(1, M, K, N_out, act, 16);
     if (st != ATTN_OK) return st;
     if (M == 0) return ATTN_OK;
     LinArgs a = {};
@@ -946,15 +949,13 @@ extern "C" attn_status attn_linear_q8(const void *xq, const float *x_scale, cons
 
 extern "C" size_t attn_linear_bwd_workspace_size(int M, int K, int N_out, attn_activation act)
 {
-    if (check_linear_sizes(M, K, N_out, act, 8) != ATTN_OK) return 0;
+    if (check_linear_sizes(1, M, K, N_out, act, 8) != ATTN_OK) return 0;
     return lin_bwd_layout(1, M, M, K, N_out, act).total;
 }
 
 extern "C" size_t attn_out_proj_bwd_workspace_size(int B, int H, int N, int d_k, int N_out)
 {
-    if (check_heads(B, H, N, d_k) != ATTN_OK ||
-        check_linear_sizes((long long)B * N, (long long)H * d_k, N_out, ATTN_ACT_NONE, 8) != ATTN_OK)
-        return 0;
+    if (check_out_proj_sizes(B, H, N, d_k, N_out) != ATTN_OK) return 0;
     LinBwdArgs a = {};
     set_heads(a, B, H, N, d_k);
     return lin_bwd_layout(a.G, a.T, B * N, H * d_k, N_out, ATTN_ACT_NONE).total;
@@ -964,7 +965,7 @@ extern "C" attn_status attn_linear_bwd(const void *x, const void *w, const void 
                                        void *dw, float *dbias, void *workspace, size_t workspace_bytes, int M,
                                        int K, int N_out, attn_activation act, cudaStream_t stream)
 {
-    attn_status st = check_linear_sizes(M, K, N_out, act, 8);
+    attn_status st = check_linear_sizes(1, M, K, N_out, act, 8);
     if (st != ATTN_OK) return st;
     LinBwdArgs a = {};
     a.x = x; a.w = w; a.dy = dy; a.z = z; a.dx = dx; a.dw = dw; a.dbias = dbias;
@@ -977,8 +978,7 @@ extern "C" attn_status attn_out_proj_bwd(const void *o, const void *w, const voi
                                          float *dbias, void *workspace, size_t workspace_bytes, int B, int H,
                                          int N, int d_k, int N_out, cudaStream_t stream)
 {
-    attn_status st = check_heads(B, H, N, d_k);
-    if (st == ATTN_OK) st = check_linear_sizes((long long)B * N, (long long)H * d_k, N_out, ATTN_ACT_NONE, 8);
+    attn_status st = check_out_proj_sizes(B, H, N, d_k, N_out);
     if (st != ATTN_OK) return st;
     LinBwdArgs a = {};
     a.x = o; a.w = w; a.dy = dy; a.dx = d_o; a.dw = dw; a.dbias = dbias;

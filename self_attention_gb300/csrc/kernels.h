@@ -130,6 +130,8 @@ struct LinArgs {
     int act, q8;
     int *status;
 };
+// Whether the rows of G groups of T can be counted: padded to whole blocks and tiles they fit an int.
+bool lin_rows_fit(int G, int T);
 cudaError_t launch_linear(const LinArgs &a, cudaStream_t stream);
 
 struct LinBwdArgs {

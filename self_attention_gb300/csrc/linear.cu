@@ -994,10 +994,10 @@ __global__ void __launch_bounds__(256) dz_kernel(const LinBwdArgs a, int blocks)
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
     if (n < a.N) {
-        const int per = (a.M + blocks - 1) / blocks;
-        const long long m_end = min((long long)a.M, (long long)(blockIdx.y + 1) * per);
+        const long long per = ((long long)a.M + blocks - 1) / blocks;
+        const long long m_end = min((long long)a.M, (blockIdx.y + 1) * per);
         // two rows at a time: their loads are in flight together
-        for (long long m = (long long)blockIdx.y * per + warp; m < m_end; m += 16) {
+        for (long long m = blockIdx.y * per + warp; m < m_end; m += 16) {
             uint4 d4[2], z4[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k)
@@ -1161,13 +1161,14 @@ long long row_tiles(int G, int T)
     return (blocks + per - 1) / per;
 }
 
-// Fills in the rows and the tiles; false if there are too many to count in an int.
+// Fills in the rows and the tiles; false if there are too many to count in an int (see lin_rows_fit: the entry
+// points refuse such rows).
 bool set_tiles(Prob &q, int G, int T, int N, int bn, int splits)
 {
     const int rb = row_block(G), rblocks = ceil_div(T, rb);
     const long long mtiles = row_tiles(G, T), tiles = mtiles * ceil_div(N, bn);
     // the kernel counts rows, those that pad a block included, and items in ints
-    if (mtiles * BM > 0x7fffffffLL || tiles * splits > 0x7fffffffLL) return false;
+    if (!lin_rows_fit(G, T) || tiles * splits > 0x7fffffffLL) return false;
     q.T = T;
     q.rb_log2 = rb == 32 ? 5 : 7;
     q.rblocks = fast_div(rblocks);
@@ -1285,6 +1286,8 @@ void level_items(GemmParams &p, int clusters)
 }
 
 }  // namespace
+
+bool lin_rows_fit(int G, int T) { return row_tiles(G, T) * BM <= 0x7fffffffLL; }
 
 cudaError_t launch_linear(const LinArgs &a, cudaStream_t stream)
 {
