@@ -376,7 +376,15 @@ def _device_stream(dev, stream):
 
 
 def qkv_proj(x, w_q, w_k, w_v, H: int, stream=None):
-    """Q, K, V = X W_Q, X W_K, X W_V split into H heads: x [B,N,D] bf16 -> 3 x [B,H,N,D/H] bf16."""
+    """Q, K, V = X W_Q, X W_K, X W_V split into H heads: x [B,N,D] bf16 -> 3 x [B,H,N,D/H] bf16.
+    Where an input requires a gradient, with autograd support (by qkv_proj_backward())."""
+    if torch.is_grad_enabled() and any(getattr(t, "requires_grad", False) for t in (x, w_q, w_k, w_v)):
+        fn = _QkvProj.apply     # (its backward runs on the stream that is current here)
+        return fn(x, w_q, w_k, w_v, H) if stream is None else _on(stream, fn, x, w_q, w_k, w_v, H)
+    return _qkv_proj(x, w_q, w_k, w_v, H, stream)
+
+
+def _qkv_proj(x, w_q, w_k, w_v, H: int, stream=None):
     B, N, D = x.shape
     with torch.cuda.device(x.device):
         st = _device_stream(x.device, stream)
@@ -481,6 +489,19 @@ def backward(q, k, v, o, dout, lse, scale: float | None = None, stream=None, wor
         fn = attn_bwd_deterministic if deterministic else attn_bwd
         fn(q, k, v, o, dout, lse, dq, dk, dv, workspace, workspace.numel(), B, H, N, D, scale, st)
     return dq, dk, dv
+
+
+class _QkvProj(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w_q, w_k, w_v, H):
+        ctx.save_for_backward(x, w_q, w_k, w_v)
+        return _qkv_proj(x, w_q, w_k, w_v, H)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dq, dk, dv):
+        grads = qkv_proj_backward(*ctx.saved_tensors, dq.contiguous(), dk.contiguous(), dv.contiguous())
+        return (*(g if need else None for g, need in zip(grads, ctx.needs_input_grad)), None)
 
 
 class _Attention(torch.autograd.Function):
