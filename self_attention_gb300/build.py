@@ -1,11 +1,11 @@
 """Builds the sm_103a shared library libattn_gb300.so in-tree with nvcc.
 
 Each .cu file is compiled as its own translation unit, in parallel, then linked into one
-shared library under self_attention_gb300/_build/.  The CUDA runtime is the shared one: a process
-that has loaded PyTorch then holds one runtime instead of two, which takes about 2 us off a call that
-follows a tensor's allocation (measured on the GB300's host).  The driver is reached through
-cudaGetDriverEntryPointByVersion, so no -lcuda is needed.  The tensor-level calls of the linear layers
-and the norm go through a small CPython extension beside the library (csrc/binding.cpp, g++).
+shared library under self_attention_gb300/_build/.  The CUDA runtime is linked statically, so that the
+library loads wherever the driver is, without a toolkit (the shared one, PyTorch's own in a process that
+has loaded it, was measured: the calls of csrc/binding.cpp take the same time with either).  The driver is
+reached through cudaGetDriverEntryPointByVersion, so no -lcuda is needed.  The tensor-level calls of the
+linear layers and the norm go through a small CPython extension beside the library (csrc/binding.cpp, g++).
 """
 from __future__ import annotations
 
@@ -100,9 +100,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         binding_obj = binding.result()
     objs = [o for o, _ in results]
     tmp = LIB_PATH + f".{tag}.tmp"
-    runtime = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(tool))), "lib64")
-    r = subprocess.run([tool, *ARCH, "-shared", "-cudart", "shared", "-Xlinker", f"-rpath={runtime}", "-o", tmp, *objs,
-                        "-ldl"], capture_output=True, text=True)
+    r = subprocess.run([tool, *ARCH, "-shared", "-o", tmp, *objs, "-ldl"], capture_output=True, text=True)
     for o in objs:
         os.remove(o)
     if r.returncode != 0:

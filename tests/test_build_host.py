@@ -1,0 +1,34 @@
+"""What the build makes, without a GPU."""
+import os
+import re
+import shutil
+import subprocess
+import sys
+
+import pytest
+
+from self_attention_gb300.build import LIB_PATH, build
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build()
+
+
+def _dynamic(path):
+    return subprocess.run(["readelf", "-d", path], capture_output=True, text=True, check=True).stdout
+
+
+def test_the_library_needs_no_toolkit(tmp_path):
+    """libattn_gb300.so carries its CUDA runtime and no path of the machine it was built on: a copy loads by
+    itself in a process without PyTorch and without library paths."""
+    text = _dynamic(LIB_PATH)
+    needed = re.findall(r"\(NEEDED\).*\[(.*)\]", text)
+    assert needed and not [n for n in needed if n.startswith(("libcuda", "libtorch", "libc10", "libpython"))], needed
+    assert not re.search(r"\((RPATH|RUNPATH)\)", text), text
+    copy = shutil.copy(LIB_PATH, tmp_path)
+    code = (f"import ctypes, sys; lib = ctypes.CDLL({str(copy)!r}); f = lib.attn_linear_bwd_workspace_size; "
+            "f.restype = ctypes.c_size_t; assert f(16, 64, 32, 2) > 0; assert 'torch' not in sys.modules")
+    env = {k: v for k, v in os.environ.items() if k not in ("LD_LIBRARY_PATH", "LD_PRELOAD")}
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, env=env, cwd=tmp_path)
+    assert r.returncode == 0, r.stderr
