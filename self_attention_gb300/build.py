@@ -38,10 +38,21 @@ def nvcc() -> str:
     return cand
 
 
-def _inputs_newest() -> float:
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "attn.h"),
-                                                                    os.path.abspath(__file__)]
-    return max(os.path.getmtime(f) for f in files)
+BINDING_SOURCE = "binding.cpp"
+
+
+def _newer(path: str, inputs) -> bool:
+    """Whether `path` is there and newer than its inputs and this file."""
+    inputs = [*inputs, os.path.join(INCLUDE, "attn.h"), os.path.abspath(__file__)]
+    return os.path.exists(path) and os.path.getmtime(path) >= max(os.path.getmtime(f) for f in inputs)
+
+
+def _library_fresh() -> bool:
+    return _newer(LIB_PATH, [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != BINDING_SOURCE])
+
+
+def _binding_fresh() -> bool:
+    return _newer(BINDING_PATH, [os.path.join(CSRC, BINDING_SOURCE)])
 
 
 def _torch_dir() -> str:
@@ -60,7 +71,7 @@ def _compile_binding(tool: str, tag: str) -> str:
     cuda_inc = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(tool))), "include")
     _run(["g++", "-O2", "-std=c++17", "-fPIC", f"-I{INCLUDE}", f"-I{torch_inc}",
           f"-I{os.path.join(torch_inc, 'torch', 'csrc', 'api', 'include')}", f"-I{cuda_inc}",
-          f"-I{sysconfig.get_paths()['include']}", "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj],
+          f"-I{sysconfig.get_paths()['include']}", "-c", os.path.join(CSRC, BINDING_SOURCE), "-o", obj],
          "g++ on binding.cpp")
     return obj
 
@@ -75,10 +86,10 @@ def _link_binding(obj: str, tag: str):
     os.replace(tmp, BINDING_PATH)
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile (if stale) the library and the Python binding; returns the path of libattn_gb300.so."""
-    newest = _inputs_newest()
-    if not force and all(os.path.exists(p) and os.path.getmtime(p) >= newest for p in (LIB_PATH, BINDING_PATH)):
+def build_library(force: bool = False, verbose: bool = False) -> str:
+    """Compile (if stale) libattn_gb300.so alone, which takes nvcc and nothing of Python's or PyTorch's;
+    returns its path."""
+    if not force and _library_fresh():
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     tool = nvcc()
@@ -94,10 +105,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(len(SOURCES) + 1) as ex:
-        binding = ex.submit(_compile_binding, tool, tag)
+    with cf.ThreadPoolExecutor(len(SOURCES)) as ex:
         results = list(ex.map(compile_one, SOURCES))
-        binding_obj = binding.result()
     objs = [o for o, _ in results]
     tmp = LIB_PATH + f".{tag}.tmp"
     r = subprocess.run([tool, *ARCH, "-shared", "-o", tmp, *objs, "-ldl"], capture_output=True, text=True)
@@ -106,10 +115,24 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
-    _link_binding(binding_obj, tag)
     if verbose:
         for _, log in results:
             print(log)
+    return LIB_PATH
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Compile (if stale) the library and the Python binding; returns the path of libattn_gb300.so.  A
+    binding that does not compile is an error, raised when the library is in its place."""
+    if not force and _library_fresh() and _binding_fresh():
+        return LIB_PATH
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    tag = f"{os.getpid()}"
+    with cf.ThreadPoolExecutor(1) as ex:    # beside the library's sources
+        obj = ex.submit(_compile_binding, nvcc(), tag) if force or not _binding_fresh() else None
+        build_library(force, verbose)
+    if obj is not None:
+        _link_binding(obj.result(), tag)
     return LIB_PATH
 
 

@@ -32,3 +32,27 @@ def test_the_library_needs_no_toolkit(tmp_path):
     env = {k: v for k, v in os.environ.items() if k not in ("LD_LIBRARY_PATH", "LD_PRELOAD")}
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, env=env, cwd=tmp_path)
     assert r.returncode == 0, r.stderr
+
+
+@pytest.fixture
+def elsewhere(tmp_path, monkeypatch):
+    """The build of one small source into an empty folder."""
+    import self_attention_gb300.build as b
+    monkeypatch.setattr(b, "BUILD_DIR", str(tmp_path))
+    monkeypatch.setattr(b, "LIB_PATH", str(tmp_path / b.LIB_NAME))
+    monkeypatch.setattr(b, "BINDING_PATH", str(tmp_path / "attn_binding.so"))
+    monkeypatch.setattr(b, "SOURCES", ["vector_add.cu"])
+    return b
+
+
+def test_a_binding_that_does_not_compile_leaves_the_library(elsewhere, monkeypatch):
+    def fail(*_):
+        raise RuntimeError("no compiler for the binding")
+
+    monkeypatch.setattr(elsewhere, "_compile_binding", fail)
+    with pytest.raises(RuntimeError, match="no compiler for the binding"):
+        elsewhere.build()
+    assert os.path.exists(elsewhere.LIB_PATH) and not os.path.exists(elsewhere.BINDING_PATH)
+    with pytest.raises(RuntimeError):       # and it is still an error the next time
+        elsewhere.build()
+    assert elsewhere.build_library() == elsewhere.LIB_PATH
