@@ -51,12 +51,23 @@ def _library_fresh() -> bool:
     return _newer(LIB_PATH, [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != BINDING_SOURCE])
 
 
-def _binding_fresh() -> bool:
-    return _newer(BINDING_PATH, [os.path.join(CSRC, BINDING_SOURCE)])
-
-
 def _torch_dir() -> str:
     return importlib.util.find_spec("torch").submodule_search_locations[0]
+
+
+def _binding_for() -> str:
+    """What the binding is built against: this interpreter, and the PyTorch it imports."""
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        return f"{sysconfig.get_config_var('SOABI')}\n{_torch_dir()}\n{f.read()}"
+
+
+def _binding_fresh() -> bool:
+    try:
+        with open(BINDING_PATH + ".for") as f:
+            same = f.read() == _binding_for()
+    except OSError:
+        return False
+    return same and _newer(BINDING_PATH, [os.path.join(CSRC, BINDING_SOURCE)])
 
 
 def _run(cmd, what):
@@ -84,6 +95,8 @@ def _link_binding(obj: str, tag: str):
          "linking the binding")
     os.remove(obj)
     os.replace(tmp, BINDING_PATH)
+    with open(BINDING_PATH + ".for", "w") as f:
+        f.write(_binding_for())
 
 
 def build_library(force: bool = False, verbose: bool = False) -> str:

@@ -56,3 +56,23 @@ def test_a_binding_that_does_not_compile_leaves_the_library(elsewhere, monkeypat
     with pytest.raises(RuntimeError):       # and it is still an error the next time
         elsewhere.build()
     assert elsewhere.build_library() == elsewhere.LIB_PATH
+
+
+def test_a_binding_for_another_pytorch_is_built_again(elsewhere, monkeypatch):
+    """Its C++ interface differs from version to version, whatever the files' times say."""
+    built = []
+    monkeypatch.setattr(elsewhere, "_compile_binding", lambda *_: built.append("compiled") or "object")
+    monkeypatch.setattr(elsewhere, "_run", lambda *_: open(elsewhere.BINDING_PATH + f".{os.getpid()}.tmp", "w").close())
+    monkeypatch.setattr(elsewhere.os, "remove", lambda path: None)
+    elsewhere.build()
+    elsewhere.build()
+    assert built == ["compiled"]
+    torch_dir = elsewhere._torch_dir()
+    other = os.path.join(elsewhere.BUILD_DIR, "torch")
+    os.makedirs(other)
+    with open(os.path.join(torch_dir, "version.py")) as f, open(os.path.join(other, "version.py"), "w") as g:
+        g.write(f.read().replace("__version__ = '", "__version__ = '9"))
+    monkeypatch.setattr(elsewhere, "_torch_dir", lambda: other)
+    elsewhere.build()
+    elsewhere.build()
+    assert built == ["compiled"] * 2
