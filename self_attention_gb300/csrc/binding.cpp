@@ -60,6 +60,15 @@ void *operand_or_null(PyObject *o, const char *name, c10::ScalarType type, c10::
     return o == Py_None ? nullptr : operand(o, name, type, shape, dev);
 }
 
+// One fp32 number a row.  A slice of rows starts on any element, the C ABI takes pointers to 16 bytes: those
+// numbers are copied first (on the current stream; call it with the device's guard set).
+const float *aligned(void *p, PyObject *o, at::Tensor &copy)
+{
+    if (reinterpret_cast<uintptr_t>(p) % 16 == 0) return static_cast<const float *>(p);
+    copy = THPVariable_Unpack(o).detach().clone();
+    return static_cast<const float *>(copy.data_ptr());
+}
+
 // Rows [..., width] of a contiguous CUDA tensor.
 struct Rows {
     const at::Tensor &t;
@@ -303,19 +312,19 @@ PyObject *linear_q8(Args a)
     matrix_columns(a[2], "wq");
     const int64_t N = THPVariable_Unpack(a[2]).size(0);
     const c10::DimVector shape = x.with(N);
-    const auto *xs = static_cast<const float *>(operand(a[1], "x_scale", kF32, x.lead(), x.dev));
+    void *xs = operand(a[1], "x_scale", kF32, x.lead(), x.dev);
     const void *w = operand(a[2], "wq", kE4m3, {N, x.width}, x.dev);
     const auto *ws = static_cast<const float *>(operand(a[3], "w_scale", kF32, {N}, x.dev));
     const auto *bias = static_cast<const float *>(operand_or_null(a[4], "bias", kF32, {N}, x.dev));
     const void *res = operand_or_null(a[5], "residual", kBf16, shape, x.dev);
     const auto act = static_cast<attn_activation>(integer(a[6]));
-    at::Tensor y;
+    at::Tensor y, copy;
     int code;
     {
         Unlocked u;
         const c10::cuda::CUDAGuard guard(x.dev);
         y = empty(shape, kBf16, x.dev);
-        code = attn_linear_q8(x.t.data_ptr(), xs, w, ws, bias, res, y.data_ptr(), count(x.M), count(x.width), count(N),
+        code = attn_linear_q8(x.t.data_ptr(), aligned(xs, a[1], copy), w, ws, bias, res, y.data_ptr(), count(x.M), count(x.width), count(N),
                               act, stream(x.dev));
     }
     check(code, "attn_linear_q8");
@@ -350,9 +359,9 @@ PyObject *rms_norm_backward(Args a)
     const Rows h(a[1], "h", kBf16);
     const void *dy = operand(a[0], "dy", kBf16, h.t.sizes(), h.dev);
     const auto *weight = static_cast<const float *>(operand(a[2], "weight", kF32, {h.width}, h.dev));
-    const auto *rstd = static_cast<const float *>(operand(a[3], "rstd", kF32, h.lead(), h.dev));
+    void *rstd = operand(a[3], "rstd", kF32, h.lead(), h.dev);
     const void *dh = operand_or_null(a[4], "dh", kBf16, h.t.sizes(), h.dev);
-    at::Tensor dx, dweight;
+    at::Tensor dx, dweight, copy;
     int code;
     {
         Unlocked u;
@@ -361,7 +370,7 @@ PyObject *rms_norm_backward(Args a)
         dweight = empty({h.width}, kF32, h.dev);
         const size_t bytes = attn_rms_norm_bwd_workspace_size(count(h.M), count(h.width));
         const at::Tensor ws = empty({(int64_t)(bytes ? bytes : 1)}, at::kByte, h.dev);
-        code = attn_rms_norm_bwd(dy, h.t.data_ptr(), weight, rstd, dh, dx.data_ptr(),
+        code = attn_rms_norm_bwd(dy, h.t.data_ptr(), weight, aligned(rstd, a[3], copy), dh, dx.data_ptr(),
                                  static_cast<float *>(dweight.data_ptr()), ws.data_ptr(), bytes, count(h.M),
                                  count(h.width), stream(h.dev));
     }
