@@ -647,8 +647,8 @@ def linear_q8(xq, x_scale, wq, w_scale, bias=None, residual=None, activation: st
 
 class _Linear(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, w, bias, residual, activation):
-        keep = activation != "none" and any(ctx.needs_input_grad[:3])
+    def forward(ctx, x, w, bias, residual, activation, graph):
+        keep = graph and activation != "none" and any(ctx.needs_input_grad[:3])
         out = linear_forward(x, w, bias, residual, activation, keep_z=keep)
         y, z = out if keep else (out, None)
         ctx.save_for_backward(x, w, z)
@@ -664,12 +664,13 @@ class _Linear(torch.autograd.Function):
         dx = dw = db = None
         if need_x or need_w or need_b:
             dx, dw, db = linear_backward(x, w, dy, z, ctx.activation, bias=need_b, need_dx=need_x, need_dw=need_w)
-        return dx, dw, db, dy if need_r else None, None
+        return dx, dw, db, dy if need_r else None, None, None
 
 
 def linear(x, w, bias=None, residual=None, activation: str = "none"):
     """act(x w + bias) + residual with autograd support (see linear_forward)."""
-    return _Linear.apply(x, w, bias, residual, activation)
+    # (leaves count as needing gradients where none are recorded, too)
+    return _Linear.apply(x, w, bias, residual, activation, torch.is_grad_enabled())
 
 
 class _OutProj(torch.autograd.Function):
