@@ -221,11 +221,13 @@ __global__ void __launch_bounds__(128 + 32 * kEpiWarps, 1)
         for (int b = 0; b < kEpiWarps; ++b) ptx::mbar_init(&bar_res[b], 1);
         ptx::fence_mbar_init();
     }
-    if (warp == 2 && ptx::elect_one()) {
-        ptx::tma_prefetch_desc(&maps.a);
-        ptx::tma_prefetch_desc(&maps.b);
-        if (P == Bwd || p.has_r) ptx::tma_prefetch_desc(&maps.a2);
-        if (P == Bwd) ptx::tma_prefetch_desc(&maps.b2);
+    if (warp == 2 && ptx::elect_one()) {   // (of the maps that there are)
+        if (P != Bwd || p.q[0].n_items > 0) {
+            ptx::tma_prefetch_desc(&maps.a);
+            ptx::tma_prefetch_desc(&maps.b);
+        }
+        if (P == Bwd ? p.q[1].n_items > 0 : p.has_r) ptx::tma_prefetch_desc(&maps.a2);
+        if (P == Bwd && p.q[1].n_items > 0) ptx::tma_prefetch_desc(&maps.b2);
     }
     if (warp == 1) {
         ptx::tmem_alloc_pair(&tmem_sh, C::TM_COLS);
@@ -1294,7 +1296,7 @@ cudaError_t launch_linear(const LinArgs &a, cudaStream_t stream)
     const int ksteps = ceil_div(a.K, a.q8 ? 128 : 64);
     const PairPlan plan = pair_plan(row_tiles(a.G, a.T), a.N, ksteps);
     const SplitPlan split = split_plan(a.G, a.T, a.N, ksteps);
-    GemmMaps m;
+    GemmMaps m = {};
     CUresult r;
     if (split.us < plan.us) {
         SplitParams sp = {};
@@ -1423,7 +1425,7 @@ cudaError_t launch_linear_bwd(const LinBwdArgs &a, cudaStream_t stream)
     if (!dx_left && !a.dw) return a.dbias ? launch_sum_rows(a.col_part, a.dbias, blocks, a.N, stream) : e;
 
     const int bn = plan.wide ? 256 : 128;
-    GemmMaps m;
+    GemmMaps m = {};
     GemmParams p = {};
     p.status = a.status;
     if (dx_left) {

@@ -49,3 +49,18 @@ def test_every_overlapped_kernel_waits_before_it_reads():
         for k in kernels:
             body = k.split("\n}\n")[0]
             assert body.count("grid_dep_wait()") == 1, f"{name}: {body[:80]}"
+
+
+def test_tensor_maps_that_are_not_made_are_not_touched():
+    """A launch may leave some of its maps out (a backward of one product alone): they are zeros, not what the
+    host's stack held, and the kernel prefetches none of them."""
+    code = _code("linear.cu")
+    assert not re.findall(r"\b(?:GemmMaps|GemmParams|SplitParams) \w+;", code)
+    block = re.search(r"if \(warp == 2 && ptx::elect_one\(\)\) \{(.*?)\n    \}\n", code, flags=re.S).group(1)
+    guards = {"maps.a2": "n_items > 0", "maps.b2": "n_items > 0"}
+    for line in block.splitlines():
+        for name, guard in guards.items():
+            if f"&{name})" in line:
+                assert guard in line, line
+    assert re.search(r"if \(P != Bwd \|\| p\.q\[0\]\.n_items > 0\) \{\s*ptx::tma_prefetch_desc\(&maps\.a\);\s*"
+                     r"ptx::tma_prefetch_desc\(&maps\.b\);\s*\}", block)
