@@ -352,6 +352,21 @@ attn_status attn_linear_q8(const void *xq, const float *x_scale, const void *wq,
                            attn_activation act, cudaStream_t stream);
 
 /*
+ * Diagnostics: the kernels that a call of the linear layers runs, a function of the sizes alone that is
+ * decided on the host (no GPU is needed).  kind: 0 attn_linear() / attn_out_proj(), 1 attn_linear_q8(),
+ * 2 attn_linear_bwd() / attn_out_proj_bwd() asked for all gradients.  x is [B, H, N, d_k] as in
+ * attn_out_proj(), or with B = H = 1 the plain [N, d_k] matrix.  Writes five ints:
+ *   plan[0]  rows of a tile of the few-row kernel (16 ... 128) where that makes y (kind 2: dx), else 0
+ *   plan[1]  its splits of the sum (1, 2, 4 or 8), else 0
+ *   plan[2]  columns of a tile of the pair kernel (128 or 256), 0 where it does not run
+ *   plan[3]  kind 2: ways in which dw's sum over the rows is split, else 0
+ *   plan[4]  kind 2: dbias from 0 a pass of its own, 1 whole columns or 2 slices of rows beside the products
+ * For tests, which assert that they reach every kernel.
+ */
+attn_status attn_debug_linear_plan(int kind, int B, int H, int N, int d_k, int N_out, attn_activation act,
+                                   int *plan);
+
+/*
  * Bytes of device workspace attn_fwd_unfused() needs: the fp32 score matrix S [B,H,N,N] and the
  * bf16 probabilities P [B,H,N,N], each region 256-byte aligned (6 B H N^2 bytes and padding).
  * Returns 0 if the sizes are unsupported.

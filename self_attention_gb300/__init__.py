@@ -37,7 +37,7 @@ __all__ = [
     "attn_rms_norm_bwd", "attn_rms_norm_bwd_workspace_size", "attn_rms_norm_q8", "attn_quantize_q8",
     "linear_forward", "linear_backward", "linear", "out_proj_forward", "out_proj_backward", "out_proj",
     "rms_norm_forward", "rms_norm_backward", "rms_norm", "rms_norm_q8", "quantize_q8", "linear_q8",
-    "ACTIVATIONS",
+    "attn_debug_linear_plan", "ACTIVATIONS",
     "load_library", "STATUS",
 ]
 
@@ -54,7 +54,7 @@ EXPORTS = ("attn_fwd", "attn_fwd_workspace_size", "attn_fwd_with_workspace", "at
            "attn_linear", "attn_out_proj", "attn_linear_bwd", "attn_linear_bwd_workspace_size",
            "attn_out_proj_bwd", "attn_out_proj_bwd_workspace_size", "attn_linear_q8", "attn_rms_norm",
            "attn_rms_norm_bwd", "attn_rms_norm_bwd_workspace_size", "attn_rms_norm_q8",
-           "attn_quantize_q8")
+           "attn_quantize_q8", "attn_debug_linear_plan")
 # attn_activation
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
@@ -130,7 +130,8 @@ def load_library(path: str = LIB_PATH):
                        ("attn_rms_norm", [_VP] * 6 + [_I] * 2 + [_F, _VP]),
                        ("attn_rms_norm_bwd", [_VP] * 8 + [_SZ] + [_I] * 2 + [_VP]),
                        ("attn_rms_norm_q8", [_VP] * 6 + [_I] * 2 + [_F, _VP]),
-                       ("attn_quantize_q8", [_VP] * 3 + [_I] * 2 + [_VP])):
+                       ("attn_quantize_q8", [_VP] * 3 + [_I] * 2 + [_VP]),
+                       ("attn_debug_linear_plan", [_I] * 7 + [_VP])):
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = _I
     for name, n in (("attn_linear_bwd_workspace_size", 4), ("attn_out_proj_bwd_workspace_size", 5),
@@ -413,6 +414,14 @@ def attn_get_device_status(stream=None) -> int:
 def attn_debug_wait_timeout(limit_us: int, stream=None):
     _raise(load_library().attn_debug_wait_timeout(int(limit_us), _stream(stream)),
            "attn_debug_wait_timeout")
+
+
+def attn_debug_linear_plan(kind: int, B: int, H: int, N: int, d_k: int, N_out: int, act: int = 0):
+    """(rows of a few-row tile, its splits, columns of a pair tile, splits of dw, way of dbias): the kernels that
+    a call of the linear layers runs, decided on the host from the sizes alone (see attn.h)."""
+    plan = (_I * 5)()
+    _raise(load_library().attn_debug_linear_plan(kind, B, H, N, d_k, N_out, int(act), plan), "attn_debug_linear_plan")
+    return tuple(plan)
 
 
 # ---------------------------------------------------------------- tensor-level convenience

@@ -987,6 +987,25 @@ extern "C" attn_status attn_out_proj_bwd(const void *o, const void *w, const voi
     return run_linear_bwd(a, workspace, workspace_bytes, stream, "attn_out_proj_bwd launch");
 }
 
+extern "C" attn_status attn_debug_linear_plan(int kind, int B, int H, int N, int d_k, int N_out, attn_activation act,
+                                              int *plan)
+{
+    if (!plan || kind < 0 || kind > 2) return ATTN_ERR_INVALID_ARG;
+    const bool plain = B == 1 && H == 1;
+    attn_status st = plain ? check_linear_sizes(1, N, d_k, N_out, act, kind == 1 ? 16 : 8)
+                           : check_out_proj_sizes(B, H, N, d_k, N_out);
+    if (st == ATTN_OK && (N < 1 || act < ATTN_ACT_NONE || act > ATTN_ACT_SILU)) st = ATTN_ERR_INVALID_ARG;
+    if (st == ATTN_OK && !plain && (kind == 1 || act != ATTN_ACT_NONE)) st = ATTN_ERR_INVALID_ARG;
+    if (st != ATTN_OK) return st;
+    LinArgs a = {};
+    set_heads(a, B, H, N, d_k);
+    if (kind == 2)
+        lin_bwd_plan(a.G, a.T, H * d_k, N_out, act != ATTN_ACT_NONE, plan);
+    else
+        lin_plan(a.G, a.T, H * d_k, N_out, kind == 1, plan);
+    return ATTN_OK;
+}
+
 namespace {
 
 attn_status check_norm_sizes(int M, int D, float eps)

@@ -132,6 +132,10 @@ struct LinArgs {
 };
 // Whether the rows of G groups of T can be counted: padded to whole blocks and tiles they fit an int.
 bool lin_rows_fit(int G, int T);
+// The plans that launch_linear() and launch_linear_bwd() (asked for everything) follow, as attn_debug_linear_plan()
+// gives them.
+void lin_plan(int G, int T, int K, int N, int q8, int plan[5]);
+void lin_bwd_plan(int G, int T, int K, int N, int has_act, int plan[5]);
 cudaError_t launch_linear(const LinArgs &a, cudaStream_t stream);
 
 struct LinBwdArgs {

@@ -1287,18 +1287,81 @@ void level_items(GemmParams &p, int clusters)
     p.x_early = (int)h.room(t, h.whole) - p.x_all;
 }
 
+// Which of the two kernels takes a forward product.
+struct FwdPlan {
+    bool few;          // the few-row kernel, by `split`; else the pair kernel
+    SplitPlan split;
+    bool wide;
+};
+
+FwdPlan fwd_plan(int G, int T, int K, int N, bool q8)
+{
+    const int ksteps = ceil_div(K, q8 ? 128 : 64);
+    const PairPlan pair = pair_plan(row_tiles(G, T), N, ksteps);
+    const SplitPlan split = split_plan(G, T, N, ksteps);
+    return FwdPlan{split.us < pair.us, split, pair.wide};
+}
+
+// How a backward runs: the plan of the products in one launch, whether dx goes to the few-row kernel beside dw
+// alone, and how the bias gradient is taken where dz is dy: where dw is taken too, the two idle warps of the
+// product kernel's CTAs read dy for it.  Each adds up whole columns where that (0.8 us for 64 rows) ends with the
+// products or within a join's time (196 x 768 x 768: 6.2 us, with the join 7.7; 16 x 1024 x 4096 10.3 and 17.8;
+// 1024 x 768 x 768 11.8 and 8.7).  Else slices of rows, which costs nothing while the products take longer, from
+// K of about 450 on (16 KB in flight a CTA against 4 K flops an element); else a pass of its own.
+enum BiasBy { kPass, kColumns, kSlices };
+struct BwdChoice {
+    BwdPlan plan;
+    SplitPlan split;
+    bool dx_split;
+    BiasBy bias;
+};
+
+BwdChoice bwd_choice(int G, int T, int K, int N, bool has_act, bool need_dx, bool need_dw)
+{
+    BwdChoice c{bwd_plan(G, T, K, N), SplitPlan{}, false, kPass};
+    if (need_dx) c.split = split_plan(G, T, K, ceil_div(N, 64));
+    c.dx_split = need_dx && c.split.us + c.plan.dw_us < c.plan.us;
+    if (has_act || !need_dw) return c;
+    const int col_warps = 4 * (N < 256 * kPlanPairs ? ceil_div(N, 256) : kPlanPairs);   // at least
+    const double direct_us = 0.8 * ceil_div((long long)G * T, 64) * ceil_div(ceil_div(N, 64), col_warps);
+    if (direct_us <= (need_dx && !c.dx_split ? c.plan.us : c.plan.dw_us) + 0.5)
+        c.bias = kColumns;
+    else if (K >= 512)
+        c.bias = kSlices;
+    return c;
+}
+
 }  // namespace
+
+void lin_plan(int G, int T, int K, int N, int q8, int plan[5])
+{
+    const FwdPlan f = fwd_plan(G, T, K, N, q8 != 0);
+    plan[0] = f.few ? f.split.tn : 0;
+    plan[1] = f.few ? f.split.splits : 0;
+    plan[2] = f.few ? 0 : f.wide ? 256 : 128;
+    plan[3] = plan[4] = 0;
+}
+
+void lin_bwd_plan(int G, int T, int K, int N, int has_act, int plan[5])
+{
+    const BwdChoice c = bwd_choice(G, T, K, N, has_act != 0, true, true);
+    plan[0] = c.dx_split ? c.split.tn : 0;
+    plan[1] = c.dx_split ? c.split.splits : 0;
+    plan[2] = c.plan.wide ? 256 : 128;
+    plan[3] = c.plan.splits;
+    plan[4] = c.bias;
+}
 
 bool lin_rows_fit(int G, int T) { return row_tiles(G, T) * BM <= 0x7fffffffLL; }
 
 cudaError_t launch_linear(const LinArgs &a, cudaStream_t stream)
 {
     const int ksteps = ceil_div(a.K, a.q8 ? 128 : 64);
-    const PairPlan plan = pair_plan(row_tiles(a.G, a.T), a.N, ksteps);
-    const SplitPlan split = split_plan(a.G, a.T, a.N, ksteps);
+    const FwdPlan plan = fwd_plan(a.G, a.T, a.K, a.N, a.q8 != 0);
+    const SplitPlan &split = plan.split;
     GemmMaps m = {};
     CUresult r;
-    if (split.us < plan.us) {
+    if (plan.few) {
         SplitParams sp = {};
         set_split_rows(sp, a.G, a.T, split.tn);
         sp.N = a.N;
@@ -1386,20 +1449,12 @@ cudaError_t launch_linear_bwd(const LinBwdArgs &a, cudaStream_t stream)
 {
     cudaError_t e = cudaSuccess;
     const int blocks = lin_bwd_row_blocks(a.M, a.N);
-    const BwdPlan plan = bwd_plan(a.G, a.T, a.K, a.N);
+    const BwdChoice choice = bwd_choice(a.G, a.T, a.K, a.N, a.z != nullptr, a.dx != nullptr, a.dw != nullptr);
+    const BwdPlan &plan = choice.plan;
     const int ksteps = ceil_div(a.N, 64);
-    // few rows: dx by the split kernel, beside dw alone
-    const SplitPlan split = a.dx ? split_plan(a.G, a.T, a.K, ksteps) : SplitPlan{};
-    const bool dx_split = a.dx && split.us + plan.dw_us < plan.us;
-    // Where dz is dy and dw is taken, the two idle warps of the product kernel's CTAs read dy for the bias
-    // gradient.  Each adds up whole columns where that (0.8 us for 64 rows) ends with the products or within
-    // a join's time (196 x 768 x 768: 6.2 us, with the join 7.7; 16 x 1024 x 4096 10.3 and 17.8; 1024 x 768 x
-    // 768 11.8 and 8.7).  Else slices of rows, which costs nothing while the products take longer, from K of
-    // about 450 on (16 KB in flight a CTA against 4 K flops an element); else a pass of its own.
-    const int col_warps = 4 * (a.N < 256 * kPlanPairs ? ceil_div(a.N, 256) : kPlanPairs);   // at least
-    const double direct_us = 0.8 * ceil_div(a.M, 64) * ceil_div(ceil_div(a.N, 64), col_warps);
-    const bool direct = a.dbias && !a.z && a.dw && direct_us <= (a.dx && !dx_split ? plan.us : plan.dw_us) + 0.5;
-    const bool beside = direct || (a.dbias && !a.z && a.dw && a.K >= 512);
+    const SplitPlan &split = choice.split;
+    const bool dx_split = choice.dx_split, direct = a.dbias && choice.bias == kColumns,
+               beside = a.dbias && choice.bias != kPass;
     if ((a.dbias && !beside) || (a.z && (a.dx || a.dw))) {
         e = launch_overlapped(dz_kernel, dim3(ceil_div(a.N, 256), blocks), 256, 0, 1, stream, a, blocks);
         if (e != cudaSuccess) return e;
