@@ -267,6 +267,8 @@ attn_status attn_linear(const void *x, const void *w, const float *bias, const v
  * Output projection: attn_linear() without an activation, reading attention's output in the
  * layout attn_fwd() writes it, so that the heads need no copy to be put side by side:
  *   y[b, i, :] = sum_h o[b, h, i, :] w[h d_k : (h+1) d_k, :] + bias + residual[b, i, :].
+ * As in attn_fwd(), B, H and N are at least 1: an empty batch is refused here and in the backward
+ * (ATTN_ERR_INVALID_ARG), not a call that does nothing.
  *   o : [B, H, N, d_k] bf16.   w : [H * d_k, N_out] bf16.   residual, y : [B, N, N_out] bf16.
  */
 attn_status attn_out_proj(const void *o, const void *w, const float *bias, const void *residual,
@@ -285,8 +287,10 @@ size_t attn_out_proj_bwd_workspace_size(int B, int H, int N, int d_k, int N_out)
  *   dy : [M, N_out] bf16.   z : [M, N_out] bf16 from attn_linear (null for ATTN_ACT_NONE).
  *   dx : [M, K] bf16, dw : [K, N_out] bf16, dbias : [N_out] fp32; each may be null (not computed).
  *   workspace : caller-owned, 256-byte aligned, at least the size above, overwritten.
- * dz is rounded to bf16 for the two products and summed unrounded for dbias.  All sums are in
- * fp32 in a fixed order: results are bitwise reproducible.
+ * dz is rounded to bf16 for the two products (the tensor cores' operands are bf16) and summed unrounded
+ * for dbias; without an activation it is dy and nothing is rounded before the outputs.  All sums are
+ * in fp32 in a fixed order: results are bitwise reproducible.  dw has the weights' type; gradients of
+ * many micro-batches are best added up in fp32 by the caller.
  */
 attn_status attn_linear_bwd(const void *x, const void *w, const void *dy, const void *z, void *dx,
                             void *dw, float *dbias, void *workspace, size_t workspace_bytes, int M,
@@ -345,7 +349,8 @@ attn_status attn_quantize_q8(const void *x, void *xq, float *scale, int M, int D
  * attn_linear() in 8 bits: z = x_scale[m] w_scale[n] (xq wq^T) + bias, y = act(z) + residual.
  *   xq : [M, K] e4m3, x_scale : [M] fp32.   wq : [N_out, K] e4m3 (one row an output column),
  *   w_scale : [N_out] fp32.   bias, residual, y as attn_linear.   K % 16 = 0, N_out % 8 = 0.
- * e4m3 products (exact) summed in fp32.
+ * e4m3 products (exact) summed in fp32.  The product of the two scales is formed first and has to be a
+ * normal fp32 number.
  */
 attn_status attn_linear_q8(const void *xq, const float *x_scale, const void *wq, const float *w_scale,
                            const float *bias, const void *residual, void *y, int M, int K, int N_out,

@@ -594,7 +594,7 @@ def linear_backward(x, w, dy, z=None, activation: str = "none", bias: bool = Tru
                     need_dw: bool = True, stream=None):
     """(dx [..., K] bf16, dw [K, N] bf16, dbias [N] fp32) of linear_forward() for dy = dL/dy; None
     for what is not asked for.  z: what linear_forward(keep_z=True) kept (none without an
-    activation).  The residual's gradient is dy itself."""
+    activation); dz = dy act'(z) is rounded to bf16 for the products.  The residual's gradient is dy itself."""
     fn, act = _binding().linear_backward, _act(activation)
     if stream is None:
         return fn(x, w, dy, z, act, bias, need_dx, need_dw)
