@@ -106,3 +106,37 @@ def test_qkv_proj_against_the_formula_and_differences():
     loss = lambda t: sum(((t @ w) * d).sum() for w, d in zip(w64, d64))  # noqa: E731
     diff = (loss(x64.view(-1, D) + e * v) - loss(x64.view(-1, D) - e * v)) / (2 * e)
     assert abs(float(diff - (dx * v).sum())) < 1e-6 * float((dx * v).abs().sum())
+
+
+def test_a_block_captured_and_replayed():
+    """Forward and backward of norm, QKV projection, attention and output projection in one graph, replayed on new
+    inputs: what the eager pass gives (its sums of dQ and dW may meet in another order: a bf16 step)."""
+    g = _gen("capture")
+    B, N, D, H = 2, 100, 128, 2
+    x, dy = _randn(g, B, N, D), _randn(g, B, N, D)
+    leaves = [t.requires_grad_() for t in (x, 1 + _randn(g, D, std=0.1, dtype=torch.float32),
+                                           *(_randn(g, D, D, std=0.1) for _ in range(4)))]
+
+    def step():
+        x, gain, wq, wk, wv, wo = leaves
+        q, k, v = sa.qkv_proj(sa.rms_norm(x, gain), wq, wk, wv, H)
+        y = sa.out_proj(sa.attention(q, k, v), wo, None, x)
+        return (y.detach(), *torch.autograd.grad(y, leaves, dy))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for _ in range(3):
+        with torch.no_grad():
+            x.copy_(_randn(g, B, N, D))
+            dy.copy_(_randn(g, B, N, D))
+        graph.replay()
+        for a, b in zip(got, step()):
+            assert float((a.double() - b.double()).norm()) <= 2 * ref.U8 * float(b.double().norm())
+    assert sa.attn_get_device_status() == 0
