@@ -372,6 +372,103 @@ attn_status attn_debug_linear_plan(int kind, int B, int H, int N, int d_k, int N
                                    int *plan);
 
 /*
+ * Positions, and a cache of keys and values for tokens that come one or a few at a time.  Shared rules:
+ *   - Tensors of heads are dense bf16 as above, d_k in {64, 128}: x [B, H, N, d_k], a cache [B, H, C, d_k] of
+ *     C slots a sequence and cached head, queries [B, H G, T, d_k] whose heads h G ... h G + G - 1 share the
+ *     cached head h.  `lengths` [B] int32 counts the slots in use, on the device: the host never reads it.
+ *   - Pointers to heads, `turns` and o start on 16 bytes, workspaces on 256, all others on their own elements.
+ *     Outputs overlap no input and no other output, except where an entry point allows it by name.
+ *   - Sizes: B H, B N, B T and the like below 2^31, no operand of 2^40 elements or more, H and H G at most
+ *     16384, C below 2^30.
+ */
+
+/*
+ * Rotary positions.  In each row the first `rotated` columns (a multiple of 16, at most d_k) are pairs
+ * (a, b), pair j turned by the angle t = position * f_j:
+ *     a' = amplitude (a cos t - b sin t);   b' = amplitude (a sin t + b cos t).
+ * interleaved = 0: pair j is columns j and j + rotated / 2; 1: columns 2 j and 2 j + 1.  The other columns are
+ * copied.
+ *   x : [B, H, N, d_k] bf16.   y : the same, output; may be x itself.
+ *   turns : [rotated / 2] uint64, f_j / (2 pi) in units of 2^-64: whole turns a position, modulo one.
+ *   positions : int32, null (row n is at position n), [N] (positions_stride 0) or [B, N] (positions_stride N);
+ *               any values, negative ones among them.
+ * The reduction of position * f_j is exact; the angle is off by at most 2^-25 of half a turn, products and sums
+ * are fp32, y is rounded once.  B, H or N = 0: nothing to do.
+ */
+attn_status attn_rotary(const void *x, void *y, const int *positions, long long positions_stride,
+                        const uint64_t *turns, int B, int H, int N, int d_k, int rotated, int interleaved,
+                        float amplitude, cudaStream_t stream);
+
+/* Its gradient: dx from dy, the turns taken backwards (with the same amplitude).  dx may be dy itself. */
+attn_status attn_rotary_bwd(const void *dy, void *dx, const int *positions, long long positions_stride,
+                            const uint64_t *turns, int B, int H, int N, int d_k, int rotated, int interleaved,
+                            float amplitude, cudaStream_t stream);
+
+/*
+ * New tokens into a cache: token rows[b, i] (i without `rows`) of sequence b goes to slot lengths[b] + i of every
+ * cached head, its key turned as by attn_rotary().  The lengths stay as they are: the slots count as used when the
+ * caller raises them.
+ *   k, v : [B, H, T, d_k] bf16.   cache_k, cache_v : [B, H, C, d_k] bf16, written in those slots alone.
+ *   turns : null (keys are copied), else with `rotated`, `interleaved` and `amplitude` as attn_rotary().
+ *   positions : [B, T] int32, or null: the slot's number.
+ *   rows : [B, n] int32 or null (n = T): the tokens that are taken (an accepted path of a tree, say); a
+ *          number below 0 or from T on leaves its slot as it was.
+ *   q, q_out : [B, Hq, T, d_k] bf16 or null: the tokens' queries, turned the same way into q_out (which may be q
+ *          itself).  Not together with `rows`.
+ *   weights : [B, H, C] fp32 or null: zeroed in the new slots.   slot_positions : [B, H, C] int32 or null: takes
+ *          the positions there.
+ * A length below 0 counts as 0; a slot from C on is not written.
+ */
+attn_status attn_cache_append(const void *k, const void *v, void *cache_k, void *cache_v, const int *lengths,
+                              const uint64_t *turns, const int *positions, const int *rows, const void *q,
+                              void *q_out, float *weights, int *slot_positions, int B, int H, int Hq, int T, int n,
+                              int d_k, int C, int rotated, int interleaved, float amplitude, cudaStream_t stream);
+
+/* Bytes of device workspace attn_cache_attention() needs (0 for sizes it rejects). */
+size_t attn_cache_attention_workspace_size(int B, int H, int G, int T, int C, int d_k);
+
+/*
+ * Attention of T tokens (1 ... 64; T = 1: the next token) of each sequence over its cache, in which they lie in slots
+ * lengths[b] ... lengths[b] + T - 1 (attn_cache_append()):
+ *     o = sum_j p_j v_j,   p_j = exp(scale q.k_j - lse),   lse = log sum_j exp(scale q.k_j),
+ * j over the slots below lengths[b] and those of the T tokens that the token sees.
+ *   q : [B, H G, T, d_k].   cache_k, cache_v : [B, H, C, d_k].   o as q, output.   lse : [B, H G, T] fp32 output.
+ *   tree : [B, T] uint64 or null.  Bit u of word t: token t sees token u (itself by bit t, if it is to).  Null: a
+ *          chain, token t sees tokens 0 ... t.  Bits from T on mean nothing.
+ *   weights, weights_out : [B, H, C] fp32 or both null: weights_out = weights, and for slots below
+ *          lengths[b] + T weights + the p_j of the counted tokens, added over them and over the G heads.
+ *          weights_out may be weights itself.
+ *   counted : [B] uint64 or null (all): bit t: token t is counted.
+ * A row that sees nothing gets o = 0 and lse = -infinity.  What a row does not see does not reach it, NaN and
+ * infinities among it; slots behind the T tokens are not read.  A length outside 0 ... C - T counts as the nearest
+ * inside.  Scores and sums are fp32.  Results are bitwise reproducible.
+ *   workspace : caller-owned, overwritten.   T <= C.   scale finite and > 0.
+ */
+attn_status attn_cache_attention(const void *q, const void *cache_k, const void *cache_v, const int *lengths,
+                                 const uint64_t *tree, const uint64_t *counted, const float *weights,
+                                 float *weights_out, void *o, float *lse, void *workspace, size_t workspace_bytes,
+                                 int B, int H, int G, int T, int C, int d_k, float scale, cudaStream_t stream);
+
+/* Bytes of device workspace attn_cache_evict() needs (0 for sizes it rejects). */
+size_t attn_cache_evict_workspace_size(int B, int H, int C, int d_k, int keep);
+
+/*
+ * Eviction by accumulated weight, in place.  Of the slots below lengths[b], each cached head keeps
+ * n = min(lengths[b], keep): first those whose position is above the newest one less `recent`, then those of the
+ * largest weights, equal ones by the lower slot (a weight that is negative or NaN ranks as zero).  A kept slot below
+ * n stays where it is; the kept ones from n on move, in ascending order, into the evicted ones below n.
+ *   cache_k, cache_v : [B, H, C, d_k] bf16, changed in the slots that are moved into alone.
+ *   weights, slot_positions : [B, H, C] fp32 and int32.   weights_out, positions_out : outputs of the same shape,
+ *          moved alike, 0 and -1 from n on; each may be its input itself.
+ *   lengths_out : [B] int32 output, n.   1 <= keep, 0 <= recent <= keep.
+ * A length outside 0 ... C counts as the nearest inside.
+ */
+attn_status attn_cache_evict(void *cache_k, void *cache_v, const float *weights, const int *slot_positions,
+                             const int *lengths, float *weights_out, int *positions_out, int *lengths_out,
+                             void *workspace, size_t workspace_bytes, int B, int H, int C, int d_k, int keep,
+                             int recent, cudaStream_t stream);
+
+/*
  * Bytes of device workspace attn_fwd_unfused() needs: the fp32 score matrix S [B,H,N,N] and the
  * bf16 probabilities P [B,H,N,N], each region 256-byte aligned (6 B H N^2 bytes and padding).
  * Returns 0 if the sizes are unsupported.

@@ -38,6 +38,10 @@ __all__ = [
     "linear_forward", "linear_backward", "linear", "out_proj_forward", "out_proj_backward", "out_proj",
     "rms_norm_forward", "rms_norm_backward", "rms_norm", "rms_norm_q8", "quantize_q8", "linear_q8",
     "attn_debug_linear_plan", "ACTIVATIONS",
+    "attn_rotary", "attn_rotary_bwd", "attn_cache_append", "attn_cache_attention", "attn_cache_attention_workspace_size",
+    "attn_cache_evict", "attn_cache_evict_workspace_size",
+    "rotary_turns", "rotary_forward", "rotary_backward", "rotary", "cache_append", "cache_attention", "cache_evict",
+    "tree_words",
     "load_library", "STATUS",
 ]
 
@@ -54,7 +58,9 @@ EXPORTS = ("attn_fwd", "attn_fwd_workspace_size", "attn_fwd_with_workspace", "at
            "attn_linear", "attn_out_proj", "attn_linear_bwd", "attn_linear_bwd_workspace_size",
            "attn_out_proj_bwd", "attn_out_proj_bwd_workspace_size", "attn_linear_q8", "attn_rms_norm",
            "attn_rms_norm_bwd", "attn_rms_norm_bwd_workspace_size", "attn_rms_norm_q8",
-           "attn_quantize_q8", "attn_debug_linear_plan")
+           "attn_quantize_q8", "attn_debug_linear_plan",
+           "attn_rotary", "attn_rotary_bwd", "attn_cache_append", "attn_cache_attention",
+           "attn_cache_attention_workspace_size", "attn_cache_evict", "attn_cache_evict_workspace_size")
 # attn_activation
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
@@ -69,7 +75,7 @@ class AttnError(RuntimeError):
 
 
 _lib = None
-_VP, _I, _F, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_VP, _I, _F, _SZ, _LL = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_longlong
 
 
 def load_library(path: str = LIB_PATH):
@@ -131,11 +137,17 @@ def load_library(path: str = LIB_PATH):
                        ("attn_rms_norm_bwd", [_VP] * 8 + [_SZ] + [_I] * 2 + [_VP]),
                        ("attn_rms_norm_q8", [_VP] * 6 + [_I] * 2 + [_F, _VP]),
                        ("attn_quantize_q8", [_VP] * 3 + [_I] * 2 + [_VP]),
+                       ("attn_rotary", [_VP] * 3 + [_LL, _VP] + [_I] * 6 + [_F, _VP]),
+                       ("attn_rotary_bwd", [_VP] * 3 + [_LL, _VP] + [_I] * 6 + [_F, _VP]),
+                       ("attn_cache_append", [_VP] * 12 + [_I] * 9 + [_F, _VP]),
+                       ("attn_cache_attention", [_VP] * 11 + [_SZ] + [_I] * 6 + [_F, _VP]),
+                       ("attn_cache_evict", [_VP] * 9 + [_SZ] + [_I] * 6 + [_VP]),
                        ("attn_debug_linear_plan", [_I] * 7 + [_VP])):
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = _I
     for name, n in (("attn_linear_bwd_workspace_size", 4), ("attn_out_proj_bwd_workspace_size", 5),
-                    ("attn_rms_norm_bwd_workspace_size", 2)):
+                    ("attn_rms_norm_bwd_workspace_size", 2), ("attn_cache_attention_workspace_size", 6),
+                    ("attn_cache_evict_workspace_size", 5)):
         getattr(lib, name).argtypes = [_I] * n
         getattr(lib, name).restype = _SZ
     if path == LIB_PATH:
@@ -352,6 +364,58 @@ def attn_rms_norm_q8(x, residual, weight, yq, scale, h, M: int, D: int, eps: flo
 def attn_quantize_q8(x, xq, scale, M: int, D: int, stream=None):
     _raise(load_library().attn_quantize_q8(_ptr(x), _ptr(xq), _ptr(scale), M, D, _stream(stream)),
            "attn_quantize_q8")
+
+
+def attn_rotary(x, y, positions, positions_stride: int, turns, B: int, H: int, N: int, d_k: int, rotated: int,
+                interleaved: int, amplitude: float, stream=None):
+    """Enqueue y = x with the pairs of its first `rotated` columns turned (positions may be None)."""
+    _raise(load_library().attn_rotary(_ptr(x), _ptr(y), _opt(positions), positions_stride, _ptr(turns), B, H, N, d_k,
+                                      rotated, int(interleaved), float(amplitude), _stream(stream)), "attn_rotary")
+
+
+def attn_rotary_bwd(dy, dx, positions, positions_stride: int, turns, B: int, H: int, N: int, d_k: int, rotated: int,
+                    interleaved: int, amplitude: float, stream=None):
+    _raise(load_library().attn_rotary_bwd(_ptr(dy), _ptr(dx), _opt(positions), positions_stride, _ptr(turns), B, H, N,
+                                          d_k, rotated, int(interleaved), float(amplitude), _stream(stream)),
+           "attn_rotary_bwd")
+
+
+def attn_cache_append(k, v, cache_k, cache_v, lengths, turns, positions, rows, q, q_out, weights, slot_positions,
+                      B: int, H: int, Hq: int, T: int, n: int, d_k: int, C: int, rotated: int, interleaved: int,
+                      amplitude: float, stream=None):
+    """Enqueue the append of new keys and values to a cache (turns, positions, rows, q, q_out, weights and
+    slot_positions may be None)."""
+    _raise(load_library().attn_cache_append(
+        _ptr(k), _ptr(v), _ptr(cache_k), _ptr(cache_v), _ptr(lengths), _opt(turns), _opt(positions), _opt(rows),
+        _opt(q), _opt(q_out), _opt(weights), _opt(slot_positions), B, H, Hq, T, n, d_k, C, rotated, int(interleaved),
+        float(amplitude), _stream(stream)), "attn_cache_append")
+
+
+def attn_cache_attention_workspace_size(B: int, H: int, G: int, T: int, C: int, d_k: int) -> int:
+    return int(load_library().attn_cache_attention_workspace_size(B, H, G, T, C, d_k))
+
+
+def attn_cache_attention(q, cache_k, cache_v, lengths, tree, counted, weights, weights_out, o, lse, workspace,
+                         workspace_bytes: int, B: int, H: int, G: int, T: int, C: int, d_k: int, scale: float,
+                         stream=None):
+    """Enqueue attention of T tokens over a cache (tree, counted, weights with weights_out may be None)."""
+    _raise(load_library().attn_cache_attention(
+        _ptr(q), _ptr(cache_k), _ptr(cache_v), _ptr(lengths), _opt(tree), _opt(counted), _opt(weights),
+        _opt(weights_out), _ptr(o), _ptr(lse), _ptr(workspace), int(workspace_bytes), B, H, G, T, C, d_k,
+        float(scale), _stream(stream)), "attn_cache_attention")
+
+
+def attn_cache_evict_workspace_size(B: int, H: int, C: int, d_k: int, keep: int) -> int:
+    return int(load_library().attn_cache_evict_workspace_size(B, H, C, d_k, keep))
+
+
+def attn_cache_evict(cache_k, cache_v, weights, slot_positions, lengths, weights_out, positions_out, lengths_out,
+                     workspace, workspace_bytes: int, B: int, H: int, C: int, d_k: int, keep: int, recent: int,
+                     stream=None):
+    _raise(load_library().attn_cache_evict(
+        _ptr(cache_k), _ptr(cache_v), _ptr(weights), _ptr(slot_positions), _ptr(lengths), _ptr(weights_out),
+        _ptr(positions_out), _ptr(lengths_out), _ptr(workspace), int(workspace_bytes), B, H, C, d_k, keep, recent,
+        _stream(stream)), "attn_cache_evict")
 
 
 def _scratch(nbytes: int, dev, st):
@@ -729,3 +793,132 @@ class _RmsNorm(torch.autograd.Function):
 def rms_norm(x, weight, residual=None, eps: float = 1e-6):
     """The norm with autograd support: y, or (y, h) with a residual (see rms_norm_forward)."""
     return _RmsNorm.apply(x, weight, residual, eps)
+
+
+# ------------------------------------------------- positions, and a cache for tokens that come one by one
+def rotary_turns(rotated: int, base: float = 10000.0, method: str = "none", factor: float = 1.0,
+                 trained: int | None = None, low: float = 1.0, high: float = 32.0, device="cuda"):
+    """The frequencies of the rotary positions, [rotated / 2] int64 on `device`: whole turns a position in units of
+    2^-64 (the fraction of a turn is what counts, so that positions are reduced exactly).  f_j = base^(-2 j / rotated)
+    radians a position, scaled for texts `factor` times as long as the trained ones by
+        "none"       nothing,
+        "positions"  f_j / factor (positions interpolated),
+        "base"       a base of base factor^(rotated / (rotated - 2)): the slowest pair as by "positions", the
+                     fastest as it was,
+        "parts"      f_j (g + (1 - g) / factor), g = (w_j - low) / (high - low) clamped to 0 ... 1, where pair j
+                     makes w_j turns over `trained` positions: fast pairs stay, slow ones are interpolated."""
+    if rotated < 16 or rotated % 16:
+        raise ValueError(f"rotated {rotated}: a multiple of 16, at least 16")
+    if not (math.isfinite(base) and base > 1.0 and math.isfinite(factor) and factor > 0.0):
+        raise ValueError("base above 1 and a positive factor, both finite")
+    if method not in ("none", "positions", "base", "parts"):
+        raise ValueError(f"method {method!r}: one of none, positions, base, parts")
+    if method == "parts" and (trained is None or trained < 1 or not low < high):
+        raise ValueError("parts needs the trained length, and low < high")
+    if method == "base":
+        base = base * factor ** (rotated / (rotated - 2))
+    turns = []
+    for j in range(rotated // 2):
+        f = base ** (-2.0 * j / rotated)
+        if method == "positions":
+            f /= factor
+        elif method == "parts":
+            g = min(max((trained * f / (2.0 * math.pi) - low) / (high - low), 0.0), 1.0)
+            f *= g + (1.0 - g) / factor
+        t = round(math.ldexp(f / (2.0 * math.pi), 64)) % (1 << 64)
+        turns.append(t - (1 << 64) if t >> 63 else t)
+    return torch.tensor(turns, dtype=torch.int64, device=device)
+
+
+def rotary_forward(x, turns, positions=None, interleaved: bool = False, amplitude: float = 1.0, stream=None):
+    """x [B, H, N, d_k] bf16 with the first 2 len(turns) columns of each row turned by its position: pairs
+    (j, j + len(turns)), or (2 j, 2 j + 1) with interleaved.  turns: rotary_turns().  positions int32 [N] or [B, N]
+    (0 ... N - 1 without).  amplitude multiplies the turned columns."""
+    fn = _binding().rotary
+    if stream is None:
+        return fn(x, turns, positions, interleaved, amplitude, False)
+    return _on(stream, fn, x, turns, positions, interleaved, amplitude, False)
+
+
+def rotary_backward(dy, turns, positions=None, interleaved: bool = False, amplitude: float = 1.0, stream=None):
+    """dx [B, H, N, d_k] bf16 of rotary_forward() for dy = dL/dy: the turns backwards."""
+    fn = _binding().rotary
+    if stream is None:
+        return fn(dy, turns, positions, interleaved, amplitude, True)
+    return _on(stream, fn, dy, turns, positions, interleaved, amplitude, True)
+
+
+class _Rotary(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, turns, positions, interleaved, amplitude):
+        ctx.save_for_backward(turns, positions)
+        ctx.how = (interleaved, amplitude)
+        return rotary_forward(x, turns, positions, interleaved, amplitude)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        turns, positions = ctx.saved_tensors
+        return rotary_backward(dy.contiguous(), turns, positions, *ctx.how), None, None, None, None
+
+
+def rotary(x, turns, positions=None, interleaved: bool = False, amplitude: float = 1.0):
+    """Rotary positions with autograd support (see rotary_forward)."""
+    return _Rotary.apply(x, turns, positions, interleaved, amplitude)
+
+
+def tree_words(parents, device="cuda"):
+    """Mask words [B, T] int64 for cache_attention() from the tokens' parents (a list of lists, or an integer tensor, on
+    the host): a number below the token's own, or a negative one at a root.  Each token sees itself and what its
+    parent sees."""
+    rows = parents.tolist() if isinstance(parents, torch.Tensor) else parents
+    out = []
+    for row in rows:
+        if not 1 <= len(row) <= 64 or len(row) != len(rows[0]):
+            raise ValueError("1 to 64 tokens a tree, as many in each")
+        words = []
+        for t, p in enumerate(row):
+            if p >= t:
+                raise ValueError(f"token {t}: its parent {p} does not come before it")
+            words.append((words[p] if p >= 0 else 0) | 1 << t)
+        out.append([w - (1 << 64) if w >> 63 else w for w in words])
+    return torch.tensor(out, dtype=torch.int64, device=device)
+
+
+def cache_append(k, v, cache_k, cache_v, lengths, turns=None, positions=None, interleaved: bool = False,
+                 amplitude: float = 1.0, rows=None, q=None, weights=None, slot_positions=None, stream=None):
+    """New tokens' keys (turned by rotary positions where `turns` is given) and values k, v [B, H, T, d_k] into slots
+    lengths[b], lengths[b] + 1 ... of cache_k, cache_v [B, H, C, d_k], in place; lengths [B] int32 stays as it is.
+    positions [B, T] int32 (the slots' numbers without).  rows [B, n] int32: take those of the T tokens (an accepted
+    path of a tree), none where negative.  weights [B, H, C] fp32 is zeroed in the new slots, slot_positions
+    [B, H, C] int32 takes the positions.  q [B, Hq, T, d_k]: the tokens' queries, returned turned (else None)."""
+    fn = _binding().cache_append
+    args = (k, v, cache_k, cache_v, lengths, turns, positions, interleaved, amplitude, rows, q, weights, slot_positions)
+    return fn(*args) if stream is None else _on(stream, fn, *args)
+
+
+def cache_attention(q, cache_k, cache_v, lengths, tree=None, weights=None, counted=None, weights_out=None,
+                    scale: float | None = None, stream=None):
+    """(o, lse): attention of T <= 64 tokens q [B, Hq, T, d_k] over the slots below lengths[b] of cache_k, cache_v
+    [B, H, C, d_k] (H divides Hq: consecutive query heads share a cached one) and over the tokens themselves, which
+    cache_append() has put into slots lengths[b] ... lengths[b] + T - 1.  tree [B, T] int64: bit u of word t says
+    that token t sees token u (tree_words()); without it a chain.  o as q, lse [B, Hq, T] fp32.
+    With weights [B, H, C] fp32, (o, lse, weights_out): weights with the attention that each slot got from the tokens
+    added, from those of bits counted [B] int64 alone where given; weights_out may be weights itself."""
+    fn = _binding().cache_attention
+    scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else scale
+    args = (q, cache_k, cache_v, lengths, tree, weights, counted, weights_out, scale)
+    out = fn(*args) if stream is None else _on(stream, fn, *args)
+    return out[:2] if weights is None else out
+
+
+def cache_evict(cache_k, cache_v, weights, slot_positions, lengths, keep: int, recent: int = 0, weights_out=None,
+                positions_out=None, stream=None):
+    """(weights, slot_positions, lengths): of each sequence and head, min(lengths[b], keep) slots stay: those of the
+    `recent` newest positions, then those of the largest weights (ties: the lower slot).  Kept slots from there on move
+    into evicted ones below, in place in cache_k and cache_v [B, H, C, d_k]; the returned weights [B, H, C] fp32 and
+    slot_positions [B, H, C] int32 are moved alike, 0 and -1 behind (weights_out and positions_out: where to write
+    them, their inputs among the choices); the lengths are a new [B] int32."""
+    fn = _binding().cache_evict
+    args = (cache_k, cache_v, weights, slot_positions, lengths, keep, recent, weights_out, positions_out)
+    return fn(*args) if stream is None else _on(stream, fn, *args)

@@ -25,7 +25,8 @@ LIB_NAME = "libattn_gb300.so"
 LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
 BINDING_PATH = os.path.join(BUILD_DIR, "attn_binding.so")   # CPython extension over the library and PyTorch
 
-SOURCES = ["attn_api.cu", "attn_fwd.cu", "attn_bwd.cu", "vector_add.cu", "proj.cu", "unfused.cu", "linear.cu", "norm.cu"]
+SOURCES = ["attn_api.cu", "attn_fwd.cu", "attn_bwd.cu", "vector_add.cu", "proj.cu", "unfused.cu", "linear.cu", "norm.cu",
+           "rotary.cu", "cache_attn.cu", "cache_evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               f"-I{INCLUDE}", f"-I{CSRC}"]

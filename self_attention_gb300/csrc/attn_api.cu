@@ -1100,3 +1100,225 @@ extern "C" attn_status attn_rms_norm_bwd(const void *dy, const void *h, const fl
     }
     return e == cudaSuccess ? ATTN_OK : fail("attn_rms_norm_bwd launch", e);
 }
+
+// --------------------------------------------------------------------------------------------
+// Rotary positions and the cache.
+namespace {
+
+// An operand of the cache's calls: its alignment, and for an output the input (by its place, or -1) that it may
+// lie exactly over.
+struct Part {
+    const void *p;
+    size_t bytes, align;
+    int over = -1;
+};
+
+template <int NI, int NO>
+attn_status check_parts(const Part (&ins)[NI], const Part (&outs)[NO])
+{
+    for (const Part &x : ins)
+        if (x.p && reinterpret_cast<uintptr_t>(x.p) % x.align) return ATTN_ERR_MISALIGNED;
+    for (const Part &x : outs)
+        if (x.p && reinterpret_cast<uintptr_t>(x.p) % x.align) return ATTN_ERR_MISALIGNED;
+    for (int i = 0; i < NO; ++i) {
+        if (!outs[i].p) continue;
+        const Range r = span(outs[i].p, outs[i].bytes);
+        for (int k = 0; k < NI; ++k)
+            if (ins[k].p && overlap(r, span(ins[k].p, ins[k].bytes)) && !(k == outs[i].over && ins[k].p == outs[i].p))
+                return ATTN_ERR_INVALID_ARG;
+        for (int j = i + 1; j < NO; ++j)
+            if (outs[j].p && overlap(r, span(outs[j].p, outs[j].bytes))) return ATTN_ERR_INVALID_ARG;
+    }
+    return ATTN_OK;
+}
+
+constexpr int kMaxHeads = 16384;
+constexpr int kMaxSlots = 1 << 30;
+constexpr int kMaxTokens = 64;     // of a tree: a mask word
+
+// [B, H, N, d_k] with any of B, H, N zero.
+bool heads_ok(int B, int H, int N, int d_k)
+{
+    return B >= 0 && H >= 0 && N >= 0 && H <= kMaxHeads && (long long)B * H <= 0x7fffffffLL &&
+           (long long)B * N <= 0x7fffffffLL && (double)B * H * N * d_k < (double)(1LL << 40);
+}
+
+bool turns_ok(int d_k, int rotated, float amplitude)
+{
+    return rotated >= 16 && rotated % 16 == 0 && rotated <= d_k && std::isfinite(amplitude);
+}
+
+attn_status run_rotary(const void *x, void *y, const int *positions, long long stride, const uint64_t *turns, int B,
+                       int H, int N, int d_k, int rotated, int interleaved, float amplitude, bool backward,
+                       cudaStream_t stream)
+{
+    if (d_k != 64 && d_k != 128) return ATTN_ERR_UNSUPPORTED_DK;
+    if (!heads_ok(B, H, N, d_k) || !turns_ok(d_k, rotated, amplitude) || (interleaved & ~1) ||
+        (positions && stride != 0 && stride != N))
+        return ATTN_ERR_INVALID_ARG;
+    if (B == 0 || H == 0 || N == 0) return ATTN_OK;
+    if (!x || !y || !turns) return ATTN_ERR_INVALID_ARG;
+    const size_t bytes = (size_t)B * H * N * d_k * 2;
+    const Part ins[3] = {{x, bytes, 16}, {positions, (stride ? (size_t)B : 1) * N * 4, 4}, {turns, (size_t)rotated * 4, 16}};
+    const Part outs[1] = {{y, bytes, 16, 0}};
+    attn_status st = check_parts(ins, outs);
+    if (st != ATTN_OK) return st;
+    DeviceState *dev = nullptr;
+    if ((st = device_state(&dev)) != ATTN_OK) return st;
+    RotaryArgs a = {};
+    a.x = x; a.y = y; a.positions = positions; a.turns = turns; a.pos_stride = stride;
+    a.B = B; a.H = H; a.N = N; a.d = d_k; a.rotated = rotated; a.amplitude = amplitude;
+    const cudaError_t e = launch_rotary(a, interleaved != 0, backward, stream);
+    return e == cudaSuccess ? ATTN_OK : fail(backward ? "attn_rotary_bwd launch" : "attn_rotary launch", e);
+}
+
+// Sizes of a cache and of the heads that read it.
+attn_status check_cache(int B, int H, int C, int d_k)
+{
+    if (d_k != 64 && d_k != 128) return ATTN_ERR_UNSUPPORTED_DK;
+    if (B < 1 || H < 1 || C < 1 || C >= kMaxSlots || !heads_ok(B, H, C, d_k)) return ATTN_ERR_INVALID_ARG;
+    // blocks of 64 slots of all heads have to fit a 1-D grid
+    return (double)B * H * ((C + 63) / 64) < 2147483647.0 ? ATTN_OK : ATTN_ERR_INVALID_ARG;
+}
+
+attn_status check_cache_attention(int B, int H, int G, int T, int C, int d_k)
+{
+    const attn_status st = check_cache(B, H, C, d_k);
+    if (st != ATTN_OK) return st;
+    if (G < 1 || G > kMaxHeads || T < 1 || T > kMaxTokens || T > C || (long long)H * G > kMaxHeads ||
+        (double)B * H * G * T >= 2147483647.0)
+        return ATTN_ERR_INVALID_ARG;
+    return ATTN_OK;
+}
+
+attn_status check_evict(int B, int H, int C, int d_k, int keep)
+{
+    const attn_status st = check_cache(B, H, C, d_k);
+    if (st != ATTN_OK) return st;
+    return keep < 1 ? ATTN_ERR_INVALID_ARG : ATTN_OK;
+}
+
+bool workspace_ok(const void *p, size_t have, size_t need)
+{
+    return p && (reinterpret_cast<uintptr_t>(p) & 255u) == 0 && have >= need;
+}
+
+}  // namespace
+
+extern "C" attn_status attn_rotary(const void *x, void *y, const int *positions, long long positions_stride,
+                                   const uint64_t *turns, int B, int H, int N, int d_k, int rotated, int interleaved,
+                                   float amplitude, cudaStream_t stream)
+{
+    return run_rotary(x, y, positions, positions_stride, turns, B, H, N, d_k, rotated, interleaved, amplitude, false,
+                      stream);
+}
+
+extern "C" attn_status attn_rotary_bwd(const void *dy, void *dx, const int *positions, long long positions_stride,
+                                       const uint64_t *turns, int B, int H, int N, int d_k, int rotated,
+                                       int interleaved, float amplitude, cudaStream_t stream)
+{
+    return run_rotary(dy, dx, positions, positions_stride, turns, B, H, N, d_k, rotated, interleaved, amplitude, true,
+                      stream);
+}
+
+extern "C" attn_status attn_cache_append(const void *k, const void *v, void *cache_k, void *cache_v,
+                                         const int *lengths, const uint64_t *turns, const int *positions,
+                                         const int *rows, const void *q, void *q_out, float *weights,
+                                         int *slot_positions, int B, int H, int Hq, int T, int n, int d_k, int C,
+                                         int rotated, int interleaved, float amplitude, cudaStream_t stream)
+{
+    attn_status st = check_cache(B < 1 ? 1 : B, H, C, d_k);
+    if (st != ATTN_OK) return st;
+    if (!heads_ok(B, H, T, d_k) || !heads_ok(B, H, n, d_k) || (q && (Hq < 1 || !heads_ok(B, Hq, T, d_k))) ||
+        (turns && !turns_ok(d_k, rotated, amplitude)) || (interleaved & ~1) || (!rows && n != T) || (rows && q) ||
+        (q != nullptr) != (q_out != nullptr))
+        return ATTN_ERR_INVALID_ARG;
+    if (B == 0 || n == 0) return ATTN_OK;
+    if (T == 0) return ATTN_ERR_INVALID_ARG;       // rows of nothing
+    if (!k || !v || !cache_k || !cache_v || !lengths) return ATTN_ERR_INVALID_ARG;
+    const size_t bh = (size_t)B * H, fresh = bh * T * d_k * 2, cache = bh * C * d_k * 2,
+                 qs = (size_t)B * (q ? Hq : 0) * T * d_k * 2;
+    const Part ins[7] = {{q, qs, 16}, {k, fresh, 16}, {v, fresh, 16}, {lengths, (size_t)B * 4, 4},
+                         {turns, (size_t)rotated * 4, 16}, {positions, (size_t)B * T * 4, 4}, {rows, (size_t)B * n * 4, 4}};
+    const Part outs[5] = {{cache_k, cache, 16}, {cache_v, cache, 16}, {q_out, qs, 16, 0}, {weights, bh * C * 4, 4},
+                          {slot_positions, bh * C * 4, 4}};
+    if ((st = check_parts(ins, outs)) != ATTN_OK) return st;
+    DeviceState *dev = nullptr;
+    if ((st = device_state(&dev)) != ATTN_OK) return st;
+    AppendArgs a = {};
+    a.k = k; a.v = v; a.q = q; a.cache_k = cache_k; a.cache_v = cache_v; a.q_out = q_out; a.lengths = lengths;
+    a.turns = turns; a.positions = positions; a.rows = rows; a.weights = weights; a.slot_positions = slot_positions;
+    a.B = B; a.H = H; a.Hq = q ? Hq : 0; a.T = T; a.n = n; a.d = d_k; a.C = C; a.rotated = rotated;
+    a.amplitude = amplitude;
+    const cudaError_t e = launch_append(a, interleaved != 0, stream);
+    return e == cudaSuccess ? ATTN_OK : fail("attn_cache_append launch", e);
+}
+
+extern "C" size_t attn_cache_attention_workspace_size(int B, int H, int G, int T, int C, int d_k)
+{
+    return check_cache_attention(B, H, G, T, C, d_k) == ATTN_OK ? cache_attn_workspace(G, T, d_k) : 0;
+}
+
+extern "C" attn_status attn_cache_attention(const void *q, const void *cache_k, const void *cache_v,
+                                            const int *lengths, const uint64_t *tree, const uint64_t *counted,
+                                            const float *weights, float *weights_out, void *o, float *lse,
+                                            void *workspace, size_t workspace_bytes, int B, int H, int G, int T,
+                                            int C, int d_k, float scale, cudaStream_t stream)
+{
+    attn_status st = check_cache_attention(B, H, G, T, C, d_k);
+    if (st != ATTN_OK) return st;
+    if (!std::isfinite(scale) || !(scale > 0.f)) return ATTN_ERR_INVALID_ARG;
+    if (!q || !cache_k || !cache_v || !lengths || !o || !lse || (weights != nullptr) != (weights_out != nullptr) ||
+        (counted && !weights))
+        return ATTN_ERR_INVALID_ARG;
+    const size_t need = cache_attn_workspace(G, T, d_k);
+    if (!workspace_ok(workspace, workspace_bytes, need)) return ATTN_ERR_WORKSPACE;
+    const size_t bh = (size_t)B * H, cache = bh * C * d_k * 2, qs = bh * G * T * d_k * 2;
+    const Part ins[7] = {{weights, bh * C * 4, 4}, {q, qs, 16}, {cache_k, cache, 16}, {cache_v, cache, 16},
+                         {lengths, (size_t)B * 4, 4}, {tree, (size_t)B * T * 8, 8}, {counted, (size_t)B * 8, 8}};
+    const Part outs[4] = {{o, qs, 16}, {lse, bh * G * T * 4, 4}, {weights_out, bh * C * 4, 4, 0}, {workspace, need, 256}};
+    if ((st = check_parts(ins, outs)) != ATTN_OK) return st;
+    DeviceState *dev = nullptr;
+    if ((st = device_state(&dev)) != ATTN_OK) return st;
+    CacheAttnArgs a = {};
+    a.q = q; a.k = cache_k; a.v = cache_v; a.lengths = lengths; a.tree = tree; a.counted = counted;
+    a.weights = weights; a.weights_out = weights_out; a.o = o; a.lse = lse; a.workspace = workspace;
+    a.B = B; a.H = H; a.G = G; a.T = T; a.C = C; a.d = d_k; a.scale = scale;
+    a.status = dev->status;
+    const cudaError_t e = launch_cache_attn(a, stream);
+    return e == cudaSuccess ? ATTN_OK : fail("attn_cache_attention launch", e);
+}
+
+extern "C" size_t attn_cache_evict_workspace_size(int B, int H, int C, int d_k, int keep)
+{
+    return check_evict(B, H, C, d_k, keep) == ATTN_OK ? align256(evict_workspace(B, H, C, keep)) : 0;
+}
+
+extern "C" attn_status attn_cache_evict(void *cache_k, void *cache_v, const float *weights, const int *slot_positions,
+                                        const int *lengths, float *weights_out, int *positions_out, int *lengths_out,
+                                        void *workspace, size_t workspace_bytes, int B, int H, int C, int d_k,
+                                        int keep, int recent, cudaStream_t stream)
+{
+    attn_status st = check_evict(B, H, C, d_k, keep);
+    if (st != ATTN_OK) return st;
+    if (recent < 0 || recent > keep) return ATTN_ERR_INVALID_ARG;
+    if (!cache_k || !cache_v || !weights || !slot_positions || !lengths || !weights_out || !positions_out ||
+        !lengths_out)
+        return ATTN_ERR_INVALID_ARG;
+    const size_t need = attn_cache_evict_workspace_size(B, H, C, d_k, keep);
+    if (!workspace_ok(workspace, workspace_bytes, need)) return ATTN_ERR_WORKSPACE;
+    const size_t bh = (size_t)B * H, cache = bh * C * d_k * 2, slots = bh * C * 4;
+    const Part ins[3] = {{weights, slots, 4}, {slot_positions, slots, 4}, {lengths, (size_t)B * 4, 4}};
+    const Part outs[6] = {{cache_k, cache, 16}, {cache_v, cache, 16}, {weights_out, slots, 4, 0},
+                          {positions_out, slots, 4, 1}, {lengths_out, (size_t)B * 4, 4}, {workspace, need, 256}};
+    if ((st = check_parts(ins, outs)) != ATTN_OK) return st;
+    DeviceState *dev = nullptr;
+    if ((st = device_state(&dev)) != ATTN_OK) return st;
+    EvictArgs a = {};
+    a.k = cache_k; a.v = cache_v; a.weights = weights; a.slot_positions = slot_positions; a.lengths = lengths;
+    a.weights_out = weights_out; a.positions_out = positions_out; a.lengths_out = lengths_out;
+    a.moves = static_cast<int *>(workspace);
+    a.B = B; a.H = H; a.C = C; a.d = d_k; a.keep = keep; a.recent = recent;
+    const cudaError_t e = launch_evict(a, stream);
+    return e == cudaSuccess ? ATTN_OK : fail("attn_cache_evict launch", e);
+}

@@ -1,4 +1,4 @@
-// The tensor-level calls of the linear layers and the norm, as a CPython extension: argument checks,
+// The tensor-level calls of the linear layers, the norm, positions and the cache, as a CPython extension: argument checks,
 // allocation of the outputs from PyTorch's caching allocator on the current stream, and one call of the
 // C ABI (include/attn.h).  Nothing is computed here.  The same through Python and ctypes took 13 to 16
 // us a call on the GB300's host, several times what the smallest kernels take on the GPU; this takes
@@ -176,7 +176,7 @@ int integer(PyObject *o)
 {
     const long v = PyLong_AsLong(o);
     if (v == -1 && PyErr_Occurred()) throw Refused{};
-    return (int)v;
+    return v != (int)v ? -1 : (int)v;
 }
 
 double number(PyObject *o)
@@ -418,6 +418,182 @@ PyObject *quantize_q8(Args a)
     return tuple(xq, scale);
 }
 
+// [B, H, N, d_k] heads under a name.
+struct HeadsOf {
+    const at::Tensor &t;
+    c10::Device dev;
+    int64_t B, H, N, d;
+    HeadsOf(PyObject *o, const char *name) : t(tensor(o, name)), dev(t.device())
+    {
+        if (t.dim() != 4 || !t.is_cuda() || t.scalar_type() != kBf16 || !t.is_contiguous())
+            refuse(std::string(name) + ": expected a contiguous bf16 CUDA tensor [B, H, N, d_k]");
+        B = t.size(0);
+        H = t.size(1);
+        N = t.size(2);
+        d = t.size(3);
+    }
+};
+
+constexpr auto kI32 = at::kInt, kI64 = at::kLong;
+
+// Turns a position of the pairs, [rotated / 2] int64 (the bits of the C ABI's uint64).
+const uint64_t *turns_of(PyObject *o, c10::Device dev, int64_t &rotated)
+{
+    const at::Tensor &t = tensor(o, "turns");
+    if (t.dim() != 1) refuse("turns: expected a vector, as rotary_turns() makes it");
+    rotated = 2 * t.size(0);
+    return static_cast<const uint64_t *>(operand(o, "turns", kI64, t.sizes(), dev));
+}
+
+// x, turns, positions or None, interleaved, amplitude, backward -> y
+PyObject *rotary(Args a)
+{
+    const HeadsOf x(a[0], "x");
+    int64_t rotated;
+    const uint64_t *turns = turns_of(a[1], x.dev, rotated);
+    const int *positions = nullptr;
+    int64_t stride = 0;
+    if (a[2] != Py_None) {
+        const bool each = tensor(a[2], "positions").dim() == 2;
+        const c10::DimVector shape = each ? c10::DimVector{x.B, x.N} : c10::DimVector{x.N};
+        positions = static_cast<const int *>(operand(a[2], "positions", kI32, shape, x.dev));
+        stride = each ? x.N : 0;
+    }
+    const int interleaved = flag(a[3]);
+    const auto amplitude = (float)number(a[4]);
+    const bool backward = flag(a[5]);
+    at::Tensor y;
+    int code;
+    {
+        Unlocked u;
+        const c10::cuda::CUDAGuard guard(x.dev);
+        y = empty(x.t.sizes(), kBf16, x.dev);
+        code = (backward ? attn_rotary_bwd : attn_rotary)(x.t.data_ptr(), y.data_ptr(), positions, stride, turns,
+                                                          count(x.B), count(x.H), count(x.N), count(x.d),
+                                                          count(rotated), interleaved, amplitude, stream(x.dev));
+    }
+    check(code, backward ? "attn_rotary_bwd" : "attn_rotary");
+    return wrap(y);
+}
+
+// k, v, cache_k, cache_v, lengths, turns, positions, interleaved, amplitude, rows, q, weights, slot_positions
+// -> q turned, or None
+PyObject *cache_append(Args a)
+{
+    const HeadsOf k(a[0], "k"), ck(a[2], "cache_k");
+    const void *v = operand(a[1], "v", kBf16, k.t.sizes(), k.dev);
+    if (ck.dev != k.dev || ck.B != k.B || ck.H != k.H || ck.d != k.d)
+        refuse("cache_k: expected [" + std::to_string(k.B) + ", " + std::to_string(k.H) + ", C, " +
+               std::to_string(k.d) + "] on " + k.dev.str());
+    void *cv = operand(a[3], "cache_v", kBf16, ck.t.sizes(), k.dev);
+    const auto *lengths = static_cast<const int *>(operand(a[4], "lengths", kI32, {k.B}, k.dev));
+    int64_t rotated = 0, n = k.N, Hq = 0;
+    const uint64_t *turns = a[5] == Py_None ? nullptr : turns_of(a[5], k.dev, rotated);
+    const auto *positions = static_cast<const int *>(operand_or_null(a[6], "positions", kI32, {k.B, k.N}, k.dev));
+    const int interleaved = flag(a[7]);
+    const auto amplitude = (float)number(a[8]);
+    const int *rows = nullptr;
+    if (a[9] != Py_None) {
+        n = matrix_columns(a[9], "rows");
+        rows = static_cast<const int *>(operand(a[9], "rows", kI32, {k.B, n}, k.dev));
+    }
+    const void *q = nullptr;
+    at::Tensor q_out;
+    if (a[10] != Py_None) {
+        const HeadsOf heads(a[10], "q");
+        Hq = heads.H;
+        q = operand(a[10], "q", kBf16, {k.B, Hq, k.N, k.d}, k.dev);
+        if (rows) refuse("q: the queries of all tokens are turned, `rows` takes some of them");
+    }
+    auto *weights = static_cast<float *>(operand_or_null(a[11], "weights", kF32, {k.B, k.H, ck.N}, k.dev));
+    auto *slots = static_cast<int *>(operand_or_null(a[12], "slot_positions", kI32, {k.B, k.H, ck.N}, k.dev));
+    int code;
+    {
+        Unlocked u;
+        const c10::cuda::CUDAGuard guard(k.dev);
+        if (a[10] != Py_None) q_out = empty({k.B, Hq, k.N, k.d}, kBf16, k.dev);
+        code = attn_cache_append(k.t.data_ptr(), v, ck.t.data_ptr(), cv, lengths, turns, positions, rows, q,
+                                 at_or_null(q_out), weights, slots, count(k.B), count(k.H), count(Hq), count(k.N),
+                                 count(n), count(k.d), count(ck.N), count(rotated), interleaved, amplitude,
+                                 stream(k.dev));
+    }
+    check(code, "attn_cache_append");
+    return wrap(q_out);
+}
+
+// q, cache_k, cache_v, lengths, tree, weights, counted, weights_out, scale -> (o, lse, weights_out or None)
+PyObject *cache_attention(Args a)
+{
+    const HeadsOf q(a[0], "q"), k(a[1], "cache_k");
+    if (k.dev != q.dev || k.B != q.B || k.d != q.d || k.H < 1 || q.H % k.H)
+        refuse("cache_k: expected [" + std::to_string(q.B) + ", H, C, " + std::to_string(q.d) + "] on " + q.dev.str() +
+               ", H a divisor of q's " + std::to_string(q.H) + " heads, got " + describe(k.t.sizes()) + " on " +
+               k.dev.str());
+    const void *v = operand(a[2], "cache_v", kBf16, k.t.sizes(), q.dev);
+    const auto *lengths = static_cast<const int *>(operand(a[3], "lengths", kI32, {q.B}, q.dev));
+    const auto *tree = static_cast<const uint64_t *>(operand_or_null(a[4], "tree", kI64, {q.B, q.N}, q.dev));
+    const auto *weights = static_cast<const float *>(operand_or_null(a[5], "weights", kF32, {k.B, k.H, k.N}, q.dev));
+    const auto *counted = static_cast<const uint64_t *>(operand_or_null(a[6], "counted", kI64, {q.B}, q.dev));
+    auto *given = static_cast<float *>(operand_or_null(a[7], "weights_out", kF32, {k.B, k.H, k.N}, q.dev));
+    if (a[5] == Py_None && (a[6] != Py_None || a[7] != Py_None))
+        refuse("counted and weights_out go with weights");
+    const auto scale = (float)number(a[8]);
+    const bool fresh = a[5] != Py_None && a[7] == Py_None;
+    at::Tensor o, lse, out;
+    int code;
+    {
+        Unlocked u;
+        const c10::cuda::CUDAGuard guard(q.dev);
+        o = empty(q.t.sizes(), kBf16, q.dev);
+        lse = empty({q.B, q.H, q.N}, kF32, q.dev);
+        if (fresh) out = empty({k.B, k.H, k.N}, kF32, q.dev);
+        const int G = count(q.H / k.H);
+        const size_t bytes =
+            attn_cache_attention_workspace_size(count(q.B), count(k.H), G, count(q.N), count(k.N), count(q.d));
+        const at::Tensor ws = empty({(int64_t)(bytes ? bytes : 1)}, at::kByte, q.dev);
+        code = attn_cache_attention(q.t.data_ptr(), k.t.data_ptr(), v, lengths, tree, counted, weights,
+                                    fresh ? static_cast<float *>(out.data_ptr()) : given, o.data_ptr(),
+                                    static_cast<float *>(lse.data_ptr()), ws.data_ptr(), bytes, count(q.B),
+                                    count(k.H), G, count(q.N), count(k.N), count(q.d), scale, stream(q.dev));
+    }
+    check(code, "attn_cache_attention");
+    if (a[7] == Py_None) return tuple(o, lse, out);
+    return tuple(o, lse, THPVariable_Unpack(a[7]));
+}
+
+// cache_k, cache_v, weights, slot_positions, lengths, keep, recent, weights_out, positions_out
+// -> (weights_out, positions_out, lengths_out)
+PyObject *cache_evict(Args a)
+{
+    const HeadsOf k(a[0], "cache_k");
+    void *v = operand(a[1], "cache_v", kBf16, k.t.sizes(), k.dev);
+    const c10::DimVector slots{k.B, k.H, k.N};
+    const auto *weights = static_cast<const float *>(operand(a[2], "weights", kF32, slots, k.dev));
+    const auto *positions = static_cast<const int *>(operand(a[3], "slot_positions", kI32, slots, k.dev));
+    const auto *lengths = static_cast<const int *>(operand(a[4], "lengths", kI32, {k.B}, k.dev));
+    const int keep = integer(a[5]), recent = integer(a[6]);
+    auto *w_given = static_cast<float *>(operand_or_null(a[7], "weights_out", kF32, slots, k.dev));
+    auto *p_given = static_cast<int *>(operand_or_null(a[8], "positions_out", kI32, slots, k.dev));
+    at::Tensor w, p, n;
+    int code;
+    {
+        Unlocked u;
+        const c10::cuda::CUDAGuard guard(k.dev);
+        if (a[7] == Py_None) w = empty(slots, kF32, k.dev);
+        if (a[8] == Py_None) p = empty(slots, kI32, k.dev);
+        n = empty({k.B}, kI32, k.dev);
+        const size_t bytes = attn_cache_evict_workspace_size(count(k.B), count(k.H), count(k.N), count(k.d), keep);
+        const at::Tensor ws = empty({(int64_t)(bytes ? bytes : 1)}, at::kByte, k.dev);
+        code = attn_cache_evict(k.t.data_ptr(), v, weights, positions, lengths,
+                                w_given || !w.defined() ? w_given : static_cast<float *>(w.data_ptr()),
+                                p_given || !p.defined() ? p_given : static_cast<int *>(p.data_ptr()),
+                                static_cast<int *>(n.data_ptr()), ws.data_ptr(), bytes, count(k.B), count(k.H),
+                                count(k.N), count(k.d), keep, recent, stream(k.dev));
+    }
+    check(code, "attn_cache_evict");
+    return tuple(a[7] == Py_None ? w : THPVariable_Unpack(a[7]), a[8] == Py_None ? p : THPVariable_Unpack(a[8]), n);
+}
+
 // A callable that raises AttnError(code, where).
 PyObject *set_error(PyObject *, PyObject *callable)
 {
@@ -437,6 +613,10 @@ PyMethodDef methods[] = {ENTRY(linear_forward, 6),
                          ENTRY(rms_norm_backward, 5),
                          ENTRY(rms_norm_q8, 4),
                          ENTRY(quantize_q8, 1),
+                         ENTRY(rotary, 6),
+                         ENTRY(cache_append, 13),
+                         ENTRY(cache_attention, 9),
+                         ENTRY(cache_evict, 9),
                          {"set_error", set_error, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 #undef ENTRY

@@ -1,0 +1,606 @@
+// Attention of one token, a chain or a tree of drafted tokens over a cache:
+//   o = sum_j p_j v_j,  p_j = exp(scale q.k_j - lse),  lse = log sum_j exp(scale q.k_j),
+// over the slots j < length and, of the T tokens that follow them in the cache, those that the token's mask
+// word names.  Bound by HBM: each slot's K and V (4 d bytes) meet the few rows of the heads that share them.
+//
+// few_kernel.  The rows of a (sequence, cached head), r = g T + t, are one contiguous block of q and o; a unit is
+// 8 NT of them.  The products are turned round so that the slots are the 16-row operand of mma.sync and the few
+// query rows its 8 columns: S^T = K Q^T, O^T = V^T P^T.  A warp takes 16 slots a step, and K and V go from global
+// memory straight into the operands' registers:
+//   K   thread (g, q) = (lane / 4, lane % 4) loads chunks 4 c + q of slots g and g + 8; the sum over d runs in the
+//       order that these chunks give, the same for Q.
+//   V   it loads chunk g (and g + 8) of slots 2 q, 2 q + 1, 2 q + 8, 2 q + 9; two slots' values of a column
+//       are put side by side by byte permutes, and column 8 g + j is row g of the j-th 16-row tile.
+//   P   leaves S^T's accumulator as pairs of rows; movmatrix turns it into pairs of slots.
+// No shared memory, no barrier in the loop: each warp keeps its own running maximum and sum, and K of the next
+// step is asked for as soon as S has consumed this one's, V likewise, so that 8 KB (d = 128) a warp are always
+// on their way.  P meets V as two bf16 terms (its own rounding and the rest), 2^-17 of it: the tensor cores are
+// idle most of the time, and one term alone would cost 2^-9 of each weight.
+//
+// Work is shared out in blocks of 64 slots over all units, the same number for each CTA (the lengths are on the
+// device, so each CTA finds its range itself).  A unit that one CTA has whole is finished there; the others'
+// parts go to the workspace with their maximum and sum, and join_kernel adds them in the order of their slots:
+// nothing depends on timing, results are bitwise reproducible.
+#include "cluster.cuh"
+#include "common.cuh"
+#include "kernels.h"
+
+namespace attn {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kFewWarps = 4;
+constexpr int kFewThreads = 32 * kFewWarps;
+constexpr int kBlock = 16 * kFewWarps;   // slots of a block of work
+
+__device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                 "{%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// Cached keys and values are read once (by one CTA): no room in L1 for them.
+__device__ __forceinline__ uint4 stream16(const uint4 *p)
+{
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+// Values that are not finite.
+__device__ __forceinline__ bool odd_value(float v) { return (__float_as_uint(v) & 0x7f800000u) == 0x7f800000u; }
+__device__ __forceinline__ bool odd_pair(uint32_t w) { return odd_value(lo(w)) || odd_value(hi(w)); }
+__device__ __forceinline__ bool any_odd(const uint4 &v)
+{
+    return odd_pair(v.x) || odd_pair(v.y) || odd_pair(v.z) || odd_pair(v.w);
+}
+__device__ __forceinline__ void drop_odd(uint32_t &w)
+{
+    if (odd_value(lo(w))) w &= 0xffff0000u;
+    if (odd_value(hi(w))) w &= 0x0000ffffu;
+}
+__device__ __forceinline__ void drop_odd(uint4 &v)
+{
+    drop_odd(v.x);
+    drop_odd(v.y);
+    drop_odd(v.z);
+    drop_odd(v.w);
+}
+
+// How the work of all units is shared out.  Sequence b has H * tiles units of blocks(b) blocks each.
+struct Plan {
+    int H, tiles, T, C;
+};
+
+// Slots of the cache ahead of the new tokens.
+__device__ __forceinline__ int length_of(const int *lengths, int b, int T, int C)
+{
+    return min(max(lengths[b], 0), C - T);
+}
+
+__device__ __forceinline__ int blocks_of(int length, int T) { return (length + T + kBlock - 1) / kBlock; }
+
+// Blocks ahead of sequence `upto` (upto = B: of all of them); by a whole warp, the same in every lane.
+__device__ __forceinline__ long long blocks_before(const int *lengths, int upto, const Plan &p)
+{
+    long long sum = 0;
+    for (int b = threadIdx.x & 31; b < upto; b += 32) sum += blocks_of(length_of(lengths, b, p.T, p.C), p.T);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return sum * p.H * p.tiles;
+}
+
+// The sequence that block `x` of all belongs to, and the blocks ahead of it; by a whole warp.
+__device__ __forceinline__ int sequence_of(const int *lengths, int B, const Plan &p, long long x, long long &before)
+{
+    const uint32_t lane = threadIdx.x & 31;
+    long long sum = 0;
+    for (int b0 = 0; b0 < B; b0 += 32) {
+        const int b = b0 + (int)lane;
+        const long long mine =
+            b < B ? (long long)blocks_of(length_of(lengths, b, p.T, p.C), p.T) * p.H * p.tiles : 0;
+        long long inc = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long t = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= (uint32_t)o) inc += t;
+        }
+        const uint32_t hit = __ballot_sync(0xffffffffu, b < B && x < sum + inc);
+        if (hit) {
+            const int l = __ffs(hit) - 1;
+            before = sum + __shfl_sync(0xffffffffu, inc - mine, l);
+            return b0 + l;
+        }
+        sum += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    return B;
+}
+
+// Which tokens token t sees, as bits.
+__device__ __forceinline__ uint64_t word_of(const uint64_t *tree, int b, int T, int t)
+{
+    return tree ? tree[(long long)b * T + t] : (2ull << t) - 1;
+}
+
+// Partial results: slot 2 c for the part that CTA c begins inside a unit, 2 c + 1 for the one it begins a unit with.
+struct Parts {
+    float *o;          // [2 grid][rows][d]
+    float2 *ml;        // [2 grid][rows]: maximum (of scores times log2 e) and sum
+};
+
+template <int D, int NT>
+struct FewSmem {
+    float o[kFewWarps][8 * NT][D + 4];
+    float m[kFewWarps][8 * NT], l[kFewWarps][8 * NT];
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) few_kernel(CacheAttnArgs a, Plan plan, Parts parts)
+{
+    constexpr int KC = D / 32;           // chunks of a K row a thread holds
+    constexpr int VC = D / 64;           // chunks of a V row a thread holds
+    constexpr int MT = D / 16;           // 16-row tiles of O^T
+    constexpr int R8 = 8 * NT;
+    __shared__ FewSmem<D, NT> sm;
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+    const int T = a.T, R = a.G * T;
+
+    const long long total = blocks_before(a.lengths, a.B, plan);
+    const long long per = (total + gridDim.x - 1) / gridDim.x;
+    long long x = per * blockIdx.x;
+    const long long end = min(x + per, total);
+    if (x >= end) return;
+    long long before;
+    int b = sequence_of(a.lengths, a.B, plan, x, before);
+    int length = length_of(a.lengths, b, T, a.C), nb = blocks_of(length, T);
+    const float to_log2 = a.scale * kLog2e;
+
+    while (x < end) {
+        while (x >= before + (long long)nb * plan.H * plan.tiles) {
+            before += (long long)nb * plan.H * plan.tiles;
+            ++b;
+            length = length_of(a.lengths, b, T, a.C);
+            nb = blocks_of(length, T);
+        }
+        const long long u = (x - before) / nb;               // unit of the sequence
+        const int first = (int)(x - before - u * nb);
+        const int last = (int)min((long long)nb, first + (end - x));
+        const int h = (int)(u / plan.tiles), tile = (int)(u % plan.tiles);
+        const int valid = length + T;
+        const long long head = (long long)b * plan.H + h;
+        const uint4 *kp = static_cast<const uint4 *>(a.k) + head * a.C * (D / 8);
+        const uint4 *vp = static_cast<const uint4 *>(a.v) + head * a.C * (D / 8);
+        const int r0 = tile * R8;
+
+        // Q's rows as the 8-column operand
+        uint4 qf[NT][KC];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int r = r0 + 8 * t + g;
+            const uint4 *qp = static_cast<const uint4 *>(a.q) + (head * R + r) * (D / 8);
+#pragma unroll
+            for (int c = 0; c < KC; ++c) qf[t][c] = r < R ? qp[4 * c + q] : make_uint4(0, 0, 0, 0);
+        }
+
+        float acc[NT][MT][4];
+        float m[NT][2], l[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            m[t][0] = m[t][1] = -INFINITY;
+            l[t][0] = l[t][1] = 0.f;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) acc[t][i][0] = acc[t][i][1] = acc[t][i][2] = acc[t][i][3] = 0.f;
+        }
+
+        uint4 kr[2][KC], vr[4][VC];
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        auto load_k = [&](int key) {     // slots behind the last one read as zeros, whatever lies there
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int c = 0; c < KC; ++c) {
+                    const int j = key + g + 8 * i;
+                    kr[i][c] = j < valid ? stream16(kp + (long long)j * (D / 8) + 4 * c + q) : zero;
+                }
+        };
+        auto load_v = [&](int key) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int c = 0; c < VC; ++c) {
+                    const int j = key + 2 * q + (i & 1) + 8 * (i >> 1);
+                    vr[i][c] = j < valid ? stream16(vp + (long long)j * (D / 8) + 8 * c + g) : zero;
+                }
+        };
+        const int key_end = min(last * kBlock, valid);
+        int key = first * kBlock + 16 * warp;
+        load_k(key);
+        load_v(key);
+        for (; key < key_end; key += kBlock) {
+            float s[NT][4];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+#pragma unroll
+            for (int c = 0; c < KC; ++c) {
+                const uint32_t a0[4] = {kr[0][c].x, kr[1][c].x, kr[0][c].y, kr[1][c].y};
+                const uint32_t a1[4] = {kr[0][c].z, kr[1][c].z, kr[0][c].w, kr[1][c].w};
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    mma16816(s[t], a0, qf[t][c].x, qf[t][c].y);
+                    mma16816(s[t], a1, qf[t][c].z, qf[t][c].w);
+                }
+            }
+            load_k(key + kBlock < key_end ? key + kBlock : valid);
+
+            const bool tail = key + 16 > length;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[t][e] *= to_log2;
+                if (tail) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int r = r0 + 8 * t + 2 * q + e;
+                        const uint64_t word = r < R ? word_of(a.tree, b, T, r % T) : 0;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int j = key + g + 8 * i - length;
+                            if (j >= 0 && !(j < T && (word >> j & 1))) s[t][e + 2 * i] = -INFINITY;
+                        }
+                    }
+                }
+                // The maximum is brought up to date only where some score exceeds it.
+                const float top[2] = {fmaxf(s[t][0], s[t][2]), fmaxf(s[t][1], s[t][3])};
+                if (__any_sync(0xffffffffu, top[0] > m[t][0] || top[1] > m[t][1])) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float w = fmaxf(m[t][e], top[e]);
+                        w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, 4));
+                        w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, 8));
+                        w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, 16));
+                        const float f = w == -INFINITY ? 1.f : ptx::ex2(m[t][e] - w);
+                        m[t][e] = w;
+                        l[t][e] *= f;
+#pragma unroll
+                        for (int i = 0; i < MT; ++i) {
+                            acc[t][i][e] *= f;
+                            acc[t][i][e + 2] *= f;
+                        }
+                    }
+                }
+            }
+            uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                float p[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float base = m[t][e & 1] == -INFINITY ? 0.f : m[t][e & 1];
+                    p[e] = ptx::ex2(s[t][e] - base);
+                    l[t][e & 1] += p[e];
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t w = ptx::pack_bf16x2(p[2 * i], p[2 * i + 1]);
+                    ph[t][i] = transpose8x8(w);
+                    pl[t][i] = transpose8x8(ptx::pack_bf16x2(p[2 * i] - lo(w), p[2 * i + 1] - hi(w)));
+                }
+            }
+            // A token's value that is not finite may reach the rows that see it alone, but 0 times it is NaN in a
+            // product: such values are added one by one and leave the operand.  Rare, and only among the T tokens.
+            if (tail && T > 1) {
+                bool odd = false;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int c = 0; c < VC; ++c)
+                        odd |= key + 2 * q + (i & 1) + 8 * (i >> 1) >= length && any_odd(vr[i][c]);
+                if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        for (int from = 0; from < 4; ++from) {      // slot 2 from + (i & 1) + 8 (i >> 1)
+                            const int j = 2 * from + (i & 1) + 8 * (i >> 1);
+                            if (key + j < length) continue;
+#pragma unroll
+                            for (int c = 0; c < VC; ++c) {
+                                const uint32_t w[4] = {__shfl_sync(0xffffffffu, vr[i][c].x, 4 * g + from),
+                                                       __shfl_sync(0xffffffffu, vr[i][c].y, 4 * g + from),
+                                                       __shfl_sync(0xffffffffu, vr[i][c].z, 4 * g + from),
+                                                       __shfl_sync(0xffffffffu, vr[i][c].w, 4 * g + from)};
+#pragma unroll
+                                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                                    for (int e = 0; e < 2; ++e) {
+                                        const float seen = __shfl_sync(0xffffffffu, s[t][e + 2 * (i >> 1)], 4 * (j % 8) + q);
+#pragma unroll
+                                        for (int x = 0; x < 8; ++x) {
+                                            const float v = x & 1 ? hi(w[x / 2]) : lo(w[x / 2]);
+                                            if (seen != -INFINITY && odd_value(v))
+                                                acc[t][D == 128 ? x : x & 3][e + 2 * (D == 128 ? c : x >> 2)] += v;
+                                        }
+                                    }
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int c = 0; c < VC; ++c)
+                            if (key + 2 * q + (i & 1) + 8 * (i >> 1) >= length) drop_odd(vr[i][c]);
+                }
+            }
+            // O^T += V^T P^T.  Tile j of 16 rows: columns 8 g + j of one chunk, and of the other (d = 64: the
+            // other half of the one).
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+                uint32_t af[4];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)          // a slot pair
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {    // rows g and g + 8 of the tile
+                        const int e = D == 128 ? j : j + 4 * c;     // column of the chunk
+                        const uint4 &x = vr[2 * i][D == 128 ? c : 0], &y = vr[2 * i + 1][D == 128 ? c : 0];
+                        const uint32_t u = e / 2 == 0 ? x.x : e / 2 == 1 ? x.y : e / 2 == 2 ? x.z : x.w;
+                        const uint32_t w = e / 2 == 0 ? y.x : e / 2 == 1 ? y.y : e / 2 == 2 ? y.z : y.w;
+                        af[2 * i + c] = __byte_perm(u, w, e & 1 ? 0x7632 : 0x5410);
+                    }
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    mma16816(acc[t][j], af, ph[t][0], ph[t][1]);
+                    mma16816(acc[t][j], af, pl[t][0], pl[t][1]);
+                }
+            }
+            load_v(key + kBlock < key_end ? key + kBlock : valid);
+        }
+
+        // Join the warps.
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 4);
+                l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 8);
+                l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 16);
+                const int r = 8 * t + 2 * q + e;
+                if (g == 0) {
+                    sm.m[warp][r] = m[t][e];
+                    sm.l[warp][r] = l[t][e];
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int j = 0; j < MT; j += 4)
+                        *reinterpret_cast<float4 *>(&sm.o[warp][r][D == 128 ? 64 * c + 8 * g + j : 8 * g + 4 * c]) =
+                            make_float4(acc[t][j][e + 2 * c], acc[t][j + 1][e + 2 * c], acc[t][j + 2][e + 2 * c],
+                                        acc[t][j + 3][e + 2 * c]);
+            }
+        __syncthreads();
+        const bool whole = first == 0 && last == nb;
+        const long long slot = 2 * blockIdx.x + (first == 0 ? 1 : 0);
+        constexpr int PER = D / 8;       // threads a row, 8 columns each
+        for (int i = threadIdx.x; i < R8 * PER; i += kFewThreads) {
+            const int r = i / PER, c = i % PER * 8;
+            float top = -INFINITY, f[kFewWarps], sum = 0.f, o[8];
+#pragma unroll
+            for (int w = 0; w < kFewWarps; ++w) top = fmaxf(top, sm.m[w][r]);
+            const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = 0.f;
+#pragma unroll
+            for (int w = 0; w < kFewWarps; ++w) {
+                f[w] = ptx::ex2(sm.m[w][r] - base);
+                sum += f[w] * sm.l[w][r];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] += f[w] * sm.o[w][r][c + e];
+            }
+            if (r0 + r >= R) continue;
+            if (whole) {
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;     // a row that sees nothing
+                const long long at = head * R + r0 + r;
+                *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + at * D + c) =
+                    make_uint4(ptx::pack_bf16x2(o[0] * inv, o[1] * inv), ptx::pack_bf16x2(o[2] * inv, o[3] * inv),
+                               ptx::pack_bf16x2(o[4] * inv, o[5] * inv), ptx::pack_bf16x2(o[6] * inv, o[7] * inv));
+                if (c == 0) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * (1.f / kLog2e);
+            } else {
+                float4 *to = reinterpret_cast<float4 *>(parts.o + (slot * R8 + r) * D + c);
+                to[0] = make_float4(o[0], o[1], o[2], o[3]);
+                to[1] = make_float4(o[4], o[5], o[6], o[7]);
+                if (c == 0) parts.ml[slot * R8 + r] = make_float2(top, sum);
+            }
+        }
+        __syncthreads();
+        x += last - first;
+    }
+}
+
+// Adds up the parts of one row, if its unit was split.  A block a row, a warp every fourth part.
+constexpr int kJoinWarps = 4;
+
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(CacheAttnArgs a, Plan plan, int rows, int ctas, Parts parts)
+{
+    __shared__ float so[kJoinWarps][D];
+    __shared__ float2 sml[kJoinWarps];
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int R = a.G * a.T;
+    const long long at = blockIdx.x;                 // row of o
+    const long long head = at / R;
+    const int r = (int)(at % R), b = (int)(head / plan.H), h = (int)(head % plan.H);
+    const long long total = blocks_before(a.lengths, a.B, plan);
+    const long long per = (total + ctas - 1) / ctas;
+    const int nb = blocks_of(length_of(a.lengths, b, a.T, a.C), a.T);
+    const long long u0 =
+        blocks_before(a.lengths, b, plan) + ((long long)h * plan.tiles + r / rows) * nb;
+    const long long c0 = u0 / per, c1 = (u0 + nb - 1) / per;
+    if (c0 == c1) return;                            // one CTA had it whole
+    const int count = (int)(c1 - c0 + 1);
+    auto slot = [&](int i) {                         // the first part begins the unit, the others inside it
+        return ((i == 0 ? 2 * c0 + 1 : 2 * (c0 + i)) * rows + r % rows);
+    };
+    float top = -INFINITY, sum = 0.f;
+    constexpr int PER = D / 32;
+    float o[PER];
+#pragma unroll
+    for (int e = 0; e < PER; ++e) o[e] = 0.f;
+    for (int i = warp; i < count; i += kJoinWarps) top = fmaxf(top, parts.ml[slot(i)].x);
+    const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll 4
+    for (int i = warp; i < count; i += kJoinWarps) {
+        const float2 ml = parts.ml[slot(i)];
+        const float f = ptx::ex2(ml.x - base);
+        const float *from = parts.o + slot(i) * D + lane * PER;
+        sum += f * ml.y;
+        if (PER == 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(from);
+            o[0] += f * v.x; o[1] += f * v.y; o[PER - 2] += f * v.z; o[PER - 1] += f * v.w;
+        } else {
+            const float2 v = *reinterpret_cast<const float2 *>(from);
+            o[0] += f * v.x; o[1] += f * v.y;
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < PER; ++e) so[warp][lane * PER + e] = o[e];
+    if (lane == 0) sml[warp] = make_float2(top, sum);
+    __syncthreads();
+    float all = -INFINITY, f[kJoinWarps], l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) all = fmaxf(all, sml[w].x);
+    const float ref = all == -INFINITY ? 0.f : all;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+        f[w] = ptx::ex2(sml[w].x - ref);
+        l += f[w] * sml[w].y;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    for (int c = threadIdx.x; c < D; c += 32 * kJoinWarps) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) v += f[w] * so[w][c];
+        static_cast<__nv_bfloat16 *>(a.o)[at * D + c] = __float2bfloat16(v * inv);
+    }
+    if (threadIdx.x == 0) a.lse[at] = l == 0.f ? -INFINITY : (all + log2f(l)) * (1.f / kLog2e);
+}
+
+// weights_out = weights + the weights that the counted rows give each slot: K is read a second time, the rows in
+// eights.  A block takes 64 slots of one (sequence, cached head).
+template <int D>
+__global__ void __launch_bounds__(kFewThreads) weights_kernel(CacheAttnArgs a, int blocks)
+{
+    constexpr int KC = D / 32;
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+    const long long head = blockIdx.x / blocks;
+    const int b = (int)(head / a.H), T = a.T, R = a.G * T;
+    const int key = (int)(blockIdx.x % blocks) * kBlock + 16 * warp;
+    const int length = length_of(a.lengths, b, T, a.C), valid = length + T;
+    float sum[2] = {0.f, 0.f};
+    if (key < valid) {
+        const uint64_t counted = a.counted ? a.counted[b] : ~0ull;
+        const uint4 *kp = static_cast<const uint4 *>(a.k) + head * a.C * (D / 8);
+        uint4 kr[2][KC];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int c = 0; c < KC; ++c) {
+                const int j = key + g + 8 * i;
+                kr[i][c] = j < valid ? stream16(kp + (long long)j * (D / 8) + 4 * c + q) : make_uint4(0, 0, 0, 0);
+            }
+        const bool tail = key + 16 > length;
+        for (int r0 = 0; r0 < R; r0 += 8) {
+            const int r = r0 + g;
+            const uint4 *qp = static_cast<const uint4 *>(a.q) + (head * R + r) * (D / 8);
+            float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < KC; ++c) {
+                const uint4 qf = r < R ? qp[4 * c + q] : make_uint4(0, 0, 0, 0);
+                const uint32_t a0[4] = {kr[0][c].x, kr[1][c].x, kr[0][c].y, kr[1][c].y};
+                const uint32_t a1[4] = {kr[0][c].z, kr[1][c].z, kr[0][c].w, kr[1][c].w};
+                mma16816(s, a0, qf.x, qf.y);
+                mma16816(s, a1, qf.z, qf.w);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int row = r0 + 2 * q + e, t = row % T;
+                if (row >= R || !(counted >> t & 1)) continue;
+                const float lse = a.lse[head * R + row];
+                const uint64_t word = tail ? word_of(a.tree, b, T, t) : 0;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int j = key + g + 8 * i - length;
+                    if (j >= 0 && !(j < T && (word >> j & 1))) continue;
+                    sum[i] += ptx::ex2((s[e + 2 * i] * a.scale - lse) * kLog2e);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
+        sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
+        const int j = key + g + 8 * i;
+        if (q == 0 && j < a.C) {
+            const long long at = head * a.C + j;
+            if (j < valid) a.weights_out[at] = a.weights[at] + sum[i];
+            else if (a.weights_out != a.weights) a.weights_out[at] = a.weights[at];
+        }
+    }
+}
+
+int rows_a_unit(int R) { return R <= 8 ? 8 : 16; }
+constexpr int kPlanSms = 152;    // the split is a function of the sizes and lengths alone
+int few_ctas(int rows) { return kPlanSms * (rows == 8 ? 3 : 2); }
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+template <int D>
+cudaError_t launch(const CacheAttnArgs &a, cudaStream_t stream)
+{
+    const int R = a.G * a.T, rows = rows_a_unit(R), ctas = few_ctas(rows);
+    const Plan plan = {a.H, (R + rows - 1) / rows, a.T, a.C};
+    Parts parts;
+    parts.o = static_cast<float *>(a.workspace);
+    parts.ml = reinterpret_cast<float2 *>(static_cast<char *>(a.workspace) + up256((size_t)2 * ctas * rows * D * 4));
+    cudaError_t e = rows == 8 ? launch_overlapped(few_kernel<D, 1>, dim3(ctas), dim3(kFewThreads), 0, 1, stream, a, plan, parts)
+                              : launch_overlapped(few_kernel<D, 2>, dim3(ctas), dim3(kFewThreads), 0, 1, stream, a, plan, parts);
+    if (e != cudaSuccess) return e;
+    e = launch_overlapped(join_kernel<D>, dim3((unsigned)((long long)a.B * a.H * R)), dim3(32 * kJoinWarps), 0, 1, stream,
+                          a, plan, rows, ctas, parts);
+    if (e != cudaSuccess || !a.weights) return e;
+    const int blocks = (a.C + kBlock - 1) / kBlock;
+    return launch_overlapped(weights_kernel<D>, dim3((unsigned)((long long)a.B * a.H * blocks)), dim3(kFewThreads), 0, 1,
+                             stream, a, blocks);
+}
+
+}  // namespace
+
+size_t cache_attn_workspace(int G, int T, int d)
+{
+    const int rows = rows_a_unit(G * T);
+    const size_t slots = (size_t)2 * few_ctas(rows) * rows;
+    return up256(slots * d * 4) + up256(slots * 8);
+}
+
+cudaError_t launch_cache_attn(const CacheAttnArgs &a, cudaStream_t stream)
+{
+    return a.d == 64 ? launch<64>(a, stream) : launch<128>(a, stream);
+}
+
+}  // namespace attn

@@ -181,6 +181,63 @@ cudaError_t launch_sum_rows(const float *part, float *out, int rows, int cols, c
 int norm_bwd_blocks(int M, int D);
 cudaError_t launch_rms_norm_bwd(const NormBwdArgs &a, cudaStream_t stream);
 
+// Rotary positions and the cache (see rotary.cu, cache_attn.cu, cache_evict.cu).
+struct RotaryArgs {
+    const void *x;              // [B,H,N,d] bf16
+    void *y;                    // the same; may be x
+    const int *positions;       // null (row n is at n), or [N] with pos_stride 0, or [B,N] with pos_stride N
+    const uint64_t *turns;      // [rotated / 2]: turns a position, in 2^-64
+    long long pos_stride;
+    int B, H, N, d, rotated;
+    float amplitude;
+};
+cudaError_t launch_rotary(const RotaryArgs &a, bool interleaved, bool backward, cudaStream_t stream);
+
+struct AppendArgs {
+    const void *k, *v, *q;              // [B,H,T,d], q null or [B,Hq,T,d] bf16
+    void *cache_k, *cache_v, *q_out;    // [B,H,C,d], q_out as q
+    const int *lengths;                 // [B]
+    const uint64_t *turns;              // null: nothing is turned
+    const int *positions;               // null (the slot's own number), or [B,T]
+    const int *rows;                    // null (all T), or [B,n]: which of the T tokens, none where negative
+    float *weights;                     // null, or [B,H,C]
+    int *slot_positions;                // null, or [B,H,C]
+    int B, H, Hq, T, n, d, C, rotated;
+    float amplitude;
+};
+cudaError_t launch_append(const AppendArgs &a, bool interleaved, cudaStream_t stream);
+
+struct CacheAttnArgs {
+    const void *q, *k, *v;              // [B,H*G,T,d], [B,H,C,d] bf16
+    const int *lengths;                 // [B]: slots ahead of the T tokens' own
+    const uint64_t *tree;               // null (a chain), or [B,T] mask words
+    const uint64_t *counted;            // null (all), or [B]: the tokens whose weights are added up
+    const float *weights;               // null, or [B,H,C]
+    float *weights_out;                 // [B,H,C], may be weights
+    void *o;                            // [B,H*G,T,d]
+    float *lse;                         // [B,H*G,T]
+    void *workspace;
+    int B, H, G, T, C, d;
+    float scale;
+    int *status;
+};
+size_t cache_attn_workspace(int G, int T, int d);
+cudaError_t launch_cache_attn(const CacheAttnArgs &a, cudaStream_t stream);
+
+struct EvictArgs {
+    void *k, *v;                        // [B,H,C,d] bf16, in place
+    const float *weights;               // [B,H,C]
+    const int *slot_positions;          // [B,H,C]
+    const int *lengths;                 // [B]
+    float *weights_out;                 // may be weights
+    int *positions_out;                 // may be slot_positions
+    int *lengths_out;                   // [B]
+    int *moves;                         // workspace: [B,H] x (count, then pairs)
+    int B, H, C, d, keep, recent;
+};
+size_t evict_workspace(int B, int H, int C, int keep);
+cudaError_t launch_evict(const EvictArgs &a, cudaStream_t stream);
+
 cudaError_t launch_vector_add(const float *a, const float *b, float *c, long long n,
                               cudaStream_t stream);
 cudaError_t launch_wait_selftest(int *status, uint64_t limit_ns, cudaStream_t stream);

@@ -1,0 +1,501 @@
+"""The cache on the GPU: append, attention of single, chained and drafted tokens, accumulated weights and eviction,
+against the formulas in 64 bits within derived bounds (see _cache_ref)."""
+import math
+import zlib
+
+import pytest
+import torch
+
+import self_attention_gb300 as sa
+import _cache_ref as ref
+
+pytestmark = pytest.mark.gpu
+NAN = float("nan")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from self_attention_gb300.build import build
+    sa.load_library(build())
+
+
+def _gen(*key):
+    return torch.Generator(device="cuda").manual_seed(zlib.crc32(repr(key).encode()))
+
+
+def _randn(g, *shape, std=1.0, dtype=torch.bfloat16):
+    return (torch.randn(shape, generator=g, device="cuda") * std).to(dtype)
+
+
+def _i32(*x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def _parents(g, B, T):
+    r = torch.rand(B, T, generator=g, device="cuda").cpu()
+    return [[int(r[b, t] * (t + 1)) - 1 for t in range(T)] for b in range(B)]
+
+
+def _cache(g, B, H, C, d, lengths, T, behind=NAN):
+    """k, v with `behind` in every slot that no token has."""
+    k, v = _randn(g, B, H, C, d), _randn(g, B, H, C, d)
+    for b, n in enumerate(lengths):
+        n = min(max(n, 0), C - T)
+        k[b, :, n + T:], v[b, :, n + T:] = behind, behind
+    return k, v
+
+
+# ------------------------------------------------------------------ append
+@pytest.mark.parametrize("B,H,Hq,T,d,C,rotated", [(1, 1, 1, 1, 64, 8, 64), (3, 2, 6, 5, 128, 40, 64),
+                                                  (32, 4, 16, 1, 128, 100, 128), (2, 5, 5, 300, 64, 333, 16)])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("given", [False, True])
+def test_append(B, H, Hq, T, d, C, rotated, interleaved, given):
+    g = _gen(B, H, T, d, interleaved, given)
+    lens = [(7 * b) % (C - T + 1) for b in range(B)]
+    k, v, q = _randn(g, B, H, T, d), _randn(g, B, H, T, d), _randn(g, B, Hq, T, d)
+    ck, cv = _randn(g, B, H, C, d), _randn(g, B, H, C, d)
+    w = torch.rand(B, H, C, generator=g, device="cuda")
+    slots = torch.full((B, H, C), -7, dtype=torch.int32, device="cuda")
+    was = [t.clone() for t in (ck, cv, w, slots)]
+    positions = torch.randint(0, 99999, (B, T), generator=g, device="cuda", dtype=torch.int32) if given else None
+    at = positions.cpu() if given else torch.tensor(lens).view(B, 1) + torch.arange(T)
+    out = sa.cache_append(k, v, ck, cv, _i32(*lens), sa.rotary_turns(rotated), positions, interleaved, 1.5, q=q,
+                          weights=w, slot_positions=slots)
+    f = ref.frequencies(rotated)
+    ref.check("q", out, *ref.turned(q.cpu(), at, f, interleaved, 1.5))
+    want, tol = ref.turned(k.cpu(), at, f, interleaved, 1.5)
+    for b, n in enumerate(lens):
+        ref.check("k", ck[b, :, n:n + T], want[b], tol[b])
+        assert torch.equal(cv[b, :, n:n + T], v[b]) and not bool(w[b, :, n:n + T].any())
+        assert torch.equal(slots[b, :, n:n + T].cpu(), at[b].int().expand(H, T))
+        for t in (ck, cv, w, slots):        # nothing else is touched
+            old = was[[ck is t, cv is t, w is t, slots is t].index(True)]
+            assert torch.equal(t[b, :, :n], old[b, :, :n]) and torch.equal(t[b, :, n + T:], old[b, :, n + T:])
+
+
+def test_append_of_rows_and_lengths_out_of_range():
+    g = _gen("rows")
+    B, H, T, d, C = 4, 3, 6, 64, 20
+    k, v = _randn(g, B, H, T, d), _randn(g, B, H, T, d)
+    ck, cv = _randn(g, B, H, C, d), _randn(g, B, H, C, d)
+    was_k, was_v = ck.clone(), cv.clone()
+    rows = torch.tensor([[0, 2, 5], [1, -1, 3], [6, 4, 4], [0, 1, 2]], dtype=torch.int32, device="cuda")
+    lens = [3, 0, -9, 18]
+    assert sa.cache_append(k, v, ck, cv, _i32(*lens), rows=rows) is None       # no turns: copied
+    for b, n in enumerate(lens):
+        n = max(n, 0)
+        want_k, want_v = was_k[b].clone(), was_v[b].clone()
+        for i, r in enumerate(rows[b].tolist()):
+            if 0 <= r < T and n + i < C:
+                want_k[:, n + i], want_v[:, n + i] = k[b, :, r], v[b, :, r]
+        assert torch.equal(ck[b], want_k) and torch.equal(cv[b], want_v)
+    ck.copy_(was_k)
+    sa.cache_append(k, v, ck, cv, _i32(C, C + 5, 2 ** 31 - 1, C))             # full: nothing is written
+    assert torch.equal(ck, was_k)
+    sa.cache_append(k[:, :, :0].contiguous(), v[:, :, :0].contiguous(), ck, cv, _i32(0, 0, 0, 0))
+    assert torch.equal(ck, was_k)
+
+
+# ------------------------------------------------------------------ attention
+CASES = [
+    # B, H, G, T, d, C, lengths
+    (1, 1, 1, 1, 64, 1, [0]),
+    (1, 1, 1, 1, 128, 130, [129]),
+    (2, 3, 4, 1, 128, 200, [63, 64]),
+    (3, 2, 1, 1, 64, 1000, [0, 999, 500]),
+    (2, 1, 8, 1, 128, 77, [15, 16]),
+    (2, 2, 9, 1, 64, 300, [290, 17]),
+    (1, 2, 16, 1, 128, 2100, [2050]),
+    (5, 1, 17, 1, 64, 90, [1, 2, 3, 88, 31]),
+    (2, 2, 1, 5, 128, 140, [120, 0]),
+    (2, 3, 2, 13, 64, 270, [255, 128]),
+    (1, 1, 4, 33, 128, 700, [600]),
+    (2, 2, 4, 64, 128, 330, [266, 1]),
+    (1, 2, 8, 64, 64, 400, [200]),
+    (2, 1, 3, 50, 128, 200, [127, 128]),
+    (1, 1, 1, 64, 64, 64, [0]),
+    (40, 2, 2, 1, 64, 70, [i % 69 for i in range(40)]),
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(map(str, c[:6])))
+@pytest.mark.parametrize("masked", [False, True])
+def test_attention(case, masked):
+    B, H, G, T, d, C, lens = case
+    g = _gen(case, masked)
+    q = _randn(g, B, H * G, T, d, std=2.0)
+    k, v = _cache(g, B, H, C, d, lens, T)
+    tree = sa.tree_words(_parents(g, B, T)) if masked else None
+    o, lse = sa.cache_attention(q, k, v, _i32(*lens), tree)
+    want_o, want_l, _ = ref.attention(q, k, v, lens, tree)
+    ref.check("o", o, *want_o)
+    ref.check("lse", lse, *want_l)
+    again = sa.cache_attention(q, k, v, _i32(*lens), tree)
+    assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(map(str, c[:6])))
+@pytest.mark.parametrize("some", [False, True])
+def test_weights(case, some):
+    B, H, G, T, d, C, lens = case
+    g = _gen(case, some, "weights")
+    q = _randn(g, B, H * G, T, d, std=2.0)
+    k, v = _cache(g, B, H, C, d, lens, T)
+    w = torch.rand(B, H, C, generator=g, device="cuda")
+    tree = sa.tree_words(_parents(g, B, T))
+    counted = torch.tensor([(0x5A5A5A5A5A5A5A5B * (b + 1)) % 2 ** 63 for b in range(B)], device="cuda") if some else None
+    was = w.clone()
+    o, lse, out = sa.cache_attention(q, k, v, _i32(*lens), tree, weights=w, counted=counted)
+    assert torch.equal(w, was)
+    want_o, want_l, want_w = ref.attention(q, k, v, lens, tree, w, counted)
+    ref.check("o", o, *want_o)
+    ref.check("lse", lse, *want_l)
+    ref.check("weights", out, *want_w)
+    o2, lse2, out2 = sa.cache_attention(q, k, v, _i32(*lens), tree, weights=w, counted=counted, weights_out=w)
+    assert out2 is w and torch.equal(out, w) and torch.equal(o, o2) and torch.equal(lse, lse2)
+    plain = sa.cache_attention(q, k, v, _i32(*lens), tree)
+    assert torch.equal(o, plain[0]) and torch.equal(lse, plain[1])
+
+
+@pytest.mark.parametrize("T,G", [(3, 1), (20, 2), (64, 4)])
+def test_rows_that_see_nothing_or_odd_sets(T, G):
+    """Masks that are no trees: empty rows, a row that sees only others, all bits."""
+    g = _gen("odd", T, G)
+    B, H, d, C = 3, 2, 64, 150
+    lens = [0, 0, 70]
+    q = _randn(g, B, H * G, T, d, std=2.0)
+    k, v = _cache(g, B, H, C, d, lens, T)
+    words = torch.randint(-(2 ** 63), 2 ** 63 - 1, (B, T), generator=g, device="cuda")
+    words[:, 0] = 0
+    words[0] = 0
+    words[1, 1] = -1
+    words[2, 2] = 1 << (T - 1) if T < 64 else -(2 ** 63)
+    w = torch.rand(B, H, C, generator=g, device="cuda")
+    o, lse, out = sa.cache_attention(q, k, v, _i32(*lens), words, weights=w)
+    want_o, want_l, want_w = ref.attention(q, k, v, lens, words.cpu(), w)
+    assert not bool(o[0].any()) and bool((lse[0] == -math.inf).all())
+    ref.check("o", o, *want_o)
+    ref.check("lse", lse, *want_l)
+    ref.check("weights", out, *want_w)
+
+
+@pytest.mark.parametrize("T,G,d", [(4, 1, 64), (7, 2, 128), (30, 4, 128), (64, 2, 64), (64, 4, 128)])
+@pytest.mark.parametrize("value", [NAN, math.inf, -math.inf])
+def test_what_a_row_does_not_see_does_not_reach_it(T, G, d, value):
+    """A drafted token whose key and value are not finite spoils its descendants' rows alone."""
+    g = _gen("poison", T, G, d, str(value))
+    B, H, C, n = 2, 2, 300, [200, 3]
+    q = _randn(g, B, H * G, T, d)
+    k, v = _cache(g, B, H, C, d, n, T)
+    parents = _parents(g, B, T)
+    parents[0][1] = parents[1][1] = 0
+    tree = sa.tree_words(parents)
+    clean = sa.cache_attention(q, k, v, _i32(*n), tree)
+    for b in range(B):
+        v[b, :, n[b] + 1, 5] = value
+        v[b, :, n[b] + T - 1, d - 1] = value
+    o, lse = sa.cache_attention(q, k, v, _i32(*n), tree)
+    assert torch.equal(lse, clean[1])
+    sees = (tree.unsqueeze(-1) >> torch.tensor([1, T - 1], device="cuda") & 1).bool().view(B, 1, T, 2)
+    bad = torch.zeros_like(o, dtype=torch.bool)
+    bad[..., 5] = sees[..., 0]
+    bad[..., d - 1] |= sees[..., 1]
+    assert torch.equal(o.isfinite(), ~bad)
+    assert torch.equal(o[~bad], clean[0][~bad])
+    k[0, :, n[0] + 1] = value                    # a key: the rows that see it have no weights at all
+    o, lse = sa.cache_attention(q, k, v, _i32(*n), tree)
+    safe = ~sees[0, 0, :, 0]
+    assert torch.equal(lse[0][:, safe], clean[1][0][:, safe])
+    keep = safe.view(1, T, 1) & ~bad[0]
+    assert torch.equal(o[0][keep.expand_as(o[0])], clean[0][0][keep.expand_as(o[0])])
+
+
+def test_lengths_out_of_range_are_taken_as_the_nearest():
+    g = _gen("range")
+    B, H, G, T, d, C = 4, 2, 2, 3, 64, 90
+    q, k, v = _randn(g, B, H * G, T, d), _randn(g, B, H, C, d), _randn(g, B, H, C, d)
+    got = sa.cache_attention(q, k, v, _i32(-1, C, -2 ** 31, 2 ** 31 - 1))
+    want = sa.cache_attention(q, k, v, _i32(0, C - T, 0, C - T))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_large_scores_and_scales():
+    """Scores of thousands: one slot takes everything; a small scale: all alike."""
+    g = _gen("large")
+    B, H, T, d, C = 2, 2, 2, 128, 300
+    q, k, v = _randn(g, B, H, T, d, std=40.0), _randn(g, B, H, C, d, std=10.0), _randn(g, B, H, C, d)
+    for scale in (1.0, 1e-4):
+        o, lse = sa.cache_attention(q, k, v, _i32(298, 100), scale=scale)
+        want_o, want_l, _ = ref.attention(q, k, v, [298, 100], scale=scale)
+        ref.check("o", o, *want_o)
+        ref.check("lse", lse, *want_l)
+
+
+def test_chain_is_attention_over_a_prefix():
+    """A token over a cache of n is the framework's attention of its row over n + 1 keys."""
+    g = _gen("prefix")
+    B, H, N, d = 2, 4, 257, 64
+    q, k, v = _randn(g, B, H, N, d), _randn(g, B, H, N, d), _randn(g, B, H, N, d)
+    o, lse = sa.forward(q, k, v)
+    one, l1 = sa.cache_attention(q[:, :, -1:].contiguous(), k, v, _i32(N - 1, N - 1))
+    assert (lse[:, :, -1:] - l1).abs().max() < 1e-3
+    assert (o[:, :, -1:].float() - one.float()).abs().max() < 1e-2
+
+
+@pytest.mark.parametrize("G,T", [(1, 1), (2, 64)])
+def test_cache_past_2_31_elements(G, T):
+    """The last head of a cache of 2^32 bytes and more."""
+    B, H, C, d = 1, 17, 1 << 20, 128
+    n = C - T
+    g = _gen("huge", G)
+    k = torch.zeros(B, H, C, d, dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros(B, H, C, d, dtype=torch.bfloat16, device="cuda")
+    assert k.numel() > 2 ** 31
+    q = _randn(g, B, H * G, T, d)
+    v[:, -1, :, :] = 1
+    k[:, -1, -T - 1, :] = 4 * q[:, -1, 0]
+    v[:, -1, -T - 1, :] = 3
+    o, lse = sa.cache_attention(q, k, v, _i32(n))
+    s = (4 * q[:, -1, 0].double()).square().sum() / 4 / math.sqrt(d)
+    z = torch.logsumexp(torch.tensor([s.item()] + [0.0] * 0), 0)
+    want = torch.logaddexp(s.cpu(), torch.tensor(math.log(n), dtype=torch.float64))
+    assert abs(lse[0, -1, 0].item() - want.item()) < 1e-3 * (1 + abs(want.item())) and z is not None
+    share = math.exp(s.item() - want.item())
+    assert abs(o[0, -1, 0].float().mean().item() - (3 * share + 1 * (1 - share))) < 3e-2
+    assert not bool(o[0, 0].any())
+
+
+def test_refusals():
+    B, H, G, T, d, C = 2, 2, 3, 4, 64, 40
+    q = torch.zeros(B, H * G, T, d, dtype=torch.bfloat16, device="cuda")
+    k = torch.zeros(B, H, C, d, dtype=torch.bfloat16, device="cuda")
+    v, n = k.clone(), _i32(1, 2)
+    w, tree = torch.zeros(B, H, C, device="cuda"), torch.zeros(B, T, dtype=torch.int64, device="cuda")
+    sa.cache_attention(q, k, v, n, tree, weights=w, counted=tree[:, 0].contiguous())
+    bad = [dict(q=q.float()), dict(q=q[0]), dict(q=q.transpose(1, 2)), dict(q=q[:, :5].contiguous()), dict(q=q.cpu()),
+           dict(k=k.half()), dict(k=k[:1]), dict(v=v[:, :, :-1].contiguous()), dict(v=v.float()), dict(n=n.long()),
+           dict(n=n[:1]), dict(n=n.cpu()), dict(tree=tree.int()), dict(tree=tree[:, :2].contiguous()),
+           dict(weights=w.double()), dict(weights=w[..., :-1].contiguous()), dict(weights=None, counted=n.long()),
+           dict(weights=None, weights_out=w), dict(weights_out=w.double()), dict(counted=n)]
+    for kw in bad:
+        a = dict(q=q, k=k, v=v, n=n, tree=tree, weights=w)
+        a.update(kw)
+        with pytest.raises(ValueError):
+            sa.cache_attention(a.pop("q"), a.pop("k"), a.pop("v"), a.pop("n"), **a)
+    for kw in (dict(scale=0.0), dict(scale=-1.0), dict(scale=NAN), dict(scale=math.inf)):
+        with pytest.raises(sa.AttnError):
+            sa.cache_attention(q, k, v, n, **kw)
+    big = torch.zeros(B, H, 65, d, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(sa.AttnError):                                # more than 64 tokens
+        sa.cache_attention(big, torch.zeros(B, H, 100, d, dtype=torch.bfloat16, device="cuda"),
+                           torch.zeros(B, H, 100, d, dtype=torch.bfloat16, device="cuda"), n)
+    with pytest.raises(sa.AttnError):                                # more tokens than slots
+        sa.cache_attention(q, k[:, :, :3].contiguous(), v[:, :, :3].contiguous(), n)
+    with pytest.raises(sa.AttnError):
+        sa.cache_attention(*(torch.zeros(1, 1, 2, 96, dtype=torch.bfloat16, device="cuda") for _ in range(3)), _i32(0))
+    for p in ([[0, 0]], [[-1, 1]], [[]], [[-1], [-1, 0]], [[-1] * 65]):
+        with pytest.raises(ValueError):
+            sa.tree_words(p)
+    with pytest.raises(ValueError):
+        sa.cache_append(q, q, k, v, n)
+    new = torch.zeros(B, H, T, d, dtype=torch.bfloat16, device="cuda")
+    rows = torch.zeros(B, 2, dtype=torch.int32, device="cuda")
+    for kw in (dict(rows=rows.long()), dict(rows=rows[:1]), dict(rows=rows, q=q), dict(q=q.float()),
+               dict(q=q[:, :, :2].contiguous()), dict(positions=rows), dict(weights=w.half()),
+               dict(slot_positions=w), dict(turns=rows)):
+        with pytest.raises(ValueError):
+            sa.cache_append(new, new, k, v, n, **kw)
+    with pytest.raises(sa.AttnError):                                # into the tokens themselves
+        sa.cache_append(new, new, new, v[:, :, :T].contiguous(), n)
+    with pytest.raises(sa.AttnError):                                # k and v into one cache
+        sa.cache_append(new, new, k, k, n)
+    slots = torch.zeros(B, H, C, dtype=torch.int32, device="cuda")
+    for kw in (dict(keep=0), dict(keep=-1), dict(keep=4, recent=5), dict(keep=4, recent=-1), dict(keep=2 ** 40)):
+        with pytest.raises(sa.AttnError):
+            sa.cache_evict(k, v, w, slots, n, **kw)
+    for a in ((k, v, w.double(), slots, n), (k, v, w, slots.long(), n), (k, v, w, slots, n.long()),
+              (k, v[:, :, :9].contiguous(), w, slots, n), (k, v, w[..., :9].contiguous(), slots, n)):
+        with pytest.raises(ValueError):
+            sa.cache_evict(*a, 4)
+    with pytest.raises(sa.AttnError):
+        sa.cache_evict(k, k, w, slots, n, 4)
+
+
+# ------------------------------------------------------------------ eviction
+def _evict_case(g, B, H, C, d):
+    k, v = _randn(g, B, H, C, d), _randn(g, B, H, C, d)
+    w = torch.rand(B, H, C, generator=g, device="cuda") ** 6 * 20
+    pos = torch.rand(B, H, C, generator=g, device="cuda").argsort(-1).to(torch.int32)
+    return k, v, w, pos
+
+
+def _check_evict(k, v, w, pos, lens, keep, recent, in_place=False):
+    want = ref.evict(k, v, w, pos, lens, keep, recent)
+    where = dict(weights_out=w, positions_out=pos) if in_place else {}
+    w2, p2, n2 = sa.cache_evict(k, v, w, pos, _i32(*lens), keep, recent, **where)
+    for name, got, x in zip(("k", "v", "weights", "positions", "lengths"), (k, v, w2, p2, n2), want):
+        x = x.to(got.device)
+        same = (got == x) | (got.isnan() & x.isnan()) if got.is_floating_point() else got == x
+        assert bool(same.all()), (name, same.logical_not().nonzero()[:5].tolist())
+    return w2, p2, n2
+
+
+@pytest.mark.parametrize("B,H,C,d,lens,keep,recent", [
+    (1, 1, 1, 64, [1], 1, 0), (1, 1, 2, 128, [2], 1, 1), (1, 1, 2, 64, [2], 1, 0),
+    (3, 2, 100, 64, [100, 64, 3], 64, 10), (2, 3, 1025, 128, [1025, 1000], 1000, 100),
+    (2, 1, 5000, 64, [5000, 4097], 33, 33), (4, 2, 300, 128, [0, 300, 1, 77], 76, 0),
+    (1, 2, 2500, 64, [2500], 2499, 1), (1, 1, 3000, 128, [2999], 1500, 700), (2, 2, 40, 64, [40, 39], 50, 50)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict(B, H, C, d, lens, keep, recent, in_place):
+    g = _gen(B, H, C, lens, keep, recent, in_place)
+    _check_evict(*_evict_case(g, B, H, C, d), lens, keep, recent, in_place)
+
+
+def test_evict_ties_and_odd_weights():
+    g = _gen("ties")
+    B, H, C, d = 2, 2, 2300, 64
+    k, v, w, pos = _evict_case(g, B, H, C, d)
+    w = (w * 2).floor().clamp_max(3.0)                       # a handful of values, most of them zero
+    w[0, 0, 5], w[0, 0, 2000], w[0, 1, 7], w[1, 0, 1111] = NAN, -3.0, math.inf, -math.inf
+    w[1, 1] = 0
+    _check_evict(k, v, w, pos, [2300, 2200], 900, 50)
+    k, v, w, pos = _evict_case(g, B, H, C, d)
+    w[0, 0] = 1e-42                                          # subnormal
+    w[0, 0, 1500:] = 2e-42
+    pos[1] = 3                                               # one position everywhere: all are the newest
+    _check_evict(k, v, w, pos, [2300, 2300], 700, 20)
+
+
+def test_evict_of_a_long_cache():
+    """More slots than fit shared memory."""
+    g = _gen("long")
+    B, H, C, d = 1, 2, 60001, 64
+    k, v, w, pos = _evict_case(g, B, H, C, d)
+    for in_place in (False, True):
+        _check_evict(k.clone(), v.clone(), w.clone(), pos.clone(), [60001], 20000, 999, in_place)
+
+
+def test_evict_leaves_the_rest():
+    """Slots that nothing moves into keep their keys and values, those behind the last among them."""
+    g = _gen("rest")
+    k, v, w, pos = _evict_case(g, 1, 1, 128, 64)
+    k[:, :, 100:], v[:, :, 100:] = NAN, NAN
+    was = k.clone()
+    _check_evict(k, v, w, pos, [100], 60, 5)
+    assert bool(k[:, :, 100:].isnan().all()) and torch.equal(k[:, :, 60:100], was[:, :, 60:100])
+
+
+# ------------------------------------------------------------------ together
+def test_decoding_with_drafts_and_eviction():
+    """A prompt, drafted trees, the accepted path, eviction, the next token: each step against the formulas."""
+    g = _gen("together")
+    B, H, G, d, C = 2, 2, 2, 64, 256
+    turns, f = sa.rotary_turns(32), ref.frequencies(32)
+    ck, cv = (torch.full((B, H, C, d), NAN, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    w = torch.zeros(B, H, C, device="cuda")
+    slots = torch.full((B, H, C), -1, dtype=torch.int32, device="cuda")
+    lengths = _i32(0, 0)
+    N = 150
+    k, v = _randn(g, B, H, N, d), _randn(g, B, H, N, d)
+    sa.cache_append(k, v, ck, cv, lengths, turns, weights=w, slot_positions=slots)
+    lengths = lengths + N
+    last = torch.full((B,), N, dtype=torch.int32, device="cuda")
+    for step in range(3):
+        T = (1, 6, 40)[step]
+        parents = _parents(g, B, T)
+        tree = sa.tree_words(parents)
+        depth = torch.zeros(B, T, dtype=torch.int32)
+        for b in range(B):
+            for t in range(T):
+                depth[b, t] = depth[b, parents[b][t]] + 1 if parents[b][t] >= 0 else 0
+        positions = last.view(B, 1) + depth.cuda()
+        k, v, q = _randn(g, B, H, T, d), _randn(g, B, H, T, d), _randn(g, B, H * G, T, d)
+        qt = sa.cache_append(k, v, ck, cv, lengths, turns, positions, q=q, weights=w, slot_positions=slots)
+        ref.check("q", qt, *ref.turned(q.cpu(), positions.cpu(), f))
+        want = ref.attention(qt, ck, cv, lengths.tolist(), tree, w)
+        o, lse, w = sa.cache_attention(qt, ck, cv, lengths, tree, weights=w)
+        for name, got, x in zip(("o", "lse", "weights"), (o, lse, w), want):
+            ref.check(name, got, *x)
+        path = torch.full((B, 3), -1, dtype=torch.int32)
+        for b in range(B):                               # from the last token to its root
+            at, line = T - 1, []
+            while at >= 0:
+                line.append(at)
+                at = parents[b][at]
+            line = line[::-1][:3]
+            path[b, :len(line)] = torch.tensor(line, dtype=torch.int32)
+        sa.cache_append(k, v, ck, cv, lengths, turns, positions, rows=path.cuda(), weights=w, slot_positions=slots)
+        for b in range(B):
+            n = int(lengths[b])
+            for i, r in enumerate(path[b].tolist()):
+                if r >= 0:
+                    assert torch.equal(cv[b, :, n + i], v[b, :, r])
+                    assert bool((slots[b, :, n + i] == positions[b, r]).all())
+        taken = (path >= 0).sum(1).to(torch.int32).cuda()
+        lengths, last = lengths + taken, last + taken
+        w, slots, lengths = _check_evict(ck, cv, w, slots, lengths.tolist(), 120, 16, in_place=bool(step % 2))
+        assert lengths.tolist() == [120, 120]
+
+
+def test_captured_and_replayed_steps_on_another_stream():
+    g = _gen("graph")
+    B, H, G, d, C = 3, 2, 4, 128, 500
+    turns = sa.rotary_turns(128)
+    ck, cv = _randn(g, B, H, C, d), _randn(g, B, H, C, d)
+    k, v, q = _randn(g, B, H, 1, d), _randn(g, B, H, 1, d), _randn(g, B, H * G, 1, d)
+    w = torch.rand(B, H, C, generator=g, device="cuda")
+    pos = torch.arange(C, dtype=torch.int32, device="cuda").repeat(B, H, 1)
+    lengths = _i32(300, 10, 499)
+    start = [t.clone() for t in (ck, cv, w, pos, lengths)]
+
+    def step():
+        qt = sa.cache_append(k, v, ck, cv, lengths, turns, q=q, weights=w, slot_positions=pos)
+        o, lse, _ = sa.cache_attention(qt, ck, cv, lengths, weights=w, weights_out=w)
+        sa.cache_evict(ck, cv, w, pos, lengths + 1, 256, 32, w, pos)
+        lengths.copy_((lengths + 1).clamp_max(256))
+        return o, lse
+
+    def reset():
+        for t, x in zip((ck, cv, w, pos, lengths), start):
+            t.copy_(x)
+
+    eager = []
+    for _ in range(3):
+        o, lse = step()
+        eager.append((o.clone(), lse.clone()))
+    after = [t.clone() for t in (ck, cv, w, pos, lengths)]
+    reset()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        o, lse = step()
+    reset()
+    for i in range(3):
+        graph.replay()
+        assert torch.equal(o, eager[i][0]) and torch.equal(lse, eager[i][1])
+    for t, x in zip((ck, cv, w, pos, lengths), after):
+        assert torch.equal(t, x)
+
+
+def test_streams_at_once():
+    """Two streams with calls in flight at once, each with its own workspace."""
+    g = _gen("streams")
+    B, H, G, T, d, C = 2, 2, 2, 8, 64, 3000
+    q = [_randn(g, B, H * G, T, d) for _ in range(2)]
+    k, v = _randn(g, B, H, C, d), _randn(g, B, H, C, d)
+    n = _i32(2990, 1234)
+    want = [sa.cache_attention(x, k, v, n) for x in q]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[] for _ in range(2)]
+    for _ in range(20):
+        for i in range(2):
+            got[i].append(sa.cache_attention(q[i], k, v, n, stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o, lse in got[i]:
+            assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
