@@ -84,6 +84,7 @@ __device__ __forceinline__ void drop_odd(uint4 &v)
 // How the work of all units is shared out.  Sequence b has H * tiles units of blocks(b) blocks each.
 struct Plan {
     int H, tiles, T, C;
+    int block;       // slots a block of work
 };
 
 // Slots of the cache ahead of the new tokens.
@@ -92,13 +93,13 @@ __device__ __forceinline__ int length_of(const int *lengths, int b, int T, int C
     return min(max(lengths[b], 0), C - T);
 }
 
-__device__ __forceinline__ int blocks_of(int length, int T) { return (length + T + kBlock - 1) / kBlock; }
+__device__ __forceinline__ int blocks_of(int length, const Plan &p) { return (length + p.T + p.block - 1) / p.block; }
 
 // Blocks ahead of sequence `upto` (upto = B: of all of them); by a whole warp, the same in every lane.
 __device__ __forceinline__ long long blocks_before(const int *lengths, int upto, const Plan &p)
 {
     long long sum = 0;
-    for (int b = threadIdx.x & 31; b < upto; b += 32) sum += blocks_of(length_of(lengths, b, p.T, p.C), p.T);
+    for (int b = threadIdx.x & 31; b < upto; b += 32) sum += blocks_of(length_of(lengths, b, p.T, p.C), p);
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     return sum * p.H * p.tiles;
@@ -112,7 +113,7 @@ __device__ __forceinline__ int sequence_of(const int *lengths, int B, const Plan
     for (int b0 = 0; b0 < B; b0 += 32) {
         const int b = b0 + (int)lane;
         const long long mine =
-            b < B ? (long long)blocks_of(length_of(lengths, b, p.T, p.C), p.T) * p.H * p.tiles : 0;
+            b < B ? (long long)blocks_of(length_of(lengths, b, p.T, p.C), p) * p.H * p.tiles : 0;
         long long inc = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -168,7 +169,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) few_kernel(Cache
     if (x >= end) return;
     long long before;
     int b = sequence_of(a.lengths, a.B, plan, x, before);
-    int length = length_of(a.lengths, b, T, a.C), nb = blocks_of(length, T);
+    int length = length_of(a.lengths, b, T, a.C), nb = blocks_of(length, plan);
     const float to_log2 = a.scale * kLog2e;
 
     while (x < end) {
@@ -176,7 +177,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) few_kernel(Cache
             before += (long long)nb * plan.H * plan.tiles;
             ++b;
             length = length_of(a.lengths, b, T, a.C);
-            nb = blocks_of(length, T);
+            nb = blocks_of(length, plan);
         }
         const long long u = (x - before) / nb;               // unit of the sequence
         const int first = (int)(x - before - u * nb);
@@ -429,6 +430,487 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) few_kernel(Cache
     }
 }
 
+// ------------------------------------------------------------------------------------------
+// many_kernel: more than 16 rows a cached head, on tcgen05.  One CTA an SM with two streams that alternate on the
+// tensor core, so that one's softmax overlaps the other's products.  Up to 128 rows (MODE 1) both streams have the
+// same rows, and every other tile of 128 slots each, with maxima, sums and O of their own that meet at the end; up
+// to 256 (MODE 2) each has 128 rows, over the same tiles, so that K and V are still read once.
+//   warps 0-7   softmax: stream warp / 4, thread = row (= TMEM lane): S from TMEM, running maximum (moved when a tile
+//               raises it by more than kTau) and sum, P back over S, O rescaled where the maximum moved.
+//   warp 8      TMA: Q, then K and V tiles through one ring, in the order in which the products take them.
+//   warp 9      tcgen05: per job (a stream's tile) O += P V, then S of the stream's next job.
+//   warps 10-11 the tiles that end behind the cache: V's rows behind the last token are zeroed, and what is not
+//               finite among the tokens' own (0 times it would be NaN in rows that do not see it; the rows that do
+//               get it when O is written).
+// P is bf16, as V is (the operands of a product share their type).  TMEM columns: S_0, S_1, O_0, O_1.
+constexpr int kManyTile = 128;
+constexpr float kTau = 8.0f;
+
+template <int D, int MODE>
+struct ManyCfg {
+    static constexpr int Q_BYTES = 128 * D * 2, KV_BYTES = kManyTile * D * 2;
+    static constexpr int STAGES = D == 128 ? 5 : 10;
+    static constexpr int SMEM = MODE * Q_BYTES + STAGES * KV_BYTES + 1024;
+    static_assert(SMEM <= 227 * 1024 - 512 - (MODE == 1 ? 2048 : 0), "dynamic + static shared memory over 227 KB");
+    static constexpr int TMA_WARP = 8, MMA_WARP = 9, FIX_WARP = 10, THREADS = 384;
+    static constexpr uint32_t TM_O = 256;
+};
+
+struct ManyMaps {
+    CUtensorMap q, k, v;      // [B H][G T][d] in boxes of 128 rows, [B H][C][d] in tiles; 64 columns each
+};
+
+// The run of blocks of one unit that a CTA works on next.
+struct Segment {
+    long long unit_row;       // (b H + h): which cached head
+    int b, h, tile, first, last, nb, length;
+};
+
+// Walks over a CTA's share; begun by a whole warp, stepped by any thread.
+struct Walk {
+    long long x, end, before;
+    int b, length, nb;
+    __device__ __forceinline__ bool begin(const CacheAttnArgs &a, const Plan &plan)
+    {
+        const long long total = blocks_before(a.lengths, a.B, plan);
+        const long long per = (total + gridDim.x - 1) / gridDim.x;
+        x = per * blockIdx.x;
+        end = min(x + per, total);
+        if (x >= end) return false;
+        b = sequence_of(a.lengths, a.B, plan, x, before);
+        length = length_of(a.lengths, b, plan.T, plan.C);
+        nb = blocks_of(length, plan);
+        return true;
+    }
+    __device__ __forceinline__ bool next(const CacheAttnArgs &a, const Plan &plan, Segment &s)
+    {
+        if (x >= end) return false;
+        while (x >= before + (long long)nb * plan.H * plan.tiles) {
+            before += (long long)nb * plan.H * plan.tiles;
+            ++b;
+            length = length_of(a.lengths, b, plan.T, plan.C);
+            nb = blocks_of(length, plan);
+        }
+        const long long u = (x - before) / nb;
+        s.first = (int)(x - before - u * nb);
+        s.last = (int)min((long long)nb, s.first + (end - x));
+        s.h = (int)(u / plan.tiles);
+        s.tile = (int)(u % plan.tiles);
+        s.b = b;
+        s.nb = nb;
+        s.length = length;
+        s.unit_row = (long long)b * plan.H + s.h;
+        x += s.last - s.first;
+        return true;
+    }
+};
+
+// Waits for what is already on its way, for a second at most, whether or not the CTA has given up.
+__device__ __forceinline__ void drain(uint64_t *bar, uint32_t parity)
+{
+    const uint64_t t0 = globaltimer_ns();
+    while (!ptx::mbar_try_wait(bar, parity))
+        if (globaltimer_ns() - t0 > 1000000000ull) return;
+}
+
+// Places of tile j's K and V among the n tiles' loads of a segment.
+template <int MODE>
+__device__ __forceinline__ int k_place(int j) { return MODE == 1 ? (j == 0 ? 0 : 2 * j - 1) : 2 * j; }
+template <int MODE>
+__device__ __forceinline__ int v_place(int j, int n) { return MODE == 1 ? (j == n - 1 ? 2 * n - 1 : 2 * j + 2) : 2 * j + 1; }
+
+template <int D, int MODE>
+__global__ void __launch_bounds__(384, 1)
+    many_kernel(const __grid_constant__ ManyMaps maps, const __grid_constant__ CacheAttnArgs a, Plan plan, Parts parts)
+{
+    using C = ManyCfg<D, MODE>;
+    constexpr int ROWS = MODE * 128, NS = C::STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sQ = align1024(smem_raw);
+    uint8_t *sKV = sQ + MODE * C::Q_BYTES;
+    __shared__ uint64_t bar_q, bar_qe, bar_full[NS], bar_empty[NS], bar_s[2], bar_p[2], bar_o[2], bar_go, bar_fix, bar_done;
+    __shared__ uint32_t tmem_sh;
+    __shared__ int abort_sh, odd_sh[4];
+    __shared__ float2 ml_sh[MODE == 1 ? 2 : 1][MODE == 1 ? 128 : 1];
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const Guard g{&abort_sh, a.status, kWaitLimitNs};
+    if (threadIdx.x == 0) {
+        abort_sh = 0;
+        ptx::mbar_init(&bar_q, 1);
+        ptx::mbar_init(&bar_qe, 1);
+        for (int s = 0; s < NS; ++s) {
+            ptx::mbar_init(&bar_full[s], 1);
+            ptx::mbar_init(&bar_empty[s], 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            ptx::mbar_init(&bar_s[t], 1);
+            ptx::mbar_init(&bar_p[t], 128);
+            ptx::mbar_init(&bar_o[t], 1);
+        }
+        ptx::mbar_init(&bar_go, 1);
+        ptx::mbar_init(&bar_fix, 64);
+        ptx::mbar_init(&bar_done, 1);
+        ptx::fence_mbar_init();
+    }
+    if (warp == C::MMA_WARP) {
+        ptx::tmem_alloc(&tmem_sh, 512);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = tmem_sh;
+    ptx::grid_dep_launch();      // (not before tensor memory is this kernel's)
+    ptx::grid_dep_wait();
+
+    Walk walk;
+    Segment seg;
+    const bool any = walk.begin(a, plan);
+    const int T = a.T, R = a.G * T;
+    if (!any) {
+        // nothing to do: the same for the whole CTA
+    } else if (warp == C::TMA_WARP) {
+        // ---------------------------------------------------------------- TMA producer
+        if (ptx::elect_one()) {
+            ptx::tma_prefetch_desc(&maps.q);
+            ptx::tma_prefetch_desc(&maps.k);
+            ptx::tma_prefetch_desc(&maps.v);
+            uint32_t seq = 0;
+            uint32_t segs = 0;       // whose Q was asked for
+            bool ok = true;          // nothing more is asked for once a wait has given up
+            for (uint32_t i = 0; ok && walk.next(a, plan, seg); ++i) {
+                if (i > 0 && !(ok = wait_bounded(&bar_qe, (i - 1) & 1, g))) break;
+                ptx::mbar_arrive_expect_tx(&bar_q, MODE * C::Q_BYTES);
+                for (int t = 0; t < MODE; ++t)
+                    for (int hf = 0; hf < D / 64; ++hf)
+                        ptx::tma_load_3d(sQ + t * C::Q_BYTES + hf * 128 * 128, &maps.q, &bar_q, hf * 64,
+                                         seg.tile * ROWS + t * 128, (int)seg.unit_row);
+                segs = i + 1;
+                const int n = seg.last - seg.first;
+                auto load = [&](const CUtensorMap *map, int j) {
+                    const uint32_t st = seq % NS;
+                    if (!ok || !(ok = wait_bounded(&bar_empty[st], ((seq / NS) & 1) ^ 1, g))) return;
+                    ptx::mbar_arrive_expect_tx(&bar_full[st], C::KV_BYTES);
+                    for (int hf = 0; hf < D / 64; ++hf)
+                        ptx::tma_load_3d(sKV + st * C::KV_BYTES + hf * kManyTile * 128, map, &bar_full[st], hf * 64,
+                                         (seg.first + j) * kManyTile, (int)seg.unit_row);
+                    ++seq;
+                };
+                load(&maps.k, 0);
+                for (int j = 0; j < n; ++j) {      // in the order of k_place() and v_place()
+                    if (MODE == 1 && j + 1 < n) load(&maps.k, j + 1);
+                    load(&maps.v, j);
+                    if (MODE == 2 && j + 1 < n) load(&maps.k, j + 1);
+                }
+            }
+            // do not leave with copies in flight (matters only after a timeout)
+            if (segs > 0) drain(&bar_q, (segs - 1) & 1);
+            for (uint32_t x = seq > (uint32_t)NS ? seq - NS : 0; x < seq; ++x) drain(&bar_full[x % NS], (x / NS) & 1);
+        }
+    } else if (warp == C::MMA_WARP) {
+        // ---------------------------------------------------------------- tensor core issuer
+        if (ptx::elect_one()) {
+            const uint32_t idS = ptx::idesc_bf16_f32(128, kManyTile, false, false);
+            const uint32_t idO = ptx::idesc_bf16_f32(128, D, false, true);
+            const uint32_t q_base = ptx::smem_u32(sQ), kv_base = ptx::smem_u32(sKV);
+            uint32_t base = 0, jobs[2] = {0, 0}, fixes = 0;
+            bool ok = true;          // no product is issued once a wait has given up
+            auto wait = [&](uint64_t *bar, uint32_t parity) {
+                ok = ok && wait_bounded(bar, parity, g);
+                ptx::tc_fence_after();
+                return ok;
+            };
+            for (uint32_t i_seg = 0; ok && walk.next(a, plan, seg); ++i_seg) {
+                const int n = seg.last - seg.first, J = MODE == 1 ? n : 2 * n;
+                // Every load is waited for here, in the order of the loads: a wait by parity must not skip a phase.
+                auto issue_s = [&](int i) {
+                    const int t = i & 1, j = MODE == 1 ? i : i >> 1;
+                    const uint32_t at = base + k_place<MODE>(j), st = at % NS;
+                    if ((MODE == 1 || t == 0) && !wait(&bar_full[st], (at / NS) & 1)) return;
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
+                        ptx::mma_ss(tmem + t * 128,
+                                    ptx::sdesc_sw128(q_base + (MODE == 2 ? t * C::Q_BYTES : 0) + off, 16, 1024),
+                                    ptx::sdesc_sw128(kv_base + st * C::KV_BYTES + off, 16, 1024), idS, kk > 0 ? 1u : 0u);
+                    }
+                    ptx::mma_commit(&bar_s[t]);
+                    if (MODE == 1 || t == 1) ptx::mma_commit(&bar_empty[st]);
+                    if (i == J - 1) ptx::mma_commit(&bar_qe);
+                };
+                if (!wait(&bar_q, i_seg & 1)) break;
+                for (int i = 0; i < 2 && i < J && ok; ++i) issue_s(i);
+                for (int i = 0; i < J && ok; ++i) {
+                    const int t = i & 1, j = MODE == 1 ? i : i >> 1;
+                    const uint32_t at = base + v_place<MODE>(j, n), st = at % NS;
+                    if (MODE == 1 || t == 0) {
+                        if (!wait(&bar_full[st], (at / NS) & 1)) break;
+                        if ((seg.first + j + 1) * kManyTile > seg.length) {
+                            ptx::mbar_arrive(&bar_go);
+                            if (!wait(&bar_fix, fixes++ & 1)) break;
+                        }
+                    }
+                    if (!wait(&bar_p[t], jobs[t]++ & 1)) break;
+#pragma unroll
+                    for (int kk = 0; kk < kManyTile / 16; ++kk)
+                        ptx::mma_ts(tmem + C::TM_O + t * D, tmem + t * 128 + kk * 8,
+                                    ptx::sdesc_sw128(kv_base + st * C::KV_BYTES + kk * 2048, kManyTile * 128, 1024), idO,
+                                    i >= 2 || kk > 0 ? 1u : 0u);
+                    if (MODE == 1 || t == 1) ptx::mma_commit(&bar_empty[st]);
+                    if (i + 2 < J) issue_s(i + 2);
+                    else ptx::mma_commit(&bar_o[t]);
+                }
+                if (J == 1 && ok) ptx::mma_commit(&bar_o[1]);
+                base += 2 * n;
+            }
+            // every product is done before shared and tensor memory are given back (matters after a timeout)
+            ptx::mma_commit(&bar_done);
+            drain(&bar_done, 0);
+        }
+    } else if (warp >= C::FIX_WARP) {
+        // ---------------------------------------------------------------- V's last rows
+        const int ft = (warp - C::FIX_WARP) * 32 + lane;
+        uint32_t base = 0, fixes = 0;
+        for (uint32_t i_seg = 0; walk.next(a, plan, seg); ++i_seg) {
+            const int n = seg.last - seg.first;
+            bool begun = false;
+            for (int j = max(0, seg.length / kManyTile - seg.first); j < n; ++j) {
+                const int k0 = (seg.first + j) * kManyTile;
+                const uint32_t at = base + v_place<MODE>(j, n), st = at % NS;
+                if (!begun) {
+                    if (ft == 0) odd_sh[i_seg & 3] = 0;
+                    ptx::named_bar(1, 64);
+                    begun = true;
+                }
+                wait_bounded(&bar_go, fixes++ & 1, g);     // the tile has landed (the issuer saw it)
+                const uint32_t v = ptx::smem_u32(sKV + st * C::KV_BYTES);
+                const int own = max(seg.length - k0, 0), behind = seg.length + T - k0;
+                bool odd = false;
+                for (int c = ft; c < C::KV_BYTES / 16; c += 64) {       // 8 chunks a row of each half
+                    const int row = (c >> 3) & 127;
+                    if (row < own) continue;
+                    if (row >= behind) {
+                        sts_u128(v + c * 16, make_uint4(0, 0, 0, 0));
+                    } else {
+                        uint4 w = lds_u128(v + c * 16);
+                        if (any_odd(w)) {
+                            odd = true;
+                            drop_odd(w);
+                            sts_u128(v + c * 16, w);
+                        }
+                    }
+                }
+                if (odd) odd_sh[i_seg & 3] = 1;
+                __threadfence_block();
+                ptx::fence_proxy_async_smem();
+                ptx::mbar_arrive(&bar_fix);
+            }
+            base += 2 * n;
+        }
+    } else {
+        // ---------------------------------------------------------------- softmax
+        const int t = warp >> 2, quarter = warp & 3, r_tile = quarter * 32 + lane;
+        const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+        const uint32_t tS = tmem + lane_off + t * 128, tO = tmem + lane_off + C::TM_O;
+        const float scale_log2 = a.scale * kLog2e;
+        uint32_t jobs = 0;
+        for (uint32_t i_seg = 0; walk.next(a, plan, seg); ++i_seg) {
+            const int n = seg.last - seg.first;
+            const int row = seg.tile * ROWS + (MODE == 2 ? t * 128 : 0) + r_tile;
+            const bool idle = row - lane >= R;          // a warp without rows
+            uint64_t word = 0;
+            if (row < R) {
+                word = word_of(a.tree, seg.b, T, row % T);
+                if (T < 64) word &= (1ull << T) - 1;
+            }
+            float m = -INFINITY, l = 0.f;
+            bool begun = false;
+            for (int j = MODE == 1 ? t : 0; j < n; j += MODE == 1 ? 2 : 1, ++jobs) {
+                wait_bounded(&bar_s[t], jobs & 1, g);
+                ptx::tc_fence_after();
+                if (!idle) {
+                    uint32_t r[128];
+                    ptx::tmem_ld32_at<0>(tS + 0, r);
+                    ptx::tmem_ld32_at<32>(tS + 32, r);
+                    ptx::tmem_ld32_at<64>(tS + 64, r);
+                    ptx::tmem_ld32_at<96>(tS + 96, r);
+                    ptx::tmem_ld_wait();
+                    reg_fence(r);
+                    const int u0 = (seg.first + j) * kManyTile - seg.length;    // the tile's first slot, from the first token's
+                    if (u0 + kManyTile > 0) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const int u = u0 + 32 * c;
+                            uint32_t bits;
+                            if (u >= 64) bits = 0;
+                            else if (u >= 0) bits = (uint32_t)(word >> u);
+                            else if (u > -32) bits = (uint32_t)(word << -u) | ((1u << -u) - 1);
+                            else bits = 0xffffffffu;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (!(bits >> i & 1)) r[32 * c + i] = __float_as_uint(-INFINITY);
+                        }
+                    }
+                    float mx[8];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) mx[u] = __uint_as_float(r[u]);
+#pragma unroll
+                    for (int i = 8; i < 128; i += 2)
+                        mx[(i >> 1) & 7] = ptx::max3(mx[(i >> 1) & 7], __uint_as_float(r[i]), __uint_as_float(r[i + 1]));
+                    const float smax = ptx::max3(ptx::max3(mx[0], mx[1], mx[2]), ptx::max3(mx[3], mx[4], mx[5]),
+                                                 fmaxf(mx[6], mx[7]));
+                    const float mt = smax * scale_log2;
+                    float m_new = m, alpha = 1.f;
+                    bool rescale = false;
+                    if (!begun) {
+                        m_new = mt;
+                    } else if (__any_sync(0xffffffffu, mt > m + kTau)) {
+                        m_new = fmaxf(m, mt);
+                        alpha = m_new == -INFINITY ? 1.f : ptx::ex2(m - m_new);
+                        rescale = true;
+                    }
+                    begun = true;
+                    const float neg_m = m_new == -INFINITY ? 0.f : -m_new;
+                    const uint64_t c2 = ptx::f2_pack(scale_log2, scale_log2), nm2 = ptx::f2_pack(neg_m, neg_m);
+                    uint64_t sum2[2] = {ptx::f2_pack(0.f, 0.f), ptx::f2_pack(0.f, 0.f)};
+#pragma unroll
+                    for (int ch = 0; ch < 4; ++ch) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            const uint64_t x = ptx::fma_f32x2(
+                                ptx::f2_pack(__uint_as_float(r[ch * 32 + i]), __uint_as_float(r[ch * 32 + i + 1])), c2, nm2);
+                            float t0, t1;
+                            ptx::f2_unpack(x, t0, t1);
+                            const float p0 = ptx::ex2(t0), p1 = ptx::ex2(t1);
+                            sum2[(i >> 1) & 1] = ptx::add_f32x2(sum2[(i >> 1) & 1], ptx::f2_pack(p0, p1));
+                            pk[i >> 1] = ptx::pack_bf16x2(p0, p1);
+                        }
+                        ptx::tmem_st16(tS + ch * 16, pk);
+                    }
+                    float sum[4];
+                    ptx::f2_unpack(sum2[0], sum[0], sum[1]);
+                    ptx::f2_unpack(sum2[1], sum[2], sum[3]);
+                    l = l * alpha + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+                    m = m_new;
+                    if (rescale) {
+#pragma unroll
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t ov[32];
+                            ptx::tmem_ld32(tO + t * D + c, ov);
+                            ptx::tmem_ld_wait();
+                            reg_fence(ov);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+                            ptx::tmem_st32(tO + t * D + c, ov);
+                        }
+                    }
+                    ptx::tmem_st_wait();
+                }
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(&bar_p[t]);
+            }
+
+            // The rows' results: both streams' (MODE 1, each warp half of the columns) or their own.
+            float f[2] = {1.f, 0.f};
+            if (MODE == 1) {
+                ml_sh[t][r_tile] = make_float2(m, l);
+                ptx::named_bar(2, 256);
+                const float2 other = ml_sh[t ^ 1][r_tile];
+                const float top = fmaxf(m, other.x), ref = top == -INFINITY ? 0.f : top;
+                const float mine = ptx::ex2(m - ref), its = ptx::ex2(other.x - ref);
+                f[0] = t == 0 ? mine : its;
+                f[1] = t == 0 ? its : mine;
+                l = t == 0 ? l * mine + other.y * its : other.y * its + l * mine;
+                m = top;
+            }
+            wait_bounded(&bar_o[t], i_seg & 1, g);
+            if (MODE == 1) wait_bounded(&bar_o[t ^ 1], i_seg & 1, g);
+            ptx::tc_fence_after();
+            const bool whole = seg.first == 0 && seg.last == seg.nb;
+            const bool tail = seg.last * kManyTile > seg.length;
+            const bool odd = tail && odd_sh[i_seg & 3];
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const long long at = seg.unit_row * R + row;
+            const long long slot = (2 * (long long)blockIdx.x + (seg.first == 0 ? 1 : 0)) * ROWS + row % ROWS;
+            constexpr int COLS = MODE == 1 ? D / 2 : D;
+            if (!idle) {
+#pragma unroll
+                for (int c0 = 0; c0 < COLS; c0 += 32) {
+                    const int c = MODE == 1 ? t * COLS + c0 : c0;
+                    uint32_t ov[32];
+                    ptx::tmem_ld32(tO + (MODE == 1 ? 0 : t * D) + c, ov);
+                    ptx::tmem_ld_wait();
+                    reg_fence(ov);
+                    if (MODE == 1) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(f[0] * __uint_as_float(ov[i]));
+                        if (n > 1) {             // (with one tile the second stream has no O)
+                            uint32_t o2[32];
+                            ptx::tmem_ld32(tO + D + c, o2);
+                            ptx::tmem_ld_wait();
+                            reg_fence(o2);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                ov[i] = __float_as_uint(__uint_as_float(ov[i]) + f[1] * __uint_as_float(o2[i]));
+                        }
+                    }
+                    if (odd && row < R) {
+                        for (int u = 0; u < T; ++u) {
+                            const int key = seg.length + u;
+                            if (!(word >> u & 1) || key < seg.first * kManyTile || key >= seg.last * kManyTile) continue;
+                            const uint4 *from = static_cast<const uint4 *>(a.v) + (seg.unit_row * a.C + key) * (D / 8) + c / 8;
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const uint4 w = from[x];
+                                const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                                for (int y = 0; y < 8; ++y) {
+                                    const float v = y & 1 ? hi(ws[y / 2]) : lo(ws[y / 2]);
+                                    if (odd_value(v)) ov[8 * x + y] = __float_as_uint(__uint_as_float(ov[8 * x + y]) + v);
+                                }
+                            }
+                        }
+                    }
+                    if (row < R) {
+                        if (whole) {
+                            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + at * D + c);
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int y = 0; y < 4; ++y)
+                                    w[y] = ptx::pack_bf16x2(__uint_as_float(ov[8 * x + 2 * y]) * inv,
+                                                            __uint_as_float(ov[8 * x + 2 * y + 1]) * inv);
+                                dst[x] = make_uint4(w[0], w[1], w[2], w[3]);
+                            }
+                        } else {
+                            uint4 *dst = reinterpret_cast<uint4 *>(parts.o + slot * D + c);
+#pragma unroll
+                            for (int x = 0; x < 8; ++x)
+                                dst[x] = make_uint4(ov[4 * x], ov[4 * x + 1], ov[4 * x + 2], ov[4 * x + 3]);
+                        }
+                    }
+                }
+                if (row < R && (MODE == 2 || t == 0)) {
+                    if (whole) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * (1.f / kLog2e);
+                    else parts.ml[slot] = make_float2(m, l);
+                }
+            }
+            ptx::tc_fence_before();
+            if (MODE == 1) ptx::named_bar(2, 256);     // both streams' O has been read
+        }
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == C::MMA_WARP) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 512);
+    }
+}
+
 // Adds up the parts of one row, if its unit was split.  A block a row, a warp every fourth part.
 constexpr int kJoinWarps = 4;
 
@@ -446,7 +928,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(CacheAttnArgs a, 
     const int r = (int)(at % R), b = (int)(head / plan.H), h = (int)(head % plan.H);
     const long long total = blocks_before(a.lengths, a.B, plan);
     const long long per = (total + ctas - 1) / ctas;
-    const int nb = blocks_of(length_of(a.lengths, b, a.T, a.C), a.T);
+    const int nb = blocks_of(length_of(a.lengths, b, a.T, a.C), plan);
     const long long u0 =
         blocks_before(a.lengths, b, plan) + ((long long)h * plan.tiles + r / rows) * nb;
     const long long c0 = u0 / per, c1 = (u0 + nb - 1) / per;
@@ -565,24 +1047,59 @@ __global__ void __launch_bounds__(kFewThreads) weights_kernel(CacheAttnArgs a, i
     }
 }
 
-int rows_a_unit(int R) { return R <= 8 ? 8 : 16; }
 constexpr int kPlanSms = 152;    // the split is a function of the sizes and lengths alone
-int few_ctas(int rows) { return kPlanSms * (rows == 8 ? 3 : 2); }
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// Rows a unit, and CTAs that share the work.
+struct Shape {
+    int rows, ctas;
+    bool many() const { return rows > 16; }
+};
+
+Shape shape_of(int R)
+{
+    if (R <= 8) return {8, 3 * kPlanSms};
+    if (R <= 16) return {16, 2 * kPlanSms};
+    return {R <= 128 ? 128 : 256, kPlanSms};
+}
+
+template <int D, int MODE>
+cudaError_t launch_many(const CacheAttnArgs &a, const Plan &plan, const Parts &parts, int ctas, cudaStream_t stream)
+{
+    using C = ManyCfg<D, MODE>;
+    ManyMaps maps;
+    const long long bh = (long long)a.B * a.H;
+    if (make_map_3d(&maps.q, a.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, D, a.G * a.T, bh, 64, 128) != CUDA_SUCCESS ||
+        make_map_3d(&maps.k, a.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, D, a.C, bh, 64, kManyTile) != CUDA_SUCCESS ||
+        make_map_3d(&maps.v, a.v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, D, a.C, bh, 64, kManyTile) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    static std::atomic<bool> set[64];
+    const cudaError_t e = raise_smem(reinterpret_cast<const void *>(many_kernel<D, MODE>), C::SMEM, set);
+    if (e != cudaSuccess) return e;
+    return launch_overlapped(many_kernel<D, MODE>, dim3((unsigned)ctas), dim3(C::THREADS), C::SMEM, 1, stream, maps, a,
+                             plan, parts);
+}
 
 template <int D>
 cudaError_t launch(const CacheAttnArgs &a, cudaStream_t stream)
 {
-    const int R = a.G * a.T, rows = rows_a_unit(R), ctas = few_ctas(rows);
-    const Plan plan = {a.H, (R + rows - 1) / rows, a.T, a.C};
+    const int R = a.G * a.T;
+    const Shape sh = shape_of(R);
+    const Plan plan = {a.H, (R + sh.rows - 1) / sh.rows, a.T, a.C, sh.many() ? kManyTile : kBlock};
     Parts parts;
     parts.o = static_cast<float *>(a.workspace);
-    parts.ml = reinterpret_cast<float2 *>(static_cast<char *>(a.workspace) + up256((size_t)2 * ctas * rows * D * 4));
-    cudaError_t e = rows == 8 ? launch_overlapped(few_kernel<D, 1>, dim3(ctas), dim3(kFewThreads), 0, 1, stream, a, plan, parts)
-                              : launch_overlapped(few_kernel<D, 2>, dim3(ctas), dim3(kFewThreads), 0, 1, stream, a, plan, parts);
+    parts.ml = reinterpret_cast<float2 *>(static_cast<char *>(a.workspace) + up256((size_t)2 * sh.ctas * sh.rows * D * 4));
+    cudaError_t e;
+    if (sh.rows == 8)
+        e = launch_overlapped(few_kernel<D, 1>, dim3(sh.ctas), dim3(kFewThreads), 0, 1, stream, a, plan, parts);
+    else if (sh.rows == 16)
+        e = launch_overlapped(few_kernel<D, 2>, dim3(sh.ctas), dim3(kFewThreads), 0, 1, stream, a, plan, parts);
+    else
+        e = sh.rows == 128 ? launch_many<D, 1>(a, plan, parts, sh.ctas, stream)
+                           : launch_many<D, 2>(a, plan, parts, sh.ctas, stream);
     if (e != cudaSuccess) return e;
     e = launch_overlapped(join_kernel<D>, dim3((unsigned)((long long)a.B * a.H * R)), dim3(32 * kJoinWarps), 0, 1, stream,
-                          a, plan, rows, ctas, parts);
+                          a, plan, sh.rows, sh.ctas, parts);
     if (e != cudaSuccess || !a.weights) return e;
     const int blocks = (a.C + kBlock - 1) / kBlock;
     return launch_overlapped(weights_kernel<D>, dim3((unsigned)((long long)a.B * a.H * blocks)), dim3(kFewThreads), 0, 1,
@@ -593,8 +1110,8 @@ cudaError_t launch(const CacheAttnArgs &a, cudaStream_t stream)
 
 size_t cache_attn_workspace(int G, int T, int d)
 {
-    const int rows = rows_a_unit(G * T);
-    const size_t slots = (size_t)2 * few_ctas(rows) * rows;
+    const Shape sh = shape_of(G * T);
+    const size_t slots = (size_t)2 * sh.ctas * sh.rows;
     return up256(slots * d * 4) + up256(slots * 8);
 }
 

@@ -76,6 +76,35 @@ def attention(q, k, v, lengths, tree=None, weights=None, counted=None, scale=Non
     return (o, to), (lse, tl), (w, tw)
 
 
+def attention_many(q, k, v, lengths, tree=None):
+    """(o, tolerance), (lse, tolerance) as attention() has them, for many finite rows at once, on q's device."""
+    B, Hq, T, d = q.shape
+    H, C = k.shape[1:3]
+    G = Hq // H
+    o, lse = torch.zeros(B, Hq, T, d, dtype=torch.float64), torch.zeros(B, Hq, T, dtype=torch.float64)
+    to, tl = torch.zeros_like(o), torch.zeros_like(lse)
+    u = torch.arange(T, device=q.device)
+    for b in range(B):
+        n = int(lengths[b])
+        own = u.view(1, T) <= u.view(T, 1) if tree is None else (tree[b].view(T, 1) >> u & 1).bool()
+        sees = torch.cat((torch.ones(T, n, dtype=torch.bool, device=q.device), own), 1)
+        m = sees.sum(1).cpu()
+        for h in range(H):
+            rows = q[b, h * G:(h + 1) * G].double()
+            kk, vv = k[b, h, :n + T].double(), v[b, h, :n + T].double()
+            s = (rows @ kk.T / math.sqrt(d)).masked_fill(~sees, -math.inf)
+            a = (rows.abs() @ kk.abs().T).masked_fill(~sees, 0.0).amax(-1)
+            ds = (d + 8) * STEP / math.sqrt(d) * a + 4 * STEP * s.masked_fill(~sees, 0.0).abs().amax(-1) + 2.0 ** -21
+            x = torch.logsumexp(s, -1)
+            p = torch.exp(s - x.unsqueeze(-1))
+            e = (2 * ds + U8 + (m + 8).to(q.device) * STEP).unsqueeze(-1) * (p @ vv.abs())
+            y = p @ vv
+            at = slice(h * G, (h + 1) * G)
+            o[b, at], lse[b, at] = y.cpu(), x.cpu()
+            to[b, at], tl[b, at] = (e + U8 * (y.abs() + e)).cpu(), (ds + 4 * STEP * x.abs()).cpu() + (m + 8) * STEP
+    return (o, to), (lse, tl)
+
+
 def evict(k, v, weights, positions, lengths, keep, recent):
     """k, v, weights, positions, lengths after the eviction (copies, on the host)."""
     k, v, w, pos = (t.cpu().clone() for t in (k, v, weights, positions))

@@ -160,6 +160,27 @@ def test_weights(case, some):
     assert torch.equal(o, plain[0]) and torch.equal(lse, plain[1])
 
 
+@pytest.mark.parametrize("B,H,G,T,d,C,ragged", [
+    (8, 4, 2, 10, 128, 1500, 1400), (8, 4, 2, 10, 64, 1500, 1400), (6, 4, 4, 50, 128, 1700, 900), (6, 4, 4, 64, 64, 1700, 1600),
+    (3, 5, 8, 60, 128, 2900, 100), (40, 8, 1, 33, 64, 300, 260), (2, 3, 2, 64, 128, 20000, 5000), (33, 7, 4, 64, 128, 270, 200),
+    (9, 16, 4, 1, 128, 5000, 4900), (9, 16, 3, 4, 64, 5000, 4900), (300, 1, 1, 20, 64, 200, 130), (1, 1, 4, 64, 128, 30000, 0)])
+@pytest.mark.parametrize("masked", [False, True])
+def test_attention_over_many_blocks(B, H, G, T, d, C, ragged, masked):
+    """CTAs with runs of blocks, and runs over several heads and sequences."""
+    g = _gen("blocks", B, H, G, T, d, masked)
+    lens = [C - T - (b * 977) % (ragged + 1) for b in range(B)]
+    q = _randn(g, B, H * G, T, d, std=2.0)
+    k, v = _cache(g, B, H, C, d, lens, T)
+    tree = sa.tree_words(_parents(g, B, T)) if masked else None
+    o, lse = sa.cache_attention(q, k, v, _i32(*lens), tree)
+    assert sa.attn_get_device_status() == 0
+    want_o, want_l = ref.attention_many(q, k, v, lens, tree)
+    ref.check("o", o, *want_o)
+    ref.check("lse", lse, *want_l)
+    again = sa.cache_attention(q, k, v, _i32(*lens), tree)
+    assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+
+
 @pytest.mark.parametrize("T,G", [(3, 1), (20, 2), (64, 4)])
 def test_rows_that_see_nothing_or_odd_sets(T, G):
     """Masks that are no trees: empty rows, a row that sees only others, all bits."""
