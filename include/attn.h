@@ -442,7 +442,7 @@ size_t attn_cache_attention_workspace_size(int B, int H, int G, int T, int C, in
  * A row that sees nothing gets o = 0 and lse = -infinity.  What a row does not see does not reach it, NaN and
  * infinities among it; slots behind the T tokens are not read.  A length outside 0 ... C - T counts as the nearest
  * inside.  Scores and sums are fp32.  Results are bitwise reproducible.
- *   workspace : caller-owned, overwritten.   T <= C.   scale finite and > 0.
+ *   workspace : caller-owned, overwritten.   T <= C.   B H G T below 2^27.   scale finite and > 0.
  */
 attn_status attn_cache_attention(const void *q, const void *cache_k, const void *cache_v, const int *lengths,
                                  const uint64_t *tree, const uint64_t *counted, const float *weights,

@@ -1186,7 +1186,7 @@ attn_status check_cache_attention(int B, int H, int G, int T, int C, int d_k)
     const attn_status st = check_cache(B, H, C, d_k);
     if (st != ATTN_OK) return st;
     if (G < 1 || G > kMaxHeads || T < 1 || T > kMaxTokens || T > C || (long long)H * G > kMaxHeads ||
-        (double)B * H * G * T >= 2147483647.0)
+        (double)B * H * G * T >= (double)(1 << 27))
         return ATTN_ERR_INVALID_ARG;
     return ATTN_OK;
 }

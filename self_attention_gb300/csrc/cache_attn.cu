@@ -95,41 +95,117 @@ __device__ __forceinline__ int length_of(const int *lengths, int b, int T, int C
 
 __device__ __forceinline__ int blocks_of(int length, const Plan &p) { return (length + p.T + p.block - 1) / p.block; }
 
-// Blocks ahead of sequence `upto` (upto = B: of all of them); by a whole warp, the same in every lane.
-__device__ __forceinline__ long long blocks_before(const int *lengths, int upto, const Plan &p)
+// Blocks of all sequences, and of those ahead of sequence `upto`; by a whole warp, the same in every lane.
+__device__ __forceinline__ long long count_blocks(const int *lengths, int B, int upto, const Plan &p, long long &before)
 {
-    long long sum = 0;
-    for (int b = threadIdx.x & 31; b < upto; b += 32) sum += blocks_of(length_of(lengths, b, p.T, p.C), p);
+    long long all = 0, ahead = 0;
+    for (int b = threadIdx.x & 31; b < B; b += 32) {
+        const int n = blocks_of(length_of(lengths, b, p.T, p.C), p);
+        all += n;
+        ahead += b < upto ? n : 0;
+    }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    return sum * p.H * p.tiles;
+    for (int o = 16; o; o >>= 1) {
+        all += __shfl_xor_sync(0xffffffffu, all, o);
+        ahead += __shfl_xor_sync(0xffffffffu, ahead, o);
+    }
+    before = ahead * p.H * p.tiles;
+    return all * p.H * p.tiles;
 }
 
-// The sequence that block `x` of all belongs to, and the blocks ahead of it; by a whole warp.
-__device__ __forceinline__ int sequence_of(const int *lengths, int B, const Plan &p, long long x, long long &before)
+// A run of blocks of one unit, that one CTA works on.
+struct Segment {
+    long long head;         // b H + h
+    int b, tile, first, last, nb, length;
+    bool there;
+    __device__ __forceinline__ bool whole() const { return first == 0 && last == nb; }
+};
+
+// a / b, by a 32-bit division where both fit.
+__device__ __forceinline__ long long divide(long long a, int b)
 {
-    const uint32_t lane = threadIdx.x & 31;
-    long long sum = 0;
-    for (int b0 = 0; b0 < B; b0 += 32) {
-        const int b = b0 + (int)lane;
-        const long long mine =
-            b < B ? (long long)blocks_of(length_of(lengths, b, p.T, p.C), p) * p.H * p.tiles : 0;
-        long long inc = mine;
+    return (a >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// Walks over a CTA's share of the blocks, the same number for each.
+struct Walk {
+    long long x, end, before;
+    int b, length, nb;
+    // By a whole warp.
+    __device__ __forceinline__ bool begin(const int *lengths, int B, const Plan &p)
+    {
+        const uint32_t lane = threadIdx.x & 31;
+        const long long per_block = (long long)p.H * p.tiles;
+        long long all = 0;
+        const int mine = (int)lane < B ? length_of(lengths, (int)lane, p.T, p.C) : 0;
+        const long long n0 = (int)lane < B ? blocks_of(mine, p) : 0;
+        long long inc = n0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long t = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= (uint32_t)o) inc += t;
         }
-        const uint32_t hit = __ballot_sync(0xffffffffu, b < B && x < sum + inc);
-        if (hit) {
-            const int l = __ffs(hit) - 1;
-            before = sum + __shfl_sync(0xffffffffu, inc - mine, l);
-            return b0 + l;
+        all = __shfl_sync(0xffffffffu, inc, 31);
+        if (B > 32) {
+            long long ignored;
+            all = count_blocks(lengths, B, 0, p, ignored);
+        } else {
+            all *= per_block;
         }
-        sum += __shfl_sync(0xffffffffu, inc, 31);
+        const long long per = divide(all + gridDim.x - 1, (int)gridDim.x);
+        x = per * blockIdx.x;
+        end = min(x + per, all);
+        if (x >= end) return false;
+        long long sum = 0;
+        for (int b0 = 0;; b0 += 32) {          // ends: x lies before `all`
+            int len = mine;
+            long long n = n0;
+            if (b0 > 0) {
+                len = b0 + (int)lane < B ? length_of(lengths, b0 + (int)lane, p.T, p.C) : 0;
+                n = b0 + (int)lane < B ? blocks_of(len, p) : 0;
+                inc = n;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long t = __shfl_up_sync(0xffffffffu, inc, o);
+                    if (lane >= (uint32_t)o) inc += t;
+                }
+            }
+            const uint32_t hit = __ballot_sync(0xffffffffu, x < (sum + inc) * per_block);
+            if (hit) {
+                const int l = __ffs(hit) - 1;
+                before = (sum + __shfl_sync(0xffffffffu, inc - n, l)) * per_block;
+                length = __shfl_sync(0xffffffffu, len, l);
+                nb = blocks_of(length, p);
+                b = b0 + l;
+                return true;
+            }
+            sum += __shfl_sync(0xffffffffu, inc, 31);
+        }
     }
-    return B;
-}
+    // By any thread.
+    __device__ __forceinline__ bool next(const int *lengths, const Plan &p, Segment &s)
+    {
+        s.there = x < end;
+        if (!s.there) return false;
+        while (x >= before + (long long)nb * p.H * p.tiles) {
+            before += (long long)nb * p.H * p.tiles;
+            ++b;
+            length = length_of(lengths, b, p.T, p.C);
+            nb = blocks_of(length, p);
+        }
+        const long long u = divide(x - before, nb);          // unit of the sequence
+        s.first = (int)(x - before - u * nb);
+        s.last = (int)min((long long)nb, s.first + (end - x));
+        const long long h = divide(u, p.tiles);
+        s.tile = (int)(u - h * p.tiles);
+        s.b = b;
+        s.nb = nb;
+        s.length = length;
+        s.head = (long long)b * p.H + h;
+        x += s.last - s.first;
+        return true;
+    }
+};
 
 // Which tokens token t sees, as bits.
 __device__ __forceinline__ uint64_t word_of(const uint64_t *tree, int b, int T, int t)
@@ -139,7 +215,7 @@ __device__ __forceinline__ uint64_t word_of(const uint64_t *tree, int b, int T, 
 
 // Partial results: slot 2 c for the part that CTA c begins inside a unit, 2 c + 1 for the one it begins a unit with.
 struct Parts {
-    float *o;          // [2 grid][rows][d]
+    float *o;          // [2 grid][rows][d]; many_kernel's [2 grid][d / 4][rows][4], so that its threads, one a row, write runs
     float2 *ml;        // [2 grid][rows]: maximum (of scores times log2 e) and sum
 };
 
@@ -162,42 +238,55 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) few_kernel(Cache
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
     const int T = a.T, R = a.G * T;
 
-    const long long total = blocks_before(a.lengths, a.B, plan);
-    const long long per = (total + gridDim.x - 1) / gridDim.x;
-    long long x = per * blockIdx.x;
-    const long long end = min(x + per, total);
-    if (x >= end) return;
-    long long before;
-    int b = sequence_of(a.lengths, a.B, plan, x, before);
-    int length = length_of(a.lengths, b, T, a.C), nb = blocks_of(length, plan);
+    Walk walk;
+    if (!walk.begin(a.lengths, a.B, plan)) return;
     const float to_log2 = a.scale * kLog2e;
+    Segment seg;
+    walk.next(a.lengths, plan, seg);
 
-    while (x < end) {
-        while (x >= before + (long long)nb * plan.H * plan.tiles) {
-            before += (long long)nb * plan.H * plan.tiles;
-            ++b;
-            length = length_of(a.lengths, b, T, a.C);
-            nb = blocks_of(length, plan);
-        }
-        const long long u = (x - before) / nb;               // unit of the sequence
-        const int first = (int)(x - before - u * nb);
-        const int last = (int)min((long long)nb, first + (end - x));
-        const int h = (int)(u / plan.tiles), tile = (int)(u % plan.tiles);
-        const int valid = length + T;
-        const long long head = (long long)b * plan.H + h;
-        const uint4 *kp = static_cast<const uint4 *>(a.k) + head * a.C * (D / 8);
-        const uint4 *vp = static_cast<const uint4 *>(a.v) + head * a.C * (D / 8);
-        const int r0 = tile * R8;
-
-        // Q's rows as the 8-column operand
-        uint4 qf[NT][KC];
+    // Q's rows as the 8-column operand
+    uint4 qf[NT][KC];
+    auto load_q = [&](const Segment &s) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            const int r = r0 + 8 * t + g;
-            const uint4 *qp = static_cast<const uint4 *>(a.q) + (head * R + r) * (D / 8);
+            const int r = s.tile * R8 + 8 * t + g;
+            const uint4 *qp = static_cast<const uint4 *>(a.q) + (s.head * R + r) * (D / 8);
 #pragma unroll
             for (int c = 0; c < KC; ++c) qf[t][c] = r < R ? qp[4 * c + q] : make_uint4(0, 0, 0, 0);
         }
+    };
+    uint4 kr[2][KC], vr[4][VC];
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    // 16 slots from `key` on; those behind the last one read as zeros, whatever lies there
+    auto load_k = [&](const Segment &s, int key) {
+        const uint4 *kp = static_cast<const uint4 *>(a.k) + (s.head * a.C + key + g) * (D / 8) + q;
+        const int left = s.length + T - key - g;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int c = 0; c < KC; ++c) kr[i][c] = 8 * i < left ? stream16(kp + i * D + 4 * c) : zero;
+    };
+    auto load_v = [&](const Segment &s, int key) {
+        const uint4 *vp = static_cast<const uint4 *>(a.v) + (s.head * a.C + key + 2 * q) * (D / 8) + g;
+        const int left = s.length + T - key - 2 * q;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < VC; ++c) {
+                const int j = (i & 1) + 8 * (i >> 1);
+                vr[i][c] = j < left ? stream16(vp + j * (D / 8) + 8 * c) : zero;
+            }
+    };
+    load_k(seg, seg.first * kBlock + 16 * warp);
+    load_q(seg);
+    load_v(seg, seg.first * kBlock + 16 * warp);
+
+    while (seg.there) {
+        const int length = seg.length, first = seg.first, last = seg.last, nb = seg.nb, b = seg.b;
+        const long long head = seg.head;
+        const int r0 = seg.tile * R8;
+        Segment nxt;
+        walk.next(a.lengths, plan, nxt);
 
         float acc[NT][MT][4];
         float m[NT][2], l[NT][2];
@@ -209,31 +298,10 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) few_kernel(Cache
             for (int i = 0; i < MT; ++i) acc[t][i][0] = acc[t][i][1] = acc[t][i][2] = acc[t][i][3] = 0.f;
         }
 
-        uint4 kr[2][KC], vr[4][VC];
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-        auto load_k = [&](int key) {     // slots behind the last one read as zeros, whatever lies there
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int c = 0; c < KC; ++c) {
-                    const int j = key + g + 8 * i;
-                    kr[i][c] = j < valid ? stream16(kp + (long long)j * (D / 8) + 4 * c + q) : zero;
-                }
-        };
-        auto load_v = [&](int key) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int c = 0; c < VC; ++c) {
-                    const int j = key + 2 * q + (i & 1) + 8 * (i >> 1);
-                    vr[i][c] = j < valid ? stream16(vp + (long long)j * (D / 8) + 8 * c + g) : zero;
-                }
-        };
-        const int key_end = min(last * kBlock, valid);
         int key = first * kBlock + 16 * warp;
-        load_k(key);
-        load_v(key);
-        for (; key < key_end; key += kBlock) {
+        // A warp's steps; its share of the last block may be empty, and then the loads ahead are the next segment's.
+        for (; key < last * kBlock; key += kBlock) {
+            const bool more = key + kBlock < last * kBlock;
             float s[NT][4];
 #pragma unroll
             for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
@@ -247,7 +315,12 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) few_kernel(Cache
                     mma16816(s[t], a1, qf[t][c].z, qf[t][c].w);
                 }
             }
-            load_k(key + kBlock < key_end ? key + kBlock : valid);
+            if (more) {
+                load_k(seg, key + kBlock);
+            } else if (nxt.there) {
+                load_k(nxt, nxt.first * kBlock + 16 * warp);
+                load_q(nxt);
+            }
 
             const bool tail = key + 16 > length;
 #pragma unroll
@@ -367,7 +440,8 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) few_kernel(Cache
                     mma16816(acc[t][j], af, pl[t][0], pl[t][1]);
                 }
             }
-            load_v(key + kBlock < key_end ? key + kBlock : valid);
+            if (more) load_v(seg, key + kBlock);
+            else if (nxt.there) load_v(nxt, nxt.first * kBlock + 16 * warp);
         }
 
         // Join the warps.
@@ -426,7 +500,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) few_kernel(Cache
             }
         }
         __syncthreads();
-        x += last - first;
+        seg = nxt;
     }
 }
 
@@ -458,51 +532,6 @@ struct ManyCfg {
 
 struct ManyMaps {
     CUtensorMap q, k, v;      // [B H][G T][d] in boxes of 128 rows, [B H][C][d] in tiles; 64 columns each
-};
-
-// The run of blocks of one unit that a CTA works on next.
-struct Segment {
-    long long unit_row;       // (b H + h): which cached head
-    int b, h, tile, first, last, nb, length;
-};
-
-// Walks over a CTA's share; begun by a whole warp, stepped by any thread.
-struct Walk {
-    long long x, end, before;
-    int b, length, nb;
-    __device__ __forceinline__ bool begin(const CacheAttnArgs &a, const Plan &plan)
-    {
-        const long long total = blocks_before(a.lengths, a.B, plan);
-        const long long per = (total + gridDim.x - 1) / gridDim.x;
-        x = per * blockIdx.x;
-        end = min(x + per, total);
-        if (x >= end) return false;
-        b = sequence_of(a.lengths, a.B, plan, x, before);
-        length = length_of(a.lengths, b, plan.T, plan.C);
-        nb = blocks_of(length, plan);
-        return true;
-    }
-    __device__ __forceinline__ bool next(const CacheAttnArgs &a, const Plan &plan, Segment &s)
-    {
-        if (x >= end) return false;
-        while (x >= before + (long long)nb * plan.H * plan.tiles) {
-            before += (long long)nb * plan.H * plan.tiles;
-            ++b;
-            length = length_of(a.lengths, b, plan.T, plan.C);
-            nb = blocks_of(length, plan);
-        }
-        const long long u = (x - before) / nb;
-        s.first = (int)(x - before - u * nb);
-        s.last = (int)min((long long)nb, s.first + (end - x));
-        s.h = (int)(u / plan.tiles);
-        s.tile = (int)(u % plan.tiles);
-        s.b = b;
-        s.nb = nb;
-        s.length = length;
-        s.unit_row = (long long)b * plan.H + s.h;
-        x += s.last - s.first;
-        return true;
-    }
 };
 
 // Waits for what is already on its way, for a second at most, whether or not the CTA has given up.
@@ -566,7 +595,7 @@ __global__ void __launch_bounds__(384, 1)
 
     Walk walk;
     Segment seg;
-    const bool any = walk.begin(a, plan);
+    const bool any = walk.begin(a.lengths, a.B, plan);
     const int T = a.T, R = a.G * T;
     if (!any) {
         // nothing to do: the same for the whole CTA
@@ -579,13 +608,13 @@ __global__ void __launch_bounds__(384, 1)
             uint32_t seq = 0;
             uint32_t segs = 0;       // whose Q was asked for
             bool ok = true;          // nothing more is asked for once a wait has given up
-            for (uint32_t i = 0; ok && walk.next(a, plan, seg); ++i) {
+            for (uint32_t i = 0; ok && walk.next(a.lengths, plan, seg); ++i) {
                 if (i > 0 && !(ok = wait_bounded(&bar_qe, (i - 1) & 1, g))) break;
                 ptx::mbar_arrive_expect_tx(&bar_q, MODE * C::Q_BYTES);
                 for (int t = 0; t < MODE; ++t)
                     for (int hf = 0; hf < D / 64; ++hf)
                         ptx::tma_load_3d(sQ + t * C::Q_BYTES + hf * 128 * 128, &maps.q, &bar_q, hf * 64,
-                                         seg.tile * ROWS + t * 128, (int)seg.unit_row);
+                                         seg.tile * ROWS + t * 128, (int)seg.head);
                 segs = i + 1;
                 const int n = seg.last - seg.first;
                 auto load = [&](const CUtensorMap *map, int j) {
@@ -594,7 +623,7 @@ __global__ void __launch_bounds__(384, 1)
                     ptx::mbar_arrive_expect_tx(&bar_full[st], C::KV_BYTES);
                     for (int hf = 0; hf < D / 64; ++hf)
                         ptx::tma_load_3d(sKV + st * C::KV_BYTES + hf * kManyTile * 128, map, &bar_full[st], hf * 64,
-                                         (seg.first + j) * kManyTile, (int)seg.unit_row);
+                                         (seg.first + j) * kManyTile, (int)seg.head);
                     ++seq;
                 };
                 load(&maps.k, 0);
@@ -621,7 +650,7 @@ __global__ void __launch_bounds__(384, 1)
                 ptx::tc_fence_after();
                 return ok;
             };
-            for (uint32_t i_seg = 0; ok && walk.next(a, plan, seg); ++i_seg) {
+            for (uint32_t i_seg = 0; ok && walk.next(a.lengths, plan, seg); ++i_seg) {
                 const int n = seg.last - seg.first, J = MODE == 1 ? n : 2 * n;
                 // Every load is waited for here, in the order of the loads: a wait by parity must not skip a phase.
                 auto issue_s = [&](int i) {
@@ -672,7 +701,7 @@ __global__ void __launch_bounds__(384, 1)
         // ---------------------------------------------------------------- V's last rows
         const int ft = (warp - C::FIX_WARP) * 32 + lane;
         uint32_t base = 0, fixes = 0;
-        for (uint32_t i_seg = 0; walk.next(a, plan, seg); ++i_seg) {
+        for (uint32_t i_seg = 0; walk.next(a.lengths, plan, seg); ++i_seg) {
             const int n = seg.last - seg.first;
             bool begun = false;
             for (int j = max(0, seg.length / kManyTile - seg.first); j < n; ++j) {
@@ -685,21 +714,20 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 wait_bounded(&bar_go, fixes++ & 1, g);     // the tile has landed (the issuer saw it)
                 const uint32_t v = ptx::smem_u32(sKV + st * C::KV_BYTES);
-                const int own = max(seg.length - k0, 0), behind = seg.length + T - k0;
+                const int own = max(seg.length - k0, 0), behind = min(seg.length + T - k0, kManyTile);
                 bool odd = false;
-                for (int c = ft; c < C::KV_BYTES / 16; c += 64) {       // 8 chunks a row of each half
-                    const int row = (c >> 3) & 127;
-                    if (row < own) continue;
-                    if (row >= behind) {
-                        sts_u128(v + c * 16, make_uint4(0, 0, 0, 0));
-                    } else {
-                        uint4 w = lds_u128(v + c * 16);
+                for (int hf = 0; hf < D / 64; ++hf) {                  // 8 chunks a row of each half
+                    const uint32_t half = v + hf * kManyTile * 128;
+#pragma unroll 4
+                    for (int c = own * 8 + ft; c < behind * 8; c += 64) {
+                        uint4 w = lds_u128(half + c * 16);
                         if (any_odd(w)) {
                             odd = true;
                             drop_odd(w);
-                            sts_u128(v + c * 16, w);
+                            sts_u128(half + c * 16, w);
                         }
                     }
+                    for (int c = behind * 8 + ft; c < kManyTile * 8; c += 64) sts_u128(half + c * 16, make_uint4(0, 0, 0, 0));
                 }
                 if (odd) odd_sh[i_seg & 3] = 1;
                 __threadfence_block();
@@ -715,7 +743,7 @@ __global__ void __launch_bounds__(384, 1)
         const uint32_t tS = tmem + lane_off + t * 128, tO = tmem + lane_off + C::TM_O;
         const float scale_log2 = a.scale * kLog2e;
         uint32_t jobs = 0;
-        for (uint32_t i_seg = 0; walk.next(a, plan, seg); ++i_seg) {
+        for (uint32_t i_seg = 0; walk.next(a.lengths, plan, seg); ++i_seg) {
             const int n = seg.last - seg.first;
             const int row = seg.tile * ROWS + (MODE == 2 ? t * 128 : 0) + r_tile;
             const bool idle = row - lane >= R;          // a warp without rows
@@ -828,12 +856,12 @@ __global__ void __launch_bounds__(384, 1)
             wait_bounded(&bar_o[t], i_seg & 1, g);
             if (MODE == 1) wait_bounded(&bar_o[t ^ 1], i_seg & 1, g);
             ptx::tc_fence_after();
-            const bool whole = seg.first == 0 && seg.last == seg.nb;
+            const bool whole = seg.whole();
             const bool tail = seg.last * kManyTile > seg.length;
             const bool odd = tail && odd_sh[i_seg & 3];
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            const long long at = seg.unit_row * R + row;
-            const long long slot = (2 * (long long)blockIdx.x + (seg.first == 0 ? 1 : 0)) * ROWS + row % ROWS;
+            const long long at = seg.head * R + row;
+            const long long slot = 2 * (long long)blockIdx.x + (seg.first == 0 ? 1 : 0);
             constexpr int COLS = MODE == 1 ? D / 2 : D;
             if (!idle) {
 #pragma unroll
@@ -860,7 +888,7 @@ __global__ void __launch_bounds__(384, 1)
                         for (int u = 0; u < T; ++u) {
                             const int key = seg.length + u;
                             if (!(word >> u & 1) || key < seg.first * kManyTile || key >= seg.last * kManyTile) continue;
-                            const uint4 *from = static_cast<const uint4 *>(a.v) + (seg.unit_row * a.C + key) * (D / 8) + c / 8;
+                            const uint4 *from = static_cast<const uint4 *>(a.v) + (seg.head * a.C + key) * (D / 8) + c / 8;
 #pragma unroll
                             for (int x = 0; x < 4; ++x) {
                                 const uint4 w = from[x];
@@ -886,16 +914,16 @@ __global__ void __launch_bounds__(384, 1)
                                 dst[x] = make_uint4(w[0], w[1], w[2], w[3]);
                             }
                         } else {
-                            uint4 *dst = reinterpret_cast<uint4 *>(parts.o + slot * D + c);
+                            uint4 *dst = reinterpret_cast<uint4 *>(parts.o) + (slot * (D / 4) + c / 4) * ROWS + row % ROWS;
 #pragma unroll
                             for (int x = 0; x < 8; ++x)
-                                dst[x] = make_uint4(ov[4 * x], ov[4 * x + 1], ov[4 * x + 2], ov[4 * x + 3]);
+                                dst[x * ROWS] = make_uint4(ov[4 * x], ov[4 * x + 1], ov[4 * x + 2], ov[4 * x + 3]);
                         }
                     }
                 }
                 if (row < R && (MODE == 2 || t == 0)) {
                     if (whole) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * (1.f / kLog2e);
-                    else parts.ml[slot] = make_float2(m, l);
+                    else parts.ml[slot * ROWS + row % ROWS] = make_float2(m, l);
                 }
             }
             ptx::tc_fence_before();
@@ -911,7 +939,46 @@ __global__ void __launch_bounds__(384, 1)
     }
 }
 
-// Adds up the parts of one row, if its unit was split.  A block a row, a warp every fourth part.
+// Adds up the parts of a unit that was split, each with its maximum and sum, in the order of their slots.
+struct Sum {
+    float top = -INFINITY, l = 0.f;
+    // Takes a part in: the factors of what is there and of the part.
+    __device__ __forceinline__ void take(float2 ml, float &old, float &part)
+    {
+        const float t = fmaxf(top, ml.x), ref = t == -INFINITY ? 0.f : t;
+        old = ptx::ex2(top - ref);
+        part = ptx::ex2(ml.x - ref);
+        l = l * old + ml.y * part;
+        top = t;
+    }
+    __device__ __forceinline__ float inverse() const { return l == 0.f ? 0.f : 1.f / l; }
+    __device__ __forceinline__ float lse() const { return l == 0.f ? -INFINITY : (top + log2f(l)) * (1.f / kLog2e); }
+};
+
+// Where a unit's parts are.  By a whole warp.
+struct Pieces {
+    long long c0;
+    int count;
+    __device__ __forceinline__ Pieces(const CacheAttnArgs &a, const Plan &plan, int ctas, int b, int h, int tile)
+    {
+        long long before;
+        const long long total = count_blocks(a.lengths, a.B, b, plan, before);
+        const long long per = divide(total + ctas - 1, ctas);
+        const int nb = blocks_of(length_of(a.lengths, b, a.T, a.C), plan);
+        const long long u0 = before + ((long long)h * plan.tiles + tile) * nb;
+        if (per <= 0x7fffffff) {
+            c0 = divide(u0, (int)per);
+            count = (int)(divide(u0 + nb - 1, (int)per) - c0) + 1;
+        } else {
+            c0 = u0 / per;
+            count = (int)((u0 + nb - 1) / per - c0) + 1;
+        }
+    }
+    // the first part begins the unit, the others inside it
+    __device__ __forceinline__ long long slot(int i) const { return i == 0 ? 2 * c0 + 1 : 2 * (c0 + i); }
+};
+
+// few_kernel's parts: a block a row, a warp every fourth part, a lane D / 32 columns.
 constexpr int kJoinWarps = 4;
 
 template <int D>
@@ -920,65 +987,89 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(CacheAttnArgs a, 
     __shared__ float so[kJoinWarps][D];
     __shared__ float2 sml[kJoinWarps];
     ptx::grid_dep_launch();
-    ptx::grid_dep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int R = a.G * a.T;
-    const long long at = blockIdx.x;                 // row of o
-    const long long head = at / R;
-    const int r = (int)(at % R), b = (int)(head / plan.H), h = (int)(head % plan.H);
-    const long long total = blocks_before(a.lengths, a.B, plan);
-    const long long per = (total + ctas - 1) / ctas;
-    const int nb = blocks_of(length_of(a.lengths, b, a.T, a.C), plan);
-    const long long u0 =
-        blocks_before(a.lengths, b, plan) + ((long long)h * plan.tiles + r / rows) * nb;
-    const long long c0 = u0 / per, c1 = (u0 + nb - 1) / per;
-    if (c0 == c1) return;                            // one CTA had it whole
-    const int count = (int)(c1 - c0 + 1);
-    auto slot = [&](int i) {                         // the first part begins the unit, the others inside it
-        return ((i == 0 ? 2 * c0 + 1 : 2 * (c0 + i)) * rows + r % rows);
-    };
-    float top = -INFINITY, sum = 0.f;
+    const int head = (int)(blockIdx.x / (unsigned)R), r = (int)(blockIdx.x % (unsigned)R);
+    const int b = head / plan.H, h = head % plan.H;
+    ptx::grid_dep_wait();
+    const Pieces pieces(a, plan, ctas, b, h, r / rows);
+    if (pieces.count == 1) return;
     constexpr int PER = D / 32;
-    float o[PER];
-#pragma unroll
-    for (int e = 0; e < PER; ++e) o[e] = 0.f;
-    for (int i = warp; i < count; i += kJoinWarps) top = fmaxf(top, parts.ml[slot(i)].x);
-    const float base = top == -INFINITY ? 0.f : top;
+    Sum sum;
+    float o[PER] = {};
 #pragma unroll 4
-    for (int i = warp; i < count; i += kJoinWarps) {
-        const float2 ml = parts.ml[slot(i)];
-        const float f = ptx::ex2(ml.x - base);
-        const float *from = parts.o + slot(i) * D + lane * PER;
-        sum += f * ml.y;
-        if (PER == 4) {
-            const float4 v = *reinterpret_cast<const float4 *>(from);
-            o[0] += f * v.x; o[1] += f * v.y; o[PER - 2] += f * v.z; o[PER - 1] += f * v.w;
-        } else {
-            const float2 v = *reinterpret_cast<const float2 *>(from);
-            o[0] += f * v.x; o[1] += f * v.y;
-        }
+    for (int i = warp; i < pieces.count; i += kJoinWarps) {
+        const long long at = pieces.slot(i) * rows + r % rows;
+        const float2 ml = parts.ml[at];
+        const float *from = parts.o + at * D + lane * PER;
+        float v[PER], f, p;
+        if (PER == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(from);
+        else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(from);
+        sum.take(ml, f, p);
+#pragma unroll
+        for (int e = 0; e < PER; ++e) o[e] = o[e] * f + v[e] * p;
     }
 #pragma unroll
     for (int e = 0; e < PER; ++e) so[warp][lane * PER + e] = o[e];
-    if (lane == 0) sml[warp] = make_float2(top, sum);
+    if (lane == 0) sml[warp] = make_float2(sum.top, sum.l);
     __syncthreads();
-    float all = -INFINITY, f[kJoinWarps], l = 0.f;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) all = fmaxf(all, sml[w].x);
-    const float ref = all == -INFINITY ? 0.f : all;
+    if (warp > 0) return;
+    Sum all;
+    float v[PER] = {};
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) {
-        f[w] = ptx::ex2(sml[w].x - ref);
-        l += f[w] * sml[w].y;
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    for (int c = threadIdx.x; c < D; c += 32 * kJoinWarps) {
-        float v = 0.f;
+        float f, p;
+        all.take(sml[w], f, p);
 #pragma unroll
-        for (int w = 0; w < kJoinWarps; ++w) v += f[w] * so[w][c];
-        static_cast<__nv_bfloat16 *>(a.o)[at * D + c] = __float2bfloat16(v * inv);
+        for (int e = 0; e < PER; ++e) v[e] = v[e] * f + so[w][lane * PER + e] * p;
     }
-    if (threadIdx.x == 0) a.lse[at] = l == 0.f ? -INFINITY : (all + log2f(l)) * (1.f / kLog2e);
+    const float inv = all.inverse();
+    uint32_t *to = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(a.o) + (long long)blockIdx.x * D + lane * PER);
+#pragma unroll
+    for (int e = 0; e < PER; e += 2) to[e / 2] = ptx::pack_bf16x2(v[e] * inv, v[e + 1] * inv);
+    if (lane == 0) a.lse[blockIdx.x] = all.lse();
+}
+
+// many_kernel's parts: a warp four columns of 32 rows, a block 32 columns of them.
+template <int D>
+__global__ void __launch_bounds__(256) join_many_kernel(CacheAttnArgs a, Plan plan, int rows, int ctas, Parts parts)
+{
+    __shared__ uint2 out[32][9];
+    ptx::grid_dep_launch();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int groups = rows / 32, cols = D / 32;
+    const int col = (int)(blockIdx.x % cols) * 32, group = (int)(blockIdx.x / cols % groups);
+    const unsigned unit = blockIdx.x / (cols * groups);
+    const int tile = (int)(unit % (unsigned)plan.tiles), head = (int)(unit / (unsigned)plan.tiles);
+    const int b = head / plan.H, h = head % plan.H, R = a.G * a.T;
+    const int r0 = tile * rows + group * 32;
+    ptx::grid_dep_wait();
+    if (r0 >= R) return;
+    const Pieces pieces(a, plan, ctas, b, h, tile);
+    if (pieces.count == 1) return;
+    Sum sum;
+    float o[4] = {};
+    const int r = group * 32 + lane;
+#pragma unroll 4
+    for (int i = 0; i < pieces.count; ++i) {
+        const long long slot = pieces.slot(i);
+        const float2 ml = parts.ml[slot * rows + r];
+        const float4 v = reinterpret_cast<const float4 *>(parts.o)[(slot * (D / 4) + col / 4 + warp) * rows + r];
+        float f, p;
+        sum.take(ml, f, p);
+        o[0] = o[0] * f + v.x * p;
+        o[1] = o[1] * f + v.y * p;
+        o[2] = o[2] * f + v.z * p;
+        o[3] = o[3] * f + v.w * p;
+    }
+    const float inv = sum.inverse();
+    out[lane][warp] = make_uint2(ptx::pack_bf16x2(o[0] * inv, o[1] * inv), ptx::pack_bf16x2(o[2] * inv, o[3] * inv));
+    __syncthreads();
+    const int row = threadIdx.x >> 3, part = threadIdx.x & 7;
+    if (r0 + row < R)
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.o) + ((long long)head * R + r0 + row) * D + col + part * 4) =
+            out[row][part];
+    if (col == 0 && warp == 0 && r0 + lane < R) a.lse[(long long)head * R + r0 + lane] = sum.lse();
 }
 
 // weights_out = weights + the weights that the counted rows give each slot: K is read a second time, the rows in
@@ -1098,8 +1189,10 @@ cudaError_t launch(const CacheAttnArgs &a, cudaStream_t stream)
         e = sh.rows == 128 ? launch_many<D, 1>(a, plan, parts, sh.ctas, stream)
                            : launch_many<D, 2>(a, plan, parts, sh.ctas, stream);
     if (e != cudaSuccess) return e;
-    e = launch_overlapped(join_kernel<D>, dim3((unsigned)((long long)a.B * a.H * R)), dim3(32 * kJoinWarps), 0, 1, stream,
-                          a, plan, sh.rows, sh.ctas, parts);
+    e = sh.many() ? launch_overlapped(join_many_kernel<D>, dim3((unsigned)(a.B * a.H) * plan.tiles * (sh.rows / 32) * (D / 32)),
+                                      dim3(256), 0, 1, stream, a, plan, sh.rows, sh.ctas, parts)
+                  : launch_overlapped(join_kernel<D>, dim3((unsigned)(a.B * a.H) * R), dim3(32 * kJoinWarps), 0, 1, stream, a,
+                                      plan, sh.rows, sh.ctas, parts);
     if (e != cudaSuccess || !a.weights) return e;
     const int blocks = (a.C + kBlock - 1) / kBlock;
     return launch_overlapped(weights_kernel<D>, dim3((unsigned)((long long)a.B * a.H * blocks)), dim3(kFewThreads), 0, 1,
