@@ -424,8 +424,11 @@ attn_status attn_cache_append(const void *k, const void *v, void *cache_k, void 
                               void *q_out, float *weights, int *slot_positions, int B, int H, int Hq, int T, int n,
                               int d_k, int C, int rotated, int interleaved, float amplitude, cudaStream_t stream);
 
-/* Bytes of device workspace attn_cache_attention() needs (0 for sizes it rejects). */
-size_t attn_cache_attention_workspace_size(int B, int H, int G, int T, int C, int d_k);
+/*
+ * Bytes of device workspace attn_cache_attention() needs, with or without accumulated weights (0 for sizes it
+ * rejects).
+ */
+size_t attn_cache_attention_workspace_size(int B, int H, int G, int T, int C, int d_k, int with_weights);
 
 /*
  * Attention of T tokens (1 ... 64; T = 1: the next token) of each sequence over its cache, in which they lie in slots

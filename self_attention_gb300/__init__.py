@@ -146,7 +146,7 @@ def load_library(path: str = LIB_PATH):
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = _I
     for name, n in (("attn_linear_bwd_workspace_size", 4), ("attn_out_proj_bwd_workspace_size", 5),
-                    ("attn_rms_norm_bwd_workspace_size", 2), ("attn_cache_attention_workspace_size", 6),
+                    ("attn_rms_norm_bwd_workspace_size", 2), ("attn_cache_attention_workspace_size", 7),
                     ("attn_cache_evict_workspace_size", 5)):
         getattr(lib, name).argtypes = [_I] * n
         getattr(lib, name).restype = _SZ
@@ -391,8 +391,9 @@ def attn_cache_append(k, v, cache_k, cache_v, lengths, turns, positions, rows, q
         float(amplitude), _stream(stream)), "attn_cache_append")
 
 
-def attn_cache_attention_workspace_size(B: int, H: int, G: int, T: int, C: int, d_k: int) -> int:
-    return int(load_library().attn_cache_attention_workspace_size(B, H, G, T, C, d_k))
+def attn_cache_attention_workspace_size(B: int, H: int, G: int, T: int, C: int, d_k: int,
+                                        with_weights: bool = False) -> int:
+    return int(load_library().attn_cache_attention_workspace_size(B, H, G, T, C, d_k, int(with_weights)))
 
 
 def attn_cache_attention(q, cache_k, cache_v, lengths, tree, counted, weights, weights_out, o, lse, workspace,

@@ -1254,9 +1254,10 @@ extern "C" attn_status attn_cache_append(const void *k, const void *v, void *cac
     return e == cudaSuccess ? ATTN_OK : fail("attn_cache_append launch", e);
 }
 
-extern "C" size_t attn_cache_attention_workspace_size(int B, int H, int G, int T, int C, int d_k)
+extern "C" size_t attn_cache_attention_workspace_size(int B, int H, int G, int T, int C, int d_k, int with_weights)
 {
-    return check_cache_attention(B, H, G, T, C, d_k) == ATTN_OK ? cache_attn_workspace(G, T, d_k) : 0;
+    return check_cache_attention(B, H, G, T, C, d_k) == ATTN_OK ? cache_attn_workspace(B, H, G, T, C, d_k, with_weights != 0)
+                                                                : 0;
 }
 
 extern "C" attn_status attn_cache_attention(const void *q, const void *cache_k, const void *cache_v,
@@ -1271,7 +1272,7 @@ extern "C" attn_status attn_cache_attention(const void *q, const void *cache_k, 
     if (!q || !cache_k || !cache_v || !lengths || !o || !lse || (weights != nullptr) != (weights_out != nullptr) ||
         (counted && !weights))
         return ATTN_ERR_INVALID_ARG;
-    const size_t need = cache_attn_workspace(G, T, d_k);
+    const size_t need = cache_attn_workspace(B, H, G, T, C, d_k, weights != nullptr);
     if (!workspace_ok(workspace, workspace_bytes, need)) return ATTN_ERR_WORKSPACE;
     const size_t bh = (size_t)B * H, cache = bh * C * d_k * 2, qs = bh * G * T * d_k * 2;
     const Part ins[7] = {{weights, bh * C * 4, 4}, {q, qs, 16}, {cache_k, cache, 16}, {cache_v, cache, 16},

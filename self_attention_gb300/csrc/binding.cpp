@@ -549,7 +549,7 @@ PyObject *cache_attention(Args a)
         if (fresh) out = empty({k.B, k.H, k.N}, kF32, q.dev);
         const int G = count(q.H / k.H);
         const size_t bytes =
-            attn_cache_attention_workspace_size(count(q.B), count(k.H), G, count(q.N), count(k.N), count(q.d));
+            attn_cache_attention_workspace_size(count(q.B), count(k.H), G, count(q.N), count(k.N), count(q.d), weights != nullptr);
         const at::Tensor ws = empty({(int64_t)(bytes ? bytes : 1)}, at::kByte, q.dev);
         code = attn_cache_attention(q.t.data_ptr(), k.t.data_ptr(), v, lengths, tree, counted, weights,
                                     fresh ? static_cast<float *>(out.data_ptr()) : given, o.data_ptr(),

@@ -98,6 +98,11 @@ __device__ __forceinline__ int blocks_of(int length, const Plan &p) { return (le
 // Blocks of all sequences, and of those ahead of sequence `upto`; by a whole warp, the same in every lane.
 __device__ __forceinline__ long long count_blocks(const int *lengths, int B, int upto, const Plan &p, long long &before)
 {
+    if (B <= 32) {
+        const int b = threadIdx.x & 31, n = b < B ? blocks_of(length_of(lengths, b, p.T, p.C), p) : 0;
+        before = (long long)__reduce_add_sync(0xffffffffu, b < upto ? n : 0) * p.H * p.tiles;
+        return (long long)__reduce_add_sync(0xffffffffu, n) * p.H * p.tiles;
+    }
     long long all = 0, ahead = 0;
     for (int b = threadIdx.x & 31; b < B; b += 32) {
         const int n = blocks_of(length_of(lengths, b, p.T, p.C), p);
@@ -135,51 +140,43 @@ struct Walk {
     __device__ __forceinline__ bool begin(const int *lengths, int B, const Plan &p)
     {
         const uint32_t lane = threadIdx.x & 31;
-        const long long per_block = (long long)p.H * p.tiles;
-        long long all = 0;
-        const int mine = (int)lane < B ? length_of(lengths, (int)lane, p.T, p.C) : 0;
-        const long long n0 = (int)lane < B ? blocks_of(mine, p) : 0;
-        long long inc = n0;
+        const long long per_unit = (long long)p.H * p.tiles;
+        int len = (int)lane < B ? length_of(lengths, (int)lane, p.T, p.C) : 0, inc;
+        int n = (int)lane < B ? blocks_of(len, p) : 0;
+        auto scan = [&] {         // blocks of these 32 sequences up to the lane's own
+            inc = n;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long t = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= (uint32_t)o) inc += t;
-        }
-        all = __shfl_sync(0xffffffffu, inc, 31);
+            for (int o = 1; o < 32; o <<= 1) {
+                const int t = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= (uint32_t)o) inc += t;
+            }
+        };
+        scan();
+        long long all = (long long)__shfl_sync(0xffffffffu, inc, 31) * per_unit;
         if (B > 32) {
             long long ignored;
             all = count_blocks(lengths, B, 0, p, ignored);
-        } else {
-            all *= per_block;
         }
         const long long per = divide(all + gridDim.x - 1, (int)gridDim.x);
         x = per * blockIdx.x;
         end = min(x + per, all);
         if (x >= end) return false;
         long long sum = 0;
-        for (int b0 = 0;; b0 += 32) {          // ends: x lies before `all`
-            int len = mine;
-            long long n = n0;
-            if (b0 > 0) {
-                len = b0 + (int)lane < B ? length_of(lengths, b0 + (int)lane, p.T, p.C) : 0;
-                n = b0 + (int)lane < B ? blocks_of(len, p) : 0;
-                inc = n;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const long long t = __shfl_up_sync(0xffffffffu, inc, o);
-                    if (lane >= (uint32_t)o) inc += t;
-                }
-            }
-            const uint32_t hit = __ballot_sync(0xffffffffu, x < (sum + inc) * per_block);
+        for (int b0 = 0;;) {          // ends: x lies before `all`
+            const uint32_t hit = __ballot_sync(0xffffffffu, x < (sum + inc) * per_unit);
             if (hit) {
                 const int l = __ffs(hit) - 1;
-                before = (sum + __shfl_sync(0xffffffffu, inc - n, l)) * per_block;
+                before = (sum + __shfl_sync(0xffffffffu, inc - n, l)) * per_unit;
                 length = __shfl_sync(0xffffffffu, len, l);
                 nb = blocks_of(length, p);
                 b = b0 + l;
                 return true;
             }
             sum += __shfl_sync(0xffffffffu, inc, 31);
+            b0 += 32;
+            len = b0 + (int)lane < B ? length_of(lengths, b0 + (int)lane, p.T, p.C) : 0;
+            n = b0 + (int)lane < B ? blocks_of(len, p) : 0;
+            scan();
         }
     }
     // By any thread.
@@ -217,6 +214,7 @@ __device__ __forceinline__ uint64_t word_of(const uint64_t *tree, int b, int T, 
 struct Parts {
     float *o;          // [2 grid][rows][d]; many_kernel's [2 grid][d / 4][rows][4], so that its threads, one a row, write runs
     float2 *ml;        // [2 grid][rows]: maximum (of scores times log2 e) and sum
+    float *scores;     // null, or [B H][G T][C]: scores times log2 e, -infinity where a row does not see a slot
 };
 
 template <int D, int NT>
@@ -337,6 +335,13 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) few_kernel(Cache
                             const int j = key + g + 8 * i - length;
                             if (j >= 0 && !(j < T && (word >> j & 1))) s[t][e + 2 * i] = -INFINITY;
                         }
+                    }
+                }
+                if (parts.scores) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int r = r0 + 8 * t + 2 * q + (e & 1), j = key + g + 8 * (e >> 1);
+                        if (r < R && j < length + T) parts.scores[(head * R + r) * a.C + j] = s[t][e];
                     }
                 }
                 // The maximum is brought up to date only where some score exceeds it.
@@ -978,8 +983,8 @@ struct Pieces {
     __device__ __forceinline__ long long slot(int i) const { return i == 0 ? 2 * c0 + 1 : 2 * (c0 + i); }
 };
 
-// few_kernel's parts: a block a row, a warp every fourth part, a lane D / 32 columns.
-constexpr int kJoinWarps = 4;
+// few_kernel's parts: a block a row, a warp every eighth part, a lane D / 32 columns.
+constexpr int kJoinWarps = 8;
 
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(CacheAttnArgs a, Plan plan, int rows, int ctas, Parts parts)
@@ -1072,8 +1077,39 @@ __global__ void __launch_bounds__(256) join_many_kernel(CacheAttnArgs a, Plan pl
     if (col == 0 && warp == 0 && r0 + lane < R) a.lse[(long long)head * R + r0 + lane] = sum.lse();
 }
 
-// weights_out = weights + the weights that the counted rows give each slot: K is read a second time, the rows in
-// eights.  A block takes 64 slots of one (sequence, cached head).
+// weights_out = weights + the weights that the counted rows give each slot, from the scores that few_kernel kept: a
+// thread a slot.  At up to 16 rows the scores (4 bytes a row and slot, twice) are less than K (2 d bytes) a second time.
+__global__ void __launch_bounds__(256) kept_weights_kernel(CacheAttnArgs a, int blocks, const float *scores)
+{
+    __shared__ float lse[16];
+    ptx::grid_dep_launch();
+    const int head = (int)(blockIdx.x / (unsigned)blocks), b = head / a.H, T = a.T, R = a.G * T;
+    const int j = (int)(blockIdx.x % (unsigned)blocks) * 256 + threadIdx.x;
+    ptx::grid_dep_wait();
+    if (threadIdx.x < R) {
+        const bool counted = !a.counted || (a.counted[b] >> (threadIdx.x % T) & 1);
+        lse[threadIdx.x] = counted ? a.lse[(long long)head * R + threadIdx.x] * kLog2e : INFINITY;
+    }
+    const int valid = length_of(a.lengths, b, T, a.C) + T;
+    __syncthreads();
+    if (j >= a.C) return;
+    const long long at = (long long)head * a.C + j;
+    if (j >= valid && a.weights_out == a.weights) return;
+    const float was = a.weights[at];
+    float sum = 0.f;
+    if (j < valid) {
+        const float *from = scores + (long long)head * R * a.C + j;
+#pragma unroll 4
+        for (int r = 0; r < R; ++r) {
+            const float s = from[(long long)r * a.C];
+            if (lse[r] != INFINITY && s != -INFINITY) sum += ptx::ex2(s - lse[r]);
+        }
+    }
+    a.weights_out[at] = was + sum;
+}
+
+// The same for more rows: K is read a second time, the rows in eights.  A block takes 64 slots of one (sequence,
+// cached head).
 template <int D>
 __global__ void __launch_bounds__(kFewThreads) weights_kernel(CacheAttnArgs a, int blocks)
 {
@@ -1154,6 +1190,13 @@ Shape shape_of(int R)
     return {R <= 128 ? 128 : 256, kPlanSms};
 }
 
+// Bytes of the parts' results.
+size_t parts_bytes(const Shape &sh, int d)
+{
+    const size_t slots = (size_t)2 * sh.ctas * sh.rows;
+    return up256(slots * d * 4) + up256(slots * 8);
+}
+
 template <int D, int MODE>
 cudaError_t launch_many(const CacheAttnArgs &a, const Plan &plan, const Parts &parts, int ctas, cudaStream_t stream)
 {
@@ -1180,6 +1223,8 @@ cudaError_t launch(const CacheAttnArgs &a, cudaStream_t stream)
     Parts parts;
     parts.o = static_cast<float *>(a.workspace);
     parts.ml = reinterpret_cast<float2 *>(static_cast<char *>(a.workspace) + up256((size_t)2 * sh.ctas * sh.rows * D * 4));
+    parts.scores = a.weights && !sh.many() ? reinterpret_cast<float *>(static_cast<char *>(a.workspace) + parts_bytes(sh, D))
+                                           : nullptr;
     cudaError_t e;
     if (sh.rows == 8)
         e = launch_overlapped(few_kernel<D, 1>, dim3(sh.ctas), dim3(kFewThreads), 0, 1, stream, a, plan, parts);
@@ -1194,6 +1239,11 @@ cudaError_t launch(const CacheAttnArgs &a, cudaStream_t stream)
                   : launch_overlapped(join_kernel<D>, dim3((unsigned)(a.B * a.H) * R), dim3(32 * kJoinWarps), 0, 1, stream, a,
                                       plan, sh.rows, sh.ctas, parts);
     if (e != cudaSuccess || !a.weights) return e;
+    if (!sh.many()) {
+        const int blocks = (a.C + 255) / 256;
+        return launch_overlapped(kept_weights_kernel, dim3((unsigned)(a.B * a.H) * blocks), dim3(256), 0, 1, stream, a, blocks,
+                                 (const float *)parts.scores);
+    }
     const int blocks = (a.C + kBlock - 1) / kBlock;
     return launch_overlapped(weights_kernel<D>, dim3((unsigned)((long long)a.B * a.H * blocks)), dim3(kFewThreads), 0, 1,
                              stream, a, blocks);
@@ -1201,11 +1251,10 @@ cudaError_t launch(const CacheAttnArgs &a, cudaStream_t stream)
 
 }  // namespace
 
-size_t cache_attn_workspace(int G, int T, int d)
+size_t cache_attn_workspace(int B, int H, int G, int T, int C, int d, bool weights)
 {
     const Shape sh = shape_of(G * T);
-    const size_t slots = (size_t)2 * sh.ctas * sh.rows;
-    return up256(slots * d * 4) + up256(slots * 8);
+    return parts_bytes(sh, d) + (weights && !sh.many() ? up256((size_t)B * H * G * T * C * 4) : 0);
 }
 
 cudaError_t launch_cache_attn(const CacheAttnArgs &a, cudaStream_t stream)

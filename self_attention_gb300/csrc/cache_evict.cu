@@ -7,9 +7,10 @@
 //
 // select_kernel: one block a sequence and head.  A slot's rank is its weight's bits (weights count as zero where
 // they are negative or NaN), all ones for the newest positions.  The n-th largest rank is found by three
-// histograms of 11, 11 and 10 bits over ranks that stay in shared memory (from L2 where they do not fit), then
-// one ordered pass over the slots numbers the ties, the holes and the movers.  move_kernel: the rows, 16 bytes
-// a lane, over the whole GPU.
+// histograms of 11, 11 and 10 bits over ranks that stay in shared memory (from L2 where they do not fit).  Then each
+// warp takes a run of neighbouring slots and numbers its ties, its holes and its movers by ballots, with one sum over
+// the warps in between: in order without a barrier a step.  move_kernel: the rows, 16 bytes a lane, over the whole
+// GPU.
 // Bound by HBM (8 bytes a slot, 8 d a moved slot) once there are enough sequences and heads, by the select's
 // latency before.
 #include "cluster.cuh"
@@ -25,14 +26,12 @@ constexpr int kMoveRows = 32;            // moves a block of move_kernel takes
 
 struct SelShared {
     uint32_t bins[kBins];
-    uint32_t warp[32];
-    uint32_t warp2[32];
+    uint32_t warp[3][32];
     uint32_t prefix;                     // rank bits found so far
     uint32_t need;                       // how many are still to be taken among those with this prefix
-    int newest;
 };
 
-// Sum over the lanes before this one, and over all of the warp.
+// Sum over the lanes before this one and this one.
 __device__ __forceinline__ uint32_t warp_scan(uint32_t v, uint32_t lane)
 {
 #pragma unroll
@@ -43,18 +42,15 @@ __device__ __forceinline__ uint32_t warp_scan(uint32_t v, uint32_t lane)
     return v;
 }
 
-// Exclusive sum over the block's threads; `total` over all of them.  `buf` is free again after the next barrier.
-__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *buf, uint32_t &total)
+// Sum of `v` over the warps before this one, `total` over all of them; v is the same in all lanes of a warp.
+__device__ __forceinline__ uint32_t warps_before(uint32_t v, uint32_t *buf, uint32_t &total)
 {
     const uint32_t lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const uint32_t inc = warp_scan(v, lane);
-    if (lane == 31) buf[w] = inc;
+    if (lane == 0) buf[w] = v;
     __syncthreads();
-    const uint32_t part = buf[lane];
-    const uint32_t sums = warp_scan(part, lane);
+    const uint32_t part = buf[lane], sums = warp_scan(part, lane);
     total = __shfl_sync(0xffffffffu, sums, 31);
-    const uint32_t before = __shfl_sync(0xffffffffu, sums - part, w);
-    return before + inc - v;
+    return __shfl_sync(0xffffffffu, sums - part, w);
 }
 
 __device__ __forceinline__ uint32_t rank_of(float w, int pos, long long oldest)
@@ -69,7 +65,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int st
     __shared__ SelShared s;
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
-    const int tid = threadIdx.x, bh = blockIdx.x, b = bh / a.H;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, bh = blockIdx.x, b = bh / a.H;
     const int L = min(max(a.lengths[b], 0), a.C), n = min(L, a.keep);
     const long long row = (long long)bh * a.C;
     const float *w = a.weights + row;
@@ -80,26 +76,27 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int st
     if (bh % a.H == 0 && tid == 0) a.lengths_out[b] = n;
     // what lies behind the kept slots is empty; sources of moves are emptied by those who read them
     if (n == L) {
+#pragma unroll 4
         for (int j = tid; j < a.C; j += kSelThreads) {
-            const float x = w[j];
-            const int p = pos[j];
-            w_out[j] = j < n ? x : 0.f;
-            pos_out[j] = j < n ? p : -1;
+            const float x = j < n ? w[j] : 0.f;
+            const int p = j < n ? pos[j] : -1;
+            w_out[j] = x;
+            pos_out[j] = p;
         }
         if (tid == 0) moves[0] = 0;
         return;
     }
 
     // the newest position
+    for (int i = tid; i < kBins; i += kSelThreads) s.bins[i] = 0;
     int newest = INT32_MIN;
+#pragma unroll 8
     for (int j = tid; j < L; j += kSelThreads) newest = max(newest, pos[j]);
     newest = __reduce_max_sync(0xffffffffu, newest);
-    if ((tid & 31) == 0) s.warp[tid >> 5] = (uint32_t)newest;
+    if (lane == 0) s.warp[0][warp] = (uint32_t)newest;
     __syncthreads();
-    newest = __reduce_max_sync(0xffffffffu, (int)s.warp[tid & 31]);
+    newest = __reduce_max_sync(0xffffffffu, (int)s.warp[0][lane]);
     const long long oldest = (long long)newest - a.recent;   // positions above it are safe
-    if (in_smem)
-        for (int j = tid; j < L; j += kSelThreads) ranks[j] = rank_of(w[j], pos[j], oldest);
     auto rank = [&](int j) { return in_smem ? ranks[j] : rank_of(w[j], pos[j], oldest); };
 
     // the n-th largest rank
@@ -107,23 +104,39 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int st
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
         const uint32_t mask = pass == 0 ? 0u : 0xffffffffu << (shift + bits);
-        for (int i = tid; i < kBins; i += kSelThreads) s.bins[i] = 0;
-        __syncthreads();
-        for (int j0 = 0; j0 < L; j0 += kSelThreads) {
-            const int j = j0 + tid;
-            const uint32_t r = j < L ? rank(j) : 0u;
-            const bool in = j < L && (r & mask) == prefix;
-            const uint32_t bin = r >> shift & ((1u << bits) - 1);
-            // neighbours often share a bin (weights of one magnitude, ties of zero): one addition for all of them
-            const uint32_t same = __match_any_sync(0xffffffffu, in ? bin : 0xffffffffu);
-            if (in && (same & ((1u << (tid & 31)) - 1)) == 0) atomicAdd(&s.bins[bin], (uint32_t)__popc(same));
+        auto count = [&](uint32_t r, bool there) {
+            const uint32_t bin = there && (r & mask) == prefix ? r >> shift & ((1u << bits) - 1) : 0xffffffffu;
+            // ties (zeros, the newest) often fill a warp: one addition for all of them
+            const uint32_t b0 = __shfl_sync(0xffffffffu, bin, 0);
+            if (__all_sync(0xffffffffu, bin == b0)) {
+                if (lane == 0 && bin != 0xffffffffu) atomicAdd(&s.bins[bin], 32u);
+            } else if (bin != 0xffffffffu) {
+                atomicAdd(&s.bins[bin], 1u);
+            }
+        };
+        if (pass == 0) {
+#pragma unroll 4
+            for (int j0 = 0; j0 < L; j0 += kSelThreads) {
+                const int j = j0 + tid;
+                const uint32_t r = j < L ? rank_of(w[j], pos[j], oldest) : 0u;
+                if (in_smem && j < L) ranks[j] = r;
+                count(r, j < L);
+            }
+        } else {
+            for (int j0 = 0; j0 < L; j0 += kSelThreads) {
+                const int j = j0 + tid;
+                count(j < L ? rank(j) : 0u, j < L);
+            }
         }
         __syncthreads();
         // bins from the top: thread t holds bins 2 (1023 - t) + 1 and 2 (1023 - t)
         const int top = 2 * (kSelThreads - 1 - tid) + 1;
         const uint32_t c1 = s.bins[top], c0 = s.bins[top - 1];
+        s.bins[top] = s.bins[top - 1] = 0;                 // for the next pass
+        const uint32_t inc = warp_scan(c0 + c1, lane);
         uint32_t total;
-        const uint32_t above = block_scan(c0 + c1, s.warp2, total);
+        const uint32_t above =
+            warps_before(__shfl_sync(0xffffffffu, inc, 31), s.warp[1], total) + inc - c0 - c1;
         if (above < need && need <= above + c0 + c1) {
             const bool first = need <= above + c1;
             s.prefix = prefix | (uint32_t)(first ? top : top - 1) << shift;
@@ -134,27 +147,45 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int st
         need = s.need;
     }
 
-    // In order: ranks above `prefix` stay, and the first `need` that equal it.
-    uint32_t ties = 0, holes = 0, movers = 0;
-    for (int j0 = 0; j0 < L; j0 += kSelThreads) {
-        const int j = j0 + tid;
-        const uint32_t r = j < L ? rank(j) : 0u;
-        const bool eq = j < L && r == prefix;
-        uint32_t total;
-        const uint32_t t = ties + block_scan(eq, s.warp, total);
-        ties += total;
-        const bool kept = j < L && (r > prefix || (eq && t < need));
-        const bool hole = j < n && !kept, mover = j >= n && kept;
-        const uint32_t at = block_scan((uint32_t)hole | (uint32_t)mover << 16, s.warp2, total);
-        if (hole) moves[1 + 2 * (holes + (at & 0xffff))] = j;
-        if (mover) moves[2 + 2 * (movers + (at >> 16))] = j;
-        holes += total & 0xffff;
-        movers += total >> 16;
-        if (j < L && j < n ? kept : j < L && !mover) {
-            const float x = w[j];
-            const int p = pos[j];
-            w_out[j] = j < n ? x : 0.f;
-            pos_out[j] = j < n ? p : -1;
+    // In order: ranks above `prefix` stay, and the first `need` that equal it.  Warp w takes slots [from, to).
+    const int run = ((L + 31) / 32 + 31) / 32 * 32, from = min(warp * run, L), to = min(from + run, L);
+    uint32_t ties = 0, holes = 0, movers = 0, total;
+    for (int j0 = from; j0 < to; j0 += 32) {
+        const int j = j0 + lane;
+        ties += __popc(__ballot_sync(0xffffffffu, j < to && rank(j) == prefix));
+    }
+    const uint32_t ties0 = warps_before(ties, s.warp[0], total), below = (1u << lane) - 1;
+    auto kept = [&](int j, uint32_t &t) {          // by a whole warp; t: ties so far
+        const uint32_t r = j < to ? rank(j) : 0u;
+        const uint32_t eq = __ballot_sync(0xffffffffu, j < to && r == prefix);
+        const bool k = j < to && (r > prefix || (r == prefix && t + __popc(eq & below) < need));
+        t += __popc(eq);
+        return k;
+    };
+    uint32_t t = ties0;
+    for (int j0 = from; j0 < to; j0 += 32) {
+        const int j = j0 + lane;
+        const bool k = kept(j, t);
+        holes += __popc(__ballot_sync(0xffffffffu, j < n && j < to && !k));
+        movers += __popc(__ballot_sync(0xffffffffu, j >= n && k));
+    }
+    uint32_t hole = warps_before(holes, s.warp[1], total), mover = warps_before(movers, s.warp[2], holes);
+    t = ties0;
+#pragma unroll 2
+    for (int j0 = from; j0 < to; j0 += 32) {
+        const int j = j0 + lane;
+        const bool k = kept(j, t);
+        const uint32_t hb = __ballot_sync(0xffffffffu, j < n && j < to && !k);
+        const uint32_t mb = __ballot_sync(0xffffffffu, j >= n && k);
+        if (hb >> lane & 1) moves[1 + 2 * (hole + __popc(hb & below))] = j;
+        if (mb >> lane & 1) moves[2 + 2 * (mover + __popc(mb & below))] = j;
+        hole += __popc(hb);
+        mover += __popc(mb);
+        if (j < n ? k : j < to && !k) {
+            const float x = j < n ? w[j] : 0.f;
+            const int p = j < n ? pos[j] : -1;
+            w_out[j] = x;
+            pos_out[j] = p;
         }
     }
     for (int j = L + tid; j < a.C; j += kSelThreads) {

@@ -221,7 +221,7 @@ struct CacheAttnArgs {
     float scale;
     int *status;
 };
-size_t cache_attn_workspace(int G, int T, int d);
+size_t cache_attn_workspace(int B, int H, int G, int T, int C, int d, bool weights);
 cudaError_t launch_cache_attn(const CacheAttnArgs &a, cudaStream_t stream);
 
 struct EvictArgs {

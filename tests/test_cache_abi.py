@@ -52,8 +52,8 @@ def test_append_argument_errors(lib):
 
 
 def test_attention_argument_errors(lib):
-    need = sa.attn_cache_attention_workspace_size(2, 2, 3, 4, 40, 64)
-    assert need > 0
+    need = sa.attn_cache_attention_workspace_size(2, 2, 3, 4, 40, 64, True)
+    assert need > sa.attn_cache_attention_workspace_size(2, 2, 3, 4, 40, 64) > 0
 
     def att(q=A[0], k=A[1], v=A[2], n=A[3], t=A[4], c=A[5], w=A[6], wo=A[7], o=A[8], l=A[9], ws=A[10], nb=need, B=2, H=2,
             G=3, T=4, C=40, d=64, scale=0.125):
