@@ -5,12 +5,14 @@
 // ones before n, both in ascending order, so that sources and targets never meet, every move can run at once
 // and a slot that stays in place costs nothing but its rank.
 //
-// select_kernel: one block a sequence and head.  A slot's rank is its weight's bits (weights count as zero where
-// they are negative or NaN), all ones for the newest positions.  The n-th largest rank is found by three
-// histograms of 11, 11 and 10 bits over ranks that stay in shared memory (from L2 where they do not fit).  Then each
-// warp takes a run of neighbouring slots and numbers its ties, its holes and its movers by ballots, with one sum over
-// the warps in between: in order without a barrier a step.  move_kernel: the rows, 16 bytes a lane, over the whole
-// GPU.
+// select_kernel: a cluster of 1 to 8 blocks a sequence and head, each with a run of its slots; more where the blocks
+// fill the GPU no better (one pass over a slot is some 30 instructions a warp, and there are seven: 16384 slots of 32
+// heads take 35 us by single blocks).  A slot's rank is its weight's bits (weights count as zero where they are
+// negative or NaN), all ones for the newest positions.  The n-th largest rank is found by three histograms of 11, 11
+// and 10 bits over ranks that stay in shared memory (from L2 where they do not fit), each added up over the cluster.
+// Then each warp takes a run of neighbouring slots and numbers its ties, its holes and its movers by ballots, with
+// sums over the warps and the cluster in between: in order without a barrier a step.  move_kernel: the rows, 16 bytes
+// a lane, over the whole GPU.
 // Bound by HBM (8 bytes a slot, 8 d a moved slot) once there are enough sequences and heads, by the select's
 // latency before.
 #include "cluster.cuh"
@@ -21,14 +23,16 @@ namespace {
 
 constexpr int kSelThreads = 1024;
 constexpr int kBins = 2048;
-constexpr int kMaxInSmem = 48 * 1024;    // ranks kept in shared memory (192 KB)
+constexpr int kMaxInSmem = 48 * 1024;    // ranks a block keeps in shared memory (192 KB)
+constexpr int kPlanSms = 152;
 constexpr int kMoveRows = 32;            // moves a block of move_kernel takes
 
 struct SelShared {
-    uint32_t bins[kBins];
-    uint32_t warp[3][32];
+    uint32_t bins[3][kBins];             // of each pass
+    uint32_t warp[4][32];
     uint32_t prefix;                     // rank bits found so far
     uint32_t need;                       // how many are still to be taken among those with this prefix
+    uint32_t sums[4];                    // this block's, read by the others: newest, ties, holes, movers
 };
 
 // Sum over the lanes before this one and this one.
@@ -59,13 +63,14 @@ __device__ __forceinline__ uint32_t rank_of(float w, int pos, long long oldest)
     return w > 0.f ? __float_as_uint(w) : 0u;
 }
 
-__global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int stride, int in_smem)
+__global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int stride, int in_smem, int blocks)
 {
     extern __shared__ __align__(16) uint32_t ranks[];
     __shared__ SelShared s;
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, bh = blockIdx.x, b = bh / a.H;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, bh = blockIdx.x / blocks, b = bh / a.H;
+    const int me = blockIdx.x % blocks;          // (= the rank in the cluster)
     const int L = min(max(a.lengths[b], 0), a.C), n = min(L, a.keep);
     const long long row = (long long)bh * a.C;
     const float *w = a.weights + row;
@@ -73,66 +78,94 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int st
     float *w_out = a.weights_out + row;
     int *pos_out = a.positions_out + row;
     int *moves = a.moves + (long long)bh * stride;
-    if (bh % a.H == 0 && tid == 0) a.lengths_out[b] = n;
+    if (bh % a.H == 0 && me == 0 && tid == 0) a.lengths_out[b] = n;
     // what lies behind the kept slots is empty; sources of moves are emptied by those who read them
     if (n == L) {
 #pragma unroll 4
-        for (int j = tid; j < a.C; j += kSelThreads) {
+        for (int j = me * kSelThreads + tid; j < a.C; j += blocks * kSelThreads) {
             const float x = j < n ? w[j] : 0.f;
             const int p = j < n ? pos[j] : -1;
             w_out[j] = x;
             pos_out[j] = p;
         }
-        if (tid == 0) moves[0] = 0;
+        if (me == 0 && tid == 0) moves[0] = 0;
         return;
     }
+    const int share = ((L + blocks - 1) / blocks + 31) / 32 * 32;       // slots [begin, end) are this block's
+    const int begin = min(me * share, L), end = min(begin + share, L);
+    auto sync = [&] {
+        if (blocks > 1) ptx::cluster_sync();
+        else __syncthreads();
+    };
+    auto other = [&](const void *p, int block) { return ptx::cluster_addr(ptx::smem_u32(p), (uint32_t)block); };
+    // the sum of the others' s.sums[i] ahead of this block's, and over all
+    auto blocks_before = [&](int i, uint32_t &total) {
+        uint32_t before = 0;
+        total = 0;
+        for (int k = 0; k < blocks; ++k) {
+            const uint32_t x = blocks > 1 ? ptx::ld_cluster_b32(other(&s.sums[i], k)) : s.sums[i];
+            total += x;
+            before += k < me ? x : 0;
+        }
+        return before;
+    };
 
     // the newest position
-    for (int i = tid; i < kBins; i += kSelThreads) s.bins[i] = 0;
+    for (int i = tid; i < 3 * kBins; i += kSelThreads) (&s.bins[0][0])[i] = 0;
     int newest = INT32_MIN;
 #pragma unroll 8
-    for (int j = tid; j < L; j += kSelThreads) newest = max(newest, pos[j]);
+    for (int j = begin + tid; j < end; j += kSelThreads) newest = max(newest, pos[j]);
     newest = __reduce_max_sync(0xffffffffu, newest);
     if (lane == 0) s.warp[0][warp] = (uint32_t)newest;
     __syncthreads();
     newest = __reduce_max_sync(0xffffffffu, (int)s.warp[0][lane]);
+    if (blocks > 1) {
+        if (tid == 0) s.sums[0] = (uint32_t)newest;
+        ptx::cluster_sync();
+        for (int k = 0; k < blocks; ++k) newest = max(newest, (int)ptx::ld_cluster_b32(other(&s.sums[0], k)));
+    }
     const long long oldest = (long long)newest - a.recent;   // positions above it are safe
-    auto rank = [&](int j) { return in_smem ? ranks[j] : rank_of(w[j], pos[j], oldest); };
+    auto rank = [&](int j) { return in_smem ? ranks[j - begin] : rank_of(w[j], pos[j], oldest); };
 
     // the n-th largest rank
     uint32_t prefix = 0, need = (uint32_t)n;
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
         const uint32_t mask = pass == 0 ? 0u : 0xffffffffu << (shift + bits);
+        uint32_t *bins = s.bins[pass];
         auto count = [&](uint32_t r, bool there) {
             const uint32_t bin = there && (r & mask) == prefix ? r >> shift & ((1u << bits) - 1) : 0xffffffffu;
             // ties (zeros, the newest) often fill a warp: one addition for all of them
             const uint32_t b0 = __shfl_sync(0xffffffffu, bin, 0);
             if (__all_sync(0xffffffffu, bin == b0)) {
-                if (lane == 0 && bin != 0xffffffffu) atomicAdd(&s.bins[bin], 32u);
+                if (lane == 0 && bin != 0xffffffffu) atomicAdd(&bins[bin], 32u);
             } else if (bin != 0xffffffffu) {
-                atomicAdd(&s.bins[bin], 1u);
+                atomicAdd(&bins[bin], 1u);
             }
         };
         if (pass == 0) {
 #pragma unroll 4
-            for (int j0 = 0; j0 < L; j0 += kSelThreads) {
+            for (int j0 = begin; j0 < end; j0 += kSelThreads) {
                 const int j = j0 + tid;
-                const uint32_t r = j < L ? rank_of(w[j], pos[j], oldest) : 0u;
-                if (in_smem && j < L) ranks[j] = r;
-                count(r, j < L);
+                const uint32_t r = j < end ? rank_of(w[j], pos[j], oldest) : 0u;
+                if (in_smem && j < end) ranks[j - begin] = r;
+                count(r, j < end);
             }
         } else {
-            for (int j0 = 0; j0 < L; j0 += kSelThreads) {
+            for (int j0 = begin; j0 < end; j0 += kSelThreads) {
                 const int j = j0 + tid;
-                count(j < L ? rank(j) : 0u, j < L);
+                count(j < end ? rank(j) : 0u, j < end);
             }
         }
-        __syncthreads();
+        sync();
         // bins from the top: thread t holds bins 2 (1023 - t) + 1 and 2 (1023 - t)
         const int top = 2 * (kSelThreads - 1 - tid) + 1;
-        const uint32_t c1 = s.bins[top], c0 = s.bins[top - 1];
-        s.bins[top] = s.bins[top - 1] = 0;                 // for the next pass
+        uint32_t c1 = bins[top], c0 = bins[top - 1];
+        for (int k = 1; k < blocks; ++k) {
+            const uint2 c = ptx::ld_cluster_b64(other(&bins[top - 1], (me + k) % blocks));
+            c0 += c.x;
+            c1 += c.y;
+        }
         const uint32_t inc = warp_scan(c0 + c1, lane);
         uint32_t total;
         const uint32_t above =
@@ -147,14 +180,20 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int st
         need = s.need;
     }
 
-    // In order: ranks above `prefix` stay, and the first `need` that equal it.  Warp w takes slots [from, to).
-    const int run = ((L + 31) / 32 + 31) / 32 * 32, from = min(warp * run, L), to = min(from + run, L);
+    // In order: ranks above `prefix` stay, and the first `need` that equal it.  A warp takes slots [from, to).
+    const int run = (end - begin + 1023) / 1024 * 32, from = min(begin + warp * run, end), to = min(from + run, end);
     uint32_t ties = 0, holes = 0, movers = 0, total;
     for (int j0 = from; j0 < to; j0 += 32) {
         const int j = j0 + lane;
         ties += __popc(__ballot_sync(0xffffffffu, j < to && rank(j) == prefix));
     }
-    const uint32_t ties0 = warps_before(ties, s.warp[0], total), below = (1u << lane) - 1;
+    uint32_t ties0 = warps_before(ties, s.warp[0], total);
+    if (blocks > 1) {
+        if (tid == 0) s.sums[1] = total;
+        ptx::cluster_sync();
+        ties0 += blocks_before(1, total);
+    }
+    const uint32_t below = (1u << lane) - 1;
     auto kept = [&](int j, uint32_t &t) {          // by a whole warp; t: ties so far
         const uint32_t r = j < to ? rank(j) : 0u;
         const uint32_t eq = __ballot_sync(0xffffffffu, j < to && r == prefix);
@@ -169,7 +208,17 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int st
         holes += __popc(__ballot_sync(0xffffffffu, j < n && j < to && !k));
         movers += __popc(__ballot_sync(0xffffffffu, j >= n && k));
     }
-    uint32_t hole = warps_before(holes, s.warp[1], total), mover = warps_before(movers, s.warp[2], holes);
+    uint32_t hole = warps_before(holes, s.warp[2], total), mover = warps_before(movers, s.warp[3], movers);
+    if (blocks > 1) {
+        if (tid == 0) {
+            s.sums[2] = total;
+            s.sums[3] = movers;
+        }
+        ptx::cluster_sync();
+        mover += blocks_before(3, movers);
+        hole += blocks_before(2, total);
+    }
+    if (me == 0 && tid == 0) moves[0] = (int)total;
     t = ties0;
 #pragma unroll 2
     for (int j0 = from; j0 < to; j0 += 32) {
@@ -177,8 +226,8 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int st
         const bool k = kept(j, t);
         const uint32_t hb = __ballot_sync(0xffffffffu, j < n && j < to && !k);
         const uint32_t mb = __ballot_sync(0xffffffffu, j >= n && k);
-        if (hb >> lane & 1) moves[1 + 2 * (hole + __popc(hb & below))] = j;
-        if (mb >> lane & 1) moves[2 + 2 * (mover + __popc(mb & below))] = j;
+        if (hb >> lane & 1) moves[2 + 2 * (hole + __popc(hb & below))] = j;
+        if (mb >> lane & 1) moves[3 + 2 * (mover + __popc(mb & below))] = j;
         hole += __popc(hb);
         mover += __popc(mb);
         if (j < n ? k : j < to && !k) {
@@ -188,11 +237,11 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int st
             pos_out[j] = p;
         }
     }
-    for (int j = L + tid; j < a.C; j += kSelThreads) {
+    for (int j = L + me * kSelThreads + tid; j < a.C; j += blocks * kSelThreads) {
         w_out[j] = 0.f;
         pos_out[j] = -1;
     }
-    if (tid == 0) moves[0] = (int)holes;
+    if (blocks > 1) ptx::cluster_sync_relaxed();     // nobody leaves while its sums are read
 }
 
 // LANES lanes a row of d = 8 LANES columns.
@@ -204,15 +253,28 @@ __global__ void __launch_bounds__(256) move_kernel(EvictArgs a, int stride, int 
     const int bh = blockIdx.x / blocks, lane = threadIdx.x % LANES;
     const int *moves = a.moves + (long long)bh * stride;
     const int count = moves[0], first = blockIdx.x % blocks * kMoveRows;
-    const int last = min(first + kMoveRows, count);
     const long long row = (long long)bh * a.C;
     uint4 *k = static_cast<uint4 *>(a.k) + row * LANES, *v = static_cast<uint4 *>(a.v) + row * LANES;
-    constexpr int STEP = 256 / LANES;
-    for (int m = first + threadIdx.x / LANES; m < last; m += STEP) {
-        const long long dst = moves[1 + 2 * m], src = moves[2 + 2 * m];
-        const uint4 x = k[src * LANES + lane], y = v[src * LANES + lane];
-        k[dst * LANES + lane] = x;
-        v[dst * LANES + lane] = y;
+    constexpr int STEP = 256 / LANES, N = kMoveRows / STEP;
+    int2 at[N];                                     // (to, from)
+    uint4 x[N], y[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int m = first + i * STEP + threadIdx.x / LANES;
+        at[i] = m < count ? *reinterpret_cast<const int2 *>(moves + 2 + 2 * m) : make_int2(-1, -1);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (at[i].x >= 0) {
+            x[i] = k[(long long)at[i].y * LANES + lane];
+            y[i] = v[(long long)at[i].y * LANES + lane];
+        }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if (at[i].x < 0) continue;
+        const long long dst = at[i].x, src = at[i].y;
+        k[dst * LANES + lane] = x[i];
+        v[dst * LANES + lane] = y[i];
         if (lane == 0) {
             a.weights_out[row + dst] = a.weights[row + src];
             a.weights_out[row + src] = 0.f;
@@ -225,7 +287,15 @@ __global__ void __launch_bounds__(256) move_kernel(EvictArgs a, int stride, int 
 }
 
 int most_moves(int C, int keep) { return keep < C - keep ? keep : C - keep > 0 ? C - keep : 0; }
-int moves_stride(int C, int keep) { return (1 + 2 * most_moves(C, keep) + 3) / 4 * 4; }
+int moves_stride(int C, int keep) { return (2 + 2 * most_moves(C, keep) + 3) / 4 * 4; }
+
+// Blocks of select_kernel a sequence and head: as many as keep the GPU's SMs from idling, 1024 slots each at least.
+int select_blocks(int heads, int C)
+{
+    int n = 1;
+    while (n < 8 && (long long)heads * n * 2 <= kPlanSms && C / (n * 2) >= 1024) n *= 2;
+    return n;
+}
 
 }  // namespace
 
@@ -233,13 +303,14 @@ size_t evict_workspace(int B, int H, int C, int keep) { return (size_t)B * H * m
 
 cudaError_t launch_evict(const EvictArgs &a, cudaStream_t stream)
 {
-    const int in_smem = a.C <= kMaxInSmem, bytes = in_smem ? (a.C + 3) / 4 * 16 : 0;
+    const int split = select_blocks(a.B * a.H, a.C), share = (a.C + split - 1) / split + 32;
+    const int in_smem = share <= kMaxInSmem, bytes = in_smem ? (share + 3) / 4 * 16 : 0;
     const int stride = moves_stride(a.C, a.keep);
     static std::atomic<bool> set[64];
     cudaError_t e = raise_smem(reinterpret_cast<const void *>(select_kernel), kMaxInSmem * 4, set);
     if (e != cudaSuccess) return e;
-    e = launch_overlapped(select_kernel, dim3((unsigned)(a.B * a.H)), dim3(kSelThreads), (size_t)bytes, 1, stream, a,
-                          stride, in_smem);
+    e = launch_overlapped(select_kernel, dim3((unsigned)(a.B * a.H * split)), dim3(kSelThreads), (size_t)bytes,
+                          (unsigned)split, stream, a, stride, in_smem, split);
     const int most = most_moves(a.C, a.keep);
     if (e != cudaSuccess || most == 0) return e;
     const int blocks = (most + kMoveRows - 1) / kMoveRows;     // a sequence and head

@@ -161,6 +161,20 @@ __device__ __forceinline__ void st_cluster_b32(uint32_t addr, uint32_t v)
     asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
+__device__ __forceinline__ uint32_t ld_cluster_b32(uint32_t addr)
+{
+    uint32_t v;
+    asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint2 ld_cluster_b64(uint32_t addr)
+{
+    uint2 v;
+    asm volatile("ld.shared::cluster.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+
 }  // namespace ptx
 
 // Four fp32 from shared memory, as two pairs.

@@ -117,12 +117,14 @@ def evict(k, v, weights, positions, lengths, keep, recent):
         for h in range(H):
             newest = max(pos[b, h, :L].tolist(), default=0)
 
+            wt, at = w[b, h].tolist(), pos[b, h].tolist()
+
             def rank(j):
-                x = float(w[b, h, j])
-                return (int(pos[b, h, j]) <= newest - recent, -(x if x > 0 else 0.0) if int(pos[b, h, j]) <=
-                        newest - recent else 0.0, j)
+                old = at[j] <= newest - recent
+                return old, -(wt[j] if wt[j] > 0 else 0.0) if old else 0.0, j
             stay = sorted(range(L), key=rank)[:n]
-            to = [j for j in range(n) if j not in set(stay)]
+            gone = set(range(n)) - set(stay)
+            to = sorted(gone)
             of = sorted(j for j in stay if j >= n)
             for t in (k, v, w, pos):
                 t[b, h, to] = t[b, h, of].clone()

@@ -368,7 +368,9 @@ def _check_evict(k, v, w, pos, lens, keep, recent, in_place=False):
     (1, 1, 1, 64, [1], 1, 0), (1, 1, 2, 128, [2], 1, 1), (1, 1, 2, 64, [2], 1, 0),
     (3, 2, 100, 64, [100, 64, 3], 64, 10), (2, 3, 1025, 128, [1025, 1000], 1000, 100),
     (2, 1, 5000, 64, [5000, 4097], 33, 33), (4, 2, 300, 128, [0, 300, 1, 77], 76, 0),
-    (1, 2, 2500, 64, [2500], 2499, 1), (1, 1, 3000, 128, [2999], 1500, 700), (2, 2, 40, 64, [40, 39], 50, 50)])
+    (1, 2, 2500, 64, [2500], 2499, 1), (1, 1, 3000, 128, [2999], 1500, 700), (2, 2, 40, 64, [40, 39], 50, 50),
+    (1, 1, 20000, 64, [19999], 9000, 100), (3, 4, 9000, 128, [9000, 1000, 8123], 999, 998), (10, 5, 4200, 64, [4200 - 7 * i for i in range(10)], 4100, 1),
+    (30, 5, 1100, 64, [1100] * 30, 1000, 5), (1, 3, 16400, 128, [5], 3, 1)])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_evict(B, H, C, d, lens, keep, recent, in_place):
     g = _gen(B, H, C, lens, keep, recent, in_place)
@@ -393,10 +395,9 @@ def test_evict_ties_and_odd_weights():
 def test_evict_of_a_long_cache():
     """More slots than fit shared memory."""
     g = _gen("long")
-    B, H, C, d = 1, 2, 60001, 64
-    k, v, w, pos = _evict_case(g, B, H, C, d)
-    for in_place in (False, True):
-        _check_evict(k.clone(), v.clone(), w.clone(), pos.clone(), [60001], 20000, 999, in_place)
+    for B, H, C, in_place in ((1, 1, 400001, False), (1, 1, 400001, True), (1, 77, 49999, True)):
+        k, v, w, pos = _evict_case(g, B, H, C, 64)           # by 8 blocks a head, by one
+        _check_evict(k, v, w, pos, [C] * B, 20000, 999, in_place)
 
 
 def test_evict_leaves_the_rest():
