@@ -98,23 +98,34 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int st
         else __syncthreads();
     };
     auto other = [&](const void *p, int block) { return ptx::cluster_addr(ptx::smem_u32(p), (uint32_t)block); };
-    // the sum of the others' s.sums[i] ahead of this block's, and over all
+    // the sum of the others' s.sums[i] ahead of this block's, and over all; lane k reads block k's
     auto blocks_before = [&](int i, uint32_t &total) {
-        uint32_t before = 0;
-        total = 0;
-        for (int k = 0; k < blocks; ++k) {
-            const uint32_t x = blocks > 1 ? ptx::ld_cluster_b32(other(&s.sums[i], k)) : s.sums[i];
-            total += x;
-            before += k < me ? x : 0;
-        }
-        return before;
+        const uint32_t x = lane < blocks ? ptx::ld_cluster_b32(other(&s.sums[i], lane)) : 0u;
+        total = __reduce_add_sync(0xffffffffu, x);
+        return __reduce_add_sync(0xffffffffu, lane < me ? x : 0u);
     };
 
     // the newest position
     for (int i = tid; i < 3 * kBins; i += kSelThreads) (&s.bins[0][0])[i] = 0;
     int newest = INT32_MIN;
+    // up to 4096 slots wait in registers for the newest position, more are read again
+    constexpr int HELD = 4;
+    const bool held = in_smem && share <= HELD * kSelThreads;
+    float wr[HELD];
+    int pr[HELD];
+    if (held) {
+#pragma unroll
+        for (int e = 0; e < HELD; ++e) {
+            const int j = begin + e * kSelThreads + tid;
+            wr[e] = j < end ? w[j] : 0.f;
+            pr[e] = j < end ? pos[j] : INT32_MIN;
+        }
+#pragma unroll
+        for (int e = 0; e < HELD; ++e) newest = max(newest, pr[e]);
+    } else {
 #pragma unroll 8
-    for (int j = begin + tid; j < end; j += kSelThreads) newest = max(newest, pos[j]);
+        for (int j = begin + tid; j < end; j += kSelThreads) newest = max(newest, pos[j]);
+    }
     newest = __reduce_max_sync(0xffffffffu, newest);
     if (lane == 0) s.warp[0][warp] = (uint32_t)newest;
     __syncthreads();
@@ -122,7 +133,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int st
     if (blocks > 1) {
         if (tid == 0) s.sums[0] = (uint32_t)newest;
         ptx::cluster_sync();
-        for (int k = 0; k < blocks; ++k) newest = max(newest, (int)ptx::ld_cluster_b32(other(&s.sums[0], k)));
+        newest = __reduce_max_sync(0xffffffffu, lane < blocks ? (int)ptx::ld_cluster_b32(other(&s.sums[0], lane)) : newest);
     }
     const long long oldest = (long long)newest - a.recent;   // positions above it are safe
     auto rank = [&](int j) { return in_smem ? ranks[j - begin] : rank_of(w[j], pos[j], oldest); };
@@ -143,7 +154,15 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int st
                 atomicAdd(&bins[bin], 1u);
             }
         };
-        if (pass == 0) {
+        if (pass == 0 && held) {
+#pragma unroll
+            for (int e = 0; e < HELD; ++e) {
+                const int j = begin + e * kSelThreads + tid;
+                const uint32_t r = rank_of(wr[e], pr[e], oldest);
+                if (j < end) ranks[j - begin] = r;
+                if (begin + e * kSelThreads < end) count(r, j < end);
+            }
+        } else if (pass == 0) {
 #pragma unroll 4
             for (int j0 = begin; j0 < end; j0 += kSelThreads) {
                 const int j = j0 + tid;
@@ -161,10 +180,16 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int st
         // bins from the top: thread t holds bins 2 (1023 - t) + 1 and 2 (1023 - t)
         const int top = 2 * (kSelThreads - 1 - tid) + 1;
         uint32_t c1 = bins[top], c0 = bins[top - 1];
-        for (int k = 1; k < blocks; ++k) {
-            const uint2 c = ptx::ld_cluster_b64(other(&bins[top - 1], (me + k) % blocks));
-            c0 += c.x;
-            c1 += c.y;
+        if (blocks > 1) {
+            uint2 c[7];
+#pragma unroll
+            for (int k = 1; k < 8; ++k)
+                c[k - 1] = k < blocks ? ptx::ld_cluster_b64(other(&bins[top - 1], me ^ k)) : make_uint2(0, 0);
+#pragma unroll
+            for (int k = 0; k < 7; ++k) {
+                c0 += c[k].x;
+                c1 += c[k].y;
+            }
         }
         const uint32_t inc = warp_scan(c0 + c1, lane);
         uint32_t total;

@@ -398,6 +398,8 @@ def test_evict_of_a_long_cache():
     for B, H, C, in_place in ((1, 1, 400001, False), (1, 1, 400001, True), (1, 77, 49999, True)):
         k, v, w, pos = _evict_case(g, B, H, C, 64)           # by 8 blocks a head, by one
         _check_evict(k, v, w, pos, [C] * B, 20000, 999, in_place)
+    k, v, w, pos = _evict_case(g, 1, 2, 400001, 64)          # few slots in use of many
+    _check_evict(k, v, w, pos, [3000], 2000, 99)
 
 
 def test_evict_leaves_the_rest():
