@@ -24,6 +24,7 @@
 #include "cluster.cuh"
 #include "common.cuh"
 #include "kernels.h"
+#include <cstdlib>
 
 namespace attn {
 namespace {
@@ -217,77 +218,20 @@ struct Parts {
     float *scores;     // null, or [B H][G T][C]: scores times log2 e, -infinity where a row does not see a slot
 };
 
+// A warp's state: 8 NT rows of one unit against 16 slots a step.
 template <int D, int NT>
-struct FewSmem {
-    float o[kFewWarps][8 * NT][D + 4];
-    float m[kFewWarps][8 * NT], l[kFewWarps][8 * NT];
-};
+struct Rows {
+    static constexpr int KC = D / 32;           // chunks of a K row a thread holds
+    static constexpr int VC = D / 64;           // chunks of a V row a thread holds
+    static constexpr int MT = D / 16;           // 16-row tiles of O^T
+    uint4 qf[NT][KC], kr[2][KC], vr[4][VC];
+    float acc[NT][MT][4], m[NT][2], l[NT][2], s[NT][4];
+    int g, q;
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) few_kernel(CacheAttnArgs a, Plan plan, Parts parts)
-{
-    constexpr int KC = D / 32;           // chunks of a K row a thread holds
-    constexpr int VC = D / 64;           // chunks of a V row a thread holds
-    constexpr int MT = D / 16;           // 16-row tiles of O^T
-    constexpr int R8 = 8 * NT;
-    __shared__ FewSmem<D, NT> sm;
-    ptx::grid_dep_launch();
-    ptx::grid_dep_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
-    const int T = a.T, R = a.G * T;
+    __device__ __forceinline__ Rows() : g((threadIdx.x & 31) >> 2), q(threadIdx.x & 3) {}
 
-    Walk walk;
-    if (!walk.begin(a.lengths, a.B, plan)) return;
-    const float to_log2 = a.scale * kLog2e;
-    Segment seg;
-    walk.next(a.lengths, plan, seg);
-
-    // Q's rows as the 8-column operand
-    uint4 qf[NT][KC];
-    auto load_q = [&](const Segment &s) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const int r = s.tile * R8 + 8 * t + g;
-            const uint4 *qp = static_cast<const uint4 *>(a.q) + (s.head * R + r) * (D / 8);
-#pragma unroll
-            for (int c = 0; c < KC; ++c) qf[t][c] = r < R ? qp[4 * c + q] : make_uint4(0, 0, 0, 0);
-        }
-    };
-    uint4 kr[2][KC], vr[4][VC];
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    // 16 slots from `key` on; those behind the last one read as zeros, whatever lies there
-    auto load_k = [&](const Segment &s, int key) {
-        const uint4 *kp = static_cast<const uint4 *>(a.k) + (s.head * a.C + key + g) * (D / 8) + q;
-        const int left = s.length + T - key - g;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int c = 0; c < KC; ++c) kr[i][c] = 8 * i < left ? stream16(kp + i * D + 4 * c) : zero;
-    };
-    auto load_v = [&](const Segment &s, int key) {
-        const uint4 *vp = static_cast<const uint4 *>(a.v) + (s.head * a.C + key + 2 * q) * (D / 8) + g;
-        const int left = s.length + T - key - 2 * q;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int c = 0; c < VC; ++c) {
-                const int j = (i & 1) + 8 * (i >> 1);
-                vr[i][c] = j < left ? stream16(vp + j * (D / 8) + 8 * c) : zero;
-            }
-    };
-    load_k(seg, seg.first * kBlock + 16 * warp);
-    load_q(seg);
-    load_v(seg, seg.first * kBlock + 16 * warp);
-
-    while (seg.there) {
-        const int length = seg.length, first = seg.first, last = seg.last, nb = seg.nb, b = seg.b;
-        const long long head = seg.head;
-        const int r0 = seg.tile * R8;
-        Segment nxt;
-        walk.next(a.lengths, plan, nxt);
-
-        float acc[NT][MT][4];
-        float m[NT][2], l[NT][2];
+    __device__ __forceinline__ void clear()
+    {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             m[t][0] = m[t][1] = -INFINITY;
@@ -295,161 +239,201 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) few_kernel(Cache
 #pragma unroll
             for (int i = 0; i < MT; ++i) acc[t][i][0] = acc[t][i][1] = acc[t][i][2] = acc[t][i][3] = 0.f;
         }
-
-        int key = first * kBlock + 16 * warp;
-        // A warp's steps; its share of the last block may be empty, and then the loads ahead are the next segment's.
-        for (; key < last * kBlock; key += kBlock) {
-            const bool more = key + kBlock < last * kBlock;
-            float s[NT][4];
+    }
+    // Q's rows from r0 on as the 8-column operand
+    __device__ __forceinline__ void load_q(const CacheAttnArgs &a, long long head, int r0)
+    {
+        const int R = a.G * a.T;
 #pragma unroll
-            for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+        for (int t = 0; t < NT; ++t) {
+            const int r = r0 + 8 * t + g;
+            const uint4 *qp = static_cast<const uint4 *>(a.q) + (head * R + r) * (D / 8);
 #pragma unroll
-            for (int c = 0; c < KC; ++c) {
-                const uint32_t a0[4] = {kr[0][c].x, kr[1][c].x, kr[0][c].y, kr[1][c].y};
-                const uint32_t a1[4] = {kr[0][c].z, kr[1][c].z, kr[0][c].w, kr[1][c].w};
+            for (int c = 0; c < KC; ++c) qf[t][c] = r < R ? qp[4 * c + q] : make_uint4(0, 0, 0, 0);
+        }
+    }
+    // 16 slots from `key` on; those from `valid` on read as zeros, whatever lies there
+    __device__ __forceinline__ void load_k(const CacheAttnArgs &a, long long head, int key, int valid)
+    {
+        const uint4 *kp = static_cast<const uint4 *>(a.k) + (head * a.C + key + g) * (D / 8) + q;
+        const int left = valid - key - g;
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    mma16816(s[t], a0, qf[t][c].x, qf[t][c].y);
-                    mma16816(s[t], a1, qf[t][c].z, qf[t][c].w);
-                }
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int c = 0; c < KC; ++c) kr[i][c] = 8 * i < left ? stream16(kp + i * D + 4 * c) : make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void load_v(const CacheAttnArgs &a, long long head, int key, int valid)
+    {
+        const uint4 *vp = static_cast<const uint4 *>(a.v) + (head * a.C + key + 2 * q) * (D / 8) + g;
+        const int left = valid - key - 2 * q;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < VC; ++c) {
+                const int j = (i & 1) + 8 * (i >> 1);
+                vr[i][c] = j < left ? stream16(vp + j * (D / 8) + 8 * c) : make_uint4(0, 0, 0, 0);
             }
-            if (more) {
-                load_k(seg, key + kBlock);
-            } else if (nxt.there) {
-                load_k(nxt, nxt.first * kBlock + 16 * warp);
-                load_q(nxt);
-            }
-
-            const bool tail = key + 16 > length;
+    }
+    // V's rows from `valid` on as zeros, where they were loaded before that was known
+    __device__ __forceinline__ void drop_behind(int key, int valid)
+    {
+        const int left = valid - key - 2 * q;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < VC; ++c)
+                if ((i & 1) + 8 * (i >> 1) >= left) vr[i][c] = make_uint4(0, 0, 0, 0);
+    }
+    // S^T = K Q^T: K is free afterwards
+    __device__ __forceinline__ void scores()
+    {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+#pragma unroll
+        for (int c = 0; c < KC; ++c) {
+            const uint32_t a0[4] = {kr[0][c].x, kr[1][c].x, kr[0][c].y, kr[1][c].y};
+            const uint32_t a1[4] = {kr[0][c].z, kr[1][c].z, kr[0][c].w, kr[1][c].w};
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
+                mma16816(s[t], a0, qf[t][c].x, qf[t][c].y);
+                mma16816(s[t], a1, qf[t][c].z, qf[t][c].w);
+            }
+        }
+    }
+    // The rest of the step at `key`: weights, and O^T += V^T P^T; V is free afterwards.  kept: see Parts::scores
+    __device__ __forceinline__ void step(const CacheAttnArgs &a, long long head, int b, int r0, int key, int length,
+                                         float to_log2, float *kept)
+    {
+        const int T = a.T, R = a.G * T;
+        const bool tail = key + 16 > length;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[t][e] *= to_log2;
-                if (tail) {
+        for (int t = 0; t < NT; ++t) {
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int r = r0 + 8 * t + 2 * q + e;
-                        const uint64_t word = r < R ? word_of(a.tree, b, T, r % T) : 0;
+            for (int e = 0; e < 4; ++e) s[t][e] *= to_log2;
+            if (tail) {
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int j = key + g + 8 * i - length;
-                            if (j >= 0 && !(j < T && (word >> j & 1))) s[t][e + 2 * i] = -INFINITY;
-                        }
-                    }
-                }
-                if (parts.scores) {
+                for (int e = 0; e < 2; ++e) {
+                    const int r = r0 + 8 * t + 2 * q + e;
+                    const uint64_t word = r < R ? word_of(a.tree, b, T, r % T) : 0;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int r = r0 + 8 * t + 2 * q + (e & 1), j = key + g + 8 * (e >> 1);
-                        if (r < R && j < length + T) parts.scores[(head * R + r) * a.C + j] = s[t][e];
-                    }
-                }
-                // The maximum is brought up to date only where some score exceeds it.
-                const float top[2] = {fmaxf(s[t][0], s[t][2]), fmaxf(s[t][1], s[t][3])};
-                if (__any_sync(0xffffffffu, top[0] > m[t][0] || top[1] > m[t][1])) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float w = fmaxf(m[t][e], top[e]);
-                        w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, 4));
-                        w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, 8));
-                        w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, 16));
-                        const float f = w == -INFINITY ? 1.f : ptx::ex2(m[t][e] - w);
-                        m[t][e] = w;
-                        l[t][e] *= f;
-#pragma unroll
-                        for (int i = 0; i < MT; ++i) {
-                            acc[t][i][e] *= f;
-                            acc[t][i][e + 2] *= f;
-                        }
+                    for (int i = 0; i < 2; ++i) {
+                        const int j = key + g + 8 * i - length;
+                        if (j >= 0 && !(j < T && (word >> j & 1))) s[t][e + 2 * i] = -INFINITY;
                     }
                 }
             }
-            uint32_t ph[NT][2], pl[NT][2];
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                float p[4];
+            if (kept) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float base = m[t][e & 1] == -INFINITY ? 0.f : m[t][e & 1];
-                    p[e] = ptx::ex2(s[t][e] - base);
-                    l[t][e & 1] += p[e];
-                }
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t w = ptx::pack_bf16x2(p[2 * i], p[2 * i + 1]);
-                    ph[t][i] = transpose8x8(w);
-                    pl[t][i] = transpose8x8(ptx::pack_bf16x2(p[2 * i] - lo(w), p[2 * i + 1] - hi(w)));
+                    const int r = r0 + 8 * t + 2 * q + (e & 1), j = key + g + 8 * (e >> 1);
+                    if (r < R && j < length + T) kept[(head * R + r) * a.C + j] = s[t][e];
                 }
             }
-            // A token's value that is not finite may reach the rows that see it alone, but 0 times it is NaN in a
-            // product: such values are added one by one and leave the operand.  Rare, and only among the T tokens.
-            if (tail && T > 1) {
-                bool odd = false;
+            // The maximum is brought up to date only where some score exceeds it.
+            const float top[2] = {fmaxf(s[t][0], s[t][2]), fmaxf(s[t][1], s[t][3])};
+            if (__any_sync(0xffffffffu, top[0] > m[t][0] || top[1] > m[t][1])) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float w = fmaxf(m[t][e], top[e]);
+                    w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, 4));
+                    w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, 8));
+                    w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, 16));
+                    const float f = w == -INFINITY ? 1.f : ptx::ex2(m[t][e] - w);
+                    m[t][e] = w;
+                    l[t][e] *= f;
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) {
+                        acc[t][i][e] *= f;
+                        acc[t][i][e + 2] *= f;
+                    }
+                }
+            }
+        }
+        uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            float p[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float base = m[t][e & 1] == -INFINITY ? 0.f : m[t][e & 1];
+                p[e] = ptx::ex2(s[t][e] - base);
+                l[t][e & 1] += p[e];
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t w = ptx::pack_bf16x2(p[2 * i], p[2 * i + 1]);
+                ph[t][i] = transpose8x8(w);
+                pl[t][i] = transpose8x8(ptx::pack_bf16x2(p[2 * i] - lo(w), p[2 * i + 1] - hi(w)));
+            }
+        }
+        // A token's value that is not finite may reach the rows that see it alone, but 0 times it is NaN in a
+        // product: such values are added one by one and leave the operand.  Rare, and only among the T tokens.
+        if (tail && T > 1) {
+            bool odd = false;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int c = 0; c < VC; ++c)
+                    odd |= key + 2 * q + (i & 1) + 8 * (i >> 1) >= length && any_odd(vr[i][c]);
+            if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    for (int from = 0; from < 4; ++from) {      // slot 2 from + (i & 1) + 8 (i >> 1)
+                        const int j = 2 * from + (i & 1) + 8 * (i >> 1);
+                        if (key + j < length) continue;
+#pragma unroll
+                        for (int c = 0; c < VC; ++c) {
+                            const uint32_t w[4] = {__shfl_sync(0xffffffffu, vr[i][c].x, 4 * g + from),
+                                                   __shfl_sync(0xffffffffu, vr[i][c].y, 4 * g + from),
+                                                   __shfl_sync(0xffffffffu, vr[i][c].z, 4 * g + from),
+                                                   __shfl_sync(0xffffffffu, vr[i][c].w, 4 * g + from)};
+#pragma unroll
+                            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const float seen = __shfl_sync(0xffffffffu, s[t][e + 2 * (i >> 1)], 4 * (j % 8) + q);
+#pragma unroll
+                                    for (int x = 0; x < 8; ++x) {
+                                        const float v = x & 1 ? hi(w[x / 2]) : lo(w[x / 2]);
+                                        if (seen != -INFINITY && odd_value(v))
+                                            acc[t][D == 128 ? x : x & 3][e + 2 * (D == 128 ? c : x >> 2)] += v;
+                                    }
+                                }
+                        }
+                    }
+                }
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int c = 0; c < VC; ++c)
-                        odd |= key + 2 * q + (i & 1) + 8 * (i >> 1) >= length && any_odd(vr[i][c]);
-                if (__any_sync(0xffffffffu, odd)) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        for (int from = 0; from < 4; ++from) {      // slot 2 from + (i & 1) + 8 (i >> 1)
-                            const int j = 2 * from + (i & 1) + 8 * (i >> 1);
-                            if (key + j < length) continue;
-#pragma unroll
-                            for (int c = 0; c < VC; ++c) {
-                                const uint32_t w[4] = {__shfl_sync(0xffffffffu, vr[i][c].x, 4 * g + from),
-                                                       __shfl_sync(0xffffffffu, vr[i][c].y, 4 * g + from),
-                                                       __shfl_sync(0xffffffffu, vr[i][c].z, 4 * g + from),
-                                                       __shfl_sync(0xffffffffu, vr[i][c].w, 4 * g + from)};
-#pragma unroll
-                                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                                    for (int e = 0; e < 2; ++e) {
-                                        const float seen = __shfl_sync(0xffffffffu, s[t][e + 2 * (i >> 1)], 4 * (j % 8) + q);
-#pragma unroll
-                                        for (int x = 0; x < 8; ++x) {
-                                            const float v = x & 1 ? hi(w[x / 2]) : lo(w[x / 2]);
-                                            if (seen != -INFINITY && odd_value(v))
-                                                acc[t][D == 128 ? x : x & 3][e + 2 * (D == 128 ? c : x >> 2)] += v;
-                                        }
-                                    }
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int c = 0; c < VC; ++c)
-                            if (key + 2 * q + (i & 1) + 8 * (i >> 1) >= length) drop_odd(vr[i][c]);
-                }
+                        if (key + 2 * q + (i & 1) + 8 * (i >> 1) >= length) drop_odd(vr[i][c]);
             }
-            // O^T += V^T P^T.  Tile j of 16 rows: columns 8 g + j of one chunk, and of the other (d = 64: the
-            // other half of the one).
-#pragma unroll
-            for (int j = 0; j < MT; ++j) {
-                uint32_t af[4];
-#pragma unroll
-                for (int i = 0; i < 2; ++i)          // a slot pair
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {    // rows g and g + 8 of the tile
-                        const int e = D == 128 ? j : j + 4 * c;     // column of the chunk
-                        const uint4 &x = vr[2 * i][D == 128 ? c : 0], &y = vr[2 * i + 1][D == 128 ? c : 0];
-                        const uint32_t u = e / 2 == 0 ? x.x : e / 2 == 1 ? x.y : e / 2 == 2 ? x.z : x.w;
-                        const uint32_t w = e / 2 == 0 ? y.x : e / 2 == 1 ? y.y : e / 2 == 2 ? y.z : y.w;
-                        af[2 * i + c] = __byte_perm(u, w, e & 1 ? 0x7632 : 0x5410);
-                    }
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    mma16816(acc[t][j], af, ph[t][0], ph[t][1]);
-                    mma16816(acc[t][j], af, pl[t][0], pl[t][1]);
-                }
-            }
-            if (more) load_v(seg, key + kBlock);
-            else if (nxt.there) load_v(nxt, nxt.first * kBlock + 16 * warp);
         }
-
-        // Join the warps.
+        // O^T += V^T P^T.  Tile j of 16 rows: columns 8 g + j of one chunk, and of the other (d = 64: the
+        // other half of the one).
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+            uint32_t af[4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)          // a slot pair
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {    // rows g and g + 8 of the tile
+                    const int e = D == 128 ? j : j + 4 * c;     // column of the chunk
+                    const uint4 &x = vr[2 * i][D == 128 ? c : 0], &y = vr[2 * i + 1][D == 128 ? c : 0];
+                    const uint32_t u = e / 2 == 0 ? x.x : e / 2 == 1 ? x.y : e / 2 == 2 ? x.z : x.w;
+                    const uint32_t w = e / 2 == 0 ? y.x : e / 2 == 1 ? y.y : e / 2 == 2 ? y.z : y.w;
+                    af[2 * i + c] = __byte_perm(u, w, e & 1 ? 0x7632 : 0x5410);
+                }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                mma16816(acc[t][j], af, ph[t][0], ph[t][1]);
+                mma16816(acc[t][j], af, pl[t][0], pl[t][1]);
+            }
+        }
+    }
+    // The warp's results into shared memory, rows of D + 4 floats.
+    __device__ __forceinline__ void leave(float *o, float2 *ml)
+    {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -458,55 +442,226 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) few_kernel(Cache
                 l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 8);
                 l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 16);
                 const int r = 8 * t + 2 * q + e;
-                if (g == 0) {
-                    sm.m[warp][r] = m[t][e];
-                    sm.l[warp][r] = l[t][e];
-                }
+                if (g == 0) ml[r] = make_float2(m[t][e], l[t][e]);
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
 #pragma unroll
                     for (int j = 0; j < MT; j += 4)
-                        *reinterpret_cast<float4 *>(&sm.o[warp][r][D == 128 ? 64 * c + 8 * g + j : 8 * g + 4 * c]) =
+                        *reinterpret_cast<float4 *>(o + r * (D + 4) + (D == 128 ? 64 * c + 8 * g + j : 8 * g + 4 * c)) =
                             make_float4(acc[t][j][e + 2 * c], acc[t][j + 1][e + 2 * c], acc[t][j + 2][e + 2 * c],
                                         acc[t][j + 3][e + 2 * c]);
             }
+    }
+};
+
+// What the warps left of a unit's rows.
+template <int D, int NT, int WARPS>
+struct Left {
+    float o[WARPS][8 * NT][D + 4];
+    float2 ml[WARPS][8 * NT];
+};
+
+// Row r, columns c ... c + 7 over the warps: maximum and sum, o unnormalised.
+template <int D, int NT, int WARPS>
+__device__ __forceinline__ float2 gather(const Left<D, NT, WARPS> &sm, int r, int c, float (&o)[8])
+{
+    float top = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) top = fmaxf(top, sm.ml[w][r].x);
+    const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+        const float2 ml = sm.ml[w][r];
+        const float f = ptx::ex2(ml.x - base);
+        sum += f * ml.y;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] += f * sm.o[w][r][c + e];
+    }
+    return make_float2(top, sum);
+}
+
+// A row that sees nothing has a sum of zero.
+__device__ __forceinline__ float inverse_of(float sum) { return sum == 0.f ? 0.f : 1.f / sum; }
+__device__ __forceinline__ float lse_of(float top, float sum)
+{
+    return sum == 0.f ? -INFINITY : (top + log2f(sum)) * (1.f / kLog2e);
+}
+
+__device__ __forceinline__ void write_o8(const CacheAttnArgs &a, long long row, int c, const float (&o)[8], float inv)
+{
+    *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + row * a.d + c) =
+        make_uint4(ptx::pack_bf16x2(o[0] * inv, o[1] * inv), ptx::pack_bf16x2(o[2] * inv, o[3] * inv),
+                   ptx::pack_bf16x2(o[4] * inv, o[5] * inv), ptx::pack_bf16x2(o[6] * inv, o[7] * inv));
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) few_kernel(CacheAttnArgs a, Plan plan, Parts parts)
+{
+    constexpr int R8 = 8 * NT;
+    __shared__ Left<D, NT, kFewWarps> sm;
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
+    const int warp = threadIdx.x >> 5, T = a.T, R = a.G * T;
+    Walk walk;
+    if (!walk.begin(a.lengths, a.B, plan)) return;
+    const float to_log2 = a.scale * kLog2e;
+    Segment seg;
+    walk.next(a.lengths, plan, seg);
+    Rows<D, NT> w;
+    auto first_key = [&](const Segment &s) { return s.first * kBlock + 16 * warp; };
+    w.load_k(a, seg.head, first_key(seg), seg.length + T);
+    w.load_q(a, seg.head, seg.tile * R8);
+    w.load_v(a, seg.head, first_key(seg), seg.length + T);
+
+    while (seg.there) {
+        const int r0 = seg.tile * R8, valid = seg.length + T, end = seg.last * kBlock;
+        Segment nxt;
+        walk.next(a.lengths, plan, nxt);
+        w.clear();
+        // A warp's steps (its share of the last block may be empty); the loads ahead of the last are the next segment's.
+        for (int key = first_key(seg); key < end; key += kBlock) {
+            const bool more = key + kBlock < end;
+            w.scores();
+            if (more) {
+                w.load_k(a, seg.head, key + kBlock, valid);
+            } else if (nxt.there) {
+                w.load_k(a, nxt.head, first_key(nxt), nxt.length + T);
+                w.load_q(a, nxt.head, nxt.tile * R8);
+            }
+            w.step(a, seg.head, seg.b, r0, key, seg.length, to_log2, parts.scores);
+            if (more) w.load_v(a, seg.head, key + kBlock, valid);
+            else if (nxt.there) w.load_v(a, nxt.head, first_key(nxt), nxt.length + T);
+        }
+        w.leave(&sm.o[warp][0][0], sm.ml[warp]);
         __syncthreads();
-        const bool whole = first == 0 && last == nb;
-        const long long slot = 2 * blockIdx.x + (first == 0 ? 1 : 0);
+        const long long slot = 2 * (long long)blockIdx.x + (seg.first == 0 ? 1 : 0);
         constexpr int PER = D / 8;       // threads a row, 8 columns each
         for (int i = threadIdx.x; i < R8 * PER; i += kFewThreads) {
             const int r = i / PER, c = i % PER * 8;
-            float top = -INFINITY, f[kFewWarps], sum = 0.f, o[8];
-#pragma unroll
-            for (int w = 0; w < kFewWarps; ++w) top = fmaxf(top, sm.m[w][r]);
-            const float base = top == -INFINITY ? 0.f : top;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = 0.f;
-#pragma unroll
-            for (int w = 0; w < kFewWarps; ++w) {
-                f[w] = ptx::ex2(sm.m[w][r] - base);
-                sum += f[w] * sm.l[w][r];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] += f[w] * sm.o[w][r][c + e];
-            }
+            float o[8];
+            const float2 ml = gather(sm, r, c, o);
             if (r0 + r >= R) continue;
-            if (whole) {
-                const float inv = sum == 0.f ? 0.f : 1.f / sum;     // a row that sees nothing
-                const long long at = head * R + r0 + r;
-                *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + at * D + c) =
-                    make_uint4(ptx::pack_bf16x2(o[0] * inv, o[1] * inv), ptx::pack_bf16x2(o[2] * inv, o[3] * inv),
-                               ptx::pack_bf16x2(o[4] * inv, o[5] * inv), ptx::pack_bf16x2(o[6] * inv, o[7] * inv));
-                if (c == 0) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * (1.f / kLog2e);
+            if (seg.whole()) {
+                const long long at = seg.head * R + r0 + r;
+                write_o8(a, at, c, o, inverse_of(ml.y));
+                if (c == 0) a.lse[at] = lse_of(ml.x, ml.y);
             } else {
                 float4 *to = reinterpret_cast<float4 *>(parts.o + (slot * R8 + r) * D + c);
                 to[0] = make_float4(o[0], o[1], o[2], o[3]);
                 to[1] = make_float4(o[4], o[5], o[6], o[7]);
-                if (c == 0) parts.ml[slot * R8 + r] = make_float2(top, sum);
+                if (c == 0) parts.ml[slot * R8 + r] = ml;
             }
         }
         __syncthreads();
         seg = nxt;
     }
+}
+
+// unit_kernel: the same where a unit's slots, as many as the cache has room for, are few enough for one cluster of 1
+// to 8 CTAs: each warp takes every (8 cluster)-th run of 16, the CTAs' results meet in distributed shared memory, and
+// there are no parts and no join_kernel (the two launches' hand-over, the lengths a second time and the parts' way
+// through L2 take 4 us).
+constexpr int kUnitWarps = 8;
+
+template <int D, int NT>
+struct UnitSmem {
+    Left<D, NT, kUnitWarps> left;
+    float o[8 * NT][D];              // the CTA's sum, read by the cluster
+    float2 ml[8 * NT];
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(32 * kUnitWarps, D == 64 ? 2 : 1) unit_kernel(CacheAttnArgs a, int tiles, float *kept)
+{
+    constexpr int R8 = 8 * NT;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    UnitSmem<D, NT> &sm = *reinterpret_cast<UnitSmem<D, NT> *>(smem_raw);
+    ptx::grid_dep_launch();
+    const int warp = threadIdx.x >> 5, T = a.T, R = a.G * T;
+    const int ctas = (int)ptx::cluster_size(), rank = (int)ptx::cluster_rank();
+    const unsigned unit = blockIdx.x / (unsigned)ctas;
+    const long long head = unit / (unsigned)tiles;
+    const int r0 = (int)(unit % (unsigned)tiles) * R8, b = (int)(head / a.H);
+    const int stride = 16 * kUnitWarps * ctas;
+    int key = 16 * (rank * kUnitWarps + warp);
+    ptx::grid_dep_wait();
+    Rows<D, NT> w;
+    // asked for along with the length: what lies behind it is masked or dropped
+    w.load_k(a, head, key, a.C);
+    w.load_q(a, head, r0);
+    w.load_v(a, head, key, a.C);
+    const int length = length_of(a.lengths, b, T, a.C), valid = length + T;
+    const float to_log2 = a.scale * kLog2e;
+    w.clear();
+    w.drop_behind(key, valid);
+    for (; key < valid; key += stride) {
+        const bool more = key + stride < valid;
+        w.scores();
+        if (more) w.load_k(a, head, key + stride, valid);
+        w.step(a, head, b, r0, key, length, to_log2, kept);
+        if (more) w.load_v(a, head, key + stride, valid);
+    }
+    w.leave(&sm.left.o[warp][0][0], sm.left.ml[warp]);
+    __syncthreads();
+    constexpr int PER = D / 8;
+    for (int i = threadIdx.x; i < R8 * PER; i += 32 * kUnitWarps) {
+        const int r = i / PER, c = i % PER * 8;
+        float o[8];
+        const float2 ml = gather(sm.left, r, c, o);
+        if (ctas == 1) {
+            if (r0 + r >= R) continue;
+            const long long at = head * R + r0 + r;
+            write_o8(a, at, c, o, inverse_of(ml.y));
+            if (c == 0) a.lse[at] = lse_of(ml.x, ml.y);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; e += 4)
+                *reinterpret_cast<float4 *>(&sm.o[r][c + e]) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            if (c == 0) sm.ml[r] = ml;
+        }
+    }
+    if (ctas == 1) return;
+    ptx::cluster_sync();
+    // each CTA finishes its share of the rows' pieces of four columns
+    constexpr int QUADS = D / 4, ALL = R8 * QUADS;
+    const int share = ALL / ctas;                       // (a power of two of CTAs)
+    for (int i = rank * share + threadIdx.x; i < (rank + 1) * share; i += 32 * kUnitWarps) {
+        const int r = i / QUADS, c = i % QUADS * 4;
+        if (r0 + r >= R) break;
+        float2 ml[8];
+        float4 o[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < ctas) {
+                const uint2 x = ptx::ld_cluster_b64(ptx::cluster_addr(ptx::smem_u32(&sm.ml[r]), (uint32_t)k));
+                ml[k] = make_float2(__uint_as_float(x.x), __uint_as_float(x.y));
+                o[k] = ptx::ld_cluster_f32x4(ptx::cluster_addr(ptx::smem_u32(&sm.o[r][c]), (uint32_t)k));
+            }
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < ctas) top = fmaxf(top, ml[k].x);
+        const float base = top == -INFINITY ? 0.f : top;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < ctas) {
+                const float f = ptx::ex2(ml[k].x - base);
+                sum += f * ml[k].y;
+                v.x += f * o[k].x;
+                v.y += f * o[k].y;
+                v.z += f * o[k].z;
+                v.w += f * o[k].w;
+            }
+        const long long at = head * R + r0 + r;
+        const float inv = inverse_of(sum);
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.o) + at * D + c) =
+            make_uint2(ptx::pack_bf16x2(v.x * inv, v.y * inv), ptx::pack_bf16x2(v.z * inv, v.w * inv));
+        if (c == 0) a.lse[at] = lse_of(top, sum);
+    }
+    ptx::cluster_sync_relaxed();       // nobody leaves while its sums are read
 }
 
 // ------------------------------------------------------------------------------------------
@@ -956,8 +1111,8 @@ struct Sum {
         l = l * old + ml.y * part;
         top = t;
     }
-    __device__ __forceinline__ float inverse() const { return l == 0.f ? 0.f : 1.f / l; }
-    __device__ __forceinline__ float lse() const { return l == 0.f ? -INFINITY : (top + log2f(l)) * (1.f / kLog2e); }
+    __device__ __forceinline__ float inverse() const { return inverse_of(l); }
+    __device__ __forceinline__ float lse() const { return lse_of(top, l); }
 };
 
 // Where a unit's parts are.  By a whole warp.
@@ -1197,6 +1352,27 @@ size_t parts_bytes(const Shape &sh, int d)
     return up256(slots * d * 4) + up256(slots * 8);
 }
 
+// CTAs of a cluster that takes a unit whole (unit_kernel), or 0 where few_kernel and join_kernel do better.
+int unit_ctas(long long units, int C, int d)
+{
+    static const char *e1 = getenv("UNIT_MAX"), *e2 = getenv("UNIT_STEPS");
+    const int most = e1 ? atoi(e1) : d == 64 ? 2 * kPlanSms : kPlanSms, steps = e2 ? atoi(e2) : 12;
+    int n = 1;
+    while (n < 8 && units * n * 2 <= most) n *= 2;
+    return units <= most && C <= steps * 16 * kUnitWarps * n ? n : 0;
+}
+
+template <int D, int NT>
+cudaError_t launch_unit(const CacheAttnArgs &a, int tiles, int ctas, float *kept, cudaStream_t stream)
+{
+    static std::atomic<bool> set[64];
+    constexpr int bytes = (int)sizeof(UnitSmem<D, NT>);
+    const cudaError_t e = raise_smem(reinterpret_cast<const void *>(unit_kernel<D, NT>), bytes, set);
+    if (e != cudaSuccess) return e;
+    return launch_overlapped(unit_kernel<D, NT>, dim3((unsigned)(a.B * a.H) * tiles * ctas), dim3(32 * kUnitWarps), bytes,
+                             (unsigned)ctas, stream, a, tiles, kept);
+}
+
 template <int D, int MODE>
 cudaError_t launch_many(const CacheAttnArgs &a, const Plan &plan, const Parts &parts, int ctas, cudaStream_t stream)
 {
@@ -1226,7 +1402,11 @@ cudaError_t launch(const CacheAttnArgs &a, cudaStream_t stream)
     parts.scores = a.weights && !sh.many() ? reinterpret_cast<float *>(static_cast<char *>(a.workspace) + parts_bytes(sh, D))
                                            : nullptr;
     cudaError_t e;
-    if (sh.rows == 8)
+    const int unit = sh.many() ? 0 : unit_ctas((long long)a.B * a.H * plan.tiles, a.C, D);
+    if (unit)
+        e = sh.rows == 8 ? launch_unit<D, 1>(a, plan.tiles, unit, parts.scores, stream)
+                         : launch_unit<D, 2>(a, plan.tiles, unit, parts.scores, stream);
+    else if (sh.rows == 8)
         e = launch_overlapped(few_kernel<D, 1>, dim3(sh.ctas), dim3(kFewThreads), 0, 1, stream, a, plan, parts);
     else if (sh.rows == 16)
         e = launch_overlapped(few_kernel<D, 2>, dim3(sh.ctas), dim3(kFewThreads), 0, 1, stream, a, plan, parts);
@@ -1234,7 +1414,7 @@ cudaError_t launch(const CacheAttnArgs &a, cudaStream_t stream)
         e = sh.rows == 128 ? launch_many<D, 1>(a, plan, parts, sh.ctas, stream)
                            : launch_many<D, 2>(a, plan, parts, sh.ctas, stream);
     if (e != cudaSuccess) return e;
-    e = sh.many() ? launch_overlapped(join_many_kernel<D>, dim3((unsigned)(a.B * a.H) * plan.tiles * (sh.rows / 32) * (D / 32)),
+    if (!unit) e = sh.many() ? launch_overlapped(join_many_kernel<D>, dim3((unsigned)(a.B * a.H) * plan.tiles * (sh.rows / 32) * (D / 32)),
                                       dim3(256), 0, 1, stream, a, plan, sh.rows, sh.ctas, parts)
                   : launch_overlapped(join_kernel<D>, dim3((unsigned)(a.B * a.H) * R), dim3(32 * kJoinWarps), 0, 1, stream, a,
                                       plan, sh.rows, sh.ctas, parts);
