@@ -218,17 +218,39 @@ struct Parts {
     float *scores;     // null, or [B H][G T][C]: scores times log2 e, -infinity where a row does not see a slot
 };
 
-// A warp's state: 8 NT rows of one unit against 16 slots a step.
-template <int D, int NT>
+// Waits for what is already on its way, for a second at most, whether or not the CTA has given up.
+__device__ __forceinline__ void drain(uint64_t *bar, uint32_t parity)
+{
+    const uint64_t t0 = globaltimer_ns();
+    while (!ptx::mbar_try_wait(bar, parity))
+        if (globaltimer_ns() - t0 > 1000000000ull) return;
+}
+
+struct KvMaps {
+    CUtensorMap k, v;         // [B H][C][d], boxes of 64 columns x 16 slots
+};
+
+// A warp's state: 8 NT rows of one unit against 16 slots a step.  K and V of the steps ahead come by TMA into a ring of
+// STAGES steps that is the warp's own (64 columns a box, 128-byte swizzle: V is read without bank conflicts, K with two
+// ways), each stage with a barrier that nobody but this warp waits on.
+template <int D, int NT, int STAGES_>
 struct Rows {
+    static constexpr int STAGES = STAGES_;
     static constexpr int KC = D / 32;           // chunks of a K row a thread holds
     static constexpr int VC = D / 64;           // chunks of a V row a thread holds
     static constexpr int MT = D / 16;           // 16-row tiles of O^T
-    uint4 qf[NT][KC], kr[2][KC], vr[4][VC];
+    static constexpr uint32_t BOX = 16 * 128, STAGE = 2 * (D / 64) * BOX, RING = STAGES * STAGE;    // bytes
+    uint4 qf[NT][KC];
     float acc[NT][MT][4], m[NT][2], l[NT][2], s[NT][4];
     int g, q;
+    uint8_t *ring;                              // 1024-byte aligned
+    uint64_t *bars;
+    uint32_t asked, taken;                      // steps
 
-    __device__ __forceinline__ Rows() : g((threadIdx.x & 31) >> 2), q(threadIdx.x & 3) {}
+    __device__ __forceinline__ Rows(uint8_t *warp_ring, uint64_t *warp_bars)
+        : g((threadIdx.x & 31) >> 2), q(threadIdx.x & 3), ring(warp_ring), bars(warp_bars), asked(0), taken(0)
+    {
+    }
 
     __device__ __forceinline__ void clear()
     {
@@ -252,41 +274,41 @@ struct Rows {
             for (int c = 0; c < KC; ++c) qf[t][c] = r < R ? qp[4 * c + q] : make_uint4(0, 0, 0, 0);
         }
     }
-    // 16 slots from `key` on; those from `valid` on read as zeros, whatever lies there
-    __device__ __forceinline__ void load_k(const CacheAttnArgs &a, long long head, int key, int valid)
+    // Asks for 16 slots from `key` on.
+    __device__ __forceinline__ void load(const KvMaps &maps, long long head, int key)
     {
-        const uint4 *kp = static_cast<const uint4 *>(a.k) + (head * a.C + key + g) * (D / 8) + q;
-        const int left = valid - key - g;
+        __syncwarp();                           // the stage's last step has been read by every lane
+        if ((threadIdx.x & 31) == 0) {
+            const uint32_t st = asked % STAGES;
+            uint8_t *to = ring + st * STAGE;
+            ptx::mbar_arrive_expect_tx(&bars[st], STAGE);
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+                ptx::tma_load_3d(to + c * BOX, &maps.k, &bars[st], 64 * c, key, (int)head);
+                ptx::tma_load_3d(to + (D / 64 + c) * BOX, &maps.v, &bars[st], 64 * c, key, (int)head);
+            }
+        }
+        ++asked;
+    }
+    // Nothing stays on its way when the warp leaves (matters only after a timeout).
+    __device__ __forceinline__ void finish()
+    {
+        for (; taken < asked; ++taken) drain(&bars[taken % STAGES], taken / STAGES & 1);
+    }
+    // S^T = K Q^T of the step that was asked for first; two sums, whose products need not wait for one another.
+    __device__ __forceinline__ void scores(const Guard &guard)
+    {
+        const uint32_t st = taken % STAGES, at = ptx::smem_u32(ring) + st * STAGE + g * 128;
+        wait_bounded(&bars[st], taken / STAGES & 1, guard);
+        uint4 kr[2][KC];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int c = 0; c < KC; ++c) kr[i][c] = 8 * i < left ? stream16(kp + i * D + 4 * c) : make_uint4(0, 0, 0, 0);
-    }
-    __device__ __forceinline__ void load_v(const CacheAttnArgs &a, long long head, int key, int valid)
-    {
-        const uint4 *vp = static_cast<const uint4 *>(a.v) + (head * a.C + key + 2 * q) * (D / 8) + g;
-        const int left = valid - key - 2 * q;
+            for (int c = 0; c < KC; ++c)
+                kr[i][c] = lds_u128(at + i * 1024 + (c >> 1) * BOX + (((q ^ g) ^ (c & 1) * 4) << 4));
+        float s1[NT][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int c = 0; c < VC; ++c) {
-                const int j = (i & 1) + 8 * (i >> 1);
-                vr[i][c] = j < left ? stream16(vp + j * (D / 8) + 8 * c) : make_uint4(0, 0, 0, 0);
-            }
-    }
-    // V's rows from `valid` on as zeros, where they were loaded before that was known
-    __device__ __forceinline__ void drop_behind(int key, int valid)
-    {
-        const int left = valid - key - 2 * q;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int c = 0; c < VC; ++c)
-                if ((i & 1) + 8 * (i >> 1) >= left) vr[i][c] = make_uint4(0, 0, 0, 0);
-    }
-    // S^T = K Q^T: K is free afterwards
-    __device__ __forceinline__ void scores()
-    {
+        for (int t = 0; t < NT; ++t) s1[t][0] = s1[t][1] = s1[t][2] = s1[t][3] = 0.f;
 #pragma unroll
         for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
 #pragma unroll
@@ -296,16 +318,38 @@ struct Rows {
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 mma16816(s[t], a0, qf[t][c].x, qf[t][c].y);
-                mma16816(s[t], a1, qf[t][c].z, qf[t][c].w);
+                mma16816(s1[t], a1, qf[t][c].z, qf[t][c].w);
             }
         }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[t][e] += s1[t][e];
     }
-    // The rest of the step at `key`: weights, and O^T += V^T P^T; V is free afterwards.  kept: see Parts::scores
+    // The rest of the step at `key`: weights, and O^T += V^T P^T.  kept: see Parts::scores
     __device__ __forceinline__ void step(const CacheAttnArgs &a, long long head, int b, int r0, int key, int length,
                                          float to_log2, float *kept)
     {
         const int T = a.T, R = a.G * T;
         const bool tail = key + 16 > length;
+        uint4 vr[4][VC];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < VC; ++c) {
+                const int j = 2 * q + (i & 1);
+                vr[i][c] = lds_u128(ptx::smem_u32(ring) + taken % STAGES * STAGE + (D / 64 + c) * BOX + (j + 8 * (i >> 1)) * 128 +
+                                    ((g ^ j) << 4));
+            }
+        ++taken;
+        if (tail) {          // whatever lies behind the last slot is not a value
+            const int left = length + T - key - 2 * q;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int c = 0; c < VC; ++c)
+                    if ((i & 1) + 8 * (i >> 1) >= left) vr[i][c] = make_uint4(0, 0, 0, 0);
+        }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -409,11 +453,11 @@ struct Rows {
                         if (key + 2 * q + (i & 1) + 8 * (i >> 1) >= length) drop_odd(vr[i][c]);
             }
         }
-        // O^T += V^T P^T.  Tile j of 16 rows: columns 8 g + j of one chunk, and of the other (d = 64: the
-        // other half of the one).
+        // O^T += V^T P^T.  Tile j of 16 rows: columns 8 g + j of one chunk, and of the other (d = 64: the other half of
+        // the one).
+        uint32_t af[MT][4];
 #pragma unroll
-        for (int j = 0; j < MT; ++j) {
-            uint32_t af[4];
+        for (int j = 0; j < MT; ++j)
 #pragma unroll
             for (int i = 0; i < 2; ++i)          // a slot pair
 #pragma unroll
@@ -422,14 +466,51 @@ struct Rows {
                     const uint4 &x = vr[2 * i][D == 128 ? c : 0], &y = vr[2 * i + 1][D == 128 ? c : 0];
                     const uint32_t u = e / 2 == 0 ? x.x : e / 2 == 1 ? x.y : e / 2 == 2 ? x.z : x.w;
                     const uint32_t w = e / 2 == 0 ? y.x : e / 2 == 1 ? y.y : e / 2 == 2 ? y.z : y.w;
-                    af[2 * i + c] = __byte_perm(u, w, e & 1 ? 0x7632 : 0x5410);
+                    af[j][2 * i + c] = __byte_perm(u, w, e & 1 ? 0x7632 : 0x5410);
                 }
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                mma16816(acc[t][j], af, ph[t][0], ph[t][1]);
-                mma16816(acc[t][j], af, pl[t][0], pl[t][1]);
+        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+            for (int j = 0; j < MT; ++j) mma16816(acc[t][j], af[j], ph[t][0], ph[t][1]);
+#pragma unroll
+            for (int j = 0; j < MT; ++j) mma16816(acc[t][j], af[j], pl[t][0], pl[t][1]);
+        }
+    }
+    // A warp's results into shared memory as they lie in its registers, and into those of another warp.
+    __device__ __forceinline__ void hand_over(float *to)          // [NT (4 MT + 4)][32]
+    {
+        float *x = to + (threadIdx.x & 31);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[((t * MT + i) * 4 + e) * 32] = acc[t][i][e];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                x[(NT * MT * 4 + t * 4 + e) * 32] = m[t][e];
+                x[(NT * MT * 4 + t * 4 + 2 + e) * 32] = l[t][e];
             }
         }
+    }
+    __device__ __forceinline__ void take_over(const float *from)
+    {
+        const float *x = from + (threadIdx.x & 31);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float other = x[(NT * MT * 4 + t * 4 + e) * 32], top = fmaxf(m[t][e], other);
+                const float base = top == -INFINITY ? 0.f : top;
+                const float f = ptx::ex2(m[t][e] - base), p = ptx::ex2(other - base);
+                m[t][e] = top;
+                l[t][e] = l[t][e] * f + x[(NT * MT * 4 + t * 4 + 2 + e) * 32] * p;
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    acc[t][i][e] = acc[t][i][e] * f + x[((t * MT + i) * 4 + e) * 32] * p;
+                    acc[t][i][e + 2] = acc[t][i][e + 2] * f + x[((t * MT + i) * 4 + e + 2) * 32] * p;
+                }
+            }
     }
     // The warp's results into shared memory, rows of D + 4 floats.
     __device__ __forceinline__ void leave(float *o, float2 *ml)
@@ -497,51 +578,90 @@ __device__ __forceinline__ void write_o8(const CacheAttnArgs &a, long long row, 
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) few_kernel(CacheAttnArgs a, Plan plan, Parts parts)
+struct FewCfg {
+    static constexpr int BLOCKS = NT == 1 ? 3 : 2;       // CTAs an SM
+    static constexpr int STAGES = D == 64 ? 4 : 2;
+    using R = Rows<D, NT, STAGES>;
+    using L = Left<D, NT, 2>;
+    static constexpr int HELD = NT * (D / 4 + 4) * 32;        // floats a warp hands over
+    static constexpr int RINGS = kFewWarps * (int)R::RING, HANDED = 2 * HELD * 4;
+    static constexpr int JOIN = HANDED > (int)sizeof(L) ? HANDED : (int)sizeof(L);
+    static constexpr int SMEM = RINGS + JOIN + 256 + 1024;
+    static_assert(BLOCKS * (SMEM + 1024) <= 228 * 1024, "");
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kFewThreads, FewCfg<D, NT>::BLOCKS)
+    few_kernel(const __grid_constant__ KvMaps maps, const __grid_constant__ CacheAttnArgs a, Plan plan, Parts parts)
 {
+    using C = FewCfg<D, NT>;
     constexpr int R8 = 8 * NT;
-    __shared__ Left<D, NT, kFewWarps> sm;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = align1024(smem_raw);
+    typename C::L &left = *reinterpret_cast<typename C::L *>(smem + C::RINGS);
+    float *handed = reinterpret_cast<float *>(smem + C::RINGS);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::RINGS + C::JOIN);
+    int *abort = reinterpret_cast<int *>(bars + kFewWarps * C::STAGES);
     ptx::grid_dep_launch();
-    ptx::grid_dep_wait();
     const int warp = threadIdx.x >> 5, T = a.T, R = a.G * T;
+    if (threadIdx.x == 0) {
+        *abort = 0;
+        for (int i = 0; i < kFewWarps * C::STAGES; ++i) ptx::mbar_init(&bars[i], 1);
+        ptx::fence_mbar_init();
+        ptx::tma_prefetch_desc(&maps.k);
+        ptx::tma_prefetch_desc(&maps.v);
+    }
+    __syncthreads();
+    ptx::grid_dep_wait();
     Walk walk;
     if (!walk.begin(a.lengths, a.B, plan)) return;
+    const Guard guard{abort, a.status, kWaitLimitNs};
     const float to_log2 = a.scale * kLog2e;
-    Segment seg;
-    walk.next(a.lengths, plan, seg);
-    Rows<D, NT> w;
+    typename C::R w(smem + warp * C::R::RING, bars + warp * C::STAGES);
     auto first_key = [&](const Segment &s) { return s.first * kBlock + 16 * warp; };
-    w.load_k(a, seg.head, first_key(seg), seg.length + T);
+    // What is asked for runs ahead of what is worked on, over the ends of segments.
+    Walk walk_ahead = walk;
+    Segment seg, ahead;
+    walk_ahead.next(a.lengths, plan, ahead);
+    int key_ahead = first_key(ahead);
+    auto ask = [&] {
+        if (!ahead.there) return;
+        w.load(maps, ahead.head, key_ahead);
+        key_ahead += kBlock;
+        if (key_ahead >= ahead.last * kBlock && walk_ahead.next(a.lengths, plan, ahead)) key_ahead = first_key(ahead);
+    };
+    ask();
+    walk.next(a.lengths, plan, seg);
     w.load_q(a, seg.head, seg.tile * R8);
-    w.load_v(a, seg.head, first_key(seg), seg.length + T);
+#pragma unroll
+    for (int i = 1; i < C::STAGES; ++i) ask();
 
     while (seg.there) {
-        const int r0 = seg.tile * R8, valid = seg.length + T, end = seg.last * kBlock;
+        const int r0 = seg.tile * R8, end = seg.last * kBlock;
         Segment nxt;
         walk.next(a.lengths, plan, nxt);
         w.clear();
-        // A warp's steps (its share of the last block may be empty); the loads ahead of the last are the next segment's.
-        for (int key = first_key(seg); key < end; key += kBlock) {
-            const bool more = key + kBlock < end;
-            w.scores();
-            if (more) {
-                w.load_k(a, seg.head, key + kBlock, valid);
-            } else if (nxt.there) {
-                w.load_k(a, nxt.head, first_key(nxt), nxt.length + T);
-                w.load_q(a, nxt.head, nxt.tile * R8);
-            }
+        for (int key = first_key(seg); key < end; key += kBlock) {       // (a warp's share of the last block may be empty)
+            w.scores(guard);
+            if (key + kBlock >= end && nxt.there) w.load_q(a, nxt.head, nxt.tile * R8);
             w.step(a, seg.head, seg.b, r0, key, seg.length, to_log2, parts.scores);
-            if (more) w.load_v(a, seg.head, key + kBlock, valid);
-            else if (nxt.there) w.load_v(a, nxt.head, first_key(nxt), nxt.length + T);
+            ask();
         }
-        w.leave(&sm.o[warp][0][0], sm.ml[warp]);
+        // four warps' results become two, then one row each
+        if (warp >= 2) w.hand_over(handed + (warp - 2) * C::HELD);
+        __syncthreads();
+        if (warp < 2) {
+            w.take_over(handed + warp * C::HELD);
+            ptx::named_bar(1, 64);
+            w.leave(&left.o[warp][0][0], left.ml[warp]);
+        }
         __syncthreads();
         const long long slot = 2 * (long long)blockIdx.x + (seg.first == 0 ? 1 : 0);
         constexpr int PER = D / 8;       // threads a row, 8 columns each
         for (int i = threadIdx.x; i < R8 * PER; i += kFewThreads) {
             const int r = i / PER, c = i % PER * 8;
             float o[8];
-            const float2 ml = gather(sm, r, c, o);
+            const float2 ml = gather(left, r, c, o);
             if (r0 + r >= R) continue;
             if (seg.whole()) {
                 const long long at = seg.head * R + r0 + r;
@@ -557,6 +677,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) few_kernel(Cache
         __syncthreads();
         seg = nxt;
     }
+    w.finish();
 }
 
 // unit_kernel: the same where a unit's slots, as many as the cache has room for, are few enough for one cluster of 1
@@ -566,50 +687,79 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) few_kernel(Cache
 constexpr int kUnitWarps = 8;
 
 template <int D, int NT>
-struct UnitSmem {
-    Left<D, NT, kUnitWarps> left;
-    float o[8 * NT][D];              // the CTA's sum, read by the cluster
-    float2 ml[8 * NT];
+struct UnitCfg {
+    static constexpr int STAGES = 3;
+    static constexpr int BLOCKS = D == 128 ? 1 : 2;
+    using R = Rows<D, NT, STAGES>;
+    using L = Left<D, NT, kUnitWarps>;
+    struct Sum {
+        float o[8 * NT][D];              // the CTA's sum, read by the cluster
+        float2 ml[8 * NT];
+    };
+    // what the warps leave goes over their rings
+    static constexpr int RINGS = kUnitWarps * (int)R::RING;
+    static_assert(sizeof(L) <= RINGS, "");
+    static constexpr int SMEM = RINGS + (int)sizeof(Sum) + 256 + 1024;
+    static_assert(BLOCKS * (SMEM + 1024) <= 228 * 1024, "");
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(32 * kUnitWarps, D == 64 ? 2 : 1) unit_kernel(CacheAttnArgs a, int tiles, float *kept)
+__global__ void __launch_bounds__(32 * kUnitWarps, UnitCfg<D, NT>::BLOCKS)
+    unit_kernel(const __grid_constant__ KvMaps maps, const __grid_constant__ CacheAttnArgs a, int tiles, float *kept)
 {
+    using C = UnitCfg<D, NT>;
     constexpr int R8 = 8 * NT;
-    extern __shared__ __align__(16) uint8_t smem_raw[];
-    UnitSmem<D, NT> &sm = *reinterpret_cast<UnitSmem<D, NT> *>(smem_raw);
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = align1024(smem_raw);
+    typename C::L &left = *reinterpret_cast<typename C::L *>(smem);
+    typename C::Sum &sm = *reinterpret_cast<typename C::Sum *>(smem + C::RINGS);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::RINGS + sizeof(typename C::Sum));
+    int *abort = reinterpret_cast<int *>(bars + kUnitWarps * C::STAGES);
     ptx::grid_dep_launch();
     const int warp = threadIdx.x >> 5, T = a.T, R = a.G * T;
+    if (threadIdx.x == 0) {
+        *abort = 0;
+        for (int i = 0; i < kUnitWarps * C::STAGES; ++i) ptx::mbar_init(&bars[i], 1);
+        ptx::fence_mbar_init();
+        ptx::tma_prefetch_desc(&maps.k);
+        ptx::tma_prefetch_desc(&maps.v);
+    }
     const int ctas = (int)ptx::cluster_size(), rank = (int)ptx::cluster_rank();
     const unsigned unit = blockIdx.x / (unsigned)ctas;
     const long long head = unit / (unsigned)tiles;
     const int r0 = (int)(unit % (unsigned)tiles) * R8, b = (int)(head / a.H);
     const int stride = 16 * kUnitWarps * ctas;
     int key = 16 * (rank * kUnitWarps + warp);
+    __syncthreads();
     ptx::grid_dep_wait();
-    Rows<D, NT> w;
-    // asked for along with the length: what lies behind it is masked or dropped
-    w.load_k(a, head, key, a.C);
-    w.load_q(a, head, r0);
-    w.load_v(a, head, key, a.C);
+    const Guard guard{abort, a.status, kWaitLimitNs};
+    typename C::R w(smem + warp * C::R::RING, bars + warp * C::STAGES);
+    if (key < a.C) w.load(maps, head, key);     // along with the length: what lies behind it is masked or dropped
     const int length = length_of(a.lengths, b, T, a.C), valid = length + T;
+    w.load_q(a, head, r0);
+    int ahead = key + stride;
+    auto ask = [&] {
+        if (ahead < valid) w.load(maps, head, ahead);
+        ahead += stride;
+    };
+#pragma unroll
+    for (int i = 1; i < C::STAGES; ++i) ask();
     const float to_log2 = a.scale * kLog2e;
     w.clear();
-    w.drop_behind(key, valid);
     for (; key < valid; key += stride) {
-        const bool more = key + stride < valid;
-        w.scores();
-        if (more) w.load_k(a, head, key + stride, valid);
+        w.scores(guard);
         w.step(a, head, b, r0, key, length, to_log2, kept);
-        if (more) w.load_v(a, head, key + stride, valid);
+        ask();
     }
-    w.leave(&sm.left.o[warp][0][0], sm.left.ml[warp]);
+    w.finish();
+    __syncthreads();                 // every ring is empty
+    w.leave(&left.o[warp][0][0], left.ml[warp]);
     __syncthreads();
     constexpr int PER = D / 8;
     for (int i = threadIdx.x; i < R8 * PER; i += 32 * kUnitWarps) {
         const int r = i / PER, c = i % PER * 8;
         float o[8];
-        const float2 ml = gather(sm.left, r, c, o);
+        const float2 ml = gather(left, r, c, o);
         if (ctas == 1) {
             if (r0 + r >= R) continue;
             const long long at = head * R + r0 + r;
@@ -693,14 +843,6 @@ struct ManyCfg {
 struct ManyMaps {
     CUtensorMap q, k, v;      // [B H][G T][d] in boxes of 128 rows, [B H][C][d] in tiles; 64 columns each
 };
-
-// Waits for what is already on its way, for a second at most, whether or not the CTA has given up.
-__device__ __forceinline__ void drain(uint64_t *bar, uint32_t parity)
-{
-    const uint64_t t0 = globaltimer_ns();
-    while (!ptx::mbar_try_wait(bar, parity))
-        if (globaltimer_ns() - t0 > 1000000000ull) return;
-}
 
 // Places of tile j's K and V among the n tiles' loads of a segment.
 template <int MODE>
@@ -1338,10 +1480,10 @@ struct Shape {
     bool many() const { return rows > 16; }
 };
 
-Shape shape_of(int R)
+Shape shape_of(int R, int d)
 {
-    if (R <= 8) return {8, 3 * kPlanSms};
-    if (R <= 16) return {16, 2 * kPlanSms};
+    if (R <= 8) return {8, (d == 128 ? FewCfg<128, 1>::BLOCKS : FewCfg<64, 1>::BLOCKS) * kPlanSms};
+    if (R <= 16) return {16, (d == 128 ? FewCfg<128, 2>::BLOCKS : FewCfg<64, 2>::BLOCKS) * kPlanSms};
     return {R <= 128 ? 128 : 256, kPlanSms};
 }
 
@@ -1362,15 +1504,37 @@ int unit_ctas(long long units, int C, int d)
     return units <= most && C <= steps * 16 * kUnitWarps * n ? n : 0;
 }
 
+bool make_kv_maps(KvMaps &maps, const CacheAttnArgs &a)
+{
+    const long long bh = (long long)a.B * a.H;
+    return make_map_3d(&maps.k, a.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.d, a.C, bh, 64, 16) == CUDA_SUCCESS &&
+           make_map_3d(&maps.v, a.v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.d, a.C, bh, 64, 16) == CUDA_SUCCESS;
+}
+
 template <int D, int NT>
 cudaError_t launch_unit(const CacheAttnArgs &a, int tiles, int ctas, float *kept, cudaStream_t stream)
 {
     static std::atomic<bool> set[64];
-    constexpr int bytes = (int)sizeof(UnitSmem<D, NT>);
+    constexpr int bytes = UnitCfg<D, NT>::SMEM;
+    KvMaps maps;
+    if (!make_kv_maps(maps, a)) return cudaErrorInvalidValue;
     const cudaError_t e = raise_smem(reinterpret_cast<const void *>(unit_kernel<D, NT>), bytes, set);
     if (e != cudaSuccess) return e;
     return launch_overlapped(unit_kernel<D, NT>, dim3((unsigned)(a.B * a.H) * tiles * ctas), dim3(32 * kUnitWarps), bytes,
-                             (unsigned)ctas, stream, a, tiles, kept);
+                             (unsigned)ctas, stream, maps, a, tiles, kept);
+}
+
+template <int D, int NT>
+cudaError_t launch_few(const CacheAttnArgs &a, const Plan &plan, const Parts &parts, int ctas, cudaStream_t stream)
+{
+    static std::atomic<bool> set[64];
+    constexpr int bytes = FewCfg<D, NT>::SMEM;
+    KvMaps maps;
+    if (!make_kv_maps(maps, a)) return cudaErrorInvalidValue;
+    const cudaError_t e = raise_smem(reinterpret_cast<const void *>(few_kernel<D, NT>), bytes, set);
+    if (e != cudaSuccess) return e;
+    return launch_overlapped(few_kernel<D, NT>, dim3((unsigned)ctas), dim3(kFewThreads), bytes, 1, stream, maps, a, plan,
+                             parts);
 }
 
 template <int D, int MODE>
@@ -1394,7 +1558,7 @@ template <int D>
 cudaError_t launch(const CacheAttnArgs &a, cudaStream_t stream)
 {
     const int R = a.G * a.T;
-    const Shape sh = shape_of(R);
+    const Shape sh = shape_of(R, D);
     const Plan plan = {a.H, (R + sh.rows - 1) / sh.rows, a.T, a.C, sh.many() ? kManyTile : kBlock};
     Parts parts;
     parts.o = static_cast<float *>(a.workspace);
@@ -1407,9 +1571,9 @@ cudaError_t launch(const CacheAttnArgs &a, cudaStream_t stream)
         e = sh.rows == 8 ? launch_unit<D, 1>(a, plan.tiles, unit, parts.scores, stream)
                          : launch_unit<D, 2>(a, plan.tiles, unit, parts.scores, stream);
     else if (sh.rows == 8)
-        e = launch_overlapped(few_kernel<D, 1>, dim3(sh.ctas), dim3(kFewThreads), 0, 1, stream, a, plan, parts);
+        e = launch_few<D, 1>(a, plan, parts, sh.ctas, stream);
     else if (sh.rows == 16)
-        e = launch_overlapped(few_kernel<D, 2>, dim3(sh.ctas), dim3(kFewThreads), 0, 1, stream, a, plan, parts);
+        e = launch_few<D, 2>(a, plan, parts, sh.ctas, stream);
     else
         e = sh.rows == 128 ? launch_many<D, 1>(a, plan, parts, sh.ctas, stream)
                            : launch_many<D, 2>(a, plan, parts, sh.ctas, stream);
@@ -1433,7 +1597,7 @@ cudaError_t launch(const CacheAttnArgs &a, cudaStream_t stream)
 
 size_t cache_attn_workspace(int B, int H, int G, int T, int C, int d, bool weights)
 {
-    const Shape sh = shape_of(G * T);
+    const Shape sh = shape_of(G * T, d);
     return parts_bytes(sh, d) + (weights && !sh.many() ? up256((size_t)B * H * G * T * C * 4) : 0);
 }
 
