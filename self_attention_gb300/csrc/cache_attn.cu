@@ -24,13 +24,12 @@
 #include "cluster.cuh"
 #include "common.cuh"
 #include "kernels.h"
-#include <cstdlib>
 
 namespace attn {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kFewWarps = 4;
+constexpr int kFewWarps = 8;
 constexpr int kFewThreads = 32 * kFewWarps;
 constexpr int kBlock = 16 * kFewWarps;   // slots of a block of work
 
@@ -579,12 +578,13 @@ __device__ __forceinline__ void write_o8(const CacheAttnArgs &a, long long row, 
 
 template <int D, int NT>
 struct FewCfg {
-    static constexpr int BLOCKS = NT == 1 ? 3 : 2;       // CTAs an SM
-    static constexpr int STAGES = D == 64 ? 4 : 2;
+    static constexpr int BLOCKS = D == 64 && NT == 1 ? 2 : 1;    // CTAs an SM
+    static constexpr int STAGES = NT == 1 ? 3 : D == 64 ? 5 : 2;
     using R = Rows<D, NT, STAGES>;
-    using L = Left<D, NT, 2>;
+    static constexpr int HALF = kFewWarps / 2;
+    using L = Left<D, NT, HALF>;
     static constexpr int HELD = NT * (D / 4 + 4) * 32;        // floats a warp hands over
-    static constexpr int RINGS = kFewWarps * (int)R::RING, HANDED = 2 * HELD * 4;
+    static constexpr int RINGS = kFewWarps * (int)R::RING, HANDED = HALF * HELD * 4;
     static constexpr int JOIN = HANDED > (int)sizeof(L) ? HANDED : (int)sizeof(L);
     static constexpr int SMEM = RINGS + JOIN + 256 + 1024;
     static_assert(BLOCKS * (SMEM + 1024) <= 228 * 1024, "");
@@ -647,12 +647,12 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, NT>::BLOCKS)
             w.step(a, seg.head, seg.b, r0, key, seg.length, to_log2, parts.scores);
             ask();
         }
-        // four warps' results become two, then one row each
-        if (warp >= 2) w.hand_over(handed + (warp - 2) * C::HELD);
+        // half of the warps take the others' results over, then the rows are put together
+        if (warp >= C::HALF) w.hand_over(handed + (warp - C::HALF) * C::HELD);
         __syncthreads();
-        if (warp < 2) {
+        if (warp < C::HALF) {
             w.take_over(handed + warp * C::HELD);
-            ptx::named_bar(1, 64);
+            ptx::named_bar(1, 32 * C::HALF);
             w.leave(&left.o[warp][0][0], left.ml[warp]);
         }
         __syncthreads();
@@ -1494,14 +1494,31 @@ size_t parts_bytes(const Shape &sh, int d)
     return up256(slots * d * 4) + up256(slots * 8);
 }
 
-// CTAs of a cluster that takes a unit whole (unit_kernel), or 0 where few_kernel and join_kernel do better.
-int unit_ctas(long long units, int C, int d)
+// CTAs of a cluster that takes a unit whole (unit_kernel), or 0 where few_kernel and join_kernel do better: the least
+// estimated time, in us, for caches that are full.  Fitted to both kernels over 1 to 1024 units of 100 to 64000 slots: a
+// step of 128 slots takes a CTA `step` at least, and the CTAs on the GPU together `hbm` each; `start` is what is left of
+// each for few slots, and few_kernel pays for every end of a unit.  (16 units of 1000 and 8000 slots: 5.6 and 17.8 us by
+// clusters of four, 7.6 and 16.7 by shares; 128 of 1000 and 16000: 12.9 and 160, 20.7 and 161.)  Sequences shorter than
+// the cache leave a long one to its cluster alone, so that it is never given more than 24 steps.
+int unit_ctas(long long units, int C, int d, int rows)
 {
-    static const char *e1 = getenv("UNIT_MAX"), *e2 = getenv("UNIT_STEPS");
-    const int most = e1 ? atoi(e1) : d == 64 ? 2 * kPlanSms : kPlanSms, steps = e2 ? atoi(e2) : 12;
-    int n = 1;
-    while (n < 8 && units * n * 2 <= most) n *= 2;
-    return units <= most && C <= steps * 16 * kUnitWarps * n ? n : 0;
+    const double hbm = d == 128 ? 0.0093 : 0.0047, step = rows == 8 ? 0.8 : 1.15;
+    const double start = rows == 8 ? 4.0 : 5.5, start_few = rows == 8 ? 7.5 : 11.5;
+    const long long slots = d == 128 ? kPlanSms : 2 * kPlanSms;              // resident CTAs
+    double best = start_few + (double)units * ((C + 127) / 128) * hbm + 1.7 * (double)units / slots;
+    int n_best = 0;
+    for (int n = 1; n <= 8; n *= 2) {
+        if (n == 8 && units > 8) break;                 // more clusters of eight wait for one another
+        const int steps = (C + 128 * n - 1) / (128 * n);
+        const long long wave = n == 4 ? slots * 18 / 19 : slots, ctas = units * n, rest = ctas % wave;
+        auto run = [&](long long active) { return steps * (active * hbm > step ? active * hbm : step) + 1.0; };
+        const double t = start - 1.0 + (double)(ctas / wave) * run(wave) + (rest ? run(rest) : 0.0);
+        if (steps <= 24 && t < best) {
+            best = t;
+            n_best = n;
+        }
+    }
+    return n_best;
 }
 
 bool make_kv_maps(KvMaps &maps, const CacheAttnArgs &a)
@@ -1566,7 +1583,7 @@ cudaError_t launch(const CacheAttnArgs &a, cudaStream_t stream)
     parts.scores = a.weights && !sh.many() ? reinterpret_cast<float *>(static_cast<char *>(a.workspace) + parts_bytes(sh, D))
                                            : nullptr;
     cudaError_t e;
-    const int unit = sh.many() ? 0 : unit_ctas((long long)a.B * a.H * plan.tiles, a.C, D);
+    const int unit = sh.many() ? 0 : unit_ctas((long long)a.B * a.H * plan.tiles, a.C, D, sh.rows);
     if (unit)
         e = sh.rows == 8 ? launch_unit<D, 1>(a, plan.tiles, unit, parts.scores, stream)
                          : launch_unit<D, 2>(a, plan.tiles, unit, parts.scores, stream);
