@@ -425,8 +425,8 @@ attn_status attn_cache_append(const void *k, const void *v, void *cache_k, void 
                               int d_k, int C, int rotated, int interleaved, float amplitude, cudaStream_t stream);
 
 /*
- * Bytes of device workspace attn_cache_attention() needs, with or without accumulated weights (0 for sizes it
- * rejects).
+ * Bytes of device workspace attn_cache_attention() needs, with or without accumulated weights; 0 where it needs none
+ * (the call then takes a null workspace) and for sizes it rejects.
  */
 size_t attn_cache_attention_workspace_size(int B, int H, int G, int T, int C, int d_k, int with_weights);
 

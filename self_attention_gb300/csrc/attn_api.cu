@@ -1200,6 +1200,7 @@ attn_status check_evict(int B, int H, int C, int d_k, int keep)
 
 bool workspace_ok(const void *p, size_t have, size_t need)
 {
+    if (need == 0) return true;
     return p && (reinterpret_cast<uintptr_t>(p) & 255u) == 0 && have >= need;
 }
 
@@ -1277,7 +1278,8 @@ extern "C" attn_status attn_cache_attention(const void *q, const void *cache_k, 
     const size_t bh = (size_t)B * H, cache = bh * C * d_k * 2, qs = bh * G * T * d_k * 2;
     const Part ins[7] = {{weights, bh * C * 4, 4}, {q, qs, 16}, {cache_k, cache, 16}, {cache_v, cache, 16},
                          {lengths, (size_t)B * 4, 4}, {tree, (size_t)B * T * 8, 8}, {counted, (size_t)B * 8, 8}};
-    const Part outs[4] = {{o, qs, 16}, {lse, bh * G * T * 4, 4}, {weights_out, bh * C * 4, 4, 0}, {workspace, need, 256}};
+    const Part outs[4] = {{o, qs, 16}, {lse, bh * G * T * 4, 4}, {weights_out, bh * C * 4, 4, 0},
+                          {need ? workspace : nullptr, need, 256}};
     if ((st = check_parts(ins, outs)) != ATTN_OK) return st;
     DeviceState *dev = nullptr;
     if ((st = device_state(&dev)) != ATTN_OK) return st;

@@ -550,10 +550,11 @@ PyObject *cache_attention(Args a)
         const int G = count(q.H / k.H);
         const size_t bytes =
             attn_cache_attention_workspace_size(count(q.B), count(k.H), G, count(q.N), count(k.N), count(q.d), weights != nullptr);
-        const at::Tensor ws = empty({(int64_t)(bytes ? bytes : 1)}, at::kByte, q.dev);
+        at::Tensor ws;
+        if (bytes) ws = empty({(int64_t)bytes}, at::kByte, q.dev);
         code = attn_cache_attention(q.t.data_ptr(), k.t.data_ptr(), v, lengths, tree, counted, weights,
                                     fresh ? static_cast<float *>(out.data_ptr()) : given, o.data_ptr(),
-                                    static_cast<float *>(lse.data_ptr()), ws.data_ptr(), bytes, count(q.B),
+                                    static_cast<float *>(lse.data_ptr()), at_or_null(ws), bytes, count(q.B),
                                     count(k.H), G, count(q.N), count(k.N), count(q.d), scale, stream(q.dev));
     }
     check(code, "attn_cache_attention");

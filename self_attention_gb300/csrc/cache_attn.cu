@@ -1374,35 +1374,51 @@ __global__ void __launch_bounds__(256) join_many_kernel(CacheAttnArgs a, Plan pl
     if (col == 0 && warp == 0 && r0 + lane < R) a.lse[(long long)head * R + r0 + lane] = sum.lse();
 }
 
-// weights_out = weights + the weights that the counted rows give each slot, from the scores that few_kernel kept: a
-// thread a slot.  At up to 16 rows the scores (4 bytes a row and slot, twice) are less than K (2 d bytes) a second time.
-__global__ void __launch_bounds__(256) kept_weights_kernel(CacheAttnArgs a, int blocks, const float *scores)
+// weights_out = weights + the weights that the counted rows give each slot, from the scores that were kept: four slots a
+// thread, 256 apart.  At up to 16 rows the scores (4 bytes a row and slot, twice, mostly in L2) are less than K (2 d
+// bytes) a second time.
+constexpr int kKeptSlots = 1024;     // a block
+
+__global__ void __launch_bounds__(256) kept_weights_kernel(const __grid_constant__ CacheAttnArgs a, int blocks,
+                                                           const float *scores)
 {
     __shared__ float lse[16];
     ptx::grid_dep_launch();
     const int head = (int)(blockIdx.x / (unsigned)blocks), b = head / a.H, T = a.T, R = a.G * T;
-    const int j = (int)(blockIdx.x % (unsigned)blocks) * 256 + threadIdx.x;
+    const int j0 = (int)(blockIdx.x % (unsigned)blocks) * kKeptSlots + threadIdx.x;
     ptx::grid_dep_wait();
+    const int valid = length_of(a.lengths, b, T, a.C) + T;
+    const long long at = (long long)head * a.C + j0;
+    const float *from = scores + (long long)head * R * a.C + j0;
+    float was[4], s[4], sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        was[e] = j0 + 256 * e < a.C ? a.weights[at + 256 * e] : 0.f;
+        s[e] = j0 + 256 * e < valid ? from[256 * e] : -INFINITY;
+    }
     if (threadIdx.x < R) {
         const bool counted = !a.counted || (a.counted[b] >> (threadIdx.x % T) & 1);
         lse[threadIdx.x] = counted ? a.lse[(long long)head * R + threadIdx.x] * kLog2e : INFINITY;
     }
-    const int valid = length_of(a.lengths, b, T, a.C) + T;
     __syncthreads();
-    if (j >= a.C) return;
-    const long long at = (long long)head * a.C + j;
-    if (j >= valid && a.weights_out == a.weights) return;
-    const float was = a.weights[at];
-    float sum = 0.f;
-    if (j < valid) {
-        const float *from = scores + (long long)head * R * a.C + j;
-#pragma unroll 4
-        for (int r = 0; r < R; ++r) {
-            const float s = from[(long long)r * a.C];
-            if (lse[r] != INFINITY && s != -INFINITY) sum += ptx::ex2(s - lse[r]);
+#pragma unroll 2
+    for (int r = 0; r < R; ++r) {
+        float next[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            next[e] = r + 1 < R && j0 + 256 * e < valid ? from[(long long)(r + 1) * a.C + 256 * e] : -INFINITY;
+        const float x = lse[r];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (x != INFINITY && s[e] != -INFINITY) sum[e] += ptx::ex2(s[e] - x);
+            s[e] = next[e];
         }
     }
-    a.weights_out[at] = was + sum;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int j = j0 + 256 * e;
+        if (j < valid || (j < a.C && a.weights_out != a.weights)) a.weights_out[at + 256 * e] = was[e] + sum[e];
+    }
 }
 
 // The same for more rows: K is read a second time, the rows in eights.  A block takes 64 slots of one (sequence,
@@ -1577,13 +1593,13 @@ cudaError_t launch(const CacheAttnArgs &a, cudaStream_t stream)
     const int R = a.G * a.T;
     const Shape sh = shape_of(R, D);
     const Plan plan = {a.H, (R + sh.rows - 1) / sh.rows, a.T, a.C, sh.many() ? kManyTile : kBlock};
+    const int unit = sh.many() ? 0 : unit_ctas((long long)a.B * a.H * plan.tiles, a.C, D, sh.rows);
     Parts parts;
     parts.o = static_cast<float *>(a.workspace);
     parts.ml = reinterpret_cast<float2 *>(static_cast<char *>(a.workspace) + up256((size_t)2 * sh.ctas * sh.rows * D * 4));
-    parts.scores = a.weights && !sh.many() ? reinterpret_cast<float *>(static_cast<char *>(a.workspace) + parts_bytes(sh, D))
+    parts.scores = a.weights && !sh.many() ? reinterpret_cast<float *>(static_cast<char *>(a.workspace) + (unit ? 0 : parts_bytes(sh, D)))
                                            : nullptr;
     cudaError_t e;
-    const int unit = sh.many() ? 0 : unit_ctas((long long)a.B * a.H * plan.tiles, a.C, D, sh.rows);
     if (unit)
         e = sh.rows == 8 ? launch_unit<D, 1>(a, plan.tiles, unit, parts.scores, stream)
                          : launch_unit<D, 2>(a, plan.tiles, unit, parts.scores, stream);
@@ -1601,7 +1617,7 @@ cudaError_t launch(const CacheAttnArgs &a, cudaStream_t stream)
                                       plan, sh.rows, sh.ctas, parts);
     if (e != cudaSuccess || !a.weights) return e;
     if (!sh.many()) {
-        const int blocks = (a.C + 255) / 256;
+        const int blocks = (a.C + kKeptSlots - 1) / kKeptSlots;
         return launch_overlapped(kept_weights_kernel, dim3((unsigned)(a.B * a.H) * blocks), dim3(256), 0, 1, stream, a, blocks,
                                  (const float *)parts.scores);
     }
@@ -1615,7 +1631,8 @@ cudaError_t launch(const CacheAttnArgs &a, cudaStream_t stream)
 size_t cache_attn_workspace(int B, int H, int G, int T, int C, int d, bool weights)
 {
     const Shape sh = shape_of(G * T, d);
-    return parts_bytes(sh, d) + (weights && !sh.many() ? up256((size_t)B * H * G * T * C * 4) : 0);
+    const bool split = sh.many() || unit_ctas((long long)B * H * ((G * T + sh.rows - 1) / sh.rows), C, d, sh.rows) == 0;
+    return (split ? parts_bytes(sh, d) : 0) + (weights && !sh.many() ? up256((size_t)B * H * G * T * C * 4) : 0);
 }
 
 cudaError_t launch_cache_attn(const CacheAttnArgs &a, cudaStream_t stream)
