@@ -452,6 +452,17 @@ attn_status attn_cache_attention(const void *q, const void *cache_k, const void 
                                  float *weights_out, void *o, float *lse, void *workspace, size_t workspace_bytes,
                                  int B, int H, int G, int T, int C, int d_k, float scale, cudaStream_t stream);
 
+/*
+ * Diagnostics: the kernels that attn_cache_attention() runs for these sizes, decided on the host (no GPU is needed).
+ * Writes three ints:
+ *   plan[0]  1: units of a cached head's rows whole, by clusters; 2: shared out in blocks of slots, and joined;
+ *            3 and 4: the same for more rows, on the larger tiles (3 by one CTA each)
+ *   plan[1]  rows of a unit (8, 16, 128 or 256)
+ *   plan[2]  1: CTAs of a cluster; 2 and 4: CTAs that share the work; 3: 0
+ * For tests, which assert that they reach every kernel.
+ */
+attn_status attn_debug_cache_plan(int B, int H, int G, int T, int C, int d_k, int *plan);
+
 /* Bytes of device workspace attn_cache_evict() needs (0 for sizes it rejects). */
 size_t attn_cache_evict_workspace_size(int B, int H, int C, int d_k, int keep);
 

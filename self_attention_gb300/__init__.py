@@ -39,7 +39,7 @@ __all__ = [
     "rms_norm_forward", "rms_norm_backward", "rms_norm", "rms_norm_q8", "quantize_q8", "linear_q8",
     "attn_debug_linear_plan", "ACTIVATIONS",
     "attn_rotary", "attn_rotary_bwd", "attn_cache_append", "attn_cache_attention", "attn_cache_attention_workspace_size",
-    "attn_cache_evict", "attn_cache_evict_workspace_size",
+    "attn_cache_evict", "attn_cache_evict_workspace_size", "attn_debug_cache_plan",
     "rotary_turns", "rotary_forward", "rotary_backward", "rotary", "cache_append", "cache_attention", "cache_evict",
     "tree_words",
     "load_library", "STATUS",
@@ -60,7 +60,8 @@ EXPORTS = ("attn_fwd", "attn_fwd_workspace_size", "attn_fwd_with_workspace", "at
            "attn_rms_norm_bwd", "attn_rms_norm_bwd_workspace_size", "attn_rms_norm_q8",
            "attn_quantize_q8", "attn_debug_linear_plan",
            "attn_rotary", "attn_rotary_bwd", "attn_cache_append", "attn_cache_attention",
-           "attn_cache_attention_workspace_size", "attn_cache_evict", "attn_cache_evict_workspace_size")
+           "attn_cache_attention_workspace_size", "attn_cache_evict", "attn_cache_evict_workspace_size",
+           "attn_debug_cache_plan")
 # attn_activation
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
@@ -142,6 +143,7 @@ def load_library(path: str = LIB_PATH):
                        ("attn_cache_append", [_VP] * 12 + [_I] * 9 + [_F, _VP]),
                        ("attn_cache_attention", [_VP] * 11 + [_SZ] + [_I] * 6 + [_F, _VP]),
                        ("attn_cache_evict", [_VP] * 9 + [_SZ] + [_I] * 6 + [_VP]),
+                       ("attn_debug_cache_plan", [_I] * 6 + [_VP]),
                        ("attn_debug_linear_plan", [_I] * 7 + [_VP])):
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = _I
@@ -404,6 +406,13 @@ def attn_cache_attention(q, cache_k, cache_v, lengths, tree, counted, weights, w
         _ptr(q), _ptr(cache_k), _ptr(cache_v), _ptr(lengths), _opt(tree), _opt(counted), _opt(weights),
         _opt(weights_out), _ptr(o), _ptr(lse), _ptr(workspace), int(workspace_bytes), B, H, G, T, C, d_k,
         float(scale), _stream(stream)), "attn_cache_attention")
+
+
+def attn_debug_cache_plan(B: int, H: int, G: int, T: int, C: int, d_k: int):
+    """(kind, rows of a unit, CTAs): the kernels that attn_cache_attention() runs, decided on the host (see attn.h)."""
+    plan = (_I * 3)()
+    _raise(load_library().attn_debug_cache_plan(B, H, G, T, C, d_k, plan), "attn_debug_cache_plan")
+    return tuple(plan)
 
 
 def attn_cache_evict_workspace_size(B: int, H: int, C: int, d_k: int, keep: int) -> int:

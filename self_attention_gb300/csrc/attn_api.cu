@@ -1292,6 +1292,15 @@ extern "C" attn_status attn_cache_attention(const void *q, const void *cache_k, 
     return e == cudaSuccess ? ATTN_OK : fail("attn_cache_attention launch", e);
 }
 
+extern "C" attn_status attn_debug_cache_plan(int B, int H, int G, int T, int C, int d_k, int *plan)
+{
+    const attn_status st = check_cache_attention(B, H, G, T, C, d_k);
+    if (st != ATTN_OK) return st;
+    if (!plan) return ATTN_ERR_INVALID_ARG;
+    cache_attn_plan(B, H, G, T, C, d_k, plan);
+    return ATTN_OK;
+}
+
 extern "C" size_t attn_cache_evict_workspace_size(int B, int H, int C, int d_k, int keep)
 {
     return check_evict(B, H, C, d_k, keep) == ATTN_OK ? align256(evict_workspace(B, H, C, keep)) : 0;

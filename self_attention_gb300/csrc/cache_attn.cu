@@ -85,6 +85,7 @@ __device__ __forceinline__ void drop_odd(uint4 &v)
 struct Plan {
     int H, tiles, T, C;
     int block;       // slots a block of work
+    int whole;       // a CTA takes one unit whole (and nothing is shared out)
 };
 
 // Slots of the cache ahead of the new tokens.
@@ -141,6 +142,15 @@ struct Walk {
     {
         const uint32_t lane = threadIdx.x & 31;
         const long long per_unit = (long long)p.H * p.tiles;
+        if (p.whole) {
+            b = (int)(blockIdx.x / (unsigned)per_unit);
+            length = length_of(lengths, b, p.T, p.C);
+            nb = blocks_of(length, p);
+            before = 0;
+            x = (long long)(blockIdx.x % (unsigned)per_unit) * nb;
+            end = x + nb;
+            return true;
+        }
         int len = (int)lane < B ? length_of(lengths, (int)lane, p.T, p.C) : 0, inc;
         int n = (int)lane < B ? blocks_of(len, p) : 0;
         auto scan = [&] {         // blocks of these 32 sequences up to the lane's own
@@ -892,6 +902,11 @@ __global__ void __launch_bounds__(384, 1)
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = tmem_sh;
+    if (threadIdx.x == 32 * C::TMA_WARP) {
+        ptx::tma_prefetch_desc(&maps.q);
+        ptx::tma_prefetch_desc(&maps.k);
+        ptx::tma_prefetch_desc(&maps.v);
+    }
     ptx::grid_dep_launch();      // (not before tensor memory is this kernel's)
     ptx::grid_dep_wait();
 
@@ -904,9 +919,6 @@ __global__ void __launch_bounds__(384, 1)
     } else if (warp == C::TMA_WARP) {
         // ---------------------------------------------------------------- TMA producer
         if (ptx::elect_one()) {
-            ptx::tma_prefetch_desc(&maps.q);
-            ptx::tma_prefetch_desc(&maps.k);
-            ptx::tma_prefetch_desc(&maps.v);
             uint32_t seq = 0;
             uint32_t segs = 0;       // whose Q was asked for
             bool ok = true;          // nothing more is asked for once a wait has given up
@@ -1490,52 +1502,77 @@ __global__ void __launch_bounds__(kFewThreads) weights_kernel(CacheAttnArgs a, i
 constexpr int kPlanSms = 152;    // the split is a function of the sizes and lengths alone
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// Rows a unit, and CTAs that share the work.
-struct Shape {
-    int rows, ctas;
-    bool many() const { return rows > 16; }
+// Which kernels a call runs, a function of the sizes alone.
+enum Kind { kUnit = 1, kFew = 2, kManyWhole = 3, kMany = 4 };
+struct Choice {
+    Kind kind;
+    int rows;        // of a unit
+    int ctas;        // kUnit: of a cluster; kFew, kMany: that share the work
+    bool few_rows() const { return rows <= 16; }
+    bool parts() const { return kind == kFew || kind == kMany; }
 };
 
-Shape shape_of(int R, int d)
+long long units_of(int B, int H, int R, int rows) { return (long long)B * H * ((R + rows - 1) / rows); }
+
+// Time in us of CTAs that take `steps` steps each, `wave` of them at a time, where a step takes a CTA `step` at least and
+// the CTAs on the GPU together `hbm` each.
+double waves(long long ctas, long long wave, int steps, double step, double hbm)
 {
-    if (R <= 8) return {8, (d == 128 ? FewCfg<128, 1>::BLOCKS : FewCfg<64, 1>::BLOCKS) * kPlanSms};
-    if (R <= 16) return {16, (d == 128 ? FewCfg<128, 2>::BLOCKS : FewCfg<64, 2>::BLOCKS) * kPlanSms};
-    return {R <= 128 ? 128 : 256, kPlanSms};
+    auto run = [&](long long active) { return steps * (active * hbm > step ? active * hbm : step) + 1.0; };
+    return (double)(ctas / wave) * run(wave) + (ctas % wave ? run(ctas % wave) : 0.0) - 1.0;
 }
 
-// Bytes of the parts' results.
-size_t parts_bytes(const Shape &sh, int d)
+// The least estimated time for caches that are full.  Fitted to the kernels over 1 to 1024 units of 100 to 64000 slots
+// (steps of 128 slots; the constants are what is left for few slots, a step's time, and the cost of a unit's end).  A
+// unit by a cluster against shares and a join: 16 units of 1000 and 8000 slots 5.6 and 17.8 us, 7.6 and 16.7; 128 units
+// of 1000 and 16000 12.9 and 160, 20.7 and 161.  Sequences shorter than the cache leave a long one to its cluster or CTA
+// alone, so that it is never given more than 24 steps.
+Choice choose(int B, int H, int G, int T, int C, int d)
 {
-    const size_t slots = (size_t)2 * sh.ctas * sh.rows;
-    return up256(slots * d * 4) + up256(slots * 8);
-}
-
-// CTAs of a cluster that takes a unit whole (unit_kernel), or 0 where few_kernel and join_kernel do better: the least
-// estimated time, in us, for caches that are full.  Fitted to both kernels over 1 to 1024 units of 100 to 64000 slots: a
-// step of 128 slots takes a CTA `step` at least, and the CTAs on the GPU together `hbm` each; `start` is what is left of
-// each for few slots, and few_kernel pays for every end of a unit.  (16 units of 1000 and 8000 slots: 5.6 and 17.8 us by
-// clusters of four, 7.6 and 16.7 by shares; 128 of 1000 and 16000: 12.9 and 160, 20.7 and 161.)  Sequences shorter than
-// the cache leave a long one to its cluster alone, so that it is never given more than 24 steps.
-int unit_ctas(long long units, int C, int d, int rows)
-{
-    const double hbm = d == 128 ? 0.0093 : 0.0047, step = rows == 8 ? 0.8 : 1.15;
-    const double start = rows == 8 ? 4.0 : 5.5, start_few = rows == 8 ? 7.5 : 11.5;
-    const long long slots = d == 128 ? kPlanSms : 2 * kPlanSms;              // resident CTAs
-    double best = start_few + (double)units * ((C + 127) / 128) * hbm + 1.7 * (double)units / slots;
-    int n_best = 0;
+    constexpr int kMostSteps = 24;
+    const int R = G * T, slots128 = (C + 127) / 128;
+    const double hbm = d == 128 ? 0.0093 : 0.0047;
+    Choice best = {kFew, R <= 8 ? 8 : 16, 0};
+    const long long units = units_of(B, H, R, best.rows), wave = d == 128 ? kPlanSms : 2 * kPlanSms;
+    const double step = best.rows == 8 ? 0.8 : 1.15, start = best.rows == 8 ? 4.0 : 5.5;
+    best.ctas = (best.rows == 8 ? d == 128 ? FewCfg<128, 1>::BLOCKS : FewCfg<64, 1>::BLOCKS
+                                : d == 128 ? FewCfg<128, 2>::BLOCKS : FewCfg<64, 2>::BLOCKS) * kPlanSms;
+    double t_best = (best.rows == 8 ? 7.5 : 11.5) + (double)units * slots128 * hbm + 1.7 * (double)units / wave;
+    if (R > 16) {
+        const int rows = R <= 128 ? 128 : 256;
+        const long long many = units_of(B, H, R, rows);
+        // both streams of 128 rows' tiles run at once
+        const double tile = (rows == 256 ? 1.8 : 0.9) * (d == 128 ? 1.0 : 0.85);
+        best = {kMany, rows, kPlanSms};
+        t_best = 15.5 + (double)many * slots128 * (tile / kPlanSms > hbm ? tile / kPlanSms : hbm) + 4.0 * (double)many / kPlanSms;
+        const double t = 4.5 + waves(many, kPlanSms, slots128, tile, hbm) + 3.0 * (double)((many + kPlanSms - 1) / kPlanSms);
+        if (slots128 <= kMostSteps && t < t_best) {
+            best = {kManyWhole, rows, 0};
+            t_best = t;
+        }
+    }
     for (int n = 1; n <= 8; n *= 2) {
         if (n == 8 && units > 8) break;                 // more clusters of eight wait for one another
         const int steps = (C + 128 * n - 1) / (128 * n);
-        const long long wave = n == 4 ? slots * 18 / 19 : slots, ctas = units * n, rest = ctas % wave;
-        auto run = [&](long long active) { return steps * (active * hbm > step ? active * hbm : step) + 1.0; };
-        const double t = start - 1.0 + (double)(ctas / wave) * run(wave) + (rest ? run(rest) : 0.0);
-        if (steps <= 24 && t < best) {
-            best = t;
-            n_best = n;
+        const double t = start + waves(units * n, n == 4 ? wave * 18 / 19 : wave, steps, step, hbm);
+        if (steps <= kMostSteps && t < t_best) {
+            best = {kUnit, R <= 8 ? 8 : 16, n};
+            t_best = t;
         }
     }
-    return n_best;
+    return best;
 }
+
+// Bytes of the parts' results.
+size_t parts_bytes(const Choice &c, int d)
+{
+    if (!c.parts()) return 0;
+    const size_t slots = (size_t)2 * c.ctas * c.rows;
+    return up256(slots * d * 4) + up256(slots * 8);
+}
+
+// Scores are kept for the accumulated weights where a cached head has few rows in all.
+bool keeps_scores(const Choice &c, int R) { return c.few_rows() && R <= 16; }
 
 bool make_kv_maps(KvMaps &maps, const CacheAttnArgs &a)
 {
@@ -1591,48 +1628,57 @@ template <int D>
 cudaError_t launch(const CacheAttnArgs &a, cudaStream_t stream)
 {
     const int R = a.G * a.T;
-    const Shape sh = shape_of(R, D);
-    const Plan plan = {a.H, (R + sh.rows - 1) / sh.rows, a.T, a.C, sh.many() ? kManyTile : kBlock};
-    const int unit = sh.many() ? 0 : unit_ctas((long long)a.B * a.H * plan.tiles, a.C, D, sh.rows);
-    Parts parts;
-    parts.o = static_cast<float *>(a.workspace);
-    parts.ml = reinterpret_cast<float2 *>(static_cast<char *>(a.workspace) + up256((size_t)2 * sh.ctas * sh.rows * D * 4));
-    parts.scores = a.weights && !sh.many() ? reinterpret_cast<float *>(static_cast<char *>(a.workspace) + (unit ? 0 : parts_bytes(sh, D)))
-                                           : nullptr;
+    const Choice c = choose(a.B, a.H, a.G, a.T, a.C, D);
+    const Plan plan = {a.H, (R + c.rows - 1) / c.rows, a.T, a.C, c.few_rows() ? kBlock : kManyTile, c.kind == kManyWhole};
+    const unsigned heads = (unsigned)a.B * (unsigned)a.H;
+    char *ws = static_cast<char *>(a.workspace);
+    Parts parts = {};
+    if (c.parts()) {
+        parts.o = reinterpret_cast<float *>(ws);
+        parts.ml = reinterpret_cast<float2 *>(ws + up256((size_t)2 * c.ctas * c.rows * D * 4));
+    }
+    const bool kept = a.weights && keeps_scores(c, R);
+    if (kept) parts.scores = reinterpret_cast<float *>(ws + parts_bytes(c, D));
     cudaError_t e;
-    if (unit)
-        e = sh.rows == 8 ? launch_unit<D, 1>(a, plan.tiles, unit, parts.scores, stream)
-                         : launch_unit<D, 2>(a, plan.tiles, unit, parts.scores, stream);
-    else if (sh.rows == 8)
-        e = launch_few<D, 1>(a, plan, parts, sh.ctas, stream);
-    else if (sh.rows == 16)
-        e = launch_few<D, 2>(a, plan, parts, sh.ctas, stream);
+    if (c.kind == kUnit)
+        e = c.rows == 8 ? launch_unit<D, 1>(a, plan.tiles, c.ctas, parts.scores, stream)
+                        : launch_unit<D, 2>(a, plan.tiles, c.ctas, parts.scores, stream);
+    else if (c.kind == kFew)
+        e = c.rows == 8 ? launch_few<D, 1>(a, plan, parts, c.ctas, stream) : launch_few<D, 2>(a, plan, parts, c.ctas, stream);
     else
-        e = sh.rows == 128 ? launch_many<D, 1>(a, plan, parts, sh.ctas, stream)
-                           : launch_many<D, 2>(a, plan, parts, sh.ctas, stream);
+        e = c.rows == 128 ? launch_many<D, 1>(a, plan, parts, c.kind == kMany ? c.ctas : (int)(heads * plan.tiles), stream)
+                          : launch_many<D, 2>(a, plan, parts, c.kind == kMany ? c.ctas : (int)(heads * plan.tiles), stream);
     if (e != cudaSuccess) return e;
-    if (!unit) e = sh.many() ? launch_overlapped(join_many_kernel<D>, dim3((unsigned)(a.B * a.H) * plan.tiles * (sh.rows / 32) * (D / 32)),
-                                      dim3(256), 0, 1, stream, a, plan, sh.rows, sh.ctas, parts)
-                  : launch_overlapped(join_kernel<D>, dim3((unsigned)(a.B * a.H) * R), dim3(32 * kJoinWarps), 0, 1, stream, a,
-                                      plan, sh.rows, sh.ctas, parts);
+    if (c.kind == kFew)
+        e = launch_overlapped(join_kernel<D>, dim3(heads * R), dim3(32 * kJoinWarps), 0, 1, stream, a, plan, c.rows, c.ctas,
+                              parts);
+    if (c.kind == kMany)
+        e = launch_overlapped(join_many_kernel<D>, dim3(heads * plan.tiles * (c.rows / 32) * (D / 32)), dim3(256), 0, 1,
+                              stream, a, plan, c.rows, c.ctas, parts);
     if (e != cudaSuccess || !a.weights) return e;
-    if (!sh.many()) {
+    if (kept) {
         const int blocks = (a.C + kKeptSlots - 1) / kKeptSlots;
-        return launch_overlapped(kept_weights_kernel, dim3((unsigned)(a.B * a.H) * blocks), dim3(256), 0, 1, stream, a, blocks,
+        return launch_overlapped(kept_weights_kernel, dim3(heads * blocks), dim3(256), 0, 1, stream, a, blocks,
                                  (const float *)parts.scores);
     }
     const int blocks = (a.C + kBlock - 1) / kBlock;
-    return launch_overlapped(weights_kernel<D>, dim3((unsigned)((long long)a.B * a.H * blocks)), dim3(kFewThreads), 0, 1,
-                             stream, a, blocks);
+    return launch_overlapped(weights_kernel<D>, dim3(heads * blocks), dim3(kFewThreads), 0, 1, stream, a, blocks);
 }
 
 }  // namespace
 
 size_t cache_attn_workspace(int B, int H, int G, int T, int C, int d, bool weights)
 {
-    const Shape sh = shape_of(G * T, d);
-    const bool split = sh.many() || unit_ctas((long long)B * H * ((G * T + sh.rows - 1) / sh.rows), C, d, sh.rows) == 0;
-    return (split ? parts_bytes(sh, d) : 0) + (weights && !sh.many() ? up256((size_t)B * H * G * T * C * 4) : 0);
+    const Choice c = choose(B, H, G, T, C, d);
+    return parts_bytes(c, d) + (weights && keeps_scores(c, G * T) ? up256((size_t)B * H * G * T * C * 4) : 0);
+}
+
+void cache_attn_plan(int B, int H, int G, int T, int C, int d, int plan[3])
+{
+    const Choice c = choose(B, H, G, T, C, d);
+    plan[0] = c.kind;
+    plan[1] = c.rows;
+    plan[2] = c.ctas;
 }
 
 cudaError_t launch_cache_attn(const CacheAttnArgs &a, cudaStream_t stream)

@@ -222,6 +222,8 @@ struct CacheAttnArgs {
     int *status;
 };
 size_t cache_attn_workspace(int B, int H, int G, int T, int C, int d, bool weights);
+// The kernels that a call runs (as attn_debug_cache_plan() tells them).
+void cache_attn_plan(int B, int H, int G, int T, int C, int d, int plan[3]);
 cudaError_t launch_cache_attn(const CacheAttnArgs &a, cudaStream_t stream);
 
 struct EvictArgs {

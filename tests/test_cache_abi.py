@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import self_attention_gb300 as sa
+import _cache_plans
 import _cache_ref as ref
 from self_attention_gb300.build import build
 
@@ -99,6 +100,15 @@ def test_sizes_of_the_largest_workspaces():
     for T, G in ((64, 128), (1, 16384), (64, 1)):
         assert 0 < sa.attn_cache_attention_workspace_size(1, 1, G, T, 1 << 20, 128) < 1 << 32
     assert sa.attn_cache_evict_workspace_size(4, 16, 1 << 20, 128, 1 << 19) >= 4 * 16 * (1 << 19) * 8
+
+
+def test_plans_of_attention_are_all_reached(lib):
+    """The GPU tests' sizes reach every kernel that the plan chooses from."""
+    want = {(k, r, d) for d in (64, 128) for k, rows in ((1, (8, 16)), (2, (8, 16)), (3, (128, 256)), (4, (128, 256))) for r in rows}
+    assert _cache_plans.reached() >= want, want - _cache_plans.reached()
+    with pytest.raises(sa.AttnError):
+        sa.attn_debug_cache_plan(1, 1, 1, 65, 100, 64)
+    assert lib.attn_debug_cache_plan(1, 1, 1, 1, 100, 64, None) == 1
 
 
 def test_tree_words():

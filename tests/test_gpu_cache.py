@@ -8,6 +8,7 @@ import torch
 
 import self_attention_gb300 as sa
 import _cache_ref as ref
+from _cache_plans import BLOCKS, CASES, ODD, POISON, ROOM
 
 pytestmark = pytest.mark.gpu
 NAN = float("nan")
@@ -100,31 +101,11 @@ def test_append_of_rows_and_lengths_out_of_range():
 
 
 # ------------------------------------------------------------------ attention
-CASES = [
-    # B, H, G, T, d, C, lengths
-    (1, 1, 1, 1, 64, 1, [0]),
-    (1, 1, 1, 1, 128, 130, [129]),
-    (2, 3, 4, 1, 128, 200, [63, 64]),
-    (3, 2, 1, 1, 64, 1000, [0, 999, 500]),
-    (2, 1, 8, 1, 128, 77, [15, 16]),
-    (2, 2, 9, 1, 64, 300, [290, 17]),
-    (1, 2, 16, 1, 128, 2100, [2050]),
-    (5, 1, 17, 1, 64, 90, [1, 2, 3, 88, 31]),
-    (2, 2, 1, 5, 128, 140, [120, 0]),
-    (2, 3, 2, 13, 64, 270, [255, 128]),
-    (1, 1, 4, 33, 128, 700, [600]),
-    (2, 2, 4, 64, 128, 330, [266, 1]),
-    (1, 2, 8, 64, 64, 400, [200]),
-    (2, 1, 3, 50, 128, 200, [127, 128]),
-    (1, 1, 1, 64, 64, 64, [0]),
-    (40, 2, 2, 1, 64, 70, [i % 69 for i in range(40)]),
-]
-
-
 @pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(map(str, c[:6])))
-@pytest.mark.parametrize("masked", [False, True])
-def test_attention(case, masked):
+@pytest.mark.parametrize("masked,room", [(False, 0), (True, 0), (True, ROOM)])
+def test_attention(case, masked, room):
     B, H, G, T, d, C, lens = case
+    C = max(C, room)
     g = _gen(case, masked)
     q = _randn(g, B, H * G, T, d, std=2.0)
     k, v = _cache(g, B, H, C, d, lens, T)
@@ -138,9 +119,10 @@ def test_attention(case, masked):
 
 
 @pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(map(str, c[:6])))
-@pytest.mark.parametrize("some", [False, True])
-def test_weights(case, some):
+@pytest.mark.parametrize("some,room", [(False, 0), (True, 0), (True, ROOM)])
+def test_weights(case, some, room):
     B, H, G, T, d, C, lens = case
+    C = max(C, room)
     g = _gen(case, some, "weights")
     q = _randn(g, B, H * G, T, d, std=2.0)
     k, v = _cache(g, B, H, C, d, lens, T)
@@ -160,10 +142,7 @@ def test_weights(case, some):
     assert torch.equal(o, plain[0]) and torch.equal(lse, plain[1])
 
 
-@pytest.mark.parametrize("B,H,G,T,d,C,ragged", [
-    (8, 4, 2, 10, 128, 1500, 1400), (8, 4, 2, 10, 64, 1500, 1400), (6, 4, 4, 50, 128, 1700, 900), (6, 4, 4, 64, 64, 1700, 1600),
-    (3, 5, 8, 60, 128, 2900, 100), (40, 8, 1, 33, 64, 300, 260), (2, 3, 2, 64, 128, 20000, 5000), (33, 7, 4, 64, 128, 270, 200),
-    (9, 16, 4, 1, 128, 5000, 4900), (9, 16, 3, 4, 64, 5000, 4900), (300, 1, 1, 20, 64, 200, 130), (1, 1, 4, 64, 128, 30000, 0)])
+@pytest.mark.parametrize("B,H,G,T,d,C,ragged", BLOCKS)
 @pytest.mark.parametrize("masked", [False, True])
 def test_attention_over_many_blocks(B, H, G, T, d, C, ragged, masked):
     """CTAs with runs of blocks, and runs over several heads and sequences."""
@@ -181,11 +160,12 @@ def test_attention_over_many_blocks(B, H, G, T, d, C, ragged, masked):
     assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
 
 
-@pytest.mark.parametrize("T,G", [(3, 1), (20, 2), (64, 4)])
-def test_rows_that_see_nothing_or_odd_sets(T, G):
+@pytest.mark.parametrize("T,G,d", ODD)
+@pytest.mark.parametrize("C", [150, ROOM])
+def test_rows_that_see_nothing_or_odd_sets(T, G, d, C):
     """Masks that are no trees: empty rows, a row that sees only others, all bits."""
     g = _gen("odd", T, G)
-    B, H, d, C = 3, 2, 64, 150
+    B, H = 3, 2
     lens = [0, 0, 70]
     q = _randn(g, B, H * G, T, d, std=2.0)
     k, v = _cache(g, B, H, C, d, lens, T)
@@ -203,12 +183,13 @@ def test_rows_that_see_nothing_or_odd_sets(T, G):
     ref.check("weights", out, *want_w)
 
 
-@pytest.mark.parametrize("T,G,d", [(4, 1, 64), (7, 2, 128), (30, 4, 128), (64, 2, 64), (64, 4, 128)])
+@pytest.mark.parametrize("T,G,d", POISON)
 @pytest.mark.parametrize("value", [NAN, math.inf, -math.inf])
-def test_what_a_row_does_not_see_does_not_reach_it(T, G, d, value):
+@pytest.mark.parametrize("C", [300, ROOM])
+def test_what_a_row_does_not_see_does_not_reach_it(T, G, d, value, C):
     """A drafted token whose key and value are not finite spoils its descendants' rows alone."""
     g = _gen("poison", T, G, d, str(value))
-    B, H, C, n = 2, 2, 300, [200, 3]
+    B, H, n = 2, 2, [200, 3]
     q = _randn(g, B, H * G, T, d)
     k, v = _cache(g, B, H, C, d, n, T)
     parents = _parents(g, B, T)
