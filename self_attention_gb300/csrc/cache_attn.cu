@@ -86,6 +86,7 @@ struct Plan {
     int H, tiles, T, C;
     int block;       // slots a block of work
     int whole;       // a CTA takes one unit whole (and nothing is shared out)
+    int slack;       // blocks that a CTA may have more if it then has one unit's alone
 };
 
 // Slots of the cache ahead of the new tokens.
@@ -96,14 +97,33 @@ __device__ __forceinline__ int length_of(const int *lengths, int b, int T, int C
 
 __device__ __forceinline__ int blocks_of(int length, const Plan &p) { return (length + p.T + p.block - 1) / p.block; }
 
+// a / b, by a 32-bit division where both fit.
+__device__ __forceinline__ long long divide(long long a, int b)
+{
+    return (a >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// What a CTA's share is: `per` blocks in the order of the units; or, where that takes at most `slack` blocks more, up to
+// `per` blocks of one unit alone (apart), since the end of a unit costs about two blocks' time.
+struct Shares {
+    long long per;
+    bool apart;
+};
+
+// From the blocks n of the lane's own sequence (up to 32 of them); by a whole warp.
+__device__ __forceinline__ Shares shares_of(int n, const Plan &p, int ctas)
+{
+    const long long units = (long long)p.H * p.tiles;
+    const long long all = (long long)__reduce_add_sync(0xffffffffu, n) * units;
+    const int per = (int)min(divide(all + ctas - 1, ctas), 0x7ffffff0ll);
+    for (int k = 0; k <= p.slack; ++k)
+        if ((long long)__reduce_add_sync(0xffffffffu, (n + per + k - 1) / (per + k)) * units <= ctas) return {per + k, true};
+    return {per, false};
+}
+
 // Blocks of all sequences, and of those ahead of sequence `upto`; by a whole warp, the same in every lane.
 __device__ __forceinline__ long long count_blocks(const int *lengths, int B, int upto, const Plan &p, long long &before)
 {
-    if (B <= 32) {
-        const int b = threadIdx.x & 31, n = b < B ? blocks_of(length_of(lengths, b, p.T, p.C), p) : 0;
-        before = (long long)__reduce_add_sync(0xffffffffu, b < upto ? n : 0) * p.H * p.tiles;
-        return (long long)__reduce_add_sync(0xffffffffu, n) * p.H * p.tiles;
-    }
     long long all = 0, ahead = 0;
     for (int b = threadIdx.x & 31; b < B; b += 32) {
         const int n = blocks_of(length_of(lengths, b, p.T, p.C), p);
@@ -127,12 +147,6 @@ struct Segment {
     __device__ __forceinline__ bool whole() const { return first == 0 && last == nb; }
 };
 
-// a / b, by a 32-bit division where both fit.
-__device__ __forceinline__ long long divide(long long a, int b)
-{
-    return (a >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
-}
-
 // Walks over a CTA's share of the blocks, the same number for each.
 struct Walk {
     long long x, end, before;
@@ -153,24 +167,42 @@ struct Walk {
         }
         int len = (int)lane < B ? length_of(lengths, (int)lane, p.T, p.C) : 0, inc;
         int n = (int)lane < B ? blocks_of(len, p) : 0;
-        auto scan = [&] {         // blocks of these 32 sequences up to the lane's own
-            inc = n;
+        auto scan = [&](int v) {         // the sum of v over the lanes up to this one
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int t = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= (uint32_t)o) inc += t;
+                const int t = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= (uint32_t)o) v += t;
             }
+            return v;
         };
-        scan();
-        long long all = (long long)__shfl_sync(0xffffffffu, inc, 31) * per_unit;
-        if (B > 32) {
+        if (B <= 32) {
+            const Shares sh = shares_of(n, p, (int)gridDim.x);
+            if (sh.apart) {
+                const int per = (int)sh.per, mine = (n + per - 1) / per;       // CTAs a unit of this sequence
+                inc = scan(mine);
+                const uint32_t hit = __ballot_sync(0xffffffffu, blockIdx.x < inc * per_unit);
+                if (!hit) return false;
+                const int l = __ffs(hit) - 1, k = __shfl_sync(0xffffffffu, mine, l);
+                const int at = (int)(blockIdx.x - __shfl_sync(0xffffffffu, inc - mine, l) * per_unit), u = at / k;
+                length = __shfl_sync(0xffffffffu, len, l);
+                nb = blocks_of(length, p);
+                b = l;
+                before = 0;
+                x = (long long)u * nb + (long long)(at - u * k) * per;
+                end = min(x + per, (long long)(u + 1) * nb);
+                return true;
+            }
+            end = (long long)__reduce_add_sync(0xffffffffu, n) * per_unit;
+            x = sh.per * blockIdx.x;
+            end = min(x + sh.per, end);
+        } else {
             long long ignored;
-            all = count_blocks(lengths, B, 0, p, ignored);
+            const long long all = count_blocks(lengths, B, 0, p, ignored), per = divide(all + gridDim.x - 1, (int)gridDim.x);
+            x = per * blockIdx.x;
+            end = min(x + per, all);
         }
-        const long long per = divide(all + gridDim.x - 1, (int)gridDim.x);
-        x = per * blockIdx.x;
-        end = min(x + per, all);
         if (x >= end) return false;
+        inc = scan(n);
         long long sum = 0;
         for (int b0 = 0;;) {          // ends: x lies before `all`
             const uint32_t hit = __ballot_sync(0xffffffffu, x < (sum + inc) * per_unit);
@@ -186,7 +218,7 @@ struct Walk {
             b0 += 32;
             len = b0 + (int)lane < B ? length_of(lengths, b0 + (int)lane, p.T, p.C) : 0;
             n = b0 + (int)lane < B ? blocks_of(len, p) : 0;
-            scan();
+            inc = scan(n);
         }
     }
     // By any thread.
@@ -226,6 +258,17 @@ struct Parts {
     float2 *ml;        // [2 grid][rows]: maximum (of scores times log2 e) and sum
     float *scores;     // null, or [B H][G T][C]: scores times log2 e, -infinity where a row does not see a slot
 };
+
+// Lanes that differ in `bit` change places: the one without it gives b for the other's a.
+__device__ __forceinline__ void exchange(uint4 &a, uint4 &b, int bit)
+{
+    const bool up = (threadIdx.x & bit) != 0;
+    const uint4 give = up ? a : b;
+    const uint4 got = make_uint4(__shfl_xor_sync(0xffffffffu, give.x, bit), __shfl_xor_sync(0xffffffffu, give.y, bit),
+                                 __shfl_xor_sync(0xffffffffu, give.z, bit), __shfl_xor_sync(0xffffffffu, give.w, bit));
+    if (up) a = got;
+    else b = got;
+}
 
 // Waits for what is already on its way, for a second at most, whether or not the CTA has given up.
 __device__ __forceinline__ void drain(uint64_t *bar, uint32_t parity)
@@ -845,7 +888,7 @@ struct ManyCfg {
     static constexpr int Q_BYTES = 128 * D * 2, KV_BYTES = kManyTile * D * 2;
     static constexpr int STAGES = D == 128 ? 5 : 10;
     static constexpr int SMEM = MODE * Q_BYTES + STAGES * KV_BYTES + 1024;
-    static_assert(SMEM <= 227 * 1024 - 512 - (MODE == 1 ? 2048 : 0), "dynamic + static shared memory over 227 KB");
+    static_assert(SMEM <= 227 * 1024 - 1280 - (MODE == 1 ? 2048 : 0), "dynamic + static shared memory over 227 KB");
     static constexpr int TMA_WARP = 8, MMA_WARP = 9, FIX_WARP = 10, THREADS = 384;
     static constexpr uint32_t TM_O = 256;
 };
@@ -872,6 +915,8 @@ __global__ void __launch_bounds__(384, 1)
     __shared__ uint64_t bar_q, bar_qe, bar_full[NS], bar_empty[NS], bar_s[2], bar_p[2], bar_o[2], bar_go, bar_fix, bar_done;
     __shared__ uint32_t tmem_sh;
     __shared__ int abort_sh, odd_sh[4];
+    __shared__ Walk walk_sh[8];
+    __shared__ Segment seg_sh[8];
     __shared__ float2 ml_sh[MODE == 1 ? 2 : 1][MODE == 1 ? 128 : 1];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -984,17 +1029,17 @@ __global__ void __launch_bounds__(384, 1)
                 };
                 if (!wait(&bar_q, i_seg & 1)) break;
                 for (int i = 0; i < 2 && i < J && ok; ++i) issue_s(i);
+                bool tail = false;           // this tile is being repaired meanwhile
                 for (int i = 0; i < J && ok; ++i) {
                     const int t = i & 1, j = MODE == 1 ? i : i >> 1;
                     const uint32_t at = base + v_place<MODE>(j, n), st = at % NS;
                     if (MODE == 1 || t == 0) {
                         if (!wait(&bar_full[st], (at / NS) & 1)) break;
-                        if ((seg.first + j + 1) * kManyTile > seg.length) {
-                            ptx::mbar_arrive(&bar_go);
-                            if (!wait(&bar_fix, fixes++ & 1)) break;
-                        }
+                        tail = (seg.first + j + 1) * kManyTile > seg.length;
+                        if (tail) ptx::mbar_arrive(&bar_go);
                     }
                     if (!wait(&bar_p[t], jobs[t]++ & 1)) break;
+                    if (tail && (MODE == 1 || t == 0) && !wait(&bar_fix, fixes++ & 1)) break;
 #pragma unroll
                     for (int kk = 0; kk < kManyTile / 16; ++kk)
                         ptx::mma_ts(tmem + C::TM_O + t * D, tmem + t * 128 + kk * 8,
@@ -1057,15 +1102,21 @@ __global__ void __launch_bounds__(384, 1)
         const uint32_t tS = tmem + lane_off + t * 128, tO = tmem + lane_off + C::TM_O;
         const float scale_log2 = a.scale * kLog2e;
         uint32_t jobs = 0;
-        for (uint32_t i_seg = 0; walk.next(a.lengths, plan, seg); ++i_seg) {
+        // the walk and the segment wait in shared memory: S takes the registers
+        const Segment &seg = seg_sh[warp];
+        if (lane == 0) walk_sh[warp] = walk;
+        for (uint32_t i_seg = 0;; ++i_seg) {
+            __syncwarp();
+            if (lane == 0) walk_sh[warp].next(a.lengths, plan, seg_sh[warp]);
+            __syncwarp();
+            if (!seg.there) break;
             const int n = seg.last - seg.first;
             const int row = seg.tile * ROWS + (MODE == 2 ? t * 128 : 0) + r_tile;
             const bool idle = row - lane >= R;          // a warp without rows
-            uint64_t word = 0;
-            if (row < R) {
-                word = word_of(a.tree, seg.b, T, row % T);
-                if (T < 64) word &= (1ull << T) - 1;
-            }
+            auto word_here = [&] {
+                uint64_t word = row < R ? word_of(a.tree, seg.b, T, row % T) : 0;
+                return T < 64 ? word & ((1ull << T) - 1) : word;
+            };
             float m = -INFINITY, l = 0.f;
             bool begun = false;
             for (int j = MODE == 1 ? t : 0; j < n; j += MODE == 1 ? 2 : 1, ++jobs) {
@@ -1081,6 +1132,7 @@ __global__ void __launch_bounds__(384, 1)
                     reg_fence(r);
                     const int u0 = (seg.first + j) * kManyTile - seg.length;    // the tile's first slot, from the first token's
                     if (u0 + kManyTile > 0) {
+                        const uint64_t word = word_here();
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
                             const int u = u0 + 32 * c;
@@ -1199,6 +1251,7 @@ __global__ void __launch_bounds__(384, 1)
                         }
                     }
                     if (odd && row < R) {
+                        const uint64_t word = word_here();
                         for (int u = 0; u < T; ++u) {
                             const int key = seg.length + u;
                             if (!(word >> u & 1) || key < seg.first * kManyTile || key >= seg.last * kManyTile) continue;
@@ -1215,24 +1268,35 @@ __global__ void __launch_bounds__(384, 1)
                             }
                         }
                     }
-                    if (row < R) {
-                        if (whole) {
-                            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + at * D + c);
+                    if (whole) {
+                        // Four neighbouring lanes write 64 bytes of one row after another: their 16-byte pieces change
+                        // places in two steps (a lane's own row a store would touch 32 lines a time).
+                        uint4 x[4];
 #pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                uint32_t w[4];
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t w[4];
 #pragma unroll
-                                for (int y = 0; y < 4; ++y)
-                                    w[y] = ptx::pack_bf16x2(__uint_as_float(ov[8 * x + 2 * y]) * inv,
-                                                            __uint_as_float(ov[8 * x + 2 * y + 1]) * inv);
-                                dst[x] = make_uint4(w[0], w[1], w[2], w[3]);
-                            }
-                        } else {
-                            uint4 *dst = reinterpret_cast<uint4 *>(parts.o) + (slot * (D / 4) + c / 4) * ROWS + row % ROWS;
-#pragma unroll
-                            for (int x = 0; x < 8; ++x)
-                                dst[x * ROWS] = make_uint4(ov[4 * x], ov[4 * x + 1], ov[4 * x + 2], ov[4 * x + 3]);
+                            for (int y = 0; y < 4; ++y)
+                                w[y] = ptx::pack_bf16x2(__uint_as_float(ov[8 * i + 2 * y]) * inv,
+                                                        __uint_as_float(ov[8 * i + 2 * y + 1]) * inv);
+                            x[i] = make_uint4(w[0], w[1], w[2], w[3]);
                         }
+                        exchange(x[0], x[1], 1);
+                        exchange(x[2], x[3], 1);
+                        exchange(x[0], x[2], 2);
+                        exchange(x[1], x[3], 2);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = row - (lane & 3) + i;
+                            if (r < R)
+                                *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + (seg.head * R + r) * D + c +
+                                                           8 * (lane & 3)) = x[i];
+                        }
+                    } else if (row < R) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(parts.o) + (slot * (D / 4) + c / 4) * ROWS + row % ROWS;
+#pragma unroll
+                        for (int x = 0; x < 8; ++x)
+                            dst[x * ROWS] = make_uint4(ov[4 * x], ov[4 * x + 1], ov[4 * x + 2], ov[4 * x + 3]);
                     }
                 }
                 if (row < R && (MODE == 2 || t == 0)) {
@@ -1275,9 +1339,22 @@ struct Pieces {
     int count;
     __device__ __forceinline__ Pieces(const CacheAttnArgs &a, const Plan &plan, int ctas, int b, int h, int tile)
     {
-        long long before;
-        const long long total = count_blocks(a.lengths, a.B, b, plan, before);
-        const long long per = divide(total + ctas - 1, ctas);
+        long long before, per;
+        if (a.B <= 32) {
+            const int l = threadIdx.x & 31, n = l < a.B ? blocks_of(length_of(a.lengths, l, a.T, a.C), plan) : 0;
+            const Shares sh = shares_of(n, plan, ctas);
+            per = sh.per;
+            if (sh.apart) {
+                const int mine = (n + (int)per - 1) / (int)per;
+                count = __shfl_sync(0xffffffffu, mine, b);
+                c0 = (long long)__reduce_add_sync(0xffffffffu, l < b ? mine : 0) * plan.H * plan.tiles +
+                     ((long long)h * plan.tiles + tile) * count;
+                return;
+            }
+            before = (long long)__reduce_add_sync(0xffffffffu, l < b ? n : 0) * plan.H * plan.tiles;
+        } else {
+            per = divide(count_blocks(a.lengths, a.B, b, plan, before) + ctas - 1, ctas);
+        }
         const int nb = blocks_of(length_of(a.lengths, b, a.T, a.C), plan);
         const long long u0 = before + ((long long)h * plan.tiles + tile) * nb;
         if (per <= 0x7fffffff) {
@@ -1629,7 +1706,8 @@ cudaError_t launch(const CacheAttnArgs &a, cudaStream_t stream)
 {
     const int R = a.G * a.T;
     const Choice c = choose(a.B, a.H, a.G, a.T, a.C, D);
-    const Plan plan = {a.H, (R + c.rows - 1) / c.rows, a.T, a.C, c.few_rows() ? kBlock : kManyTile, c.kind == kManyWhole};
+    const Plan plan = {a.H, (R + c.rows - 1) / c.rows, a.T, a.C, c.few_rows() ? kBlock : kManyTile, c.kind == kManyWhole,
+                       c.few_rows() ? 1 : 2};
     const unsigned heads = (unsigned)a.B * (unsigned)a.H;
     char *ws = static_cast<char *>(a.workspace);
     Parts parts = {};
