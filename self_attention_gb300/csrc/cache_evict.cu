@@ -25,6 +25,8 @@ constexpr int kSelThreads = 1024;
 constexpr int kBins = 2048;
 constexpr int kMaxInSmem = 48 * 1024;    // ranks a block keeps in shared memory (192 KB)
 constexpr int kPlanSms = 152;
+constexpr int kOwnBlocks = 128;          // blocks from which on they move what they select, and moves a block up to which
+constexpr int kOwnMoves = 256;           // fewer do
 constexpr int kMoveRows = 32;            // moves a block of move_kernel takes
 
 struct SelShared {
@@ -32,6 +34,7 @@ struct SelShared {
     uint32_t warp[4][32];
     uint32_t prefix;                     // rank bits found so far
     uint32_t need;                       // how many are still to be taken among those with this prefix
+    uint32_t have;                       // and how many there are
     uint32_t sums[4];                    // this block's, read by the others: newest, ties, holes, movers
 };
 
@@ -63,6 +66,45 @@ __device__ __forceinline__ uint32_t rank_of(float w, int pos, long long oldest)
     return w > 0.f ? __float_as_uint(w) : 0u;
 }
 
+// Moves first, first + step ... of a list: each by LANES lanes (16 bytes each) of d = 8 LANES columns, N at once.
+template <int LANES, int N>
+__device__ __forceinline__ void move_rows(const EvictArgs &a, int bh, const int *moves, int count, int first, int step)
+{
+    const int lane = threadIdx.x % LANES;
+    const long long row = (long long)bh * a.C;
+    uint4 *k = static_cast<uint4 *>(a.k) + row * LANES, *v = static_cast<uint4 *>(a.v) + row * LANES;
+    int2 at[N];                                     // (to, from)
+    uint4 x[N], y[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int m = first + i * step;
+        at[i] = m < count ? *reinterpret_cast<const int2 *>(moves + 2 + 2 * m) : make_int2(-1, -1);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (at[i].x >= 0) {
+            x[i] = k[(long long)at[i].y * LANES + lane];
+            y[i] = v[(long long)at[i].y * LANES + lane];
+        }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if (at[i].x < 0) continue;
+        const long long dst = at[i].x, src = at[i].y;
+        k[dst * LANES + lane] = x[i];
+        v[dst * LANES + lane] = y[i];
+        if (lane == 0) {
+            a.weights_out[row + dst] = a.weights[row + src];
+            a.weights_out[row + src] = 0.f;
+        }
+        if (lane == 1) {
+            a.positions_out[row + dst] = a.slot_positions[row + src];
+            a.positions_out[row + src] = -1;
+        }
+    }
+}
+
+// LANES > 0: the blocks move the rows themselves, 0: move_kernel does.
+template <int LANES>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int stride, int in_smem, int blocks)
 {
     extern __shared__ __align__(16) uint32_t ranks[];
@@ -199,6 +241,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int st
             const bool first = need <= above + c1;
             s.prefix = prefix | (uint32_t)(first ? top : top - 1) << shift;
             s.need = need - above - (first ? 0 : c1);
+            s.have = first ? c1 : c0;
         }
         __syncthreads();
         prefix = s.prefix;
@@ -207,16 +250,19 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int st
 
     // In order: ranks above `prefix` stay, and the first `need` that equal it.  A warp takes slots [from, to).
     const int run = (end - begin + 1023) / 1024 * 32, from = min(begin + warp * run, end), to = min(from + run, end);
-    uint32_t ties = 0, holes = 0, movers = 0, total;
-    for (int j0 = from; j0 < to; j0 += 32) {
-        const int j = j0 + lane;
-        ties += __popc(__ballot_sync(0xffffffffu, j < to && rank(j) == prefix));
-    }
-    uint32_t ties0 = warps_before(ties, s.warp[0], total);
-    if (blocks > 1) {
-        if (tid == 0) s.sums[1] = total;
-        ptx::cluster_sync();
-        ties0 += blocks_before(1, total);
+    uint32_t ties0 = 0, holes = 0, movers = 0, total;
+    if (s.have != need) {            // the order of the ties matters: some of them go
+        uint32_t ties = 0;
+        for (int j0 = from; j0 < to; j0 += 32) {
+            const int j = j0 + lane;
+            ties += __popc(__ballot_sync(0xffffffffu, j < to && rank(j) == prefix));
+        }
+        ties0 = warps_before(ties, s.warp[0], total);
+        if (blocks > 1) {
+            if (tid == 0) s.sums[1] = total;
+            ptx::cluster_sync();
+            ties0 += blocks_before(1, total);
+        }
     }
     const uint32_t below = (1u << lane) - 1;
     auto kept = [&](int j, uint32_t &t) {          // by a whole warp; t: ties so far
@@ -266,49 +312,27 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int st
         w_out[j] = 0.f;
         pos_out[j] = -1;
     }
-    if (blocks > 1) ptx::cluster_sync_relaxed();     // nobody leaves while its sums are read
+    if (LANES > 0) {
+        // the list is complete, and nothing of the sources' numbers is needed any more but by those who move them
+        if (blocks > 1) ptx::cluster_sync();
+        else __syncthreads();
+        constexpr int AT_ONCE = kSelThreads / (LANES > 0 ? LANES : 1), N = 2;
+        for (int m = me * AT_ONCE + tid / (LANES > 0 ? LANES : 1); m < (int)total; m += N * blocks * AT_ONCE)
+            move_rows<(LANES > 0 ? LANES : 1), N>(a, bh, moves, (int)total, m, blocks * AT_ONCE);
+    } else {
+        if (blocks > 1) ptx::cluster_sync_relaxed();     // nobody leaves while its sums are read
+    }
 }
 
-// LANES lanes a row of d = 8 LANES columns.
 template <int LANES>
 __global__ void __launch_bounds__(256) move_kernel(EvictArgs a, int stride, int blocks)
 {
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
-    const int bh = blockIdx.x / blocks, lane = threadIdx.x % LANES;
+    const int bh = blockIdx.x / blocks;
     const int *moves = a.moves + (long long)bh * stride;
-    const int count = moves[0], first = blockIdx.x % blocks * kMoveRows;
-    const long long row = (long long)bh * a.C;
-    uint4 *k = static_cast<uint4 *>(a.k) + row * LANES, *v = static_cast<uint4 *>(a.v) + row * LANES;
-    constexpr int STEP = 256 / LANES, N = kMoveRows / STEP;
-    int2 at[N];                                     // (to, from)
-    uint4 x[N], y[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int m = first + i * STEP + threadIdx.x / LANES;
-        at[i] = m < count ? *reinterpret_cast<const int2 *>(moves + 2 + 2 * m) : make_int2(-1, -1);
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        if (at[i].x >= 0) {
-            x[i] = k[(long long)at[i].y * LANES + lane];
-            y[i] = v[(long long)at[i].y * LANES + lane];
-        }
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        if (at[i].x < 0) continue;
-        const long long dst = at[i].x, src = at[i].y;
-        k[dst * LANES + lane] = x[i];
-        v[dst * LANES + lane] = y[i];
-        if (lane == 0) {
-            a.weights_out[row + dst] = a.weights[row + src];
-            a.weights_out[row + src] = 0.f;
-        }
-        if (lane == 1) {
-            a.positions_out[row + dst] = a.slot_positions[row + src];
-            a.positions_out[row + src] = -1;
-        }
-    }
+    constexpr int STEP = 256 / LANES;
+    move_rows<LANES, kMoveRows / STEP>(a, bh, moves, moves[0], blockIdx.x % blocks * kMoveRows + threadIdx.x / LANES, STEP);
 }
 
 int most_moves(int C, int keep) { return keep < C - keep ? keep : C - keep > 0 ? C - keep : 0; }
@@ -331,17 +355,22 @@ cudaError_t launch_evict(const EvictArgs &a, cudaStream_t stream)
     const int split = select_blocks(a.B * a.H, a.C), share = (a.C + split - 1) / split + 32;
     const int in_smem = share <= kMaxInSmem, bytes = in_smem ? (share + 3) / 4 * 16 : 0;
     const int stride = moves_stride(a.C, a.keep);
-    static std::atomic<bool> set[64];
-    cudaError_t e = raise_smem(reinterpret_cast<const void *>(select_kernel), kMaxInSmem * 4, set);
+    const int most = most_moves(a.C, a.keep), blocks = a.B * a.H * split;
+    // The selecting blocks move the rows too where there are enough of them to keep HBM busy, or little to move (one launch
+    // less, and no hand-over of the list: 128 heads of 2049 slots less one 8.2 us, by two kernels 9.7); a few leave that to
+    // the whole GPU (8 heads of 100000 slots less half 75 us, themselves 114).
+    const bool own = blocks >= kOwnBlocks || (long long)most * a.B * a.H <= (long long)kOwnMoves * blocks;
+    static std::atomic<bool> set[3][64];
+    auto *const kernel = !own ? select_kernel<0> : a.d == 64 ? select_kernel<8> : select_kernel<16>;
+    cudaError_t e = raise_smem(reinterpret_cast<const void *>(kernel), kMaxInSmem * 4, set[!own ? 0 : a.d == 64 ? 1 : 2]);
     if (e != cudaSuccess) return e;
-    e = launch_overlapped(select_kernel, dim3((unsigned)(a.B * a.H * split)), dim3(kSelThreads), (size_t)bytes,
-                          (unsigned)split, stream, a, stride, in_smem, split);
-    const int most = most_moves(a.C, a.keep);
-    if (e != cudaSuccess || most == 0) return e;
-    const int blocks = (most + kMoveRows - 1) / kMoveRows;     // a sequence and head
-    const dim3 grid((unsigned)blocks * (unsigned)(a.B * a.H));
-    return a.d == 64 ? launch_overlapped(move_kernel<8>, grid, dim3(256), 0, 1, stream, a, stride, blocks)
-                     : launch_overlapped(move_kernel<16>, grid, dim3(256), 0, 1, stream, a, stride, blocks);
+    e = launch_overlapped(kernel, dim3((unsigned)blocks), dim3(kSelThreads), (size_t)bytes, (unsigned)split, stream, a, stride,
+                          in_smem, split);
+    if (e != cudaSuccess || most == 0 || own) return e;
+    const int each = (most + kMoveRows - 1) / kMoveRows;     // blocks a sequence and head
+    const dim3 grid((unsigned)each * (unsigned)(a.B * a.H));
+    return a.d == 64 ? launch_overlapped(move_kernel<8>, grid, dim3(256), 0, 1, stream, a, stride, each)
+                     : launch_overlapped(move_kernel<16>, grid, dim3(256), 0, 1, stream, a, stride, each);
 }
 
 }  // namespace attn
