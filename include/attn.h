@@ -378,6 +378,7 @@ attn_status attn_debug_linear_plan(int kind, int B, int H, int N, int d_k, int N
  *     cached head h.  `lengths` [B] int32 counts the slots in use, on the device: the host never reads it.
  *   - Pointers to heads, `turns` and o start on 16 bytes, workspaces on 256, all others on their own elements.
  *     Outputs overlap no input and no other output, except where an entry point allows it by name.
+ *   - The cache's calls take B, H and C of at least 1 (the append of no tokens, or of none of B = 0, does nothing).
  *   - Sizes: B H, B N, B T and the like below 2^31, no operand of 2^40 elements or more, H and H G at most
  *     16384, C below 2^30.
  */

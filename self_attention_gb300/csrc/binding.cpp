@@ -6,6 +6,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -13,6 +14,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <initializer_list>
 #include <string>
 
 #include "attn.h"
@@ -436,6 +438,15 @@ struct HeadsOf {
 
 constexpr auto kI32 = at::kInt, kI64 = at::kLong;
 
+// The cache's calls have no backward: an operand that a graph is being recorded for is refused, not cut off from it.
+void refuse_graph(std::initializer_list<PyObject *> operands, const char *what)
+{
+    if (!at::GradMode::is_enabled()) return;
+    for (PyObject *o : operands)
+        if (THPVariable_Check(o) && THPVariable_Unpack(o).requires_grad())
+            refuse(std::string(what) + " has no backward: run it under torch.no_grad(), or on detached tensors");
+}
+
 // Turns a position of the pairs, [rotated / 2] int64 (the bits of the C ABI's uint64).
 const uint64_t *turns_of(PyObject *o, c10::Device dev, int64_t &rotated)
 {
@@ -481,6 +492,7 @@ PyObject *rotary(Args a)
 PyObject *cache_append(Args a)
 {
     const HeadsOf k(a[0], "k"), ck(a[2], "cache_k");
+    refuse_graph({a[0], a[1], a[2], a[3], a[10], a[11]}, "cache_append");
     const void *v = operand(a[1], "v", kBf16, k.t.sizes(), k.dev);
     if (ck.dev != k.dev || ck.B != k.B || ck.H != k.H || ck.d != k.d)
         refuse("cache_k: expected [" + std::to_string(k.B) + ", " + std::to_string(k.H) + ", C, " +
@@ -525,6 +537,7 @@ PyObject *cache_append(Args a)
 PyObject *cache_attention(Args a)
 {
     const HeadsOf q(a[0], "q"), k(a[1], "cache_k");
+    refuse_graph({a[0], a[1], a[2], a[5], a[7]}, "cache_attention");
     if (k.dev != q.dev || k.B != q.B || k.d != q.d || k.H < 1 || q.H % k.H)
         refuse("cache_k: expected [" + std::to_string(q.B) + ", H, C, " + std::to_string(q.d) + "] on " + q.dev.str() +
                ", H a divisor of q's " + std::to_string(q.H) + " heads, got " + describe(k.t.sizes()) + " on " +
@@ -567,6 +580,7 @@ PyObject *cache_attention(Args a)
 PyObject *cache_evict(Args a)
 {
     const HeadsOf k(a[0], "cache_k");
+    refuse_graph({a[0], a[1], a[2], a[7]}, "cache_evict");
     void *v = operand(a[1], "cache_v", kBf16, k.t.sizes(), k.dev);
     const c10::DimVector slots{k.B, k.H, k.N};
     const auto *weights = static_cast<const float *>(operand(a[2], "weights", kF32, slots, k.dev));

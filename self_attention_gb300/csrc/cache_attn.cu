@@ -826,6 +826,7 @@ __global__ void __launch_bounds__(32 * kUnitWarps, UnitCfg<D, NT>::BLOCKS)
         }
     }
     if (ctas == 1) return;
+    __syncwarp();
     ptx::cluster_sync();
     // each CTA finishes its share of the rows' pieces of four columns
     constexpr int QUADS = D / 4, ALL = R8 * QUADS;
@@ -864,6 +865,7 @@ __global__ void __launch_bounds__(32 * kUnitWarps, UnitCfg<D, NT>::BLOCKS)
             make_uint2(ptx::pack_bf16x2(v.x * inv, v.y * inv), ptx::pack_bf16x2(v.z * inv, v.w * inv));
         if (c == 0) a.lse[at] = lse_of(top, sum);
     }
+    __syncwarp();                      // (a warp arrives as one)
     ptx::cluster_sync_relaxed();       // nobody leaves while its sums are read
 }
 

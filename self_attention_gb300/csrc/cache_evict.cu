@@ -136,6 +136,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int st
     const int share = ((L + blocks - 1) / blocks + 31) / 32 * 32;       // slots [begin, end) are this block's
     const int begin = min(me * share, L), end = min(begin + share, L);
     auto sync = [&] {
+        __syncwarp();                // (a warp arrives as one)
         if (blocks > 1) ptx::cluster_sync();
         else __syncthreads();
     };
@@ -174,7 +175,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int st
     newest = __reduce_max_sync(0xffffffffu, (int)s.warp[0][lane]);
     if (blocks > 1) {
         if (tid == 0) s.sums[0] = (uint32_t)newest;
-        ptx::cluster_sync();
+        sync();
         newest = __reduce_max_sync(0xffffffffu, lane < blocks ? (int)ptx::ld_cluster_b32(other(&s.sums[0], lane)) : newest);
     }
     const long long oldest = (long long)newest - a.recent;   // positions above it are safe
@@ -260,7 +261,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int st
         ties0 = warps_before(ties, s.warp[0], total);
         if (blocks > 1) {
             if (tid == 0) s.sums[1] = total;
-            ptx::cluster_sync();
+            sync();
             ties0 += blocks_before(1, total);
         }
     }
@@ -285,7 +286,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int st
             s.sums[2] = total;
             s.sums[3] = movers;
         }
-        ptx::cluster_sync();
+        sync();
         mover += blocks_before(3, movers);
         hole += blocks_before(2, total);
     }
@@ -314,12 +315,12 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int st
     }
     if (LANES > 0) {
         // the list is complete, and nothing of the sources' numbers is needed any more but by those who move them
-        if (blocks > 1) ptx::cluster_sync();
-        else __syncthreads();
+        sync();
         constexpr int AT_ONCE = kSelThreads / (LANES > 0 ? LANES : 1), N = 2;
         for (int m = me * AT_ONCE + tid / (LANES > 0 ? LANES : 1); m < (int)total; m += N * blocks * AT_ONCE)
             move_rows<(LANES > 0 ? LANES : 1), N>(a, bh, moves, (int)total, m, blocks * AT_ONCE);
     } else {
+        __syncwarp();
         if (blocks > 1) ptx::cluster_sync_relaxed();     // nobody leaves while its sums are read
     }
 }

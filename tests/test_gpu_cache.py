@@ -315,6 +315,16 @@ def test_refusals():
     with pytest.raises(sa.AttnError):                                # k and v into one cache
         sa.cache_append(new, new, k, k, n)
     slots = torch.zeros(B, H, C, dtype=torch.int32, device="cuda")
+    # no backward: what a graph is recorded for is refused, without one it is taken
+    wants = q.clone().requires_grad_()
+    with pytest.raises(ValueError, match="no backward"):
+        sa.cache_attention(wants, k, v, n)
+    with pytest.raises(ValueError, match="no backward"):
+        sa.cache_append(new.clone().requires_grad_(), new, k, v, n)
+    with pytest.raises(ValueError, match="no backward"):
+        sa.cache_evict(k, v, w.clone().requires_grad_(), slots, n, 4)
+    with torch.no_grad():
+        assert not sa.cache_attention(wants, k, v, n)[0].requires_grad
     for kw in (dict(keep=0), dict(keep=-1), dict(keep=4, recent=5), dict(keep=4, recent=-1), dict(keep=2 ** 40)):
         with pytest.raises(sa.AttnError):
             sa.cache_evict(k, v, w, slots, n, **kw)
@@ -484,6 +494,77 @@ def test_captured_and_replayed_steps_on_another_stream():
         assert torch.equal(o, eager[i][0]) and torch.equal(lse, eager[i][1])
     for t, x in zip((ck, cv, w, pos, lengths), after):
         assert torch.equal(t, x)
+
+
+def test_calls_at_once_on_one_cache_and_by_host_threads():
+    """Captured calls of several sizes replayed over one another's streams, and eager ones from several threads."""
+    import threading
+    g = _gen("threads")
+    B, H, d, C = 2, 2, 128, ROOM
+    k, v = _randn(g, B, H, C, d), _randn(g, B, H, C, d)
+    n = _i32(3000, 777)
+    qs = [_randn(g, B, H * G, T, d) for G, T in ((1, 1), (4, 4), (2, 30), (4, 64))]
+    want = [sa.cache_attention(q, k, v, n) for q in qs]
+    graphs = []
+    for q in qs:
+        s, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.graph(graph, stream=s):
+            out = [sa.cache_attention(q, k, v, n) for _ in range(3)]
+        graphs.append((graph, s, out))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for graph, s, _out in graphs:
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    for (_, _, out), w in zip(graphs, want):
+        for o, lse in out:
+            assert torch.equal(o, w[0]) and torch.equal(lse, w[1])
+    wrong = []
+
+    def work(i):
+        s = torch.cuda.Stream()
+        for _ in range(10):
+            o, lse = sa.cache_attention(qs[i], k, v, n, stream=s)
+            s.synchronize()
+            if not (torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])):
+                wrong.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(qs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong and sa.attn_get_device_status() == 0
+
+
+def test_between_other_kernels_that_use_tensor_memory():
+    """A step of a block: the projections before and after share the SMs' tensor memory with the attention."""
+    g = _gen("block")
+    B, H, G, T, d, C = 4, 2, 4, 16, 64, ROOM
+    D = H * G * d
+    x, wq, wo = _randn(g, B, T, D), _randn(g, D, D, std=D ** -0.5), _randn(g, D, D, std=D ** -0.5)
+    wk = _randn(g, D, H * d, std=D ** -0.5)
+    k, v = _randn(g, B, H, C, d), _randn(g, B, H, C, d)
+    n = _i32(1000, 5000, 0, 313)
+    turns = sa.rotary_turns(64)
+
+    def step():
+        h, _, _ = sa.rms_norm_forward(x, torch.ones(D, device="cuda"))
+        q = sa.linear_forward(h, wq).view(B, T, H * G, d).transpose(1, 2).contiguous()
+        nk = sa.linear_forward(h, wk).view(B, T, H, d).transpose(1, 2).contiguous()
+        qt = sa.cache_append(nk, nk, k, v, n, turns, q=q)
+        o, lse = sa.cache_attention(qt, k, v, n)
+        return sa.out_proj_forward(o, wo, None, x), o, lse, qt
+
+    first = [t.clone() for t in step()]
+    for _ in range(30):
+        again = step()
+    assert all(torch.equal(a, b) for a, b in zip(first, again)) and sa.attn_get_device_status() == 0
+    want_o, want_l = ref.attention_many(first[3], k, v, n.tolist())
+    ref.check("o", first[1], *want_o)
+    ref.check("lse", first[2], *want_l)
 
 
 def test_streams_at_once():

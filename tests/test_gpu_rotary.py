@@ -118,6 +118,53 @@ def test_gradient(interleaved):
         gx.sum().backward()
 
 
+def test_training_through_projection_rotary_and_attention():
+    """The gradients of a projection's input and weights with rotary positions ahead of attention, against PyTorch's own
+    differentiation of the formulas in 64 bits: within 1e-2 of their norms, as the attention's own gradients are held."""
+    g = _gen("train")
+    B, N, H, d = 2, 130, 4, 64
+    D = H * d
+    x, dy = _randn(g, B, N, D), _randn(g, B, H, N, d)
+    ws = [_randn(g, D, D, std=D ** -0.5) for _ in range(3)]
+    turns, f = sa.rotary_turns(d), ref.frequencies(d).cuda()
+    leaves = [t.clone().requires_grad_() for t in (x, *ws)]
+    q, k, v = sa.qkv_proj(*leaves, H)
+    o = sa.attention(sa.rotary(q, turns), sa.rotary(k, turns), v)
+    o.backward(dy)
+    plain = [t.double().requires_grad_() for t in (x, *ws)]
+    heads = [(plain[0] @ w).view(B, N, H, d).transpose(1, 2) for w in plain[1:]]
+    angle = torch.arange(N, device="cuda").double().view(N, 1) * f
+
+    def turn(t):
+        a, b = t[..., :d // 2], t[..., d // 2:]
+        return torch.cat((a * angle.cos() - b * angle.sin(), a * angle.sin() + b * angle.cos()), -1)
+
+    p = (turn(heads[0]) @ turn(heads[1]).transpose(2, 3) / math.sqrt(d)).softmax(-1)
+    (p @ heads[2]).backward(dy.double())
+    for name, got, want in zip(("x", "w_q", "w_k", "w_v"), leaves, plain):
+        err = (got.grad.double() - want.grad).norm() / want.grad.norm()
+        assert err < 1e-2, (name, err.item())
+
+
+def test_backward_captured_and_replayed():
+    """The gradient in a graph, with leaves that no eager graph holds."""
+    g = _gen("capture")
+    x, dy = _randn(g, 2, 3, 40, 64), _randn(g, 2, 3, 40, 64)
+    turns = sa.rotary_turns(64)
+    want = sa.rotary_backward(dy, turns)
+    leaf = x.clone().requires_grad_()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        y = sa.rotary(leaf, turns)
+        grad, = torch.autograd.grad(y, leaf, dy)
+    for _ in range(2):
+        grad.zero_()
+        graph.replay()
+        assert torch.equal(grad, want)
+
+
 def test_in_place_and_guards():
     g = _gen("inplace")
     B, H, N, d = 3, 5, 37, 128
