@@ -293,6 +293,7 @@ struct Rows {
     static constexpr int MT = D / 16;           // 16-row tiles of O^T
     static constexpr uint32_t BOX = 16 * 128, STAGE = 2 * (D / 64) * BOX, RING = STAGES * STAGE;    // bytes
     uint4 qf[NT][KC];
+    uint64_t word[NT][2];                       // what rows 2 q and 2 q + 1 see of the tokens
     float acc[NT][MT][4], m[NT][2], l[NT][2], s[NT][4];
     int g, q;
     uint8_t *ring;                              // 1024-byte aligned
@@ -314,10 +315,17 @@ struct Rows {
             for (int i = 0; i < MT; ++i) acc[t][i][0] = acc[t][i][1] = acc[t][i][2] = acc[t][i][3] = 0.f;
         }
     }
-    // Q's rows from r0 on as the 8-column operand
-    __device__ __forceinline__ void load_q(const CacheAttnArgs &a, long long head, int r0)
+    // Q's rows from r0 on as the 8-column operand, and their mask words (the last step needs them at once)
+    __device__ __forceinline__ void load_q(const CacheAttnArgs &a, long long head, int b, int r0)
     {
         const int R = a.G * a.T;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = r0 + 8 * t + 2 * q + e;
+                word[t][e] = r < R ? word_of(a.tree, b, a.T, r % a.T) : 0;
+            }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             const int r = r0 + 8 * t + g;
@@ -379,8 +387,8 @@ struct Rows {
             for (int e = 0; e < 4; ++e) s[t][e] += s1[t][e];
     }
     // The rest of the step at `key`: weights, and O^T += V^T P^T.  kept: see Parts::scores
-    __device__ __forceinline__ void step(const CacheAttnArgs &a, long long head, int b, int r0, int key, int length,
-                                         float to_log2, float *kept)
+    __device__ __forceinline__ void step(const CacheAttnArgs &a, long long head, int r0, int key, int length, float to_log2,
+                                         float *kept)
     {
         const int T = a.T, R = a.G * T;
         const bool tail = key + 16 > length;
@@ -409,12 +417,10 @@ struct Rows {
             if (tail) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int r = r0 + 8 * t + 2 * q + e;
-                    const uint64_t word = r < R ? word_of(a.tree, b, T, r % T) : 0;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const int j = key + g + 8 * i - length;
-                        if (j >= 0 && !(j < T && (word >> j & 1))) s[t][e + 2 * i] = -INFINITY;
+                        if (j >= 0 && !(j < T && (word[t][e] >> j & 1))) s[t][e + 2 * i] = -INFINITY;
                     }
                 }
             }
@@ -685,7 +691,7 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, NT>::BLOCKS)
     };
     ask();
     walk.next(a.lengths, plan, seg);
-    w.load_q(a, seg.head, seg.tile * R8);
+    w.load_q(a, seg.head, seg.b, seg.tile * R8);
 #pragma unroll
     for (int i = 1; i < C::STAGES; ++i) ask();
 
@@ -696,9 +702,9 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, NT>::BLOCKS)
         w.clear();
         for (int key = first_key(seg); key < end; key += kBlock) {       // (a warp's share of the last block may be empty)
             w.scores(guard);
-            if (key + kBlock >= end && nxt.there) w.load_q(a, nxt.head, nxt.tile * R8);
-            w.step(a, seg.head, seg.b, r0, key, seg.length, to_log2, parts.scores);
+            w.step(a, seg.head, r0, key, seg.length, to_log2, parts.scores);
             ask();
+            if (key + kBlock >= end && nxt.there) w.load_q(a, nxt.head, nxt.b, nxt.tile * R8);
         }
         // half of the warps take the others' results over, then the rows are put together
         if (warp >= C::HALF) w.hand_over(handed + (warp - C::HALF) * C::HELD);
@@ -789,7 +795,7 @@ __global__ void __launch_bounds__(32 * kUnitWarps, UnitCfg<D, NT>::BLOCKS)
     typename C::R w(smem + warp * C::R::RING, bars + warp * C::STAGES);
     if (key < a.C) w.load(maps, head, key);     // along with the length: what lies behind it is masked or dropped
     const int length = length_of(a.lengths, b, T, a.C), valid = length + T;
-    w.load_q(a, head, r0);
+    w.load_q(a, head, b, r0);
     int ahead = key + stride;
     auto ask = [&] {
         if (ahead < valid) w.load(maps, head, ahead);
@@ -801,7 +807,7 @@ __global__ void __launch_bounds__(32 * kUnitWarps, UnitCfg<D, NT>::BLOCKS)
     w.clear();
     for (; key < valid; key += stride) {
         w.scores(guard);
-        w.step(a, head, b, r0, key, length, to_log2, kept);
+        w.step(a, head, r0, key, length, to_log2, kept);
         ask();
     }
     w.finish();
@@ -1115,10 +1121,8 @@ __global__ void __launch_bounds__(384, 1)
             const int n = seg.last - seg.first;
             const int row = seg.tile * ROWS + (MODE == 2 ? t * 128 : 0) + r_tile;
             const bool idle = row - lane >= R;          // a warp without rows
-            auto word_here = [&] {
-                uint64_t word = row < R ? word_of(a.tree, seg.b, T, row % T) : 0;
-                return T < 64 ? word & ((1ull << T) - 1) : word;
-            };
+            uint64_t word = row < R ? word_of(a.tree, seg.b, T, row % T) : 0;    // (the last tile needs it at once)
+            if (T < 64) word &= (1ull << T) - 1;
             float m = -INFINITY, l = 0.f;
             bool begun = false;
             for (int j = MODE == 1 ? t : 0; j < n; j += MODE == 1 ? 2 : 1, ++jobs) {
@@ -1134,7 +1138,6 @@ __global__ void __launch_bounds__(384, 1)
                     reg_fence(r);
                     const int u0 = (seg.first + j) * kManyTile - seg.length;    // the tile's first slot, from the first token's
                     if (u0 + kManyTile > 0) {
-                        const uint64_t word = word_here();
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
                             const int u = u0 + 32 * c;
@@ -1253,7 +1256,6 @@ __global__ void __launch_bounds__(384, 1)
                         }
                     }
                     if (odd && row < R) {
-                        const uint64_t word = word_here();
                         for (int u = 0; u < T; ++u) {
                             const int key = seg.length + u;
                             if (!(word >> u & 1) || key < seg.first * kManyTile || key >= seg.last * kManyTile) continue;
