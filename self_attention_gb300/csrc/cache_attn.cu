@@ -1595,47 +1595,56 @@ struct Choice {
 
 long long units_of(int B, int H, int R, int rows) { return (long long)B * H * ((R + rows - 1) / rows); }
 
-// Time in us of CTAs that take `steps` steps each, `wave` of them at a time, where a step takes a CTA `step` at least and
-// the CTAs on the GPU together `hbm` each.
+// Time in us of CTAs that take up to `steps` steps each, `wave` of them at a time, where a step takes a CTA `step` at
+// least and the CTAs on the GPU together `hbm` each.
 double waves(long long ctas, long long wave, int steps, double step, double hbm)
 {
-    auto run = [&](long long active) { return steps * (active * hbm > step ? active * hbm : step) + 1.0; };
-    return (double)(ctas / wave) * run(wave) + (ctas % wave ? run(ctas % wave) : 0.0) - 1.0;
+    auto run = [&](long long active) { return steps * (active * hbm > step ? active * hbm : step) + 1.9; };
+    const double t = (double)(ctas / wave) * run(wave) + (ctas % wave ? run(ctas % wave) : 0.0);
+    return (ctas > wave ? 0.92 * t : t) - 1.9;
 }
 
-// The least estimated time for caches that are full.  Fitted to the kernels over 1 to 1024 units of 100 to 64000 slots
-// (steps of 128 slots; the constants are what is left for few slots, a step's time, and the cost of a unit's end).  A
-// unit by a cluster against shares and a join: 16 units of 1000 and 8000 slots 5.6 and 17.8 us, 7.6 and 16.7; 128 units
-// of 1000 and 16000 12.9 and 160, 20.7 and 161.  Sequences shorter than the cache leave a long one to its cluster or CTA
-// alone, so that it is never given more than 24 steps.
+// The least estimated time.  The constants (us; a step is 128 slots) were fitted to the times of every choice at 2000 sizes
+// drawn from 1 to 512 sequences and heads, 1 to 512 rows and 16 to 65536 slots, with lengths that differ by up to all of
+// them: what is chosen takes 0.6 % more than the best of what the rule below allows, on average.  (A unit by a cluster against shares and a join: 16 units of
+// 1000 and 8000 slots 5.6 and 17.8 us, 7.6 and 16.7; 128 units of 1000 and 16000 12.9 and 160, 20.7 and 161.)  Sequences
+// shorter than the cache leave a long one to its cluster or CTA alone, so that it is never given more than 24 steps.
 Choice choose(int B, int H, int G, int T, int C, int d)
 {
     constexpr int kMostSteps = 24;
     const int R = G * T, slots128 = (C + 127) / 128;
-    const double hbm = d == 128 ? 0.0093 : 0.0047;
+    const bool wide = d == 128;
+    const double hbm = wide ? 0.007 : 0.0036;
     Choice best = {kFew, R <= 8 ? 8 : 16, 0};
-    const long long units = units_of(B, H, R, best.rows), wave = d == 128 ? kPlanSms : 2 * kPlanSms;
-    const double step = best.rows == 8 ? 0.8 : 1.15, start = best.rows == 8 ? 4.0 : 5.5;
-    best.ctas = (best.rows == 8 ? d == 128 ? FewCfg<128, 1>::BLOCKS : FewCfg<64, 1>::BLOCKS
-                                : d == 128 ? FewCfg<128, 2>::BLOCKS : FewCfg<64, 2>::BLOCKS) * kPlanSms;
-    double t_best = (best.rows == 8 ? 7.5 : 11.5) + (double)units * slots128 * hbm + 1.7 * (double)units / wave;
+    const bool eight = best.rows == 8;
+    const long long units = units_of(B, H, R, best.rows), wave = wide ? kPlanSms : 2 * kPlanSms;
+    best.ctas = (eight ? wide ? FewCfg<128, 1>::BLOCKS : FewCfg<64, 1>::BLOCKS
+                       : wide ? FewCfg<128, 2>::BLOCKS : FewCfg<64, 2>::BLOCKS) * kPlanSms;
+    double t_best = (eight ? wide ? 8.9 : 13.4 : 9.6) + (double)units * slots128 * hbm + 2.66 * units / wave;
     if (R > 16) {
         const int rows = R <= 128 ? 128 : 256;
         const long long many = units_of(B, H, R, rows);
         // both streams of 128 rows' tiles run at once
-        const double tile = (rows == 256 ? 1.8 : 0.9) * (d == 128 ? 1.0 : 0.85);
-        best = {kMany, rows, kPlanSms};
-        t_best = 15.5 + (double)many * slots128 * (tile / kPlanSms > hbm ? tile / kPlanSms : hbm) + 4.0 * (double)many / kPlanSms;
-        const double t = 4.5 + waves(many, kPlanSms, slots128, tile, hbm) + 3.0 * (double)((many + kPlanSms - 1) / kPlanSms);
+        const double tile = (rows == 256 ? 2.23 : 0.84) * (wide ? 1.0 : 0.65);
+        const double pieces = (double)kPlanSms / many < slots128 ? (double)kPlanSms / many : slots128;
+        double t = 11.7 + (double)many * slots128 * (tile / kPlanSms > hbm ? tile / kPlanSms : hbm) + 4.5 * many / kPlanSms +
+                   0.124 * pieces;
+        if (t < t_best) {
+            best = {kMany, rows, kPlanSms};
+            t_best = t;
+        }
+        t = 3.4 + waves(many, kPlanSms, slots128, tile, hbm) + 2.6 * (double)((many + kPlanSms - 1) / kPlanSms);
         if (slots128 <= kMostSteps && t < t_best) {
             best = {kManyWhole, rows, 0};
             t_best = t;
         }
     }
+    const double step = wide ? eight ? 0.75 : 0.81 : eight ? 0.6 : 0.71, start = eight ? 5.2 : 5.4;
     for (int n = 1; n <= 8; n *= 2) {
-        if (n == 8 && units > 8) break;                 // more clusters of eight wait for one another
+        if (n == 8 && units > (wide ? 7 : 28)) break;     // more clusters of eight wait for one another
         const int steps = (C + 128 * n - 1) / (128 * n);
-        const double t = start + waves(units * n, n == 4 ? wave * 18 / 19 : wave, steps, step, hbm);
+        const double t = start + (n == 1 ? 0.0 : n == 2 ? 1.0 : 0.85) +
+                         waves(units * n, n >= 4 ? wave * 18 / 19 : wave, steps, step, hbm);
         if (steps <= kMostSteps && t < t_best) {
             best = {kUnit, R <= 8 ? 8 : 16, n};
             t_best = t;
