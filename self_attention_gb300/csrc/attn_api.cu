@@ -1270,8 +1270,7 @@ extern "C" attn_status attn_cache_attention(const void *q, const void *cache_k, 
     attn_status st = check_cache_attention(B, H, G, T, C, d_k);
     if (st != ATTN_OK) return st;
     if (!std::isfinite(scale) || !(scale > 0.f)) return ATTN_ERR_INVALID_ARG;
-    if (!q || !cache_k || !cache_v || !lengths || !o || !lse || (weights != nullptr) != (weights_out != nullptr) ||
-        (counted && !weights))
+    if (!q || !cache_k || !cache_v || !lengths || !o || !lse || (weights != nullptr) != (weights_out != nullptr))
         return ATTN_ERR_INVALID_ARG;
     const size_t need = cache_attn_workspace(B, H, G, T, C, d_k, weights != nullptr);
     if (!workspace_ok(workspace, workspace_bytes, need)) return ATTN_ERR_WORKSPACE;

@@ -548,8 +548,7 @@ PyObject *cache_attention(Args a)
     const auto *weights = static_cast<const float *>(operand_or_null(a[5], "weights", kF32, {k.B, k.H, k.N}, q.dev));
     const auto *counted = static_cast<const uint64_t *>(operand_or_null(a[6], "counted", kI64, {q.B}, q.dev));
     auto *given = static_cast<float *>(operand_or_null(a[7], "weights_out", kF32, {k.B, k.H, k.N}, q.dev));
-    if (a[5] == Py_None && (a[6] != Py_None || a[7] != Py_None))
-        refuse("counted and weights_out go with weights");
+    if (a[5] == Py_None && a[7] != Py_None) refuse("weights_out goes with weights");
     const auto scale = (float)number(a[8]);
     const bool fresh = a[5] != Py_None && a[7] == Py_None;
     at::Tensor o, lse, out;

@@ -69,7 +69,7 @@ def test_attention_argument_errors(lib):
         a.update(bad)
         assert sa.attn_cache_attention_workspace_size(*a.values(), 64) == 0
     for bad in (dict(scale=0.0), dict(scale=float("nan")), dict(q=0), dict(k=0), dict(v=0), dict(n=0), dict(o=0),
-                dict(l=0), dict(w=0), dict(wo=0), dict(w=0, wo=0), dict(o=A[0]), dict(l=A[8] + 64), dict(wo=A[6] + 4),
+                dict(l=0), dict(w=0), dict(wo=0), dict(o=A[0]), dict(l=A[8] + 64), dict(wo=A[6] + 4),
                 dict(wo=A[2]), dict(ws=A[6]), dict(o=A[10]), dict(l=A[4]), dict(l=A[5])):
         assert att(**bad) == 1, bad
     for bad in (dict(ws=0), dict(nb=need - 1), dict(ws=A[10] + 128)):

@@ -277,11 +277,11 @@ def test_refusals():
     v, n = k.clone(), _i32(1, 2)
     w, tree = torch.zeros(B, H, C, device="cuda"), torch.zeros(B, T, dtype=torch.int64, device="cuda")
     sa.cache_attention(q, k, v, n, tree, weights=w, counted=tree[:, 0].contiguous())
+    assert len(sa.cache_attention(q, k, v, n, tree, counted=tree[:, 0].contiguous())) == 2     # of no account alone
     bad = [dict(q=q.float()), dict(q=q[0]), dict(q=q.transpose(1, 2)), dict(q=q[:, :5].contiguous()), dict(q=q.cpu()),
            dict(k=k.half()), dict(k=k[:1]), dict(v=v[:, :, :-1].contiguous()), dict(v=v.float()), dict(n=n.long()),
            dict(n=n[:1]), dict(n=n.cpu()), dict(tree=tree.int()), dict(tree=tree[:, :2].contiguous()),
-           dict(weights=w.double()), dict(weights=w[..., :-1].contiguous()), dict(weights=None, counted=n.long()),
-           dict(weights=None, weights_out=w), dict(weights_out=w.double()), dict(counted=n)]
+           dict(weights=w.double()), dict(weights=w[..., :-1].contiguous()),            dict(weights=None, weights_out=w), dict(weights_out=w.double()), dict(counted=n)]
     for kw in bad:
         a = dict(q=q, k=k, v=v, n=n, tree=tree, weights=w)
         a.update(kw)
