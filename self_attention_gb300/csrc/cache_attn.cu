@@ -1620,12 +1620,12 @@ Choice choose(int B, int H, int G, int T, int C, int d)
     const long long units = units_of(B, H, R, best.rows), wave = wide ? kPlanSms : 2 * kPlanSms;
     best.ctas = (eight ? wide ? FewCfg<128, 1>::BLOCKS : FewCfg<64, 1>::BLOCKS
                        : wide ? FewCfg<128, 2>::BLOCKS : FewCfg<64, 2>::BLOCKS) * kPlanSms;
-    double t_best = (eight ? wide ? 8.9 : 13.4 : 9.6) + (double)units * slots128 * hbm + 2.66 * units / wave;
+    double t_best = (eight ? wide ? 8.4 : 11.4 : 11.6) + (double)units * slots128 * hbm + 3.3 * units / wave;
     if (R > 16) {
         const int rows = R <= 128 ? 128 : 256;
         const long long many = units_of(B, H, R, rows);
         // both streams of 128 rows' tiles run at once
-        const double tile = (rows == 256 ? 2.23 : 0.84) * (wide ? 1.0 : 0.65);
+        double tile = (rows == 256 ? 2.23 : 0.63) * (wide ? 1.0 : 0.36);
         const double pieces = (double)kPlanSms / many < slots128 ? (double)kPlanSms / many : slots128;
         double t = 11.7 + (double)many * slots128 * (tile / kPlanSms > hbm ? tile / kPlanSms : hbm) + 4.5 * many / kPlanSms +
                    0.124 * pieces;
@@ -1633,17 +1633,18 @@ Choice choose(int B, int H, int G, int T, int C, int d)
             best = {kMany, rows, kPlanSms};
             t_best = t;
         }
+        tile = (rows == 256 ? 1.53 : 0.84) * (wide ? 1.0 : 0.66);
         t = 3.4 + waves(many, kPlanSms, slots128, tile, hbm) + 2.6 * (double)((many + kPlanSms - 1) / kPlanSms);
         if (slots128 <= kMostSteps && t < t_best) {
             best = {kManyWhole, rows, 0};
             t_best = t;
         }
     }
-    const double step = wide ? eight ? 0.75 : 0.81 : eight ? 0.6 : 0.71, start = eight ? 5.2 : 5.4;
+    const double step = wide ? eight ? 0.68 : 0.98 : eight ? 0.6 : 0.71, start = eight ? 5.2 : 5.4;
     for (int n = 1; n <= 8; n *= 2) {
-        if (n == 8 && units > (wide ? 7 : 28)) break;     // more clusters of eight wait for one another
+        if (n == 8 && units > (wide ? 7 : 12)) break;     // more clusters of eight wait for one another
         const int steps = (C + 128 * n - 1) / (128 * n);
-        const double t = start + (n == 1 ? 0.0 : n == 2 ? 1.0 : 0.85) +
+        const double t = start + (n == 1 ? 0.0 : 1.05) +
                          waves(units * n, n >= 4 ? wave * 18 / 19 : wave, steps, step, hbm);
         if (steps <= kMostSteps && t < t_best) {
             best = {kUnit, R <= 8 ? 8 : 16, n};
