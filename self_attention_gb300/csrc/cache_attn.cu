@@ -1,26 +1,31 @@
 // Attention of one token, a chain or a tree of drafted tokens over a cache:
 //   o = sum_j p_j v_j,  p_j = exp(scale q.k_j - lse),  lse = log sum_j exp(scale q.k_j),
 // over the slots j < length and, of the T tokens that follow them in the cache, those that the token's mask
-// word names.  Bound by HBM: each slot's K and V (4 d bytes) meet the few rows of the heads that share them.
+// word names.  Bound by HBM: each slot's K and V (4 d bytes) meet the few rows of the heads that share them; short
+// caches by latency.  The rows of a (sequence, cached head), r = g T + t, are one contiguous block of q and o; a unit is 8,
+// 16, 128 or 256 of them.
 //
-// few_kernel.  The rows of a (sequence, cached head), r = g T + t, are one contiguous block of q and o; a unit is
-// 8 NT of them.  The products are turned round so that the slots are the 16-row operand of mma.sync and the few
-// query rows its 8 columns: S^T = K Q^T, O^T = V^T P^T.  A warp takes 16 slots a step, and K and V go from global
-// memory straight into the operands' registers:
-//   K   thread (g, q) = (lane / 4, lane % 4) loads chunks 4 c + q of slots g and g + 8; the sum over d runs in the
+// Up to 16 rows (unit_kernel, few_kernel; more where the cache is short).  The products are turned round so that the
+// slots are the 16-row operand of mma.sync and the few query rows its 8 columns: S^T = K Q^T, O^T = V^T P^T (a tcgen05
+// tile would be nearly empty with so few rows, and its result is a round trip through tensor memory away; the tensor pipe
+// is at 12 % as it is).  A warp takes 16 slots a step, from a ring that TMA fills for it alone:
+//   K   thread (g, q) = (lane / 4, lane % 4) reads chunks 4 c + q of slots g and g + 8; the sum over d runs in the
 //       order that these chunks give, the same for Q.
-//   V   it loads chunk g (and g + 8) of slots 2 q, 2 q + 1, 2 q + 8, 2 q + 9; two slots' values of a column
+//   V   it reads chunk g (and g + 8) of slots 2 q, 2 q + 1, 2 q + 8, 2 q + 9; two slots' values of a column
 //       are put side by side by byte permutes, and column 8 g + j is row g of the j-th 16-row tile.
 //   P   leaves S^T's accumulator as pairs of rows; movmatrix turns it into pairs of slots.
-// No shared memory, no barrier in the loop: each warp keeps its own running maximum and sum, and K of the next
-// step is asked for as soon as S has consumed this one's, V likewise, so that 8 KB (d = 128) a warp are always
-// on their way.  P meets V as two bf16 terms (its own rounding and the rest), 2^-17 of it: the tensor cores are
-// idle most of the time, and one term alone would cost 2^-9 of each weight.
+// No barrier of the CTA in the loop: each warp keeps its own running maximum and sum, and asks for a step as soon as it
+// has used one up.  Eight warps with three steps each (192 KB an SM on their way at d = 128) draw 6.4 TB/s (32 sequences
+// of 16000 slots and 4 cached heads, 160 us); loads into registers, twelve warps with one step ahead, 6.1 (170 us), and
+// the same ring by cp.async 5.2 (201 us: the copies' instructions sit on each warp's chain).  P meets V as two bf16
+// terms (its own rounding and the rest), 2^-16 of it: one term alone would cost 2^-8 of each weight, and the pipe has room.
 //
-// Work is shared out in blocks of 64 slots over all units, the same number for each CTA (the lengths are on the
-// device, so each CTA finds its range itself).  A unit that one CTA has whole is finished there; the others'
-// parts go to the workspace with their maximum and sum, and join_kernel adds them in the order of their slots:
-// nothing depends on timing, results are bitwise reproducible.
+// Work is shared out in blocks of 128 slots over all units (few_kernel, many_kernel), the same number for each CTA or
+// nearly so (the lengths are on the device: each CTA finds its share itself).  A unit that one CTA has whole is finished
+// there; the others' parts go to the workspace with their maximum and sum, and a second kernel adds them in the order of
+// their slots.  Where a unit's slots are few enough for one CTA or cluster (unit_kernel, many_kernel by whole units)
+// nothing is joined through memory.  choose() takes the kernels by the sizes.  Nothing depends on timing: results are
+// bitwise reproducible.
 #include "cluster.cuh"
 #include "common.cuh"
 #include "kernels.h"
@@ -887,7 +892,10 @@ __global__ void __launch_bounds__(32 * kUnitWarps, UnitCfg<D, NT>::BLOCKS)
 //   warps 10-11 the tiles that end behind the cache: V's rows behind the last token are zeroed, and what is not
 //               finite among the tokens' own (0 times it would be NaN in rows that do not see it; the rows that do
 //               get it when O is written).
-// P is bf16, as V is (the operands of a product share their type).  TMEM columns: S_0, S_1, O_0, O_1.
+// P is bf16, as V is (the operands of a product share their type): up to 2^-8 of each weight, 2.3e-3 of o's norm off where
+// o's own rounding is 1.7e-3.  A second term for the rest, as with few rows, costs 128 rows 9 to 25 % and 256 rows 25 to
+// 35 % (64000 slots of 16 cached heads 112 -> 152 us), since the softmax's chain and the products set the pace here:
+// 5.8 TB/s are drawn at 256 rows, 6.4 at 128.  TMEM columns: S_0, S_1, O_0, O_1.
 constexpr int kManyTile = 128;
 constexpr float kTau = 8.0f;
 
@@ -1514,7 +1522,7 @@ __global__ void __launch_bounds__(256) kept_weights_kernel(const __grid_constant
     }
 }
 
-// The same for more rows: K is read a second time, the rows in eights.  A block takes 64 slots of one (sequence,
+// The same for more rows: K is read a second time, the rows in eights.  A block takes 128 slots of one (sequence,
 // cached head).
 template <int D>
 __global__ void __launch_bounds__(kFewThreads) weights_kernel(CacheAttnArgs a, int blocks)
@@ -1604,11 +1612,12 @@ double waves(long long ctas, long long wave, int steps, double step, double hbm)
     return (ctas > wave ? 0.92 * t : t) - 1.9;
 }
 
-// The least estimated time.  The constants (us; a step is 128 slots) were fitted to the times of every choice at 2000 sizes
-// drawn from 1 to 512 sequences and heads, 1 to 512 rows and 16 to 65536 slots, with lengths that differ by up to all of
-// them: what is chosen takes 0.6 % more than the best of what the rule below allows, on average.  (A unit by a cluster against shares and a join: 16 units of
-// 1000 and 8000 slots 5.6 and 17.8 us, 7.6 and 16.7; 128 units of 1000 and 16000 12.9 and 160, 20.7 and 161.)  Sequences
-// shorter than the cache leave a long one to its cluster or CTA alone, so that it is never given more than 24 steps.
+// The least estimated time.  The constants (us; a step is 128 slots) were fitted to the times of every choice at 2000
+// sizes drawn from 1 to 512 sequences and heads, 1 to 512 rows and 16 to 65536 slots, with lengths that differ by up to
+// all of them: what is chosen takes 0.6 % more on average than the best of what the rule below allows.  (A unit by a
+// cluster against shares and a join: 16 units of 1000 and 8000 slots 5.6 and 17.8 us, 7.6 and 16.7; 128 units of 1000
+// and 16000 12.9 and 160, 20.7 and 161.)  Sequences shorter than the cache leave a long one to its cluster or CTA alone,
+// so that it is never given more than 24 steps.
 Choice choose(int B, int H, int G, int T, int C, int d)
 {
     constexpr int kMostSteps = 24;
