@@ -447,6 +447,17 @@ void refuse_graph(std::initializer_list<PyObject *> operands, const char *what)
             refuse(std::string(what) + " has no backward: run it under torch.no_grad(), or on detached tensors");
 }
 
+// What a call wrote in place: a recorded graph that saved such a tensor refuses its backward, as after PyTorch's own
+// in-place operators.
+void written(std::initializer_list<PyObject *> outputs)
+{
+    for (PyObject *o : outputs) {
+        if (!THPVariable_Check(o)) continue;
+        const at::Tensor &t = THPVariable_Unpack(o);
+        if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+    }
+}
+
 // Turns a position of the pairs, [rotated / 2] int64 (the bits of the C ABI's uint64).
 const uint64_t *turns_of(PyObject *o, c10::Device dev, int64_t &rotated)
 {
@@ -530,6 +541,7 @@ PyObject *cache_append(Args a)
                                  stream(k.dev));
     }
     check(code, "attn_cache_append");
+    written({a[2], a[3], a[11], a[12]});
     return wrap(q_out);
 }
 
@@ -570,6 +582,7 @@ PyObject *cache_attention(Args a)
                                     count(k.H), G, count(q.N), count(k.N), count(q.d), scale, stream(q.dev));
     }
     check(code, "attn_cache_attention");
+    written({a[7]});
     if (a[7] == Py_None) return tuple(o, lse, out);
     return tuple(o, lse, THPVariable_Unpack(a[7]));
 }
@@ -605,6 +618,7 @@ PyObject *cache_evict(Args a)
                                 count(k.N), count(k.d), keep, recent, stream(k.dev));
     }
     check(code, "attn_cache_evict");
+    written({a[0], a[1], a[7], a[8]});
     return tuple(a[7] == Py_None ? w : THPVariable_Unpack(a[7]), a[8] == Py_None ? p : THPVariable_Unpack(a[8]), n);
 }
 

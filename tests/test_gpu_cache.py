@@ -281,7 +281,7 @@ def test_refusals():
     bad = [dict(q=q.float()), dict(q=q[0]), dict(q=q.transpose(1, 2)), dict(q=q[:, :5].contiguous()), dict(q=q.cpu()),
            dict(k=k.half()), dict(k=k[:1]), dict(v=v[:, :, :-1].contiguous()), dict(v=v.float()), dict(n=n.long()),
            dict(n=n[:1]), dict(n=n.cpu()), dict(tree=tree.int()), dict(tree=tree[:, :2].contiguous()),
-           dict(weights=w.double()), dict(weights=w[..., :-1].contiguous()),            dict(weights=None, weights_out=w), dict(weights_out=w.double()), dict(counted=n)]
+           dict(weights=w.double()), dict(weights=w[..., :-1].contiguous()), dict(weights=None, weights_out=w), dict(weights_out=w.double()), dict(counted=n)]
     for kw in bad:
         a = dict(q=q, k=k, v=v, n=n, tree=tree, weights=w)
         a.update(kw)
@@ -585,3 +585,29 @@ def test_streams_at_once():
     for i in range(2):
         for o, lse in got[i]:
             assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+def test_what_is_written_in_place_is_seen_by_recorded_graphs():
+    """A graph that saved a cache, its weights or its positions refuses a backward over what was written since."""
+    g = _gen("written")
+    B, H, C, d = 2, 2, 40, 64
+    ck, cv, k, v = (_randn(g, B, H, n, d) for n in (C, C, 1, 1))
+    w = torch.rand(B, H, C, generator=g, device="cuda")
+    pos = torch.arange(C, dtype=torch.int32, device="cuda").repeat(B, H, 1)
+    lengths = _i32(20, 30)
+    calls = [(lambda: sa.cache_append(k, v, ck, cv, lengths, weights=w, slot_positions=pos), (ck, cv, w, pos)),
+             (lambda: sa.cache_attention(k, ck, cv, lengths, weights=w, weights_out=w), (w,)),
+             (lambda: sa.cache_evict(ck, cv, w, pos, lengths, 16, 4, w, pos), (ck, cv, w, pos))]
+    for call, out in calls:
+        others = [t for t in (ck, cv, w, pos, k, v, lengths) if not any(t is x for x in out)]
+        before = [t._version for t in out], [t._version for t in others]
+        leaf = torch.ones((), device="cuda", requires_grad=True)
+        y = sum((leaf * t).float().sum() for t in out if t.is_floating_point())
+        call()
+        assert all(t._version > n for t, n in zip(out, before[0]))
+        assert [t._version for t in others] == before[1]
+        with pytest.raises(RuntimeError, match="inplace operation"):
+            y.backward()
+    with torch.inference_mode():                       # (such tensors have no version)
+        ci, cj = ck.clone(), cv.clone()
+        sa.cache_append(k, v, ci, cj, lengths)
