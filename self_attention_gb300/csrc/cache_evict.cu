@@ -30,7 +30,7 @@ constexpr int kOwnMoves = 256;           // fewer do
 constexpr int kMoveRows = 32;            // moves a block of move_kernel takes
 
 struct SelShared {
-    uint32_t bins[3][kBins];             // of each pass
+    alignas(16) uint32_t bins[3][kBins]; // of each pass, then a short list of moves
     uint32_t warp[4][32];
     uint32_t prefix;                     // rank bits found so far
     uint32_t need;                       // how many are still to be taken among those with this prefix
@@ -113,10 +113,25 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int st
     ptx::grid_dep_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, bh = blockIdx.x / blocks, b = bh / a.H;
     const int me = blockIdx.x % blocks;          // (= the rank in the cluster)
-    const int L = min(max(a.lengths[b], 0), a.C), n = min(L, a.keep);
     const long long row = (long long)bh * a.C;
     const float *w = a.weights + row;
     const int *pos = a.slot_positions + row;
+    // up to 4096 slots wait in registers for the newest position, more are read again; those of a single block are asked
+    // for along with the length
+    constexpr int HELD = 4;
+    float wr[HELD];
+    int pr[HELD];
+    auto hold = [&](int from, int to) {
+#pragma unroll
+        for (int e = 0; e < HELD; ++e) {
+            const int j = from + e * kSelThreads + tid;
+            wr[e] = j < to ? w[j] : 0.f;
+            pr[e] = j < to ? pos[j] : INT32_MIN;
+        }
+    };
+    const bool early = blocks == 1 && in_smem && a.C <= HELD * kSelThreads;
+    if (early) hold(0, a.C);
+    const int L = min(max(a.lengths[b], 0), a.C), n = min(L, a.keep);
     float *w_out = a.weights_out + row;
     int *pos_out = a.positions_out + row;
     int *moves = a.moves + (long long)bh * stride;
@@ -151,20 +166,12 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int st
     // the newest position
     for (int i = tid; i < 3 * kBins; i += kSelThreads) (&s.bins[0][0])[i] = 0;
     int newest = INT32_MIN;
-    // up to 4096 slots wait in registers for the newest position, more are read again
-    constexpr int HELD = 4;
     const bool held = in_smem && share <= HELD * kSelThreads;
-    float wr[HELD];
-    int pr[HELD];
     if (held) {
+        if (!early) hold(begin, end);
 #pragma unroll
-        for (int e = 0; e < HELD; ++e) {
-            const int j = begin + e * kSelThreads + tid;
-            wr[e] = j < end ? w[j] : 0.f;
-            pr[e] = j < end ? pos[j] : INT32_MIN;
-        }
-#pragma unroll
-        for (int e = 0; e < HELD; ++e) newest = max(newest, pr[e]);
+        for (int e = 0; e < HELD; ++e)
+            if (begin + e * kSelThreads + tid < end) newest = max(newest, pr[e]);
     } else {
 #pragma unroll 8
         for (int j = begin + tid; j < end; j += kSelThreads) newest = max(newest, pos[j]);
@@ -182,6 +189,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int st
     auto rank = [&](int j) { return in_smem ? ranks[j - begin] : rank_of(w[j], pos[j], oldest); };
 
     // the n-th largest rank
+    constexpr uint32_t kAll = 0xffffffffu;
     uint32_t prefix = 0, need = (uint32_t)n;
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
@@ -246,13 +254,14 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int st
         }
         __syncthreads();
         prefix = s.prefix;
-        need = s.need;
+        need = s.have == s.need ? kAll : s.need;
+        if (need == kAll) break;         // all that begin with these bits stay: two passes where weights differ
     }
 
     // In order: ranks above `prefix` stay, and the first `need` that equal it.  A warp takes slots [from, to).
     const int run = (end - begin + 1023) / 1024 * 32, from = min(begin + warp * run, end), to = min(from + run, end);
     uint32_t ties0 = 0, holes = 0, movers = 0, total;
-    if (s.have != need) {            // the order of the ties matters: some of them go
+    if (need != kAll) {              // the order of the ties matters: some of them go
         uint32_t ties = 0;
         for (int j0 = from; j0 < to; j0 += 32) {
             const int j = j0 + lane;
@@ -291,6 +300,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int st
         hole += blocks_before(2, total);
     }
     if (me == 0 && tid == 0) moves[0] = (int)total;
+    int *list = LANES > 0 && blocks == 1 && total < 3 * kBins / 2 ? reinterpret_cast<int *>(&s.bins[0][0]) : moves;
     t = ties0;
 #pragma unroll 2
     for (int j0 = from; j0 < to; j0 += 32) {
@@ -298,8 +308,8 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int st
         const bool k = kept(j, t);
         const uint32_t hb = __ballot_sync(0xffffffffu, j < n && j < to && !k);
         const uint32_t mb = __ballot_sync(0xffffffffu, j >= n && k);
-        if (hb >> lane & 1) moves[2 + 2 * (hole + __popc(hb & below))] = j;
-        if (mb >> lane & 1) moves[3 + 2 * (mover + __popc(mb & below))] = j;
+        if (hb >> lane & 1) list[2 + 2 * (hole + __popc(hb & below))] = j;
+        if (mb >> lane & 1) list[3 + 2 * (mover + __popc(mb & below))] = j;
         hole += __popc(hb);
         mover += __popc(mb);
         if (j < n ? k : j < to && !k) {
@@ -318,7 +328,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int st
         sync();
         constexpr int AT_ONCE = kSelThreads / (LANES > 0 ? LANES : 1), N = 2;
         for (int m = me * AT_ONCE + tid / (LANES > 0 ? LANES : 1); m < (int)total; m += N * blocks * AT_ONCE)
-            move_rows<(LANES > 0 ? LANES : 1), N>(a, bh, moves, (int)total, m, blocks * AT_ONCE);
+            move_rows<(LANES > 0 ? LANES : 1), N>(a, bh, list, (int)total, m, blocks * AT_ONCE);
     } else {
         __syncwarp();
         if (blocks > 1) ptx::cluster_sync_relaxed();     // nobody leaves while its sums are read
