@@ -1433,46 +1433,79 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(CacheAttnArgs a, 
     if (lane == 0) a.lse[blockIdx.x] = all.lse();
 }
 
-// many_kernel's parts: a warp four columns of 32 rows, a block 32 columns of them.
-template <int D>
-__global__ void __launch_bounds__(256) join_many_kernel(CacheAttnArgs a, Plan plan, int rows, int ctas, Parts parts)
+// many_kernel's parts: a block 32 rows and, `sweep` times, 32 / GROUPS columns of them, a warp four columns and every
+// GROUPS-th part, six at once.
+constexpr int kJoinAtOnce = 6;
+constexpr unsigned kJoinBlocks = 4 * 152;
+
+template <int D, int GROUPS>
+__global__ void __launch_bounds__(256, 4) join_many_kernel(CacheAttnArgs a, Plan plan, int rows, int ctas, Parts parts,
+                                                           int sweep)
 {
-    __shared__ uint2 out[32][9];
+    constexpr int QUADS = 8 / GROUPS;
+    __shared__ float4 so[GROUPS][QUADS][32];
+    __shared__ float2 sml[GROUPS][32];
+    __shared__ uint2 out[32][QUADS + 1];
     ptx::grid_dep_launch();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int groups = rows / 32, cols = D / 32;
-    const int col = (int)(blockIdx.x % cols) * 32, group = (int)(blockIdx.x / cols % groups);
-    const unsigned unit = blockIdx.x / (cols * groups);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quad = warp % QUADS, share = warp / QUADS;
+    const unsigned groups = rows / 32, sweeps = D / (4 * QUADS) / sweep;
+    const int first = (int)(blockIdx.x % sweeps) * sweep * 4 * QUADS, group = (int)(blockIdx.x / sweeps % groups);
+    const unsigned unit = blockIdx.x / (sweeps * groups);
     const int tile = (int)(unit % (unsigned)plan.tiles), head = (int)(unit / (unsigned)plan.tiles);
     const int b = head / plan.H, h = head % plan.H, R = a.G * a.T;
-    const int r0 = tile * rows + group * 32;
+    const int r0 = tile * rows + group * 32, r = group * 32 + lane;
     ptx::grid_dep_wait();
     if (r0 >= R) return;
     const Pieces pieces(a, plan, ctas, b, h, tile);
     if (pieces.count == 1) return;
-    Sum sum;
-    float o[4] = {};
-    const int r = group * 32 + lane;
-#pragma unroll 4
-    for (int i = 0; i < pieces.count; ++i) {
-        const long long slot = pieces.slot(i);
-        const float2 ml = parts.ml[slot * rows + r];
-        const float4 v = reinterpret_cast<const float4 *>(parts.o)[(slot * (D / 4) + col / 4 + warp) * rows + r];
-        float f, p;
-        sum.take(ml, f, p);
-        o[0] = o[0] * f + v.x * p;
-        o[1] = o[1] * f + v.y * p;
-        o[2] = o[2] * f + v.z * p;
-        o[3] = o[3] * f + v.w * p;
+    for (int col = first; col < first + sweep * 4 * QUADS; col += 4 * QUADS) {
+        Sum sum;
+        float o[4] = {};
+        auto take = [&](float2 ml, float4 v) {
+            float f, p;
+            sum.take(ml, f, p);
+            o[0] = o[0] * f + v.x * p;
+            o[1] = o[1] * f + v.y * p;
+            o[2] = o[2] * f + v.z * p;
+            o[3] = o[3] * f + v.w * p;
+        };
+        for (int i0 = share; i0 < pieces.count; i0 += GROUPS * kJoinAtOnce) {  // (a part that is not there changes nothing)
+            float2 ml[kJoinAtOnce];
+            float4 v[kJoinAtOnce];
+#pragma unroll
+            for (int e = 0; e < kJoinAtOnce; ++e) {
+                const int i = i0 + GROUPS * e;
+                const long long slot = pieces.slot(i);
+                const bool there = i < pieces.count;
+                ml[e] = there ? parts.ml[slot * rows + r] : make_float2(-INFINITY, 0.f);
+                v[e] = there ? reinterpret_cast<const float4 *>(parts.o)[(slot * (D / 4) + col / 4 + quad) * rows + r]
+                             : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int e = 0; e < kJoinAtOnce; ++e) take(ml[e], v[e]);
+        }
+        if (GROUPS > 1) {
+            so[share][quad][lane] = make_float4(o[0], o[1], o[2], o[3]);
+            if (quad == 0) sml[share][lane] = make_float2(sum.top, sum.l);
+            __syncthreads();
+            if (share == 0) {
+#pragma unroll
+                for (int g = 1; g < GROUPS; ++g) take(sml[g][lane], so[g][quad][lane]);
+            }
+        }
+        if (share == 0) {
+            const float inv = sum.inverse();
+            out[lane][quad] =
+                make_uint2(ptx::pack_bf16x2(o[0] * inv, o[1] * inv), ptx::pack_bf16x2(o[2] * inv, o[3] * inv));
+            if (col == 0 && quad == 0 && r0 + lane < R) a.lse[(long long)head * R + r0 + lane] = sum.lse();
+        }
+        __syncthreads();
+        const int row = threadIdx.x / QUADS, part = threadIdx.x % QUADS;
+        if (row < 32 && r0 + row < R)
+            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.o) + ((long long)head * R + r0 + row) * D + col +
+                                       part * 4) = out[row][part];
+        if (col + 4 * QUADS < first + sweep * 4 * QUADS) __syncthreads();      // `out` is used again
     }
-    const float inv = sum.inverse();
-    out[lane][warp] = make_uint2(ptx::pack_bf16x2(o[0] * inv, o[1] * inv), ptx::pack_bf16x2(o[2] * inv, o[3] * inv));
-    __syncthreads();
-    const int row = threadIdx.x >> 3, part = threadIdx.x & 7;
-    if (r0 + row < R)
-        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.o) + ((long long)head * R + r0 + row) * D + col + part * 4) =
-            out[row][part];
-    if (col == 0 && warp == 0 && r0 + lane < R) a.lse[(long long)head * R + r0 + lane] = sum.lse();
 }
 
 // weights_out = weights + the weights that the counted rows give each slot, from the scores that were kept: four slots a
@@ -1480,6 +1513,7 @@ __global__ void __launch_bounds__(256) join_many_kernel(CacheAttnArgs a, Plan pl
 // bytes) a second time.
 constexpr int kKeptSlots = 1024;     // a block
 
+template <int AT_ONCE>
 __global__ void __launch_bounds__(256) kept_weights_kernel(const __grid_constant__ CacheAttnArgs a, int blocks,
                                                            const float *scores)
 {
@@ -1491,29 +1525,32 @@ __global__ void __launch_bounds__(256) kept_weights_kernel(const __grid_constant
     const int valid = length_of(a.lengths, b, T, a.C) + T;
     const long long at = (long long)head * a.C + j0;
     const float *from = scores + (long long)head * R * a.C + j0;
-    float was[4], s[4], sum[4] = {0.f, 0.f, 0.f, 0.f};
+    float was[4], s[AT_ONCE][4], sum[4] = {0.f, 0.f, 0.f, 0.f};
+    auto load = [&](int r0) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        was[e] = j0 + 256 * e < a.C ? a.weights[at + 256 * e] : 0.f;
-        s[e] = j0 + 256 * e < valid ? from[256 * e] : -INFINITY;
-    }
-    if (threadIdx.x < R) {
-        const bool counted = !a.counted || (a.counted[b] >> (threadIdx.x % T) & 1);
+        for (int i = 0; i < AT_ONCE; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                s[i][e] = r0 + i < R && j0 + 256 * e < valid ? from[(long long)(r0 + i) * a.C + 256 * e] : -INFINITY;
+    };
+#pragma unroll
+    for (int e = 0; e < 4; ++e) was[e] = j0 + 256 * e < a.C ? a.weights[at + 256 * e] : 0.f;
+    load(0);
+    if (threadIdx.x < 16) {
+        const bool counted = threadIdx.x < R && (!a.counted || (a.counted[b] >> (threadIdx.x % T) & 1));
         lse[threadIdx.x] = counted ? a.lse[(long long)head * R + threadIdx.x] * kLog2e : INFINITY;
     }
     __syncthreads();
-#pragma unroll 2
-    for (int r = 0; r < R; ++r) {
-        float next[4];
+    for (int r0 = 0;;) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            next[e] = r + 1 < R && j0 + 256 * e < valid ? from[(long long)(r + 1) * a.C + 256 * e] : -INFINITY;
-        const float x = lse[r];
+        for (int i = 0; i < AT_ONCE; ++i) {
+            const float x = lse[r0 + i];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (x != INFINITY && s[e] != -INFINITY) sum[e] += ptx::ex2(s[e] - x);
-            s[e] = next[e];
+            for (int e = 0; e < 4; ++e)
+                if (x != INFINITY && s[i][e] != -INFINITY) sum[e] += ptx::ex2(s[i][e] - x);
         }
+        if ((r0 += AT_ONCE) >= R) break;
+        load(r0);
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -1754,13 +1791,25 @@ cudaError_t launch(const CacheAttnArgs &a, cudaStream_t stream)
         e = launch_overlapped(join_kernel<D>, dim3(heads * R), dim3(32 * kJoinWarps), 0, 1, stream, a, plan, c.rows, c.ctas,
                               parts);
     if (c.kind == kMany)
-        e = launch_overlapped(join_many_kernel<D>, dim3(heads * plan.tiles * (c.rows / 32) * (D / 32)), dim3(256), 0, 1,
-                              stream, a, plan, c.rows, c.ctas, parts);
+    {
+        // About as many blocks as the GPU holds at once: more go over the columns one after another (128 units of 256 rows 90
+        // -> 79 us), fewer share the parts of a row (one unit of 32000 slots 47 -> 20 us, two of 16000 33 -> 19).
+        const unsigned blocks = heads * plan.tiles * (c.rows / 32) * (D / 32);
+        int groups = 1, sweep = 1;
+        while (groups < 8 && blocks * groups * 2 <= kJoinBlocks) groups *= 2;
+        while (sweep < D / 32 && blocks / sweep > kJoinBlocks) sweep *= 2;
+        auto *const kernel = groups == 8   ? join_many_kernel<D, 8>
+                             : groups == 4 ? join_many_kernel<D, 4>
+                             : groups == 2 ? join_many_kernel<D, 2>
+                                           : join_many_kernel<D, 1>;
+        e = launch_overlapped(kernel, dim3(blocks / sweep * groups), dim3(256), 0, 1, stream, a, plan, c.rows, c.ctas, parts,
+                              sweep);
+    }
     if (e != cudaSuccess || !a.weights) return e;
     if (kept) {
         const int blocks = (a.C + kKeptSlots - 1) / kKeptSlots;
-        return launch_overlapped(kept_weights_kernel, dim3(heads * blocks), dim3(256), 0, 1, stream, a, blocks,
-                                 (const float *)parts.scores);
+        return launch_overlapped(R == 1 ? kept_weights_kernel<1> : kept_weights_kernel<4>, dim3(heads * blocks), dim3(256), 0,
+                                 1, stream, a, blocks, (const float *)parts.scores);
     }
     const int blocks = (a.C + kBlock - 1) / kBlock;
     return launch_overlapped(weights_kernel<D>, dim3(heads * blocks), dim3(kFewThreads), 0, 1, stream, a, blocks);

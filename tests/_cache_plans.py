@@ -31,7 +31,10 @@ BLOCKS = [
     (3, 5, 8, 60, 128, 2900, 100), (40, 8, 1, 33, 64, 300, 260), (2, 3, 2, 64, 128, 20000, 5000), (33, 7, 4, 64, 128, 270, 200),
     (9, 16, 4, 1, 128, 5000, 4900), (9, 16, 3, 4, 64, 5000, 4900), (300, 1, 1, 20, 64, 200, 130), (1, 1, 4, 64, 128, 30000, 0),
     (9, 16, 4, 1, 128, 9000, 8900), (40, 8, 1, 1, 64, 9000, 8000), (20, 8, 3, 4, 128, 6000, 5000), (33, 8, 3, 4, 64, 6500, 5000),
-    (300, 1, 3, 1, 64, 4200, 4100), (11, 7, 2, 33, 128, 1300, 1200), (11, 7, 4, 40, 64, 1300, 1200)]
+    (300, 1, 3, 1, 64, 4200, 4100), (11, 7, 2, 33, 128, 1300, 1200), (11, 7, 4, 40, 64, 1300, 1200),
+    # parts of the larger tiles, joined by few blocks and by many
+    (2, 4, 4, 64, 128, 9000, 3000), (4, 4, 4, 50, 128, 6000, 700), (7, 4, 3, 64, 128, 3700, 900),
+    (11, 4, 3, 64, 128, 3700, 900), (2, 1, 2, 40, 64, 20000, 9000), (10, 4, 5, 50, 64, 8000, 600)]
 
 # T, G, d: masks that are no trees, values that are not finite
 ODD = [(3, 1, 64), (20, 2, 64), (64, 4, 64), (7, 2, 128), (50, 1, 128), (64, 8, 128)]
