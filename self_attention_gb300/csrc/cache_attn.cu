@@ -1436,7 +1436,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(CacheAttnArgs a, 
 // many_kernel's parts: a block 32 rows and, `sweep` times, 32 / GROUPS columns of them, a warp four columns and every
 // GROUPS-th part, six at once.
 constexpr int kJoinAtOnce = 6;
-constexpr unsigned kJoinBlocks = 4 * 152;
+constexpr unsigned kJoinBlocks = 4 * 152;    // 4 an SM
 
 template <int D, int GROUPS>
 __global__ void __launch_bounds__(256, 4) join_many_kernel(CacheAttnArgs a, Plan plan, int rows, int ctas, Parts parts,
@@ -1638,20 +1638,28 @@ struct Choice {
     bool parts() const { return kind == kFew || kind == kMany; }
 };
 
+// Shares of a row's parts in join_many_kernel that has `blocks` blocks without: see launch().
+int join_groups(long long blocks)
+{
+    int groups = 1;
+    while (groups < 8 && blocks * groups * 2 <= kJoinBlocks) groups *= 2;
+    return groups;
+}
+
 long long units_of(int B, int H, int R, int rows) { return (long long)B * H * ((R + rows - 1) / rows); }
 
 // Time in us of CTAs that take up to `steps` steps each, `wave` of them at a time, where a step takes a CTA `step` at
 // least and the CTAs on the GPU together `hbm` each.
 double waves(long long ctas, long long wave, int steps, double step, double hbm)
 {
-    auto run = [&](long long active) { return steps * (active * hbm > step ? active * hbm : step) + 1.9; };
+    auto run = [&](long long active) { return steps * (active * hbm > step ? active * hbm : step) + 2.6; };
     const double t = (double)(ctas / wave) * run(wave) + (ctas % wave ? run(ctas % wave) : 0.0);
-    return (ctas > wave ? 0.92 * t : t) - 1.9;
+    return (ctas > wave ? 0.92 * t : t) - 2.6;
 }
 
 // The least estimated time.  The constants (us; a step is 128 slots) were fitted to the times of every choice at 2000
 // sizes drawn from 1 to 512 sequences and heads, 1 to 512 rows and 16 to 65536 slots, with lengths that differ by up to
-// all of them: what is chosen takes 0.6 % more on average than the best of what the rule below allows.  (A unit by a
+// all of them: what is chosen takes 0.7 % more on average than the best of what the rule below allows, at 700 others.  (A unit by a
 // cluster against shares and a join: 16 units of 1000 and 8000 slots 5.6 and 17.8 us, 7.6 and 16.7; 128 units of 1000
 // and 16000 12.9 and 160, 20.7 and 161.)  Sequences shorter than the cache leave a long one to its cluster or CTA alone,
 // so that it is never given more than 24 steps.
@@ -1666,31 +1674,31 @@ Choice choose(int B, int H, int G, int T, int C, int d)
     const long long units = units_of(B, H, R, best.rows), wave = wide ? kPlanSms : 2 * kPlanSms;
     best.ctas = (eight ? wide ? FewCfg<128, 1>::BLOCKS : FewCfg<64, 1>::BLOCKS
                        : wide ? FewCfg<128, 2>::BLOCKS : FewCfg<64, 2>::BLOCKS) * kPlanSms;
-    double t_best = (eight ? wide ? 8.4 : 11.4 : 11.6) + (double)units * slots128 * hbm + 3.3 * units / wave;
+    double t_best = (eight ? wide ? 9.2 : 13.0 : 12.2) + (double)units * slots128 * hbm + 5.1 * units / wave;
     if (R > 16) {
         const int rows = R <= 128 ? 128 : 256;
         const long long many = units_of(B, H, R, rows);
         // both streams of 128 rows' tiles run at once
-        double tile = (rows == 256 ? 2.23 : 0.63) * (wide ? 1.0 : 0.36);
+        double tile = (rows == 256 ? 2.67 : 0.63) * (wide ? 1.0 : 0.29);
         const double pieces = (double)kPlanSms / many < slots128 ? (double)kPlanSms / many : slots128;
-        double t = 11.7 + (double)many * slots128 * (tile / kPlanSms > hbm ? tile / kPlanSms : hbm) + 4.5 * many / kPlanSms +
-                   0.124 * pieces;
+        double t = 10.5 + (double)many * slots128 * (tile / kPlanSms > hbm ? tile / kPlanSms : hbm) + 4.9 * many / kPlanSms +
+                   0.14 * pieces / join_groups(many * (rows / 32) * (d / 32));
         if (t < t_best) {
             best = {kMany, rows, kPlanSms};
             t_best = t;
         }
-        tile = (rows == 256 ? 1.53 : 0.84) * (wide ? 1.0 : 0.66);
-        t = 3.4 + waves(many, kPlanSms, slots128, tile, hbm) + 2.6 * (double)((many + kPlanSms - 1) / kPlanSms);
+        tile = (rows == 256 ? 1.35 : 0.83) * (wide ? 1.0 : 0.67);
+        t = 3.2 + waves(many, kPlanSms, slots128, tile, hbm) + 2.7 * (double)((many + kPlanSms - 1) / kPlanSms);
         if (slots128 <= kMostSteps && t < t_best) {
             best = {kManyWhole, rows, 0};
             t_best = t;
         }
     }
-    const double step = wide ? eight ? 0.68 : 0.98 : eight ? 0.6 : 0.71, start = eight ? 5.2 : 5.4;
+    const double step = wide ? eight ? 0.68 : 0.98 : eight ? 0.6 : 0.71;
     for (int n = 1; n <= 8; n *= 2) {
-        if (n == 8 && units > (wide ? 7 : 12)) break;     // more clusters of eight wait for one another
+        if (n == 8 && units > (wide ? 15 : 60)) break;    // more clusters of eight wait for one another
         const int steps = (C + 128 * n - 1) / (128 * n);
-        const double t = start + (n == 1 ? 0.0 : 1.05) +
+        const double t = 5.4 + (n == 1 ? 0.0 : 1.2) +
                          waves(units * n, n >= 4 ? wave * 18 / 19 : wave, steps, step, hbm);
         if (steps <= kMostSteps && t < t_best) {
             best = {kUnit, R <= 8 ? 8 : 16, n};
@@ -1795,8 +1803,8 @@ cudaError_t launch(const CacheAttnArgs &a, cudaStream_t stream)
         // About as many blocks as the GPU holds at once: more go over the columns one after another (128 units of 256 rows 90
         // -> 79 us), fewer share the parts of a row (one unit of 32000 slots 47 -> 20 us, two of 16000 33 -> 19).
         const unsigned blocks = heads * plan.tiles * (c.rows / 32) * (D / 32);
-        int groups = 1, sweep = 1;
-        while (groups < 8 && blocks * groups * 2 <= kJoinBlocks) groups *= 2;
+        const int groups = join_groups(blocks);
+        int sweep = 1;
         while (sweep < D / 32 && blocks / sweep > kJoinBlocks) sweep *= 2;
         auto *const kernel = groups == 8   ? join_many_kernel<D, 8>
                              : groups == 4 ? join_many_kernel<D, 4>
