@@ -1659,10 +1659,10 @@ double waves(long long ctas, long long wave, int steps, double step, double hbm)
 
 // The least estimated time.  The constants (us; a step is 128 slots) were fitted to the times of every choice at 2000
 // sizes drawn from 1 to 512 sequences and heads, 1 to 512 rows and 16 to 65536 slots, with lengths that differ by up to
-// all of them: what is chosen takes 0.7 % more on average than the best of what the rule below allows, at 700 others.  (A unit by a
-// cluster against shares and a join: 16 units of 1000 and 8000 slots 5.6 and 17.8 us, 7.6 and 16.7; 128 units of 1000
-// and 16000 12.9 and 160, 20.7 and 161.)  Sequences shorter than the cache leave a long one to its cluster or CTA alone,
-// so that it is never given more than 24 steps.
+// all of them: at 700 others what is chosen takes 0.7 % more on average than the best of what the rule below allows.  (A
+// unit by a cluster against shares and a join: 16 units of 1000 and 8000 slots 5.6 and 17.8 us, 7.6 and 16.7; 128 units
+// of 1000 and 16000 12.9 and 160, 20.7 and 161.)  Sequences shorter than the cache leave a long one to its cluster or CTA
+// alone, so that it is never given more than 24 steps.
 Choice choose(int B, int H, int G, int T, int C, int d)
 {
     constexpr int kMostSteps = 24;
