@@ -841,8 +841,8 @@ __global__ void __launch_bounds__(32 * kUnitWarps, UnitCfg<D, NT>::BLOCKS)
     ptx::cluster_sync();
     // each CTA finishes its share of the rows' pieces of four columns
     constexpr int QUADS = D / 4, ALL = R8 * QUADS;
-    const int share = ALL / ctas;                       // (a power of two of CTAs)
-    for (int i = rank * share + threadIdx.x; i < (rank + 1) * share; i += 32 * kUnitWarps) {
+    const int share = (ALL + ctas - 1) / ctas;
+    for (int i = rank * share + threadIdx.x; i < min((rank + 1) * share, ALL); i += 32 * kUnitWarps) {
         const int r = i / QUADS, c = i % QUADS * 4;
         if (r0 + r >= R) break;
         float2 ml[8];
@@ -1657,9 +1657,13 @@ double waves(long long ctas, long long wave, int steps, double step, double hbm)
     return (ctas > wave ? 0.92 * t : t) - 2.6;
 }
 
+// Clusters of 1 to 8 CTAs of unit_kernel that the GPU holds at once (as CUDA's occupancy call says; one CTA an SM at
+// d = 128, two at 64).
+constexpr short kClusters[2][8] = {{304, 152, 97, 74, 58, 46, 38, 36}, {152, 76, 46, 36, 28, 23, 15, 15}};
+
 // The least estimated time.  The constants (us; a step is 128 slots) were fitted to the times of every choice at 2000
 // sizes drawn from 1 to 512 sequences and heads, 1 to 512 rows and 16 to 65536 slots, with lengths that differ by up to
-// all of them: at 700 others what is chosen takes 0.7 % more on average than the best of what the rule below allows.  (A
+// all of them: at 300 others what is chosen takes 0.7 % more on average than the best of what the rule below allows.  (A
 // unit by a cluster against shares and a join: 16 units of 1000 and 8000 slots 5.6 and 17.8 us, 7.6 and 16.7; 128 units
 // of 1000 and 16000 12.9 and 160, 20.7 and 161.)  Sequences shorter than the cache leave a long one to its cluster or CTA
 // alone, so that it is never given more than 24 steps.
@@ -1695,11 +1699,9 @@ Choice choose(int B, int H, int G, int T, int C, int d)
         }
     }
     const double step = wide ? eight ? 0.68 : 0.98 : eight ? 0.6 : 0.71;
-    for (int n = 1; n <= 8; n *= 2) {
-        if (n == 8 && units > (wide ? 15 : 60)) break;    // more clusters of eight wait for one another
+    for (int n = 1; n <= 8; ++n) {
         const int steps = (C + 128 * n - 1) / (128 * n);
-        const double t = 5.4 + (n == 1 ? 0.0 : 1.2) +
-                         waves(units * n, n >= 4 ? wave * 18 / 19 : wave, steps, step, hbm);
+        const double t = 5.4 + (n == 1 ? 0.0 : 1.2) + waves(units * n, kClusters[wide][n - 1] * n, steps, step, hbm);
         if (steps <= kMostSteps && t < t_best) {
             best = {kUnit, R <= 8 ? 8 : 16, n};
             t_best = t;

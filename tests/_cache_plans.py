@@ -36,6 +36,10 @@ BLOCKS = [
     (2, 4, 4, 64, 128, 9000, 3000), (4, 4, 4, 50, 128, 6000, 700), (7, 4, 3, 64, 128, 3700, 900),
     (11, 4, 3, 64, 128, 3700, 900), (2, 1, 2, 40, 64, 20000, 9000), (10, 4, 5, 50, 64, 8000, 600)]
 
+# units by clusters of every size
+BLOCKS += [(2, 1, 4, T, d, C, 250) for T in (1, 4) for d in (64, 128) for C in (260, 390, 520, 650, 780, 910)]
+BLOCKS += [(8, 5, 4, 1, 128, 390, 300), (8, 5, 3, 3, 128, 386, 300), (6, 9, 3, 3, 64, 650, 500), (20, 8, 2, 1, 128, 210, 200)]
+
 # T, G, d: masks that are no trees, values that are not finite
 ODD = [(3, 1, 64), (20, 2, 64), (64, 4, 64), (7, 2, 128), (50, 1, 128), (64, 8, 128)]
 POISON = [(4, 1, 64), (7, 2, 128), (30, 4, 128), (64, 2, 64), (64, 4, 128), (64, 8, 64)]
@@ -48,3 +52,9 @@ def reached():
     sizes += [(3, 2, G, T, c, d) for T, G, d in ODD for c in (150, ROOM)]
     sizes += [(2, 2, G, T, c, d) for T, G, d in POISON for c in (300, ROOM)]
     return {sa.attn_debug_cache_plan(*x)[:2] + (x[5],) for x in sizes}
+
+
+def clusters():
+    """(CTAs of a cluster, d) of the cases with few rows."""
+    plans = {sa.attn_debug_cache_plan(B, H, G, T, C, d) + (d,) for B, H, G, T, d, C, _ in BLOCKS}
+    return {p[2:] for p in plans if p[0] == 1}

@@ -106,6 +106,11 @@ def test_plans_of_attention_are_all_reached(lib):
     """The GPU tests' sizes reach every kernel that the plan chooses from."""
     want = {(k, r, d) for d in (64, 128) for k, rows in ((1, (8, 16)), (2, (8, 16)), (3, (128, 256)), (4, (128, 256))) for r in rows}
     assert _cache_plans.reached() >= want, want - _cache_plans.reached()
+
+
+def test_clusters_of_every_size_are_reached(lib):
+    want = {(n, d) for n in range(1, 9) for d in (64, 128)}
+    assert _cache_plans.clusters() >= want, want - _cache_plans.clusters()
     with pytest.raises(sa.AttnError):
         sa.attn_debug_cache_plan(1, 1, 1, 65, 100, 64)
     assert lib.attn_debug_cache_plan(1, 1, 1, 1, 100, 64, None) == 1
