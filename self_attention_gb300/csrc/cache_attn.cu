@@ -1650,11 +1650,18 @@ long long units_of(int B, int H, int R, int rows) { return (long long)B * H * ((
 
 // Time in us of CTAs that take up to `steps` steps each, `wave` of them at a time, where a step takes a CTA `step` at
 // least and the CTAs on the GPU together `hbm` each.
-double waves(long long ctas, long long wave, int steps, double step, double hbm)
+double waves(long long ctas, long long wave, double steps, double step, double hbm)
 {
     auto run = [&](long long active) { return steps * (active * hbm > step ? active * hbm : step) + 2.6; };
     const double t = (double)(ctas / wave) * run(wave) + (ctas % wave ? run(ctas % wave) : 0.0);
     return (ctas > wave ? 0.92 * t : t) - 2.6;
+}
+
+// Steps of `slots` each: the mean of a full cache's and of one full to nine tenths (few sequences end at the last slot).
+double steps_of(int C, int slots)
+{
+    const long long c = C, s = slots;
+    return 0.5 * (double)((c + s - 1) / s + (c * 9 / 10 + s - 1) / s);
 }
 
 // Clusters of 1 to 8 CTAs of unit_kernel that the GPU holds at once (as CUDA's occupancy call says; one CTA an SM at
@@ -1663,10 +1670,10 @@ constexpr short kClusters[2][8] = {{304, 152, 97, 74, 58, 46, 38, 36}, {152, 76,
 
 // The least estimated time.  The constants (us; a step is 128 slots) were fitted to the times of every choice at 2000
 // sizes drawn from 1 to 512 sequences and heads, 1 to 512 rows and 16 to 65536 slots, with lengths that differ by up to
-// all of them: at 300 others what is chosen takes 0.7 % more on average than the best of what the rule below allows.  (A
-// unit by a cluster against shares and a join: 16 units of 1000 and 8000 slots 5.6 and 17.8 us, 7.6 and 16.7; 128 units
-// of 1000 and 16000 12.9 and 160, 20.7 and 161.)  Sequences shorter than the cache leave a long one to its cluster or CTA
-// alone, so that it is never given more than 24 steps.
+// all of them: what is chosen takes 0.8 % more on average than the best of what the rule below allows at 300 other sizes,
+// 1.0 % at 1200 where up to a quarter of the room is free.  (A unit by a cluster against shares and a join: 16 units of
+// 1000 and 8000 slots 5.6 and 17.8 us, 7.6 and 16.7; 128 units of 1000 and 16000 12.9 and 160, 20.7 and 161.)  Sequences
+// shorter than the cache leave a long one to its cluster or CTA alone, so that it is never given more than 24 steps.
 Choice choose(int B, int H, int G, int T, int C, int d)
 {
     constexpr int kMostSteps = 24;
@@ -1692,7 +1699,7 @@ Choice choose(int B, int H, int G, int T, int C, int d)
             t_best = t;
         }
         tile = (rows == 256 ? 1.35 : 0.83) * (wide ? 1.0 : 0.67);
-        t = 3.2 + waves(many, kPlanSms, slots128, tile, hbm) + 2.7 * (double)((many + kPlanSms - 1) / kPlanSms);
+        t = 3.2 + waves(many, kPlanSms, steps_of(C, 128), tile, hbm) + 2.7 * (double)((many + kPlanSms - 1) / kPlanSms);
         if (slots128 <= kMostSteps && t < t_best) {
             best = {kManyWhole, rows, 0};
             t_best = t;
@@ -1701,7 +1708,8 @@ Choice choose(int B, int H, int G, int T, int C, int d)
     const double step = wide ? eight ? 0.68 : 0.98 : eight ? 0.6 : 0.71;
     for (int n = 1; n <= 8; ++n) {
         const int steps = (C + 128 * n - 1) / (128 * n);
-        const double t = 5.4 + (n == 1 ? 0.0 : 1.2) + waves(units * n, kClusters[wide][n - 1] * n, steps, step, hbm);
+        const double t =
+            5.4 + (n == 1 ? 0.0 : 1.2) + waves(units * n, kClusters[wide][n - 1] * n, steps_of(C, 128 * n), step, hbm);
         if (steps <= kMostSteps && t < t_best) {
             best = {kUnit, R <= 8 ? 8 : 16, n};
             t_best = t;
@@ -1802,8 +1810,8 @@ cudaError_t launch(const CacheAttnArgs &a, cudaStream_t stream)
                               parts);
     if (c.kind == kMany)
     {
-        // About as many blocks as the GPU holds at once: more go over the columns one after another (128 units of 256 rows 90
-        // -> 79 us), fewer share the parts of a row (one unit of 32000 slots 47 -> 20 us, two of 16000 33 -> 19).
+        // About as many blocks as the GPU holds at once: more go over the columns one after another (128 units of 256
+        // rows 90 -> 79 us), fewer share the parts of a row (one unit of 32000 slots 47 -> 20 us, two of 16000 33 -> 19).
         const unsigned blocks = heads * plan.tiles * (c.rows / 32) * (D / 32);
         const int groups = join_groups(blocks);
         int sweep = 1;
