@@ -6,10 +6,12 @@
 // and a slot that stays in place costs nothing but its rank.
 //
 // select_kernel: a cluster of 1 to 8 blocks a sequence and head, each with a run of its slots; more where the blocks
-// fill the GPU no better (one pass over a slot is some 30 instructions a warp, and there are seven: 16384 slots of 32
-// heads take 35 us by single blocks).  A slot's rank is its weight's bits (weights count as zero where they are
-// negative or NaN), all ones for the newest positions.  The n-th largest rank is found by three histograms of 11, 11
-// and 10 bits over ranks that stay in shared memory (from L2 where they do not fit), each added up over the cluster.
+// fill the GPU no better (one pass over a slot is some 30 instructions a warp, and there are six: 16384 slots of 32
+// heads, most of them evicted, take 27 us by clusters of four and took 35 by single blocks).  A slot's rank is its
+// weight's bits (weights count as zero where they are negative or NaN), all ones for the newest positions.  The n-th
+// largest rank is found by up to three histograms of 11, 11 and 10 bits over ranks that stay in shared memory (from L2
+// where they do not fit), each added up over the cluster; two are enough where no rank that goes begins with the bits of
+// one that stays (a third takes 32 heads of 16384 slots 2 us).
 // Then each warp takes a run of neighbouring slots and numbers its ties, its holes and its movers by ballots, with
 // sums over the warps and the cluster in between: in order without a barrier a step.  move_kernel: the rows, 16 bytes
 // a lane, over the whole GPU.
@@ -368,7 +370,7 @@ cudaError_t launch_evict(const EvictArgs &a, cudaStream_t stream)
     const int stride = moves_stride(a.C, a.keep);
     const int most = most_moves(a.C, a.keep), blocks = a.B * a.H * split;
     // The selecting blocks move the rows too where there are enough of them to keep HBM busy, or little to move (one launch
-    // less, and no hand-over of the list: 128 heads of 2049 slots less one 8.2 us, by two kernels 9.7); a few leave that to
+    // less, and no hand-over of the list: 128 heads of 2049 slots less one 6.8 us, by two kernels 1.5 more); a few leave that to
     // the whole GPU (8 heads of 100000 slots less half 75 us, themselves 114).
     const bool own = blocks >= kOwnBlocks || (long long)most * a.B * a.H <= (long long)kOwnMoves * blocks;
     static std::atomic<bool> set[3][64];
