@@ -393,6 +393,16 @@ def test_evict_of_a_long_cache():
     _check_evict(k, v, w, pos, [3000], 2000, 99)
 
 
+def test_evict_of_whole_halves():
+    """All that stays lies behind all that goes: as many moves as slots stay, around what a block's list holds."""
+    g = _gen("halves")
+    k, v, w, pos = _evict_case(g, 1, 1, 6300, 64)
+    w = torch.arange(6300, device="cuda").float().repeat(1, 80, 1)
+    for keep in (3070, 3071, 3073):
+        ks, vs = k.repeat(1, 80, 1, 1), v.repeat(1, 80, 1, 1)
+        _check_evict(ks, vs, w, pos.repeat(1, 80, 1), [6300], keep, 0)
+
+
 def test_evict_leaves_the_rest():
     """Slots that nothing moves into keep their keys and values, those behind the last among them."""
     g = _gen("rest")
