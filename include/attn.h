@@ -464,7 +464,7 @@ attn_status attn_cache_attention(const void *q, const void *cache_k, const void 
  */
 attn_status attn_debug_cache_plan(int B, int H, int G, int T, int C, int d_k, int *plan);
 
-/* Bytes of device workspace attn_cache_evict() needs (0 for sizes it rejects). */
+/* Bytes of device workspace attn_cache_evict() needs (0 for sizes it rejects, and for small ones, which need none). */
 size_t attn_cache_evict_workspace_size(int B, int H, int C, int d_k, int keep);
 
 /*

@@ -1321,7 +1321,8 @@ extern "C" attn_status attn_cache_evict(void *cache_k, void *cache_v, const floa
     const size_t bh = (size_t)B * H, cache = bh * C * d_k * 2, slots = bh * C * 4;
     const Part ins[3] = {{weights, slots, 4}, {slot_positions, slots, 4}, {lengths, (size_t)B * 4, 4}};
     const Part outs[6] = {{cache_k, cache, 16}, {cache_v, cache, 16}, {weights_out, slots, 4, 0},
-                          {positions_out, slots, 4, 1}, {lengths_out, (size_t)B * 4, 4}, {workspace, need, 256}};
+                          {positions_out, slots, 4, 1}, {lengths_out, (size_t)B * 4, 4},
+                          {need ? workspace : nullptr, need, 256}};
     if ((st = check_parts(ins, outs)) != ATTN_OK) return st;
     DeviceState *dev = nullptr;
     if ((st = device_state(&dev)) != ATTN_OK) return st;

@@ -610,11 +610,12 @@ PyObject *cache_evict(Args a)
         if (a[8] == Py_None) p = empty(slots, kI32, k.dev);
         n = empty({k.B}, kI32, k.dev);
         const size_t bytes = attn_cache_evict_workspace_size(count(k.B), count(k.H), count(k.N), count(k.d), keep);
-        const at::Tensor ws = empty({(int64_t)(bytes ? bytes : 1)}, at::kByte, k.dev);
+        at::Tensor ws;
+        if (bytes) ws = empty({(int64_t)bytes}, at::kByte, k.dev);
         code = attn_cache_evict(k.t.data_ptr(), v, weights, positions, lengths,
                                 w_given || !w.defined() ? w_given : static_cast<float *>(w.data_ptr()),
                                 p_given || !p.defined() ? p_given : static_cast<int *>(p.data_ptr()),
-                                static_cast<int *>(n.data_ptr()), ws.data_ptr(), bytes, count(k.B), count(k.H),
+                                static_cast<int *>(n.data_ptr()), at_or_null(ws), bytes, count(k.B), count(k.H),
                                 count(k.N), count(k.d), keep, recent, stream(k.dev));
     }
     check(code, "attn_cache_evict");

@@ -29,6 +29,7 @@ constexpr int kMaxInSmem = 48 * 1024;    // ranks a block keeps in shared memory
 constexpr int kPlanSms = 152;
 constexpr int kOwnBlocks = 128;          // blocks from which on they move what they select, and moves a block up to which
 constexpr int kOwnMoves = 256;           // fewer do
+constexpr int kListMoves = 3 * kBins / 2; // moves a block's own list has room for, and one more
 constexpr int kMoveRows = 32;            // moves a block of move_kernel takes
 
 struct SelShared {
@@ -147,7 +148,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int st
             w_out[j] = x;
             pos_out[j] = p;
         }
-        if (me == 0 && tid == 0) moves[0] = 0;
+        if (LANES == 0 && me == 0 && tid == 0) moves[0] = 0;
         return;
     }
     const int share = ((L + blocks - 1) / blocks + 31) / 32 * 32;       // slots [begin, end) are this block's
@@ -301,8 +302,8 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int st
         mover += blocks_before(3, movers);
         hole += blocks_before(2, total);
     }
-    if (me == 0 && tid == 0) moves[0] = (int)total;
-    int *list = LANES > 0 && blocks == 1 && total < 3 * kBins / 2 ? reinterpret_cast<int *>(&s.bins[0][0]) : moves;
+    if (LANES == 0 && me == 0 && tid == 0) moves[0] = (int)total;
+    int *list = LANES > 0 && blocks == 1 && total < kListMoves ? reinterpret_cast<int *>(&s.bins[0][0]) : moves;
     t = ties0;
 #pragma unroll 2
     for (int j0 = from; j0 < to; j0 += 32) {
@@ -359,20 +360,31 @@ int select_blocks(int heads, int C)
     return n;
 }
 
+// The selecting blocks move the rows too where there are enough of them to keep HBM busy, or little to move (one launch
+// less, and no hand-over of the list: 128 heads of 2049 slots less one 6.8 us, by two kernels 1.5 more); a few leave that
+// to the whole GPU (8 heads of 100000 slots less half 75 us, themselves 114).
+bool own_moves(int heads, int split, int C, int keep)
+{
+    const long long blocks = (long long)heads * split;
+    return blocks >= kOwnBlocks || (long long)most_moves(C, keep) * heads <= kOwnMoves * blocks;
+}
+
 }  // namespace
 
-size_t evict_workspace(int B, int H, int C, int keep) { return (size_t)B * H * moves_stride(C, keep) * 4; }
+size_t evict_workspace(int B, int H, int C, int keep)
+{
+    const int split = select_blocks(B * H, C);
+    // single blocks that move a short list keep it in shared memory
+    if (split == 1 && own_moves(B * H, split, C, keep) && most_moves(C, keep) < kListMoves) return 0;
+    return (size_t)B * H * moves_stride(C, keep) * 4;
+}
 
 cudaError_t launch_evict(const EvictArgs &a, cudaStream_t stream)
 {
     const int split = select_blocks(a.B * a.H, a.C), share = (a.C + split - 1) / split + 32;
     const int in_smem = share <= kMaxInSmem, bytes = in_smem ? (share + 3) / 4 * 16 : 0;
-    const int stride = moves_stride(a.C, a.keep);
-    const int most = most_moves(a.C, a.keep), blocks = a.B * a.H * split;
-    // The selecting blocks move the rows too where there are enough of them to keep HBM busy, or little to move (one launch
-    // less, and no hand-over of the list: 128 heads of 2049 slots less one 6.8 us, by two kernels 1.5 more); a few leave that to
-    // the whole GPU (8 heads of 100000 slots less half 75 us, themselves 114).
-    const bool own = blocks >= kOwnBlocks || (long long)most * a.B * a.H <= (long long)kOwnMoves * blocks;
+    const int stride = moves_stride(a.C, a.keep), most = most_moves(a.C, a.keep), blocks = a.B * a.H * split;
+    const bool own = own_moves(a.B * a.H, split, a.C, a.keep);
     static std::atomic<bool> set[3][64];
     auto *const kernel = !own ? select_kernel<0> : a.d == 64 ? select_kernel<8> : select_kernel<16>;
     cudaError_t e = raise_smem(reinterpret_cast<const void *>(kernel), kMaxInSmem * 4, set[!own ? 0 : a.d == 64 ? 1 : 2]);

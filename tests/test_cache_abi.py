@@ -79,11 +79,12 @@ def test_attention_argument_errors(lib):
 
 
 def test_evict_argument_errors(lib):
-    need = sa.attn_cache_evict_workspace_size(2, 3, 40, 64, 16)
-    assert need > 0 and sa.attn_cache_evict_workspace_size(2, 3, 40, 64, 0) == 0
-    assert sa.attn_cache_evict_workspace_size(2, 3, 40, 96, 16) == 0
+    need = sa.attn_cache_evict_workspace_size(2, 3, 7000, 64, 16)
+    assert need > 0 and sa.attn_cache_evict_workspace_size(2, 3, 7000, 64, 0) == 0
+    assert sa.attn_cache_evict_workspace_size(2, 3, 7000, 96, 16) == 0
+    assert sa.attn_cache_evict_workspace_size(2, 3, 40, 64, 16) == 0             # by single blocks, in shared memory
 
-    def ev(k=A[0], v=A[1], w=A[2], p=A[3], n=A[4], wo=A[5], po=A[6], no=A[7], ws=A[8], nb=need, B=2, H=3, C=40, d=64,
+    def ev(k=A[0], v=A[1], w=A[2], p=A[3], n=A[4], wo=A[5], po=A[6], no=A[7], ws=A[8], nb=need, B=2, H=3, C=7000, d=64,
            keep=16, recent=4):
         return lib.attn_cache_evict(k, v, w, p, n, wo, po, no, ws, nb, B, H, C, d, keep, recent, None)
     assert ev(d=72) == 2
