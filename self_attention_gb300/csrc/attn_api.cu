@@ -1302,7 +1302,7 @@ extern "C" attn_status attn_debug_cache_plan(int B, int H, int G, int T, int C, 
 
 extern "C" size_t attn_cache_evict_workspace_size(int B, int H, int C, int d_k, int keep)
 {
-    return check_evict(B, H, C, d_k, keep) == ATTN_OK ? align256(evict_workspace(B, H, C, keep)) : 0;
+    return check_evict(B, H, C, d_k, keep) == ATTN_OK ? align256(evict_workspace(B, H, C, d_k, keep)) : 0;
 }
 
 extern "C" attn_status attn_cache_evict(void *cache_k, void *cache_v, const float *weights, const int *slot_positions,

@@ -27,8 +27,9 @@ constexpr int kSelThreads = 1024;
 constexpr int kBins = 2048;
 constexpr int kMaxInSmem = 48 * 1024;    // ranks a block keeps in shared memory (192 KB)
 constexpr int kPlanSms = 152;
-constexpr int kOwnBlocks = 128;          // blocks from which on they move what they select, and moves a block up to which
-constexpr int kOwnMoves = 256;           // fewer do
+constexpr int kOwnBlocks = 128;          // blocks from which on they move what they select,
+constexpr int kOwnElements = 128 * 1024; // up to these elements of k a block, and
+constexpr int kOwnMoves = 256;           // moves a block up to which fewer do
 constexpr int kListMoves = 3 * kBins / 2; // moves a block's own list has room for, and one more
 constexpr int kMoveRows = 32;            // moves a block of move_kernel takes
 
@@ -361,21 +362,22 @@ int select_blocks(int heads, int C)
 }
 
 // The selecting blocks move the rows too where there are enough of them to keep HBM busy, or little to move (one launch
-// less, and no hand-over of the list: 128 heads of 2049 slots less one 6.8 us, by two kernels 1.5 more); a few leave that
-// to the whole GPU (8 heads of 100000 slots less half 75 us, themselves 114).
-bool own_moves(int heads, int split, int C, int keep)
+// less, and no hand-over of the list: 128 heads of 2049 slots less one 6.8 us, by two kernels 1.5 more).  A few leave that
+// to the whole GPU (8 heads of 100000 slots less half 75 us, themselves 114), and so do all of them where it takes longer
+// than the select (d = 128: 32 heads 16384 -> 8192 slots 38.7 us, themselves 43.4; 128 heads 8192 -> 4096 65.7 and 69.1).
+bool own_moves(int heads, int split, int C, int d, int keep)
 {
-    const long long blocks = (long long)heads * split;
-    return blocks >= kOwnBlocks || (long long)most_moves(C, keep) * heads <= kOwnMoves * blocks;
+    const long long blocks = (long long)heads * split, moves = (long long)most_moves(C, keep) * heads;
+    return (blocks >= kOwnBlocks && moves * d <= kOwnElements * blocks) || moves <= kOwnMoves * blocks;
 }
 
 }  // namespace
 
-size_t evict_workspace(int B, int H, int C, int keep)
+size_t evict_workspace(int B, int H, int C, int d, int keep)
 {
     const int split = select_blocks(B * H, C);
     // single blocks that move a short list keep it in shared memory
-    if (split == 1 && own_moves(B * H, split, C, keep) && most_moves(C, keep) < kListMoves) return 0;
+    if (split == 1 && own_moves(B * H, split, C, d, keep) && most_moves(C, keep) < kListMoves) return 0;
     return (size_t)B * H * moves_stride(C, keep) * 4;
 }
 
@@ -384,7 +386,7 @@ cudaError_t launch_evict(const EvictArgs &a, cudaStream_t stream)
     const int split = select_blocks(a.B * a.H, a.C), share = (a.C + split - 1) / split + 32;
     const int in_smem = share <= kMaxInSmem, bytes = in_smem ? (share + 3) / 4 * 16 : 0;
     const int stride = moves_stride(a.C, a.keep), most = most_moves(a.C, a.keep), blocks = a.B * a.H * split;
-    const bool own = own_moves(a.B * a.H, split, a.C, a.keep);
+    const bool own = own_moves(a.B * a.H, split, a.C, a.d, a.keep);
     static std::atomic<bool> set[3][64];
     auto *const kernel = !own ? select_kernel<0> : a.d == 64 ? select_kernel<8> : select_kernel<16>;
     cudaError_t e = raise_smem(reinterpret_cast<const void *>(kernel), kMaxInSmem * 4, set[!own ? 0 : a.d == 64 ? 1 : 2]);

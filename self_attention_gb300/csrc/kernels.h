@@ -237,7 +237,7 @@ struct EvictArgs {
     int *moves;                         // workspace: [B,H] x (count, then pairs)
     int B, H, C, d, keep, recent;
 };
-size_t evict_workspace(int B, int H, int C, int keep);
+size_t evict_workspace(int B, int H, int C, int d, int keep);
 cudaError_t launch_evict(const EvictArgs &a, cudaStream_t stream);
 
 cudaError_t launch_vector_add(const float *a, const float *b, float *c, long long n,

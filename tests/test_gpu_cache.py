@@ -361,7 +361,8 @@ def _check_evict(k, v, w, pos, lens, keep, recent, in_place=False):
     (2, 1, 5000, 64, [5000, 4097], 33, 33), (4, 2, 300, 128, [0, 300, 1, 77], 76, 0),
     (1, 2, 2500, 64, [2500], 2499, 1), (1, 1, 3000, 128, [2999], 1500, 700), (2, 2, 40, 64, [40, 39], 50, 50),
     (1, 1, 20000, 64, [19999], 9000, 100), (3, 4, 9000, 128, [9000, 1000, 8123], 999, 998), (10, 5, 4200, 64, [4200 - 7 * i for i in range(10)], 4100, 1),
-    (30, 5, 1100, 64, [1100] * 30, 1000, 5), (1, 3, 16400, 128, [5], 3, 1)])
+    (30, 5, 1100, 64, [1100] * 30, 1000, 5), (1, 3, 16400, 128, [5], 3, 1),
+    (16, 8, 3000, 128, [3000 - 11 * i for i in range(16)], 1400, 100), (4, 8, 9000, 128, [9000, 8999, 4000, 0], 4500, 50)])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_evict(B, H, C, d, lens, keep, recent, in_place):
     g = _gen(B, H, C, lens, keep, recent, in_place)
