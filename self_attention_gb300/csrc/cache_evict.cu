@@ -23,13 +23,13 @@
 namespace attn {
 namespace {
 
-constexpr int kSelThreads = 1024;
 constexpr int kBins = 2048;
 constexpr int kMaxInSmem = 48 * 1024;    // ranks a block keeps in shared memory (192 KB)
 constexpr int kPlanSms = 152;
 constexpr int kOwnBlocks = 128;          // blocks from which on they move what they select,
 constexpr int kOwnElements = 128 * 1024; // up to these elements of k a block, and
 constexpr int kOwnMoves = 256;           // moves a block up to which fewer do
+constexpr int kSmallSlots = 8192;        // up to which two blocks of 512 threads share an SM
 constexpr int kListMoves = 3 * kBins / 2; // moves a block's own list has room for, and one more
 constexpr int kMoveRows = 32;            // moves a block of move_kernel takes
 
@@ -54,12 +54,13 @@ __device__ __forceinline__ uint32_t warp_scan(uint32_t v, uint32_t lane)
 }
 
 // Sum of `v` over the warps before this one, `total` over all of them; v is the same in all lanes of a warp.
+template <int WARPS>
 __device__ __forceinline__ uint32_t warps_before(uint32_t v, uint32_t *buf, uint32_t &total)
 {
     const uint32_t lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     if (lane == 0) buf[w] = v;
     __syncthreads();
-    const uint32_t part = buf[lane], sums = warp_scan(part, lane);
+    const uint32_t part = lane < WARPS ? buf[lane] : 0u, sums = warp_scan(part, lane);
     total = __shfl_sync(0xffffffffu, sums, 31);
     return __shfl_sync(0xffffffffu, sums - part, w);
 }
@@ -108,8 +109,8 @@ __device__ __forceinline__ void move_rows(const EvictArgs &a, int bh, const int 
 }
 
 // LANES > 0: the blocks move the rows themselves, 0: move_kernel does.
-template <int LANES>
-__global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int stride, int in_smem, int blocks)
+template <int LANES, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) select_kernel(EvictArgs a, int stride, int in_smem, int blocks)
 {
     extern __shared__ __align__(16) uint32_t ranks[];
     __shared__ SelShared s;
@@ -122,18 +123,18 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int st
     const int *pos = a.slot_positions + row;
     // up to 4096 slots wait in registers for the newest position, more are read again; those of a single block are asked
     // for along with the length
-    constexpr int HELD = 4;
+    constexpr int WARPS = THREADS / 32, HELD = 4096 / THREADS;
     float wr[HELD];
     int pr[HELD];
     auto hold = [&](int from, int to) {
 #pragma unroll
         for (int e = 0; e < HELD; ++e) {
-            const int j = from + e * kSelThreads + tid;
+            const int j = from + e * THREADS + tid;
             wr[e] = j < to ? w[j] : 0.f;
             pr[e] = j < to ? pos[j] : INT32_MIN;
         }
     };
-    const bool early = blocks == 1 && in_smem && a.C <= HELD * kSelThreads;
+    const bool early = blocks == 1 && in_smem && a.C <= HELD * THREADS;
     if (early) hold(0, a.C);
     const int L = min(max(a.lengths[b], 0), a.C), n = min(L, a.keep);
     float *w_out = a.weights_out + row;
@@ -143,7 +144,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int st
     // what lies behind the kept slots is empty; sources of moves are emptied by those who read them
     if (n == L) {
 #pragma unroll 4
-        for (int j = me * kSelThreads + tid; j < a.C; j += blocks * kSelThreads) {
+        for (int j = me * THREADS + tid; j < a.C; j += blocks * THREADS) {
             const float x = j < n ? w[j] : 0.f;
             const int p = j < n ? pos[j] : -1;
             w_out[j] = x;
@@ -168,22 +169,22 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int st
     };
 
     // the newest position
-    for (int i = tid; i < 3 * kBins; i += kSelThreads) (&s.bins[0][0])[i] = 0;
+    for (int i = tid; i < 3 * kBins; i += THREADS) (&s.bins[0][0])[i] = 0;
     int newest = INT32_MIN;
-    const bool held = in_smem && share <= HELD * kSelThreads;
+    const bool held = in_smem && share <= HELD * THREADS;
     if (held) {
         if (!early) hold(begin, end);
 #pragma unroll
         for (int e = 0; e < HELD; ++e)
-            if (begin + e * kSelThreads + tid < end) newest = max(newest, pr[e]);
+            if (begin + e * THREADS + tid < end) newest = max(newest, pr[e]);
     } else {
 #pragma unroll 8
-        for (int j = begin + tid; j < end; j += kSelThreads) newest = max(newest, pos[j]);
+        for (int j = begin + tid; j < end; j += THREADS) newest = max(newest, pos[j]);
     }
     newest = __reduce_max_sync(0xffffffffu, newest);
     if (lane == 0) s.warp[0][warp] = (uint32_t)newest;
     __syncthreads();
-    newest = __reduce_max_sync(0xffffffffu, (int)s.warp[0][lane]);
+    newest = __reduce_max_sync(0xffffffffu, lane < WARPS ? (int)s.warp[0][lane] : INT32_MIN);
     if (blocks > 1) {
         if (tid == 0) s.sums[0] = (uint32_t)newest;
         sync();
@@ -212,49 +213,56 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int st
         if (pass == 0 && held) {
 #pragma unroll
             for (int e = 0; e < HELD; ++e) {
-                const int j = begin + e * kSelThreads + tid;
+                const int j = begin + e * THREADS + tid;
                 const uint32_t r = rank_of(wr[e], pr[e], oldest);
                 if (j < end) ranks[j - begin] = r;
-                if (begin + e * kSelThreads < end) count(r, j < end);
+                if (begin + e * THREADS < end) count(r, j < end);
             }
         } else if (pass == 0) {
 #pragma unroll 4
-            for (int j0 = begin; j0 < end; j0 += kSelThreads) {
+            for (int j0 = begin; j0 < end; j0 += THREADS) {
                 const int j = j0 + tid;
                 const uint32_t r = j < end ? rank_of(w[j], pos[j], oldest) : 0u;
                 if (in_smem && j < end) ranks[j - begin] = r;
                 count(r, j < end);
             }
         } else {
-            for (int j0 = begin; j0 < end; j0 += kSelThreads) {
+            for (int j0 = begin; j0 < end; j0 += THREADS) {
                 const int j = j0 + tid;
                 count(j < end ? rank(j) : 0u, j < end);
             }
         }
         sync();
-        // bins from the top: thread t holds bins 2 (1023 - t) + 1 and 2 (1023 - t)
-        const int top = 2 * (kSelThreads - 1 - tid) + 1;
-        uint32_t c1 = bins[top], c0 = bins[top - 1];
-        if (blocks > 1) {
-            uint2 c[7];
+        // bins from the top: thread t holds PER of them
+        constexpr int PER = kBins / THREADS;
+        const int base = PER * (THREADS - 1 - tid);
+        uint32_t c[PER], sum = 0;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) c[e] = bins[base + e];
+        if (PER == 2 && blocks > 1) {
+            uint2 x[7];
 #pragma unroll
             for (int k = 1; k < 8; ++k)
-                c[k - 1] = k < blocks ? ptx::ld_cluster_b64(other(&bins[top - 1], me ^ k)) : make_uint2(0, 0);
+                x[k - 1] = k < blocks ? ptx::ld_cluster_b64(other(&bins[base], me ^ k)) : make_uint2(0, 0);
 #pragma unroll
             for (int k = 0; k < 7; ++k) {
-                c0 += c[k].x;
-                c1 += c[k].y;
+                c[0] += x[k].x;
+                c[1] += x[k].y;
             }
         }
-        const uint32_t inc = warp_scan(c0 + c1, lane);
+#pragma unroll
+        for (int e = 0; e < PER; ++e) sum += c[e];
+        const uint32_t inc = warp_scan(sum, lane);
         uint32_t total;
-        const uint32_t above =
-            warps_before(__shfl_sync(0xffffffffu, inc, 31), s.warp[1], total) + inc - c0 - c1;
-        if (above < need && need <= above + c0 + c1) {
-            const bool first = need <= above + c1;
-            s.prefix = prefix | (uint32_t)(first ? top : top - 1) << shift;
-            s.need = need - above - (first ? 0 : c1);
-            s.have = first ? c1 : c0;
+        uint32_t above = warps_before<WARPS>(__shfl_sync(0xffffffffu, inc, 31), s.warp[1], total) + inc - sum;
+#pragma unroll
+        for (int e = PER - 1; e >= 0; --e) {
+            if (above < need && need <= above + c[e]) {
+                s.prefix = prefix | (uint32_t)(base + e) << shift;
+                s.need = need - above;
+                s.have = c[e];
+            }
+            above += c[e];
         }
         __syncthreads();
         prefix = s.prefix;
@@ -263,7 +271,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int st
     }
 
     // In order: ranks above `prefix` stay, and the first `need` that equal it.  A warp takes slots [from, to).
-    const int run = (end - begin + 1023) / 1024 * 32, from = min(begin + warp * run, end), to = min(from + run, end);
+    const int run = (end - begin + THREADS - 1) / THREADS * 32, from = min(begin + warp * run, end), to = min(from + run, end);
     uint32_t ties0 = 0, holes = 0, movers = 0, total;
     if (need != kAll) {              // the order of the ties matters: some of them go
         uint32_t ties = 0;
@@ -271,7 +279,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int st
             const int j = j0 + lane;
             ties += __popc(__ballot_sync(0xffffffffu, j < to && rank(j) == prefix));
         }
-        ties0 = warps_before(ties, s.warp[0], total);
+        ties0 = warps_before<WARPS>(ties, s.warp[0], total);
         if (blocks > 1) {
             if (tid == 0) s.sums[1] = total;
             sync();
@@ -293,7 +301,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int st
         holes += __popc(__ballot_sync(0xffffffffu, j < n && j < to && !k));
         movers += __popc(__ballot_sync(0xffffffffu, j >= n && k));
     }
-    uint32_t hole = warps_before(holes, s.warp[2], total), mover = warps_before(movers, s.warp[3], movers);
+    uint32_t hole = warps_before<WARPS>(holes, s.warp[2], total), mover = warps_before<WARPS>(movers, s.warp[3], movers);
     if (blocks > 1) {
         if (tid == 0) {
             s.sums[2] = total;
@@ -323,14 +331,14 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a, int st
             pos_out[j] = p;
         }
     }
-    for (int j = L + me * kSelThreads + tid; j < a.C; j += blocks * kSelThreads) {
+    for (int j = L + me * THREADS + tid; j < a.C; j += blocks * THREADS) {
         w_out[j] = 0.f;
         pos_out[j] = -1;
     }
     if (LANES > 0) {
         // the list is complete, and nothing of the sources' numbers is needed any more but by those who move them
         sync();
-        constexpr int AT_ONCE = kSelThreads / (LANES > 0 ? LANES : 1), N = 2;
+        constexpr int AT_ONCE = THREADS / (LANES > 0 ? LANES : 1), N = 2;
         for (int m = me * AT_ONCE + tid / (LANES > 0 ? LANES : 1); m < (int)total; m += N * blocks * AT_ONCE)
             move_rows<(LANES > 0 ? LANES : 1), N>(a, bh, list, (int)total, m, blocks * AT_ONCE);
     } else {
@@ -387,12 +395,21 @@ cudaError_t launch_evict(const EvictArgs &a, cudaStream_t stream)
     const int in_smem = share <= kMaxInSmem, bytes = in_smem ? (share + 3) / 4 * 16 : 0;
     const int stride = moves_stride(a.C, a.keep), most = most_moves(a.C, a.keep), blocks = a.B * a.H * split;
     const bool own = own_moves(a.B * a.H, split, a.C, a.d, a.keep);
-    static std::atomic<bool> set[3][64];
-    auto *const kernel = !own ? select_kernel<0> : a.d == 64 ? select_kernel<8> : select_kernel<16>;
-    cudaError_t e = raise_smem(reinterpret_cast<const void *>(kernel), kMaxInSmem * 4, set[!own ? 0 : a.d == 64 ? 1 : 2]);
+    // Two smaller blocks an SM where larger ones would come in waves (512 heads of 2049 slots less one 15.0 us, by 1024
+    // threads 22.4; 256 heads 4096 -> 2048 62.9 and 66.5); not for long runs (160 heads of 20000 slots 109, and 105 as it is).
+    const bool small = split == 1 && blocks > kPlanSms && a.C <= kSmallSlots;
+    static std::atomic<bool> set[6][64];
+    const int which = (!own ? 0 : a.d == 64 ? 1 : 2) + (small ? 3 : 0);
+    auto *const kernel = which == 0   ? select_kernel<0, 1024>
+                         : which == 1 ? select_kernel<8, 1024>
+                         : which == 2 ? select_kernel<16, 1024>
+                         : which == 3 ? select_kernel<0, 512>
+                         : which == 4 ? select_kernel<8, 512>
+                                      : select_kernel<16, 512>;
+    cudaError_t e = raise_smem(reinterpret_cast<const void *>(kernel), kMaxInSmem * 4, set[which]);
     if (e != cudaSuccess) return e;
-    e = launch_overlapped(kernel, dim3((unsigned)blocks), dim3(kSelThreads), (size_t)bytes, (unsigned)split, stream, a, stride,
-                          in_smem, split);
+    e = launch_overlapped(kernel, dim3((unsigned)blocks), dim3(small ? 512 : 1024), (size_t)bytes, (unsigned)split, stream, a,
+                          stride, in_smem, split);
     if (e != cudaSuccess || most == 0 || own) return e;
     const int each = (most + kMoveRows - 1) / kMoveRows;     // blocks a sequence and head
     const dim3 grid((unsigned)each * (unsigned)(a.B * a.H));
