@@ -903,8 +903,10 @@ def cache_append(k, v, cache_k, cache_v, lengths, turns=None, positions=None, in
     path of a tree), none where negative.  weights [B, H, C] fp32 is zeroed in the new slots, slot_positions
     [B, H, C] int32 takes the positions.  q [B, Hq, T, d_k]: the tokens' queries, returned turned (else None)."""
     fn = _binding().cache_append
-    args = (k, v, cache_k, cache_v, lengths, turns, positions, interleaved, amplitude, rows, q, weights, slot_positions)
-    return fn(*args) if stream is None else _on(stream, fn, *args)
+    if stream is None:
+        return fn(k, v, cache_k, cache_v, lengths, turns, positions, interleaved, amplitude, rows, q, weights, slot_positions)
+    return _on(stream, fn, k, v, cache_k, cache_v, lengths, turns, positions, interleaved, amplitude, rows, q, weights,
+               slot_positions)
 
 
 def cache_attention(q, cache_k, cache_v, lengths, tree=None, weights=None, counted=None, weights_out=None,
@@ -916,10 +918,9 @@ def cache_attention(q, cache_k, cache_v, lengths, tree=None, weights=None, count
     With weights [B, H, C] fp32, (o, lse, weights_out): weights with the attention that each slot got from the tokens
     added, from those of bits counted [B] int64 alone where given; weights_out may be weights itself."""
     fn = _binding().cache_attention
-    scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else scale
-    args = (q, cache_k, cache_v, lengths, tree, weights, counted, weights_out, scale)
-    out = fn(*args) if stream is None else _on(stream, fn, *args)
-    return out[:2] if weights is None else out
+    if stream is None:
+        return fn(q, cache_k, cache_v, lengths, tree, weights, counted, weights_out, scale)
+    return _on(stream, fn, q, cache_k, cache_v, lengths, tree, weights, counted, weights_out, scale)
 
 
 def cache_evict(cache_k, cache_v, weights, slot_positions, lengths, keep: int, recent: int = 0, weights_out=None,
@@ -930,5 +931,6 @@ def cache_evict(cache_k, cache_v, weights, slot_positions, lengths, keep: int, r
     slot_positions [B, H, C] int32 are moved alike, 0 and -1 behind (weights_out and positions_out: where to write
     them, their inputs among the choices); the lengths are a new [B] int32."""
     fn = _binding().cache_evict
-    args = (cache_k, cache_v, weights, slot_positions, lengths, keep, recent, weights_out, positions_out)
-    return fn(*args) if stream is None else _on(stream, fn, *args)
+    if stream is None:
+        return fn(cache_k, cache_v, weights, slot_positions, lengths, keep, recent, weights_out, positions_out)
+    return _on(stream, fn, cache_k, cache_v, weights, slot_positions, lengths, keep, recent, weights_out, positions_out)

@@ -14,6 +14,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <initializer_list>
 #include <string>
 
@@ -545,7 +546,7 @@ PyObject *cache_append(Args a)
     return wrap(q_out);
 }
 
-// q, cache_k, cache_v, lengths, tree, weights, counted, weights_out, scale -> (o, lse, weights_out or None)
+// q, cache_k, cache_v, lengths, tree, weights, counted, weights_out, scale or None -> (o, lse), and weights_out with weights
 PyObject *cache_attention(Args a)
 {
     const HeadsOf q(a[0], "q"), k(a[1], "cache_k");
@@ -561,7 +562,7 @@ PyObject *cache_attention(Args a)
     const auto *counted = static_cast<const uint64_t *>(operand_or_null(a[6], "counted", kI64, {q.B}, q.dev));
     auto *given = static_cast<float *>(operand_or_null(a[7], "weights_out", kF32, {k.B, k.H, k.N}, q.dev));
     if (a[5] == Py_None && a[7] != Py_None) refuse("weights_out goes with weights");
-    const auto scale = (float)number(a[8]);
+    const auto scale = (float)(a[8] == Py_None ? 1.0 / std::sqrt((double)q.d) : number(a[8]));
     const bool fresh = a[5] != Py_None && a[7] == Py_None;
     at::Tensor o, lse, out;
     int code;
@@ -583,6 +584,7 @@ PyObject *cache_attention(Args a)
     }
     check(code, "attn_cache_attention");
     written({a[7]});
+    if (a[5] == Py_None) return tuple(o, lse);
     if (a[7] == Py_None) return tuple(o, lse, out);
     return tuple(o, lse, THPVariable_Unpack(a[7]));
 }
