@@ -281,7 +281,8 @@ def test_refusals():
     bad = [dict(q=q.float()), dict(q=q[0]), dict(q=q.transpose(1, 2)), dict(q=q[:, :5].contiguous()), dict(q=q.cpu()),
            dict(k=k.half()), dict(k=k[:1]), dict(v=v[:, :, :-1].contiguous()), dict(v=v.float()), dict(n=n.long()),
            dict(n=n[:1]), dict(n=n.cpu()), dict(tree=tree.int()), dict(tree=tree[:, :2].contiguous()),
-           dict(weights=w.double()), dict(weights=w[..., :-1].contiguous()), dict(weights=None, weights_out=w), dict(weights_out=w.double()), dict(counted=n)]
+           dict(weights=w.double()), dict(weights=w[..., :-1].contiguous()), dict(weights=None, weights_out=w),
+           dict(weights_out=w.double()), dict(counted=n)]
     for kw in bad:
         a = dict(q=q, k=k, v=v, n=n, tree=tree, weights=w)
         a.update(kw)
@@ -362,7 +363,9 @@ def _check_evict(k, v, w, pos, lens, keep, recent, in_place=False):
     (1, 2, 2500, 64, [2500], 2499, 1), (1, 1, 3000, 128, [2999], 1500, 700), (2, 2, 40, 64, [40, 39], 50, 50),
     (1, 1, 20000, 64, [19999], 9000, 100), (3, 4, 9000, 128, [9000, 1000, 8123], 999, 998), (10, 5, 4200, 64, [4200 - 7 * i for i in range(10)], 4100, 1),
     (30, 5, 1100, 64, [1100] * 30, 1000, 5), (1, 3, 16400, 128, [5], 3, 1),
-    (16, 8, 3000, 128, [3000 - 11 * i for i in range(16)], 1400, 100), (4, 8, 9000, 128, [9000, 8999, 4000, 0], 4500, 50)])
+    (16, 8, 3000, 128, [3000 - 11 * i for i in range(16)], 1400, 100), (4, 8, 9000, 128, [9000, 8999, 4000, 0], 4500, 50),
+    (40, 4, 1100, 64, [1100 - i for i in range(40)], 1000, 5), (4, 40, 1100, 128, [1100, 1000, 501, 31], 500, 50),
+    (2, 90, 5001, 128, [5001, 4000], 2400, 100), (2, 80, 8192, 64, [8192, 8000], 900, 10), (2, 80, 8193, 64, [8193, 33], 900, 10)])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_evict(B, H, C, d, lens, keep, recent, in_place):
     g = _gen(B, H, C, lens, keep, recent, in_place)
@@ -376,6 +379,7 @@ def test_evict_ties_and_odd_weights():
     w = (w * 2).floor().clamp_max(3.0)                       # a handful of values, most of them zero
     w[0, 0, 5], w[0, 0, 2000], w[0, 1, 7], w[1, 0, 1111] = NAN, -3.0, math.inf, -math.inf
     w[1, 1] = 0
+    _check_evict(*(t.repeat(1, 40, *[1] * (t.dim() - 2)) for t in (k, v, w, pos)), [2300, 2200], 900, 50)
     _check_evict(k, v, w, pos, [2300, 2200], 900, 50)
     k, v, w, pos = _evict_case(g, B, H, C, d)
     w[0, 0] = 1e-42                                          # subnormal
@@ -399,9 +403,9 @@ def test_evict_of_whole_halves():
     g = _gen("halves")
     k, v, w, pos = _evict_case(g, 1, 1, 6300, 64)
     w = torch.arange(6300, device="cuda").float().repeat(1, 80, 1)
-    for keep in (3070, 3071, 3073):
-        ks, vs = k.repeat(1, 80, 1, 1), v.repeat(1, 80, 1, 1)
-        _check_evict(ks, vs, w, pos.repeat(1, 80, 1), [6300], keep, 0)
+    for heads, keep in ((80, 3070), (80, 3071), (80, 3073), (160, 2000), (160, 3071)):
+        ks, vs = k.repeat(1, heads, 1, 1), v.repeat(1, heads, 1, 1)
+        _check_evict(ks, vs, w[:, :1].repeat(1, heads, 1), pos.repeat(1, heads, 1), [6300], keep, 0)
 
 
 def test_evict_leaves_the_rest():
