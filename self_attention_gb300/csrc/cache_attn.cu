@@ -474,8 +474,9 @@ struct Rows {
             }
         }
         // A token's value that is not finite may reach the rows that see it alone, but 0 times it is NaN in a
-        // product: such values are added one by one and leave the operand.  Rare, and only among the T tokens.
-        if (tail && T > 1) {
+        // product: such values are added one by one and leave the operand.  Rare, and only among the T tokens (a mask word
+        // may leave out a single one; without masks it sees itself).
+        if (tail && (T > 1 || a.tree)) {
             bool odd = false;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
