@@ -57,3 +57,74 @@ def test_a_single_token_that_does_not_see_itself(G, d, value, C):
     ref.check("o", o, *want_o)
     ref.check("lse", lse, *want_l)
     ref.check("weights", out, *want_w)
+
+
+def _lay(v, lens, T, g):
+    """Values that are not finite among the cached slots and the first token's: one of each kind alone in a column, the
+    two infinities together, an infinity with NaN, and the same infinity twice; every chunk of columns has some."""
+    B, H, _, d = v.shape
+    for b, n in enumerate(lens):
+        for h in range(H):
+            at = torch.randint(0, n + 1, (d,), generator=g, device="cuda").tolist()      # (slot n: the first token's)
+            for c in range(0, d, 3):
+                kind = (c // 3 + h + b) % 7
+                v[b, h, at[c], c] = (INF, -INF, NAN, INF, INF, -INF, INF)[kind]
+                if kind in (3, 4, 5, 6) and at[c + 1 - (c == d - 1)] != at[c]:
+                    v[b, h, at[c + 1 - (c == d - 1)], c] = (-INF, NAN, -INF, INF)[kind - 3]
+
+
+# B, H, G, T, d, C, lengths
+INFINITIES = [(2, 2, 1, 1, d, 130, [0, 129]) for d in (64, 128)]
+INFINITIES += [(4, 2, G, T, d, C, [0, 7, 100, 299 - T]) for G, T in ((1, 1), (4, 1), (3, 3), (16, 1), (2, 8), (17, 1), (9, 20))
+               for d in (64, 128) for C in (300, ROOM)]
+INFINITIES += [(2, 2, 4, 1, d, ROOM, [39000, 777]) for d in (64, 128)]                       # parts, joined
+INFINITIES += [(2, 2, 3, 5, d, ROOM, [39000, 777]) for d in (64, 128)]
+INFINITIES += [(2, 2, 10, 5, d, ROOM, [39000, 777]) for d in (64, 128)]
+INFINITIES += [(33, 3, 2, 2, d, 5000, [4990 - 151 * i for i in range(33)]) for d in (64, 128)]    # runs over several units
+INFINITIES += [(40, 8, 1, 33, d, 300, [260 - 6 * i for i in range(40)]) for d in (64, 128)]      # whole units of larger tiles
+
+
+def test_the_sizes_reach_every_kernel():
+    plans = {sa.attn_debug_cache_plan(B, H, G, T, C, d)[:2] + (d,) for B, H, G, T, d, C, _ in INFINITIES}
+    assert plans >= {(kind, rows, d) for kind in (1, 2) for rows in (8, 16) for d in (64, 128)}, plans
+    assert {(3, 128), (4, 128)} <= {p[:2] for p in plans}, plans
+
+
+@pytest.mark.parametrize("B,H,G,T,d,C,lens", INFINITIES, ids=lambda x: len(x) if isinstance(x, list) else x)
+def test_infinities_among_the_cached_values(B, H, G, T, d, C, lens):
+    """A sum of products with positive weights: infinite where one of its values is, by sign, NaN where both signs meet."""
+    g = _gen("infinities", B, H, G, T, d, C)
+    q = _randn(g, B, H * G, T, d)
+    k, v = _randn(g, B, H, C, d), _randn(g, B, H, C, d)
+    for b, n in enumerate(lens):
+        k[b, :, n + T:], v[b, :, n + T:] = NAN, NAN
+    clean = sa.cache_attention(q, k, v, _i32(*lens))
+    _lay(v, lens, T, g)
+    o, lse = sa.cache_attention(q, k, v, _i32(*lens))
+    want_o, want_l = ref.attention_many(q, k, v, lens)
+    ref.check("o", o, *want_o)
+    ref.check("lse", lse, *want_l)
+    assert bool(want_o[0].isinf().any()) and bool(want_o[0].isnan().any()) and torch.equal(lse, clean[1])
+    columns = v[:, :, :1].new_zeros(B, H, 1, d)
+    for b, n in enumerate(lens):
+        columns[b] = (~v[b, :, :n + T].isfinite()).any(1, keepdim=True).to(v.dtype)
+    same = (columns == 0).repeat_interleave(G, 1).expand_as(o)
+    assert torch.equal(o[same], clean[0][same])              # the other columns are as they were
+    assert sa.attn_get_device_status() == 0
+
+
+def test_a_row_without_weights_stays_nan():
+    """Queries that are not finite make their own rows NaN, whatever the values are."""
+    g = _gen("nan rows")
+    B, H, G, d, C = 2, 2, 4, 128, 1000
+    q, k, v = _randn(g, B, H * G, 1, d), _randn(g, B, H, C, d), _randn(g, B, H, C, d)
+    q[0, 1, 0, 7], q[1, 6] = NAN, NAN
+    v[:, :, 11, 5], v[:, :, 500, 6] = INF, -INF
+    o, lse = sa.cache_attention(q, k, v, _i32(990, 30))
+    bad = torch.zeros(B, H * G, dtype=torch.bool, device="cuda")
+    bad[0, 1] = bad[1, 6] = True
+    assert bool(o[bad].isnan().all()) and bool(lse[bad].isnan().all())
+    good = o[~bad]
+    assert bool((good[..., 5] == INF).all()) and not bool(lse[~bad].isnan().any())
+    seen = o[0][~bad[0]]
+    assert bool((seen[..., 6] == -INF).all()) and not bool(good.isnan().any())
