@@ -37,6 +37,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kFewWarps = 8;
 constexpr int kFewThreads = 32 * kFewWarps;
 constexpr int kBlock = 16 * kFewWarps;   // slots of a block of work
+constexpr int kAbortBytes = 16;          // of the word that says a wait has given up, behind the barriers
 
 __device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
@@ -721,7 +722,7 @@ struct FewCfg {
     static constexpr int HELD = NT * (D / 4 + 4) * 32;        // floats a warp hands over
     static constexpr int RINGS = kFewWarps * (int)R::RING, HANDED = HALF * HELD * 4;
     static constexpr int JOIN = HANDED > (int)sizeof(L) ? HANDED : (int)sizeof(L);
-    static constexpr int SMEM = RINGS + JOIN + 256 + 1024;
+    static constexpr int SMEM = RINGS + JOIN + kFewWarps * STAGES * 8 + kAbortBytes + 1024;
     static_assert(BLOCKS * (SMEM + 1024) <= 228 * 1024, "");
 };
 
@@ -835,7 +836,7 @@ struct UnitCfg {
     // what the warps leave goes over their rings
     static constexpr int RINGS = kUnitWarps * (int)R::RING;
     static_assert(sizeof(L) <= RINGS, "");
-    static constexpr int SMEM = RINGS + (int)sizeof(Sum) + 256 + 1024;
+    static constexpr int SMEM = RINGS + (int)sizeof(Sum) + kUnitWarps * STAGES * 8 + kAbortBytes + 1024;
     static_assert(BLOCKS * (SMEM + 1024) <= 228 * 1024, "");
 };
 
