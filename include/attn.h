@@ -393,7 +393,8 @@ attn_status attn_debug_linear_plan(int kind, int B, int H, int N, int d_k, int N
  *   turns : [rotated / 2] uint64, f_j / (2 pi) in units of 2^-64: whole turns a position, modulo one.
  *   positions : int32, null (row n is at position n), [N] (positions_stride 0) or [B, N] (positions_stride N);
  *               any values, negative ones among them.
- * The reduction of position * f_j is exact; the angle is off by at most 2^-25 of half a turn, products and sums
+ * The reduction of position * turns is exact; the angle is off by at most 2^-25 of half a turn (and by what the
+ * rounding of `turns` to 2^-64 gives at the position, up to |position| 2^-64 of half a turn), products and sums
  * are fp32, y is rounded once.  B, H or N = 0: nothing to do.
  */
 attn_status attn_rotary(const void *x, void *y, const int *positions, long long positions_stride,

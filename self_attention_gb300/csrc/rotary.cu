@@ -4,7 +4,8 @@
 // amplitude; the gradient is the same with -t.  The frequency f comes as whole turns a position in units of
 // 2^-64, so that p f mod 1 is one 64-bit product whose overflow is the reduction: exact for any position,
 // where an fp32 angle is off by a whole 2^-24 p f.  Its upper 32 bits, as a fraction of half a turn, go to
-// sincospif(): the angle is off by at most 2^-25 of half a turn.
+// sincospif(), the last of them set where a lower one is, so that the rounding to fp32 is that of all 64: the angle is
+// off by at most 2^-25 of half a turn from the p-fold of f as it was given (cutting first would add 2^-31).
 //
 // Bound by HBM.  A thread takes eight pairs of one token (16 columns: two 16-byte chunks), computes their
 // eight sines and cosines once and walks over heads with them, as many as still leave the GPU full of threads;
@@ -32,7 +33,8 @@ __device__ __forceinline__ void turn_of(Turn &t, const uint64_t *turns, int i, i
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             float s, c;
-            sincospif((float)(int32_t)(a[k] >> 32) * 0x1p-31f, &s, &c);
+            const int32_t u = (int32_t)(a[k] >> 32) | ((uint32_t)a[k] != 0);
+            sincospif((float)u * 0x1p-31f, &s, &c);
             t.c[e + k] = c * amplitude;
             t.s[e + k] = s * (amplitude * sign);
         }
