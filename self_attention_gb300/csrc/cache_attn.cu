@@ -18,7 +18,7 @@
 // has used one up.  Eight warps with three steps each (192 KB an SM on their way at d = 128) draw 6.4 TB/s (32 sequences
 // of 16000 slots and 4 cached heads, 160 us); loads into registers, twelve warps with one step ahead, 6.1 (170 us), and
 // the same ring by cp.async 5.2 (201 us: the copies' instructions sit on each warp's chain).  P meets V as two bf16
-// terms (its own rounding and the rest), 2^-16 of it: one term alone would cost 2^-8 of each weight, and the pipe has room.
+// terms (its upper bits and the rest), 2^-15 of it: one term alone would cost 2^-8 of each weight, and the pipe has room.
 //
 // Work is shared out in blocks of 128 slots over all units (few_kernel, many_kernel), the same number for each CTA or
 // nearly so (the lengths are on the device: each CTA finds its share itself).  A unit that one CTA has whole is finished
@@ -34,6 +34,7 @@ namespace attn {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLeast = 0x1p-126f;      // the least positive number that no product flushes
 constexpr int kFewWarps = 8;
 constexpr int kFewThreads = 32 * kFewWarps;
 constexpr int kBlock = 16 * kFewWarps;   // slots of a block of work
@@ -469,9 +470,13 @@ struct Rows {
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const uint32_t w = ptx::pack_bf16x2(p[2 * i], p[2 * i + 1]);
+                // the upper bits and the rest, which is not negative, and 0 only where p is: an infinite value keeps its sign
+                // under both
+                const uint32_t w = __byte_perm(__float_as_uint(p[2 * i]), __float_as_uint(p[2 * i + 1]), 0x7632);
+                const float x0 = fmaxf(p[2 * i] - lo(w), fminf(p[2 * i], kLeast));
+                const float x1 = fmaxf(p[2 * i + 1] - hi(w), fminf(p[2 * i + 1], kLeast));
                 ph[t][i] = transpose8x8(w);
-                pl[t][i] = transpose8x8(ptx::pack_bf16x2(p[2 * i] - lo(w), p[2 * i + 1] - hi(w)));
+                pl[t][i] = transpose8x8(ptx::pack_bf16x2(x0, x1));
             }
         }
         // A token's value that is not finite may reach the rows that see it alone, but 0 times it is NaN in a
@@ -540,76 +545,6 @@ struct Rows {
 #pragma unroll
             for (int j = 0; j < MT; ++j) mma16816(acc[t][j], af[j], pl[t][0], pl[t][1]);
         }
-    }
-    // After the last step.  Weights are positive, so that a value that is not finite decides its column's sum wherever it is
-    // seen; but P's second term has a sign of its own (or is 0), and makes NaN of an infinity.  Where sums are not finite and
-    // their weights are, V of the warp's slots (16 from `key` on, every `stride`, below `end`) is looked through, and the
-    // sums with such values are theirs alone.  A second pass over V, rare; looking for it is one product a sum and unit (a
-    // look at each value would be one in each step): one token over 1000 slots of 16 heads 6.0 to 6.3 us with it and
-    // without, trees of 13 over 1100 slots 9.4 and 9.3, the long batch 119 both.
-    __device__ __forceinline__ void mend(const CacheAttnArgs &a, long long head, int b, int r0, int key, int end, int stride,
-                                         int length)
-    {
-        bool look = false;
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float z = 0.f;           // NaN if a sum is not finite
-#pragma unroll
-                for (int i = 0; i < MT; ++i) z = fmaf(acc[t][i][e], 0.f, fmaf(acc[t][i][e + 2], 0.f, z));
-                look |= z != z;
-            }
-        if (!__any_sync(0xffffffffu, look)) return;
-        look = false;
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {            // (a row of NaN weights stays NaN without a look)
-                float sum = l[t][e], z = 0.f;
-                for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-#pragma unroll
-                for (int i = 0; i < MT; ++i) z = fmaf(acc[t][i][e], 0.f, fmaf(acc[t][i][e + 2], 0.f, z));
-                look |= sum == sum && z != z;
-            }
-        if (!__any_sync(0xffffffffu, look)) return;
-        end = min(end, length + a.T);
-        uint64_t sees[NT][2];                        // (`word` may be the next unit's)
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = r0 + 8 * t + 2 * q + e;
-                sees[t][e] = r < a.G * a.T ? word_of(a.tree, b, a.T, r % a.T) : 0;
-            }
-        const uint4 *vp = static_cast<const uint4 *>(a.v) + head * a.C * (D / 8) + g;
-        for (int pass = 0; pass < 2; ++pass)         // clears the sums, and adds
-            for (int k0 = key; k0 < end; k0 += stride)
-                for (int j = k0; j < min(k0 + 16, end); ++j) {
-                    uint4 v[VC];
-                    bool odd = false;
-#pragma unroll
-                    for (int c = 0; c < VC; ++c) {
-                        v[c] = vp[(long long)j * (D / 8) + 8 * c];
-                        odd |= any_odd(v[c]);
-                    }
-                    if (!odd) continue;
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            if (j >= length && !(sees[t][e] >> (j - length) & 1)) continue;
-#pragma unroll
-                            for (int c = 0; c < VC; ++c)
-#pragma unroll
-                                for (int x = 0; x < 8; ++x) {
-                                    const uint32_t w = x / 2 == 0 ? v[c].x : x / 2 == 1 ? v[c].y : x / 2 == 2 ? v[c].z : v[c].w;
-                                    const float f = x & 1 ? hi(w) : lo(w);
-                                    float &to = acc[t][D == 128 ? x : x & 3][e + 2 * (D == 128 ? c : x >> 2)];
-                                    if (odd_value(f)) to = pass ? to + f : 0.f;
-                                }
-                        }
-                }
     }
     // A warp's results into shared memory as they lie in its registers, and into those of another warp.
     __device__ __forceinline__ void hand_over(float *to)          // [NT (4 MT + 4)][32]
@@ -783,7 +718,6 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, NT>::BLOCKS)
             ask();
             if (key + kBlock >= end && nxt.there) w.load_q(a, nxt.head, nxt.b, nxt.tile * R8);
         }
-        w.mend(a, seg.head, seg.b, r0, first_key(seg), end, kBlock, seg.length);
         // half of the warps take the others' results over, then the rows are put together
         if (warp >= C::HALF) w.hand_over(handed + (warp - C::HALF) * C::HELD);
         __syncthreads();
@@ -882,14 +816,12 @@ __global__ void __launch_bounds__(32 * kUnitWarps, UnitCfg<D, NT>::BLOCKS)
 #pragma unroll
     for (int i = 1; i < C::STAGES; ++i) ask();
     const float to_log2 = a.scale * kLog2e;
-    const int first = key;
     w.clear();
     for (; key < valid; key += stride) {
         w.scores(guard);
         w.step(a, head, r0, key, length, to_log2, kept);
         ask();
     }
-    w.mend(a, head, b, r0, first, valid, stride, length);
     w.finish();
     __syncthreads();                 // every ring is empty
     w.leave(&left.o[warp][0][0], left.ml[warp]);
