@@ -443,7 +443,8 @@ size_t attn_cache_attention_workspace_size(int B, int H, int G, int T, int C, in
  *   weights, weights_out : [B, H, C] fp32 or both null: weights_out = weights, and for slots below
  *          lengths[b] + T weights + the p_j of the counted tokens, added over them and over the G heads.
  *          weights_out may be weights itself.
- *   counted : [B] uint64 or null (all): bit t: token t is counted.  Of no account without weights.
+ *   counted : [B] uint64 or null (all, drafts that are rejected later among them): bit t: token t is counted.  Of no
+ *          account without weights.
  * A row that sees nothing gets o = 0 and lse = -infinity.  What a row does not see does not reach it, NaN and
  * infinities among it; slots behind the T tokens are not read.  A value that is not finite, in a slot that the row
  * sees, makes its column of o infinite by its sign, NaN where both signs or NaN meet (or where a weight is below

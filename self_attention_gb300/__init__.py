@@ -916,7 +916,8 @@ def cache_attention(q, cache_k, cache_v, lengths, tree=None, weights=None, count
     cache_append() has put into slots lengths[b] ... lengths[b] + T - 1.  tree [B, T] int64: bit u of word t says
     that token t sees token u (tree_words()); without it a chain.  o as q, lse [B, Hq, T] fp32.
     With weights [B, H, C] fp32, (o, lse, weights_out): weights with the attention that each slot got from the tokens
-    added, from those of bits counted [B] int64 alone where given; weights_out may be weights itself."""
+    added, from those of bits counted [B] int64 alone where given (without it from all, drafts that are rejected
+    later among them); weights_out may be weights itself."""
     fn = _binding().cache_attention
     if stream is None:
         return fn(q, cache_k, cache_v, lengths, tree, weights, counted, weights_out, scale)

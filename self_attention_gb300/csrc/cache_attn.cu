@@ -8,7 +8,7 @@
 // Up to 16 rows (unit_kernel, few_kernel; more where the cache is short).  The products are turned round so that the
 // slots are the 16-row operand of mma.sync and the few query rows its 8 columns: S^T = K Q^T, O^T = V^T P^T (a tcgen05
 // tile would be nearly empty with so few rows, and its result is a round trip through tensor memory away; the tensor pipe
-// is at 12 % as it is).  A warp takes 16 slots a step, from a ring that TMA fills for it alone:
+// is at 15 % as it is).  A warp takes 16 slots a step, from a ring that TMA fills for it alone:
 //   K   thread (g, q) = (lane / 4, lane % 4) reads chunks 4 c + q of slots g and g + 8; the sum over d runs in the
 //       order that these chunks give, the same for Q.
 //   V   it reads chunk g (and g + 8) of slots 2 q, 2 q + 1, 2 q + 8, 2 q + 9; two slots' values of a column
@@ -1567,7 +1567,8 @@ __global__ void __launch_bounds__(256) kept_weights_kernel(const __grid_constant
 }
 
 // The same for more rows: K is read a second time, the rows in eights.  A block takes 128 slots of one (sequence,
-// cached head).
+// cached head).  Bound by latency: each warp loads Q and lse again for its 16 slots (4 trees of 64 over 16384 slots of 4 cached
+// heads of 256 rows 252-259 us, tensor pipe 11 %, L2 2 %; K alone is 64 MB, 9.5 us).
 template <int D>
 __global__ void __launch_bounds__(kFewThreads) weights_kernel(CacheAttnArgs a, int blocks)
 {
