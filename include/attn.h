@@ -448,7 +448,7 @@ size_t attn_cache_attention_workspace_size(int B, int H, int G, int T, int C, in
  * A row that sees nothing gets o = 0 and lse = -infinity.  What a row does not see does not reach it, NaN and
  * infinities among it; slots behind the T tokens are not read.  A value that is not finite, in a slot that the row
  * sees, makes its column of o infinite by its sign, NaN where both signs or NaN meet (or where a weight is below
- * 2^-126 of the row's largest, which may count as 0).  A length outside 0 ... C - T counts as the nearest
+ * 2^-100 of the row's largest, which may count as 0).  A length outside 0 ... C - T counts as the nearest
  * inside.  Scores and sums are fp32.  Results are bitwise reproducible.
  *   workspace : caller-owned, overwritten.   T <= C.   B H G T below 2^27.   scale finite and > 0.
  */

@@ -34,7 +34,6 @@ namespace attn {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLeast = 0x1p-126f;      // the least positive number that no product flushes
 constexpr int kFewWarps = 8;
 constexpr int kFewThreads = 32 * kFewWarps;
 constexpr int kBlock = 16 * kFewWarps;   // slots of a block of work
@@ -470,11 +469,11 @@ struct Rows {
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                // the upper bits and the rest, which is not negative, and 0 only where p is: an infinite value keeps its sign
-                // under both
+                // the upper bits and the rest, at least 2^-24 of p: it is of p's sign, and 0 only where p is (or below 2^-100),
+                // so that an infinite value keeps its sign under both
                 const uint32_t w = __byte_perm(__float_as_uint(p[2 * i]), __float_as_uint(p[2 * i + 1]), 0x7632);
-                const float x0 = fmaxf(p[2 * i] - lo(w), fminf(p[2 * i], kLeast));
-                const float x1 = fmaxf(p[2 * i + 1] - hi(w), fminf(p[2 * i + 1], kLeast));
+                const float x0 = fmaxf(p[2 * i] - lo(w), p[2 * i] * 0x1p-24f);
+                const float x1 = fmaxf(p[2 * i + 1] - hi(w), p[2 * i + 1] * 0x1p-24f);
                 ph[t][i] = transpose8x8(w);
                 pl[t][i] = transpose8x8(ptx::pack_bf16x2(x0, x1));
             }

@@ -128,3 +128,30 @@ def test_a_row_without_weights_stays_nan():
     assert bool((good[..., 5] == INF).all()) and not bool(lse[~bad].isnan().any())
     seen = o[0][~bad[0]]
     assert bool((seen[..., 6] == -INF).all()) and not bool(good.isnan().any())
+
+
+@pytest.mark.parametrize("G,d,C", [(1, 64, 300), (4, 128, 300), (16, 64, 300), (3, 128, ROOM), (12, 64, ROOM), (16, 128, ROOM), (20, 64, ROOM)])
+def test_large_values_under_small_weights(G, d, C):
+    """Weights 2^(-33 j / 4) of 16 slots that one warp takes, under values of 2^(8 j + 4): each product is held to its weight's
+    rounding, not to an absolute one."""
+    B, H, n = 1, 2, 16
+    k, v = (torch.zeros(B, H, C, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q = torch.zeros(B, H * G, 1, d, dtype=torch.bfloat16, device="cuda")
+    q[..., 0], q[..., 1] = 1, 0.25
+    j = torch.arange(n, device="cuda").float()
+    k[..., :n, 0], k[..., :n, 1] = -8 * j, -j                    # score j is exact: -33 j / 4
+    c = torch.arange(d, device="cuda")                           # a column has one value, at slot c % 16
+    v[:, :, c % n, c] = torch.exp2(8.0 * (c % n) + 4).to(torch.bfloat16)
+    o, lse = sa.cache_attention(q, k, v, _i32(n - 1), scale=math.log(2.0))
+    weights = torch.exp2(-33 * j.double() / 4)
+    want = (weights[c % n] / weights.sum() * torch.exp2(8.0 * (c % n).double() + 4)).expand_as(o)
+    # the scale, its product with log2 e and with the score are rounded (2^-24 each of at most 124 units of ln 2); the weight's
+    # 2^-8 and o's
+    tol = want * (3 * 124 * 2.0 ** -24 + 2.0 ** -8 + 2.0 ** -8 * 1.01)
+    ref.check("o", o, want, tol)
+    assert (lse.double() - math.log(weights.sum().item())).abs().max() < 1e-5
+    low = c % n <= 12                                            # weights down to 2^-99: infinite values there keep their sign
+    for value in (INF, -INF):
+        v[:, :, (c % n)[low], c[low]] = value
+        o2, lse2 = sa.cache_attention(q, k, v, _i32(n - 1), scale=math.log(2.0))
+        assert bool((o2[..., low] == value).all()) and torch.equal(o2[..., ~low], o[..., ~low]) and torch.equal(lse2, lse)
